@@ -22,12 +22,20 @@ _lib: Optional[ctypes.CDLL] = None
 
 CSA_OK, CSA_ERR_INVALID_VALUE, CSA_ERR_UNSUPPORTED, CSA_ERR_WORKSPACE, CSA_ERR_CUDA = 0, 1, 2, 3, 4
 CSA_DEVERR_CU_SEQLENS, CSA_DEVERR_OUT_ROWS, CSA_DEVERR_TIMEOUT, CSA_DEVERR_LEAD = 1, 2, 3, 4
+CSA_DEVERR_SLOT, CSA_DEVERR_ENTRIES, CSA_DEVERR_PAGE = 5, 6, 7
+CSA_DTYPE_BF16, CSA_DTYPE_FP16, CSA_DTYPE_FP32 = 0, 1, 2
+CSA_ROPE_PLAIN, CSA_ROPE_LINEAR, CSA_ROPE_YARN = 0, 1, 2
+CSA_ROPE_HALF, CSA_ROPE_INTERLEAVED = 0, 1
+CSA_CACHE_BF16, CSA_CACHE_E4M3, CSA_CACHE_E2M1 = 0, 1, 2
+CSA_MAX_HEAD_DIM, CSA_CACHE_GROUP = 1024, 32
 CSA_TEST_MIN_WAIT_CYCLES = 1000000
 CSA_KPOOL_MAX_POOL = 1024
 EXPORTED = ("csa_status_string", "csa_last_error_string", "csa_compressor_total_comp", "csa_compressor_fwd",
             "csa_compressor_bwd_workspace_bytes", "csa_compressor_bwd",
             "csa_compressor_bwd_noalloc", "csa_compressor_test_hooks",
-            "csa_compressor_map_blocks", "csa_kpool_total", "csa_kpool_fwd")
+            "csa_compressor_map_blocks", "csa_kpool_total", "csa_kpool_fwd", "csa_rope_table",
+            "csa_norm_rope_fwd", "csa_norm_rope_bwd_workspace_bytes", "csa_norm_rope_bwd",
+            "csa_cache_write", "csa_cache_read", "csa_cache_attn_workspace_bytes", "csa_cache_attn")
 
 
 class CsaError(RuntimeError):
@@ -74,6 +82,26 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.csa_kpool_total.argtypes = [vp, vp, i32, i32]
     lib.csa_kpool_fwd.restype = ctypes.c_int
     lib.csa_kpool_fwd.argtypes = [vp, vp, vp, vp, i32, i32, i32, i64, vp, i64, i32, vp, vp]
+    f32, f64 = ctypes.c_float, ctypes.c_double
+    lib.csa_rope_table.restype = ctypes.c_int
+    lib.csa_rope_table.argtypes = [i32, f64, i32, f64, f64, f64, f64, vp, vp]
+    lib.csa_norm_rope_fwd.restype = ctypes.c_int
+    lib.csa_norm_rope_fwd.argtypes = [vp, i32, i64, i32, i32, i64, i64, vp, i32, f32, vp, vp, i32,
+                                      i32, i32, f32, vp, i64, i64, vp]
+    lib.csa_norm_rope_bwd_workspace_bytes.restype = sz
+    lib.csa_norm_rope_bwd_workspace_bytes.argtypes = [i64, i32, i32]
+    lib.csa_norm_rope_bwd.restype = ctypes.c_int
+    lib.csa_norm_rope_bwd.argtypes = [vp, vp, i32, i64, i32, i32, i64, i64, i64, i64, vp, i32, f32,
+                                      vp, vp, i32, i32, i32, f32, vp, i64, i64, vp, i32, vp, sz, vp]
+    lib.csa_cache_write.restype = ctypes.c_int
+    lib.csa_cache_write.argtypes = [vp, i32, i64, i32, i32, i64, i64, vp, i64, i32, vp, vp, vp, vp]
+    lib.csa_cache_read.restype = ctypes.c_int
+    lib.csa_cache_read.argtypes = [vp, vp, i32, vp, i64, i64, i32, i32, vp, i32, i64, i64, vp, vp]
+    lib.csa_cache_attn_workspace_bytes.restype = sz
+    lib.csa_cache_attn_workspace_bytes.argtypes = [i32, i64, i32, i32, i32, i64]
+    lib.csa_cache_attn.restype = ctypes.c_int
+    lib.csa_cache_attn.argtypes = [vp, i64, i64, vp, i32, i64, i32, i32, i32, vp, vp, i32, vp, i32,
+                                   i64, i32, vp, vp, i32, f32, vp, vp, i64, i64, vp, vp, sz, vp, vp]
     if path == LIB_PATH:
         _lib = lib
     return lib
@@ -191,3 +219,85 @@ def csa_kpool_fwd(key, gate, cu_seqlens, lead, S: int, pool: int, d: int, capaci
                                 capacity, _ptr(out), out_rows, int(compress), _ptr(dev_error),
                                 _stream(stream)), "csa_kpool_fwd")
 
+
+
+def csa_rope_table(rot_dim: int, base: float = 10000.0, scaling: int = CSA_ROPE_PLAIN,
+                   factor: float = 1.0, original_length: float = 4096.0, beta_fast: float = 32.0,
+                   beta_slow: float = 1.0):
+    """``(turns, amplitude)``: a host int64 tensor [rot_dim / 2] holding the uint64 turns of
+    each pair (move it to the GPU for the calls), and the amplitude to pass with it."""
+    import torch
+    turns = torch.zeros(max(rot_dim, 0) // 2, dtype=torch.int64)
+    amplitude = ctypes.c_float(1.0)
+    _check(load().csa_rope_table(rot_dim, base, scaling, factor, original_length, beta_fast,
+                                 beta_slow, turns.data_ptr() or None, ctypes.byref(amplitude)),
+           "csa_rope_table")
+    return turns, amplitude.value
+
+
+def csa_norm_rope_fwd(x, dtype: int, rows: int, heads: int, d: int, x_row_stride: int,
+                      x_head_stride: int, weight, norm: int, eps: float, positions, turns,
+                      rot_dim: int, rot_start: int, layout: int, amplitude: float, y,
+                      y_row_stride: int, y_head_stride: int, stream=None) -> None:
+    """Norm of every head and rotation to the row's position; strides in elements."""
+    _check(load().csa_norm_rope_fwd(_ptr(x), dtype, rows, heads, d, x_row_stride, x_head_stride,
+                                    _ptr(weight), int(norm), eps, _ptr(positions), _ptr(turns),
+                                    rot_dim, rot_start, layout, amplitude, _ptr(y), y_row_stride,
+                                    y_head_stride, _stream(stream)), "csa_norm_rope_fwd")
+
+
+def csa_norm_rope_bwd_workspace_bytes(rows: int, heads: int, d: int) -> int:
+    return int(load().csa_norm_rope_bwd_workspace_bytes(rows, heads, d))
+
+
+def csa_norm_rope_bwd(x, dy, dtype: int, rows: int, heads: int, d: int, x_row_stride: int,
+                      x_head_stride: int, dy_row_stride: int, dy_head_stride: int, weight,
+                      norm: int, eps: float, positions, turns, rot_dim: int, rot_start: int,
+                      layout: int, amplitude: float, dx, dx_row_stride: int, dx_head_stride: int,
+                      dweight, accumulate_dweight: int, workspace, workspace_bytes: int,
+                      stream=None) -> None:
+    _check(load().csa_norm_rope_bwd(_ptr(x), _ptr(dy), dtype, rows, heads, d, x_row_stride,
+                                    x_head_stride, dy_row_stride, dy_head_stride, _ptr(weight),
+                                    int(norm), eps, _ptr(positions), _ptr(turns), rot_dim,
+                                    rot_start, layout, amplitude, _ptr(dx), dx_row_stride,
+                                    dx_head_stride, _ptr(dweight), int(accumulate_dweight),
+                                    _ptr(workspace), workspace_bytes, _stream(stream)),
+           "csa_norm_rope_bwd")
+
+
+def csa_cache_write(x, dtype: int, rows: int, heads: int, d: int, x_row_stride: int,
+                    x_head_stride: int, slots, num_slots: int, format: int, data, scales,
+                    dev_error=None, stream=None) -> None:
+    """Rows into slots of the paged cache, quantised as ``format`` says."""
+    _check(load().csa_cache_write(_ptr(x), dtype, rows, heads, d, x_row_stride, x_head_stride,
+                                  _ptr(slots), num_slots, format, _ptr(data), _ptr(scales),
+                                  _ptr(dev_error), _stream(stream)), "csa_cache_write")
+
+
+def csa_cache_read(data, scales, format: int, slots, rows: int, num_slots: int, heads: int, d: int,
+                   out, dtype: int, out_row_stride: int, out_head_stride: int, dev_error=None,
+                   stream=None) -> None:
+    """Slots of the paged cache back into rows of ``dtype``."""
+    _check(load().csa_cache_read(_ptr(data), _ptr(scales), format, _ptr(slots), rows, num_slots,
+                                 heads, d, _ptr(out), dtype, out_row_stride, out_head_stride,
+                                 _ptr(dev_error), _stream(stream)), "csa_cache_read")
+
+
+def csa_cache_attn_workspace_bytes(S: int, tokens: int, q_heads: int, kv_heads: int, d: int,
+                                   max_entries: int) -> int:
+    return int(load().csa_cache_attn_workspace_bytes(S, tokens, q_heads, kv_heads, d, max_entries))
+
+
+def csa_cache_attn(q, q_row_stride: int, q_head_stride: int, cu_seqlens, S: int, tokens: int,
+                   q_heads: int, kv_heads: int, d: int, data, scales, format: int, page_table,
+                   max_pages: int, num_pages: int, page_size: int, entries, first, ratio: int,
+                   softmax_scale: float, sink, out, out_row_stride: int, out_head_stride: int,
+                   lse, workspace, workspace_bytes: int, dev_error=None, stream=None) -> None:
+    """New tokens over the paged cache, an entry being key and value at once."""
+    _check(load().csa_cache_attn(_ptr(q), q_row_stride, q_head_stride, _ptr(cu_seqlens), S, tokens,
+                                 q_heads, kv_heads, d, _ptr(data), _ptr(scales), format,
+                                 _ptr(page_table), max_pages, num_pages, page_size, _ptr(entries),
+                                 _ptr(first), ratio, softmax_scale, _ptr(sink), _ptr(out),
+                                 out_row_stride, out_head_stride, _ptr(lse), _ptr(workspace),
+                                 workspace_bytes, _ptr(dev_error), _stream(stream)),
+           "csa_cache_attn")

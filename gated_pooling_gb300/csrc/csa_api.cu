@@ -289,7 +289,8 @@ __global__ void __launch_bounds__(COLS * SPLIT)
   constexpr int kReduceCols = COLS;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // read with the partials (only the final write depends on it)
-  const int32_t call_status = *reinterpret_cast<const volatile int32_t*>(status);
+  const int32_t call_status =
+      status != nullptr ? *reinterpret_cast<const volatile int32_t*>(status) : 0;
   __shared__ float s_sum[kReduceSplit][kReduceCols];
   __shared__ float s_cmp[kReduceSplit][kReduceCols];
   const int lane = threadIdx.x % kReduceCols;
@@ -333,6 +334,47 @@ __global__ void __launch_bounds__(COLS * SPLIT)
     dape[e] = t + tc;
   }
 }
+
+}  // namespace
+
+// Enqueues dape_reduce_kernel: out[e] = (accumulate ? out[e] : 0) + the R partials of entry e,
+// as a programmatic dependent of the stream's previous kernel.
+cudaError_t launch_partial_reduce(const float* part, int R, int n, float* out, bool accumulate,
+                                  const int32_t* status, cudaStream_t stream) {
+  int acc = accumulate ? 1 : 0;
+  void* rargs[] = {&part, &R, &n, &out, &acc, &status};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  // thread groups per block: the power of two nearest above R/5 (R/10 when R is below 32),
+  // at most 32; 16 entries per block when 32-entry blocks would be fewer than 64
+  const int per = R < 32 ? 10 : 5;
+  int split = 1;
+  while (split < 32 && split * per < R) split *= 2;
+  const bool narrow = (n + 31) / 32 < 64;
+  const int cols = narrow ? 16 : 32;
+  auto pick = [&](auto c) -> const void* {
+    constexpr int C = decltype(c)::value;
+    return split == 1    ? reinterpret_cast<const void*>(dape_reduce_kernel<1, C>)
+           : split == 2  ? reinterpret_cast<const void*>(dape_reduce_kernel<2, C>)
+           : split == 4  ? reinterpret_cast<const void*>(dape_reduce_kernel<4, C>)
+           : split == 8  ? reinterpret_cast<const void*>(dape_reduce_kernel<8, C>)
+           : split == 16 ? reinterpret_cast<const void*>(dape_reduce_kernel<16, C>)
+                         : reinterpret_cast<const void*>(dape_reduce_kernel<32, C>);
+  };
+  const void* rk = narrow ? pick(std::integral_constant<int, 16>{})
+                          : pick(std::integral_constant<int, 32>{});
+  cfg.gridDim = dim3((n + cols - 1) / cols);
+  cfg.blockDim = dim3(cols * split);
+  cfg.dynamicSmemBytes = 0;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return note(cudaLaunchKernelExC(&cfg, rk, rargs));
+}
+
+namespace {
 
 __global__ void map_blocks_kernel(const int32_t* __restrict__ cu, int S, int ratio,
                                   int64_t capacity, int64_t out_rows, int32_t* __restrict__ out,
@@ -470,43 +512,10 @@ csa_status_t csa_compressor_bwd(const void* kv, const void* score, const float* 
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   st = launch(k, pl, p, s);
   if (st != CSA_OK) return st;
-  const float* part = static_cast<const float*>(workspace);
-  int n = ratio * coff * d;
-  int R = pl.R;
-  int acc = accumulate_dape != 0;
-  const int32_t* status = p.status;
-  void* rargs[] = {&part, &R, &n, &dape, &acc, &status};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  // thread groups per block: the power of two nearest above R/5 (R/10 when R is below 32),
-  // at most 32; 16 entries per block when 32-entry blocks would be fewer than 64
-  const int per = R < 32 ? 10 : 5;
-  int split = 1;
-  while (split < 32 && split * per < R) split *= 2;
-  const bool narrow = (n + 31) / 32 < 64;
-  const int cols = narrow ? 16 : 32;
-  auto pick = [&](auto c) -> const void* {
-    constexpr int C = decltype(c)::value;
-    return split == 1    ? reinterpret_cast<const void*>(dape_reduce_kernel<1, C>)
-           : split == 2  ? reinterpret_cast<const void*>(dape_reduce_kernel<2, C>)
-           : split == 4  ? reinterpret_cast<const void*>(dape_reduce_kernel<4, C>)
-           : split == 8  ? reinterpret_cast<const void*>(dape_reduce_kernel<8, C>)
-           : split == 16 ? reinterpret_cast<const void*>(dape_reduce_kernel<16, C>)
-                         : reinterpret_cast<const void*>(dape_reduce_kernel<32, C>);
-  };
-  const void* rk = narrow ? pick(std::integral_constant<int, 16>{})
-                          : pick(std::integral_constant<int, 32>{});
-  cfg.gridDim = dim3((n + cols - 1) / cols);
-  cfg.blockDim = dim3(cols * split);
-  cfg.dynamicSmemBytes = 0;
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e =
-      note(cudaLaunchKernelExC(&cfg, rk, rargs));
-  return e == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
+  return launch_partial_reduce(static_cast<const float*>(workspace), pl.R, ratio * coff * d, dape,
+                               accumulate_dape != 0, p.status, s) == cudaSuccess
+             ? CSA_OK
+             : CSA_ERR_CUDA;
 }
 
 csa_status_t csa_compressor_test_hooks(int64_t wait_cycles, int32_t withhold_row) {

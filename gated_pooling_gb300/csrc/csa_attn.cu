@@ -1,0 +1,261 @@
+// csa_attn.cu -- attention of new tokens over the paged cache of entries that are key and value
+// at once (the interface and the formulas are in csa_compressor.h).
+#include <climits>
+#include <cmath>
+#include <cstdint>
+#include <type_traits>
+
+#include "csa_compressor.h"
+#include "csa_element.cuh"
+#include "csa_internal.h"
+
+namespace csa {
+namespace {
+
+struct AttnParams {
+  const uint16_t* q;
+  const int32_t* cu;
+  const uint8_t* data;
+  const uint8_t* scales;
+  const int32_t* table;
+  const int32_t* entries;
+  const int32_t* first;
+  const float* sink;
+  uint16_t* out;
+  float* lse;
+  int32_t* dev_error;
+  int32_t* status;  // workspace: 0, or why the call's lengths were refused
+  int64_t q_row, q_head, out_row, out_head;
+  int64_t tokens, num_pages, max_entries;
+  int S, q_heads, kv_heads, group, d, max_pages, page_size, ratio;
+  float scale;  // softmax_scale
+};
+
+// Entries that the token at position pos sees, of a sequence's n.
+__device__ __forceinline__ int visible(int64_t pos, int ratio, int n) {
+  if (ratio == 0) return n;
+  const int64_t done = pos + 1 <= 0 ? 0 : (pos + 1) / ratio;
+  return done < n ? static_cast<int>(done) : n;
+}
+
+// Sequence of a token, and -1 when it belongs to none (cu holds S + 1 non-decreasing offsets):
+// the largest s with cu[s] <= t whose end lies behind t.
+__device__ __forceinline__ int sequence_of(const int32_t* cu, int S, int64_t t) {
+  if (t < cu[0] || t >= cu[S]) return -1;
+  int lo = 0, hi = S;  // cu[lo] <= t < cu[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (cu[mid] <= t) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// Checks the call's lengths and publishes the verdict for the kernels behind it.
+constexpr int kPlanThreads = 256;
+__global__ void __launch_bounds__(kPlanThreads) attn_check_kernel(AttnParams p) {
+  pdl_wait();
+  int bad = 0;
+  for (int s = threadIdx.x; s < p.S; s += kPlanThreads) {
+    const int32_t a = p.cu[s], b = p.cu[s + 1], n = p.entries[s];
+    if (b < a || a < 0 || b > p.tokens) bad |= 1;
+    if (n < 0 || n > p.max_entries) bad |= 2;
+  }
+  const int cu_bad = __syncthreads_or(bad & 1), n_bad = __syncthreads_or(bad & 2);
+  if (threadIdx.x == 0) {
+    const int code = cu_bad ? CSA_DEVERR_CU_SEQLENS : n_bad ? CSA_DEVERR_ENTRIES : 0;
+    *p.status = code;
+    if (code != 0 && p.dev_error != nullptr) *p.dev_error = code;
+  }
+}
+
+// Scalar kernel, any d and alignment: a warp per new token and query head, a lane the columns
+// lane, lane + 32, ...; one pass over the entries with the running maximum and sum.
+constexpr int kScalarThreads = 128;
+template <int FORMAT, int NL>
+__global__ void __launch_bounds__(kScalarThreads) attn_scalar_kernel(AttnParams p) {
+  using B = Element<CSA_DTYPE_BF16>;
+  const int lane = threadIdx.x & 31;
+  pdl_wait();
+  if (*p.status != 0) return;
+  const int64_t u = (static_cast<int64_t>(blockIdx.x) * kScalarThreads + threadIdx.x) / 32;
+  if (u >= p.tokens * p.q_heads) return;
+  const int64_t t = u / p.q_heads;
+  const int h = static_cast<int>(u - t * p.q_heads);
+  const int s = sequence_of(p.cu, p.S, t);
+  if (s < 0) return;
+  const int64_t pos = static_cast<int64_t>(p.first != nullptr ? p.first[s] : 0) + (t - p.cu[s]);
+  const int n = visible(pos, p.ratio, p.entries[s]);
+  const uint16_t* q = p.q + t * p.q_row + h * p.q_head;
+  float qv[NL], acc[NL];
+#pragma unroll
+  for (int j = 0; j < NL; ++j) {
+    const int c = lane + 32 * j;
+    qv[j] = c < p.d ? B::to_float(q[c]) * p.scale : 0.f;
+    acc[j] = 0.f;
+  }
+  float m = -INFINITY, z = 0.f;
+  const int kvh = h / p.group;
+  for (int e = 0; e < n; ++e) {
+    const int page = p.table[static_cast<int64_t>(s) * p.max_pages + e / p.page_size];
+    if (page < 0 || page >= p.num_pages) {
+      if (p.dev_error != nullptr) *p.dev_error = CSA_DEVERR_PAGE;
+      continue;
+    }
+    const int64_t entry = (static_cast<int64_t>(page) * p.page_size + e % p.page_size) * p.kv_heads + kvh;
+    float k[NL], x = 0.f;
+#pragma unroll
+    for (int j = 0; j < NL; ++j) {
+      const int c = lane + 32 * j;
+      k[j] = 0.f;
+      if (c < p.d) {
+        if constexpr (FORMAT == CSA_CACHE_BF16)
+          k[j] = B::to_float(reinterpret_cast<const uint16_t*>(p.data)[entry * p.d + c]);
+        else {
+          const float sc = scale_value(p.scales[entry * (p.d / 32) + j]);
+          if constexpr (FORMAT == CSA_CACHE_E4M3) {
+            k[j] = e4m3x2_to_float2(p.data[entry * p.d + c]).x * sc;
+          } else {
+            const float2 two = e2m1x2_to_float2(p.data[entry * (p.d / 2) + c / 2]);
+            k[j] = (lane % 2 == 0 ? two.x : two.y) * sc;
+          }
+        }
+      }
+      x = fmaf(qv[j], k[j], x);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+    const float top = fmaxf(m, x);
+    // a score of -inf adds nothing; while every score was -inf the maximum stays -inf
+    const float old = m == top ? 1.f : expf(m - top), w = x == -INFINITY ? 0.f : expf(x - top);
+    z = z * old + w;
+#pragma unroll
+    for (int j = 0; j < NL; ++j) acc[j] = acc[j] * old + w * k[j];
+    m = top;
+  }
+  const float sink = p.sink != nullptr ? p.sink[h] : -INFINITY;
+  const float top = fmaxf(m, sink);
+  if (top != -INFINITY) {
+    const float old = m == -INFINITY ? 0.f : expf(m - top);
+    z = z * old + (sink == -INFINITY ? 0.f : expf(sink - top));
+    const float f = old / z;
+#pragma unroll
+    for (int j = 0; j < NL; ++j) acc[j] *= f;
+  }
+  uint16_t* out = p.out + t * p.out_row + h * p.out_head;
+#pragma unroll
+  for (int j = 0; j < NL; ++j) {
+    const int c = lane + 32 * j;
+    if (c < p.d) out[c] = B::from_float(acc[j]);
+  }
+  if (p.lse != nullptr && lane == 0) p.lse[u] = top == -INFINITY ? -INFINITY : top + logf(z);
+}
+
+const void* scalar_kernel_for(int format, int d) {
+  auto pick = [&](auto f) -> const void* {
+    constexpr int F = decltype(f)::value;
+    return d <= 128   ? reinterpret_cast<const void*>(attn_scalar_kernel<F, 4>)
+           : d <= 512 ? reinterpret_cast<const void*>(attn_scalar_kernel<F, 16>)
+                      : reinterpret_cast<const void*>(attn_scalar_kernel<F, 32>);
+  };
+  return format == CSA_CACHE_BF16   ? pick(std::integral_constant<int, CSA_CACHE_BF16>{})
+         : format == CSA_CACHE_E4M3 ? pick(std::integral_constant<int, CSA_CACHE_E4M3>{})
+                                    : pick(std::integral_constant<int, CSA_CACHE_E2M1>{});
+}
+
+csa_status_t check_attn_sizes(int32_t S, int64_t tokens, int32_t q_heads, int32_t kv_heads,
+                              int32_t d, int64_t max_entries) {
+  if (S < 0 || tokens < 0 || q_heads < 1 || kv_heads < 1 || d < 1 || max_entries < 0 ||
+      q_heads % kv_heads != 0)
+    return CSA_ERR_INVALID_VALUE;
+  if (d > CSA_MAX_HEAD_DIM || S > CSA_MAX_SEGMENTS || tokens > INT_MAX / q_heads ||
+      max_entries > INT_MAX)
+    return CSA_ERR_UNSUPPORTED;
+  return CSA_OK;
+}
+
+constexpr size_t kStatusBytes = 16;
+
+}  // namespace
+}  // namespace csa
+
+using namespace csa;
+
+extern "C" size_t csa_cache_attn_workspace_bytes(int32_t S, int64_t tokens, int32_t q_heads,
+                                                 int32_t kv_heads, int32_t d, int64_t max_entries) {
+  if (check_attn_sizes(S, tokens, q_heads, kv_heads, d, max_entries) != CSA_OK) return 0;
+  return kStatusBytes;
+}
+
+extern "C" csa_status_t csa_cache_attn(
+    const void* q, int64_t q_row_stride, int64_t q_head_stride, const int32_t* cu_seqlens, int32_t S,
+    int64_t tokens, int32_t q_heads, int32_t kv_heads, int32_t d, const void* data,
+    const uint8_t* scales, int32_t format, const int32_t* page_table, int32_t max_pages,
+    int64_t num_pages, int32_t page_size, const int32_t* entries, const int32_t* first,
+    int32_t ratio, float softmax_scale, const float* sink, void* out, int64_t out_row_stride,
+    int64_t out_head_stride, float* lse, void* workspace, size_t workspace_bytes,
+    int32_t* dev_error, csa_stream_t stream) {
+  if (max_pages < 0 || page_size < 1 || num_pages < 0 || ratio < 0 || q_row_stride < 0 ||
+      q_head_stride < 0 || out_row_stride < 0 || out_head_stride < 0 || !std::isfinite(softmax_scale))
+    return CSA_ERR_INVALID_VALUE;
+  const int64_t max_entries = static_cast<int64_t>(max_pages) * page_size;
+  const csa_status_t st = check_attn_sizes(S, tokens, q_heads, kv_heads, d, max_entries);
+  if (st != CSA_OK) return st;
+  if (format < CSA_CACHE_BF16 || format > CSA_CACHE_E2M1) return CSA_ERR_UNSUPPORTED;
+  if (format != CSA_CACHE_BF16 && d % CSA_CACHE_GROUP != 0) return CSA_ERR_UNSUPPORTED;
+  if (num_pages > INT64_MAX / 64 / page_size / (static_cast<int64_t>(kv_heads) * d))
+    return CSA_ERR_UNSUPPORTED;
+  if (cu_seqlens == nullptr || (S > 0 && entries == nullptr)) return CSA_ERR_INVALID_VALUE;
+  if (tokens > 0 && (q == nullptr || out == nullptr)) return CSA_ERR_INVALID_VALUE;
+  if (S > 0 && max_pages > 0 && page_table == nullptr) return CSA_ERR_INVALID_VALUE;
+  if (num_pages > 0 && (data == nullptr || (format != CSA_CACHE_BF16 && scales == nullptr)))
+    return CSA_ERR_INVALID_VALUE;
+  if (!is_aligned(q, 2) || !is_aligned(out, 2) || !is_aligned(cu_seqlens, 4) ||
+      !is_aligned(page_table, 4) || !is_aligned(entries, 4) || !is_aligned(first, 4) ||
+      !is_aligned(sink, 4) || !is_aligned(lse, 4) || !is_aligned(dev_error, 4) ||
+      !is_aligned(workspace, 16) || (format == CSA_CACHE_BF16 && !is_aligned(data, 2)))
+    return CSA_ERR_INVALID_VALUE;
+  if (S == 0 || tokens == 0) return CSA_OK;
+  if (workspace == nullptr || workspace_bytes < kStatusBytes) return CSA_ERR_WORKSPACE;
+
+  AttnParams p{};
+  p.q = static_cast<const uint16_t*>(q);
+  p.cu = cu_seqlens;
+  p.data = static_cast<const uint8_t*>(data);
+  p.scales = scales;
+  p.table = page_table;
+  p.entries = entries;
+  p.first = first;
+  p.sink = sink;
+  p.out = static_cast<uint16_t*>(out);
+  p.lse = lse;
+  p.dev_error = dev_error;
+  p.status = static_cast<int32_t*>(workspace);
+  p.q_row = q_row_stride;
+  p.q_head = q_head_stride;
+  p.out_row = out_row_stride;
+  p.out_head = out_head_stride;
+  p.tokens = tokens;
+  p.num_pages = num_pages;
+  p.max_entries = max_entries;
+  p.S = S;
+  p.q_heads = q_heads;
+  p.kv_heads = kv_heads;
+  p.group = q_heads / kv_heads;
+  p.d = d;
+  p.max_pages = max_pages;
+  p.page_size = page_size;
+  p.ratio = ratio;
+  p.scale = softmax_scale;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  void* args[] = {&p};
+  if (launch_pdl(reinterpret_cast<const void*>(attn_check_kernel), dim3(1), dim3(kPlanThreads), 0, cs,
+                 args) != cudaSuccess)
+    return CSA_ERR_CUDA;
+  const int64_t warps = tokens * q_heads;
+  const int64_t blocks = (warps + kScalarThreads / 32 - 1) / (kScalarThreads / 32);
+  return launch_pdl(scalar_kernel_for(format, d), dim3(static_cast<unsigned>(blocks)),
+                    dim3(kScalarThreads), 0, cs, args) == cudaSuccess
+             ? CSA_OK
+             : CSA_ERR_CUDA;
+}

@@ -25,5 +25,10 @@ cudaError_t device_sms(int dev, int* sms);
 cudaError_t blocks_per_sm(int dev, const void* kernel, int threads, size_t smem, int* blocks);
 cudaError_t launch_pdl(const void* k, dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
                        void** args);
+// launch_partial_reduce(): out[e] = (accumulate ? out[e] : 0) + sum of part[0..R-1][e] over n
+// entries, in a fixed order with compensated sums; a non-zero *status (may be NULL) on the
+// device leaves out untouched.
+cudaError_t launch_partial_reduce(const float* part, int R, int n, float* out, bool accumulate,
+                                  const int32_t* status, cudaStream_t stream);
 
 }  // namespace csa

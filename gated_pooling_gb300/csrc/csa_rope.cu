@@ -1,0 +1,378 @@
+// csa_rope.cu -- head norm and rotation in one pass, forward and backward (the interface and
+// the formulas are in csa_compressor.h).
+//
+// A row's head is read once, its mean square taken in fp32, and the columns written back
+// normed and turned; backward, x and dy are read once and dx written. Bound by HBM bytes.
+//
+// Angles: a pair turns by positions[r] * turns[i] in units of 2^-64 of a full turn, an
+// integer product modulo 2^64. Its upper 32 bits, taken as a signed number, are the angle
+// within half a turn either way, to 2^-32 of a turn, whatever the position; only then does
+// it become a float. No position loses precision, and no 64-bit floating point is needed.
+#include <cmath>
+#include <climits>
+#include <cstdint>
+#include <type_traits>
+
+#include "csa_compressor.h"
+#include "csa_element.cuh"
+#include "csa_internal.h"
+
+namespace csa {
+namespace {
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopeWarps = kRopeThreads / 32;
+
+struct RopeParams {
+  const void* x;
+  const void* dy;  // backward
+  void* y;         // backward: dx
+  const float* weight;
+  const int32_t* pos;
+  const uint64_t* turns;
+  float* partial;  // backward: [gridDim.x, d]
+  int64_t x_row, x_head, dy_row, dy_head, y_row, y_head;
+  int64_t units;  // rows * heads
+  int heads, d, rot, start;
+  int norm, interleaved;
+  float eps, amp;
+};
+
+// cos and sin of a turn, times amp.
+__device__ __forceinline__ void turn_cos_sin(int32_t pos, uint64_t per, float amp, float& c, float& s) {
+  const uint64_t t = static_cast<uint64_t>(static_cast<int64_t>(pos)) * per;
+  const float half_turns = static_cast<float>(static_cast<int32_t>(t >> 32)) * 0x1p-31f;
+  sincospif(half_turns, &s, &c);
+  c *= amp;
+  s *= amp;
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+
+// Columns of pair i of the rotated part.
+__device__ __forceinline__ void pair_columns(const RopeParams& p, int i, int& a, int& b) {
+  a = p.start + (p.interleaved ? 2 * i : i);
+  b = a + (p.interleaved ? 1 : p.rot / 2);
+}
+// Column of the j-th column outside the rotated part.
+__device__ __forceinline__ int other_column(const RopeParams& p, int j) {
+  return j < p.start ? j : j + p.rot;
+}
+
+// Scalar kernel, any d and alignment: a warp per row and head. Each lane takes whole pairs
+// and the columns outside the rotated part, reads both of a pair before it writes them (so
+// y may be x), and the backward's dweight sums stay with the lane that owns the column.
+template <int DTYPE>
+__global__ void __launch_bounds__(kRopeThreads) rope_scalar_kernel(RopeParams p) {
+  using E = Element<DTYPE>;
+  using T = typename E::T;
+  const int lane = threadIdx.x & 31;
+  pdl_wait();
+  for (int64_t u = static_cast<int64_t>(blockIdx.x) * kRopeWarps + (threadIdx.x >> 5); u < p.units;
+       u += static_cast<int64_t>(gridDim.x) * kRopeWarps) {
+    const int64_t row = u / p.heads, head = u - row * p.heads;
+    const int32_t pos = p.pos != nullptr ? p.pos[row] : 0;
+    if (pos < 0) continue;
+    const T* x = static_cast<const T*>(p.x) + row * p.x_row + head * p.x_head;
+    T* y = static_cast<T*>(p.y) + row * p.y_row + head * p.y_head;
+    float r = 1.f;
+    if (p.norm) {
+      float ss = 0.f;
+      for (int c = lane; c < p.d; c += 32) {
+        const float v = E::to_float(x[c]);
+        ss = fmaf(v, v, ss);
+      }
+      r = 1.f / sqrtf(warp_sum(ss) / static_cast<float>(p.d) + p.eps);
+    }
+    auto normed = [&](int c) {
+      const float v = E::to_float(x[c]);
+      return p.norm ? (p.weight != nullptr ? v * r * p.weight[c] : v * r) : v;
+    };
+    for (int i = lane; i < p.rot / 2; i += 32) {
+      int a, b;
+      pair_columns(p, i, a, b);
+      float cs, sn;
+      turn_cos_sin(pos, p.turns[i], p.amp, cs, sn);
+      const float va = normed(a), vb = normed(b);
+      y[a] = E::from_float(va * cs - vb * sn);
+      y[b] = E::from_float(va * sn + vb * cs);
+    }
+    for (int j = lane; j < p.d - p.rot; j += 32) {
+      const int c = other_column(p, j);
+      y[c] = E::from_float(normed(c));
+    }
+  }
+}
+
+// Backward of the same. dweight: a warp adds its units' terms per column in shared memory
+// (compensated fp32 sums), then the block adds its warps in order and writes one partial
+// row; csa_api.cu's fixed-order reduction adds the rows.
+template <int DTYPE>
+__global__ void __launch_bounds__(kRopeThreads) rope_scalar_bwd_kernel(RopeParams p) {
+  using E = Element<DTYPE>;
+  using T = typename E::T;
+  extern __shared__ float s_dw[];  // [warps][2][d]: sums and their compensation
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float* sum = s_dw + static_cast<size_t>(warp) * 2 * p.d;
+  float* cmp = sum + p.d;
+  if (p.partial != nullptr) {
+    for (int c = threadIdx.x; c < kRopeWarps * 2 * p.d; c += kRopeThreads) s_dw[c] = 0.f;
+    __syncthreads();
+  }
+  pdl_wait();
+  for (int64_t u = static_cast<int64_t>(blockIdx.x) * kRopeWarps + warp; u < p.units;
+       u += static_cast<int64_t>(gridDim.x) * kRopeWarps) {
+    const int64_t row = u / p.heads, head = u - row * p.heads;
+    const int32_t pos = p.pos != nullptr ? p.pos[row] : 0;
+    if (pos < 0) continue;
+    const T* x = static_cast<const T*>(p.x) + row * p.x_row + head * p.x_head;
+    const T* dy = static_cast<const T*>(p.dy) + row * p.dy_row + head * p.dy_head;
+    T* dx = static_cast<T*>(p.y) + row * p.y_row + head * p.y_head;
+    // f(column, gradient of n) for every column the lane owns; both of a pair are read
+    // before either is handed on
+    auto each = [&](auto f) {
+      for (int i = lane; i < p.rot / 2; i += 32) {
+        int a, b;
+        pair_columns(p, i, a, b);
+        float cs, sn;
+        turn_cos_sin(pos, p.turns[i], p.amp, cs, sn);
+        const float ga = E::to_float(dy[a]), gb = E::to_float(dy[b]);
+        f(a, ga * cs + gb * sn);
+        f(b, gb * cs - ga * sn);
+      }
+      for (int j = lane; j < p.d - p.rot; j += 32) {
+        const int c = other_column(p, j);
+        f(c, E::to_float(dy[c]));
+      }
+    };
+    if (!p.norm) {
+      each([&](int c, float g) { dx[c] = E::from_float(g); });
+      continue;
+    }
+    float ss = 0.f, dot = 0.f;
+    each([&](int c, float g) {
+      const float v = E::to_float(x[c]);
+      ss = fmaf(v, v, ss);
+      dot = fmaf(p.weight != nullptr ? g * p.weight[c] : g, v, dot);
+    });
+    const float n = static_cast<float>(p.d);
+    const float r = 1.f / sqrtf(warp_sum(ss) / n + p.eps);
+    const float k = warp_sum(dot) / n * r * r;  // mean(dn w xhat) * r
+    each([&](int c, float g) {
+      const float v = E::to_float(x[c]);
+      if (p.partial != nullptr) {
+        float s = sum[c], e = cmp[c];
+        neumaier_add(s, e, g * (v * r));
+        sum[c] = s;
+        cmp[c] = e;
+      }
+      dx[c] = E::from_float(r * ((p.weight != nullptr ? g * p.weight[c] : g) - v * k));
+    });
+  }
+  if (p.partial == nullptr) return;
+  __syncthreads();
+  for (int c = threadIdx.x; c < p.d; c += kRopeThreads) {
+    float s = 0.f, e = 0.f;
+    for (int w = 0; w < kRopeWarps; ++w) {
+      neumaier_add(s, e, s_dw[static_cast<size_t>(w) * 2 * p.d + c]);
+      neumaier_add(s, e, s_dw[static_cast<size_t>(w) * 2 * p.d + p.d + c]);
+    }
+    p.partial[static_cast<int64_t>(blockIdx.x) * p.d + c] = s + e;
+  }
+}
+
+// Blocks of the backward (= partial rows): enough to fill the GPU, at most one per warp's worth
+// of units.
+int64_t bwd_blocks(int64_t units, int sms) {
+  const int64_t want = (units + kRopeWarps - 1) / kRopeWarps, most = 2 * static_cast<int64_t>(sms);
+  return want < 1 ? 1 : (want < most ? want : most);
+}
+
+csa_status_t check_rope(int32_t dtype, int64_t rows, int32_t heads, int32_t d,
+                        const float* weight, int32_t norm, float eps, const int32_t* positions,
+                        const uint64_t* turns, int32_t rot_dim, int32_t rot_start, int32_t layout) {
+  if (rows < 0 || heads < 1 || d < 1 || (norm != 0 && norm != 1) || rot_dim < 0 ||
+      rot_dim % 2 != 0 || rot_start < 0 || !(eps >= 0.f) || std::isinf(eps))
+    return CSA_ERR_INVALID_VALUE;
+  if (d > CSA_MAX_HEAD_DIM || rows > INT_MAX / heads) return CSA_ERR_UNSUPPORTED;
+  if (dtype < CSA_DTYPE_BF16 || dtype > CSA_DTYPE_FP32 ||
+      (layout != CSA_ROPE_HALF && layout != CSA_ROPE_INTERLEAVED))
+    return CSA_ERR_UNSUPPORTED;
+  if (rot_dim > d || rot_start > d - rot_dim) return CSA_ERR_INVALID_VALUE;
+  if (norm == 0 && weight != nullptr) return CSA_ERR_INVALID_VALUE;
+  if (rot_dim > 0 && rows > 0 && (positions == nullptr || turns == nullptr))
+    return CSA_ERR_INVALID_VALUE;
+  if (!is_aligned(weight, 4) || !is_aligned(positions, 4) || !is_aligned(turns, 8))
+    return CSA_ERR_INVALID_VALUE;
+  return CSA_OK;
+}
+
+RopeParams rope_params(int64_t rows, int32_t heads, int32_t d, const float* weight, int32_t norm,
+                       float eps, const int32_t* positions, const uint64_t* turns, int32_t rot_dim,
+                       int32_t rot_start, int32_t layout, float amplitude) {
+  RopeParams p{};
+  p.weight = weight;
+  p.pos = positions;
+  p.turns = turns;
+  p.units = rows * heads;
+  p.heads = heads;
+  p.d = d;
+  p.rot = rot_dim;
+  p.start = rot_start;
+  p.norm = norm;
+  p.interleaved = layout == CSA_ROPE_INTERLEAVED;
+  p.eps = eps;
+  p.amp = amplitude;
+  return p;
+}
+
+}  // namespace
+}  // namespace csa
+
+using namespace csa;
+
+extern "C" csa_status_t csa_rope_table(int32_t rot_dim, double base, int32_t scaling, double factor,
+                                       double original_length, double beta_fast, double beta_slow,
+                                       uint64_t* turns_host, float* amplitude) {
+  if (rot_dim < 0 || rot_dim % 2 != 0 || !(base > 1.0) || std::isinf(base) ||
+      (rot_dim > 0 && turns_host == nullptr))
+    return CSA_ERR_INVALID_VALUE;
+  if (rot_dim > CSA_MAX_HEAD_DIM || scaling < CSA_ROPE_PLAIN || scaling > CSA_ROPE_YARN)
+    return CSA_ERR_UNSUPPORTED;
+  if (scaling != CSA_ROPE_PLAIN && (!(factor >= 1.0) || std::isinf(factor))) return CSA_ERR_INVALID_VALUE;
+  if (scaling == CSA_ROPE_YARN &&
+      (!(original_length >= 1.0) || std::isinf(original_length) || !(beta_fast > 0.0) ||
+       !(beta_slow > 0.0) || std::isinf(beta_fast) || std::isinf(beta_slow)))
+    return CSA_ERR_INVALID_VALUE;
+  const double two_pi = 6.283185307179586476925286766559;
+  double lo = 0.0, span = 1.0;
+  if (scaling == CSA_ROPE_YARN && rot_dim > 0) {
+    auto at = [&](double beta) {
+      return rot_dim * std::log(original_length / (two_pi * beta)) / (2.0 * std::log(base));
+    };
+    const double last = rot_dim - 1;
+    lo = std::fmin(std::fmax(std::floor(at(beta_fast)), 0.0), last);
+    const double hi = std::fmin(std::fmax(std::ceil(at(beta_slow)), 0.0), last);
+    span = std::fmax(hi - lo, 0.001);
+  }
+  for (int32_t i = 0; i < rot_dim / 2; ++i) {
+    double f = std::pow(base, -2.0 * i / rot_dim);
+    if (scaling == CSA_ROPE_LINEAR) f /= factor;
+    if (scaling == CSA_ROPE_YARN) {
+      const double m = std::fmin(std::fmax((i - lo) / span, 0.0), 1.0);
+      f = f / factor * m + f * (1.0 - m);
+    }
+    turns_host[i] = static_cast<uint64_t>(std::nearbyint(std::ldexp(f / two_pi, 64)));
+  }
+  if (amplitude != nullptr)
+    *amplitude = scaling == CSA_ROPE_YARN ? static_cast<float>(0.1 * std::log(factor) + 1.0) : 1.f;
+  return CSA_OK;
+}
+
+extern "C" csa_status_t csa_norm_rope_fwd(const void* x, int32_t dtype, int64_t rows, int32_t heads,
+                                          int32_t d, int64_t x_row_stride, int64_t x_head_stride,
+                                          const float* weight, int32_t norm, float eps,
+                                          const int32_t* positions, const uint64_t* turns,
+                                          int32_t rot_dim, int32_t rot_start, int32_t layout,
+                                          float amplitude, void* y, int64_t y_row_stride,
+                                          int64_t y_head_stride, csa_stream_t stream) {
+  csa_status_t st = check_rope(dtype, rows, heads, d, weight, norm, eps, positions, turns, rot_dim,
+                               rot_start, layout);
+  if (st != CSA_OK) return st;
+  if (x_row_stride < 0 || x_head_stride < 0 || y_row_stride < 0 || y_head_stride < 0)
+    return CSA_ERR_INVALID_VALUE;
+  const uintptr_t size = dtype_size(dtype);
+  if (!is_aligned(x, size) || !is_aligned(y, size)) return CSA_ERR_INVALID_VALUE;
+  if (rows == 0) return CSA_OK;
+  if (x == nullptr || y == nullptr) return CSA_ERR_INVALID_VALUE;
+  RopeParams p = rope_params(rows, heads, d, weight, norm, eps, positions, turns, rot_dim, rot_start,
+                             layout, amplitude);
+  p.x = x;
+  p.y = y;
+  p.x_row = x_row_stride;
+  p.x_head = x_head_stride;
+  p.y_row = y_row_stride;
+  p.y_head = y_head_stride;
+  const void* k = by_dtype(dtype, [](auto t) {
+    return reinterpret_cast<const void*>(rope_scalar_kernel<decltype(t)::value>);
+  });
+  const int64_t blocks = (p.units + kRopeWarps - 1) / kRopeWarps;
+  void* args[] = {&p};
+  if (launch_pdl(k, dim3(static_cast<unsigned>(blocks)), dim3(kRopeThreads), 0,
+                 reinterpret_cast<cudaStream_t>(stream), args) != cudaSuccess)
+    return CSA_ERR_CUDA;
+  return CSA_OK;
+}
+
+extern "C" size_t csa_norm_rope_bwd_workspace_bytes(int64_t rows, int32_t heads, int32_t d) {
+  if (rows < 0 || heads < 1 || d < 1 || d > CSA_MAX_HEAD_DIM || rows > INT_MAX / heads) return 0;
+  int dev = 0, sms = 0;
+  if (note(cudaGetDevice(&dev)) != cudaSuccess || device_sms(dev, &sms) != cudaSuccess) return 0;
+  return (static_cast<size_t>(bwd_blocks(rows * heads, sms)) * d * sizeof(float) + 15) &
+         ~static_cast<size_t>(15);
+}
+
+extern "C" csa_status_t csa_norm_rope_bwd(
+    const void* x, const void* dy, int32_t dtype, int64_t rows, int32_t heads, int32_t d,
+    int64_t x_row_stride, int64_t x_head_stride, int64_t dy_row_stride, int64_t dy_head_stride,
+    const float* weight, int32_t norm, float eps, const int32_t* positions, const uint64_t* turns,
+    int32_t rot_dim, int32_t rot_start, int32_t layout, float amplitude, void* dx,
+    int64_t dx_row_stride, int64_t dx_head_stride, float* dweight, int32_t accumulate_dweight,
+    void* workspace, size_t workspace_bytes, csa_stream_t stream) {
+  csa_status_t st = check_rope(dtype, rows, heads, d, weight, norm, eps, positions, turns, rot_dim,
+                               rot_start, layout);
+  if (st != CSA_OK) return st;
+  if (x_row_stride < 0 || x_head_stride < 0 || dy_row_stride < 0 || dy_head_stride < 0 ||
+      dx_row_stride < 0 || dx_head_stride < 0)
+    return CSA_ERR_INVALID_VALUE;
+  if (norm == 0 && dweight != nullptr) return CSA_ERR_INVALID_VALUE;
+  const uintptr_t size = dtype_size(dtype);
+  if (!is_aligned(x, size) || !is_aligned(dy, size) || !is_aligned(dx, size) ||
+      !is_aligned(dweight, 4) || !is_aligned(workspace, 16))
+    return CSA_ERR_INVALID_VALUE;
+  if (rows > 0 && ((norm != 0 && x == nullptr) || dy == nullptr || dx == nullptr))
+    return CSA_ERR_INVALID_VALUE;
+  if (rows == 0 && (dweight == nullptr || accumulate_dweight != 0)) return CSA_OK;
+  // the smallest partial is one row: refused before the device is asked
+  if (dweight != nullptr && (workspace == nullptr || workspace_bytes < sizeof(float) * d))
+    return CSA_ERR_WORKSPACE;
+  int dev = 0, sms = 0;
+  if (note(cudaGetDevice(&dev)) != cudaSuccess || device_sms(dev, &sms) != cudaSuccess)
+    return CSA_ERR_CUDA;
+  RopeParams p = rope_params(rows, heads, d, weight, norm, eps, positions, turns, rot_dim, rot_start,
+                             layout, amplitude);
+  const int64_t blocks = bwd_blocks(p.units, sms);
+  if (dweight != nullptr && workspace_bytes < static_cast<size_t>(blocks) * d * sizeof(float))
+    return CSA_ERR_WORKSPACE;
+  p.x = x;
+  p.dy = dy;
+  p.y = dx;
+  p.x_row = x_row_stride;
+  p.x_head = x_head_stride;
+  p.dy_row = dy_row_stride;
+  p.dy_head = dy_head_stride;
+  p.y_row = dx_row_stride;
+  p.y_head = dx_head_stride;
+  p.partial = dweight != nullptr ? static_cast<float*>(workspace) : nullptr;
+  const void* k = by_dtype(dtype, [](auto t) {
+    return reinterpret_cast<const void*>(rope_scalar_bwd_kernel<decltype(t)::value>);
+  });
+  const size_t smem = dweight != nullptr ? sizeof(float) * kRopeWarps * 2 * d : 0;
+  int bps = 0;
+  if (blocks_per_sm(dev, k, kRopeThreads, smem, &bps) != cudaSuccess) return CSA_ERR_CUDA;
+  if (bps < 1) return CSA_ERR_UNSUPPORTED;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  void* args[] = {&p};
+  if (launch_pdl(k, dim3(static_cast<unsigned>(blocks)), dim3(kRopeThreads), smem, s, args) !=
+      cudaSuccess)
+    return CSA_ERR_CUDA;
+  if (dweight == nullptr) return CSA_OK;
+  return launch_partial_reduce(p.partial, static_cast<int>(blocks), d, dweight,
+                               accumulate_dweight != 0, nullptr, s) == cudaSuccess
+             ? CSA_OK
+             : CSA_ERR_CUDA;
+}

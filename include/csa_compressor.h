@@ -70,6 +70,10 @@ typedef enum {
                                    kernel stopped early, outputs (dAPE included) are
                                    incomplete */
 #define CSA_DEVERR_LEAD 4       /* KPool: a negative lead */
+#define CSA_DEVERR_SLOT 5       /* cache: a slot >= num_slots (that row alone is skipped) */
+#define CSA_DEVERR_ENTRIES 6    /* cache attention: entries[s] < 0 or > max_pages * page_size */
+#define CSA_DEVERR_PAGE 7       /* cache attention: a page number a sequence needs is outside
+                                   [0, num_pages); its entries are not read */
 
 /* Limits checked on the host (CSA_ERR_UNSUPPORTED beyond them). */
 #define CSA_MAX_SEGMENTS 16384   /* S */
@@ -77,6 +81,27 @@ typedef enum {
 #define CSA_MAX_GENERIC_WINDOW 256 /* coff * ratio when d % 8 != 0 or a pointer is not 16-byte aligned */
 #define CSA_MAX_ELEMS 2147483647 /* capacity*coff*d and out_rows*d must stay below 2^31 */
 #define CSA_KPOOL_MAX_POOL 1024  /* KPool pool size */
+#define CSA_MAX_HEAD_DIM 1024    /* d of the head norm / rotation and of the cache attention */
+#define CSA_CACHE_GROUP 32       /* columns that share a scale byte in the quantised cache formats */
+
+/* Element types of csa_norm_rope_*, csa_cache_write and csa_cache_read. */
+#define CSA_DTYPE_BF16 0
+#define CSA_DTYPE_FP16 1
+#define CSA_DTYPE_FP32 2
+
+/* Frequency scaling of csa_rope_table. */
+#define CSA_ROPE_PLAIN 0
+#define CSA_ROPE_LINEAR 1
+#define CSA_ROPE_YARN 2
+
+/* Pairing of the rotated columns: column i with i + rot_dim/2, or 2i with 2i + 1. */
+#define CSA_ROPE_HALF 0
+#define CSA_ROPE_INTERLEAVED 1
+
+/* Formats of the paged cache (see csa_cache_write). */
+#define CSA_CACHE_BF16 0
+#define CSA_CACHE_E4M3 1
+#define CSA_CACHE_E2M1 2
 
 /* Text for a status code (static storage). */
 const char* csa_status_string(int status);
@@ -224,6 +249,174 @@ csa_status_t csa_kpool_fwd(const void* key, const void* gate, const int32_t* cu_
                            const int32_t* lead, int32_t S, int32_t pool, int32_t d,
                            int64_t capacity, void* out, int64_t out_rows, int32_t compress,
                            int32_t* dev_error, csa_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * Head norm and rotation: what queries and pooled entries go through before attention.
+ *
+ *   x is [rows, heads, d]; element (r, h, c) lies at x[r*x_row_stride + h*x_head_stride + c]
+ *   (strides in elements, the columns contiguous). For every row and head:
+ *     norm = 1:  n = x * rsqrt(mean over the d columns of x^2 + eps) * weight   (weight NULL: 1)
+ *     norm = 0:  n = x
+ *   then the rot_dim columns from rot_start on are turned in pairs (a, b), pair i by the
+ *   angle t = 2 pi * (positions[r] * turns[i] mod 2^64) / 2^64:
+ *     a' = amplitude * (a cos t - b sin t),   b' = amplitude * (a sin t + b cos t).
+ *   The product is exact integer arithmetic, so a position near 2^31 turns as exactly as
+ *   a small one. The columns outside the rotated part keep n. All arithmetic is in fp32
+ *   (cos and sin within 1e-6 for 16-bit types, which round by 2^-12 or more), rounded once.
+ *   A row whose position is negative is left out: its y (or dx) stays as it was, and it
+ *   adds nothing to dweight. So a padded pack needs no row count on the host.
+ * ------------------------------------------------------------------------------------ */
+
+/* Frequencies of the rotation, on the host: turns_host[i], i < rot_dim/2, is
+ * round(2^64 * f_i / (2 pi)), the part of a full turn that one position turns pair i by.
+ *   CSA_ROPE_PLAIN   f_i = base^(-2i/rot_dim)
+ *   CSA_ROPE_LINEAR  f_i / factor (position interpolation)
+ *   CSA_ROPE_YARN    (f_i / factor) m_i + f_i (1 - m_i), m_i = clamp((i - lo)/(hi - lo), 0, 1),
+ *                    lo = floor, hi = ceil of rot_dim ln(original_length / (2 pi b)) / (2 ln base)
+ *                    at b = beta_fast and b = beta_slow, clamped to [0, rot_dim - 1]
+ *                    (hi - lo at least 0.001); *amplitude = 0.1 ln(factor) + 1
+ * *amplitude (may be NULL) is 1 for the other two. factor, original_length and the betas are
+ * read only by the scalings that use them. CSA_ERR_INVALID_VALUE for an odd or negative
+ * rot_dim, base <= 1, factor < 1, original_length < 1 or betas that are not positive;
+ * CSA_ERR_UNSUPPORTED for rot_dim > CSA_MAX_HEAD_DIM or an unknown scaling. */
+csa_status_t csa_rope_table(int32_t rot_dim, double base, int32_t scaling, double factor,
+                            double original_length, double beta_fast, double beta_slow,
+                            uint64_t* turns_host, float* amplitude);
+
+/* Head norm and rotation, forward.
+ *   x, y        dtype [rows, heads, d] with their strides (device); y may be x itself with
+ *               the same strides, and overlaps it in no other way
+ *   weight      fp32 [d] (device) or NULL; must be NULL when norm = 0
+ *   positions   int32 [rows] (device); NULL: every row is taken, needs rot_dim = 0
+ *   turns       uint64 [rot_dim/2] (device), from csa_rope_table; NULL when rot_dim = 0
+ * rows = 0 is a valid no-op. CSA_ERR_INVALID_VALUE for NULL or misaligned pointers, odd
+ * rot_dim, rot_start + rot_dim > d, negative strides, eps negative or not finite;
+ * CSA_ERR_UNSUPPORTED for d > CSA_MAX_HEAD_DIM, rows * heads >= 2^31 or an unknown dtype or
+ * layout. The vector kernel runs when d, the strides and rot_start are multiples of 8
+ * and rot_dim of 16 (half) or 8 (interleaved), and x and y (weight too) are 16-byte
+ * aligned; anything else takes a scalar kernel. */
+csa_status_t csa_norm_rope_fwd(const void* x, int32_t dtype, int64_t rows, int32_t heads,
+                               int32_t d, int64_t x_row_stride, int64_t x_head_stride,
+                               const float* weight, int32_t norm, float eps,
+                               const int32_t* positions, const uint64_t* turns, int32_t rot_dim,
+                               int32_t rot_start, int32_t layout, float amplitude, void* y,
+                               int64_t y_row_stride, int64_t y_head_stride, csa_stream_t stream);
+
+/* Bytes of device workspace csa_norm_rope_bwd needs for these sizes on the current device
+ * when dweight is asked for (per-block dweight sums, reduced in a fixed order); 0 on bad
+ * sizes. */
+size_t csa_norm_rope_bwd_workspace_bytes(int64_t rows, int32_t heads, int32_t d);
+
+/* Gradients of csa_norm_rope_fwd from its input x (the statistics are recomputed).
+ *   dy, dx      dtype [rows, heads, d] with their strides; dx may be dy or x itself with the
+ *               same strides, and overlaps neither in another way
+ *   x           not read (may be NULL) when norm = 0
+ *   dweight     fp32 [d] or NULL (not wanted; must be NULL when norm = 0): the sum over rows
+ *               and heads of dn * x * rsqrt(...), dn the gradient turned back;
+ *               accumulate_dweight = 0 stores it, 1 adds it to the current contents. It may be
+ *               asked for with weight NULL (the gradient at a weight of ones).
+ *   workspace   csa_norm_rope_bwd_workspace_bytes(...) bytes, 16-byte aligned, when dweight
+ *               is asked for (CSA_ERR_WORKSPACE otherwise); calls that may run at the same time
+ *               need workspaces of their own
+ * dweight is bitwise reproducible (no atomics). Other arguments as for the forward. */
+csa_status_t csa_norm_rope_bwd(const void* x, const void* dy, int32_t dtype, int64_t rows,
+                               int32_t heads, int32_t d, int64_t x_row_stride,
+                               int64_t x_head_stride, int64_t dy_row_stride,
+                               int64_t dy_head_stride, const float* weight, int32_t norm, float eps,
+                               const int32_t* positions, const uint64_t* turns, int32_t rot_dim,
+                               int32_t rot_start, int32_t layout, float amplitude, void* dx,
+                               int64_t dx_row_stride, int64_t dx_head_stride, float* dweight,
+                               int32_t accumulate_dweight, void* workspace, size_t workspace_bytes,
+                               csa_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * Paged cache of entries. A pool of num_pages pages of page_size entries each; slot
+ * page * page_size + offset holds one entry of `heads` heads of d columns:
+ *   CSA_CACHE_BF16   data bf16 [slots, heads, d]; scales unused (NULL)
+ *   CSA_CACHE_E4M3   data e4m3 [slots, heads, d], scales uint8 [slots, heads, d/32]
+ *   CSA_CACHE_E2M1   data [slots, heads, d/2] bytes, column 2j in a byte's low four bits and
+ *                    2j + 1 in its high ones, scales uint8 [slots, heads, d/32]
+ * A scale byte k stands for 2^(k - 127) and belongs to 32 consecutive columns; a value is
+ * code * scale. Writing picks the smallest scale (from 2^-127 on) at which the group's
+ * largest magnitude does not exceed the format's largest value (448; 6), so nothing
+ * saturates, and rounds value / scale to the nearest code, ties to the even one. A group
+ * that holds an infinity or NaN gets scale byte 255 and reads back as NaN.
+ * ------------------------------------------------------------------------------------ */
+
+/* Writes rows into the cache.
+ *   x           dtype [rows, heads, d] with row and head strides in elements (device)
+ *   slots       int64 [rows] (device): where each row goes; a negative one leaves its row
+ *               out; the others must differ from one another within a call (the contents of a
+ *               slot that two rows name are unspecified). slots >= num_slots: the row is left
+ *               out and CSA_DEVERR_SLOT reported
+ *   data, scales   the pool as above; every other slot stays as it was
+ * d must be a multiple of 32 for the quantised formats (CSA_ERR_UNSUPPORTED). The vector
+ * kernel runs when x, data (and d and the strides in multiples of 8 elements) are 16-byte
+ * aligned; anything else takes a scalar kernel. */
+csa_status_t csa_cache_write(const void* x, int32_t dtype, int64_t rows, int32_t heads, int32_t d,
+                             int64_t x_row_stride, int64_t x_head_stride, const int64_t* slots,
+                             int64_t num_slots, int32_t format, void* data, uint8_t* scales,
+                             int32_t* dev_error, csa_stream_t stream);
+
+/* Reads rows of the cache back: out[r] = the entry in slots[r], in `dtype`, out [rows, heads,
+ * d] with strides in elements. A negative slot leaves its row of out as it was, so does one
+ * >= num_slots, which reports CSA_DEVERR_SLOT. Any slot may be read by several rows. */
+csa_status_t csa_cache_read(const void* data, const uint8_t* scales, int32_t format,
+                            const int64_t* slots, int64_t rows, int64_t num_slots, int32_t heads,
+                            int32_t d, void* out, int32_t dtype, int64_t out_row_stride,
+                            int64_t out_head_stride, int32_t* dev_error, csa_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * Attention of new tokens over the paged cache; an entry is key and value at once, as the
+ * compressor's pooled kv is.
+ *
+ *   Sequence s has the new tokens [cu_seqlens[s], cu_seqlens[s+1]) and entries[s] entries;
+ *   entry e lies in page page_table[s*max_pages + e / page_size] at offset e % page_size.
+ *   Its token i stands at position p = first[s] + i (first NULL: 0) and sees the entries
+ *   e < entries[s] with (e + 1) * ratio <= p + 1, those whose block of `ratio` tokens is
+ *   complete by then (ratio 1: causal attention to single tokens); ratio 0: all of them.
+ *   Query head h reads the entries' head h / (q_heads / kv_heads):
+ *     out = sum_e w_e k_e,  w_e = exp(softmax_scale q.k_e) / (sum over seen entries + exp(sink[h]))
+ *     lse = log(that denominator)
+ *   (sink NULL: no such term). A token that sees nothing gets out = 0 and lse = sink[h], or
+ *   -inf without a sink. An infinity or NaN in an entry reaches only the tokens that see it.
+ *   Scores, maxima and sums are fp32; the weights are rounded to bf16 before the second
+ *   product on the tensor cores (off by at most 2^-8 of each, as the outputs themselves are).
+ * ------------------------------------------------------------------------------------ */
+
+/* Bytes of device workspace csa_cache_attn needs on the current device; 0 on bad sizes.
+ * max_entries = max_pages * page_size of the call. */
+size_t csa_cache_attn_workspace_bytes(int32_t S, int64_t tokens, int32_t q_heads, int32_t kv_heads,
+                                      int32_t d, int64_t max_entries);
+
+/*   q           bf16 [tokens, q_heads, d], row and head strides in elements (device)
+ *   cu_seqlens  int32 [S+1] (device), non-decreasing, cu_seqlens[S] <= tokens; rows of out and
+ *               lse that belong to no sequence stay as they were
+ *   data, scales, format   the cache of num_pages * page_size slots, kv_heads heads of d
+ *   page_table  int32 [S, max_pages] (device); only the pages that entries[s] needs are read
+ *   entries     int32 [S] (device), first int32 [S] (device) or NULL
+ *   sink        fp32 [q_heads] (device) or NULL
+ *   out         bf16 [tokens, q_heads, d], row and head strides in elements
+ *   lse         fp32 [tokens, q_heads], contiguous, or NULL
+ *   workspace   at least csa_cache_attn_workspace_bytes(...) bytes, 16-byte aligned
+ *               (CSA_ERR_WORKSPACE otherwise); calls that may run at the same time need
+ *               workspaces of their own
+ * CSA_ERR_INVALID_VALUE: NULL or misaligned pointers, q_heads not a multiple of kv_heads,
+ * negative sizes or strides, softmax_scale not finite. CSA_ERR_UNSUPPORTED: d >
+ * CSA_MAX_HEAD_DIM, quantised formats with d not a multiple of 32, S > CSA_MAX_SEGMENTS,
+ * tokens * q_heads or max_pages * page_size >= 2^31, an unknown format. A bad
+ * cu_seqlens or entries (CSA_DEVERR_CU_SEQLENS, CSA_DEVERR_ENTRIES) skips all outputs; after
+ * CSA_DEVERR_PAGE the outputs of that sequence are unspecified. Results are bitwise
+ * reproducible for the same arguments on the same device. */
+csa_status_t csa_cache_attn(const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                            const int32_t* cu_seqlens, int32_t S, int64_t tokens, int32_t q_heads,
+                            int32_t kv_heads, int32_t d, const void* data, const uint8_t* scales,
+                            int32_t format, const int32_t* page_table, int32_t max_pages,
+                            int64_t num_pages, int32_t page_size, const int32_t* entries,
+                            const int32_t* first, int32_t ratio, float softmax_scale,
+                            const float* sink, void* out, int64_t out_row_stride,
+                            int64_t out_head_stride, float* lse, void* workspace,
+                            size_t workspace_bytes, int32_t* dev_error, csa_stream_t stream);
 
 #ifdef __cplusplus
 }
