@@ -6,37 +6,11 @@
 #include <type_traits>
 
 #include "csa_compressor.h"
-#include "csa_element.cuh"
+#include "csa_attn_tile.cuh"
 #include "csa_internal.h"
 
 namespace csa {
 namespace {
-
-struct AttnParams {
-  const uint16_t* q;
-  const int32_t* cu;
-  const uint8_t* data;
-  const uint8_t* scales;
-  const int32_t* table;
-  const int32_t* entries;
-  const int32_t* first;
-  const float* sink;
-  uint16_t* out;
-  float* lse;
-  int32_t* dev_error;
-  int32_t* status;  // workspace: 0, or why the call's lengths were refused
-  int64_t q_row, q_head, out_row, out_head;
-  int64_t tokens, num_pages, max_entries;
-  int S, q_heads, kv_heads, group, d, max_pages, page_size, ratio;
-  float scale;  // softmax_scale
-};
-
-// Entries that the token at position pos sees, of a sequence's n.
-__device__ __forceinline__ int visible(int64_t pos, int ratio, int n) {
-  if (ratio == 0) return n;
-  const int64_t done = pos + 1 <= 0 ? 0 : (pos + 1) / ratio;
-  return done < n ? static_cast<int>(done) : n;
-}
 
 // Sequence of a token, and -1 when it belongs to none (cu holds S + 1 non-decreasing offsets):
 // the largest s with cu[s] <= t whose end lies behind t.
@@ -51,9 +25,38 @@ __device__ __forceinline__ int sequence_of(const int32_t* cu, int S, int64_t t) 
   return lo;
 }
 
-// Checks the call's lengths and publishes the verdict for the kernels behind it.
-constexpr int kPlanThreads = 256;
-__global__ void __launch_bounds__(kPlanThreads) attn_check_kernel(AttnParams p) {
+// Exclusive sum over the block, and the block's total (64 bits).
+constexpr int kPlanThreads = 1024;
+__device__ __forceinline__ int64_t plan_scan(int64_t v, int64_t* warps, int64_t& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) warps[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int64_t s = warps[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xFFFFFFFFu, s, o);
+      if (lane >= o) s += y;
+    }
+    warps[lane] = s;
+  }
+  __syncthreads();
+  total = warps[31];
+  return x - v + (warp > 0 ? warps[warp - 1] : 0);
+}
+
+// One block: checks the call's lengths, publishes the verdict for the kernels behind it, and
+// (units wanted) lists the units, their first tiles and where each CTA's share begins.
+__global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnParams p) {
+  extern __shared__ int s_first[];  // [S + 1] first row block of each sequence
+  __shared__ int64_t s_warps[32];
   pdl_wait();
   int bad = 0;
   for (int s = threadIdx.x; s < p.S; s += kPlanThreads) {
@@ -62,10 +65,63 @@ __global__ void __launch_bounds__(kPlanThreads) attn_check_kernel(AttnParams p) 
     if (n < 0 || n > p.max_entries) bad |= 2;
   }
   const int cu_bad = __syncthreads_or(bad & 1), n_bad = __syncthreads_or(bad & 2);
+  const int code = cu_bad ? CSA_DEVERR_CU_SEQLENS : n_bad ? CSA_DEVERR_ENTRIES : 0;
   if (threadIdx.x == 0) {
-    const int code = cu_bad ? CSA_DEVERR_CU_SEQLENS : n_bad ? CSA_DEVERR_ENTRIES : 0;
     *p.status = code;
     if (code != 0 && p.dev_error != nullptr) *p.dev_error = code;
+  }
+  if (code != 0 || p.units == nullptr) return;
+  const int per = (p.S + kPlanThreads - 1) / kPlanThreads;
+  const int lo = min(p.S, static_cast<int>(threadIdx.x) * per), hi = min(p.S, lo + per);
+  int64_t mine = 0, blocks = 0;
+  for (int s = lo; s < hi; ++s) mine += (sequence_rows(p, s) + kAttnRows - 1) / kAttnRows;
+  int64_t at = plan_scan(mine, s_warps, blocks);
+  for (int s = lo; s < hi; ++s) {
+    s_first[s] = static_cast<int>(at);
+    at += (sequence_rows(p, s) + kAttnRows - 1) / kAttnRows;
+  }
+  if (threadIdx.x == 0) s_first[p.S] = static_cast<int>(blocks);
+  __syncthreads();
+  const int64_t units = blocks * p.kv_heads;
+  int64_t all = 0;
+  for (int64_t u0 = 0; u0 < units; u0 += kPlanThreads) {
+    const int64_t i = u0 + threadIdx.x;
+    AttnUnit u{0, 0, 0, 0};
+    if (i < units) {
+      const int b = static_cast<int>(i / p.kv_heads);
+      int l = 0, h = p.S;  // s_first[l] <= b < s_first[h]
+      while (h - l > 1) {
+        const int mid = (l + h) / 2;
+        if (s_first[mid] <= b) l = mid;
+        else h = mid;
+      }
+      u = {l, static_cast<int>(i - static_cast<int64_t>(b) * p.kv_heads), b - s_first[l], 0};
+      const int seen = unit_entries(p, u);
+      u.tiles = seen <= kAttnEntries ? 1 : (seen - 1) / kAttnEntries + 1;
+    }
+    int64_t sum = 0;
+    const int64_t first = all + plan_scan(u.tiles, s_warps, sum);
+    if (i < units) {
+      p.units[i] = u;
+      p.unit_first[i] = first;
+    }
+    all += sum;
+  }
+  if (threadIdx.x == 0) {
+    p.unit_first[units] = all;
+    *p.tiles = all;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < p.ctas; i += kPlanThreads) {
+    const int64_t t = attn_share(all, p.ctas, i);
+    if (t >= all) continue;
+    int64_t l = 0, h = units;  // unit_first[l] <= t < unit_first[h]
+    while (h - l > 1) {
+      const int64_t mid = (l + h) / 2;
+      if (p.unit_first[mid] <= t) l = mid;
+      else h = mid;
+    }
+    p.starts[i] = {static_cast<int32_t>(l), static_cast<int32_t>(t - p.unit_first[l])};
   }
 }
 
@@ -151,6 +207,12 @@ __global__ void __launch_bounds__(kScalarThreads) attn_scalar_kernel(AttnParams 
   if (p.lse != nullptr && lane == 0) p.lse[u] = top == -INFINITY ? -INFINITY : top + logf(z);
 }
 
+template <typename F>
+auto by_format(int format, F f) {
+  return format == CSA_CACHE_BF16   ? f(std::integral_constant<int, CSA_CACHE_BF16>{})
+         : format == CSA_CACHE_E4M3 ? f(std::integral_constant<int, CSA_CACHE_E4M3>{})
+                                    : f(std::integral_constant<int, CSA_CACHE_E2M1>{});
+}
 const void* scalar_kernel_for(int format, int d) {
   auto pick = [&](auto f) -> const void* {
     constexpr int F = decltype(f)::value;
@@ -158,9 +220,7 @@ const void* scalar_kernel_for(int format, int d) {
            : d <= 512 ? reinterpret_cast<const void*>(attn_scalar_kernel<F, 16>)
                       : reinterpret_cast<const void*>(attn_scalar_kernel<F, 32>);
   };
-  return format == CSA_CACHE_BF16   ? pick(std::integral_constant<int, CSA_CACHE_BF16>{})
-         : format == CSA_CACHE_E4M3 ? pick(std::integral_constant<int, CSA_CACHE_E4M3>{})
-                                    : pick(std::integral_constant<int, CSA_CACHE_E2M1>{});
+  return by_format(format, pick);
 }
 
 csa_status_t check_attn_sizes(int32_t S, int64_t tokens, int32_t q_heads, int32_t kv_heads,
@@ -175,6 +235,52 @@ csa_status_t check_attn_sizes(int32_t S, int64_t tokens, int32_t q_heads, int32_
 }
 
 constexpr size_t kStatusBytes = 16;
+constexpr int kTileMaxDim = 512;
+
+int tile_chunks(int d) { return d <= 128 ? 2 : d <= 256 ? 4 : 8; }
+
+template <typename F>
+auto by_chunks(int chunks, F f) {
+  return chunks == 2   ? f(std::integral_constant<int, 2>{})
+         : chunks == 4 ? f(std::integral_constant<int, 4>{})
+                       : f(std::integral_constant<int, 8>{});
+}
+
+// The workspace: the plan, then the pieces. base may be null (sizes only).
+size_t lay_out(AttnParams& p, unsigned char* base) {
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    unsigned char* r = base == nullptr ? nullptr : base + at;
+    at += (bytes + 255) & ~static_cast<size_t>(255);
+    return r;
+  };
+  unsigned char* head = take(kStatusBytes);
+  p.status = reinterpret_cast<int32_t*>(head);
+  p.tiles = base == nullptr ? nullptr : reinterpret_cast<int64_t*>(head + 8);
+  p.starts = reinterpret_cast<AttnStart*>(take(sizeof(AttnStart) * p.ctas));
+  p.units = reinterpret_cast<AttnUnit*>(take(sizeof(AttnUnit) * p.max_units));
+  p.unit_first = reinterpret_cast<int64_t*>(take(sizeof(int64_t) * (p.max_units + 1)));
+  const size_t pieces = 2 * static_cast<size_t>(p.ctas);
+  p.part_ml = reinterpret_cast<float*>(take(pieces * 2 * kAttnRows * sizeof(float)));
+  p.part_o = reinterpret_cast<float*>(take(pieces * kAttnRows * (tile_chunks(p.d) * 64) * sizeof(float)));
+  return at;
+}
+
+// Sizes that the workspace depends on; d beyond the tile kernel's needs the status alone.
+cudaError_t plan_sizes(AttnParams& p, int32_t S, int64_t tokens, int32_t q_heads, int32_t kv_heads, int32_t d) {
+  int dev = 0, sms = 0;
+  cudaError_t e = note(cudaGetDevice(&dev));
+  if (e != cudaSuccess || (e = device_sms(dev, &sms)) != cudaSuccess) return e;
+  p.S = S;
+  p.tokens = tokens;
+  p.q_heads = q_heads;
+  p.kv_heads = kv_heads;
+  p.group = q_heads / kv_heads;
+  p.d = d;
+  p.ctas = sms;
+  p.max_units = ((tokens * p.group + kAttnRows - 1) / kAttnRows + S) * kv_heads;
+  return cudaSuccess;
+}
 
 }  // namespace
 }  // namespace csa
@@ -184,7 +290,10 @@ using namespace csa;
 extern "C" size_t csa_cache_attn_workspace_bytes(int32_t S, int64_t tokens, int32_t q_heads,
                                                  int32_t kv_heads, int32_t d, int64_t max_entries) {
   if (check_attn_sizes(S, tokens, q_heads, kv_heads, d, max_entries) != CSA_OK) return 0;
-  return kStatusBytes;
+  if (d > kTileMaxDim) return kStatusBytes;
+  AttnParams p{};
+  if (plan_sizes(p, S, tokens, q_heads, kv_heads, d) != cudaSuccess) return 0;
+  return lay_out(p, nullptr);
 }
 
 extern "C" csa_status_t csa_cache_attn(
@@ -219,6 +328,18 @@ extern "C" csa_status_t csa_cache_attn(
   if (workspace == nullptr || workspace_bytes < kStatusBytes) return CSA_ERR_WORKSPACE;
 
   AttnParams p{};
+  if (plan_sizes(p, S, tokens, q_heads, kv_heads, d) != cudaSuccess) return CSA_ERR_CUDA;
+  // a call's pointers and strides decide between the kernels, its workspace serves either
+  const bool tile = d <= kTileMaxDim && d % 8 == 0 && q_row_stride % 8 == 0 && q_head_stride % 8 == 0 &&
+                    out_row_stride % 8 == 0 && out_head_stride % 8 == 0 && is_aligned(q, 16) &&
+                    is_aligned(out, 16) && is_aligned(data, 16);
+  if (d <= kTileMaxDim) {
+    if (workspace_bytes < lay_out(p, nullptr)) return CSA_ERR_WORKSPACE;
+    lay_out(p, static_cast<unsigned char*>(workspace));
+  } else {
+    p.status = static_cast<int32_t*>(workspace);
+  }
+  if (!tile) p.units = nullptr;
   p.q = static_cast<const uint16_t*>(q);
   p.cu = cu_seqlens;
   p.data = static_cast<const uint8_t*>(data);
@@ -230,28 +351,43 @@ extern "C" csa_status_t csa_cache_attn(
   p.out = static_cast<uint16_t*>(out);
   p.lse = lse;
   p.dev_error = dev_error;
-  p.status = static_cast<int32_t*>(workspace);
   p.q_row = q_row_stride;
   p.q_head = q_head_stride;
   p.out_row = out_row_stride;
   p.out_head = out_head_stride;
-  p.tokens = tokens;
   p.num_pages = num_pages;
   p.max_entries = max_entries;
-  p.S = S;
-  p.q_heads = q_heads;
-  p.kv_heads = kv_heads;
-  p.group = q_heads / kv_heads;
-  p.d = d;
   p.max_pages = max_pages;
   p.page_size = page_size;
   p.ratio = ratio;
   p.scale = softmax_scale;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   void* args[] = {&p};
-  if (launch_pdl(reinterpret_cast<const void*>(attn_check_kernel), dim3(1), dim3(kPlanThreads), 0, cs,
-                 args) != cudaSuccess)
-    return CSA_ERR_CUDA;
+  int dev = 0, bps = 0;
+  if (note(cudaGetDevice(&dev)) != cudaSuccess) return CSA_ERR_CUDA;
+  const size_t plan_smem = sizeof(int) * (static_cast<size_t>(S) + 1);
+  const void* plan = reinterpret_cast<const void*>(attn_plan_kernel);
+  if (blocks_per_sm(dev, plan, kPlanThreads, plan_smem, &bps) != cudaSuccess) return CSA_ERR_CUDA;
+  if (launch_pdl(plan, dim3(1), dim3(kPlanThreads), plan_smem, cs, args) != cudaSuccess) return CSA_ERR_CUDA;
+  if (tile) {
+    const int nc = tile_chunks(d);
+    size_t smem = 0;
+    const void *k = nullptr, *join = nullptr;
+    by_chunks(nc, [&](auto c) {
+      constexpr int NC = decltype(c)::value;
+      smem = TileShape<NC>::kSmemBytes;
+      join = reinterpret_cast<const void*>(attn_join_kernel<NC>);
+      k = by_format(format, [](auto f) {
+        return reinterpret_cast<const void*>(attn_tile_kernel<NC, decltype(f)::value>);
+      });
+      return 0;
+    });
+    if (blocks_per_sm(dev, k, kTileThreads, smem, &bps) != cudaSuccess) return CSA_ERR_CUDA;
+    if (bps < 1) return CSA_ERR_UNSUPPORTED;
+    if (launch_pdl(k, dim3(p.ctas), dim3(kTileThreads), smem, cs, args) != cudaSuccess) return CSA_ERR_CUDA;
+    return launch_pdl(join, dim3(p.ctas, kAttnRows / 8), dim3(256), 0, cs, args) == cudaSuccess ? CSA_OK
+                                                                                               : CSA_ERR_CUDA;
+  }
   const int64_t warps = tokens * q_heads;
   const int64_t blocks = (warps + kScalarThreads / 32 - 1) / (kScalarThreads / 32);
   return launch_pdl(scalar_kernel_for(format, d), dim3(static_cast<unsigned>(blocks)),

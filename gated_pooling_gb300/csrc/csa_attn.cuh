@@ -1,0 +1,77 @@
+// csa_attn.cuh -- what the kernels of the cache attention share: the call's parameters, the
+// visibility rule, and the work list that the plan kernel leaves in the workspace.
+#pragma once
+
+#include <stdint.h>
+
+#include "csa_compressor.h"
+#include "csa_element.cuh"
+
+namespace csa {
+
+constexpr int kAttnRows = 64;      // (token, head) rows of a unit
+constexpr int kAttnEntries = 128;  // entries of a tile
+
+// A unit is up to 64 consecutive rows (token, head of the group) of one sequence and cache head;
+// its work is a run of tiles of 128 entries, at least one. The tiles of all units in order are
+// split evenly over the CTAs (attn_share).
+struct AttnUnit {
+  int32_t s, kvh, block, tiles;
+};
+struct AttnStart {  // where a CTA's share begins
+  int32_t unit, tile;
+};
+
+struct AttnParams {
+  const uint16_t* q;
+  const int32_t* cu;
+  const uint8_t* data;
+  const uint8_t* scales;
+  const int32_t* table;
+  const int32_t* entries;
+  const int32_t* first;
+  const float* sink;
+  uint16_t* out;
+  float* lse;
+  int32_t* dev_error;
+  // workspace
+  int32_t* status;      // 0, or why the call's lengths were refused
+  int64_t* tiles;       // all units' tiles
+  AttnStart* starts;    // [ctas + 1]
+  AttnUnit* units;      // [max_units]
+  int64_t* unit_first;  // [max_units + 1]: first tile of each unit
+  float* part_o;        // [2 ctas][64][dpad]: sums of the pieces of units that CTAs share
+  float* part_ml;       // [2 ctas][2][64]: their maxima (in log2) and weight sums
+  int64_t q_row, q_head, out_row, out_head;
+  int64_t tokens, num_pages, max_entries, max_units;
+  int S, q_heads, kv_heads, group, d, max_pages, page_size, ratio, ctas;
+  float scale;  // softmax_scale
+};
+
+// Entries that the token at position pos sees, of a sequence's n.
+__device__ __forceinline__ int visible(int64_t pos, int ratio, int n) {
+  if (ratio == 0) return n;
+  const int64_t done = pos + 1 <= 0 ? 0 : (pos + 1) / ratio;
+  return done < n ? static_cast<int>(done) : n;
+}
+__device__ __forceinline__ int visible_to_token(const AttnParams& p, int s, int token, int n) {
+  return visible(static_cast<int64_t>(p.first != nullptr ? __ldg(p.first + s) : 0) + token, p.ratio, n);
+}
+// Rows of a sequence and cache head (below 2^31: tokens * q_heads is).
+__device__ __forceinline__ int sequence_rows(const AttnParams& p, int s) {
+  return (__ldg(p.cu + s + 1) - __ldg(p.cu + s)) * p.group;
+}
+// Entries that some row of the unit sees.
+__device__ __forceinline__ int unit_entries(const AttnParams& p, const AttnUnit& u) {
+  const int rows = sequence_rows(p, u.s);
+  const int last = min(u.block * kAttnRows + kAttnRows, rows) - 1;
+  return visible_to_token(p, u.s, last / p.group, __ldg(p.entries + u.s));
+}
+
+// First tile of CTA i's share of all tiles; at most one CTA per tile.
+__device__ __forceinline__ int64_t attn_share(int64_t tiles, int ctas, int i) {
+  const int64_t n = tiles < ctas ? tiles : ctas;
+  return i >= n ? tiles : tiles * i / n;
+}
+
+}  // namespace csa
