@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnParams p) {
   int64_t all = 0;
   for (int64_t u0 = 0; u0 < units; u0 += kPlanThreads) {
     const int64_t i = u0 + threadIdx.x;
-    AttnUnit u{0, 0, 0, 0};
+    AttnUnit u{};
     if (i < units) {
       const int b = static_cast<int>(i / p.kv_heads);
       int l = 0, h = p.S;  // s_first[l] <= b < s_first[h]
@@ -95,9 +95,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnParams p) {
         if (s_first[mid] <= b) l = mid;
         else h = mid;
       }
-      u = {l, static_cast<int>(i - static_cast<int64_t>(b) * p.kv_heads), b - s_first[l], 0};
-      const int seen = unit_entries(p, u);
-      u.tiles = seen <= kAttnEntries ? 1 : (seen - 1) / kAttnEntries + 1;
+      u = make_unit(p, l, static_cast<int>(i - static_cast<int64_t>(b) * p.kv_heads), b - s_first[l]);
     }
     int64_t sum = 0;
     const int64_t first = all + plan_scan(u.tiles, s_warps, sum);
@@ -114,14 +112,22 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnParams p) {
   __syncthreads();
   for (int i = threadIdx.x; i < p.ctas; i += kPlanThreads) {
     const int64_t t = attn_share(all, p.ctas, i);
-    if (t >= all) continue;
+    AttnStart start{};
+    start.left = attn_share(all, p.ctas, i + 1) - t;
+    if (start.left == 0) {
+      p.starts[i] = start;
+      continue;
+    }
     int64_t l = 0, h = units;  // unit_first[l] <= t < unit_first[h]
     while (h - l > 1) {
       const int64_t mid = (l + h) / 2;
       if (p.unit_first[mid] <= t) l = mid;
       else h = mid;
     }
-    p.starts[i] = {static_cast<int32_t>(l), static_cast<int32_t>(t - p.unit_first[l])};
+    start.u = p.units[l];
+    start.unit = static_cast<int32_t>(l);
+    start.tile = static_cast<int32_t>(t - p.unit_first[l]);
+    p.starts[i] = start;
   }
 }
 

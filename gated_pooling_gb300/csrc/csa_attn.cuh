@@ -15,12 +15,21 @@ constexpr int kAttnEntries = 128;  // entries of a tile
 // A unit is up to 64 consecutive rows (token, head of the group) of one sequence and cache head;
 // its work is a run of tiles of 128 entries, at least one. The tiles of all units in order are
 // split evenly over the CTAs (attn_share).
-struct AttnUnit {
+struct alignas(16) AttnUnit {
   int32_t s, kvh, block, tiles;
+  int32_t token, rows;  // the sequence's first token, and its rows
+  int32_t first;        // position of that token
+  int32_t n;            // the sequence's entries
+  int32_t seen_all;     // entries that every row of the unit sees
+  int32_t seen;         // entries that some row sees
+  int32_t pad[2];
 };
-struct AttnStart {  // where a CTA's share begins
+struct alignas(16) AttnStart {  // a CTA's share: its first unit, the tile there, and how many tiles
+  AttnUnit u;
   int32_t unit, tile;
+  int64_t left;
 };
+static_assert(sizeof(AttnUnit) == 48 && sizeof(AttnStart) == 64, "read in 16-byte pieces");
 
 struct AttnParams {
   const uint16_t* q;
@@ -37,7 +46,7 @@ struct AttnParams {
   // workspace
   int32_t* status;      // 0, or why the call's lengths were refused
   int64_t* tiles;       // all units' tiles
-  AttnStart* starts;    // [ctas + 1]
+  AttnStart* starts;    // [ctas]
   AttnUnit* units;      // [max_units]
   int64_t* unit_first;  // [max_units + 1]: first tile of each unit
   float* part_o;        // [2 ctas][64][dpad]: sums of the pieces of units that CTAs share
@@ -54,18 +63,25 @@ __device__ __forceinline__ int visible(int64_t pos, int ratio, int n) {
   const int64_t done = pos + 1 <= 0 ? 0 : (pos + 1) / ratio;
   return done < n ? static_cast<int>(done) : n;
 }
-__device__ __forceinline__ int visible_to_token(const AttnParams& p, int s, int token, int n) {
-  return visible(static_cast<int64_t>(p.first != nullptr ? __ldg(p.first + s) : 0) + token, p.ratio, n);
-}
 // Rows of a sequence and cache head (below 2^31: tokens * q_heads is).
 __device__ __forceinline__ int sequence_rows(const AttnParams& p, int s) {
   return (__ldg(p.cu + s + 1) - __ldg(p.cu + s)) * p.group;
 }
-// Entries that some row of the unit sees.
-__device__ __forceinline__ int unit_entries(const AttnParams& p, const AttnUnit& u) {
-  const int rows = sequence_rows(p, u.s);
-  const int last = min(u.block * kAttnRows + kAttnRows, rows) - 1;
-  return visible_to_token(p, u.s, last / p.group, __ldg(p.entries + u.s));
+// A unit of sequence s from its place.
+__device__ __forceinline__ AttnUnit make_unit(const AttnParams& p, int s, int kvh, int block) {
+  AttnUnit u{};
+  u.s = s;
+  u.kvh = kvh;
+  u.block = block;
+  u.token = __ldg(p.cu + s);
+  u.rows = sequence_rows(p, s);
+  u.first = p.first != nullptr ? __ldg(p.first + s) : 0;
+  u.n = __ldg(p.entries + s);
+  const int last = min(block * kAttnRows + kAttnRows, u.rows) - 1;
+  u.seen_all = visible(static_cast<int64_t>(u.first) + block * kAttnRows / p.group, p.ratio, u.n);
+  u.seen = visible(static_cast<int64_t>(u.first) + last / p.group, p.ratio, u.n);
+  u.tiles = u.seen <= kAttnEntries ? 1 : (u.seen - 1) / kAttnEntries + 1;
+  return u;
 }
 
 // First tile of CTA i's share of all tiles; at most one CTA per tile.

@@ -11,8 +11,9 @@
 // columns) leaves room for S^T at d = 512, where O with the rows along M would fill the tensor
 // memory. With few rows per sequence (decoding) no part of the 128 rows is idle.
 //
-// Warps: 0-7 softmax (a warp reads the 32 tensor-memory lanes of its quadrant, each group of
-// four warps 32 of the 64 rows), 8 issues the products, 9-16 fetch: they follow the page table,
+// Warps: 0-15 softmax (a warp reads the 32 tensor-memory lanes of its quadrant, each group of
+// four warps 16 of the 64 rows), 16 issues the products (17-19 only complete its register
+// group), 20-27 fetch: they follow the page table,
 // widen 8- and 4-bit codes to bf16 (exact, but for bf16's own subnormals) and store the swizzled tile; a pair of
 // 64-column chunks (32 KB) is the unit of the ring, and the next pair's loads are in flight
 // in registers while one is stored.
@@ -33,9 +34,14 @@
 
 namespace csa {
 
-constexpr int kTileSoftWarps = 8, kTileLoadWarps = 8;
+constexpr int kTileSoftWarps = 16, kTileLoadWarps = 8;
+constexpr int kSoftThreads = kTileSoftWarps * 32;
+constexpr int kSoftCols = 16;  // rows of a softmax thread's group
 constexpr int kTileLoaders = kTileLoadWarps * 32;
-constexpr int kTileThreads = (kTileSoftWarps + 1 + kTileLoadWarps) * 32;
+constexpr int kTileFirstLoader = kTileSoftWarps + 4;
+constexpr int kTileThreads = (kTileFirstLoader + kTileLoadWarps) * 32;
+// Registers a thread: 896 threads launch with 72, and 16 x 72 + 4 x 40 + 8 x 88 = 28 x 72.
+constexpr int kIssueRegs = 40, kLoadRegs = 88;
 constexpr int kChunkBytes = kAttnEntries * 128;  // 128 entries x 64 columns
 constexpr int kPairBytes = 2 * kChunkBytes;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -149,31 +155,47 @@ __device__ __forceinline__ void tile_wait(TileSmall& sm, const AttnParams& p, ui
   }
 }
 
+// Place in the ring of pairs: slot, and the parity of its current lap.
+template <int RING>
+struct RingAt {
+  int slot = 0;
+  uint32_t lap = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == RING) {
+      slot = 0;
+      lap ^= 1u;
+    }
+  }
+};
+
 // The runs of tiles of one unit in a CTA's share.
 struct SegmentWalk {
   const AttnParams& p;
-  int unit, t0, t1;
-  int64_t left;
+  int unit, t0, t1, left;  // (a CTA's share stays below 2^31 tiles: checked on the host)
   AttnUnit u;
   __device__ __forceinline__ SegmentWalk(const AttnParams& pp) : p(pp) {
-    const int64_t all = *p.tiles;
-    left = attn_share(all, p.ctas, blockIdx.x + 1) - attn_share(all, p.ctas, blockIdx.x);
-    const AttnStart s = p.starts[blockIdx.x];
-    unit = s.unit;
-    t0 = s.tile;
-    if (left > 0) fetch();
+    const AttnStart* at = p.starts + blockIdx.x;
+    take(reinterpret_cast<const int4*>(&at->u));
+    const int4 v = __ldg(reinterpret_cast<const int4*>(at) + 3);
+    unit = v.x;
+    t0 = v.y;
+    left = v.z;
+    bound();
   }
-  __device__ __forceinline__ void fetch() {
-    const int4 v = *reinterpret_cast<const int4*>(p.units + unit);
-    u = {v.x, v.y, v.z, v.w};
-    t1 = left < u.tiles - t0 ? t0 + static_cast<int>(left) : u.tiles;
+  __device__ __forceinline__ void take(const int4* at) {
+    const int4 a = __ldg(at), b = __ldg(at + 1), c = __ldg(at + 2);
+    u = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, {0, 0}};
   }
+  __device__ __forceinline__ void bound() { t1 = left < u.tiles - t0 ? t0 + left : u.tiles; }
   __device__ __forceinline__ bool valid() const { return left > 0; }
   __device__ __forceinline__ void next() {
     left -= t1 - t0;
     ++unit;
     t0 = 0;
-    if (left > 0) fetch();
+    if (left > 0) {
+      take(reinterpret_cast<const int4*>(p.units + unit));
+      bound();
+    }
   }
 };
 
@@ -181,22 +203,31 @@ struct SegmentWalk {
 template <int NC, int FORMAT>
 __device__ void tile_fetch(const AttnParams& p, TileSmall& sm, uint32_t base) {
   using SH = TileShape<NC>;
-  const int lt = threadIdx.x - (kTileSoftWarps + 1) * 32;
+  const int lt = threadIdx.x - kTileFirstLoader * 32;
   const int piece = lt & 15, rg = lt >> 4;  // 8 columns of the pair's 128; rows rg, rg + 16, ...
   const uint32_t dst = (piece >> 3) * kChunkBytes + rg * 128 + (((piece & 7) ^ (rg & 7)) << 4);
 
   SegmentWalk w(p);
   if (!w.valid()) return;
   int tile = w.t0, pair = 0, buf = 0, seg = 0;
-  int seen = unit_entries(p, w.u);
+  bool q_due = false;  // the current segment's q is still to be stored
 
-  // the tile's rows in the pool, by the first 128 threads, then a barrier of all
-  auto rows = [&]() {
+  // The tile's rows in the pool, by the first 128 threads, then a barrier of all. The page numbers
+  // are read one tile ahead within a unit.
+  int page = -1, ahead = -1;  // this thread's page of tile `ahead`
+  auto read_page = [&](int tl) {
+    const int e = tl * kAttnEntries + lt;
+    ahead = tl;
+    page = lt < kAttnEntries && e < w.u.seen
+               ? __ldg(p.table + static_cast<int64_t>(w.u.s) * p.max_pages + e / p.page_size)
+               : -1;
+  };
+  auto rows = [&](bool new_unit) {
+    if (new_unit || ahead != tile) read_page(tile);
     if (lt < kAttnEntries) {
       const int e = tile * kAttnEntries + lt;
       int64_t r = -1;
-      if (e < seen) {
-        const int page = __ldg(p.table + static_cast<int64_t>(w.u.s) * p.max_pages + e / p.page_size);
+      if (e < w.u.seen) {
         if (page >= 0 && page < p.num_pages)
           r = (static_cast<int64_t>(page) * p.page_size + e % p.page_size) * p.kv_heads + w.u.kvh;
         else if (p.dev_error != nullptr)
@@ -204,7 +235,8 @@ __device__ void tile_fetch(const AttnParams& p, TileSmall& sm, uint32_t base) {
       }
       sm.row[buf][lt] = r;
     }
-    named_barrier(3, kTileLoaders);
+    named_barrier(6, kTileLoaders);
+    if (tile + 1 < w.t1) read_page(tile + 1);
   };
   auto load = [&](Piece<FORMAT>(&v)[8]) {
 #pragma unroll
@@ -215,29 +247,27 @@ __device__ void tile_fetch(const AttnParams& p, TileSmall& sm, uint32_t base) {
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
   };
-  int64_t n = 0;  // pairs stored
+  RingAt<SH::kRing> ring;
   auto store = [&](const Piece<FORMAT>(&v)[8]) {
-    const int slot = static_cast<int>(n % SH::kRing);
-    tile_wait(sm, p, &sm.empty[slot], static_cast<uint32_t>(n / SH::kRing + 1) & 1u);
-    const uint32_t at = base + slot * kPairBytes + dst;
+    tile_wait(sm, p, &sm.empty[ring.slot], ring.lap ^ 1u);
+    const uint32_t at = base + ring.slot * kPairBytes + dst;
 #pragma unroll
     for (int i = 0; i < 8; ++i) sts128(at + i * 16 * 128, v[i].bf16());
-    arrive(&sm.full[slot]);
-    ++n;
+    arrive(&sm.full[ring.slot]);
+    ring.next();
   };
   // the unit's rows of q, zeros behind the last row and column
-  auto load_q = [&](const AttnUnit& u) {
+  auto load_q = [&](int kvh, int block, int token, int all) {
     if (seg > 0) tile_wait(sm, p, &sm.q_free, static_cast<uint32_t>(seg - 1) & 1u);
-    const int all = sequence_rows(p, u.s);
-    const int64_t t0 = __ldg(p.cu + u.s);
     constexpr int kPer = NC * 8;  // 16-byte pieces of a row
-#pragma unroll 4
+#pragma unroll 2
     for (int i = lt; i < kAttnRows * kPer; i += kTileLoaders) {
-      const int r = i / kPer, c = i % kPer, row = u.block * kAttnRows + r;
+      const int r = i / kPer, c = i % kPer, row = block * kAttnRows + r;
       uint4 v = make_uint4(0, 0, 0, 0);
       if (row < all && c * 8 < p.d) {
-        const int tok = row / p.group, head = u.kvh * p.group + row % p.group;
-        v = __ldg(reinterpret_cast<const uint4*>(p.q + (t0 + tok) * p.q_row + head * p.q_head + c * 8));
+        const int tok = row / p.group, head = kvh * p.group + row % p.group;
+        v = __ldg(reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(token) + tok) * p.q_row +
+                                                 head * p.q_head + c * 8));
       }
       sts128(base + SH::kQOff + (c >> 3) * (kAttnRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4), v);
     }
@@ -248,34 +278,32 @@ __device__ void tile_fetch(const AttnParams& p, TileSmall& sm, uint32_t base) {
   auto advance = [&]() {
     if (++pair < SH::kPairs) return true;
     pair = 0;
+    bool new_unit = false;
     if (++tile == w.t1) {
       w.next();
       if (!w.valid()) return false;
       tile = w.t0;
-      seen = unit_entries(p, w.u);
+      new_unit = q_due = true;
     }
     buf ^= 1;
-    rows();
+    rows(new_unit);
     return true;
   };
   // q of a segment goes in after its first tile's pairs (the fetch of these need not wait for
   // the previous segment's output to leave the buffer); the first segment's at once
-  auto stored_first_tile = [&](int stored_pair, int stored_tile, int first_tile) {
-    return stored_pair == SH::kPairs - 1 && stored_tile == first_tile;
-  };
-
   Piece<FORMAT> va[8], vb[8];
-  rows();
+  rows(true);
   load(va);
-  load_q(w.u);
+  load_q(w.u.kvh, w.u.block, w.u.token, w.u.rows);
   bool more = true;
   auto step = [&](Piece<FORMAT>(&cur)[8], Piece<FORMAT>(&nxt)[8]) {
-    const AttnUnit u = w.u;
-    const bool q_after = stored_first_tile(pair, tile, w.t0) && n >= SH::kPairs;
+    const bool q_after = q_due && pair == SH::kPairs - 1;
+    const int kvh = w.u.kvh, block = w.u.block, token = w.u.token, all = w.u.rows;
+    if (q_after) q_due = false;
     more = advance();
     if (more) load(nxt);
     store(cur);
-    if (q_after) load_q(u);
+    if (q_after) load_q(kvh, block, token, all);
   };
   while (true) {
     step(va, vb);
@@ -285,51 +313,50 @@ __device__ void tile_fetch(const AttnParams& p, TileSmall& sm, uint32_t base) {
   }
 }
 
-// ------------------------------------------------------------------------ the products' warp
+// ------------------------------------------------- the products' warp (all lanes take part)
 template <int NC>
 __device__ void tile_products(const AttnParams& p, TileSmall& sm, uint32_t base, uint32_t tmem) {
   using SH = TileShape<NC>;
   constexpr uint32_t kScoreDesc = mma_desc(128, kAttnRows, 0, 0);
   constexpr uint32_t kSumDesc = mma_desc(128, kAttnRows, 1, 1);
-  int64_t ns = 0, no = 0;  // pairs used by score products, and by sums
-  int64_t t = 0;           // tiles whose scores have been issued
-  int seg = 0;
+  // descriptors count in 16 bytes: a step adds to their address field
+  const uint64_t by_row = smem_desc(base, 16, 1024), by_column = smem_desc(base, kChunkBytes, 1024);
+  const uint64_t q = smem_desc(base + SH::kQOff, 16, 1024), probs = smem_desc(base + SH::kPOff, 16, 1024);
+  RingAt<SH::kRing> rs, ro;  // next pair of the score products, and of the sums
+  uint32_t t = 0;            // tiles whose scores have been issued
   auto scores = [&]() {
     const uint32_t d = tmem + SH::kTmemS + (t & 1) * kAttnRows;
-    for (int c = 0; c < SH::kPairs; ++c, ++ns) {
-      const int slot = static_cast<int>(ns % SH::kRing);
-      tile_wait(sm, p, &sm.full[slot], static_cast<uint32_t>(ns / SH::kRing) & 1u);
+#pragma unroll 1
+    for (int c = 0; c < SH::kPairs; ++c, rs.next()) {
+      tile_wait(sm, p, &sm.full[rs.slot], rs.lap);
       tc_fence_after();
+      const uint64_t a = by_row + rs.slot * (kPairBytes >> 4), b = q + 2 * c * (kAttnRows * 128 >> 4);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {  // 16 columns a step, 4 to a chunk
-        const uint32_t a = base + slot * kPairBytes + (k >> 2) * kChunkBytes + (k & 3) * 32;
-        const uint32_t b = base + SH::kQOff + (2 * c + (k >> 2)) * (kAttnRows * 128) + (k & 3) * 32;
-        tc_mma(d, smem_desc(a, 16, 1024), smem_desc(b, 16, 1024), kScoreDesc, c > 0 || k > 0);
-      }
+      for (int k = 0; k < 8; ++k)  // 16 columns a step, 4 to a chunk
+        tc_mma(d, a + (((k >> 2) * kChunkBytes + (k & 3) * 32) >> 4),
+               b + (((k >> 2) * kAttnRows * 128 + (k & 3) * 32) >> 4), kScoreDesc, c > 0 || k > 0);
     }
     tc_commit(&sm.scores[t & 1]);
     ++t;
   };
-  int64_t done = 0;  // tiles summed
+  uint32_t done = 0, seg = 0;  // tiles summed, segments
   for (SegmentWalk w(p); w.valid(); w.next(), ++seg) {
     const int tiles = w.t1 - w.t0;
-    tile_wait(sm, p, &sm.q_full, static_cast<uint32_t>(seg) & 1u);
+    tile_wait(sm, p, &sm.q_full, seg & 1u);
     tc_fence_after();
     scores();
     for (int j = 0; j < tiles; ++j) {
       if (SH::kAhead && j + 1 < tiles) scores();
-      tile_wait(sm, p, &sm.probs, static_cast<uint32_t>(done) & 1u);
+      tile_wait(sm, p, &sm.probs, done & 1u);
       tc_fence_after();
-      for (int c = 0; c < SH::kPairs; ++c, ++no) {
-        const int slot = static_cast<int>(no % SH::kRing);
+#pragma unroll 1
+      for (int c = 0; c < SH::kPairs; ++c, ro.next()) {
+        const uint64_t a = by_column + ro.slot * (kPairBytes >> 4);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {  // 16 entries a step
-          const uint32_t a = base + slot * kPairBytes + k * 2048;
-          const uint32_t b = base + SH::kPOff + k * 2048;
-          tc_mma(tmem + SH::kTmemO + c * kAttnRows, smem_desc(a, kChunkBytes, 1024), smem_desc(b, 16, 1024),
-                 kSumDesc, j > 0 || k > 0);
-        }
-        tc_commit(&sm.empty[slot]);
+        for (int k = 0; k < 8; ++k)  // 16 entries a step
+          tc_mma(tmem + SH::kTmemO + c * kAttnRows, a + k * (2048 >> 4), probs + k * (2048 >> 4), kSumDesc,
+                 j > 0 || k > 0);
+        tc_commit(&sm.empty[ro.slot]);
       }
       tc_commit(&sm.summed);
       ++done;
@@ -345,73 +372,73 @@ __device__ void tile_products(const AttnParams& p, TileSmall& sm, uint32_t base,
 template <int NC>
 __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* smem, uint32_t base, uint32_t tmem) {
   using SH = TileShape<NC>;
-  const int tid = threadIdx.x, lane = tid & 31, quad = (tid >> 5) & 3, half = tid >> 7;
-  const int c0 = half * 32;             // the rows (columns of S^T) of this group of warps
+  const int tid = threadIdx.x, lane = tid & 31, quad = (tid >> 5) & 3, group = tid >> 7;
+  const int c0 = group * kSoftCols;     // the rows (columns of S^T) of this group of four warps
   const int e0 = quad * 32 + lane;      // the entry (row of S^T) of this thread
   const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-  const float sl2 = p.scale * kLog2e;
-  int64_t t = 0;
-  int seg = 0;
-  auto barrier_half = [&]() { named_barrier(1 + half, 128); };
+  // (a scale of 0, under which every score is equal, becomes one that no score can show)
+  const float sl2 = p.scale == 0.f ? 1.17549435e-38f : p.scale * kLog2e;
+  uint32_t t = 0;  // tiles so far
+  auto barrier_group = [&]() { named_barrier(1 + group, 128); };
 
-  for (SegmentWalk w(p); w.valid(); w.next(), ++seg) {
+  for (SegmentWalk w(p); w.valid(); w.next()) {
     const AttnUnit u = w.u;
-    const int all = sequence_rows(p, u.s), n = __ldg(p.entries + u.s);
     const int row0 = u.block * kAttnRows;
     // what each row sees; rows behind the last one see everything (they are never stored)
     if (tid < kAttnRows) {
-      sm.lim[tid] = row0 + tid < all ? visible_to_token(p, u.s, (row0 + tid) / p.group, n) : INT_MAX;
+      sm.lim[tid] = row0 + tid < u.rows
+                        ? visible(static_cast<int64_t>(u.first) + (row0 + tid) / p.group, p.ratio, u.n)
+                        : INT_MAX;
       sm.m[tid] = kNoMax;
     }
-    const int lim_all = visible_to_token(p, u.s, row0 / p.group, n);  // seen by every row
-    named_barrier(4, 256);
-    float l[32];
+    named_barrier(5, kSoftThreads);
+    float l[kSoftCols];
 #pragma unroll
-    for (int c = 0; c < 32; ++c) l[c] = 0.f;
+    for (int c = 0; c < kSoftCols; ++c) l[c] = 0.f;
 
     for (int j = w.t0; j < w.t1; ++j, ++t) {
       const int e = j * kAttnEntries + e0;
-      const bool masked = (j + 1) * kAttnEntries > lim_all;
-      const uint32_t s_at = lanes + SH::kTmemS + static_cast<uint32_t>(t & 1) * kAttnRows + c0;
-      tile_wait(sm, p, &sm.scores[t & 1], static_cast<uint32_t>(t >> 1) & 1u);
+      const bool masked = (j + 1) * static_cast<int64_t>(kAttnEntries) > u.seen_all;
+      const uint32_t s_at = lanes + SH::kTmemS + (t & 1u) * kAttnRows + c0;
+      tile_wait(sm, p, &sm.scores[t & 1u], (t >> 1) & 1u);
       tc_fence_after();
-      float s[32];
+      float s[kSoftCols];
       bool odd = false;  // a masked score of this entry is not finite
       auto take = [&](bool subtract) {
-        tmem_load32(s_at, s);
+        tmem_load16(s_at, s);
+        if (masked) {
 #pragma unroll
-        for (int c = 0; c < 32; c += 4) {
-          const float4 m = *reinterpret_cast<const float4*>(&sm.m[c0 + c]);
-          const float mm[4] = {m.x, m.y, m.z, m.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float x = subtract ? fmaf(s[c + i], sl2, -mm[i]) : s[c + i] * sl2;
-            if (masked && e >= sm.lim[c0 + c + i]) {
-              odd = odd || !(fabsf(s[c + i]) <= 3.4028234e38f);
-              s[c + i] = -INFINITY;
-            } else {
-              s[c + i] = x;
+          for (int c = 0; c < kSoftCols; ++c)
+            if (e >= sm.lim[c0 + c]) {
+              odd = odd || !(fabsf(s[c]) <= 3.4028234e38f);
+              s[c] = sl2 < 0.f ? INFINITY : -INFINITY;  // -inf once scaled
             }
-          }
+        }
+#pragma unroll
+        for (int c = 0; c < kSoftCols; c += 4) {
+          const float4 m = subtract ? *reinterpret_cast<const float4*>(&sm.m[c0 + c]) : make_float4(0.f, 0.f, 0.f, 0.f);
+          s[c] = fmaf(s[c], sl2, -m.x);
+          s[c + 1] = fmaf(s[c + 1], sl2, -m.y);
+          s[c + 2] = fmaf(s[c + 2], sl2, -m.z);
+          s[c + 3] = fmaf(s[c + 3], sl2, -m.w);
         }
       };
       take(true);
-      float top = s[0];
+      float top = fmaxf(s[0], s[1]);
 #pragma unroll
-      for (int c = 1; c + 1 < 32; c += 2) top = fmax3(top, s[c], s[c + 1]);
-      top = fmaxf(top, s[31]);
-      if (named_barrier_or(1 + half, 128, top > kRescaleAt)) {
+      for (int c = 2; c < kSoftCols; c += 2) top = fmax3(top, s[c], s[c + 1]);
+      if (named_barrier_or(1 + group, 128, top > kRescaleAt)) {
         // new bounds: the true maxima so far
         take(false);
         float mine = kNoMax;
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
+        for (int c = 0; c < kSoftCols; ++c) {
           const float v = warp_max_f32(s[c]);
           if (lane == c) mine = v;
         }
-        sm.red[quad][c0 + lane] = mine;
-        barrier_half();
-        if (quad == 0) {
+        if (lane < kSoftCols) sm.red[quad][c0 + lane] = mine;
+        barrier_group();
+        if (quad == 0 && lane < kSoftCols) {
           const int c = c0 + lane;
           const float old = sm.m[c];
           float m = fmaxf(fmaxf(sm.red[0][c], sm.red[1][c]), fmaxf(sm.red[2][c], sm.red[3][c]));
@@ -419,42 +446,45 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
           sm.fac[c] = fast_exp2(old - m);
           sm.m[c] = m;
         }
-        barrier_half();
+        barrier_group();
 #pragma unroll
-        for (int c = 0; c < 32; ++c) l[c] *= sm.fac[c0 + c];
+        for (int c = 0; c < kSoftCols; ++c) l[c] *= sm.fac[c0 + c];
         if (j > w.t0) {
-          tile_wait(sm, p, &sm.summed, static_cast<uint32_t>(t - 1) & 1u);
+          tile_wait(sm, p, &sm.summed, (t - 1u) & 1u);
           tc_fence_after();
+#pragma unroll 1
           for (int b = 0; b < SH::kPairs; ++b) {
             const uint32_t at = lanes + SH::kTmemO + b * kAttnRows + c0;
-            tmem_load32(at, s);
+            tmem_load16(at, s);
 #pragma unroll
-            for (int c = 0; c < 32; ++c) s[c] *= sm.fac[c0 + c];
-            tmem_store32(at, s);
+            for (int c = 0; c < kSoftCols; ++c) s[c] *= sm.fac[c0 + c];
+            tmem_store16(at, s);
           }
         }
         take(true);
       }
       // weights; their sums before rounding
-      uint32_t w2[16];
+      uint32_t w2[kSoftCols / 2];
 #pragma unroll
-      for (int c = 0; c < 32; c += 2) {
+      for (int c = 0; c < kSoftCols; c += 2) {
         const float a = fast_exp2(s[c]), b = fast_exp2(s[c + 1]);
         l[c] += a;
         l[c + 1] += b;
         w2[c / 2] = pack_bf16x2(a, b);
       }
-      if (j > w.t0) tile_wait(sm, p, &sm.summed, static_cast<uint32_t>(t - 1) & 1u);  // P is free
+      if (j > w.t0) tile_wait(sm, p, &sm.summed, (t - 1u) & 1u);  // P is free
       const uint32_t row = base + SH::kPOff + e0 * 128;
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        sts128(row + (((half * 4 + c) ^ (e0 & 7)) << 4), make_uint4(w2[4 * c], w2[4 * c + 1], w2[4 * c + 2], w2[4 * c + 3]));
+      for (int c = 0; c < 2; ++c)
+        sts128(row + (((group * 2 + c) ^ (e0 & 7)) << 4), make_uint4(w2[4 * c], w2[4 * c + 1], w2[4 * c + 2], w2[4 * c + 3]));
       if (odd) {
         // 0 * NaN would reach the rows that do not see this entry: its non-finite values become
         // 0 before the second product (the rows that see it have a non-finite score)
+#pragma unroll 1
         for (int b = 0; b < NC; ++b) {
           const int slot = static_cast<int>((t * SH::kPairs + (b >> 1)) % SH::kRing);
           unsigned char* at = smem + slot * kPairBytes + (b & 1) * kChunkBytes + e0 * 128;
+#pragma unroll 1
           for (int i = 0; i < 64; ++i) {
             uint16_t* v = reinterpret_cast<uint16_t*>(at) + i;
             if ((*v & 0x7F80u) == 0x7F80u) *v = 0;
@@ -468,74 +498,77 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
     }
 
     // the unit's (or its piece's) sums are complete
-    tile_wait(sm, p, &sm.summed, static_cast<uint32_t>(t - 1) & 1u);
+    tile_wait(sm, p, &sm.summed, (t - 1u) & 1u);
     tc_fence_after();
     float mine = 0.f;
 #pragma unroll
-    for (int c = 0; c < 32; ++c) {
+    for (int c = 0; c < kSoftCols; ++c) {
       float v = l[c];
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
       if (lane == c) mine = v;
     }
-    sm.red[quad][c0 + lane] = mine;
-    barrier_half();
+    if (lane < kSoftCols) sm.red[quad][c0 + lane] = mine;
+    barrier_group();
     const bool whole = w.t0 == 0 && w.t1 == u.tiles;
-    if (quad == 0) {
+    const int64_t piece = 2 * static_cast<int64_t>(blockIdx.x) + (w.t0 == 0 ? 1 : 0);
+    if (quad == 0 && lane < kSoftCols) {
       const int c = c0 + lane;
       const float z = (sm.red[0][c] + sm.red[1][c]) + (sm.red[2][c] + sm.red[3][c]), m = sm.m[c];
       if (!whole) {
-        float* ml = p.part_ml + (2 * static_cast<int64_t>(blockIdx.x) + (w.t0 == 0 ? 1 : 0)) * 2 * kAttnRows;
+        float* ml = p.part_ml + piece * 2 * kAttnRows;
         ml[c] = m;
         ml[kAttnRows + c] = z;
       } else {
         const int row = row0 + c;
         const int head = u.kvh * p.group + row % p.group;
-        const float sink_e = p.sink != nullptr && row < all ? p.sink[head] : -INFINITY;
+        const float sink_e = p.sink != nullptr && row < u.rows ? p.sink[head] : -INFINITY;
         const float sink = sink_e * kLog2e;
         const float mx = fmaxf(z > 0.f || z != z ? m : -INFINITY, sink);
         const float old = mx == -INFINITY ? 0.f : fast_exp2(m - mx);
         const float den = mx == -INFINITY ? 0.f : z * old + fast_exp2(sink - mx);
         sm.fac[c] = mx == -INFINITY ? 0.f : old / den;
-        if (p.lse != nullptr && row < all)
-          p.lse[(__ldg(p.cu + u.s) + row / p.group) * static_cast<int64_t>(p.q_heads) + head] =
+        if (p.lse != nullptr && row < u.rows)
+          p.lse[(static_cast<int64_t>(u.token) + row / p.group) * p.q_heads + head] =
               z == 0.f ? sink_e : (mx + log2f(den)) * kLn2;
       }
     }
-    barrier_half();
+    barrier_group();
     if (whole) {
       // O^T times the rows' factors, as bf16 rows in q's buffer, then out in 16-byte pieces
       uint16_t* stage = reinterpret_cast<uint16_t*>(smem + SH::kQOff);
+#pragma unroll 1
       for (int b = 0; b < SH::kPairs; ++b) {
-        float v[32];
-        tmem_load32(lanes + SH::kTmemO + b * kAttnRows + c0, v);
+        float v[kSoftCols];
+        tmem_load16(lanes + SH::kTmemO + b * kAttnRows + c0, v);
 #pragma unroll
-        for (int c = 0; c < 32; ++c)
+        for (int c = 0; c < kSoftCols; ++c)
           stage[(c0 + c) * SH::kDpad + b * 128 + e0] = Element<CSA_DTYPE_BF16>::from_float(v[c] * sm.fac[c0 + c]);
       }
       tc_fence_before();
-      barrier_half();
+      barrier_group();
       constexpr int kPer = NC * 8;
-      const int64_t tok0 = __ldg(p.cu + u.s);
-      for (int i = (tid & 127); i < 32 * kPer; i += 128) {
+#pragma unroll 1
+      for (int i = (tid & 127); i < kSoftCols * kPer; i += 128) {
         const int r = c0 + i / kPer, c = i % kPer, row = row0 + r;
-        if (row < all && c * 8 < p.d) {
+        if (row < u.rows && c * 8 < p.d) {
           const uint4 v = lds128(base + SH::kQOff + r * (SH::kDpad * 2) + c * 16);
-          *reinterpret_cast<uint4*>(p.out + (tok0 + row / p.group) * p.out_row +
+          *reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(u.token) + row / p.group) * p.out_row +
                                     (u.kvh * p.group + row % p.group) * p.out_head + c * 8) = v;
         }
       }
     } else {
-      float* o = p.part_o + (2 * static_cast<int64_t>(blockIdx.x) + (w.t0 == 0 ? 1 : 0)) * kAttnRows * SH::kDpad;
+      float* o = p.part_o + piece * kAttnRows * SH::kDpad;
+#pragma unroll 1
       for (int b = 0; b < SH::kPairs; ++b) {
-        float v[32];
-        tmem_load32(lanes + SH::kTmemO + b * kAttnRows + c0, v);
+        float v[kSoftCols];
+        tmem_load16(lanes + SH::kTmemO + b * kAttnRows + c0, v);
 #pragma unroll
-        for (int c = 0; c < 32; ++c) o[(c0 + c) * SH::kDpad + b * 128 + e0] = v[c];
+        for (int c = 0; c < kSoftCols; ++c) o[(c0 + c) * SH::kDpad + b * 128 + e0] = v[c];
       }
       tc_fence_before();
     }
-    named_barrier(4, 256);  // the small arrays and the staging are free again
+    named_barrier(5, kSoftThreads);  // the small arrays and the staging are free again
     if (lane == 0) mbar_arrive(&sm.q_free);
   }
 }
@@ -569,15 +602,15 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
   pdl_wait();
-  if (*p.status == 0) {
-    if (warp < kTileSoftWarps) {
-      tile_softmax<NC>(p, sm, smem, base, tmem);
-    } else if (warp == kTileSoftWarps) {
-      if ((threadIdx.x & 31) == 0) tile_products<NC>(p, sm, base, tmem);
-      __syncwarp();
-    } else {
-      tile_fetch<NC, FORMAT>(p, sm, base);
-    }
+  const bool run = *p.status == 0;
+  if (warp >= kTileFirstLoader) {
+    regs_up<kLoadRegs>();
+    if (run) tile_fetch<NC, FORMAT>(p, sm, base);
+  } else if (warp >= kTileSoftWarps) {
+    regs_down<kIssueRegs>();
+    if (run && warp == kTileSoftWarps) tile_products<NC>(p, sm, base, tmem);
+  } else if (run) {
+    tile_softmax<NC>(p, sm, smem, base, tmem);
   }
   tc_fence_before();
   __syncthreads();
@@ -596,7 +629,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
   const int ctas = static_cast<int>(all_tiles < p.ctas ? all_tiles : p.ctas);
   const int i = blockIdx.x;
   if (i + 1 >= ctas) return;
-  const AttnStart nx = p.starts[i + 1];
+  const AttnStart& nx = p.starts[i + 1];
   if (nx.tile == 0) return;                                             // ends with its share
   if (p.unit_first[nx.unit] < attn_share(all_tiles, p.ctas, i)) return;  // begins before it
   const int64_t end = p.unit_first[nx.unit + 1];
@@ -605,9 +638,9 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
   const AttnUnit u = p.units[nx.unit];
   const int r = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int row = u.block * kAttnRows + r;
-  if (row >= sequence_rows(p, u.s)) return;
+  if (row >= u.rows) return;
   const int head = u.kvh * p.group + row % p.group;
-  const int64_t token = __ldg(p.cu + u.s) + row / p.group;
+  const int64_t token = static_cast<int64_t>(u.token) + row / p.group;
 
   auto slot = [&](int k) { return 2 * static_cast<int64_t>(k) + (k == i ? 1 : 0); };
   const float sink_e = p.sink != nullptr ? p.sink[head] : -INFINITY, sink = sink_e * kLog2e;
