@@ -13,10 +13,11 @@
 //
 // Warps: 0-15 softmax (a warp reads the 32 tensor-memory lanes of its quadrant, each group of
 // four warps 16 of the 64 rows), 16 issues the products (17-19 only complete its register
-// group), 20-27 fetch: they follow the page table,
-// widen 8- and 4-bit codes to bf16 (exact, but for bf16's own subnormals) and store the swizzled tile; a pair of
-// 64-column chunks (32 KB) is the unit of the ring, and the next pair's loads are in flight
-// in registers while one is stored.
+// group), 20-27 fetch: they follow the page table, widen 8- and 4-bit codes to bf16 (exact, but
+// for bf16's own subnormals) and store the swizzled tile in pairs of 64-column chunks (32 KB).
+// Two groups of four warps take alternate pairs: a group holds its next pair in registers
+// while the ring is full, and one group's loads are under way while the other stores. Rows of
+// the next tile are prefetched into L2.
 //
 // Softmax without a maximum per tile: the weights are taken against a running bound m that
 // only moves when some score passes it by 2^8; then m becomes the true maximum and O^T and the
@@ -40,10 +41,11 @@ constexpr int kSoftCols = 16;  // rows of a softmax thread's group
 constexpr int kTileLoaders = kTileLoadWarps * 32;
 constexpr int kTileFirstLoader = kTileSoftWarps + 4;
 constexpr int kTileThreads = (kTileFirstLoader + kTileLoadWarps) * 32;
-// Registers a thread: 896 threads launch with 72, and 16 x 72 + 4 x 40 + 8 x 88 = 28 x 72.
-constexpr int kIssueRegs = 40, kLoadRegs = 88;
+// Registers a thread: 896 threads launch with 72, and 16 x 64 + 4 x 40 + 8 x 104 = 28 x 72.
+constexpr int kSoftRegs = 64, kIssueRegs = 40, kLoadRegs = 104;
 constexpr int kChunkBytes = kAttnEntries * 128;  // 128 entries x 64 columns
 constexpr int kPairBytes = 2 * kChunkBytes;
+constexpr int kSmallBytes = 7168;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNoMax = -1e30f;     // bound of a row that has seen nothing
 constexpr float kRescaleAt = 8.f;    // log2 of how far a weight may pass 1
@@ -64,45 +66,48 @@ struct TileShape {
   static constexpr int kQOff = kRing * kPairBytes;
   static constexpr int kPOff = kQOff + kQBytes;
   static constexpr int kSmallOff = kPOff + kPBytes;
-  static constexpr int kSmemBytes = kSmallOff + 4096 + 1024;  // and the 1024-byte alignment
+  static constexpr int kSmemBytes = kSmallOff + kSmallBytes + 1024;  // and the 1024-byte alignment
 };
 
 struct TileSmall {
-  int64_t row[2][kAttnEntries];  // entry rows of a tile in the pool, -1: none
+  int64_t row[2][2][kAttnEntries];  // by fetching group and turn: bytes to an entry in the pool, -1: none
+  int64_t q_at[kAttnRows];          // elements to a row of q, -1: none
   float m[kAttnRows];
   float fac[kAttnRows];
   float red[4][kAttnRows];  // column maxima, then weight sums, by quadrant
   int lim[kAttnRows];
-  uint64_t full[5], empty[5], scores[2], probs, summed, q_full, q_free, drain;
+  uint64_t full[5], empty[5], scores[2], probs, summed, q_full, drain;
   uint32_t tmem;
   int stop;
 };
-static_assert(sizeof(TileSmall) <= 4096, "small arrays");
+static_assert(sizeof(TileSmall) <= kSmallBytes, "small arrays");
 
-// 8 columns of an entry as they lie in the cache, and their scale byte.
+// 8 columns of an entry as they lie in the cache, and their scale byte; `at` is the entry's byte
+// offset in the pool (that of its scales is a 32nd or a 16th of it), -1 for none.
+__device__ __forceinline__ uint32_t scaled_bf16x2(float2 v, float s) { return pack_bf16x2(v.x * s, v.y * s); }
 template <int FORMAT>
 struct Piece;
 template <>
 struct Piece<CSA_CACHE_BF16> {
+  static __device__ __forceinline__ int row_bytes(int d) { return 2 * d; }
   uint4 w;
-  __device__ __forceinline__ void load(const AttnParams& p, int64_t row, int col) {
+  __device__ __forceinline__ void load(const AttnParams& p, int64_t at, int col) {
     w = make_uint4(0, 0, 0, 0);
-    if (row >= 0 && col < p.d)
-      w = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.data) + row * p.d + col));
+    if (at >= 0 && col < p.d) w = __ldg(reinterpret_cast<const uint4*>(p.data + at + 2 * col));
   }
   __device__ __forceinline__ uint4 bf16() const { return w; }
 };
-__device__ __forceinline__ uint32_t scaled_bf16x2(float2 v, float s) { return pack_bf16x2(v.x * s, v.y * s); }
 template <>
 struct Piece<CSA_CACHE_E4M3> {
+  static __device__ __forceinline__ int row_bytes(int d) { return d; }
   uint2 w;
   uint32_t k;
-  __device__ __forceinline__ void load(const AttnParams& p, int64_t row, int col) {
+  __device__ __forceinline__ void load(const AttnParams& p, int64_t at, int col) {
     w = make_uint2(0, 0);
     k = 127;
-    if (row >= 0 && col < p.d) {
-      w = __ldg(reinterpret_cast<const uint2*>(p.data + row * p.d + col));
-      k = __ldg(p.scales + row * (p.d / CSA_CACHE_GROUP) + col / CSA_CACHE_GROUP);
+    if (at >= 0 && col < p.d) {
+      w = __ldg(reinterpret_cast<const uint2*>(p.data + at + col));
+      k = __ldg(p.scales + (at >> 5) + (col >> 5));
     }
   }
   __device__ __forceinline__ uint4 bf16() const {
@@ -113,13 +118,14 @@ struct Piece<CSA_CACHE_E4M3> {
 };
 template <>
 struct Piece<CSA_CACHE_E2M1> {
+  static __device__ __forceinline__ int row_bytes(int d) { return d / 2; }
   uint32_t w, k;
-  __device__ __forceinline__ void load(const AttnParams& p, int64_t row, int col) {
+  __device__ __forceinline__ void load(const AttnParams& p, int64_t at, int col) {
     w = 0;
     k = 127;
-    if (row >= 0 && col < p.d) {
-      w = __ldg(reinterpret_cast<const uint32_t*>(p.data + row * (p.d / 2) + col / 2));
-      k = __ldg(p.scales + row * (p.d / CSA_CACHE_GROUP) + col / CSA_CACHE_GROUP);
+    if (at >= 0 && col < p.d) {
+      w = __ldg(reinterpret_cast<const uint32_t*>(p.data + at + (col >> 1)));
+      k = __ldg(p.scales + (at >> 4) + (col >> 5));
     }
   }
   __device__ __forceinline__ uint4 bf16() const {
@@ -168,6 +174,18 @@ struct RingAt {
   }
 };
 
+// A unit from the work list; volatile, so that a later reading is a new one and its fields do not
+// stay in registers over a loop that has no use for them.
+__device__ __forceinline__ AttnUnit read_unit(const AttnUnit* at) {
+  int4 v[3];
+#pragma unroll
+  for (int i = 0; i < 3; ++i)
+    asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v[i].x), "=r"(v[i].y), "=r"(v[i].z), "=r"(v[i].w)
+                 : "l"(reinterpret_cast<const int4*>(at) + i));
+  return {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w, v[2].x, v[2].y, {0, 0}};
+}
+
 // The runs of tiles of one unit in a CTA's share.
 struct SegmentWalk {
   const AttnParams& p;
@@ -175,16 +193,12 @@ struct SegmentWalk {
   AttnUnit u;
   __device__ __forceinline__ SegmentWalk(const AttnParams& pp) : p(pp) {
     const AttnStart* at = p.starts + blockIdx.x;
-    take(reinterpret_cast<const int4*>(&at->u));
+    u = read_unit(&at->u);
     const int4 v = __ldg(reinterpret_cast<const int4*>(at) + 3);
     unit = v.x;
     t0 = v.y;
     left = v.z;
     bound();
-  }
-  __device__ __forceinline__ void take(const int4* at) {
-    const int4 a = __ldg(at), b = __ldg(at + 1), c = __ldg(at + 2);
-    u = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, {0, 0}};
   }
   __device__ __forceinline__ void bound() { t1 = left < u.tiles - t0 ? t0 + left : u.tiles; }
   __device__ __forceinline__ bool valid() const { return left > 0; }
@@ -193,7 +207,7 @@ struct SegmentWalk {
     ++unit;
     t0 = 0;
     if (left > 0) {
-      take(reinterpret_cast<const int4*>(p.units + unit));
+      u = read_unit(p.units + unit);
       bound();
     }
   }
@@ -203,113 +217,76 @@ struct SegmentWalk {
 template <int NC, int FORMAT>
 __device__ void tile_fetch(const AttnParams& p, TileSmall& sm, uint32_t base) {
   using SH = TileShape<NC>;
+  using P = Piece<FORMAT>;
+  constexpr int kGroup = kTileLoaders / 2;
+  constexpr int kStep = SH::kPairs == 1 ? 2 : 1;  // tiles from one of a group's to its next
   const int lt = threadIdx.x - kTileFirstLoader * 32;
-  const int piece = lt & 15, rg = lt >> 4;  // 8 columns of the pair's 128; rows rg, rg + 16, ...
-  const uint32_t dst = (piece >> 3) * kChunkBytes + rg * 128 + (((piece & 7) ^ (rg & 7)) << 4);
+  const int group = lt / kGroup, gt = lt % kGroup;
+  const int piece = gt & 15, rg = gt >> 4;  // 8 columns of the pair's 128; rows rg, rg + 8, ...
+  const uint32_t dst = (piece >> 3) * kChunkBytes + rg * 128 + (((piece & 7) ^ rg) << 4);
+  const int row_bytes = P::row_bytes(p.d);
 
   SegmentWalk w(p);
-  if (!w.valid()) return;
-  int tile = w.t0, pair = 0, buf = 0, seg = 0;
-  bool q_due = false;  // the current segment's q is still to be stored
-
-  // The tile's rows in the pool, by the first 128 threads, then a barrier of all. The page numbers
-  // are read one tile ahead within a unit.
-  int page = -1, ahead = -1;  // this thread's page of tile `ahead`
-  auto read_page = [&](int tl) {
-    const int e = tl * kAttnEntries + lt;
-    ahead = tl;
-    page = lt < kAttnEntries && e < w.u.seen
-               ? __ldg(p.table + static_cast<int64_t>(w.u.s) * p.max_pages + e / p.page_size)
-               : -1;
-  };
-  auto rows = [&](bool new_unit) {
-    if (new_unit || ahead != tile) read_page(tile);
-    if (lt < kAttnEntries) {
-      const int e = tile * kAttnEntries + lt;
-      int64_t r = -1;
-      if (e < w.u.seen) {
-        if (page >= 0 && page < p.num_pages)
-          r = (static_cast<int64_t>(page) * p.page_size + e % p.page_size) * p.kv_heads + w.u.kvh;
-        else if (p.dev_error != nullptr)
-          *p.dev_error = CSA_DEVERR_PAGE;
-      }
-      sm.row[buf][lt] = r;
-    }
-    named_barrier(6, kTileLoaders);
-    if (tile + 1 < w.t1) read_page(tile + 1);
-  };
-  auto load = [&](Piece<FORMAT>(&v)[8]) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i].load(p, sm.row[buf][i * 16 + rg], pair * 128 + piece * 8);
-  };
-  auto arrive = [&](uint64_t* bar) {
-    fence_proxy_async_smem();
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
-  };
+  int tile = w.t0, pair = 0, buf = 0;
   RingAt<SH::kRing> ring;
-  auto store = [&](const Piece<FORMAT>(&v)[8]) {
-    tile_wait(sm, p, &sm.empty[ring.slot], ring.lap ^ 1u);
-    const uint32_t at = base + ring.slot * kPairBytes + dst;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sts128(at + i * 16 * 128, v[i].bf16());
-    arrive(&sm.full[ring.slot]);
+  bool fresh = true;  // the tile's rows are still to be looked up
+  auto next_pair = [&]() {
     ring.next();
-  };
-  // the unit's rows of q, zeros behind the last row and column
-  auto load_q = [&](int kvh, int block, int token, int all) {
-    if (seg > 0) tile_wait(sm, p, &sm.q_free, static_cast<uint32_t>(seg - 1) & 1u);
-    constexpr int kPer = NC * 8;  // 16-byte pieces of a row
-#pragma unroll 2
-    for (int i = lt; i < kAttnRows * kPer; i += kTileLoaders) {
-      const int r = i / kPer, c = i % kPer, row = block * kAttnRows + r;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (row < all && c * 8 < p.d) {
-        const int tok = row / p.group, head = kvh * p.group + row % p.group;
-        v = __ldg(reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(token) + tok) * p.q_row +
-                                                 head * p.q_head + c * 8));
-      }
-      sts128(base + SH::kQOff + (c >> 3) * (kAttnRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4), v);
-    }
-    arrive(&sm.q_full);
-    ++seg;
-  };
-  // moves on to the next pair; false at the end of the CTA's share
-  auto advance = [&]() {
-    if (++pair < SH::kPairs) return true;
+    if (++pair < SH::kPairs) return;
     pair = 0;
-    bool new_unit = false;
+    fresh = true;
     if (++tile == w.t1) {
       w.next();
-      if (!w.valid()) return false;
       tile = w.t0;
-      new_unit = q_due = true;
+    }
+  };
+  // this thread's page of tile `ahead` of unit `unit`, read early
+  int page = -1, ahead = -1, unit = -1;
+  auto read_page = [&](int tl) {
+    const int e = tl * kAttnEntries + gt;
+    ahead = tl;
+    unit = w.unit;
+    page = e < w.u.seen ? __ldg(p.table + static_cast<int64_t>(w.u.s) * p.max_pages + e / p.page_size) : -1;
+  };
+  auto entry_at = [&](int e) {
+    return ((static_cast<int64_t>(page) * p.page_size + e % p.page_size) * p.kv_heads + w.u.kvh) * row_bytes;
+  };
+  auto rows = [&]() {
+    if (ahead != tile || unit != w.unit) read_page(tile);
+    const int e = tile * kAttnEntries + gt;
+    int64_t at = -1;
+    if (e < w.u.seen) {
+      if (page >= 0 && page < p.num_pages) at = entry_at(e);
+      else if (p.dev_error != nullptr) *p.dev_error = CSA_DEVERR_PAGE;
     }
     buf ^= 1;
-    rows(new_unit);
-    return true;
+    sm.row[group][buf][gt] = at;
+    named_barrier(6 + group, kGroup);
+    fresh = false;
+    if (tile + kStep < w.t1) {
+      read_page(tile + kStep);
+      if ((SH::kPairs == 1 || group == 0) && page >= 0 && page < p.num_pages)
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p.data + entry_at((tile + kStep) * kAttnEntries + gt)),
+                     "r"(row_bytes)
+                     : "memory");
+    }
   };
-  // q of a segment goes in after its first tile's pairs (the fetch of these need not wait for
-  // the previous segment's output to leave the buffer); the first segment's at once
-  Piece<FORMAT> va[8], vb[8];
-  rows(true);
-  load(va);
-  load_q(w.u.kvh, w.u.block, w.u.token, w.u.rows);
-  bool more = true;
-  auto step = [&](Piece<FORMAT>(&cur)[8], Piece<FORMAT>(&nxt)[8]) {
-    const bool q_after = q_due && pair == SH::kPairs - 1;
-    const int kvh = w.u.kvh, block = w.u.block, token = w.u.token, all = w.u.rows;
-    if (q_after) q_due = false;
-    more = advance();
-    if (more) load(nxt);
-    store(cur);
-    if (q_after) load_q(kvh, block, token, all);
-  };
-  while (true) {
-    step(va, vb);
-    if (!more) break;
-    step(vb, va);
-    if (!more) break;
+
+  if (group == 1 && w.valid()) next_pair();
+  while (w.valid()) {
+    if (fresh) rows();
+    P v[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i].load(p, sm.row[group][buf][i * 8 + rg], pair * 128 + piece * 8);
+    tile_wait(sm, p, &sm.empty[ring.slot], ring.lap ^ 1u);
+    const uint32_t to = base + ring.slot * kPairBytes + dst;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sts128(to + i * 8 * 128, v[i].bf16());
+    fence_proxy_async_smem();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&sm.full[ring.slot]);
+    next_pair();
+    if (w.valid()) next_pair();
   }
 }
 
@@ -382,23 +359,45 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
   auto barrier_group = [&]() { named_barrier(1 + group, 128); };
 
   for (SegmentWalk w(p); w.valid(); w.next()) {
-    const AttnUnit u = w.u;
-    const int row0 = u.block * kAttnRows;
-    // what each row sees; rows behind the last one see everything (they are never stored)
+    const int seen_all = w.u.seen_all;
+    // where each row of q lies, and what it sees; rows behind the last one are zeros and see
+    // everything (they are never stored)
     if (tid < kAttnRows) {
-      sm.lim[tid] = row0 + tid < u.rows
-                        ? visible(static_cast<int64_t>(u.first) + (row0 + tid) / p.group, p.ratio, u.n)
-                        : INT_MAX;
+      const int row = w.u.block * kAttnRows + tid, token = row / p.group;
+      const bool some = row < w.u.rows;
+      sm.lim[tid] = some ? visible(static_cast<int64_t>(w.u.first) + token, p.ratio, w.u.n) : INT_MAX;
+      sm.q_at[tid] = some ? (static_cast<int64_t>(w.u.token) + token) * p.q_row +
+                                (w.u.kvh * p.group + (row - token * p.group)) * p.q_head
+                          : -1;
       sm.m[tid] = kNoMax;
     }
     named_barrier(5, kSoftThreads);
+    {
+      constexpr int kPer = NC * 8;  // 16-byte pieces of a row; NC pieces a thread
+      uint4 v[NC];
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const int at = tid + i * kSoftThreads, r = at / kPer, c = at % kPer;
+        const int64_t q_at = sm.q_at[r];
+        v[i] = make_uint4(0, 0, 0, 0);
+        if (q_at >= 0 && c * 8 < p.d) v[i] = __ldg(reinterpret_cast<const uint4*>(p.q + q_at + c * 8));
+      }
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const int at = tid + i * kSoftThreads, r = at / kPer, c = at % kPer;
+        sts128(base + SH::kQOff + (c >> 3) * (kAttnRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4), v[i]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.q_full);
+    }
     float l[kSoftCols];
 #pragma unroll
     for (int c = 0; c < kSoftCols; ++c) l[c] = 0.f;
 
     for (int j = w.t0; j < w.t1; ++j, ++t) {
       const int e = j * kAttnEntries + e0;
-      const bool masked = (j + 1) * static_cast<int64_t>(kAttnEntries) > u.seen_all;
+      const bool masked = (j + 1) * static_cast<int64_t>(kAttnEntries) > seen_all;
       const uint32_t s_at = lanes + SH::kTmemS + (t & 1u) * kAttnRows + c0;
       tile_wait(sm, p, &sm.scores[t & 1u], (t >> 1) & 1u);
       tc_fence_after();
@@ -500,16 +499,21 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
     // the unit's (or its piece's) sums are complete
     tile_wait(sm, p, &sm.summed, (t - 1u) & 1u);
     tc_fence_after();
-    float mine = 0.f;
+    // the lanes' sums of each column: halves change hands until a lane has one column
 #pragma unroll
-    for (int c = 0; c < kSoftCols; ++c) {
-      float v = l[c];
+    for (int k = 8; k > 0; k >>= 1) {
+      const bool upper = (lane & (2 * k)) != 0;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-      if (lane == c) mine = v;
+      for (int c = 0; c < k; ++c) {
+        const float give = upper ? l[c] : l[c + k], keep = upper ? l[c + k] : l[c];
+        l[c] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, 2 * k);
+      }
     }
-    if (lane < kSoftCols) sm.red[quad][c0 + lane] = mine;
+    l[0] += __shfl_xor_sync(0xFFFFFFFFu, l[0], 1);
+    if ((lane & 1) == 0) sm.red[quad][c0 + (lane >> 1)] = l[0];
     barrier_group();
+    const AttnUnit u = read_unit(p.units + w.unit);
+    const int row0 = u.block * kAttnRows;
     const bool whole = w.t0 == 0 && w.t1 == u.tiles;
     const int64_t piece = 2 * static_cast<int64_t>(blockIdx.x) + (w.t0 == 0 ? 1 : 0);
     if (quad == 0 && lane < kSoftCols) {
@@ -564,12 +568,12 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
         float v[kSoftCols];
         tmem_load16(lanes + SH::kTmemO + b * kAttnRows + c0, v);
 #pragma unroll
-        for (int c = 0; c < kSoftCols; ++c) o[(c0 + c) * SH::kDpad + b * 128 + e0] = v[c];
+        for (int c = 0; c < kSoftCols; ++c)
+          if (row0 + c0 + c < u.rows) o[(c0 + c) * SH::kDpad + b * 128 + e0] = v[c];
       }
       tc_fence_before();
     }
     named_barrier(5, kSoftThreads);  // the small arrays and the staging are free again
-    if (lane == 0) mbar_arrive(&sm.q_free);
   }
 }
 
@@ -584,15 +588,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
   if (warp == 0) tmem_alloc(&sm.tmem, SH::kTmemColumns);
   if (threadIdx.x == 32) {
     for (int i = 0; i < SH::kRing; ++i) {
-      mbar_init(&sm.full[i], kTileLoadWarps);
+      mbar_init(&sm.full[i], kTileLoadWarps / 2);
       mbar_init(&sm.empty[i], 1);
     }
     mbar_init(&sm.scores[0], 1);
     mbar_init(&sm.scores[1], 1);
     mbar_init(&sm.probs, kTileSoftWarps);
     mbar_init(&sm.summed, 1);
-    mbar_init(&sm.q_full, kTileLoadWarps);
-    mbar_init(&sm.q_free, kTileSoftWarps);
+    mbar_init(&sm.q_full, kTileSoftWarps);
     mbar_init(&sm.drain, 1);
     sm.stop = 0;
     fence_mbar_init();
@@ -609,8 +612,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
   } else if (warp >= kTileSoftWarps) {
     regs_down<kIssueRegs>();
     if (run && warp == kTileSoftWarps) tile_products<NC>(p, sm, base, tmem);
-  } else if (run) {
-    tile_softmax<NC>(p, sm, smem, base, tmem);
+  } else {
+    regs_down<kSoftRegs>();
+    if (run) tile_softmax<NC>(p, sm, smem, base, tmem);
   }
   tc_fence_before();
   __syncthreads();
