@@ -109,6 +109,169 @@ __global__ void __launch_bounds__(kCacheThreads) cache_read_scalar_kernel(CacheP
   }
 }
 
+// Vector kernels: a thread takes 16 consecutive columns of a row's head (8 of a bf16 cache), two
+// neighbouring threads share a scale; kItems of them are under way per thread. 16-byte
+// accesses throughout (8 bytes of e2m1).
+constexpr int kItems = 2;
+template <int FORMAT>
+struct CachePiece {
+  static constexpr int kCols = FORMAT == CSA_CACHE_BF16 ? 8 : 16;
+};
+
+// Row, head and first column of a thread's item.
+struct ItemAt {
+  int64_t row;
+  int head, col;
+  __device__ __forceinline__ ItemAt(const CacheParams& p, int64_t item, int cols) {
+    const uint32_t per = static_cast<uint32_t>(p.d / cols);
+    if (item < INT_MAX) {  // 32-bit divisions
+      const uint32_t i = static_cast<uint32_t>(item), rh = i / per;
+      col = static_cast<int>(i - rh * per) * cols;
+      const uint32_t r = rh / static_cast<uint32_t>(p.heads);
+      row = r;
+      head = static_cast<int>(rh - r * p.heads);
+    } else {
+      const int64_t rh = item / per;
+      col = static_cast<int>(item - rh * per) * cols;
+      row = rh / p.heads;
+      head = static_cast<int>(rh - row * p.heads);
+    }
+  }
+};
+
+template <int DTYPE, int FORMAT>
+__global__ void __launch_bounds__(kCacheThreads) cache_write_vec_kernel(CacheParams p) {
+  using T = typename Element<DTYPE>::T;
+  constexpr int kCols = CachePiece<FORMAT>::kCols, kEights = kCols / 8;
+  pdl_wait();
+  const int64_t items = p.rows * p.heads * (p.d / kCols);
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * (kCacheThreads * kItems) + threadIdx.x;
+  Eight<DTYPE> v[kItems][kEights];
+  int64_t slot[kItems];
+#pragma unroll
+  for (int k = 0; k < kItems; ++k) {
+    const int64_t i = i0 + k * kCacheThreads;
+    slot[k] = -1;
+    if (i < items) {
+      const ItemAt at(p, i, kCols);
+      slot[k] = row_slot(p, at.row);
+      const T* x = static_cast<const T*>(p.x) + at.row * p.row_stride + at.head * p.head_stride + at.col;
+#pragma unroll
+      for (int e = 0; e < kEights; ++e) v[k][e].load(x + 8 * e);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kItems; ++k) {
+    const int64_t i = i0 + k * kCacheThreads;
+    const ItemAt at(p, i < items ? i : 0, kCols);
+    const int64_t entry = slot[k] * p.heads + at.head;
+    float f[kEights][8];
+#pragma unroll
+    for (int e = 0; e < kEights; ++e) v[k][e].get(f[e]);
+    if constexpr (FORMAT == CSA_CACHE_BF16) {
+      Eight<CSA_DTYPE_BF16> out;
+      out.set(f[0]);
+      if (slot[k] >= 0) out.store(reinterpret_cast<uint16_t*>(p.data) + entry * p.d + at.col);
+    } else {
+      // the group's largest magnitude, as bits: an infinity or NaN is above every number
+      uint32_t top = 0;
+#pragma unroll
+      for (int e = 0; e < kEights; ++e)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) top = max(top, __float_as_uint(f[e][c]) & 0x7FFFFFFFu);
+      top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+      const uint32_t b = scale_byte<FORMAT>(top);
+      const float inv = scale_inverse(b == 255u ? 127u : b);
+      if (slot[k] >= 0) {
+        uint32_t w[4];
+        if constexpr (FORMAT == CSA_CACHE_E4M3) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float* g = &f[q / 2][(q % 2) * 4];
+            w[q] = float2_to_e4m3x2(g[0] * inv, g[1] * inv) |
+                   (static_cast<uint32_t>(float2_to_e4m3x2(g[2] * inv, g[3] * inv)) << 16);
+          }
+          *reinterpret_cast<uint4*>(p.data + entry * p.d + at.col) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const float* g = f[q];
+            w[q] = float2_to_e2m1x2(g[0] * inv, g[1] * inv) | (float2_to_e2m1x2(g[2] * inv, g[3] * inv) << 8) |
+                   (float2_to_e2m1x2(g[4] * inv, g[5] * inv) << 16) | (float2_to_e2m1x2(g[6] * inv, g[7] * inv) << 24);
+          }
+          *reinterpret_cast<uint2*>(p.data + entry * (p.d / 2) + at.col / 2) = make_uint2(w[0], w[1]);
+        }
+        if ((at.col & 16) == 0) p.scales[entry * (p.d / CSA_CACHE_GROUP) + at.col / CSA_CACHE_GROUP] = static_cast<uint8_t>(b);
+      }
+    }
+  }
+}
+
+template <int DTYPE, int FORMAT>
+__global__ void __launch_bounds__(kCacheThreads) cache_read_vec_kernel(CacheParams p) {
+  using T = typename Element<DTYPE>::T;
+  constexpr int kCols = CachePiece<FORMAT>::kCols, kEights = kCols / 8;
+  pdl_wait();
+  const int64_t items = p.rows * p.heads * (p.d / kCols);
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * (kCacheThreads * kItems) + threadIdx.x;
+  uint4 v[kItems];
+  uint32_t b[kItems];
+  bool on[kItems];
+#pragma unroll
+  for (int k = 0; k < kItems; ++k) {
+    const int64_t i = i0 + k * kCacheThreads;
+    on[k] = false;
+    if (i < items) {
+      const ItemAt at(p, i, kCols);
+      const int64_t slot = row_slot(p, at.row);
+      on[k] = slot >= 0;
+      if (on[k]) {
+        const int64_t entry = slot * p.heads + at.head;
+        if constexpr (FORMAT == CSA_CACHE_BF16) {
+          v[k] = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.data) + entry * p.d + at.col));
+        } else {
+          b[k] = __ldg(p.scales + entry * (p.d / CSA_CACHE_GROUP) + at.col / CSA_CACHE_GROUP);
+          if constexpr (FORMAT == CSA_CACHE_E4M3) {
+            v[k] = __ldg(reinterpret_cast<const uint4*>(p.data + entry * p.d + at.col));
+          } else {
+            const uint2 w = __ldg(reinterpret_cast<const uint2*>(p.data + entry * (p.d / 2) + at.col / 2));
+            v[k].x = w.x;
+            v[k].y = w.y;
+          }
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kItems; ++k) {
+    if (!on[k]) continue;
+    const ItemAt at(p, i0 + k * kCacheThreads, kCols);
+    T* out = static_cast<T*>(p.out) + at.row * p.row_stride + at.head * p.head_stride + at.col;
+    float f[kEights][8];
+    if constexpr (FORMAT == CSA_CACHE_BF16) {
+      Eight<CSA_DTYPE_BF16> e;
+      e.w[0] = v[k];
+      e.get(f[0]);
+    } else {
+      const float s = scale_value(b[k]);
+      const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const float2 two = FORMAT == CSA_CACHE_E4M3 ? e4m3x2_to_float2((w[q / 2] >> (16 * (q % 2))) & 0xFFFFu)
+                                                   : e2m1x2_to_float2(w[q / 4] >> (8 * (q % 4)));
+        f[q / 4][(q % 4) * 2] = two.x * s;
+        f[q / 4][(q % 4) * 2 + 1] = two.y * s;
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < kEights; ++e) {
+      Eight<DTYPE> o;
+      o.set(f[e]);
+      o.store(out + 8 * e);
+    }
+  }
+}
+
 // Calls f with the cache format as a compile-time constant.
 template <typename F>
 auto by_format(int format, F f) {
@@ -139,15 +302,28 @@ csa_status_t check_cache(const void* x, int32_t dtype, int64_t rows, int32_t hea
   return CSA_OK;
 }
 
-csa_status_t launch_scalar(const void* k, CacheParams& p, csa_stream_t stream) {
-  int dev = 0, sms = 0;
-  if (note(cudaGetDevice(&dev)) != cudaSuccess || device_sms(dev, &sms) != cudaSuccess)
-    return CSA_ERR_CUDA;
-  const int64_t warps = p.rows * p.heads * ((p.d + 31) / 32);
-  const int64_t want = (warps + kCacheThreads / 32 - 1) / (kCacheThreads / 32);
-  const int64_t most = 64 * static_cast<int64_t>(sms);
+// Whether a call's shapes and pointers suit the vector kernels.
+bool vector_call(const CacheParams& p, const void* x) {
+  return p.d % 8 == 0 && p.row_stride % 8 == 0 && p.head_stride % 8 == 0 && is_aligned(x, 16) &&
+         is_aligned(p.data, 16);
+}
+
+csa_status_t launch_cache(const void* k, bool vec, int cols, CacheParams& p, csa_stream_t stream) {
+  int64_t blocks;
+  if (vec) {
+    blocks = (p.rows * p.heads * (p.d / cols) + kCacheThreads * kItems - 1) / (kCacheThreads * kItems);
+    if (blocks > INT_MAX) return CSA_ERR_UNSUPPORTED;
+  } else {
+    int dev = 0, sms = 0;
+    if (note(cudaGetDevice(&dev)) != cudaSuccess || device_sms(dev, &sms) != cudaSuccess)
+      return CSA_ERR_CUDA;
+    const int64_t warps = p.rows * p.heads * ((p.d + 31) / 32);
+    const int64_t want = (warps + kCacheThreads / 32 - 1) / (kCacheThreads / 32);
+    const int64_t most = 64 * static_cast<int64_t>(sms);
+    blocks = want < most ? want : most;
+  }
   void* args[] = {&p};
-  return launch_pdl(k, dim3(static_cast<unsigned>(want < most ? want : most)), dim3(kCacheThreads), 0,
+  return launch_pdl(k, dim3(static_cast<unsigned>(blocks)), dim3(kCacheThreads), 0,
                     reinterpret_cast<cudaStream_t>(stream), args) == cudaSuccess
              ? CSA_OK
              : CSA_ERR_CUDA;
@@ -178,12 +354,17 @@ extern "C" csa_status_t csa_cache_write(const void* x, int32_t dtype, int64_t ro
   p.head_stride = x_head_stride;
   p.heads = heads;
   p.d = d;
+  const bool vec = vector_call(p, x);
+  int cols = 0;
   const void* k = by_dtype(dtype, [&](auto t) {
-    return by_format(format, [](auto f) {
-      return reinterpret_cast<const void*>(cache_write_scalar_kernel<decltype(t)::value, decltype(f)::value>);
+    return by_format(format, [&](auto f) {
+      constexpr int T = decltype(t)::value, F = decltype(f)::value;
+      cols = CachePiece<F>::kCols;
+      return vec ? reinterpret_cast<const void*>(cache_write_vec_kernel<T, F>)
+                 : reinterpret_cast<const void*>(cache_write_scalar_kernel<T, F>);
     });
   });
-  return launch_scalar(k, p, stream);
+  return launch_cache(k, vec, cols, p, stream);
 }
 
 extern "C" csa_status_t csa_cache_read(const void* data, const uint8_t* scales, int32_t format,
@@ -206,10 +387,15 @@ extern "C" csa_status_t csa_cache_read(const void* data, const uint8_t* scales, 
   p.head_stride = out_head_stride;
   p.heads = heads;
   p.d = d;
+  const bool vec = vector_call(p, out);
+  int cols = 0;
   const void* k = by_dtype(dtype, [&](auto t) {
-    return by_format(format, [](auto f) {
-      return reinterpret_cast<const void*>(cache_read_scalar_kernel<decltype(t)::value, decltype(f)::value>);
+    return by_format(format, [&](auto f) {
+      constexpr int T = decltype(t)::value, F = decltype(f)::value;
+      cols = CachePiece<F>::kCols;
+      return vec ? reinterpret_cast<const void*>(cache_read_vec_kernel<T, F>)
+                 : reinterpret_cast<const void*>(cache_read_scalar_kernel<T, F>);
     });
   });
-  return launch_scalar(k, p, stream);
+  return launch_cache(k, vec, cols, p, stream);
 }

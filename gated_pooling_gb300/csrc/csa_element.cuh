@@ -51,6 +51,59 @@ inline bool is_aligned(const void* p, uintptr_t a) {
   return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
 }
 
+// 8 consecutive columns, 16-byte aligned: as they lie in memory, and as fp32.
+template <int DTYPE>
+struct Eight {
+  static constexpr int kWords = dtype_size(DTYPE) / 2;  // 16-byte words
+  uint4 w[kWords];
+  __device__ __forceinline__ void load(const void* p) {
+    const uint4* q = static_cast<const uint4*>(p);
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
+                   : "l"(q + i));
+    }
+  }
+  __device__ __forceinline__ void store(void* p) const {
+    uint4* q = static_cast<uint4*>(p);
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) q[i] = w[i];
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (DTYPE == CSA_DTYPE_FP32) {
+        v[2 * i] = __uint_as_float(i < 2 ? (i == 0 ? w[0].x : w[0].z) : (i == 2 ? w[kWords - 1].x : w[kWords - 1].z));
+        v[2 * i + 1] = __uint_as_float(i < 2 ? (i == 0 ? w[0].y : w[0].w) : (i == 2 ? w[kWords - 1].y : w[kWords - 1].w));
+      } else {
+        const uint32_t x = i == 0 ? w[0].x : i == 1 ? w[0].y : i == 2 ? w[0].z : w[0].w;
+        if constexpr (DTYPE == CSA_DTYPE_BF16) {
+          v[2 * i] = bf16_lo(x);
+          v[2 * i + 1] = bf16_hi(x);
+        } else {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x));
+          v[2 * i] = f.x;
+          v[2 * i + 1] = f.y;
+        }
+      }
+    }
+  }
+  static __device__ __forceinline__ uint32_t two(float a, float b) {
+    if constexpr (DTYPE == CSA_DTYPE_BF16) return pack_bf16x2(a, b);
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  __device__ __forceinline__ void set(const float (&v)[8]) {
+    if constexpr (DTYPE == CSA_DTYPE_FP32) {
+      w[0] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+      w[kWords - 1] = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
+    } else {
+      w[0] = make_uint4(two(v[0], v[1]), two(v[2], v[3]), two(v[4], v[5]), two(v[6], v[7]));
+    }
+  }
+};
+
 // ---------------------------------------------------------------------------------
 // Cache codes. Two e4m3 codes to two fp32 values (both exact in fp16), four e2m1 codes
 // likewise, and back, rounding to nearest even.

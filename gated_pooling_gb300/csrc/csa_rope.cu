@@ -35,6 +35,7 @@ struct RopeParams {
   int64_t units;  // rows * heads
   int heads, d, rot, start;
   int norm, interleaved;
+  int lanes;  // vector kernels: lanes of a row's head (a power of two)
   float eps, amp;
 };
 
@@ -185,6 +186,406 @@ __global__ void __launch_bounds__(kRopeThreads) rope_scalar_bwd_kernel(RopeParam
   }
 }
 
+// ---------------------------------------------------------------------------------
+// Vector kernels: d, strides and the rotated part in pieces of 8 columns.
+//
+// A lane owns PP pairs of pieces: with the half layout a rotated pair's two pieces hold the
+// members of 8 column pairs, so no value changes lanes; all other pieces are paired by
+// distance, so that neighbouring lanes read neighbouring pieces. `lanes` (up to 32) lanes
+// share a row's head, 32 / lanes heads go through a warp at once, and a warp takes a run of
+// consecutive heads and rows, so the angles of a row serve all its heads. The next head's
+// pieces are loaded while one is computed.
+//
+// 16-bit types take cos and sin from the hardware approximation (within 2^-21 of the value at
+// an angle already brought to half a turn either way: 2^-9 and 2^-12 of a result are
+// rounded away behind it); fp32 from CUDA's functions.
+// ---------------------------------------------------------------------------------
+template <int DTYPE, int PP>
+struct RopeLane {
+  int a[PP], b[PP];        // first columns of the pair's pieces, -1: none
+  int ia[PP], ib[PP];      // first turns of their 8 (half) or 4 + 4 (interleaved) pairs, -1: not rotated
+  float cs[PP][8], sn[PP][8];
+  int lane, sub, group, groups;
+
+  __device__ __forceinline__ explicit RopeLane(const RopeParams& p) {
+    lane = threadIdx.x & 31;
+    sub = lane & (p.lanes - 1);
+    group = lane / p.lanes;
+    groups = 32 / p.lanes;
+    const int n = p.d / 8, s0 = p.start / 8, nr = p.rot / 8;
+#pragma unroll
+    for (int s = 0; s < PP; ++s) {
+      const int k = sub + 32 * s;
+      ia[s] = ib[s] = -1;
+      int ca, cb;
+      if (p.interleaved) {
+        const int h = (n + 1) / 2;
+        ca = k < h ? k : -1;
+        cb = k < h && k + h < n ? k + h : -1;
+        if (ca >= s0 && ca < s0 + nr) ia[s] = (ca - s0) * 4;
+        if (cb >= s0 && cb < s0 + nr) ib[s] = (cb - s0) * 4;
+      } else if (k < nr / 2) {
+        ca = s0 + k;
+        cb = ca + nr / 2;
+        ia[s] = k * 8;
+      } else {
+        const int m = n - nr, h = (m + 1) / 2, j = k - nr / 2;
+        ca = j < h ? j : -1;
+        cb = j < h && j + h < m ? j + h : -1;
+        if (ca >= s0) ca += nr;
+        if (cb >= s0) cb += nr;
+      }
+      a[s] = ca < 0 ? -1 : ca * 8;
+      b[s] = cb < 0 ? -1 : cb * 8;
+    }
+  }
+
+  __device__ __forceinline__ void angle(const RopeParams& p, int32_t pos, uint64_t per, float& c, float& s) {
+    if constexpr (DTYPE == CSA_DTYPE_FP32) {
+      turn_cos_sin(pos, per, p.amp, c, s);
+    } else {
+      const uint64_t t = static_cast<uint64_t>(static_cast<int64_t>(pos)) * per;
+      const float x = static_cast<float>(static_cast<int32_t>(t >> 32)) * 1.46291807926715968105e-9f;  // pi 2^-31
+      c = __cosf(x) * p.amp;
+      s = __sinf(x) * p.amp;
+    }
+  }
+  // the angles of a row
+  __device__ __forceinline__ void turn_to(const RopeParams& p, int32_t pos) {
+#pragma unroll
+    for (int s = 0; s < PP; ++s) {
+      if (ia[s] < 0 && ib[s] < 0) continue;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int i0 = h == 0 ? ia[s] : (p.interleaved ? ib[s] : ia[s] + 4);
+        if (i0 < 0) continue;
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+          const ulonglong2 per = __ldg(reinterpret_cast<const ulonglong2*>(p.turns + i0 + i));
+          angle(p, pos, per.x, cs[s][4 * h + i], sn[s][4 * h + i]);
+          angle(p, pos, per.y, cs[s][4 * h + i + 1], sn[s][4 * h + i + 1]);
+        }
+      }
+    }
+  }
+  // the pair's values turned, or turned back
+  template <bool BACK>
+  __device__ __forceinline__ void turn(const RopeParams& p, int s, float (&x)[8], float (&y)[8]) const {
+    auto two = [&](float& u, float& v, float c, float n) {
+      if (BACK) n = -n;
+      const float w = u * c - v * n;
+      v = u * n + v * c;
+      u = w;
+    };
+    if (p.interleaved) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (ia[s] >= 0) two(x[2 * i], x[2 * i + 1], cs[s][i], sn[s][i]);
+        if (ib[s] >= 0) two(y[2 * i], y[2 * i + 1], cs[s][4 + i], sn[s][4 + i]);
+      }
+    } else if (ia[s] >= 0) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) two(x[i], y[i], cs[s][i], sn[s][i]);
+    }
+  }
+  // sum over the head's lanes
+  __device__ __forceinline__ float sum(const RopeParams& p, float v) const {
+    for (int o = p.lanes / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+  }
+};
+
+// A warp's run of heads: this lane's row and head, moving on by the warp's groups.
+struct RopeRun {
+  int64_t u, end;  // unit of this lane's group, end of the warp's run
+  int64_t row;
+  int head, step_rows, step_heads;
+  __device__ __forceinline__ RopeRun(const RopeParams& p, int group, int groups) {
+    const int64_t warps = static_cast<int64_t>(gridDim.x) * kRopeWarps;
+    const int64_t w = static_cast<int64_t>(blockIdx.x) * kRopeWarps + (threadIdx.x >> 5);
+    u = p.units * w / warps;
+    end = p.units * (w + 1) / warps;
+    u += group;
+    row = u / p.heads;
+    head = static_cast<int>(u - row * p.heads);
+    step_rows = groups / p.heads;
+    step_heads = groups - step_rows * p.heads;
+  }
+  __device__ __forceinline__ bool valid() const { return u < end; }
+  __device__ __forceinline__ void next(const RopeParams& p, int groups) {
+    u += groups;
+    row += step_rows;
+    head += step_heads;
+    if (head >= p.heads) {
+      head -= p.heads;
+      ++row;
+    }
+  }
+};
+
+// This lane's pieces of a row's head.
+template <int DTYPE, int PP>
+struct RopePieces {
+  Eight<DTYPE> a[PP], b[PP];
+  __device__ __forceinline__ void load(const RopeLane<DTYPE, PP>& L, const void* x, int64_t at) {
+    const typename Element<DTYPE>::T* q = static_cast<const typename Element<DTYPE>::T*>(x) + at;
+#pragma unroll
+    for (int s = 0; s < PP; ++s) {
+      if (L.a[s] >= 0) a[s].load(q + L.a[s]);
+      if (L.b[s] >= 0) b[s].load(q + L.b[s]);
+    }
+  }
+};
+
+__device__ __forceinline__ void load_weight(const RopeParams& p, int col, float (&w)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = 1.f;
+  if (p.weight == nullptr || col < 0) return;
+#pragma unroll
+  for (int i = 0; i < 8; i += 4) {
+    const float4 t = __ldg(reinterpret_cast<const float4*>(p.weight + col + i));
+    w[i] = t.x;
+    w[i + 1] = t.y;
+    w[i + 2] = t.z;
+    w[i + 3] = t.w;
+  }
+}
+
+template <int DTYPE, int PP>
+__global__ void __launch_bounds__(kRopeThreads, PP == 1 && DTYPE != CSA_DTYPE_FP32 ? 3 : 2)
+    rope_vec_kernel(RopeParams p) {
+  using T = typename Element<DTYPE>::T;
+  RopeLane<DTYPE, PP> L(p);
+  pdl_wait();
+  float wa[PP][8], wb[PP][8];
+#pragma unroll
+  for (int s = 0; s < PP; ++s) {
+    load_weight(p, L.a[s], wa[s]);
+    load_weight(p, L.b[s], wb[s]);
+  }
+  const float inv_d = 1.f / static_cast<float>(p.d);
+  RopeRun run(p, L.group, L.groups);
+  int64_t base = p.units;  // the warp's first unit: all its lanes leave the loop together
+  base = run.u - L.group;
+  RopePieces<DTYPE, PP> cur, nxt;
+  int32_t pos = -1, pos_n = -1;
+  auto fetch = [&](RopePieces<DTYPE, PP>& v, int32_t& ps) {
+    ps = -1;
+    if (run.valid()) {
+      ps = p.pos != nullptr ? __ldg(p.pos + run.row) : 0;
+      v.load(L, p.x, run.row * p.x_row + run.head * p.x_head);
+    }
+  };
+  fetch(cur, pos);
+  int64_t turned = -1;
+  for (; base < run.end; base += L.groups) {
+    const int64_t row = run.row;
+    const int head = run.head;
+    run.next(p, L.groups);
+    fetch(nxt, pos_n);
+    float xa[PP][8], xb[PP][8];
+    float r = 1.f;
+    float ss = 0.f;
+#pragma unroll
+    for (int s = 0; s < PP; ++s) {
+      cur.a[s].get(xa[s]);
+      cur.b[s].get(xb[s]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (L.a[s] >= 0) ss = fmaf(xa[s][i], xa[s][i], ss);
+        if (L.b[s] >= 0) ss = fmaf(xb[s][i], xb[s][i], ss);
+      }
+    }
+    if (p.norm) r = rsqrtf(fmaf(L.sum(p, ss), inv_d, p.eps));
+    if (pos >= 0) {
+      if (row != turned) {
+        L.turn_to(p, pos);
+        turned = row;
+      }
+      T* y = static_cast<T*>(p.y) + row * p.y_row + head * p.y_head;
+#pragma unroll
+      for (int s = 0; s < PP; ++s) {
+        if (p.norm) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            xa[s][i] = xa[s][i] * r * wa[s][i];
+            xb[s][i] = xb[s][i] * r * wb[s][i];
+          }
+        }
+        L.template turn<false>(p, s, xa[s], xb[s]);
+        Eight<DTYPE> o;
+        if (L.a[s] >= 0) {
+          o.set(xa[s]);
+          o.store(y + L.a[s]);
+        }
+        if (L.b[s] >= 0) {
+          o.set(xb[s]);
+          o.store(y + L.b[s]);
+        }
+      }
+    }
+    cur = nxt;
+    pos = pos_n;
+  }
+}
+
+// Backward. dweight: a lane sums its columns over at most kDwRun heads in registers, then the
+// warp's groups join them and add them to the warp's sums in shared memory; the block adds
+// its warps in order and writes one partial row. No chain of plain additions is longer than
+// kDwRun, or a warp's heads / (kDwRun * groups).
+constexpr int kDwRun = 16;
+template <int DTYPE, int PP>
+__global__ void __launch_bounds__(kRopeThreads, PP == 1 ? 2 : 1) rope_vec_bwd_kernel(RopeParams p) {
+  using T = typename Element<DTYPE>::T;
+  extern __shared__ float s_dw[];  // [warps][d]
+  RopeLane<DTYPE, PP> L(p);
+  float* sums = s_dw + (threadIdx.x >> 5) * p.d;
+  if (p.partial != nullptr)
+    for (int c = L.lane; c < p.d; c += 32) sums[c] = 0.f;
+  __syncwarp();
+  pdl_wait();
+  float wa[PP][8], wb[PP][8], da[PP][8], db[PP][8];
+#pragma unroll
+  for (int s = 0; s < PP; ++s) {
+    load_weight(p, L.a[s], wa[s]);
+    load_weight(p, L.b[s], wb[s]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) da[s][i] = db[s][i] = 0.f;
+  }
+  auto flush = [&]() {
+#pragma unroll
+    for (int s = 0; s < PP; ++s)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float va = da[s][i], vb = db[s][i];
+        for (int o = p.lanes; o < 32; o <<= 1) {
+          va += __shfl_xor_sync(0xFFFFFFFFu, va, o);
+          vb += __shfl_xor_sync(0xFFFFFFFFu, vb, o);
+        }
+        if (L.group == 0) {
+          if (L.a[s] >= 0) sums[L.a[s] + i] += va;
+          if (L.b[s] >= 0) sums[L.b[s] + i] += vb;
+        }
+        da[s][i] = db[s][i] = 0.f;
+      }
+  };
+  const float inv_d = 1.f / static_cast<float>(p.d);
+  RopeRun run(p, L.group, L.groups);
+  int64_t base = run.u - L.group;
+  RopePieces<DTYPE, PP> cx, cg, nx, ng;
+  int32_t pos = -1, pos_n = -1;
+  auto fetch = [&](RopePieces<DTYPE, PP>& vx, RopePieces<DTYPE, PP>& vg, int32_t& ps) {
+    ps = -1;
+    if (run.valid()) {
+      ps = p.pos != nullptr ? __ldg(p.pos + run.row) : 0;
+      if (p.norm) vx.load(L, p.x, run.row * p.x_row + run.head * p.x_head);
+      vg.load(L, p.dy, run.row * p.dy_row + run.head * p.dy_head);
+    }
+  };
+  fetch(cx, cg, pos);
+  int64_t turned = -1;
+  int since = 0;
+  for (; base < run.end; base += L.groups) {
+    const int64_t row = run.row;
+    const int head = run.head;
+    run.next(p, L.groups);
+    fetch(nx, ng, pos_n);
+    if (pos >= 0 && row != turned) {
+      L.turn_to(p, pos);
+      turned = row;
+    }
+    float ga[PP][8], gb[PP][8], xa[PP][8], xb[PP][8];
+    float ss = 0.f, dot = 0.f;
+#pragma unroll
+    for (int s = 0; s < PP; ++s) {
+      cg.a[s].get(ga[s]);
+      cg.b[s].get(gb[s]);
+      if (pos >= 0) L.template turn<true>(p, s, ga[s], gb[s]);
+      if (p.norm) {
+        cx.a[s].get(xa[s]);
+        cx.b[s].get(xb[s]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (L.a[s] >= 0) {
+            ss = fmaf(xa[s][i], xa[s][i], ss);
+            dot = fmaf(ga[s][i] * wa[s][i], xa[s][i], dot);
+          }
+          if (L.b[s] >= 0) {
+            ss = fmaf(xb[s][i], xb[s][i], ss);
+            dot = fmaf(gb[s][i] * wb[s][i], xb[s][i], dot);
+          }
+        }
+      }
+    }
+    if (p.norm) {
+      const float r = rsqrtf(fmaf(L.sum(p, ss), inv_d, p.eps));
+      const float k = L.sum(p, dot) * inv_d * r * r;
+      if (pos >= 0) {
+#pragma unroll
+        for (int s = 0; s < PP; ++s)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            da[s][i] = fmaf(ga[s][i], xa[s][i] * r, da[s][i]);
+            db[s][i] = fmaf(gb[s][i], xb[s][i] * r, db[s][i]);
+            ga[s][i] = r * (ga[s][i] * wa[s][i] - xa[s][i] * k);
+            gb[s][i] = r * (gb[s][i] * wb[s][i] - xb[s][i] * k);
+          }
+      }
+    }
+    if (pos >= 0) {
+      T* dx = static_cast<T*>(p.y) + row * p.y_row + head * p.y_head;
+#pragma unroll
+      for (int s = 0; s < PP; ++s) {
+        Eight<DTYPE> o;
+        if (L.a[s] >= 0) {
+          o.set(ga[s]);
+          o.store(dx + L.a[s]);
+        }
+        if (L.b[s] >= 0) {
+          o.set(gb[s]);
+          o.store(dx + L.b[s]);
+        }
+      }
+    }
+    cx = nx;
+    cg = ng;
+    pos = pos_n;
+    if (p.partial != nullptr && ++since == kDwRun) {
+      flush();
+      since = 0;
+    }
+  }
+  if (p.partial == nullptr) return;
+  flush();
+  __syncthreads();
+  for (int c = threadIdx.x; c < p.d; c += kRopeThreads) {
+    float s = 0.f, e = 0.f;
+    for (int w = 0; w < kRopeWarps; ++w) neumaier_add(s, e, s_dw[w * p.d + c]);
+    p.partial[static_cast<int64_t>(blockIdx.x) * p.d + c] = s + e;
+  }
+}
+
+// Lanes of a row's head, or 0 where the vector kernels do not take the call.
+int vector_lanes(const RopeParams& p, int dtype, const void* x, const void* y, const void* z) {
+  const bool fits = p.d % 8 == 0 && p.start % 8 == 0 && p.rot % (p.interleaved ? 8 : 16) == 0 &&
+                    p.x_row % 8 == 0 && p.x_head % 8 == 0 && p.y_row % 8 == 0 && p.y_head % 8 == 0 &&
+                    p.dy_row % 8 == 0 && p.dy_head % 8 == 0 && is_aligned(x, 16) && is_aligned(y, 16) &&
+                    is_aligned(z, 16) && is_aligned(p.weight, 16) && is_aligned(p.turns, 16);
+  if (!fits) return 0;
+  const int n = p.d / 8;
+  // pairs of pieces: the half layout's rotated pieces pair among themselves
+  const int pairs = p.interleaved ? (n + 1) / 2 : p.rot / 16 + (n - p.rot / 8 + 1) / 2;
+  int lanes = 1;
+  while (lanes < 32 && lanes < pairs) lanes *= 2;
+  return lanes;
+}
+// Pairs of pieces a lane holds: one up to d = 512.
+int vector_pairs(const RopeParams& p) {
+  const int n = p.d / 8;
+  const int pairs = p.interleaved ? (n + 1) / 2 : p.rot / 16 + (n - p.rot / 8 + 1) / 2;
+  return pairs <= 32 ? 1 : 2;
+}
+
 // Blocks of the backward (= partial rows): enough to fill the GPU, at most one per warp's worth
 // of units.
 int64_t bwd_blocks(int64_t units, int sms) {
@@ -297,10 +698,25 @@ extern "C" csa_status_t csa_norm_rope_fwd(const void* x, int32_t dtype, int64_t 
   p.x_head = x_head_stride;
   p.y_row = y_row_stride;
   p.y_head = y_head_stride;
-  const void* k = by_dtype(dtype, [](auto t) {
-    return reinterpret_cast<const void*>(rope_scalar_kernel<decltype(t)::value>);
+  p.lanes = vector_lanes(p, dtype, x, y, nullptr);
+  const bool wide = vector_pairs(p) == 2;
+  const void* k = by_dtype(dtype, [&](auto t) {
+    constexpr int T = decltype(t)::value;
+    return p.lanes == 0 ? reinterpret_cast<const void*>(rope_scalar_kernel<T>)
+           : wide       ? reinterpret_cast<const void*>(rope_vec_kernel<T, 2>)
+                        : reinterpret_cast<const void*>(rope_vec_kernel<T, 1>);
   });
-  const int64_t blocks = (p.units + kRopeWarps - 1) / kRopeWarps;
+  int64_t blocks = (p.units + kRopeWarps - 1) / kRopeWarps;
+  if (p.lanes != 0) {
+    // one run of heads a resident warp
+    int dev = 0, sms = 0, bps = 0;
+    if (note(cudaGetDevice(&dev)) != cudaSuccess || device_sms(dev, &sms) != cudaSuccess ||
+        blocks_per_sm(dev, k, kRopeThreads, 0, &bps) != cudaSuccess)
+      return CSA_ERR_CUDA;
+    const int64_t per = kRopeWarps * (32 / p.lanes), most = static_cast<int64_t>(sms) * bps;
+    blocks = (p.units + per - 1) / per;
+    if (blocks > most) blocks = most;
+  }
   void* args[] = {&p};
   if (launch_pdl(k, dim3(static_cast<unsigned>(blocks)), dim3(kRopeThreads), 0,
                  reinterpret_cast<cudaStream_t>(stream), args) != cudaSuccess)
@@ -358,10 +774,15 @@ extern "C" csa_status_t csa_norm_rope_bwd(
   p.y_row = dx_row_stride;
   p.y_head = dx_head_stride;
   p.partial = dweight != nullptr ? static_cast<float*>(workspace) : nullptr;
-  const void* k = by_dtype(dtype, [](auto t) {
-    return reinterpret_cast<const void*>(rope_scalar_bwd_kernel<decltype(t)::value>);
+  p.lanes = vector_lanes(p, dtype, norm != 0 ? x : nullptr, dx, dy);
+  const bool wide = vector_pairs(p) == 2;
+  const void* k = by_dtype(dtype, [&](auto t) {
+    constexpr int T = decltype(t)::value;
+    return p.lanes == 0 ? reinterpret_cast<const void*>(rope_scalar_bwd_kernel<T>)
+           : wide       ? reinterpret_cast<const void*>(rope_vec_bwd_kernel<T, 2>)
+                        : reinterpret_cast<const void*>(rope_vec_bwd_kernel<T, 1>);
   });
-  const size_t smem = dweight != nullptr ? sizeof(float) * kRopeWarps * 2 * d : 0;
+  const size_t smem = dweight != nullptr ? sizeof(float) * kRopeWarps * (p.lanes == 0 ? 2 : 1) * d : 0;
   int bps = 0;
   if (blocks_per_sm(dev, k, kRopeThreads, smem, &bps) != cudaSuccess) return CSA_ERR_CUDA;
   if (bps < 1) return CSA_ERR_UNSUPPORTED;
