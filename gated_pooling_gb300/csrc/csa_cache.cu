@@ -20,6 +20,22 @@ namespace {
 
 constexpr int kCacheThreads = 256;
 
+// Division of numbers below 2^31 by n: floor(x m / 2^(31 + l)) with l = ceil(log2 n) and m =
+// floor(2^(31 + l) / n) + 1 < 2^32 is exact there (Granlund and Montgomery 1994).
+struct FastDivisor {
+  uint32_t n = 1, m = 0, shift = 31;
+  FastDivisor() = default;
+  explicit FastDivisor(uint32_t d) : n(d) {
+    uint32_t l = 0;
+    while ((1ull << l) < d) ++l;
+    shift = 31 + l;
+    m = static_cast<uint32_t>((1ull << shift) / d + (d == 1 ? 0 : 1));
+  }
+  __device__ __forceinline__ uint32_t quotient(uint32_t x) const {
+    return static_cast<uint32_t>((static_cast<uint64_t>(x) * m) >> shift);
+  }
+};
+
 struct CacheParams {
   const void* x;  // rows: read by the write kernels
   void* out;      // rows: written by the read kernels
@@ -29,6 +45,7 @@ struct CacheParams {
   int32_t* dev_error;
   int64_t rows, num_slots, row_stride, head_stride;
   int heads, d;
+  FastDivisor pieces, by_heads;  // vector kernels: pieces of a row's head, heads
 };
 
 // Slot of a row, or -1 where the row is left out; reports slots past the pool's end.
@@ -110,9 +127,12 @@ __global__ void __launch_bounds__(kCacheThreads) cache_read_scalar_kernel(CacheP
 }
 
 // Vector kernels: a thread takes 16 consecutive columns of a row's head (8 of a bf16 cache), two
-// neighbouring threads share a scale; kItems of them are under way per thread. 16-byte
-// accesses throughout (8 bytes of e2m1).
-constexpr int kItems = 2;
+// neighbouring threads share a scale; 16-byte accesses (8 bytes of e2m1). What is left beside
+// the bytes is finding a thread's place, so its two divisions are products with reciprocals
+// (items below 2^31), and 8 columns a thread, with twice the places, was slower: 24571 entries
+// of 512 written and read back took 25.4 us instead of 14.9 (5.1 TB/s).
+// One item a thread: with 2 or 4 under way the same took 16.0 or 19.4 us instead of 14.9.
+constexpr int kItems = 1;
 template <int FORMAT>
 struct CachePiece {
   static constexpr int kCols = FORMAT == CSA_CACHE_BF16 ? 8 : 16;
@@ -120,22 +140,12 @@ struct CachePiece {
 
 // Row, head and first column of a thread's item.
 struct ItemAt {
-  int64_t row;
-  int head, col;
-  __device__ __forceinline__ ItemAt(const CacheParams& p, int64_t item, int cols) {
-    const uint32_t per = static_cast<uint32_t>(p.d / cols);
-    if (item < INT_MAX) {  // 32-bit divisions
-      const uint32_t i = static_cast<uint32_t>(item), rh = i / per;
-      col = static_cast<int>(i - rh * per) * cols;
-      const uint32_t r = rh / static_cast<uint32_t>(p.heads);
-      row = r;
-      head = static_cast<int>(rh - r * p.heads);
-    } else {
-      const int64_t rh = item / per;
-      col = static_cast<int>(item - rh * per) * cols;
-      row = rh / p.heads;
-      head = static_cast<int>(rh - row * p.heads);
-    }
+  int row, head, col;
+  __device__ __forceinline__ ItemAt(const CacheParams& p, uint32_t item, int cols) {
+    const uint32_t rh = p.pieces.quotient(item), r = p.by_heads.quotient(rh);
+    col = static_cast<int>(item - rh * p.pieces.n) * cols;
+    row = static_cast<int>(r);
+    head = static_cast<int>(rh - r * p.by_heads.n);
   }
 };
 
@@ -144,34 +154,36 @@ __global__ void __launch_bounds__(kCacheThreads) cache_write_vec_kernel(CachePar
   using T = typename Element<DTYPE>::T;
   constexpr int kCols = CachePiece<FORMAT>::kCols, kEights = kCols / 8;
   pdl_wait();
-  const int64_t items = p.rows * p.heads * (p.d / kCols);
-  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * (kCacheThreads * kItems) + threadIdx.x;
+  const uint32_t items = static_cast<uint32_t>(p.rows) * p.heads * p.pieces.n;
+  const uint32_t i0 = blockIdx.x * (kCacheThreads * kItems) + threadIdx.x;
   Eight<DTYPE> v[kItems][kEights];
-  int64_t slot[kItems];
+  int64_t entry[kItems];  // -1: left out
+  int cols[kItems];
 #pragma unroll
   for (int k = 0; k < kItems; ++k) {
-    const int64_t i = i0 + k * kCacheThreads;
-    slot[k] = -1;
+    const uint32_t i = i0 + k * kCacheThreads;
+    entry[k] = -1;
+    cols[k] = 0;
     if (i < items) {
       const ItemAt at(p, i, kCols);
-      slot[k] = row_slot(p, at.row);
-      const T* x = static_cast<const T*>(p.x) + at.row * p.row_stride + at.head * p.head_stride + at.col;
+      cols[k] = at.col;
+      const int64_t slot = row_slot(p, at.row);
+      if (slot >= 0) entry[k] = slot * p.heads + at.head;
+      const T* x = static_cast<const T*>(p.x) + static_cast<int64_t>(at.row) * p.row_stride + at.head * p.head_stride + at.col;
 #pragma unroll
       for (int e = 0; e < kEights; ++e) v[k][e].load(x + 8 * e);
     }
   }
 #pragma unroll
   for (int k = 0; k < kItems; ++k) {
-    const int64_t i = i0 + k * kCacheThreads;
-    const ItemAt at(p, i < items ? i : 0, kCols);
-    const int64_t entry = slot[k] * p.heads + at.head;
+    const int col = cols[k];
     float f[kEights][8];
 #pragma unroll
     for (int e = 0; e < kEights; ++e) v[k][e].get(f[e]);
     if constexpr (FORMAT == CSA_CACHE_BF16) {
       Eight<CSA_DTYPE_BF16> out;
       out.set(f[0]);
-      if (slot[k] >= 0) out.store(reinterpret_cast<uint16_t*>(p.data) + entry * p.d + at.col);
+      if (entry[k] >= 0) out.store(reinterpret_cast<uint16_t*>(p.data) + entry[k] * p.d + col);
     } else {
       // the group's largest magnitude, as bits: an infinity or NaN is above every number
       uint32_t top = 0;
@@ -182,7 +194,7 @@ __global__ void __launch_bounds__(kCacheThreads) cache_write_vec_kernel(CachePar
       top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
       const uint32_t b = scale_byte<FORMAT>(top);
       const float inv = scale_inverse(b == 255u ? 127u : b);
-      if (slot[k] >= 0) {
+      if (entry[k] >= 0) {
         uint32_t w[4];
         if constexpr (FORMAT == CSA_CACHE_E4M3) {
 #pragma unroll
@@ -191,7 +203,7 @@ __global__ void __launch_bounds__(kCacheThreads) cache_write_vec_kernel(CachePar
             w[q] = float2_to_e4m3x2(g[0] * inv, g[1] * inv) |
                    (static_cast<uint32_t>(float2_to_e4m3x2(g[2] * inv, g[3] * inv)) << 16);
           }
-          *reinterpret_cast<uint4*>(p.data + entry * p.d + at.col) = make_uint4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<uint4*>(p.data + entry[k] * p.d + col) = make_uint4(w[0], w[1], w[2], w[3]);
         } else {
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
@@ -199,9 +211,9 @@ __global__ void __launch_bounds__(kCacheThreads) cache_write_vec_kernel(CachePar
             w[q] = float2_to_e2m1x2(g[0] * inv, g[1] * inv) | (float2_to_e2m1x2(g[2] * inv, g[3] * inv) << 8) |
                    (float2_to_e2m1x2(g[4] * inv, g[5] * inv) << 16) | (float2_to_e2m1x2(g[6] * inv, g[7] * inv) << 24);
           }
-          *reinterpret_cast<uint2*>(p.data + entry * (p.d / 2) + at.col / 2) = make_uint2(w[0], w[1]);
+          *reinterpret_cast<uint2*>(p.data + entry[k] * (p.d / 2) + col / 2) = make_uint2(w[0], w[1]);
         }
-        if ((at.col & 16) == 0) p.scales[entry * (p.d / CSA_CACHE_GROUP) + at.col / CSA_CACHE_GROUP] = static_cast<uint8_t>(b);
+        if ((col & 16) == 0) p.scales[entry[k] * (p.d / CSA_CACHE_GROUP) + col / CSA_CACHE_GROUP] = static_cast<uint8_t>(b);
       }
     }
   }
@@ -212,20 +224,20 @@ __global__ void __launch_bounds__(kCacheThreads) cache_read_vec_kernel(CachePara
   using T = typename Element<DTYPE>::T;
   constexpr int kCols = CachePiece<FORMAT>::kCols, kEights = kCols / 8;
   pdl_wait();
-  const int64_t items = p.rows * p.heads * (p.d / kCols);
-  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * (kCacheThreads * kItems) + threadIdx.x;
+  const uint32_t items = static_cast<uint32_t>(p.rows) * p.heads * p.pieces.n;
+  const uint32_t i0 = blockIdx.x * (kCacheThreads * kItems) + threadIdx.x;
   uint4 v[kItems];
   uint32_t b[kItems];
-  bool on[kItems];
+  T* to[kItems];  // null: left out
 #pragma unroll
   for (int k = 0; k < kItems; ++k) {
-    const int64_t i = i0 + k * kCacheThreads;
-    on[k] = false;
+    const uint32_t i = i0 + k * kCacheThreads;
+    to[k] = nullptr;
     if (i < items) {
       const ItemAt at(p, i, kCols);
       const int64_t slot = row_slot(p, at.row);
-      on[k] = slot >= 0;
-      if (on[k]) {
+      if (slot >= 0) {
+        to[k] = static_cast<T*>(p.out) + static_cast<int64_t>(at.row) * p.row_stride + at.head * p.head_stride + at.col;
         const int64_t entry = slot * p.heads + at.head;
         if constexpr (FORMAT == CSA_CACHE_BF16) {
           v[k] = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.data) + entry * p.d + at.col));
@@ -244,9 +256,7 @@ __global__ void __launch_bounds__(kCacheThreads) cache_read_vec_kernel(CachePara
   }
 #pragma unroll
   for (int k = 0; k < kItems; ++k) {
-    if (!on[k]) continue;
-    const ItemAt at(p, i0 + k * kCacheThreads, kCols);
-    T* out = static_cast<T*>(p.out) + at.row * p.row_stride + at.head * p.head_stride + at.col;
+    if (to[k] == nullptr) continue;
     float f[kEights][8];
     if constexpr (FORMAT == CSA_CACHE_BF16) {
       Eight<CSA_DTYPE_BF16> e;
@@ -267,7 +277,7 @@ __global__ void __launch_bounds__(kCacheThreads) cache_read_vec_kernel(CachePara
     for (int e = 0; e < kEights; ++e) {
       Eight<DTYPE> o;
       o.set(f[e]);
-      o.store(out + 8 * e);
+      o.store(to[k] + 8 * e);
     }
   }
 }
@@ -303,16 +313,22 @@ csa_status_t check_cache(const void* x, int32_t dtype, int64_t rows, int32_t hea
 }
 
 // Whether a call's shapes and pointers suit the vector kernels.
-bool vector_call(const CacheParams& p, const void* x) {
-  return p.d % 8 == 0 && p.row_stride % 8 == 0 && p.head_stride % 8 == 0 && is_aligned(x, 16) &&
-         is_aligned(p.data, 16);
+bool vector_call(CacheParams& p, const void* x, int format) {
+  const int cols = format == CSA_CACHE_BF16 ? 8 : 16;
+  if (p.d % 8 != 0 || p.row_stride % 8 != 0 || p.head_stride % 8 != 0 || !is_aligned(x, 16) ||
+      !is_aligned(p.data, 16))
+    return false;
+  const int64_t items = p.rows * p.heads * (p.d / cols);
+  if (items > INT_MAX - kCacheThreads * kItems) return false;
+  p.pieces = FastDivisor(static_cast<uint32_t>(p.d / cols));
+  p.by_heads = FastDivisor(static_cast<uint32_t>(p.heads));
+  return true;
 }
 
-csa_status_t launch_cache(const void* k, bool vec, int cols, CacheParams& p, csa_stream_t stream) {
+csa_status_t launch_cache(const void* k, bool vec, CacheParams& p, csa_stream_t stream) {
   int64_t blocks;
   if (vec) {
-    blocks = (p.rows * p.heads * (p.d / cols) + kCacheThreads * kItems - 1) / (kCacheThreads * kItems);
-    if (blocks > INT_MAX) return CSA_ERR_UNSUPPORTED;
+    blocks = (p.rows * p.heads * p.pieces.n + kCacheThreads * kItems - 1) / (kCacheThreads * kItems);
   } else {
     int dev = 0, sms = 0;
     if (note(cudaGetDevice(&dev)) != cudaSuccess || device_sms(dev, &sms) != cudaSuccess)
@@ -354,17 +370,15 @@ extern "C" csa_status_t csa_cache_write(const void* x, int32_t dtype, int64_t ro
   p.head_stride = x_head_stride;
   p.heads = heads;
   p.d = d;
-  const bool vec = vector_call(p, x);
-  int cols = 0;
+  const bool vec = vector_call(p, x, format);
   const void* k = by_dtype(dtype, [&](auto t) {
     return by_format(format, [&](auto f) {
       constexpr int T = decltype(t)::value, F = decltype(f)::value;
-      cols = CachePiece<F>::kCols;
       return vec ? reinterpret_cast<const void*>(cache_write_vec_kernel<T, F>)
                  : reinterpret_cast<const void*>(cache_write_scalar_kernel<T, F>);
     });
   });
-  return launch_cache(k, vec, cols, p, stream);
+  return launch_cache(k, vec, p, stream);
 }
 
 extern "C" csa_status_t csa_cache_read(const void* data, const uint8_t* scales, int32_t format,
@@ -387,15 +401,13 @@ extern "C" csa_status_t csa_cache_read(const void* data, const uint8_t* scales, 
   p.head_stride = out_head_stride;
   p.heads = heads;
   p.d = d;
-  const bool vec = vector_call(p, out);
-  int cols = 0;
+  const bool vec = vector_call(p, out, format);
   const void* k = by_dtype(dtype, [&](auto t) {
     return by_format(format, [&](auto f) {
       constexpr int T = decltype(t)::value, F = decltype(f)::value;
-      cols = CachePiece<F>::kCols;
       return vec ? reinterpret_cast<const void*>(cache_read_vec_kernel<T, F>)
                  : reinterpret_cast<const void*>(cache_read_scalar_kernel<T, F>);
     });
   });
-  return launch_cache(k, vec, cols, p, stream);
+  return launch_cache(k, vec, p, stream);
 }
