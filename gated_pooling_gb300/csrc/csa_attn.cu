@@ -113,7 +113,8 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnParams p) {
   for (int i = threadIdx.x; i < p.ctas; i += kPlanThreads) {
     const int64_t t = attn_share(all, p.ctas, i);
     AttnStart start{};
-    start.left = attn_share(all, p.ctas, i + 1) - t;
+    const int64_t next = attn_share(all, p.ctas, i + 1);
+    start.left = static_cast<int32_t>(next - t);
     if (start.left == 0) {
       p.starts[i] = start;
       continue;
@@ -127,6 +128,19 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnParams p) {
     start.u = p.units[l];
     start.unit = static_cast<int32_t>(l);
     start.tile = static_cast<int32_t>(t - p.unit_first[l]);
+    // the unit of the share's last tile: whether it begins here and goes on in later shares
+    h = units;
+    while (h - l > 1) {
+      const int64_t mid = (l + h) / 2;
+      if (p.unit_first[mid] < next) l = mid;
+      else h = mid;
+    }
+    const int64_t end = p.unit_first[l + 1];
+    if (p.unit_first[l] >= t && end > next) {
+      int last = i + 1;
+      while (last + 1 < p.ctas && attn_share(all, p.ctas, last + 1) < end) ++last;
+      start.pieces = last - i + 1;
+    }
     p.starts[i] = start;
   }
 }
@@ -378,11 +392,13 @@ extern "C" csa_status_t csa_cache_attn(
   if (tile) {
     const int nc = tile_chunks(d);
     size_t smem = 0;
+    int join_threads = 0;
     const void *k = nullptr, *join = nullptr;
     by_chunks(nc, [&](auto c) {
       constexpr int NC = decltype(c)::value;
       smem = TileShape<NC>::kSmemBytes;
       join = reinterpret_cast<const void*>(attn_join_kernel<NC>);
+      join_threads = JoinShape<NC>::kWarps * 32;
       k = by_format(format, [](auto f) {
         return reinterpret_cast<const void*>(attn_tile_kernel<NC, decltype(f)::value>);
       });
@@ -391,7 +407,7 @@ extern "C" csa_status_t csa_cache_attn(
     if (blocks_per_sm(dev, k, kTileThreads, smem, &bps) != cudaSuccess) return CSA_ERR_CUDA;
     if (bps < 1) return CSA_ERR_UNSUPPORTED;
     if (launch_pdl(k, dim3(p.ctas), dim3(kTileThreads), smem, cs, args) != cudaSuccess) return CSA_ERR_CUDA;
-    return launch_pdl(join, dim3(p.ctas, kAttnRows / 8), dim3(256), 0, cs, args) == cudaSuccess ? CSA_OK
+    return launch_pdl(join, dim3(p.ctas, kAttnRows / 4), dim3(join_threads), 0, cs, args) == cudaSuccess ? CSA_OK
                                                                                                : CSA_ERR_CUDA;
   }
   const int64_t warps = tokens * q_heads;

@@ -26,8 +26,8 @@ struct alignas(16) AttnUnit {
 };
 struct alignas(16) AttnStart {  // a CTA's share: its first unit, the tile there, and how many tiles
   AttnUnit u;
-  int32_t unit, tile;
-  int64_t left;
+  int32_t unit, tile, left;
+  int32_t pieces;  // CTAs that share the unit which begins here and ends elsewhere (0: none)
 };
 static_assert(sizeof(AttnUnit) == 48 && sizeof(AttnStart) == 64, "read in 16-byte pieces");
 

@@ -251,12 +251,19 @@ __device__ void tile_fetch(const AttnParams& p, TileSmall& sm, uint32_t base) {
   auto entry_at = [&](int e) {
     return ((static_cast<int64_t>(page) * p.page_size + e % p.page_size) * p.kv_heads + w.u.kvh) * row_bytes;
   };
+  auto prefetch = [&](int64_t at) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p.data + at), "r"(row_bytes) : "memory");
+  };
   auto rows = [&]() {
-    if (ahead != tile || unit != w.unit) read_page(tile);
+    const bool cold = ahead != tile || unit != w.unit;
+    if (cold) read_page(tile);
     const int e = tile * kAttnEntries + gt;
     int64_t at = -1;
     if (e < w.u.seen) {
-      if (page >= 0 && page < p.num_pages) at = entry_at(e);
+      if (page >= 0 && page < p.num_pages) {
+        at = entry_at(e);
+        if (cold && SH::kPairs > 1 && group == 0) prefetch(at);
+      }
       else if (p.dev_error != nullptr) *p.dev_error = CSA_DEVERR_PAGE;
     }
     buf ^= 1;
@@ -266,9 +273,7 @@ __device__ void tile_fetch(const AttnParams& p, TileSmall& sm, uint32_t base) {
     if (tile + kStep < w.t1) {
       read_page(tile + kStep);
       if ((SH::kPairs == 1 || group == 0) && page >= 0 && page < p.num_pages)
-        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p.data + entry_at((tile + kStep) * kAttnEntries + gt)),
-                     "r"(row_bytes)
-                     : "memory");
+        prefetch(entry_at((tile + kStep) * kAttnEntries + gt));
     }
   };
 
@@ -562,14 +567,17 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
         }
       }
     } else {
-      float* o = p.part_o + piece * kAttnRows * SH::kDpad;
+      // four rows of a column in 16 bytes, a warp's 32 columns side by side
+      float4* o = reinterpret_cast<float4*>(p.part_o + piece * kAttnRows * SH::kDpad);
 #pragma unroll 1
       for (int b = 0; b < SH::kPairs; ++b) {
         float v[kSoftCols];
         tmem_load16(lanes + SH::kTmemO + b * kAttnRows + c0, v);
 #pragma unroll
-        for (int c = 0; c < kSoftCols; ++c)
-          if (row0 + c0 + c < u.rows) o[(c0 + c) * SH::kDpad + b * 128 + e0] = v[c];
+        for (int c = 0; c < kSoftCols; c += 4)
+          if (row0 + c0 + c < u.rows)
+            o[((b * 4 + quad) * (kAttnRows / 4) + (c0 + c) / 4) * 32 + lane] =
+                make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
       }
       tc_fence_before();
     }
@@ -622,72 +630,110 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
   if (warp == 0) tmem_free(tmem, SH::kTmemColumns);
 }
 
-// Joins the pieces of the units that CTAs share: block (i, y) the rows y*8 .. y*8+7 of the unit
-// whose first piece is CTA i's last one. A warp per row.
+// Joins the pieces of the units that CTAs share: block (i, y) the rows 4y .. 4y + 3 of the unit
+// whose first piece is CTA i's last one. Lane k of every warp holds piece k's weights for the
+// four rows (32 pieces at a time); a warp adds up 32 or 64 columns of them.
 template <int NC>
-__global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnParams p) {
+struct JoinShape {
+  static constexpr int kColumnBlocks = NC * 2;  // of 32 columns
+  static constexpr int kWarps = kColumnBlocks < 8 ? kColumnBlocks : 8;
+  static constexpr int kPer = kColumnBlocks / kWarps;
+};
+template <int NC>
+__global__ void __launch_bounds__(JoinShape<NC>::kWarps * 32) attn_join_kernel(const __grid_constant__ AttnParams p) {
   using SH = TileShape<NC>;
+  using JS = JoinShape<NC>;
   pdl_wait();
   if (*p.status != 0) return;
-  const int64_t all_tiles = *p.tiles;
-  const int ctas = static_cast<int>(all_tiles < p.ctas ? all_tiles : p.ctas);
   const int i = blockIdx.x;
-  if (i + 1 >= ctas) return;
-  const AttnStart& nx = p.starts[i + 1];
-  if (nx.tile == 0) return;                                             // ends with its share
-  if (p.unit_first[nx.unit] < attn_share(all_tiles, p.ctas, i)) return;  // begins before it
-  const int64_t end = p.unit_first[nx.unit + 1];
-  int last = i + 1;  // last CTA with a piece
-  while (last + 1 < ctas && attn_share(all_tiles, p.ctas, last + 1) < end) ++last;
-  const AttnUnit u = p.units[nx.unit];
-  const int r = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int row = u.block * kAttnRows + r;
-  if (row >= u.rows) return;
-  const int head = u.kvh * p.group + row % p.group;
-  const int64_t token = static_cast<int64_t>(u.token) + row / p.group;
+  const int n = p.starts[i].pieces;
+  if (n == 0) return;
+  const AttnUnit u = p.starts[i + 1].u;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r0 = blockIdx.y * 4, row0 = u.block * kAttnRows + r0;
+  if (row0 >= u.rows) return;
+  auto slot = [&](int k) { return 2 * static_cast<int64_t>(i + k) + (k == 0 ? 1 : 0); };
 
-  auto slot = [&](int k) { return 2 * static_cast<int64_t>(k) + (k == i ? 1 : 0); };
-  const float sink_e = p.sink != nullptr ? p.sink[head] : -INFINITY, sink = sink_e * kLog2e;
-  float mx = sink;
-  bool some = false;
-  for (int k = i; k <= last; ++k) {
-    const float* ml = p.part_ml + slot(k) * 2 * kAttnRows;
-    if (!(ml[kAttnRows + r] <= 0.f)) {
-      mx = fmaxf(mx, ml[r]);
-      some = true;
-    }
+  float sink_e[4], mx[4], den[4], acc[JS::kPer][4];
+  bool some[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int row = row0 + r;
+    sink_e[r] = p.sink != nullptr && row < u.rows ? p.sink[u.kvh * p.group + row % p.group] : -INFINITY;
+    mx[r] = sink_e[r] * kLog2e;
+    some[r] = false;
+    for (int b = 0; b < JS::kPer; ++b) acc[b][r] = 0.f;
   }
-  float den = mx == -INFINITY ? 0.f : fast_exp2(sink - mx);
-  float acc[SH::kDpad / 32];
+  auto read = [&](int k, float (&m)[4], float (&z)[4]) {
+    const float* ml = p.part_ml + slot(k) * 2 * kAttnRows + r0;
+    const float4 a = *reinterpret_cast<const float4*>(ml), b = *reinterpret_cast<const float4*>(ml + kAttnRows);
+    m[0] = a.x, m[1] = a.y, m[2] = a.z, m[3] = a.w;
+    z[0] = b.x, z[1] = b.y, z[2] = b.z, z[3] = b.w;
+  };
+  for (int k = lane; k < n; k += 32) {
+    float m[4], z[4];
+    read(k, m, z);
 #pragma unroll
-  for (int c = 0; c < SH::kDpad / 32; ++c) acc[c] = 0.f;
-  if (mx != -INFINITY) {
-    for (int k = i; k <= last; ++k) {
-      const float* ml = p.part_ml + slot(k) * 2 * kAttnRows;
-      const float f = fast_exp2(ml[r] - mx);
-      den += f * ml[kAttnRows + r];
-      const float4* o = reinterpret_cast<const float4*>(p.part_o + (slot(k) * kAttnRows + r) * SH::kDpad);
+    for (int r = 0; r < 4; ++r)
+      if (!(z[r] <= 0.f)) {
+        mx[r] = fmaxf(mx[r], m[r]);
+        some[r] = true;
+      }
+  }
 #pragma unroll
-      for (int c = 0; c < SH::kDpad / 128; ++c) {
-        const float4 v = o[c * 32 + lane];
-        acc[4 * c] += f * v.x;
-        acc[4 * c + 1] += f * v.y;
-        acc[4 * c + 2] += f * v.z;
-        acc[4 * c + 3] += f * v.w;
+  for (int r = 0; r < 4; ++r) {
+    mx[r] = warp_max_f32(mx[r]);
+    some[r] = __any_sync(0xFFFFFFFFu, some[r]);
+    den[r] = 0.f;
+  }
+  const float4* o = reinterpret_cast<const float4*>(p.part_o);
+  constexpr int kPiece = kAttnRows * SH::kDpad / 4;
+  for (int k0 = 0; k0 < n; k0 += 32) {
+    float f[4] = {0.f, 0.f, 0.f, 0.f};
+    if (k0 + lane < n) {
+      float m[4], z[4];
+      read(k0 + lane, m, z);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        f[r] = mx[r] == -INFINITY ? 0.f : fast_exp2(m[r] - mx[r]);
+        den[r] += f[r] * z[r];
+      }
+    }
+    const int some_k = min(32, n - k0);
+#pragma unroll 4
+    for (int k = 0; k < some_k; ++k) {
+      float g[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) g[r] = __shfl_sync(0xFFFFFFFFu, f[r], k);
+#pragma unroll
+      for (int b = 0; b < JS::kPer; ++b) {
+        const float4 v = o[slot(k0 + k) * kPiece + ((warp * JS::kPer + b) * (kAttnRows / 4) + blockIdx.y) * 32 + lane];
+        acc[b][0] = fmaf(g[0], v.x, acc[b][0]);
+        acc[b][1] = fmaf(g[1], v.y, acc[b][1]);
+        acc[b][2] = fmaf(g[2], v.z, acc[b][2]);
+        acc[b][3] = fmaf(g[3], v.w, acc[b][3]);
       }
     }
   }
-  const float inv = mx == -INFINITY ? 0.f : 1.f / den;
-  uint16_t* out = p.out + token * p.out_row + head * p.out_head;
 #pragma unroll
-  for (int c = 0; c < SH::kDpad / 128; ++c) {
-    const int col = (c * 32 + lane) * 4;
-    if (col < p.d)
-      *reinterpret_cast<uint2*>(out + col) = make_uint2(pack_bf16x2(acc[4 * c] * inv, acc[4 * c + 1] * inv),
-                                                        pack_bf16x2(acc[4 * c + 2] * inv, acc[4 * c + 3] * inv));
+  for (int r = 0; r < 4; ++r) {
+    const int row = row0 + r;
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) den[r] += __shfl_xor_sync(0xFFFFFFFFu, den[r], s);
+    if (row >= u.rows) continue;
+    const int head = u.kvh * p.group + row % p.group;
+    const int64_t token = static_cast<int64_t>(u.token) + row / p.group;
+    const float all = mx[r] == -INFINITY ? 1.f : den[r] + fast_exp2(sink_e[r] * kLog2e - mx[r]);
+    const float inv = 1.f / all;
+    uint16_t* out = p.out + token * p.out_row + head * p.out_head;
+#pragma unroll
+    for (int b = 0; b < JS::kPer; ++b) {
+      const int col = (warp * JS::kPer + b) * 32 + lane;
+      if (col < p.d) out[col] = Element<CSA_DTYPE_BF16>::from_float(acc[b][r] * inv);
+    }
+    if (p.lse != nullptr && warp == 0 && lane == 0)
+      p.lse[token * p.q_heads + head] = some[r] ? (mx[r] + log2f(all)) * kLn2 : sink_e[r];
   }
-  if (p.lse != nullptr && lane == 0)
-    p.lse[token * p.q_heads + head] = some ? (mx + log2f(den)) * kLn2 : sink_e;
 }
 
 }  // namespace csa
