@@ -82,59 +82,6 @@ struct TileSmall {
 };
 static_assert(sizeof(TileSmall) <= kSmallBytes, "small arrays");
 
-// 8 columns of an entry as they lie in the cache, and their scale byte; `at` is the entry's byte
-// offset in the pool (that of its scales is a 32nd or a 16th of it), -1 for none.
-__device__ __forceinline__ uint32_t scaled_bf16x2(float2 v, float s) { return pack_bf16x2(v.x * s, v.y * s); }
-template <int FORMAT>
-struct Piece;
-template <>
-struct Piece<CSA_CACHE_BF16> {
-  static __device__ __forceinline__ int row_bytes(int d) { return 2 * d; }
-  uint4 w;
-  __device__ __forceinline__ void load(const AttnParams& p, int64_t at, int col) {
-    w = make_uint4(0, 0, 0, 0);
-    if (at >= 0 && col < p.d) w = __ldg(reinterpret_cast<const uint4*>(p.data + at + 2 * col));
-  }
-  __device__ __forceinline__ uint4 bf16() const { return w; }
-};
-template <>
-struct Piece<CSA_CACHE_E4M3> {
-  static __device__ __forceinline__ int row_bytes(int d) { return d; }
-  uint2 w;
-  uint32_t k;
-  __device__ __forceinline__ void load(const AttnParams& p, int64_t at, int col) {
-    w = make_uint2(0, 0);
-    k = 127;
-    if (at >= 0 && col < p.d) {
-      w = __ldg(reinterpret_cast<const uint2*>(p.data + at + col));
-      k = __ldg(p.scales + (at >> 5) + (col >> 5));
-    }
-  }
-  __device__ __forceinline__ uint4 bf16() const {
-    const float s = scale_value(k);
-    return make_uint4(scaled_bf16x2(e4m3x2_to_float2(w.x & 0xFFFF), s), scaled_bf16x2(e4m3x2_to_float2(w.x >> 16), s),
-                      scaled_bf16x2(e4m3x2_to_float2(w.y & 0xFFFF), s), scaled_bf16x2(e4m3x2_to_float2(w.y >> 16), s));
-  }
-};
-template <>
-struct Piece<CSA_CACHE_E2M1> {
-  static __device__ __forceinline__ int row_bytes(int d) { return d / 2; }
-  uint32_t w, k;
-  __device__ __forceinline__ void load(const AttnParams& p, int64_t at, int col) {
-    w = 0;
-    k = 127;
-    if (at >= 0 && col < p.d) {
-      w = __ldg(reinterpret_cast<const uint32_t*>(p.data + at + (col >> 1)));
-      k = __ldg(p.scales + (at >> 4) + (col >> 5));
-    }
-  }
-  __device__ __forceinline__ uint4 bf16() const {
-    const float s = scale_value(k);
-    return make_uint4(scaled_bf16x2(e2m1x2_to_float2(w), s), scaled_bf16x2(e2m1x2_to_float2(w >> 8), s),
-                      scaled_bf16x2(e2m1x2_to_float2(w >> 16), s), scaled_bf16x2(e2m1x2_to_float2(w >> 24), s));
-  }
-};
-
 __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                : "memory");
@@ -144,6 +91,114 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
   return v;
 }
+
+// What a fetching thread takes of a pair (128 entries x 128 columns), from loading to the
+// swizzled tile. `at` is an entry's byte offset in the pool, -1 for none. A bf16 thread takes 8
+// columns of 16 entries (neighbouring lanes neighbouring columns); with codes it takes 32
+// columns, a scale's, of 4 entries, so that finding a place and its scale is paid once per 32
+// values: a fetch of 8-bit entries in pieces of 8 took 1100 instructions a pair and thread
+// instead of about 400, and was bound by them.
+__device__ __forceinline__ uint32_t widen2(uint32_t half2, uint64_t scale) {
+  const float2 f = __half22float2(*reinterpret_cast<__half2*>(&half2));
+  return f2_to_bf2(f2_mul(f2_pack(f.x, f.y), scale));
+}
+template <int FORMAT>
+struct Take;
+template <>
+struct Take<CSA_CACHE_BF16> {
+  static constexpr int kRows = 16, kRowStep = 8;  // entries row, row + 8, ...
+  static __device__ __forceinline__ int row_bytes(int d) { return 2 * d; }
+  static __device__ __forceinline__ int first_row(int t) { return t >> 4; }
+  static __device__ __forceinline__ int column(int t) { return (t & 15) * 8; }
+  uint4 w;
+  __device__ __forceinline__ void load(const AttnParams& p, int64_t at, int col) {
+    w = make_uint4(0, 0, 0, 0);
+    if (at >= 0 && col < p.d) w = __ldg(reinterpret_cast<const uint4*>(p.data + at + 2 * col));
+  }
+  __device__ __forceinline__ void store(uint32_t pair, int row, int t) const {
+    const int piece = t & 15;
+    sts128(pair + (piece >> 3) * kChunkBytes + row * 128 + (((piece & 7) ^ (row & 7)) << 4), w);
+  }
+};
+// Four pieces of 8 columns from a thread's 32. Lanes of the pair's second half (other chunk, same
+// banks) take theirs in another order, so that eight neighbouring lanes use all banks.
+template <typename F>
+__device__ __forceinline__ void store_pieces(uint32_t pair, int row, int t, F widened) {
+  const int g = t & 3;
+  const uint32_t to = pair + (g >> 1) * kChunkBytes + row * 128;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int piece = (g & 1) * 4 + (i ^ (g & 2));
+    sts128(to + ((piece ^ (row & 7)) << 4), widened(i));
+  }
+}
+template <>
+struct Take<CSA_CACHE_E4M3> {
+  static constexpr int kRows = 4, kRowStep = 32;
+  static __device__ __forceinline__ int row_bytes(int d) { return d; }
+  static __device__ __forceinline__ int first_row(int t) { return t >> 2; }
+  static __device__ __forceinline__ int column(int t) { return (t & 3) * 32; }
+  uint4 a, b;
+  uint32_t k;
+  __device__ __forceinline__ void load(const AttnParams& p, int64_t at, int col) {
+    a = b = make_uint4(0, 0, 0, 0);
+    k = 127;
+    if (at >= 0 && col < p.d) {
+      const uint4* w = reinterpret_cast<const uint4*>(p.data + at + col);
+      a = __ldg(w);
+      b = __ldg(w + 1);
+      k = __ldg(p.scales + (at >> 5) + (col >> 5));
+    }
+  }
+  static __device__ __forceinline__ uint32_t two(uint32_t c, uint64_t s) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(c)));
+    return widen2(h, s);
+  }
+  __device__ __forceinline__ void store(uint32_t pair, int row, int t) const {
+    const float f = scale_value(k);
+    const uint64_t s = f2_pack(f, f);
+    const bool swap = (t & 2) != 0;
+    const uint4 u = swap ? b : a, v = swap ? a : b;
+    store_pieces(pair, row, t, [&](int i) {
+      const uint32_t x = i == 0 ? u.x : i == 1 ? u.z : i == 2 ? v.x : v.z;
+      const uint32_t y = i == 0 ? u.y : i == 1 ? u.w : i == 2 ? v.y : v.w;
+      return make_uint4(two(x, s), two(x >> 16, s), two(y, s), two(y >> 16, s));
+    });
+  }
+};
+template <>
+struct Take<CSA_CACHE_E2M1> {
+  static constexpr int kRows = 4, kRowStep = 32;
+  static __device__ __forceinline__ int row_bytes(int d) { return d / 2; }
+  static __device__ __forceinline__ int first_row(int t) { return t >> 2; }
+  static __device__ __forceinline__ int column(int t) { return (t & 3) * 32; }
+  uint4 a;
+  uint32_t k;
+  __device__ __forceinline__ void load(const AttnParams& p, int64_t at, int col) {
+    a = make_uint4(0, 0, 0, 0);
+    k = 127;
+    if (at >= 0 && col < p.d) {
+      a = __ldg(reinterpret_cast<const uint4*>(p.data + at + (col >> 1)));
+      k = __ldg(p.scales + (at >> 4) + (col >> 5));
+    }
+  }
+  static __device__ __forceinline__ uint32_t two(uint32_t c, uint64_t s) {
+    uint32_t h;
+    asm("{\n\t.reg .b8 b;\n\tcvt.u8.u32 b, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}" : "=r"(h) : "r"(c & 0xFFu));
+    return widen2(h, s);
+  }
+  __device__ __forceinline__ void store(uint32_t pair, int row, int t) const {
+    const float f = scale_value(k);
+    const uint64_t s = f2_pack(f, f);
+    const bool swap = (t & 2) != 0;
+    const uint4 u = swap ? make_uint4(a.z, a.w, a.x, a.y) : a;
+    store_pieces(pair, row, t, [&](int i) {
+      const uint32_t x = i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w;
+      return make_uint4(two(x, s), two(x >> 8, s), two(x >> 16, s), two(x >> 24, s));
+    });
+  }
+};
 
 // Waits are bounded: one that runs out sets the CTA's stop word and reports, after which every
 // wait returns at once and every role runs through the rest of its (finite) loops, so that
@@ -217,13 +272,11 @@ struct SegmentWalk {
 template <int NC, int FORMAT>
 __device__ void tile_fetch(const AttnParams& p, TileSmall& sm, uint32_t base) {
   using SH = TileShape<NC>;
-  using P = Piece<FORMAT>;
+  using P = Take<FORMAT>;
   constexpr int kGroup = kTileLoaders / 2;
   constexpr int kStep = SH::kPairs == 1 ? 2 : 1;  // tiles from one of a group's to its next
   const int lt = threadIdx.x - kTileFirstLoader * 32;
   const int group = lt / kGroup, gt = lt % kGroup;
-  const int piece = gt & 15, rg = gt >> 4;  // 8 columns of the pair's 128; rows rg, rg + 8, ...
-  const uint32_t dst = (piece >> 3) * kChunkBytes + rg * 128 + (((piece & 7) ^ rg) << 4);
   const int row_bytes = P::row_bytes(p.d);
 
   SegmentWalk w(p);
@@ -251,42 +304,32 @@ __device__ void tile_fetch(const AttnParams& p, TileSmall& sm, uint32_t base) {
   auto entry_at = [&](int e) {
     return ((static_cast<int64_t>(page) * p.page_size + e % p.page_size) * p.kv_heads + w.u.kvh) * row_bytes;
   };
-  auto prefetch = [&](int64_t at) {
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p.data + at), "r"(row_bytes) : "memory");
-  };
   auto rows = [&]() {
-    const bool cold = ahead != tile || unit != w.unit;
-    if (cold) read_page(tile);
+    if (ahead != tile || unit != w.unit) read_page(tile);
     const int e = tile * kAttnEntries + gt;
     int64_t at = -1;
     if (e < w.u.seen) {
-      if (page >= 0 && page < p.num_pages) {
-        at = entry_at(e);
-        if (cold && SH::kPairs > 1 && group == 0) prefetch(at);
-      }
+      if (page >= 0 && page < p.num_pages) at = entry_at(e);
       else if (p.dev_error != nullptr) *p.dev_error = CSA_DEVERR_PAGE;
     }
     buf ^= 1;
     sm.row[group][buf][gt] = at;
     named_barrier(6 + group, kGroup);
     fresh = false;
-    if (tile + kStep < w.t1) {
-      read_page(tile + kStep);
-      if ((SH::kPairs == 1 || group == 0) && page >= 0 && page < p.num_pages)
-        prefetch(entry_at((tile + kStep) * kAttnEntries + gt));
-    }
+    if (tile + kStep < w.t1) read_page(tile + kStep);
   };
 
   if (group == 1 && w.valid()) next_pair();
   while (w.valid()) {
     if (fresh) rows();
-    P v[16];
+    P v[P::kRows];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i].load(p, sm.row[group][buf][i * 8 + rg], pair * 128 + piece * 8);
+    for (int i = 0; i < P::kRows; ++i)
+      v[i].load(p, sm.row[group][buf][P::first_row(gt) + i * P::kRowStep], pair * 128 + P::column(gt));
     tile_wait(sm, p, &sm.empty[ring.slot], ring.lap ^ 1u);
-    const uint32_t to = base + ring.slot * kPairBytes + dst;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) sts128(to + i * 8 * 128, v[i].bf16());
+    for (int i = 0; i < P::kRows; ++i)
+      v[i].store(base + ring.slot * kPairBytes, P::first_row(gt) + i * P::kRowStep, gt);
     fence_proxy_async_smem();
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(&sm.full[ring.slot]);
