@@ -53,7 +53,7 @@ __device__ __forceinline__ int64_t plan_scan(int64_t v, int64_t* warps, int64_t&
 }
 
 // One block: checks the call's lengths, publishes the verdict for the kernels behind it, and
-// (units wanted) lists the units, their first tiles and where each CTA's share begins.
+// (units wanted) lists the units, their first tiles and where each worker's share begins.
 __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnParams p) {
   extern __shared__ int s_first[];  // [S + 1] first row block of each sequence
   __shared__ int64_t s_warps[32];
@@ -74,11 +74,11 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnParams p) {
   const int per = (p.S + kPlanThreads - 1) / kPlanThreads;
   const int lo = min(p.S, static_cast<int>(threadIdx.x) * per), hi = min(p.S, lo + per);
   int64_t mine = 0, blocks = 0;
-  for (int s = lo; s < hi; ++s) mine += (sequence_rows(p, s) + kAttnRows - 1) / kAttnRows;
+  for (int s = lo; s < hi; ++s) mine += (sequence_rows(p, s) + p.unit_rows - 1) / p.unit_rows;
   int64_t at = plan_scan(mine, s_warps, blocks);
   for (int s = lo; s < hi; ++s) {
     s_first[s] = static_cast<int>(at);
-    at += (sequence_rows(p, s) + kAttnRows - 1) / kAttnRows;
+    at += (sequence_rows(p, s) + p.unit_rows - 1) / p.unit_rows;
   }
   if (threadIdx.x == 0) s_first[p.S] = static_cast<int>(blocks);
   __syncthreads();
@@ -110,10 +110,10 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnParams p) {
     *p.tiles = all;
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < p.ctas; i += kPlanThreads) {
-    const int64_t t = attn_share(all, p.ctas, i);
+  for (int i = threadIdx.x; i < p.workers; i += kPlanThreads) {
+    const int64_t t = attn_share(all, p.workers, i);
     AttnStart start{};
-    const int64_t next = attn_share(all, p.ctas, i + 1);
+    const int64_t next = attn_share(all, p.workers, i + 1);
     start.left = static_cast<int32_t>(next - t);
     if (start.left == 0) {
       p.starts[i] = start;
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnParams p) {
     const int64_t end = p.unit_first[l + 1];
     if (p.unit_first[l] >= t && end > next) {
       int last = i + 1;
-      while (last + 1 < p.ctas && attn_share(all, p.ctas, last + 1) < end) ++last;
+      while (last + 1 < p.workers && attn_share(all, p.workers, last + 1) < end) ++last;
       start.pieces = last - i + 1;
     }
     p.starts[i] = start;
@@ -266,8 +266,8 @@ auto by_chunks(int chunks, F f) {
                        : f(std::integral_constant<int, 8>{});
 }
 
-// The workspace: the plan, then the pieces. base may be null (sizes only).
-size_t lay_out(AttnParams& p, unsigned char* base) {
+// The workspace: the plan, the pieces, and (chunks) the packed entries. base may be null (sizes only).
+size_t lay_out(AttnParams& p, int sms, bool chunks, unsigned char* base) {
   size_t at = 0;
   auto take = [&](size_t bytes) {
     unsigned char* r = base == nullptr ? nullptr : base + at;
@@ -277,29 +277,47 @@ size_t lay_out(AttnParams& p, unsigned char* base) {
   unsigned char* head = take(kStatusBytes);
   p.status = reinterpret_cast<int32_t*>(head);
   p.tiles = base == nullptr ? nullptr : reinterpret_cast<int64_t*>(head + 8);
-  p.starts = reinterpret_cast<AttnStart*>(take(sizeof(AttnStart) * p.ctas));
+  p.starts = reinterpret_cast<AttnStart*>(take(sizeof(AttnStart) * sms));
   p.units = reinterpret_cast<AttnUnit*>(take(sizeof(AttnUnit) * p.max_units));
   p.unit_first = reinterpret_cast<int64_t*>(take(sizeof(int64_t) * (p.max_units + 1)));
-  const size_t pieces = 2 * static_cast<size_t>(p.ctas);
+  const size_t pieces = 2 * static_cast<size_t>(sms), dpad = tile_chunks(p.d) * 64;
   p.part_ml = reinterpret_cast<float*>(take(pieces * 2 * kAttnRows * sizeof(float)));
-  p.part_o = reinterpret_cast<float*>(take(pieces * kAttnRows * (tile_chunks(p.d) * 64) * sizeof(float)));
+  p.part_o = reinterpret_cast<float*>(take(pieces * kAttnRows * dpad * sizeof(float)));
+  if (chunks)
+    p.packed = reinterpret_cast<uint16_t*>(take(static_cast<size_t>(p.S) * p.kv_heads * p.packed_rows * dpad * 2));
   return at;
 }
 
 // Sizes that the workspace depends on; d beyond the tile kernel's needs the status alone.
-cudaError_t plan_sizes(AttnParams& p, int32_t S, int64_t tokens, int32_t q_heads, int32_t kv_heads, int32_t d) {
-  int dev = 0, sms = 0;
+cudaError_t plan_sizes(AttnParams& p, int* sms, int32_t S, int64_t tokens, int32_t q_heads, int32_t kv_heads,
+                       int32_t d, int64_t max_entries) {
+  int dev = 0;
   cudaError_t e = note(cudaGetDevice(&dev));
-  if (e != cudaSuccess || (e = device_sms(dev, &sms)) != cudaSuccess) return e;
+  if (e != cudaSuccess || (e = device_sms(dev, sms)) != cudaSuccess) return e;
   p.S = S;
   p.tokens = tokens;
   p.q_heads = q_heads;
   p.kv_heads = kv_heads;
   p.group = q_heads / kv_heads;
   p.d = d;
-  p.ctas = sms;
+  p.workers = *sms;
+  p.unit_rows = kAttnRows;
+  p.max_entries = max_entries;
   p.max_units = ((tokens * p.group + kAttnRows - 1) / kAttnRows + S) * kv_heads;
+  p.packed_rows = static_cast<int>((max_entries + kAttnEntries - 1) / kAttnEntries * kAttnEntries);
   return cudaSuccess;
+}
+
+// Whether a call's chunks are long enough for pairs of CTAs over packed entries: 256 rows (two
+// units) a sequence on average, so that packing an entry (read and written once) is small
+// beside the units that read it, and packed entries within kMaxPacked bytes. Measured: 606
+// GFLOP of three chunks of up to 1024 tokens x 64 heads of 512
+constexpr int64_t kChunkRows = 256;
+constexpr int64_t kMaxPacked = int64_t{4} << 30;
+bool chunked(const AttnParams& p) {
+  if (p.d > kTileMaxDim || p.S < 1 || p.tokens * p.group < kChunkRows * p.S) return false;
+  const int64_t rows = static_cast<int64_t>(p.S) * p.kv_heads * p.packed_rows;
+  return rows > 0 && rows < INT_MAX && rows * tile_chunks(p.d) * 128 <= kMaxPacked && p.S < 65536 && p.kv_heads < 65536;
 }
 
 }  // namespace
@@ -312,8 +330,9 @@ extern "C" size_t csa_cache_attn_workspace_bytes(int32_t S, int64_t tokens, int3
   if (check_attn_sizes(S, tokens, q_heads, kv_heads, d, max_entries) != CSA_OK) return 0;
   if (d > kTileMaxDim) return kStatusBytes;
   AttnParams p{};
-  if (plan_sizes(p, S, tokens, q_heads, kv_heads, d) != cudaSuccess) return 0;
-  return lay_out(p, nullptr);
+  int sms = 0;
+  if (plan_sizes(p, &sms, S, tokens, q_heads, kv_heads, d, max_entries) != cudaSuccess) return 0;
+  return lay_out(p, sms, chunked(p), nullptr);
 }
 
 extern "C" csa_status_t csa_cache_attn(
@@ -348,18 +367,24 @@ extern "C" csa_status_t csa_cache_attn(
   if (workspace == nullptr || workspace_bytes < kStatusBytes) return CSA_ERR_WORKSPACE;
 
   AttnParams p{};
-  if (plan_sizes(p, S, tokens, q_heads, kv_heads, d) != cudaSuccess) return CSA_ERR_CUDA;
+  int sms = 0;
+  if (plan_sizes(p, &sms, S, tokens, q_heads, kv_heads, d, max_entries) != cudaSuccess) return CSA_ERR_CUDA;
   // a call's pointers and strides decide between the kernels, its workspace serves either
   const bool tile = d <= kTileMaxDim && d % 8 == 0 && q_row_stride % 8 == 0 && q_head_stride % 8 == 0 &&
                     out_row_stride % 8 == 0 && out_head_stride % 8 == 0 && is_aligned(q, 16) &&
                     is_aligned(out, 16) && is_aligned(data, 16);
   if (d <= kTileMaxDim) {
-    if (workspace_bytes < lay_out(p, nullptr)) return CSA_ERR_WORKSPACE;
-    lay_out(p, static_cast<unsigned char*>(workspace));
+    if (workspace_bytes < lay_out(p, sms, chunked(p), nullptr)) return CSA_ERR_WORKSPACE;
+    lay_out(p, sms, chunked(p), static_cast<unsigned char*>(workspace));
   } else {
     p.status = static_cast<int32_t*>(workspace);
   }
   if (!tile) p.units = nullptr;
+  const bool chunks = tile && chunked(p);
+  if (chunks) {
+    p.workers = sms / 2;
+    p.unit_rows = 2 * kAttnRows;
+  }
   p.q = static_cast<const uint16_t*>(q);
   p.cu = cu_seqlens;
   p.data = static_cast<const uint8_t*>(data);
@@ -376,7 +401,6 @@ extern "C" csa_status_t csa_cache_attn(
   p.out_row = out_row_stride;
   p.out_head = out_head_stride;
   p.num_pages = num_pages;
-  p.max_entries = max_entries;
   p.max_pages = max_pages;
   p.page_size = page_size;
   p.ratio = ratio;
@@ -391,24 +415,66 @@ extern "C" csa_status_t csa_cache_attn(
   if (launch_pdl(plan, dim3(1), dim3(kPlanThreads), plan_smem, cs, args) != cudaSuccess) return CSA_ERR_CUDA;
   if (tile) {
     const int nc = tile_chunks(d);
+    // Tensor copies straight from bf16 pages where a power of two of at least 8 entries
+    // divides the page: smaller boxes copy slower than threads (8 entries 3.2 TB/s from L2,
+    // 16 4.2, 64 and up 5.7).
+    p.box_rows = 1;
+    while (p.box_rows < kAttnEntries && page_size % (2 * p.box_rows) == 0) p.box_rows *= 2;
+    CUtensorMap map{};
+    int source = format;
+    if (chunks) {
+      source = kFromPacked;
+      const uint64_t dims[2] = {static_cast<uint64_t>(nc) * 64,
+                                static_cast<uint64_t>(S) * kv_heads * static_cast<uint64_t>(p.packed_rows)};
+      const uint64_t strides[1] = {static_cast<uint64_t>(nc) * 128};
+      const uint32_t box[2] = {64, kAttnEntries};
+      if (!encode_bf16_boxes(&map, p.packed, 2, dims, strides, box)) return CSA_ERR_CUDA;
+    } else if (format == CSA_CACHE_BF16 && p.box_rows >= 8 && num_pages > 0 && num_pages <= INT_MAX / page_size) {
+      const uint64_t dims[3] = {static_cast<uint64_t>(d), static_cast<uint64_t>(kv_heads),
+                                static_cast<uint64_t>(num_pages) * page_size};
+      const uint64_t strides[2] = {static_cast<uint64_t>(d) * 2, static_cast<uint64_t>(kv_heads) * d * 2};
+      const uint32_t box[3] = {64, 1, static_cast<uint32_t>(p.box_rows)};
+      if (!encode_bf16_boxes(&map, data, 3, dims, strides, box)) return CSA_ERR_CUDA;
+      source = kFromBoxes;
+    }
     size_t smem = 0;
-    int join_threads = 0;
-    const void *k = nullptr, *join = nullptr;
+    int threads = 0, join_threads = 0;
+    const void *k = nullptr, *join = nullptr, *pack = nullptr;
     by_chunks(nc, [&](auto c) {
       constexpr int NC = decltype(c)::value;
       smem = TileShape<NC>::kSmemBytes;
-      join = reinterpret_cast<const void*>(attn_join_kernel<NC>);
       join_threads = JoinShape<NC>::kWarps * 32;
-      k = by_format(format, [](auto f) {
-        return reinterpret_cast<const void*>(attn_tile_kernel<NC, decltype(f)::value>);
-      });
+      auto use = [&](auto src) {
+        constexpr int SRC = decltype(src)::value;
+        k = reinterpret_cast<const void*>(attn_tile_kernel<NC, SRC>);
+        threads = TileCta<SRC>::kThreads;
+        join = reinterpret_cast<const void*>(attn_join_kernel<NC, TileCta<SRC>::kCluster>);
+        return 0;
+      };
+      if (source == kFromPacked) {
+        use(std::integral_constant<int, kFromPacked>{});
+        pack = by_format(format, [](auto f) {
+          return reinterpret_cast<const void*>(attn_pack_kernel<NC, decltype(f)::value>);
+        });
+      } else if (source == kFromBoxes) {
+        use(std::integral_constant<int, kFromBoxes>{});
+      } else {
+        by_format(format, use);
+      }
       return 0;
     });
-    if (blocks_per_sm(dev, k, kTileThreads, smem, &bps) != cudaSuccess) return CSA_ERR_CUDA;
+    if (blocks_per_sm(dev, k, threads, smem, &bps) != cudaSuccess) return CSA_ERR_CUDA;
     if (bps < 1) return CSA_ERR_UNSUPPORTED;
-    if (launch_pdl(k, dim3(p.ctas), dim3(kTileThreads), smem, cs, args) != cudaSuccess) return CSA_ERR_CUDA;
-    return launch_pdl(join, dim3(p.ctas, kAttnRows / 4), dim3(join_threads), 0, cs, args) == cudaSuccess ? CSA_OK
-                                                                                               : CSA_ERR_CUDA;
+    const int cluster = chunks ? 2 : 1;
+    if (chunks && launch_pdl(pack, dim3(p.packed_rows / kPackRows, S, kv_heads), dim3(kPackThreads), 0, cs, args) !=
+                      cudaSuccess)
+      return CSA_ERR_CUDA;
+    void* targs[] = {&p, &map};
+    if (launch_pdl(k, dim3(p.workers * cluster), dim3(threads), smem, cs, targs, cluster) != cudaSuccess)
+      return CSA_ERR_CUDA;
+    return launch_pdl(join, dim3(p.workers, cluster * kAttnRows / 4), dim3(join_threads), 0, cs, args) == cudaSuccess
+               ? CSA_OK
+               : CSA_ERR_CUDA;
   }
   const int64_t warps = tokens * q_heads;
   const int64_t blocks = (warps + kScalarThreads / 32 - 1) / (kScalarThreads / 32);

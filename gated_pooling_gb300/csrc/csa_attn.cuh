@@ -12,9 +12,10 @@ namespace csa {
 constexpr int kAttnRows = 64;      // (token, head) rows of a unit
 constexpr int kAttnEntries = 128;  // entries of a tile
 
-// A unit is up to 64 consecutive rows (token, head of the group) of one sequence and cache head;
-// its work is a run of tiles of 128 entries, at least one. The tiles of all units in order are
-// split evenly over the CTAs (attn_share).
+// A unit is up to unit_rows (64, or 128 for a pair of CTAs) consecutive rows (token, head of the
+// group) of one sequence and cache head; its work is a run of tiles of 128 entries, at least
+// one. The tiles of all units in order are split evenly over the workers, CTAs or pairs of
+// them (attn_share).
 struct alignas(16) AttnUnit {
   int32_t s, kvh, block, tiles;
   int32_t token, rows;  // the sequence's first token, and its rows
@@ -24,10 +25,10 @@ struct alignas(16) AttnUnit {
   int32_t seen;         // entries that some row sees
   int32_t pad[2];
 };
-struct alignas(16) AttnStart {  // a CTA's share: its first unit, the tile there, and how many tiles
+struct alignas(16) AttnStart {  // a worker's share: its first unit, the tile there, and how many tiles
   AttnUnit u;
   int32_t unit, tile, left;
-  int32_t pieces;  // CTAs that share the unit which begins here and ends elsewhere (0: none)
+  int32_t pieces;  // workers that share the unit which begins here and ends elsewhere (0: none)
 };
 static_assert(sizeof(AttnUnit) == 48 && sizeof(AttnStart) == 64, "read in 16-byte pieces");
 
@@ -46,14 +47,18 @@ struct AttnParams {
   // workspace
   int32_t* status;      // 0, or why the call's lengths were refused
   int64_t* tiles;       // all units' tiles
-  AttnStart* starts;    // [ctas]
+  AttnStart* starts;    // [workers]
   AttnUnit* units;      // [max_units]
   int64_t* unit_first;  // [max_units + 1]: first tile of each unit
-  float* part_o;        // [2 ctas][64][dpad]: sums of the pieces of units that CTAs share
-  float* part_ml;       // [2 ctas][2][64]: their maxima (in log2) and weight sums
+  float* part_o;        // [2 workers][CTAs of one][64 x dpad]: sums of the pieces of shared units
+  float* part_ml;       // likewise [2][64]: their maxima (in log2) and weight sums
+  uint16_t* packed;     // chunks: the sequences' entries as bf16 rows [S][kv_heads][packed_rows][dpad]
   int64_t q_row, q_head, out_row, out_head;
   int64_t tokens, num_pages, max_entries, max_units;
-  int S, q_heads, kv_heads, group, d, max_pages, page_size, ratio, ctas;
+  int S, q_heads, kv_heads, group, d, max_pages, page_size, ratio;
+  int workers, unit_rows;
+  int packed_rows;  // rows of a sequence's cache head in `packed`, a multiple of 128
+  int box_rows;     // entries of a tensor copy's box from the pages
   float scale;  // softmax_scale
 };
 
@@ -77,16 +82,16 @@ __device__ __forceinline__ AttnUnit make_unit(const AttnParams& p, int s, int kv
   u.rows = sequence_rows(p, s);
   u.first = p.first != nullptr ? __ldg(p.first + s) : 0;
   u.n = __ldg(p.entries + s);
-  const int last = min(block * kAttnRows + kAttnRows, u.rows) - 1;
-  u.seen_all = visible(static_cast<int64_t>(u.first) + block * kAttnRows / p.group, p.ratio, u.n);
+  const int last = min(block * p.unit_rows + p.unit_rows, u.rows) - 1;
+  u.seen_all = visible(static_cast<int64_t>(u.first) + block * p.unit_rows / p.group, p.ratio, u.n);
   u.seen = visible(static_cast<int64_t>(u.first) + last / p.group, p.ratio, u.n);
   u.tiles = u.seen <= kAttnEntries ? 1 : (u.seen - 1) / kAttnEntries + 1;
   return u;
 }
 
-// First tile of CTA i's share of all tiles; at most one CTA per tile.
-__device__ __forceinline__ int64_t attn_share(int64_t tiles, int ctas, int i) {
-  const int64_t n = tiles < ctas ? tiles : ctas;
+// First tile of worker i's share of all tiles; at most one worker per tile.
+__device__ __forceinline__ int64_t attn_share(int64_t tiles, int workers, int i) {
+  const int64_t n = tiles < workers ? tiles : workers;
   return i >= n ? tiles : tiles * i / n;
 }
 

@@ -12,8 +12,8 @@
 // memory. With few rows per sequence (decoding) no part of the 128 rows is idle.
 //
 // Warps: 0-15 softmax (a warp reads the 32 tensor-memory lanes of its quadrant, each group of
-// four warps 16 of the 64 rows), 16 issues the products (17-19 only complete its register
-// group), 20-27 fetch: they follow the page table, widen 8- and 4-bit codes to bf16 (exact, but
+// four warps 16 of the 64 rows), 16 issues the products, 17 the tensor copies where the tile comes
+// by those (18 and 19 only complete the register group); otherwise 20-27 fetch: they follow the page table, widen 8- and 4-bit codes to bf16 (exact, but
 // for bf16's own subnormals) and store the swizzled tile in pairs of 64-column chunks (32 KB).
 // Two groups of four warps take alternate pairs: a group holds its next pair in registers
 // while the ring is full, and one group's loads are under way while the other stores. Rows of
@@ -40,7 +40,16 @@ constexpr int kSoftThreads = kTileSoftWarps * 32;
 constexpr int kSoftCols = 16;  // rows of a softmax thread's group
 constexpr int kTileLoaders = kTileLoadWarps * 32;
 constexpr int kTileFirstLoader = kTileSoftWarps + 4;
-constexpr int kTileThreads = (kTileFirstLoader + kTileLoadWarps) * 32;
+// Where a tile comes from: threads that read the pages (in each of the cache's formats), tensor
+// copies of the pages' bf16 boxes, or tensor copies of a sequence's packed entries that go to
+// both CTAs of a pair.
+enum TileSource { kFromBf16 = CSA_CACHE_BF16, kFromE4m3 = CSA_CACHE_E4M3, kFromE2m1 = CSA_CACHE_E2M1, kFromBoxes, kFromPacked };
+template <int SRC>
+struct TileCta {
+  static constexpr bool kByThreads = SRC < kFromBoxes;
+  static constexpr int kCluster = SRC == kFromPacked ? 2 : 1;
+  static constexpr int kThreads = (kTileFirstLoader + (kByThreads ? kTileLoadWarps : 0)) * 32;
+};
 // Registers a thread: 896 threads launch with 72, and 16 x 64 + 4 x 40 + 8 x 104 = 28 x 72.
 constexpr int kSoftRegs = 64, kIssueRegs = 40, kLoadRegs = 104;
 constexpr int kChunkBytes = kAttnEntries * 128;  // 128 entries x 64 columns
@@ -241,13 +250,13 @@ __device__ __forceinline__ AttnUnit read_unit(const AttnUnit* at) {
   return {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w, v[2].x, v[2].y, {0, 0}};
 }
 
-// The runs of tiles of one unit in a CTA's share.
+// The runs of tiles of one unit in a worker's share.
 struct SegmentWalk {
   const AttnParams& p;
   int unit, t0, t1, left;  // (a CTA's share stays below 2^31 tiles: checked on the host)
   AttnUnit u;
-  __device__ __forceinline__ SegmentWalk(const AttnParams& pp) : p(pp) {
-    const AttnStart* at = p.starts + blockIdx.x;
+  __device__ __forceinline__ SegmentWalk(const AttnParams& pp, int worker) : p(pp) {
+    const AttnStart* at = p.starts + worker;
     u = read_unit(&at->u);
     const int4 v = __ldg(reinterpret_cast<const int4*>(at) + 3);
     unit = v.x;
@@ -279,7 +288,7 @@ __device__ void tile_fetch(const AttnParams& p, TileSmall& sm, uint32_t base) {
   const int group = lt / kGroup, gt = lt % kGroup;
   const int row_bytes = P::row_bytes(p.d);
 
-  SegmentWalk w(p);
+  SegmentWalk w(p, blockIdx.x);
   int tile = w.t0, pair = 0, buf = 0;
   RingAt<SH::kRing> ring;
   bool fresh = true;  // the tile's rows are still to be looked up
@@ -338,8 +347,70 @@ __device__ void tile_fetch(const AttnParams& p, TileSmall& sm, uint32_t base) {
   }
 }
 
+// ------------------------------------------------------------- the warp that issues tensor copies
+// From the pages: lane i copies box i mod n of chunk i / n of each pair, n = 128 / box_rows of them.
+// A box behind the last entry that the unit sees is not copied, and rows behind it in a copied
+// box are whatever the pool holds there: masked in the scores, and made finite where they are
+// not before the second product. From packed entries: one box of a pair by each CTA of the
+// pair, to both.
+template <int NC, int SRC>
+__device__ void tile_copy(const AttnParams& p, TileSmall& sm, uint32_t base, const CUtensorMap* map) {
+  using SH = TileShape<NC>;
+  const int lane = threadIdx.x & 31;
+  RingAt<SH::kRing> ring;
+  uint32_t issued = 0;
+  if constexpr (SRC == kFromPacked) {
+    const int rank = static_cast<int>(cluster_rank());
+    for (SegmentWalk w(p, blockIdx.x / 2); w.valid(); w.next()) {
+      const int row = (w.u.s * p.kv_heads + w.u.kvh) * p.packed_rows;
+      for (int tile = w.t0; tile < w.t1; ++tile)
+        for (int c = 0; c < SH::kPairs; ++c, ring.next(), ++issued) {
+          tile_wait(sm, p, &sm.empty[ring.slot], ring.lap ^ 1u);
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&sm.full[ring.slot], kPairBytes);
+            box_load2_all(base + ring.slot * kPairBytes + rank * kChunkBytes, map, c * 128 + rank * 64,
+                          row + tile * kAttnEntries, &sm.full[ring.slot], 3);
+          }
+          __syncwarp();
+        }
+    }
+  } else {
+    const int n = kAttnEntries / p.box_rows, chunk = lane / n, box = lane % n;
+    for (SegmentWalk w(p, blockIdx.x); w.valid(); w.next()) {
+      for (int tile = w.t0; tile < w.t1; ++tile) {
+        const int e = tile * kAttnEntries + box * p.box_rows;
+        bool on = chunk < 2 && e < w.u.seen;
+        int slot = 0;
+        if (on) {
+          const int page = __ldg(p.table + static_cast<int64_t>(w.u.s) * p.max_pages + e / p.page_size);
+          on = page >= 0 && page < p.num_pages;
+          if (on) slot = page * p.page_size + e % p.page_size;
+          else if (p.dev_error != nullptr) *p.dev_error = CSA_DEVERR_PAGE;
+        }
+        const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, on)) * p.box_rows * 128;
+        for (int c = 0; c < SH::kPairs; ++c, ring.next(), ++issued) {
+          tile_wait(sm, p, &sm.empty[ring.slot], ring.lap ^ 1u);
+          if (lane == 0) mbar_arrive_expect_tx(&sm.full[ring.slot], bytes);
+          __syncwarp();
+          if (on)
+            box_load3(base + ring.slot * kPairBytes + chunk * kChunkBytes + box * p.box_rows * 128, map,
+                      c * 128 + chunk * 64, w.u.kvh, slot, &sm.full[ring.slot]);
+        }
+      }
+    }
+  }
+  // the other CTA's last arrivals have come in before this one's barriers go
+  if constexpr (SRC == kFromPacked)
+    for (uint32_t k = issued > SH::kRing ? issued - SH::kRing : 0; k < issued; ++k)
+      tile_wait(sm, p, &sm.empty[k % SH::kRing], (k / SH::kRing) & 1u);
+  // after a stop, the copies that nobody waited for: the last lap of the ring
+  if (*reinterpret_cast<volatile int*>(&sm.stop) != 0)
+    for (uint32_t k = issued > SH::kRing ? issued - SH::kRing : 0; k < issued; ++k)
+      mbar_wait_bounded(&sm.full[k % SH::kRing], (k / SH::kRing) & 1u, kWaitCycles);
+}
+
 // ------------------------------------------------- the products' warp (all lanes take part)
-template <int NC>
+template <int NC, int CL>
 __device__ void tile_products(const AttnParams& p, TileSmall& sm, uint32_t base, uint32_t tmem) {
   using SH = TileShape<NC>;
   constexpr uint32_t kScoreDesc = mma_desc(128, kAttnRows, 0, 0);
@@ -365,7 +436,7 @@ __device__ void tile_products(const AttnParams& p, TileSmall& sm, uint32_t base,
     ++t;
   };
   uint32_t done = 0, seg = 0;  // tiles summed, segments
-  for (SegmentWalk w(p); w.valid(); w.next(), ++seg) {
+  for (SegmentWalk w(p, blockIdx.x / CL); w.valid(); w.next(), ++seg) {
     const int tiles = w.t1 - w.t0;
     tile_wait(sm, p, &sm.q_full, seg & 1u);
     tc_fence_after();
@@ -381,7 +452,8 @@ __device__ void tile_products(const AttnParams& p, TileSmall& sm, uint32_t base,
         for (int k = 0; k < 8; ++k)  // 16 entries a step
           tc_mma(tmem + SH::kTmemO + c * kAttnRows, a + k * (2048 >> 4), probs + k * (2048 >> 4), kSumDesc,
                  j > 0 || k > 0);
-        tc_commit(&sm.empty[ro.slot]);
+        if (CL == 1) tc_commit(&sm.empty[ro.slot]);
+        else tc_commit_all(&sm.empty[ro.slot], 3);  // a pair's slot is free when both have used it
       }
       tc_commit(&sm.summed);
       ++done;
@@ -394,7 +466,7 @@ __device__ void tile_products(const AttnParams& p, TileSmall& sm, uint32_t base,
 }
 
 // ------------------------------------------------------------------------- the softmax warps
-template <int NC>
+template <int NC, int CL>
 __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* smem, uint32_t base, uint32_t tmem) {
   using SH = TileShape<NC>;
   const int tid = threadIdx.x, lane = tid & 31, quad = (tid >> 5) & 3, group = tid >> 7;
@@ -406,14 +478,15 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
   uint32_t t = 0;  // tiles so far
   auto barrier_group = [&]() { named_barrier(1 + group, 128); };
 
-  for (SegmentWalk w(p); w.valid(); w.next()) {
+  const int worker = blockIdx.x / CL, rank = CL == 1 ? 0 : static_cast<int>(cluster_rank());
+  for (SegmentWalk w(p, worker); w.valid(); w.next()) {
     const int seen_all = w.u.seen_all;
-    // where each row of q lies, and what it sees; rows behind the last one are zeros and see
-    // everything (they are never stored)
+    // where each row of q lies, and what it sees (rows behind the last one are zeros, see what
+    // the last one sees, and are never stored)
     if (tid < kAttnRows) {
-      const int row = w.u.block * kAttnRows + tid, token = row / p.group;
+      const int row = w.u.block * (CL * kAttnRows) + rank * kAttnRows + tid, token = row / p.group;
       const bool some = row < w.u.rows;
-      sm.lim[tid] = some ? visible(static_cast<int64_t>(w.u.first) + token, p.ratio, w.u.n) : INT_MAX;
+      sm.lim[tid] = some ? visible(static_cast<int64_t>(w.u.first) + token, p.ratio, w.u.n) : w.u.seen;
       sm.q_at[tid] = some ? (static_cast<int64_t>(w.u.token) + token) * p.q_row +
                                 (w.u.kvh * p.group + (row - token * p.group)) * p.q_head
                           : -1;
@@ -561,9 +634,9 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
     if ((lane & 1) == 0) sm.red[quad][c0 + (lane >> 1)] = l[0];
     barrier_group();
     const AttnUnit u = read_unit(p.units + w.unit);
-    const int row0 = u.block * kAttnRows;
+    const int row0 = u.block * (CL * kAttnRows) + rank * kAttnRows;
     const bool whole = w.t0 == 0 && w.t1 == u.tiles;
-    const int64_t piece = 2 * static_cast<int64_t>(blockIdx.x) + (w.t0 == 0 ? 1 : 0);
+    const int64_t piece = (2 * static_cast<int64_t>(worker) + (w.t0 == 0 ? 1 : 0)) * CL + rank;
     if (quad == 0 && lane < kSoftCols) {
       const int c = c0 + lane;
       const float z = (sm.red[0][c] + sm.red[1][c]) + (sm.red[2][c] + sm.red[3][c]), m = sm.m[c];
@@ -628,9 +701,61 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
   }
 }
 
+// Chunks: the entries that a sequence's last token sees, as bf16 rows in order, zeros up to the next
+// multiple of 128 rows and of 64 NC columns, so that the tile kernel's copies are whole boxes
+// whatever the format, the page size and the heads. Every unit of the sequence (one per 128
+// rows) reads them again; packing reads and writes them once. Block (x, s, cache head): 32
+// entries, a thread 8 columns at a time.
+constexpr int kPackThreads = 256, kPackRows = 32;
 template <int NC, int FORMAT>
-__global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(kPackThreads) attn_pack_kernel(const __grid_constant__ AttnParams p) {
+  constexpr int kPer = NC * 8;  // pieces of 8 columns
+  pdl_wait();
+  if (*p.status != 0) return;
+  const int s = blockIdx.y, kvh = blockIdx.z, e0 = blockIdx.x * kPackRows;
+  const int rows = sequence_rows(p, s);
+  if (rows == 0) return;
+  const int64_t first = p.first != nullptr ? __ldg(p.first + s) : 0;
+  const int n = visible(first + rows / p.group - 1, p.ratio, __ldg(p.entries + s));
+  if (e0 >= (n + kAttnEntries - 1) / kAttnEntries * kAttnEntries && e0 >= kAttnEntries) return;
+  uint16_t* to = p.packed + ((static_cast<int64_t>(s) * p.kv_heads + kvh) * p.packed_rows + e0) * (NC * 64);
+#pragma unroll 4
+  for (int i = threadIdx.x; i < kPackRows * kPer; i += kPackThreads) {
+    const int r = i / kPer, col = (i % kPer) * 8, e = e0 + r;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (e < n && col < p.d) {
+      const int page = __ldg(p.table + static_cast<int64_t>(s) * p.max_pages + e / p.page_size);
+      if (page >= 0 && page < p.num_pages) {
+        const int64_t entry = (static_cast<int64_t>(page) * p.page_size + e % p.page_size) * p.kv_heads + kvh;
+        if constexpr (FORMAT == CSA_CACHE_BF16) {
+          v = __ldg(reinterpret_cast<const uint4*>(p.data + (entry * p.d + col) * 2));
+        } else {
+          const float f = scale_value(__ldg(p.scales + entry * (p.d / CSA_CACHE_GROUP) + col / CSA_CACHE_GROUP));
+          const uint64_t sc = f2_pack(f, f);
+          if constexpr (FORMAT == CSA_CACHE_E4M3) {
+            const uint2 w = __ldg(reinterpret_cast<const uint2*>(p.data + entry * p.d + col));
+            v = make_uint4(Take<FORMAT>::two(w.x, sc), Take<FORMAT>::two(w.x >> 16, sc), Take<FORMAT>::two(w.y, sc),
+                           Take<FORMAT>::two(w.y >> 16, sc));
+          } else {
+            const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(p.data + entry * (p.d / 2) + col / 2));
+            v = make_uint4(Take<FORMAT>::two(w, sc), Take<FORMAT>::two(w >> 8, sc), Take<FORMAT>::two(w >> 16, sc),
+                           Take<FORMAT>::two(w >> 24, sc));
+          }
+        }
+      } else if (p.dev_error != nullptr) {
+        *p.dev_error = CSA_DEVERR_PAGE;
+      }
+    }
+    *reinterpret_cast<uint4*>(to + r * (NC * 64) + col) = v;
+  }
+}
+
+template <int NC, int SRC>
+__global__ void __launch_bounds__(TileCta<SRC>::kThreads, 1)
+    attn_tile_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap map) {
   using SH = TileShape<NC>;
+  using CTA = TileCta<SRC>;
+  constexpr int CL = CTA::kCluster;
   extern __shared__ unsigned char raw[];
   unsigned char* smem = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
   TileSmall& sm = *reinterpret_cast<TileSmall*>(smem + SH::kSmallOff);
@@ -639,8 +764,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
   if (warp == 0) tmem_alloc(&sm.tmem, SH::kTmemColumns);
   if (threadIdx.x == 32) {
     for (int i = 0; i < SH::kRing; ++i) {
-      mbar_init(&sm.full[i], kTileLoadWarps / 2);
-      mbar_init(&sm.empty[i], 1);
+      mbar_init(&sm.full[i], CTA::kByThreads ? kTileLoadWarps / 2 : 1);
+      mbar_init(&sm.empty[i], CL);
     }
     mbar_init(&sm.scores[0], 1);
     mbar_init(&sm.scores[1], 1);
@@ -653,28 +778,36 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (CL > 1) cluster_barrier();  // both CTAs' barriers are set up
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
   pdl_wait();
   const bool run = *p.status == 0;
-  if (warp >= kTileFirstLoader) {
-    regs_up<kLoadRegs>();
-    if (run) tile_fetch<NC, FORMAT>(p, sm, base);
-  } else if (warp >= kTileSoftWarps) {
-    regs_down<kIssueRegs>();
-    if (run && warp == kTileSoftWarps) tile_products<NC>(p, sm, base, tmem);
-  } else {
-    regs_down<kSoftRegs>();
-    if (run) tile_softmax<NC>(p, sm, smem, base, tmem);
+  if constexpr (CTA::kByThreads) {
+    if (warp >= kTileFirstLoader) {
+      regs_up<kLoadRegs>();
+      if (run) tile_fetch<NC, SRC>(p, sm, base);
+    } else if (warp >= kTileSoftWarps) {
+      regs_down<kIssueRegs>();
+      if (run && warp == kTileSoftWarps) tile_products<NC, CL>(p, sm, base, tmem);
+    } else {
+      regs_down<kSoftRegs>();
+      if (run) tile_softmax<NC, CL>(p, sm, smem, base, tmem);
+    }
+  } else if (run) {
+    if (warp == kTileSoftWarps) tile_products<NC, CL>(p, sm, base, tmem);
+    else if (warp == kTileSoftWarps + 1) tile_copy<NC, SRC>(p, sm, base, &map);
+    else if (warp < kTileSoftWarps) tile_softmax<NC, CL>(p, sm, smem, base, tmem);
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (CL > 1) cluster_barrier();  // nothing of the other CTA's is on its way here
   tc_fence_after();
   if (warp == 0) tmem_free(tmem, SH::kTmemColumns);
 }
 
-// Joins the pieces of the units that CTAs share: block (i, y) the rows 4y .. 4y + 3 of the unit
-// whose first piece is CTA i's last one. Lane k of every warp holds piece k's weights for the
+// Joins the pieces of the units that workers share: block (i, y) the rows 4y .. 4y + 3 of the unit
+// whose first piece is worker i's last one. Lane k of every warp holds piece k's weights for the
 // four rows (32 pieces at a time); a warp adds up 32 or 64 columns of them.
 template <int NC>
 struct JoinShape {
@@ -682,7 +815,7 @@ struct JoinShape {
   static constexpr int kWarps = kColumnBlocks < 8 ? kColumnBlocks : 8;
   static constexpr int kPer = kColumnBlocks / kWarps;
 };
-template <int NC>
+template <int NC, int CL>
 __global__ void __launch_bounds__(JoinShape<NC>::kWarps * 32) attn_join_kernel(const __grid_constant__ AttnParams p) {
   using SH = TileShape<NC>;
   using JS = JoinShape<NC>;
@@ -693,9 +826,10 @@ __global__ void __launch_bounds__(JoinShape<NC>::kWarps * 32) attn_join_kernel(c
   if (n == 0) return;
   const AttnUnit u = p.starts[i + 1].u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int r0 = blockIdx.y * 4, row0 = u.block * kAttnRows + r0;
+  const int rank = blockIdx.y / (kAttnRows / 4), quarter = blockIdx.y % (kAttnRows / 4);
+  const int r0 = quarter * 4, row0 = (u.block * CL + rank) * kAttnRows + r0;
   if (row0 >= u.rows) return;
-  auto slot = [&](int k) { return 2 * static_cast<int64_t>(i + k) + (k == 0 ? 1 : 0); };
+  auto slot = [&](int k) { return (2 * static_cast<int64_t>(i + k) + (k == 0 ? 1 : 0)) * CL + rank; };
 
   float sink_e[4], mx[4], den[4], acc[JS::kPer][4];
   bool some[4];
@@ -750,7 +884,7 @@ __global__ void __launch_bounds__(JoinShape<NC>::kWarps * 32) attn_join_kernel(c
       for (int r = 0; r < 4; ++r) g[r] = __shfl_sync(0xFFFFFFFFu, f[r], k);
 #pragma unroll
       for (int b = 0; b < JS::kPer; ++b) {
-        const float4 v = o[slot(k0 + k) * kPiece + ((warp * JS::kPer + b) * (kAttnRows / 4) + blockIdx.y) * 32 + lane];
+        const float4 v = o[slot(k0 + k) * kPiece + ((warp * JS::kPer + b) * (kAttnRows / 4) + quarter) * 32 + lane];
         acc[b][0] = fmaf(g[0], v.x, acc[b][0]);
         acc[b][1] = fmaf(g[1], v.y, acc[b][1]);
         acc[b][2] = fmaf(g[2], v.z, acc[b][2]);
