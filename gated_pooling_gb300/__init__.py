@@ -108,24 +108,39 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
 
 
 def _ptr(x) -> Optional[int]:
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or isinstance(x, int):
         return x
     return x.data_ptr()
 
 
+_raw_stream = None
+
+
+def _find_raw_stream():
+    """The current stream's handle: torch's raw getter where it has one (0.1 us; making a Stream
+    object for it takes 2.9 us, as long as the rest of a small call), else the public way."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    device = getattr(torch._C, "_cuda_getDevice", None)
+    if raw is not None and device is not None:
+        torch.cuda.init()
+        return lambda: raw(device())
+    return lambda: torch.cuda.current_stream().cuda_stream
+
+
 def _stream(stream) -> Optional[int]:
+    global _raw_stream
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        if _raw_stream is None:
+            _raw_stream = _find_raw_stream()
+        return _raw_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
 
 
 def _check(status: int, what: str) -> None:
-    if status != CSA_OK:
+    if status:
         msg = load().csa_status_string(status).decode()
         if status == CSA_ERR_CUDA:
             msg += f" ({load().csa_last_error_string().decode()})"
