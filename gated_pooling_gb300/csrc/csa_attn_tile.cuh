@@ -40,13 +40,24 @@ constexpr int kSoftThreads = kTileSoftWarps * 32;
 constexpr int kSoftCols = 16;  // rows of a softmax thread's group
 constexpr int kTileLoaders = kTileLoadWarps * 32;
 constexpr int kTileFirstLoader = kTileSoftWarps + 4;
-// Where a tile comes from: threads that read the pages (in each of the cache's formats), tensor
-// copies of the pages' bf16 boxes, or tensor copies of a sequence's packed entries that go to
-// both CTAs of a pair.
-enum TileSource { kFromBf16 = CSA_CACHE_BF16, kFromE4m3 = CSA_CACHE_E4M3, kFromE2m1 = CSA_CACHE_E2M1, kFromBoxes, kFromPacked };
+// Where a tile comes from: threads that read the pages (in each of the cache's formats); tensor
+// copies of the pages' codes into the second half of a pair's slot, which threads widen over the
+// whole of it; tensor copies of the pages' bf16 boxes; or tensor copies of a sequence's packed
+// entries that go to both CTAs of a pair.
+enum TileSource {
+  kFromBf16 = CSA_CACHE_BF16,
+  kFromE4m3 = CSA_CACHE_E4M3,
+  kFromE2m1 = CSA_CACHE_E2M1,
+  kFromE4m3Boxes,
+  kFromE2m1Boxes,
+  kFromBoxes,
+  kFromPacked
+};
 template <int SRC>
 struct TileCta {
-  static constexpr bool kByThreads = SRC < kFromBoxes;
+  static constexpr bool kByThreads = SRC < kFromBoxes;  // threads fetch or widen
+  static constexpr bool kByCopies = SRC >= kFromE4m3Boxes;
+  static constexpr int kFormat = SRC == kFromE4m3Boxes ? kFromE4m3 : SRC == kFromE2m1Boxes ? kFromE2m1 : SRC;
   static constexpr int kCluster = SRC == kFromPacked ? 2 : 1;
   static constexpr int kThreads = (kTileFirstLoader + (kByThreads ? kTileLoadWarps : 0)) * 32;
 };
@@ -85,7 +96,7 @@ struct TileSmall {
   float fac[kAttnRows];
   float red[4][kAttnRows];  // column maxima, then weight sums, by quadrant
   int lim[kAttnRows];
-  uint64_t full[5], empty[5], scores[2], probs, summed, q_full, drain;
+  uint64_t full[5], empty[5], raw[5], scores[2], probs, summed, q_full, drain;
   uint32_t tmem;
   int stop;
 };
@@ -111,6 +122,7 @@ __device__ __forceinline__ uint32_t widen2(uint32_t half2, uint64_t scale) {
   const float2 f = __half22float2(*reinterpret_cast<__half2*>(&half2));
   return f2_to_bf2(f2_mul(f2_pack(f.x, f.y), scale));
 }
+constexpr uint32_t kNoScale = 256;  // no entry here
 template <int FORMAT>
 struct Take;
 template <>
@@ -151,12 +163,22 @@ struct Take<CSA_CACHE_E4M3> {
   uint32_t k;
   __device__ __forceinline__ void load(const AttnParams& p, int64_t at, int col) {
     a = b = make_uint4(0, 0, 0, 0);
-    k = 127;
+    load_scale(p, at, col);
     if (at >= 0 && col < p.d) {
       const uint4* w = reinterpret_cast<const uint4*>(p.data + at + col);
       a = __ldg(w);
       b = __ldg(w + 1);
-      k = __ldg(p.scales + (at >> 5) + (col >> 5));
+    }
+  }
+  // the scale alone (none: -1), then the codes from a copied pair (128 bytes an entry)
+  __device__ __forceinline__ void load_scale(const AttnParams& p, int64_t at, int col) {
+    k = at >= 0 && col < p.d ? __ldg(p.scales + (at >> 5) + (col >> 5)) : kNoScale;
+  }
+  __device__ __forceinline__ void load_codes(uint32_t raw, int row, int t) {
+    a = b = make_uint4(0, 0, 0, 0);
+    if (k != kNoScale) {
+      a = lds128(raw + row * 128 + (t & 3) * 32);
+      b = lds128(raw + row * 128 + (t & 3) * 32 + 16);
     }
   }
   static __device__ __forceinline__ uint32_t two(uint32_t c, uint64_t s) {
@@ -165,7 +187,7 @@ struct Take<CSA_CACHE_E4M3> {
     return widen2(h, s);
   }
   __device__ __forceinline__ void store(uint32_t pair, int row, int t) const {
-    const float f = scale_value(k);
+    const float f = k == kNoScale ? 0.f : scale_value(k);
     const uint64_t s = f2_pack(f, f);
     const bool swap = (t & 2) != 0;
     const uint4 u = swap ? b : a, v = swap ? a : b;
@@ -186,11 +208,14 @@ struct Take<CSA_CACHE_E2M1> {
   uint32_t k;
   __device__ __forceinline__ void load(const AttnParams& p, int64_t at, int col) {
     a = make_uint4(0, 0, 0, 0);
-    k = 127;
-    if (at >= 0 && col < p.d) {
-      a = __ldg(reinterpret_cast<const uint4*>(p.data + at + (col >> 1)));
-      k = __ldg(p.scales + (at >> 4) + (col >> 5));
-    }
+    load_scale(p, at, col);
+    if (at >= 0 && col < p.d) a = __ldg(reinterpret_cast<const uint4*>(p.data + at + (col >> 1)));
+  }
+  __device__ __forceinline__ void load_scale(const AttnParams& p, int64_t at, int col) {
+    k = at >= 0 && col < p.d ? __ldg(p.scales + (at >> 4) + (col >> 5)) : kNoScale;
+  }
+  __device__ __forceinline__ void load_codes(uint32_t raw, int row, int t) {  // 64 bytes an entry
+    a = k != kNoScale ? lds128(raw + row * 64 + (t & 3) * 16) : make_uint4(0, 0, 0, 0);
   }
   static __device__ __forceinline__ uint32_t two(uint32_t c, uint64_t s) {
     uint32_t h;
@@ -198,7 +223,7 @@ struct Take<CSA_CACHE_E2M1> {
     return widen2(h, s);
   }
   __device__ __forceinline__ void store(uint32_t pair, int row, int t) const {
-    const float f = scale_value(k);
+    const float f = k == kNoScale ? 0.f : scale_value(k);
     const uint64_t s = f2_pack(f, f);
     const bool swap = (t & 2) != 0;
     const uint4 u = swap ? make_uint4(a.z, a.w, a.x, a.y) : a;
@@ -278,10 +303,11 @@ struct SegmentWalk {
 };
 
 // ------------------------------------------------------------------------------ the fetchers
-template <int NC, int FORMAT>
+template <int NC, int SRC>
 __device__ void tile_fetch(const AttnParams& p, TileSmall& sm, uint32_t base) {
   using SH = TileShape<NC>;
-  using P = Take<FORMAT>;
+  constexpr bool kCopied = TileCta<SRC>::kByCopies;
+  using P = Take<TileCta<SRC>::kFormat>;
   constexpr int kGroup = kTileLoaders / 2;
   constexpr int kStep = SH::kPairs == 1 ? 2 : 1;  // tiles from one of a group's to its next
   const int lt = threadIdx.x - kTileFirstLoader * 32;
@@ -332,10 +358,21 @@ __device__ void tile_fetch(const AttnParams& p, TileSmall& sm, uint32_t base) {
   while (w.valid()) {
     if (fresh) rows();
     P v[P::kRows];
+    const int64_t* at = &sm.row[group][buf][P::first_row(gt)];
+    const int col = pair * 128 + P::column(gt);
+    if constexpr (kCopied) {
 #pragma unroll
-    for (int i = 0; i < P::kRows; ++i)
-      v[i].load(p, sm.row[group][buf][P::first_row(gt) + i * P::kRowStep], pair * 128 + P::column(gt));
-    tile_wait(sm, p, &sm.empty[ring.slot], ring.lap ^ 1u);
+      for (int i = 0; i < P::kRows; ++i) v[i].load_scale(p, at[i * P::kRowStep], col);
+      tile_wait(sm, p, &sm.raw[ring.slot], ring.lap);
+#pragma unroll
+      for (int i = 0; i < P::kRows; ++i)
+        v[i].load_codes(base + ring.slot * kPairBytes + kChunkBytes, P::first_row(gt) + i * P::kRowStep, gt);
+      named_barrier(6 + group, kGroup);  // the codes are in registers: their place is written over
+    } else {
+#pragma unroll
+      for (int i = 0; i < P::kRows; ++i) v[i].load(p, at[i * P::kRowStep], col);
+      tile_wait(sm, p, &sm.empty[ring.slot], ring.lap ^ 1u);
+    }
 #pragma unroll
     for (int i = 0; i < P::kRows; ++i)
       v[i].store(base + ring.slot * kPairBytes, P::first_row(gt) + i * P::kRowStep, gt);
@@ -348,7 +385,8 @@ __device__ void tile_fetch(const AttnParams& p, TileSmall& sm, uint32_t base) {
 }
 
 // ------------------------------------------------------------- the warp that issues tensor copies
-// From the pages: lane i copies box i mod n of chunk i / n of each pair, n = 128 / box_rows of them.
+// From the pages: lane i copies box i mod n of chunk i / n of each pair (codes: of the pair), n =
+// 128 / box_rows of them.
 // A box behind the last entry that the unit sees is not copied, and rows behind it in a copied
 // box are whatever the pool holds there: masked in the scores, and made finite where they are
 // not before the second product. From packed entries: one box of a pair by each CTA of the
@@ -375,11 +413,14 @@ __device__ void tile_copy(const AttnParams& p, TileSmall& sm, uint32_t base, con
         }
     }
   } else {
+    // boxes of a pair: of both chunks (bf16), or of the codes of both together
+    constexpr bool kCodes = SRC != kFromBoxes;
+    constexpr int kEntryBytes = SRC == kFromE2m1Boxes ? 64 : 128;
     const int n = kAttnEntries / p.box_rows, chunk = lane / n, box = lane % n;
     for (SegmentWalk w(p, blockIdx.x); w.valid(); w.next()) {
       for (int tile = w.t0; tile < w.t1; ++tile) {
         const int e = tile * kAttnEntries + box * p.box_rows;
-        bool on = chunk < 2 && e < w.u.seen;
+        bool on = chunk < (kCodes ? 1 : 2) && e < w.u.seen;
         int slot = 0;
         if (on) {
           const int page = __ldg(p.table + static_cast<int64_t>(w.u.s) * p.max_pages + e / p.page_size);
@@ -387,14 +428,16 @@ __device__ void tile_copy(const AttnParams& p, TileSmall& sm, uint32_t base, con
           if (on) slot = page * p.page_size + e % p.page_size;
           else if (p.dev_error != nullptr) *p.dev_error = CSA_DEVERR_PAGE;
         }
-        const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, on)) * p.box_rows * 128;
+        const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, on)) * p.box_rows * kEntryBytes;
         for (int c = 0; c < SH::kPairs; ++c, ring.next(), ++issued) {
           tile_wait(sm, p, &sm.empty[ring.slot], ring.lap ^ 1u);
-          if (lane == 0) mbar_arrive_expect_tx(&sm.full[ring.slot], bytes);
+          uint64_t* bar = kCodes ? &sm.raw[ring.slot] : &sm.full[ring.slot];
+          if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
           __syncwarp();
           if (on)
-            box_load3(base + ring.slot * kPairBytes + chunk * kChunkBytes + box * p.box_rows * 128, map,
-                      c * 128 + chunk * 64, w.u.kvh, slot, &sm.full[ring.slot]);
+            box_load3(base + ring.slot * kPairBytes + (kCodes ? 1 : chunk) * kChunkBytes +
+                          box * p.box_rows * kEntryBytes,
+                      map, kCodes ? c * kEntryBytes : c * 128 + chunk * 64, w.u.kvh, slot, bar);
         }
       }
     }
@@ -406,7 +449,8 @@ __device__ void tile_copy(const AttnParams& p, TileSmall& sm, uint32_t base, con
   // after a stop, the copies that nobody waited for: the last lap of the ring
   if (*reinterpret_cast<volatile int*>(&sm.stop) != 0)
     for (uint32_t k = issued > SH::kRing ? issued - SH::kRing : 0; k < issued; ++k)
-      mbar_wait_bounded(&sm.full[k % SH::kRing], (k / SH::kRing) & 1u, kWaitCycles);
+      mbar_wait_bounded(SRC < kFromBoxes ? &sm.raw[k % SH::kRing] : &sm.full[k % SH::kRing], (k / SH::kRing) & 1u,
+                        kWaitCycles);
 }
 
 // ------------------------------------------------- the products' warp (all lanes take part)
@@ -766,6 +810,7 @@ __global__ void __launch_bounds__(TileCta<SRC>::kThreads, 1)
     for (int i = 0; i < SH::kRing; ++i) {
       mbar_init(&sm.full[i], CTA::kByThreads ? kTileLoadWarps / 2 : 1);
       mbar_init(&sm.empty[i], CL);
+      mbar_init(&sm.raw[i], 1);
     }
     mbar_init(&sm.scores[0], 1);
     mbar_init(&sm.scores[1], 1);
@@ -790,6 +835,8 @@ __global__ void __launch_bounds__(TileCta<SRC>::kThreads, 1)
     } else if (warp >= kTileSoftWarps) {
       regs_down<kIssueRegs>();
       if (run && warp == kTileSoftWarps) tile_products<NC, CL>(p, sm, base, tmem);
+      if constexpr (CTA::kByCopies)
+        if (run && warp == kTileSoftWarps + 1) tile_copy<NC, SRC>(p, sm, base, &map);
     } else {
       regs_down<kSoftRegs>();
       if (run) tile_softmax<NC, CL>(p, sm, smem, base, tmem);
