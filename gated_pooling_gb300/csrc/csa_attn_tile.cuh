@@ -118,9 +118,53 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
 // columns, a scale's, of 4 entries, so that finding a place and its scale is paid once per 32
 // values: a fetch of 8-bit entries in pieces of 8 took 1100 instructions a pair and thread
 // instead of about 400, and was bound by them.
-__device__ __forceinline__ uint32_t widen2(uint32_t half2, uint64_t scale) {
-  const float2 f = __half22float2(*reinterpret_cast<__half2*>(&half2));
-  return f2_to_bf2(f2_mul(f2_pack(f.x, f.y), scale));
+//
+// Codes become bf16 by moving their bits: sign, exponent and mantissa go where bf16 has its own,
+// which is the code's value times 2^-120 (e4m3) or 2^-126 (e2m1), its subnormals among bf16's
+// subnormals, and one bf16 product with 2^120 (2^126) times the scale makes the value (two where
+// that factor is past bf16's range). A conversion instruction per two codes and one per two
+// bf16 values, 16 lanes a cycle each, took 2.2 thousand cycles for the two pairs under way.
+struct Widen {
+  __nv_bfloat162 f, g;
+  bool twice;
+  // LIFT: 120 or 126
+  template <int LIFT>
+  static __device__ __forceinline__ Widen of(uint32_t k) {
+    constexpr uint32_t kMost = 254 - LIFT;
+    auto factor = [](uint32_t field) {
+      const uint32_t b = field << 7 | field << 23;
+      return *reinterpret_cast<const __nv_bfloat162*>(&b);
+    };
+    Widen w;
+    w.twice = k > kMost;
+    w.f = factor(k >= 255u ? 0x1FFu & (k == 255u ? 0x1FFu : 127u) : (w.twice ? kMost : k) + LIFT);
+    w.g = factor(w.twice && k < 255u ? 127u + k - kMost : 127u);
+    return w;
+  }
+  __device__ __forceinline__ uint32_t two(uint32_t bits) const {
+    __nv_bfloat162 v = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&bits), f);
+    if (twice) v = __hmul2(v, g);
+    return *reinterpret_cast<uint32_t*>(&v);
+  }
+  // four e4m3 codes; eight e2m1 codes
+  __device__ __forceinline__ uint2 four(uint32_t w) const {
+    const uint32_t x = __byte_perm(w, 0, 0x1404), y = __byte_perm(w, 0, 0x3424);
+    return make_uint2(two(((x >> 4) & 0x07F007F0u) | (x & 0x80008000u)),
+                      two(((y >> 4) & 0x07F007F0u) | (y & 0x80008000u)));
+  }
+  __device__ __forceinline__ uint4 eight(uint32_t w) const {
+    const uint32_t lo = (w << 4) & 0xF0F0F0F0u, hi = w & 0xF0F0F0F0u;
+    auto at = [&](uint32_t x) { return two(((x >> 6) & 0x01C001C0u) | (x & 0x80008000u)); };
+    return make_uint4(at(__byte_perm(lo, hi, 0x4400)), at(__byte_perm(lo, hi, 0x5511)), at(__byte_perm(lo, hi, 0x6622)),
+                      at(__byte_perm(lo, hi, 0x7733)));
+  }
+};
+// Whether a word holds an e4m3 NaN (csa_cache_write makes none; such a code is no number to move).
+__device__ __forceinline__ uint32_t e4m3_nans(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
+__device__ __forceinline__ uint32_t nan_where(uint32_t v, uint32_t w, int byte) {
+  if (((w >> (8 * byte)) & 0x7Fu) == 0x7Fu) v |= 0x00007FFFu;
+  if (((w >> (8 * byte + 8)) & 0x7Fu) == 0x7Fu) v |= 0x7FFF0000u;
+  return v;
 }
 constexpr uint32_t kNoScale = 256;  // no entry here
 template <int FORMAT>
@@ -181,20 +225,25 @@ struct Take<CSA_CACHE_E4M3> {
       b = lds128(raw + row * 128 + (t & 3) * 32 + 16);
     }
   }
-  static __device__ __forceinline__ uint32_t two(uint32_t c, uint64_t s) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(c)));
-    return widen2(h, s);
+  // 8 codes
+  static __device__ __forceinline__ uint4 widen(const Widen& s, uint32_t x, uint32_t y) {
+    const uint2 u = s.four(x), v = s.four(y);
+    uint4 r = make_uint4(u.x, u.y, v.x, v.y);
+    if (e4m3_nans(x) | e4m3_nans(y)) {
+      r.x = nan_where(r.x, x, 0);
+      r.y = nan_where(r.y, x, 2);
+      r.z = nan_where(r.z, y, 0);
+      r.w = nan_where(r.w, y, 2);
+    }
+    return r;
   }
+  static constexpr int kLift = 120;
   __device__ __forceinline__ void store(uint32_t pair, int row, int t) const {
-    const float f = k == kNoScale ? 0.f : scale_value(k);
-    const uint64_t s = f2_pack(f, f);
+    const Widen s = Widen::of<kLift>(k);
     const bool swap = (t & 2) != 0;
     const uint4 u = swap ? b : a, v = swap ? a : b;
     store_pieces(pair, row, t, [&](int i) {
-      const uint32_t x = i == 0 ? u.x : i == 1 ? u.z : i == 2 ? v.x : v.z;
-      const uint32_t y = i == 0 ? u.y : i == 1 ? u.w : i == 2 ? v.y : v.w;
-      return make_uint4(two(x, s), two(x >> 16, s), two(y, s), two(y >> 16, s));
+      return i == 0 ? widen(s, u.x, u.y) : i == 1 ? widen(s, u.z, u.w) : i == 2 ? widen(s, v.x, v.y) : widen(s, v.z, v.w);
     });
   }
 };
@@ -217,20 +266,12 @@ struct Take<CSA_CACHE_E2M1> {
   __device__ __forceinline__ void load_codes(uint32_t raw, int row, int t) {  // 64 bytes an entry
     a = k != kNoScale ? lds128(raw + row * 64 + (t & 3) * 16) : make_uint4(0, 0, 0, 0);
   }
-  static __device__ __forceinline__ uint32_t two(uint32_t c, uint64_t s) {
-    uint32_t h;
-    asm("{\n\t.reg .b8 b;\n\tcvt.u8.u32 b, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}" : "=r"(h) : "r"(c & 0xFFu));
-    return widen2(h, s);
-  }
+  static constexpr int kLift = 126;
   __device__ __forceinline__ void store(uint32_t pair, int row, int t) const {
-    const float f = k == kNoScale ? 0.f : scale_value(k);
-    const uint64_t s = f2_pack(f, f);
+    const Widen s = Widen::of<kLift>(k);
     const bool swap = (t & 2) != 0;
     const uint4 u = swap ? make_uint4(a.z, a.w, a.x, a.y) : a;
-    store_pieces(pair, row, t, [&](int i) {
-      const uint32_t x = i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w;
-      return make_uint4(two(x, s), two(x >> 8, s), two(x >> 16, s), two(x >> 24, s));
-    });
+    store_pieces(pair, row, t, [&](int i) { return s.eight(i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w); });
   }
 };
 
@@ -427,6 +468,15 @@ __device__ void tile_copy(const AttnParams& p, TileSmall& sm, uint32_t base, con
           on = page >= 0 && page < p.num_pages;
           if (on) slot = page * p.page_size + e % p.page_size;
           else if (p.dev_error != nullptr) *p.dev_error = CSA_DEVERR_PAGE;
+        }
+        // the next tile's boxes on their way into L2 meanwhile
+        const int e1 = e + kAttnEntries;
+        if (chunk < (kCodes ? 1 : 2) && tile + 1 < w.t1 && e1 < w.u.seen) {
+          const int page = __ldg(p.table + static_cast<int64_t>(w.u.s) * p.max_pages + e1 / p.page_size);
+          if (page >= 0 && page < p.num_pages)
+            for (int c = 0; c < SH::kPairs; ++c)
+              box_prefetch3(map, kCodes ? c * kEntryBytes : c * 128 + chunk * 64, w.u.kvh,
+                            page * p.page_size + e1 % p.page_size);
         }
         const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, on)) * p.box_rows * kEntryBytes;
         for (int c = 0; c < SH::kPairs; ++c, ring.next(), ++issued) {
@@ -756,34 +806,31 @@ __global__ void __launch_bounds__(kPackThreads) attn_pack_kernel(const __grid_co
   constexpr int kPer = NC * 8;  // pieces of 8 columns
   pdl_wait();
   if (*p.status != 0) return;
-  const int s = blockIdx.y, kvh = blockIdx.z, e0 = blockIdx.x * kPackRows;
-  const int rows = sequence_rows(p, s);
+  const int seq = blockIdx.y, kvh = blockIdx.z, e0 = blockIdx.x * kPackRows;
+  const int rows = sequence_rows(p, seq);
   if (rows == 0) return;
-  const int64_t first = p.first != nullptr ? __ldg(p.first + s) : 0;
-  const int n = visible(first + rows / p.group - 1, p.ratio, __ldg(p.entries + s));
+  const int64_t first = p.first != nullptr ? __ldg(p.first + seq) : 0;
+  const int n = visible(first + rows / p.group - 1, p.ratio, __ldg(p.entries + seq));
   if (e0 >= (n + kAttnEntries - 1) / kAttnEntries * kAttnEntries && e0 >= kAttnEntries) return;
-  uint16_t* to = p.packed + ((static_cast<int64_t>(s) * p.kv_heads + kvh) * p.packed_rows + e0) * (NC * 64);
+  uint16_t* to = p.packed + ((static_cast<int64_t>(seq) * p.kv_heads + kvh) * p.packed_rows + e0) * (NC * 64);
 #pragma unroll 4
   for (int i = threadIdx.x; i < kPackRows * kPer; i += kPackThreads) {
     const int r = i / kPer, col = (i % kPer) * 8, e = e0 + r;
     uint4 v = make_uint4(0, 0, 0, 0);
     if (e < n && col < p.d) {
-      const int page = __ldg(p.table + static_cast<int64_t>(s) * p.max_pages + e / p.page_size);
+      const int page = __ldg(p.table + static_cast<int64_t>(seq) * p.max_pages + e / p.page_size);
       if (page >= 0 && page < p.num_pages) {
         const int64_t entry = (static_cast<int64_t>(page) * p.page_size + e % p.page_size) * p.kv_heads + kvh;
         if constexpr (FORMAT == CSA_CACHE_BF16) {
           v = __ldg(reinterpret_cast<const uint4*>(p.data + (entry * p.d + col) * 2));
         } else {
-          const float f = scale_value(__ldg(p.scales + entry * (p.d / CSA_CACHE_GROUP) + col / CSA_CACHE_GROUP));
-          const uint64_t sc = f2_pack(f, f);
+          const Widen s = Widen::of<Take<FORMAT>::kLift>(
+              __ldg(p.scales + entry * (p.d / CSA_CACHE_GROUP) + col / CSA_CACHE_GROUP));
           if constexpr (FORMAT == CSA_CACHE_E4M3) {
             const uint2 w = __ldg(reinterpret_cast<const uint2*>(p.data + entry * p.d + col));
-            v = make_uint4(Take<FORMAT>::two(w.x, sc), Take<FORMAT>::two(w.x >> 16, sc), Take<FORMAT>::two(w.y, sc),
-                           Take<FORMAT>::two(w.y >> 16, sc));
+            v = Take<FORMAT>::widen(s, w.x, w.y);
           } else {
-            const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(p.data + entry * (p.d / 2) + col / 2));
-            v = make_uint4(Take<FORMAT>::two(w, sc), Take<FORMAT>::two(w >> 8, sc), Take<FORMAT>::two(w >> 16, sc),
-                           Take<FORMAT>::two(w >> 24, sc));
+            v = s.eight(__ldg(reinterpret_cast<const uint32_t*>(p.data + entry * (p.d / 2) + col / 2)));
           }
         }
       } else if (p.dev_error != nullptr) {

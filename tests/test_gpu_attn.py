@@ -203,6 +203,29 @@ def test_nonfinite_entries_stay_behind_the_mask(cuda_lib, H, d, fmt, bad):
     assert torch.isfinite(ref).all()
 
 
+@pytest.mark.parametrize("fmt", [R.E4M3, R.FP4])
+@pytest.mark.parametrize("H,kv,d,lens,page", [(64, 1, 512, [2], 16), (8, 2, 128, [3], 16), (8, 1, 96, [3], 5), (64, 1, 128, [9], 16)])
+def test_every_code_and_scales_far_from_one(cuda_lib, fmt, H, kv, d, lens, page):
+    """Random codes (all of them but NaN's) at scales from 2^-9 to 2^11, past the range in which one
+    product with a bf16 factor widens them; then an e4m3 NaN code, which only its readers see."""
+    c = Case(lens, [300], H, kv, d, fmt, page=page, ratio=0, seed=11)
+    g = torch.Generator().manual_seed(12)
+    slots = c.data.shape[0]
+    codes = torch.randint(0, 256 if fmt == R.E4M3 else 16, (slots, kv, d), generator=g)
+    if fmt == R.E4M3:
+        codes[codes % 128 == 127] = 3
+    k = torch.randint(118, 139, (slots, kv, d // 32), generator=g)
+    c.data, c.scales = R.pack(codes, fmt), k.to(torch.uint8)
+    c.values = R.dequantise(codes, k, fmt)
+    c.scale = 1.0 / (float(c.values.abs().max()) * math.sqrt(d))
+    c.check(cuda_lib)
+    if fmt == R.E4M3:
+        c.data[int(c.table[0, 0]) * page, 0, 5] = 0x7F
+        out, _, err = c.run(cuda_lib)
+        assert err == 0
+        assert torch.isnan(out[:lens[0], :H // kv].float()).all() and torch.isfinite(out[:lens[0], H // kv:].float()).all()
+
+
 def test_query_rows_are_apart(cuda_lib):
     for H, d in ((16, 512), (8, 128), (3, 65)):
         c = Case([12], [200], H, 1, d, ratio=1, first="end", seed=2)
