@@ -121,37 +121,30 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
 //
 // Codes become bf16 by moving their bits: sign, exponent and mantissa go where bf16 has its own,
 // which is the code's value times 2^-120 (e4m3) or 2^-126 (e2m1), its subnormals among bf16's
-// subnormals, and one bf16 product with 2^120 (2^126) times the scale makes the value (two where
-// that factor is past bf16's range). A conversion instruction per two codes and one per two
-// bf16 values, 16 lanes a cycle each, took 2.2 thousand cycles for the two pairs under way.
+// subnormals, and one bf16 product with 2^120 (2^126) times the scale makes the value. Without a
+// branch, for the scales up to 2^7 (2^1) whose factor is within bf16's range, and no NaN
+// among the codes; anything else goes through fp32, code by code. (The conversion
+// instructions, 16 lanes a cycle each, took 2.2 thousand cycles for the two pairs under way.)
+template <int FORMAT>
 struct Widen {
-  __nv_bfloat162 f, g;
-  bool twice;
-  // LIFT: 120 or 126
-  template <int LIFT>
-  static __device__ __forceinline__ Widen of(uint32_t k) {
-    constexpr uint32_t kMost = 254 - LIFT;
-    auto factor = [](uint32_t field) {
-      const uint32_t b = field << 7 | field << 23;
-      return *reinterpret_cast<const __nv_bfloat162*>(&b);
-    };
-    Widen w;
-    w.twice = k > kMost;
-    w.f = factor(k >= 255u ? 0x1FFu & (k == 255u ? 0x1FFu : 127u) : (w.twice ? kMost : k) + LIFT);
-    w.g = factor(w.twice && k < 255u ? 127u + k - kMost : 127u);
-    return w;
+  static constexpr uint32_t kLift = FORMAT == CSA_CACHE_E4M3 ? 120 : 126;
+  static __device__ __forceinline__ bool plain(uint32_t k) { return k <= 254u - kLift; }
+  __nv_bfloat162 f;
+  __device__ __forceinline__ explicit Widen(uint32_t k) {
+    const uint32_t b = (k + kLift) << 7 | (k + kLift) << 23;
+    f = *reinterpret_cast<const __nv_bfloat162*>(&b);
   }
   __device__ __forceinline__ uint32_t two(uint32_t bits) const {
-    __nv_bfloat162 v = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&bits), f);
-    if (twice) v = __hmul2(v, g);
-    return *reinterpret_cast<uint32_t*>(&v);
+    const __nv_bfloat162 v = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&bits), f);
+    return *reinterpret_cast<const uint32_t*>(&v);
   }
-  // four e4m3 codes; eight e2m1 codes
-  __device__ __forceinline__ uint2 four(uint32_t w) const {
-    const uint32_t x = __byte_perm(w, 0, 0x1404), y = __byte_perm(w, 0, 0x3424);
-    return make_uint2(two(((x >> 4) & 0x07F007F0u) | (x & 0x80008000u)),
-                      two(((y >> 4) & 0x07F007F0u) | (y & 0x80008000u)));
+  // 8 e4m3 codes
+  __device__ __forceinline__ uint4 eight(uint32_t w, uint32_t v) const {
+    auto at = [&](uint32_t x) { return two(((x >> 4) & 0x07F007F0u) | (x & 0x80008000u)); };
+    return make_uint4(at(__byte_perm(w, 0, 0x1404)), at(__byte_perm(w, 0, 0x3424)), at(__byte_perm(v, 0, 0x1404)),
+                      at(__byte_perm(v, 0, 0x3424)));
   }
+  // 8 e2m1 codes
   __device__ __forceinline__ uint4 eight(uint32_t w) const {
     const uint32_t lo = (w << 4) & 0xF0F0F0F0u, hi = w & 0xF0F0F0F0u;
     auto at = [&](uint32_t x) { return two(((x >> 6) & 0x01C001C0u) | (x & 0x80008000u)); };
@@ -159,14 +152,28 @@ struct Widen {
                       at(__byte_perm(lo, hi, 0x7733)));
   }
 };
-// Whether a word holds an e4m3 NaN (csa_cache_write makes none; such a code is no number to move).
+// Bits left where a word holds an e4m3 NaN.
 __device__ __forceinline__ uint32_t e4m3_nans(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
-__device__ __forceinline__ uint32_t nan_where(uint32_t v, uint32_t w, int byte) {
-  if (((w >> (8 * byte)) & 0x7Fu) == 0x7Fu) v |= 0x00007FFFu;
-  if (((w >> (8 * byte + 8)) & 0x7Fu) == 0x7Fu) v |= 0x7FFF0000u;
-  return v;
+// Any codes at any scale, by fp32 (exact but for bf16's own subnormals).
+__device__ __forceinline__ uint4 widen_any(uint32_t w, uint32_t v, float s) {
+  uint32_t r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = e4m3x2_to_float2(((i < 2 ? w : v) >> (16 * (i % 2))) & 0xFFFFu);
+    r[i] = pack_bf16x2(f.x * s, f.y * s);
+  }
+  return make_uint4(r[0], r[1], r[2], r[3]);
 }
-constexpr uint32_t kNoScale = 256;  // no entry here
+__device__ __forceinline__ uint4 widen_any(uint32_t w, float s) {
+  uint32_t r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = e2m1x2_to_float2(w >> (8 * i));
+    r[i] = pack_bf16x2(f.x * s, f.y * s);
+  }
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+constexpr uint32_t kNoScale = 0;  // no entry here: zeros at any scale
 template <int FORMAT>
 struct Take;
 template <>
@@ -205,6 +212,7 @@ struct Take<CSA_CACHE_E4M3> {
   static __device__ __forceinline__ int column(int t) { return (t & 3) * 32; }
   uint4 a, b;
   uint32_t k;
+  bool some;
   __device__ __forceinline__ void load(const AttnParams& p, int64_t at, int col) {
     a = b = make_uint4(0, 0, 0, 0);
     load_scale(p, at, col);
@@ -216,35 +224,39 @@ struct Take<CSA_CACHE_E4M3> {
   }
   // the scale alone (none: -1), then the codes from a copied pair (128 bytes an entry)
   __device__ __forceinline__ void load_scale(const AttnParams& p, int64_t at, int col) {
-    k = at >= 0 && col < p.d ? __ldg(p.scales + (at >> 5) + (col >> 5)) : kNoScale;
+    some = at >= 0 && col < p.d;
+    k = some ? __ldg(p.scales + (at >> 5) + (col >> 5)) : kNoScale;
   }
   __device__ __forceinline__ void load_codes(uint32_t raw, int row, int t) {
     a = b = make_uint4(0, 0, 0, 0);
-    if (k != kNoScale) {
+    if (some) {
       a = lds128(raw + row * 128 + (t & 3) * 32);
       b = lds128(raw + row * 128 + (t & 3) * 32 + 16);
     }
   }
   // 8 codes
-  static __device__ __forceinline__ uint4 widen(const Widen& s, uint32_t x, uint32_t y) {
-    const uint2 u = s.four(x), v = s.four(y);
-    uint4 r = make_uint4(u.x, u.y, v.x, v.y);
-    if (e4m3_nans(x) | e4m3_nans(y)) {
-      r.x = nan_where(r.x, x, 0);
-      r.y = nan_where(r.y, x, 2);
-      r.z = nan_where(r.z, y, 0);
-      r.w = nan_where(r.w, y, 2);
-    }
-    return r;
+  static __device__ __forceinline__ uint4 widen(uint32_t k, uint32_t x, uint32_t y) {
+    return Widen<CSA_CACHE_E4M3>::plain(k) && (e4m3_nans(x) | e4m3_nans(y)) == 0
+               ? Widen<CSA_CACHE_E4M3>(k).eight(x, y)
+               : widen_any(x, y, scale_value(k));
   }
-  static constexpr int kLift = 120;
   __device__ __forceinline__ void store(uint32_t pair, int row, int t) const {
-    const Widen s = Widen::of<kLift>(k);
     const bool swap = (t & 2) != 0;
     const uint4 u = swap ? b : a, v = swap ? a : b;
-    store_pieces(pair, row, t, [&](int i) {
-      return i == 0 ? widen(s, u.x, u.y) : i == 1 ? widen(s, u.z, u.w) : i == 2 ? widen(s, v.x, v.y) : widen(s, v.z, v.w);
-    });
+    const uint32_t nans = e4m3_nans(a.x) | e4m3_nans(a.y) | e4m3_nans(a.z) | e4m3_nans(a.w) | e4m3_nans(b.x) |
+                          e4m3_nans(b.y) | e4m3_nans(b.z) | e4m3_nans(b.w);
+    auto pieces = [&](auto w) {
+      store_pieces(pair, row, t, [&](int i) {
+        return i == 0 ? w(u.x, u.y) : i == 1 ? w(u.z, u.w) : i == 2 ? w(v.x, v.y) : w(v.z, v.w);
+      });
+    };
+    if (Widen<CSA_CACHE_E4M3>::plain(k) && nans == 0) {
+      const Widen<CSA_CACHE_E4M3> s(k);
+      pieces([&](uint32_t x, uint32_t y) { return s.eight(x, y); });
+    } else {
+      const float s = scale_value(k);
+      pieces([&](uint32_t x, uint32_t y) { return widen_any(x, y, s); });
+    }
   }
 };
 template <>
@@ -255,23 +267,35 @@ struct Take<CSA_CACHE_E2M1> {
   static __device__ __forceinline__ int column(int t) { return (t & 3) * 32; }
   uint4 a;
   uint32_t k;
+  bool some;
   __device__ __forceinline__ void load(const AttnParams& p, int64_t at, int col) {
     a = make_uint4(0, 0, 0, 0);
     load_scale(p, at, col);
     if (at >= 0 && col < p.d) a = __ldg(reinterpret_cast<const uint4*>(p.data + at + (col >> 1)));
   }
   __device__ __forceinline__ void load_scale(const AttnParams& p, int64_t at, int col) {
-    k = at >= 0 && col < p.d ? __ldg(p.scales + (at >> 4) + (col >> 5)) : kNoScale;
+    some = at >= 0 && col < p.d;
+    k = some ? __ldg(p.scales + (at >> 4) + (col >> 5)) : kNoScale;
   }
   __device__ __forceinline__ void load_codes(uint32_t raw, int row, int t) {  // 64 bytes an entry
-    a = k != kNoScale ? lds128(raw + row * 64 + (t & 3) * 16) : make_uint4(0, 0, 0, 0);
+    a = some ? lds128(raw + row * 64 + (t & 3) * 16) : make_uint4(0, 0, 0, 0);
   }
-  static constexpr int kLift = 126;
+  static __device__ __forceinline__ uint4 widen(uint32_t k, uint32_t x) {
+    return Widen<CSA_CACHE_E2M1>::plain(k) ? Widen<CSA_CACHE_E2M1>(k).eight(x) : widen_any(x, scale_value(k));
+  }
   __device__ __forceinline__ void store(uint32_t pair, int row, int t) const {
-    const Widen s = Widen::of<kLift>(k);
     const bool swap = (t & 2) != 0;
     const uint4 u = swap ? make_uint4(a.z, a.w, a.x, a.y) : a;
-    store_pieces(pair, row, t, [&](int i) { return s.eight(i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w); });
+    auto pieces = [&](auto w) {
+      store_pieces(pair, row, t, [&](int i) { return w(i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w); });
+    };
+    if (Widen<CSA_CACHE_E2M1>::plain(k)) {
+      const Widen<CSA_CACHE_E2M1> s(k);
+      pieces([&](uint32_t x) { return s.eight(x); });
+    } else {
+      const float s = scale_value(k);
+      pieces([&](uint32_t x) { return widen_any(x, s); });
+    }
   }
 };
 
@@ -824,13 +848,12 @@ __global__ void __launch_bounds__(kPackThreads) attn_pack_kernel(const __grid_co
         if constexpr (FORMAT == CSA_CACHE_BF16) {
           v = __ldg(reinterpret_cast<const uint4*>(p.data + (entry * p.d + col) * 2));
         } else {
-          const Widen s = Widen::of<Take<FORMAT>::kLift>(
-              __ldg(p.scales + entry * (p.d / CSA_CACHE_GROUP) + col / CSA_CACHE_GROUP));
+          const uint32_t k = __ldg(p.scales + entry * (p.d / CSA_CACHE_GROUP) + col / CSA_CACHE_GROUP);
           if constexpr (FORMAT == CSA_CACHE_E4M3) {
             const uint2 w = __ldg(reinterpret_cast<const uint2*>(p.data + entry * p.d + col));
-            v = Take<FORMAT>::widen(s, w.x, w.y);
+            v = Take<FORMAT>::widen(k, w.x, w.y);
           } else {
-            v = s.eight(__ldg(reinterpret_cast<const uint32_t*>(p.data + entry * (p.d / 2) + col / 2)));
+            v = Take<FORMAT>::widen(k, __ldg(reinterpret_cast<const uint32_t*>(p.data + entry * (p.d / 2) + col / 2)));
           }
         }
       } else if (p.dev_error != nullptr) {
