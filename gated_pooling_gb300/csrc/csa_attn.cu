@@ -354,7 +354,8 @@ extern "C" csa_status_t csa_cache_attn(
   if (num_pages > INT64_MAX / 64 / page_size / (static_cast<int64_t>(kv_heads) * d))
     return CSA_ERR_UNSUPPORTED;
   if (cu_seqlens == nullptr || (S > 0 && entries == nullptr)) return CSA_ERR_INVALID_VALUE;
-  if (tokens > 0 && (q == nullptr || out == nullptr)) return CSA_ERR_INVALID_VALUE;
+  if (tokens > 0 && (q == nullptr || out == nullptr || !separate(tokens, q_heads, d, out_row_stride, out_head_stride)))
+    return CSA_ERR_INVALID_VALUE;
   if (S > 0 && max_pages > 0 && page_table == nullptr) return CSA_ERR_INVALID_VALUE;
   if (num_pages > 0 && (data == nullptr || (format != CSA_CACHE_BF16 && scales == nullptr)))
     return CSA_ERR_INVALID_VALUE;
@@ -472,9 +473,15 @@ extern "C" csa_status_t csa_cache_attn(
     if (blocks_per_sm(dev, k, threads, smem, &bps) != cudaSuccess) return CSA_ERR_CUDA;
     if (bps < 1) return CSA_ERR_UNSUPPORTED;
     const int cluster = chunks ? 2 : 1;
-    if (chunks && launch_pdl(pack, dim3(p.packed_rows / kPackRows, S, kv_heads), dim3(kPackThreads), 0, cs, args) !=
-                      cudaSuccess)
-      return CSA_ERR_CUDA;
+    if (chunks) {
+      // a few blocks an SM, which go on to their sequence's next entries: the table's capacity may
+      // be far above what the sequences hold
+      const int64_t heads = static_cast<int64_t>(S) * kv_heads, most = p.packed_rows / kPackRows;
+      const int64_t want = (16 * static_cast<int64_t>(sms) + heads - 1) / heads;
+      if (launch_pdl(pack, dim3(static_cast<unsigned>(want < most ? want : most), S, kv_heads), dim3(kPackThreads), 0,
+                     cs, args) != cudaSuccess)
+        return CSA_ERR_CUDA;
+    }
     void* targs[] = {&p, &map};
     if (launch_pdl(k, dim3(p.workers * cluster), dim3(threads), smem, cs, targs, cluster) != cudaSuccess)
       return CSA_ERR_CUDA;

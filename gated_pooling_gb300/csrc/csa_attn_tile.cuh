@@ -823,44 +823,47 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
 // multiple of 128 rows and of 64 NC columns, so that the tile kernel's copies are whole boxes
 // whatever the format, the page size and the heads. Every unit of the sequence (one per 128
 // rows) reads them again; packing reads and writes them once. Block (x, s, cache head): 32
-// entries, a thread 8 columns at a time.
+// entries at a time, a thread 8 columns at a time.
 constexpr int kPackThreads = 256, kPackRows = 32;
 template <int NC, int FORMAT>
 __global__ void __launch_bounds__(kPackThreads) attn_pack_kernel(const __grid_constant__ AttnParams p) {
   constexpr int kPer = NC * 8;  // pieces of 8 columns
   pdl_wait();
   if (*p.status != 0) return;
-  const int seq = blockIdx.y, kvh = blockIdx.z, e0 = blockIdx.x * kPackRows;
+  const int seq = blockIdx.y, kvh = blockIdx.z;
   const int rows = sequence_rows(p, seq);
   if (rows == 0) return;
   const int64_t first = p.first != nullptr ? __ldg(p.first + seq) : 0;
   const int n = visible(first + rows / p.group - 1, p.ratio, __ldg(p.entries + seq));
-  if (e0 >= (n + kAttnEntries - 1) / kAttnEntries * kAttnEntries && e0 >= kAttnEntries) return;
-  uint16_t* to = p.packed + ((static_cast<int64_t>(seq) * p.kv_heads + kvh) * p.packed_rows + e0) * (NC * 64);
+  const int end = max(kAttnEntries, (n + kAttnEntries - 1) / kAttnEntries * kAttnEntries);
+  uint16_t* all = p.packed + (static_cast<int64_t>(seq) * p.kv_heads + kvh) * p.packed_rows * (NC * 64);
+  for (int e0 = blockIdx.x * kPackRows; e0 < end; e0 += gridDim.x * kPackRows) {
+    uint16_t* to = all + static_cast<int64_t>(e0) * (NC * 64);
 #pragma unroll 4
-  for (int i = threadIdx.x; i < kPackRows * kPer; i += kPackThreads) {
-    const int r = i / kPer, col = (i % kPer) * 8, e = e0 + r;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (e < n && col < p.d) {
-      const int page = __ldg(p.table + static_cast<int64_t>(seq) * p.max_pages + e / p.page_size);
-      if (page >= 0 && page < p.num_pages) {
-        const int64_t entry = (static_cast<int64_t>(page) * p.page_size + e % p.page_size) * p.kv_heads + kvh;
-        if constexpr (FORMAT == CSA_CACHE_BF16) {
-          v = __ldg(reinterpret_cast<const uint4*>(p.data + (entry * p.d + col) * 2));
-        } else {
-          const uint32_t k = __ldg(p.scales + entry * (p.d / CSA_CACHE_GROUP) + col / CSA_CACHE_GROUP);
-          if constexpr (FORMAT == CSA_CACHE_E4M3) {
-            const uint2 w = __ldg(reinterpret_cast<const uint2*>(p.data + entry * p.d + col));
-            v = Take<FORMAT>::widen(k, w.x, w.y);
+    for (int i = threadIdx.x; i < kPackRows * kPer; i += kPackThreads) {
+      const int r = i / kPer, col = (i % kPer) * 8, e = e0 + r;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (e < n && col < p.d) {
+        const int page = __ldg(p.table + static_cast<int64_t>(seq) * p.max_pages + e / p.page_size);
+        if (page >= 0 && page < p.num_pages) {
+          const int64_t entry = (static_cast<int64_t>(page) * p.page_size + e % p.page_size) * p.kv_heads + kvh;
+          if constexpr (FORMAT == CSA_CACHE_BF16) {
+            v = __ldg(reinterpret_cast<const uint4*>(p.data + (entry * p.d + col) * 2));
           } else {
-            v = Take<FORMAT>::widen(k, __ldg(reinterpret_cast<const uint32_t*>(p.data + entry * (p.d / 2) + col / 2)));
+            const uint32_t k = __ldg(p.scales + entry * (p.d / CSA_CACHE_GROUP) + col / CSA_CACHE_GROUP);
+            if constexpr (FORMAT == CSA_CACHE_E4M3) {
+              const uint2 w = __ldg(reinterpret_cast<const uint2*>(p.data + entry * p.d + col));
+              v = Take<FORMAT>::widen(k, w.x, w.y);
+            } else {
+              v = Take<FORMAT>::widen(k, __ldg(reinterpret_cast<const uint32_t*>(p.data + entry * (p.d / 2) + col / 2)));
+            }
           }
+        } else if (p.dev_error != nullptr) {
+          *p.dev_error = CSA_DEVERR_PAGE;
         }
-      } else if (p.dev_error != nullptr) {
-        *p.dev_error = CSA_DEVERR_PAGE;
       }
+      *reinterpret_cast<uint4*>(to + r * (NC * 64) + col) = v;
     }
-    *reinterpret_cast<uint4*>(to + r * (NC * 64) + col) = v;
   }
 }
 

@@ -389,6 +389,7 @@ extern "C" csa_status_t csa_cache_read(const void* data, const uint8_t* scales, 
   const csa_status_t st = check_cache(out, dtype, rows, heads, d, out_row_stride, out_head_stride,
                                       slots, num_slots, format, data, scales, dev_error);
   if (st != CSA_OK || rows == 0) return st;
+  if (!separate(rows, heads, d, out_row_stride, out_head_stride)) return CSA_ERR_INVALID_VALUE;
   CacheParams p{};
   p.out = out;
   p.data = static_cast<uint8_t*>(const_cast<void*>(data));

@@ -47,6 +47,24 @@ auto by_dtype(int dtype, F f) {
                                    : f(std::integral_constant<int, CSA_DTYPE_FP32>{});
 }
 
+// Whether an output [rows, heads, d] with these strides writes every element to a place of its
+// own: the heads of a row (or the rows of a head) side by side, d columns each, and these
+// groups one behind another.
+inline bool separate(int64_t rows, int64_t heads, int64_t d, int64_t row_stride, int64_t head_stride) {
+  struct Axis {
+    int64_t n, stride;
+  } inner{heads, head_stride}, outer{rows, row_stride};
+  if (rows < 1) return true;
+  if (outer.n > 1 && (inner.n == 1 || outer.stride < inner.stride)) {
+    const Axis t = inner;
+    inner = outer;
+    outer = t;
+  }
+  if (inner.n > 1 && inner.stride < d) return false;
+  const __int128 span = static_cast<__int128>(inner.n - 1) * inner.stride + d;
+  return outer.n <= 1 || outer.stride >= span;
+}
+
 inline bool is_aligned(const void* p, uintptr_t a) {
   return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
 }

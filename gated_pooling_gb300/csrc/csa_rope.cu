@@ -707,7 +707,8 @@ extern "C" csa_status_t csa_norm_rope_fwd(const void* x, int32_t dtype, int64_t 
   const uintptr_t size = dtype_size(dtype);
   if (!is_aligned(x, size) || !is_aligned(y, size)) return CSA_ERR_INVALID_VALUE;
   if (rows == 0) return CSA_OK;
-  if (x == nullptr || y == nullptr) return CSA_ERR_INVALID_VALUE;
+  if (x == nullptr || y == nullptr || !separate(rows, heads, d, y_row_stride, y_head_stride))
+    return CSA_ERR_INVALID_VALUE;
   RopeParams p = rope_params(rows, heads, d, weight, norm, eps, positions, turns, rot_dim, rot_start,
                              layout, amplitude);
   p.x = x;
@@ -768,7 +769,8 @@ extern "C" csa_status_t csa_norm_rope_bwd(
   if (!is_aligned(x, size) || !is_aligned(dy, size) || !is_aligned(dx, size) ||
       !is_aligned(dweight, 4) || !is_aligned(workspace, 16))
     return CSA_ERR_INVALID_VALUE;
-  if (rows > 0 && ((norm != 0 && x == nullptr) || dy == nullptr || dx == nullptr))
+  if (rows > 0 && ((norm != 0 && x == nullptr) || dy == nullptr || dx == nullptr ||
+                   !separate(rows, heads, d, dx_row_stride, dx_head_stride)))
     return CSA_ERR_INVALID_VALUE;
   if (rows == 0 && (dweight == nullptr || accumulate_dweight != 0)) return CSA_OK;
   // the smallest partial is one row: refused before the device is asked

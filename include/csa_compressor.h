@@ -290,7 +290,8 @@ csa_status_t csa_rope_table(int32_t rot_dim, double base, int32_t scaling, doubl
  *   positions   int32 [rows] (device); NULL: every row is taken, needs rot_dim = 0
  *   turns       uint64 [rot_dim/2] (device), from csa_rope_table; NULL when rot_dim = 0
  * rows = 0 is a valid no-op. CSA_ERR_INVALID_VALUE for NULL or misaligned pointers, odd
- * rot_dim, rot_start + rot_dim > d, negative strides, eps negative or not finite;
+ * rot_dim, rot_start + rot_dim > d, negative strides, strides of y under which two elements
+ * share a place (an input may repeat: a stride of 0), eps negative or not finite;
  * CSA_ERR_UNSUPPORTED for d > CSA_MAX_HEAD_DIM, rows * heads >= 2^31 or an unknown dtype or
  * layout. The vector kernel runs when d, the strides and rot_start are multiples of 8
  * and rot_dim of 16 (half) or 8 (interleaved), and x and y (weight too) are 16-byte
@@ -359,7 +360,7 @@ csa_status_t csa_cache_write(const void* x, int32_t dtype, int64_t rows, int32_t
                              int32_t* dev_error, csa_stream_t stream);
 
 /* Reads rows of the cache back: out[r] = the entry in slots[r], in `dtype`, out [rows, heads,
- * d] with strides in elements. A negative slot leaves its row of out as it was, so does one
+ * d] with strides in elements that give every element a place of its own. A negative slot leaves its row of out as it was, so does one
  * >= num_slots, which reports CSA_DEVERR_SLOT. Any slot may be read by several rows. */
 csa_status_t csa_cache_read(const void* data, const uint8_t* scales, int32_t format,
                             const int64_t* slots, int64_t rows, int64_t num_slots, int32_t heads,
@@ -401,8 +402,9 @@ size_t csa_cache_attn_workspace_bytes(int32_t S, int64_t tokens, int32_t q_heads
  *   workspace   at least csa_cache_attn_workspace_bytes(...) bytes, 16-byte aligned
  *               (CSA_ERR_WORKSPACE otherwise); calls that may run at the same time need
  *               workspaces of their own
- * CSA_ERR_INVALID_VALUE: NULL or misaligned pointers, q_heads not a multiple of kv_heads,
- * negative sizes or strides, softmax_scale not finite. CSA_ERR_UNSUPPORTED: d >
+ * out and lse overlap no input. CSA_ERR_INVALID_VALUE: NULL or misaligned pointers, q_heads not a
+ * multiple of kv_heads, negative sizes or strides, strides of out under which two elements share
+ * a place, softmax_scale not finite. CSA_ERR_UNSUPPORTED: d >
  * CSA_MAX_HEAD_DIM, quantised formats with d not a multiple of 32, S > CSA_MAX_SEGMENTS,
  * tokens * q_heads or max_pages * page_size >= 2^31, an unknown format. A bad
  * cu_seqlens or entries (CSA_DEVERR_CU_SEQLENS, CSA_DEVERR_ENTRIES) skips all outputs; after

@@ -324,3 +324,46 @@ def test_streams_apart(cuda_lib):
     torch.cuda.synchronize()
     for r, w, c in zip(runs, want, cases):
         assert torch.equal(r[3][21][:c.cu[-1]], w[:c.cu[-1]])
+
+
+@pytest.mark.parametrize("fmt", [R.BF16, R.E4M3, R.FP4])
+@pytest.mark.parametrize("H,kv,d,lens,entries,ratio", [
+    (64, 1, 512, [70, 5, 0, 33], [530, 40, 9, 260], 4),   # units of 128 rows over several tiles, split over pairs
+    (64, 1, 512, [9], [1500], 1),                         # few units: every unit in many pieces
+    (16, 2, 128, [130, 3], [900, 400], 1),
+    (8, 2, 256, [65, 64], [300, 129], 2),
+    (20, 1, 192, [40], [700], 0),
+    (24, 1, 64, [33, 90], [128, 1024], 1),
+    (128, 1, 320, [3, 2], [257, 640], 0)])
+def test_long_chunks(cuda_lib, fmt, H, kv, d, lens, entries, ratio):
+    """Chunks long enough for packed entries and pairs of blocks, every format, odd row counts."""
+    Case(lens, entries, H, kv, d, fmt, page=48, ratio=ratio, first="end", sink=True, seed=d + H).check(cuda_lib)
+
+
+def test_many_sequences(cuda_lib):
+    """The most sequences a call takes, most of them with a token and a few entries."""
+    S = 16384
+    g = torch.Generator().manual_seed(4)
+    lens = torch.randint(0, 2, (S,), generator=g).tolist()
+    entries = torch.randint(0, 6, (S,), generator=g).tolist()
+    c = Case(lens, entries, 2, 1, 64, page=4, ratio=0, seed=3)
+    out, lse, err = c.run(cuda_lib)
+    assert err == 0
+    some = [s for s in range(S) if lens[s]][::97] + [s for s in range(S) if lens[s]][-3:]
+    for s in some:
+        t, n = c.cu[s], entries[s]
+        e = torch.arange(n)
+        k = c.values[c.table[s].long()[e // 4] * 4 + e % 4, 0]
+        x = c.q[t].double() @ k.T * c.scale
+        want = torch.softmax(x, -1) @ k if n else torch.zeros(2, 64, dtype=torch.float64)
+        # weights and output rounded to 16 bits (2^-8 each), scores of 64 fp32 products
+        assert ((out[t].double().cpu() - want).abs() <= 2.1 * 2.0 ** -8 * (torch.softmax(x, -1) @ k.abs() if n else 1e-9)).all(), s
+
+
+def test_a_table_much_larger_than_its_sequences(cuda_lib):
+    """Chunks whose table could hold far more entries than there are."""
+    c = Case([40, 30], [200, 90], 16, 1, 128, page=64, ratio=1, first="end", seed=6)
+    wide = torch.full((2, 4000), -5, dtype=torch.int32)
+    wide[:, :c.table.shape[1]] = c.table
+    c.table, c.max_pages = wide, 4000
+    c.check(cuda_lib)

@@ -107,6 +107,9 @@ ROPE_BOTH = [
     (dict(norm=0), INVALID),  # a weight without a norm
     (dict(y=None), INVALID), (dict(y=FAKE + 1), INVALID), (dict(yr=-1), INVALID), (dict(yh=-1), INVALID),
     (dict(rows=0), OK), (dict(rows=0, x=None, y=None, pos=None, turns=None), OK),
+    # outputs whose elements would share a place
+    (dict(yh=63), INVALID), (dict(yr=127), INVALID), (dict(yr=0), INVALID), (dict(yh=0), INVALID),
+    (dict(yr=64, yh=255), INVALID), (dict(yr=1 << 62, yh=63), INVALID),
 ])
 def test_rope_fwd_refusals(lib, over, code):
     assert rope_fwd(lib, **over) == code
@@ -119,6 +122,7 @@ def test_rope_fwd_refusals(lib, over, code):
     (dict(ws=FAKE + 8), INVALID), (dict(gr=-1), INVALID), (dict(gh=-1), INVALID), (dict(dr=-1), INVALID),
     (dict(dh=-1), INVALID), (dict(ws=None), WORKSPACE), (dict(nb=255), WORKSPACE),
     (dict(rows=0, dw=None), OK), (dict(rows=0, acc=1), OK),
+    (dict(dh=63), INVALID), (dict(dr=127), INVALID), (dict(dr=0), INVALID), (dict(dr=64, dh=255), INVALID),
 ])
 def test_rope_bwd_refusals(lib, over, code):
     assert rope_bwd(lib, **over) == code
@@ -159,6 +163,11 @@ def test_cache_refusals(lib, call, over, code):
     assert call(lib, **over) == code
 
 
+@pytest.mark.parametrize("over", [dict(xh=63), dict(xr=127), dict(xr=0), dict(xh=0), dict(xr=64, xh=255)])
+def test_cache_read_refuses_overlapping_rows(lib, over):
+    assert cache_read(lib, **over) == INVALID
+
+
 # -------------------------------------------------------------------------------- attention
 def attn(lib, **over):
     a = dict(q=FAKE, qr=128, qh=64, cu=FAKE, S=2, tokens=4, H=2, kv=1, d=64, data=FAKE, scales=FAKE, fmt=1,
@@ -184,6 +193,7 @@ def attn(lib, **over):
     (dict(tokens=1 << 30), UNSUPPORTED), (dict(max_pages=1 << 30), UNSUPPORTED),
     (dict(num_pages=1 << 60), UNSUPPORTED), (dict(ws=None), WORKSPACE), (dict(nb=8), WORKSPACE),
     (dict(S=0), OK), (dict(tokens=0), OK), (dict(tokens=0, q=None, out=None), OK),
+    (dict(outh=63), INVALID), (dict(outr=127), INVALID), (dict(outr=0), INVALID), (dict(outr=64, outh=255), INVALID),
 ])
 def test_attn_refusals(lib, over, code):
     assert attn(lib, **over) == code
