@@ -57,6 +57,9 @@ __device__ __forceinline__ int64_t plan_scan(int64_t v, int64_t* warps, int64_t&
 __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnParams p) {
   extern __shared__ int s_first[];  // [S + 1] first row block of each sequence
   __shared__ int64_t s_warps[32];
+  __shared__ int64_t s_tile[kPlanThreads + 1];  // first tiles of the units, where they are no more
+  __shared__ int s_joins;
+  if (threadIdx.x == 0) s_joins = 0;
   pdl_wait();
   int bad = 0;
   for (int s = threadIdx.x; s < p.S; s += kPlanThreads) {
@@ -67,7 +70,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnParams p) {
   const int cu_bad = __syncthreads_or(bad & 1), n_bad = __syncthreads_or(bad & 2);
   const int code = cu_bad ? CSA_DEVERR_CU_SEQLENS : n_bad ? CSA_DEVERR_ENTRIES : 0;
   if (threadIdx.x == 0) {
-    *p.status = code;
+    p.head->status = code;
     if (code != 0 && p.dev_error != nullptr) *p.dev_error = code;
   }
   if (code != 0 || p.units == nullptr) return;
@@ -102,47 +105,49 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnParams p) {
     if (i < units) {
       p.units[i] = u;
       p.unit_first[i] = first;
+      if (units <= kPlanThreads) s_tile[i] = first;
     }
     all += sum;
   }
   if (threadIdx.x == 0) {
     p.unit_first[units] = all;
-    *p.tiles = all;
+    if (units <= kPlanThreads) s_tile[units] = all;
+    p.head->tiles = all;
   }
   __syncthreads();
+  const int64_t* unit_first = units <= kPlanThreads ? s_tile : p.unit_first;
+  auto unit_of = [&](int64_t tile) {  // unit_first[l] <= tile < unit_first[h]
+    int64_t l = 0, h = units;
+    while (h - l > 1) {
+      const int64_t mid = (l + h) / 2;
+      if (unit_first[mid] <= tile) l = mid;
+      else h = mid;
+    }
+    return l;
+  };
   for (int i = threadIdx.x; i < p.workers; i += kPlanThreads) {
-    const int64_t t = attn_share(all, p.workers, i);
+    const int64_t t = attn_share(all, p.workers, i), next = attn_share(all, p.workers, i + 1);
     AttnStart start{};
-    const int64_t next = attn_share(all, p.workers, i + 1);
     start.left = static_cast<int32_t>(next - t);
-    if (start.left == 0) {
-      p.starts[i] = start;
-      continue;
-    }
-    int64_t l = 0, h = units;  // unit_first[l] <= t < unit_first[h]
-    while (h - l > 1) {
-      const int64_t mid = (l + h) / 2;
-      if (p.unit_first[mid] <= t) l = mid;
-      else h = mid;
-    }
-    start.u = p.units[l];
-    start.unit = static_cast<int32_t>(l);
-    start.tile = static_cast<int32_t>(t - p.unit_first[l]);
-    // the unit of the share's last tile: whether it begins here and goes on in later shares
-    h = units;
-    while (h - l > 1) {
-      const int64_t mid = (l + h) / 2;
-      if (p.unit_first[mid] < next) l = mid;
-      else h = mid;
-    }
-    const int64_t end = p.unit_first[l + 1];
-    if (p.unit_first[l] >= t && end > next) {
-      int last = i + 1;
-      while (last + 1 < p.workers && attn_share(all, p.workers, last + 1) < end) ++last;
-      start.pieces = last - i + 1;
+    if (start.left > 0) {
+      const int64_t l = unit_of(t);
+      start.u = p.units[l];
+      start.unit = static_cast<int32_t>(l);
+      start.tile = static_cast<int32_t>(t - unit_first[l]);
+      // a unit that begins in this share and goes on in later ones
+      const int64_t m = unit_of(next - 1), end = unit_first[m + 1];
+      if (unit_first[m] >= t && end > next) {
+        AttnJoin join{};
+        join.u = p.units[m];
+        join.worker = i;
+        join.pieces = attn_last_before(all, p.workers, end) - i + 1;
+        p.joins[atomicAdd(&s_joins, 1)] = join;  // (in any order: each is joined by itself)
+      }
     }
     p.starts[i] = start;
   }
+  __syncthreads();
+  if (threadIdx.x == 0) p.head->joins = s_joins;
 }
 
 // Scalar kernel, any d and alignment: a warp per new token and query head, a lane the columns
@@ -153,7 +158,7 @@ __global__ void __launch_bounds__(kScalarThreads) attn_scalar_kernel(AttnParams 
   using B = Element<CSA_DTYPE_BF16>;
   const int lane = threadIdx.x & 31;
   pdl_wait();
-  if (*p.status != 0) return;
+  if (p.head->status != 0) return;
   const int64_t u = (static_cast<int64_t>(blockIdx.x) * kScalarThreads + threadIdx.x) / 32;
   if (u >= p.tokens * p.q_heads) return;
   const int64_t t = u / p.q_heads;
@@ -254,7 +259,7 @@ csa_status_t check_attn_sizes(int32_t S, int64_t tokens, int32_t q_heads, int32_
   return CSA_OK;
 }
 
-constexpr size_t kStatusBytes = 16;
+constexpr size_t kStatusBytes = sizeof(AttnHead);
 constexpr int kTileMaxDim = 512;
 
 int tile_chunks(int d) { return d <= 128 ? 2 : d <= 256 ? 4 : 8; }
@@ -274,10 +279,9 @@ size_t lay_out(AttnParams& p, int sms, bool chunks, unsigned char* base) {
     at += (bytes + 255) & ~static_cast<size_t>(255);
     return r;
   };
-  unsigned char* head = take(kStatusBytes);
-  p.status = reinterpret_cast<int32_t*>(head);
-  p.tiles = base == nullptr ? nullptr : reinterpret_cast<int64_t*>(head + 8);
+  p.head = reinterpret_cast<AttnHead*>(take(kStatusBytes));
   p.starts = reinterpret_cast<AttnStart*>(take(sizeof(AttnStart) * sms));
+  p.joins = reinterpret_cast<AttnJoin*>(take(sizeof(AttnJoin) * sms));
   p.units = reinterpret_cast<AttnUnit*>(take(sizeof(AttnUnit) * p.max_units));
   p.unit_first = reinterpret_cast<int64_t*>(take(sizeof(int64_t) * (p.max_units + 1)));
   const size_t pieces = 2 * static_cast<size_t>(sms), dpad = tile_chunks(p.d) * 64;
@@ -378,7 +382,7 @@ extern "C" csa_status_t csa_cache_attn(
     if (workspace_bytes < lay_out(p, sms, chunked(p), nullptr)) return CSA_ERR_WORKSPACE;
     lay_out(p, sms, chunked(p), static_cast<unsigned char*>(workspace));
   } else {
-    p.status = static_cast<int32_t*>(workspace);
+    p.head = static_cast<AttnHead*>(workspace);
   }
   if (!tile) p.units = nullptr;
   const bool chunks = tile && chunked(p);
@@ -485,7 +489,7 @@ extern "C" csa_status_t csa_cache_attn(
     void* targs[] = {&p, &map};
     if (launch_pdl(k, dim3(p.workers * cluster), dim3(threads), smem, cs, targs, cluster) != cudaSuccess)
       return CSA_ERR_CUDA;
-    return launch_pdl(join, dim3(p.workers, cluster * kAttnRows / 4), dim3(join_threads), 0, cs, args) == cudaSuccess
+    return launch_pdl(join, dim3(p.workers * cluster * (kAttnRows / 4)), dim3(join_threads), 0, cs, args) == cudaSuccess
                ? CSA_OK
                : CSA_ERR_CUDA;
   }

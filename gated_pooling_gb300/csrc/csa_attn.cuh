@@ -27,10 +27,20 @@ struct alignas(16) AttnUnit {
 };
 struct alignas(16) AttnStart {  // a worker's share: its first unit, the tile there, and how many tiles
   AttnUnit u;
-  int32_t unit, tile, left;
-  int32_t pieces;  // workers that share the unit which begins here and ends elsewhere (0: none)
+  int32_t unit, tile, left, pad;
 };
-static_assert(sizeof(AttnUnit) == 48 && sizeof(AttnStart) == 64, "read in 16-byte pieces");
+struct alignas(16) AttnJoin {  // a unit whose tiles several workers share, from `worker` on
+  AttnUnit u;
+  int32_t worker, pieces;
+  int32_t pad[2];
+};
+struct alignas(16) AttnHead {
+  int32_t status;  // 0, or why the call's lengths were refused
+  int32_t joins;   // shared units
+  int64_t tiles;   // all units' tiles
+};
+static_assert(sizeof(AttnUnit) == 48 && sizeof(AttnStart) == 64 && sizeof(AttnJoin) == 64 && sizeof(AttnHead) == 16,
+              "read in 16-byte pieces");
 
 struct AttnParams {
   const uint16_t* q;
@@ -45,9 +55,9 @@ struct AttnParams {
   float* lse;
   int32_t* dev_error;
   // workspace
-  int32_t* status;      // 0, or why the call's lengths were refused
-  int64_t* tiles;       // all units' tiles
+  AttnHead* head;
   AttnStart* starts;    // [workers]
+  AttnJoin* joins;      // [workers]
   AttnUnit* units;      // [max_units]
   int64_t* unit_first;  // [max_units + 1]: first tile of each unit
   float* part_o;        // [2 workers][CTAs of one][64 x dpad]: sums of the pieces of shared units
@@ -93,6 +103,12 @@ __device__ __forceinline__ AttnUnit make_unit(const AttnParams& p, int s, int kv
 __device__ __forceinline__ int64_t attn_share(int64_t tiles, int workers, int i) {
   const int64_t n = tiles < workers ? tiles : workers;
   return i >= n ? tiles : tiles * i / n;
+}
+// Last worker whose share begins before tile `end` (0 < end <= tiles): the largest k with tiles k / n
+// < end.
+__device__ __forceinline__ int attn_last_before(int64_t tiles, int workers, int64_t end) {
+  const int64_t n = tiles < workers ? tiles : workers;
+  return static_cast<int>((end * n + tiles - 1) / tiles) - 1;
 }
 
 }  // namespace csa

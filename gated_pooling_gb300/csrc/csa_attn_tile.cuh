@@ -432,7 +432,10 @@ __device__ void tile_fetch(const AttnParams& p, TileSmall& sm, uint32_t base) {
 #pragma unroll
       for (int i = 0; i < P::kRows; ++i)
         v[i].load_codes(base + ring.slot * kPairBytes + kChunkBytes, P::first_row(gt) + i * P::kRowStep, gt);
-      named_barrier(6 + group, kGroup);  // the codes are in registers: their place is written over
+      // The codes are in registers, and their place is written over: an 8-bit entry's is its own row's,
+      // read by four lanes of one warp; 4-bit ones lie two to a row.
+      if (TileCta<SRC>::kFormat == CSA_CACHE_E4M3) __syncwarp();
+      else named_barrier(6 + group, kGroup);
     } else {
 #pragma unroll
       for (int i = 0; i < P::kRows; ++i) v[i].load(p, at[i * P::kRowStep], col);
@@ -829,7 +832,7 @@ template <int NC, int FORMAT>
 __global__ void __launch_bounds__(kPackThreads) attn_pack_kernel(const __grid_constant__ AttnParams p) {
   constexpr int kPer = NC * 8;  // pieces of 8 columns
   pdl_wait();
-  if (*p.status != 0) return;
+  if (p.head->status != 0) return;
   const int seq = blockIdx.y, kvh = blockIdx.z;
   const int rows = sequence_rows(p, seq);
   if (rows == 0) return;
@@ -900,7 +903,7 @@ __global__ void __launch_bounds__(TileCta<SRC>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
   pdl_wait();
-  const bool run = *p.status == 0;
+  const bool run = p.head->status == 0;
   if constexpr (CTA::kByThreads) {
     if (warp >= kTileFirstLoader) {
       regs_up<kLoadRegs>();
@@ -926,110 +929,105 @@ __global__ void __launch_bounds__(TileCta<SRC>::kThreads, 1)
   if (warp == 0) tmem_free(tmem, SH::kTmemColumns);
 }
 
-// Joins the pieces of the units that workers share: block (i, y) the rows 4y .. 4y + 3 of the unit
-// whose first piece is worker i's last one. Lane k of every warp holds piece k's weights for the
-// four rows (32 pieces at a time); a warp adds up 32 or 64 columns of them.
+// Joins the pieces of the units that workers share, four rows at a time: the blocks take (unit, four
+// rows) in turn. Lane k of every warp holds piece k's weights for the four rows (32 pieces at a
+// time); a warp adds up 32 columns of them, eight pieces' loads under way.
 template <int NC>
 struct JoinShape {
-  static constexpr int kColumnBlocks = NC * 2;  // of 32 columns
-  static constexpr int kWarps = kColumnBlocks < 8 ? kColumnBlocks : 8;
-  static constexpr int kPer = kColumnBlocks / kWarps;
+  static constexpr int kWarps = NC * 2;  // of 32 columns
 };
 template <int NC, int CL>
 __global__ void __launch_bounds__(JoinShape<NC>::kWarps * 32) attn_join_kernel(const __grid_constant__ AttnParams p) {
   using SH = TileShape<NC>;
-  using JS = JoinShape<NC>;
-  pdl_wait();
-  if (*p.status != 0) return;
-  const int i = blockIdx.x;
-  const int n = p.starts[i].pieces;
-  if (n == 0) return;
-  const AttnUnit u = p.starts[i + 1].u;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = blockIdx.y / (kAttnRows / 4), quarter = blockIdx.y % (kAttnRows / 4);
-  const int r0 = quarter * 4, row0 = (u.block * CL + rank) * kAttnRows + r0;
-  if (row0 >= u.rows) return;
-  auto slot = [&](int k) { return (2 * static_cast<int64_t>(i + k) + (k == 0 ? 1 : 0)) * CL + rank; };
-
-  float sink_e[4], mx[4], den[4], acc[JS::kPer][4];
-  bool some[4];
-#pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int row = row0 + r;
-    sink_e[r] = p.sink != nullptr && row < u.rows ? p.sink[u.kvh * p.group + row % p.group] : -INFINITY;
-    mx[r] = sink_e[r] * kLog2e;
-    some[r] = false;
-    for (int b = 0; b < JS::kPer; ++b) acc[b][r] = 0.f;
-  }
-  auto read = [&](int k, float (&m)[4], float (&z)[4]) {
-    const float* ml = p.part_ml + slot(k) * 2 * kAttnRows + r0;
-    const float4 a = *reinterpret_cast<const float4*>(ml), b = *reinterpret_cast<const float4*>(ml + kAttnRows);
-    m[0] = a.x, m[1] = a.y, m[2] = a.z, m[3] = a.w;
-    z[0] = b.x, z[1] = b.y, z[2] = b.z, z[3] = b.w;
-  };
-  for (int k = lane; k < n; k += 32) {
-    float m[4], z[4];
-    read(k, m, z);
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-      if (!(z[r] <= 0.f)) {
-        mx[r] = fmaxf(mx[r], m[r]);
-        some[r] = true;
-      }
-  }
-#pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    mx[r] = warp_max_f32(mx[r]);
-    some[r] = __any_sync(0xFFFFFFFFu, some[r]);
-    den[r] = 0.f;
-  }
-  const float4* o = reinterpret_cast<const float4*>(p.part_o);
+  constexpr int kParts = CL * kAttnRows / 4;  // of a unit
   constexpr int kPiece = kAttnRows * SH::kDpad / 4;
-  for (int k0 = 0; k0 < n; k0 += 32) {
-    float f[4] = {0.f, 0.f, 0.f, 0.f};
-    if (k0 + lane < n) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_wait();
+  const int4 head = *reinterpret_cast<const int4*>(p.head);
+  if (head.x != 0) return;
+  for (int item = blockIdx.x; item < head.y * kParts; item += gridDim.x) {
+    const AttnJoin& J = p.joins[item / kParts];
+    const int rank = item % kParts / (kAttnRows / 4), quarter = item % (kAttnRows / 4);
+    const AttnUnit u = J.u;
+    const int i = J.worker, n = J.pieces;
+    const int r0 = quarter * 4, row0 = (u.block * CL + rank) * kAttnRows + r0;
+    if (row0 >= u.rows) continue;
+    auto slot = [&](int k) { return (2 * static_cast<int64_t>(i + k) + (k == 0 ? 1 : 0)) * CL + rank; };
+
+    float sink_e[4], mx[4], den[4], acc[4];
+    bool some[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = row0 + r;
+      sink_e[r] = p.sink != nullptr && row < u.rows ? p.sink[u.kvh * p.group + row % p.group] : -INFINITY;
+      mx[r] = sink_e[r] * kLog2e;
+      some[r] = false;
+      den[r] = acc[r] = 0.f;
+    }
+    auto read = [&](int k, float (&m)[4], float (&z)[4]) {
+      const float* ml = p.part_ml + slot(k) * 2 * kAttnRows + r0;
+      const float4 a = *reinterpret_cast<const float4*>(ml), b = *reinterpret_cast<const float4*>(ml + kAttnRows);
+      m[0] = a.x, m[1] = a.y, m[2] = a.z, m[3] = a.w;
+      z[0] = b.x, z[1] = b.y, z[2] = b.z, z[3] = b.w;
+    };
+    for (int k = lane; k < n; k += 32) {
       float m[4], z[4];
-      read(k0 + lane, m, z);
+      read(k, m, z);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        f[r] = mx[r] == -INFINITY ? 0.f : fast_exp2(m[r] - mx[r]);
-        den[r] += f[r] * z[r];
+      for (int r = 0; r < 4; ++r)
+        if (!(z[r] <= 0.f)) {
+          mx[r] = fmaxf(mx[r], m[r]);
+          some[r] = true;
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      mx[r] = warp_max_f32(mx[r]);
+      some[r] = __any_sync(0xFFFFFFFFu, some[r]);
+    }
+    const float4* o = reinterpret_cast<const float4*>(p.part_o) + (warp * (kAttnRows / 4) + quarter) * 32 + lane;
+    for (int k0 = 0; k0 < n; k0 += 32) {
+      float f[4] = {0.f, 0.f, 0.f, 0.f};
+      if (k0 + lane < n) {
+        float m[4], z[4];
+        read(k0 + lane, m, z);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          f[r] = mx[r] == -INFINITY ? 0.f : fast_exp2(m[r] - mx[r]);
+          den[r] += f[r] * z[r];
+        }
+      }
+      const int some_k = min(32, n - k0);
+#pragma unroll 1
+      for (int k1 = 0; k1 < some_k; k1 += 8) {
+        float4 v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          v[k] = k1 + k < some_k ? o[slot(k0 + k1 + k) * kPiece] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          acc[0] = fmaf(__shfl_sync(0xFFFFFFFFu, f[0], k1 + k), v[k].x, acc[0]);
+          acc[1] = fmaf(__shfl_sync(0xFFFFFFFFu, f[1], k1 + k), v[k].y, acc[1]);
+          acc[2] = fmaf(__shfl_sync(0xFFFFFFFFu, f[2], k1 + k), v[k].z, acc[2]);
+          acc[3] = fmaf(__shfl_sync(0xFFFFFFFFu, f[3], k1 + k), v[k].w, acc[3]);
+        }
       }
     }
-    const int some_k = min(32, n - k0);
-#pragma unroll 4
-    for (int k = 0; k < some_k; ++k) {
-      float g[4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) g[r] = __shfl_sync(0xFFFFFFFFu, f[r], k);
+    for (int r = 0; r < 4; ++r) {
+      const int row = row0 + r;
 #pragma unroll
-      for (int b = 0; b < JS::kPer; ++b) {
-        const float4 v = o[slot(k0 + k) * kPiece + ((warp * JS::kPer + b) * (kAttnRows / 4) + quarter) * 32 + lane];
-        acc[b][0] = fmaf(g[0], v.x, acc[b][0]);
-        acc[b][1] = fmaf(g[1], v.y, acc[b][1]);
-        acc[b][2] = fmaf(g[2], v.z, acc[b][2]);
-        acc[b][3] = fmaf(g[3], v.w, acc[b][3]);
-      }
+      for (int s = 16; s > 0; s >>= 1) den[r] += __shfl_xor_sync(0xFFFFFFFFu, den[r], s);
+      if (row >= u.rows) continue;
+      const int head_of = u.kvh * p.group + row % p.group;
+      const int64_t token = static_cast<int64_t>(u.token) + row / p.group;
+      const float all = mx[r] == -INFINITY ? 1.f : den[r] + fast_exp2(sink_e[r] * kLog2e - mx[r]);
+      const int col = warp * 32 + lane;
+      if (col < p.d)
+        p.out[token * p.out_row + head_of * p.out_head + col] = Element<CSA_DTYPE_BF16>::from_float(acc[r] * (1.f / all));
+      if (p.lse != nullptr && warp == 0 && lane == 0)
+        p.lse[token * p.q_heads + head_of] = some[r] ? (mx[r] + log2f(all)) * kLn2 : sink_e[r];
     }
-  }
-#pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int row = row0 + r;
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) den[r] += __shfl_xor_sync(0xFFFFFFFFu, den[r], s);
-    if (row >= u.rows) continue;
-    const int head = u.kvh * p.group + row % p.group;
-    const int64_t token = static_cast<int64_t>(u.token) + row / p.group;
-    const float all = mx[r] == -INFINITY ? 1.f : den[r] + fast_exp2(sink_e[r] * kLog2e - mx[r]);
-    const float inv = 1.f / all;
-    uint16_t* out = p.out + token * p.out_row + head * p.out_head;
-#pragma unroll
-    for (int b = 0; b < JS::kPer; ++b) {
-      const int col = (warp * JS::kPer + b) * 32 + lane;
-      if (col < p.d) out[col] = Element<CSA_DTYPE_BF16>::from_float(acc[b][r] * inv);
-    }
-    if (p.lse != nullptr && warp == 0 && lane == 0)
-      p.lse[token * p.q_heads + head] = some[r] ? (mx[r] + log2f(all)) * kLn2 : sink_e[r];
   }
 }
 
