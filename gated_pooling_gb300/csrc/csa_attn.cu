@@ -53,31 +53,32 @@ __device__ __forceinline__ int64_t plan_scan(int64_t v, int64_t* warps, int64_t&
 }
 
 // One block: checks the call's lengths, publishes the verdict for the kernels behind it, and
-// (units wanted) lists the units, their first tiles and where each worker's share begins.
+// (units wanted) lists the units, where each worker's share begins, and the units that several
+// workers share.
 __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnParams p) {
   extern __shared__ int s_first[];  // [S + 1] first row block of each sequence
   __shared__ int64_t s_warps[32];
-  __shared__ int64_t s_tile[kPlanThreads + 1];  // first tiles of the units, where they are no more
+  __shared__ int64_t s_work[kPlanThreads + 1];  // where the units' work begins, if there are no more
   __shared__ int s_joins;
   if (threadIdx.x == 0) s_joins = 0;
   pdl_wait();
+  const int per = (p.S + kPlanThreads - 1) / kPlanThreads;
+  const int lo = min(p.S, static_cast<int>(threadIdx.x) * per), hi = min(p.S, lo + per);
   int bad = 0;
-  for (int s = threadIdx.x; s < p.S; s += kPlanThreads) {
-    const int32_t a = p.cu[s], b = p.cu[s + 1], n = p.entries[s];
+  int64_t mine = 0, blocks = 0;
+  for (int s = lo; s < hi; ++s) {
+    const int32_t a = __ldg(p.cu + s), b = __ldg(p.cu + s + 1), n = __ldg(p.entries + s);
     if (b < a || a < 0 || b > p.tokens) bad |= 1;
+    else mine += ((b - a) * p.group + p.unit_rows - 1) / p.unit_rows;
     if (n < 0 || n > p.max_entries) bad |= 2;
   }
-  const int cu_bad = __syncthreads_or(bad & 1), n_bad = __syncthreads_or(bad & 2);
-  const int code = cu_bad ? CSA_DEVERR_CU_SEQLENS : n_bad ? CSA_DEVERR_ENTRIES : 0;
+  int code = 0;
+  if (__syncthreads_or(bad)) code = __syncthreads_or(bad & 1) ? CSA_DEVERR_CU_SEQLENS : CSA_DEVERR_ENTRIES;
   if (threadIdx.x == 0) {
     p.head->status = code;
     if (code != 0 && p.dev_error != nullptr) *p.dev_error = code;
   }
   if (code != 0 || p.units == nullptr) return;
-  const int per = (p.S + kPlanThreads - 1) / kPlanThreads;
-  const int lo = min(p.S, static_cast<int>(threadIdx.x) * per), hi = min(p.S, lo + per);
-  int64_t mine = 0, blocks = 0;
-  for (int s = lo; s < hi; ++s) mine += (sequence_rows(p, s) + p.unit_rows - 1) / p.unit_rows;
   int64_t at = plan_scan(mine, s_warps, blocks);
   for (int s = lo; s < hi; ++s) {
     s_first[s] = static_cast<int>(at);
@@ -86,12 +87,13 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnParams p) {
   if (threadIdx.x == 0) s_first[p.S] = static_cast<int>(blocks);
   __syncthreads();
   const int64_t units = blocks * p.kv_heads;
+  const bool few = units <= kPlanThreads;
   int64_t all = 0;
   for (int64_t u0 = 0; u0 < units; u0 += kPlanThreads) {
     const int64_t i = u0 + threadIdx.x;
     AttnUnit u{};
     if (i < units) {
-      const int b = static_cast<int>(i / p.kv_heads);
+      const int b = static_cast<int>(units < INT_MAX ? static_cast<int>(i) / p.kv_heads : i / p.kv_heads);
       int l = 0, h = p.S;  // s_first[l] <= b < s_first[h]
       while (h - l > 1) {
         const int mid = (l + h) / 2;
@@ -101,46 +103,54 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnParams p) {
       u = make_unit(p, l, static_cast<int>(i - static_cast<int64_t>(b) * p.kv_heads), b - s_first[l]);
     }
     int64_t sum = 0;
-    const int64_t first = all + plan_scan(u.tiles, s_warps, sum);
+    const int64_t first = all + plan_scan(i < units ? u.tiles + 1 : 0, s_warps, sum);
     if (i < units) {
       p.units[i] = u;
       p.unit_first[i] = first;
-      if (units <= kPlanThreads) s_tile[i] = first;
+      if (few) s_work[i] = first;
     }
     all += sum;
   }
   if (threadIdx.x == 0) {
     p.unit_first[units] = all;
-    if (units <= kPlanThreads) s_tile[units] = all;
-    p.head->tiles = all;
+    if (few) s_work[units] = all;
   }
   __syncthreads();
-  const int64_t* unit_first = units <= kPlanThreads ? s_tile : p.unit_first;
-  auto unit_of = [&](int64_t tile) {  // unit_first[l] <= tile < unit_first[h]
-    int64_t l = 0, h = units;
+  const int64_t* work = few ? s_work : p.unit_first;
+  // the unit and tile that a place in the work stands for, and how many tiles lie before it
+  struct Place {
+    int64_t unit, tile, before;
+  };
+  auto place = [&](int64_t x) {
+    if (x >= all) return Place{units, 0, all - units};
+    int64_t l = 0, h = units;  // work[l] <= x < work[h]
     while (h - l > 1) {
       const int64_t mid = (l + h) / 2;
-      if (unit_first[mid] <= tile) l = mid;
+      if (work[mid] <= x) l = mid;
       else h = mid;
     }
-    return l;
+    const int64_t tile = x - work[l];
+    if (tile == work[l + 1] - work[l] - 1) return Place{l + 1, 0, x - l};  // behind the unit's last tile
+    return Place{l, tile, x - l};
   };
+  const AttnShares share(all, p.workers);
   for (int i = threadIdx.x; i < p.workers; i += kPlanThreads) {
-    const int64_t t = attn_share(all, p.workers, i), next = attn_share(all, p.workers, i + 1);
+    const Place a = place(share(i)), b = place(share(i + 1));
     AttnStart start{};
-    start.left = static_cast<int32_t>(next - t);
+    start.left = static_cast<int32_t>(b.before - a.before);
     if (start.left > 0) {
-      const int64_t l = unit_of(t);
-      start.u = p.units[l];
-      start.unit = static_cast<int32_t>(l);
-      start.tile = static_cast<int32_t>(t - unit_first[l]);
+      start.u = p.units[a.unit];
+      start.unit = static_cast<int32_t>(a.unit);
+      start.tile = static_cast<int32_t>(a.tile);
       // a unit that begins in this share and goes on in later ones
-      const int64_t m = unit_of(next - 1), end = unit_first[m + 1];
-      if (unit_first[m] >= t && end > next) {
+      if (b.tile > 0 && (b.unit > a.unit || a.tile == 0)) {
+        const int64_t end = work[b.unit + 1] - 1;
         AttnJoin join{};
-        join.u = p.units[m];
+        join.u = p.units[b.unit];
         join.worker = i;
-        join.pieces = attn_last_before(all, p.workers, end) - i + 1;
+        int last = i + 1;
+        while (share(last + 1) < end) ++last;
+        join.pieces = last - i + 1;
         p.joins[atomicAdd(&s_joins, 1)] = join;  // (in any order: each is joined by itself)
       }
     }
@@ -445,12 +455,13 @@ extern "C" csa_status_t csa_cache_attn(
       source = format == CSA_CACHE_BF16 ? kFromBoxes : format == CSA_CACHE_E4M3 ? kFromE4m3Boxes : kFromE2m1Boxes;
     }
     size_t smem = 0;
-    int threads = 0, join_threads = 0;
+    int threads = 0, join_threads = 0, join_items = 0;
     const void *k = nullptr, *join = nullptr, *pack = nullptr;
     by_chunks(nc, [&](auto c) {
       constexpr int NC = decltype(c)::value;
       smem = TileShape<NC>::kSmemBytes;
       join_threads = JoinShape<NC>::kWarps * 32;
+      join_items = JoinShape<NC>::kItems;
       auto use = [&](auto src) {
         constexpr int SRC = decltype(src)::value;
         k = reinterpret_cast<const void*>(attn_tile_kernel<NC, SRC>);
@@ -489,7 +500,7 @@ extern "C" csa_status_t csa_cache_attn(
     void* targs[] = {&p, &map};
     if (launch_pdl(k, dim3(p.workers * cluster), dim3(threads), smem, cs, targs, cluster) != cudaSuccess)
       return CSA_ERR_CUDA;
-    return launch_pdl(join, dim3(p.workers * cluster * (kAttnRows / 4)), dim3(join_threads), 0, cs, args) == cudaSuccess
+    return launch_pdl(join, dim3(p.workers * cluster * join_items), dim3(join_threads), 0, cs, args) == cudaSuccess
                ? CSA_OK
                : CSA_ERR_CUDA;
   }

@@ -2,6 +2,7 @@
 // visibility rule, and the work list that the plan kernel leaves in the workspace.
 #pragma once
 
+#include <climits>
 #include <stdint.h>
 
 #include "csa_compressor.h"
@@ -14,8 +15,8 @@ constexpr int kAttnEntries = 128;  // entries of a tile
 
 // A unit is up to unit_rows (64, or 128 for a pair of CTAs) consecutive rows (token, head of the
 // group) of one sequence and cache head; its work is a run of tiles of 128 entries, at least
-// one. The tiles of all units in order are split evenly over the workers, CTAs or pairs of
-// them (attn_share).
+// one. The work of all units in order is split evenly over the workers, CTAs or pairs of them
+// (AttnShares).
 struct alignas(16) AttnUnit {
   int32_t s, kvh, block, tiles;
   int32_t token, rows;  // the sequence's first token, and its rows
@@ -37,7 +38,7 @@ struct alignas(16) AttnJoin {  // a unit whose tiles several workers share, from
 struct alignas(16) AttnHead {
   int32_t status;  // 0, or why the call's lengths were refused
   int32_t joins;   // shared units
-  int64_t tiles;   // all units' tiles
+  int32_t pad[2];
 };
 static_assert(sizeof(AttnUnit) == 48 && sizeof(AttnStart) == 64 && sizeof(AttnJoin) == 64 && sizeof(AttnHead) == 16,
               "read in 16-byte pieces");
@@ -59,7 +60,7 @@ struct AttnParams {
   AttnStart* starts;    // [workers]
   AttnJoin* joins;      // [workers]
   AttnUnit* units;      // [max_units]
-  int64_t* unit_first;  // [max_units + 1]: first tile of each unit
+  int64_t* unit_first;  // [max_units + 1]: where each unit's work begins
   float* part_o;        // [2 workers][CTAs of one][64 x dpad]: sums of the pieces of shared units
   float* part_ml;       // likewise [2][64]: their maxima (in log2) and weight sums
   uint16_t* packed;     // chunks: the sequences' entries as bf16 rows [S][kv_heads][packed_rows][dpad]
@@ -75,8 +76,10 @@ struct AttnParams {
 // Entries that the token at position pos sees, of a sequence's n.
 __device__ __forceinline__ int visible(int64_t pos, int ratio, int n) {
   if (ratio == 0) return n;
-  const int64_t done = pos + 1 <= 0 ? 0 : (pos + 1) / ratio;
-  return done < n ? static_cast<int>(done) : n;
+  if (pos < 0) return 0;
+  const uint64_t done = pos < 0xFFFFFFFFll ? static_cast<uint32_t>(pos + 1) / static_cast<uint32_t>(ratio)
+                                           : static_cast<uint64_t>(pos + 1) / static_cast<uint32_t>(ratio);
+  return done < static_cast<uint64_t>(n) ? static_cast<int>(done) : n;
 }
 // Rows of a sequence and cache head (below 2^31: tokens * q_heads is).
 __device__ __forceinline__ int sequence_rows(const AttnParams& p, int s) {
@@ -99,16 +102,20 @@ __device__ __forceinline__ AttnUnit make_unit(const AttnParams& p, int s, int kv
   return u;
 }
 
-// First tile of worker i's share of all tiles; at most one worker per tile.
-__device__ __forceinline__ int64_t attn_share(int64_t tiles, int workers, int i) {
-  const int64_t n = tiles < workers ? tiles : workers;
-  return i >= n ? tiles : tiles * i / n;
-}
-// Last worker whose share begins before tile `end` (0 < end <= tiles): the largest k with tiles k / n
-// < end.
-__device__ __forceinline__ int attn_last_before(int64_t tiles, int workers, int64_t end) {
-  const int64_t n = tiles < workers ? tiles : workers;
-  return static_cast<int>((end * n + tiles - 1) / tiles) - 1;
-}
+// Worker i's share of the work, a unit counting its tiles and one more (loading q, bringing the
+// output out): [share(i), share(i + 1)) of n = min(work, workers) equal ones.
+struct AttnShares {
+  int64_t work, q;
+  int n, r;
+  __device__ __forceinline__ AttnShares(int64_t w, int workers) : work(w) {
+    n = w < workers ? static_cast<int>(w) : workers;
+    const int d = n > 0 ? n : 1;
+    q = w < INT_MAX ? static_cast<int>(w) / d : w / d;
+    r = static_cast<int>(w - q * d);
+  }
+  __device__ __forceinline__ int64_t operator()(int i) const {
+    return i >= n ? work : q * i + static_cast<int>(static_cast<uint32_t>(r) * static_cast<uint32_t>(i) / static_cast<uint32_t>(n));
+  }
+};
 
 }  // namespace csa

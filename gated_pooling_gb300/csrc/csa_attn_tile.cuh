@@ -931,15 +931,19 @@ __global__ void __launch_bounds__(TileCta<SRC>::kThreads, 1)
 
 // Joins the pieces of the units that workers share, four rows at a time: the blocks take (unit, four
 // rows) in turn. Lane k of every warp holds piece k's weights for the four rows (32 pieces at a
-// time); a warp adds up 32 columns of them, eight pieces' loads under way.
+// time); a warp adds up 32 columns of them, four pieces' loads under way. Small blocks, all of them
+// resident at once: the kernel is a chain of five loads, and blocks behind others would double it.
 template <int NC>
 struct JoinShape {
-  static constexpr int kWarps = NC * 2;  // of 32 columns
+  static constexpr int kWarps = NC < 4 ? NC * 2 : 8;                   // of 32 columns
+  static constexpr int kSplit = NC * 2 / kWarps;                       // blocks for all columns
+  static constexpr int kItems = kAttnRows / 4 * kSplit;                // of 64 rows
 };
 template <int NC, int CL>
-__global__ void __launch_bounds__(JoinShape<NC>::kWarps * 32) attn_join_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(JoinShape<NC>::kWarps * 32, 5) attn_join_kernel(const __grid_constant__ AttnParams p) {
   using SH = TileShape<NC>;
-  constexpr int kParts = CL * kAttnRows / 4;  // of a unit
+  constexpr int kSplit = JoinShape<NC>::kSplit;
+  constexpr int kParts = CL * JoinShape<NC>::kItems;  // of a unit
   constexpr int kPiece = kAttnRows * SH::kDpad / 4;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
@@ -947,7 +951,8 @@ __global__ void __launch_bounds__(JoinShape<NC>::kWarps * 32) attn_join_kernel(c
   if (head.x != 0) return;
   for (int item = blockIdx.x; item < head.y * kParts; item += gridDim.x) {
     const AttnJoin& J = p.joins[item / kParts];
-    const int rank = item % kParts / (kAttnRows / 4), quarter = item % (kAttnRows / 4);
+    const int part = item % kParts / kSplit, rank = part / (kAttnRows / 4), quarter = part % (kAttnRows / 4);
+    const int columns = (item % kSplit) * JoinShape<NC>::kWarps + warp;  // block of 32
     const AttnUnit u = J.u;
     const int i = J.worker, n = J.pieces;
     const int r0 = quarter * 4, row0 = (u.block * CL + rank) * kAttnRows + r0;
@@ -985,7 +990,7 @@ __global__ void __launch_bounds__(JoinShape<NC>::kWarps * 32) attn_join_kernel(c
       mx[r] = warp_max_f32(mx[r]);
       some[r] = __any_sync(0xFFFFFFFFu, some[r]);
     }
-    const float4* o = reinterpret_cast<const float4*>(p.part_o) + (warp * (kAttnRows / 4) + quarter) * 32 + lane;
+    const float4* o = reinterpret_cast<const float4*>(p.part_o) + (columns * (kAttnRows / 4) + quarter) * 32 + lane;
     for (int k0 = 0; k0 < n; k0 += 32) {
       float f[4] = {0.f, 0.f, 0.f, 0.f};
       if (k0 + lane < n) {
@@ -999,13 +1004,13 @@ __global__ void __launch_bounds__(JoinShape<NC>::kWarps * 32) attn_join_kernel(c
       }
       const int some_k = min(32, n - k0);
 #pragma unroll 1
-      for (int k1 = 0; k1 < some_k; k1 += 8) {
-        float4 v[8];
+      for (int k1 = 0; k1 < some_k; k1 += 4) {
+        float4 v[4];
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
+        for (int k = 0; k < 4; ++k)
           v[k] = k1 + k < some_k ? o[slot(k0 + k1 + k) * kPiece] : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < 4; ++k) {
           acc[0] = fmaf(__shfl_sync(0xFFFFFFFFu, f[0], k1 + k), v[k].x, acc[0]);
           acc[1] = fmaf(__shfl_sync(0xFFFFFFFFu, f[1], k1 + k), v[k].y, acc[1]);
           acc[2] = fmaf(__shfl_sync(0xFFFFFFFFu, f[2], k1 + k), v[k].z, acc[2]);
@@ -1022,10 +1027,10 @@ __global__ void __launch_bounds__(JoinShape<NC>::kWarps * 32) attn_join_kernel(c
       const int head_of = u.kvh * p.group + row % p.group;
       const int64_t token = static_cast<int64_t>(u.token) + row / p.group;
       const float all = mx[r] == -INFINITY ? 1.f : den[r] + fast_exp2(sink_e[r] * kLog2e - mx[r]);
-      const int col = warp * 32 + lane;
+      const int col = columns * 32 + lane;
       if (col < p.d)
         p.out[token * p.out_row + head_of * p.out_head + col] = Element<CSA_DTYPE_BF16>::from_float(acc[r] * (1.f / all));
-      if (p.lse != nullptr && warp == 0 && lane == 0)
+      if (p.lse != nullptr && columns == 0 && lane == 0)
         p.lse[token * p.q_heads + head_of] = some[r] ? (mx[r] + log2f(all)) * kLn2 : sink_e[r];
     }
   }
