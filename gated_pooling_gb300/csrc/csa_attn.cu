@@ -26,7 +26,9 @@ __device__ __forceinline__ int sequence_of(const int32_t* cu, int S, int64_t t) 
 }
 
 // Exclusive sum over the block, and the block's total (64 bits).
-constexpr int kPlanThreads = 1024;
+// (few threads: every warp walks through all of the plan's code, 1024 threads took 13 thousand
+// cycles for 48 sequences)
+constexpr int kPlanThreads = 256, kPlanUnits = 1024;
 __device__ __forceinline__ int64_t plan_scan(int64_t v, int64_t* warps, int64_t& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t x = v;
@@ -39,7 +41,7 @@ __device__ __forceinline__ int64_t plan_scan(int64_t v, int64_t* warps, int64_t&
   if (lane == 31) warps[warp] = x;
   __syncthreads();
   if (warp == 0) {
-    int64_t s = warps[lane];
+    int64_t s = lane < kPlanThreads / 32 ? warps[lane] : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t y = __shfl_up_sync(0xFFFFFFFFu, s, o);
@@ -58,7 +60,7 @@ __device__ __forceinline__ int64_t plan_scan(int64_t v, int64_t* warps, int64_t&
 __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnParams p) {
   extern __shared__ int s_first[];  // [S + 1] first row block of each sequence
   __shared__ int64_t s_warps[32];
-  __shared__ int64_t s_work[kPlanThreads + 1];  // where the units' work begins, if there are no more
+  __shared__ int64_t s_work[kPlanUnits + 1];  // where the units' work begins, if there are no more
   __shared__ int s_joins;
   if (threadIdx.x == 0) s_joins = 0;
   pdl_wait();
@@ -87,7 +89,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnParams p) {
   if (threadIdx.x == 0) s_first[p.S] = static_cast<int>(blocks);
   __syncthreads();
   const int64_t units = blocks * p.kv_heads;
-  const bool few = units <= kPlanThreads;
+  const bool few = units <= kPlanUnits;
   int64_t all = 0;
   for (int64_t u0 = 0; u0 < units; u0 += kPlanThreads) {
     const int64_t i = u0 + threadIdx.x;
@@ -103,7 +105,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnParams p) {
       u = make_unit(p, l, static_cast<int>(i - static_cast<int64_t>(b) * p.kv_heads), b - s_first[l]);
     }
     int64_t sum = 0;
-    const int64_t first = all + plan_scan(i < units ? u.tiles + 1 : 0, s_warps, sum);
+    const int64_t first = all + plan_scan(i < units ? u.tiles + p.unit_cost : 0, s_warps, sum);
     if (i < units) {
       p.units[i] = u;
       p.unit_first[i] = first;
@@ -122,7 +124,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnParams p) {
     int64_t unit, tile, before;
   };
   auto place = [&](int64_t x) {
-    if (x >= all) return Place{units, 0, all - units};
+    if (x >= all) return Place{units, 0, all - units * p.unit_cost};
     int64_t l = 0, h = units;  // work[l] <= x < work[h]
     while (h - l > 1) {
       const int64_t mid = (l + h) / 2;
@@ -130,8 +132,8 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnParams p) {
       else h = mid;
     }
     const int64_t tile = x - work[l];
-    if (tile == work[l + 1] - work[l] - 1) return Place{l + 1, 0, x - l};  // behind the unit's last tile
-    return Place{l, tile, x - l};
+    if (tile >= work[l + 1] - work[l] - p.unit_cost) return Place{l + 1, 0, work[l + 1] - (l + 1) * p.unit_cost};  // behind the unit's last tile
+    return Place{l, tile, x - l * p.unit_cost};
   };
   const AttnShares share(all, p.workers);
   for (int i = threadIdx.x; i < p.workers; i += kPlanThreads) {
@@ -144,7 +146,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnParams p) {
       start.tile = static_cast<int32_t>(a.tile);
       // a unit that begins in this share and goes on in later ones
       if (b.tile > 0 && (b.unit > a.unit || a.tile == 0)) {
-        const int64_t end = work[b.unit + 1] - 1;
+        const int64_t end = work[b.unit + 1] - p.unit_cost;
         AttnJoin join{};
         join.u = p.units[b.unit];
         join.worker = i;
@@ -396,9 +398,14 @@ extern "C" csa_status_t csa_cache_attn(
   }
   if (!tile) p.units = nullptr;
   const bool chunks = tile && chunked(p);
+  // A unit's own cost (q in, output out, the pipeline's start) in tiles, by which shares are
+  // evened out: measured best of 1 to 12 for chunks at d = 512 (606 GFLOP in 731 us; at 1 867 us)
+  // and 128 (86 GFLOP in 138 us; at 1 161 us), and for single tokens (84 us; at 4 89 us).
+  p.unit_cost = 1;
   if (chunks) {
     p.workers = sms / 2;
     p.unit_rows = 2 * kAttnRows;
+    p.unit_cost = d > 256 ? 4 : 6;
   }
   p.q = static_cast<const uint16_t*>(q);
   p.cu = cu_seqlens;
@@ -500,7 +507,7 @@ extern "C" csa_status_t csa_cache_attn(
     void* targs[] = {&p, &map};
     if (launch_pdl(k, dim3(p.workers * cluster), dim3(threads), smem, cs, targs, cluster) != cudaSuccess)
       return CSA_ERR_CUDA;
-    return launch_pdl(join, dim3(p.workers * cluster * join_items), dim3(join_threads), 0, cs, args) == cudaSuccess
+    return launch_pdl(join, dim3(5 * sms), dim3(join_threads), 0, cs, args) == cudaSuccess
                ? CSA_OK
                : CSA_ERR_CUDA;
   }

@@ -67,7 +67,7 @@ struct AttnParams {
   int64_t q_row, q_head, out_row, out_head;
   int64_t tokens, num_pages, max_entries, max_units;
   int S, q_heads, kv_heads, group, d, max_pages, page_size, ratio;
-  int workers, unit_rows;
+  int workers, unit_rows, unit_cost;
   int packed_rows;  // rows of a sequence's cache head in `packed`, a multiple of 128
   int box_rows;     // entries of a tensor copy's box from the pages
   float scale;  // softmax_scale
@@ -102,8 +102,8 @@ __device__ __forceinline__ AttnUnit make_unit(const AttnParams& p, int s, int kv
   return u;
 }
 
-// Worker i's share of the work, a unit counting its tiles and one more (loading q, bringing the
-// output out): [share(i), share(i + 1)) of n = min(work, workers) equal ones.
+// Worker i's share of the work, a unit counting its tiles and unit_cost more (loading q, bringing
+// the output out): [share(i), share(i + 1)) of n = min(work, workers) equal ones.
 struct AttnShares {
   int64_t work, q;
   int n, r;
