@@ -65,7 +65,7 @@ struct TileCta {
 constexpr int kSoftRegs = 64, kIssueRegs = 40, kLoadRegs = 104;
 constexpr int kChunkBytes = kAttnEntries * 128;  // 128 entries x 64 columns
 constexpr int kPairBytes = 2 * kChunkBytes;
-constexpr int kSmallBytes = 7168;
+constexpr int kSmallBytes = 8192;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNoMax = -1e30f;     // bound of a row that has seen nothing
 constexpr float kRescaleAt = 8.f;    // log2 of how far a weight may pass 1
@@ -92,6 +92,10 @@ struct TileShape {
 struct TileSmall {
   int64_t row[2][2][kAttnEntries];  // by fetching group and turn: bytes to an entry in the pool, -1: none
   int64_t q_at[kAttnRows];          // elements to a row of q, -1: none
+  int64_t out_at[kAttnRows];        // and of out
+  AttnUnit next;                    // the worker's next unit
+  float sink[kAttnRows];
+  int32_t lse_at[kAttnRows];
   float m[kAttnRows];
   float fac[kAttnRows];
   float red[4][kAttnRows];  // column maxima, then weight sums, by quadrant
@@ -365,6 +369,7 @@ struct SegmentWalk {
       bound();
     }
   }
+  __device__ __forceinline__ bool last() const { return left == t1 - t0; }
 };
 
 // ------------------------------------------------------------------------------ the fetchers
@@ -600,18 +605,26 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
   auto barrier_group = [&]() { named_barrier(1 + group, 128); };
 
   const int worker = blockIdx.x / CL, rank = CL == 1 ? 0 : static_cast<int>(cluster_rank());
-  for (SegmentWalk w(p, worker); w.valid(); w.next()) {
+  SegmentWalk w(p, worker);
+  while (w.valid()) {
     const int seen_all = w.u.seen_all;
-    // where each row of q lies, and what it sees (rows behind the last one are zeros, see what
-    // the last one sees, and are never stored)
+    const bool whole = w.t0 == 0 && w.t1 == w.u.tiles, more = !w.last();
+    // where each row of q, out and lse lies, what it sees, its sink (rows behind the last one are
+    // zeros, see what the last one sees, and are never stored); and the next unit on its way
     if (tid < kAttnRows) {
       const int row = w.u.block * (CL * kAttnRows) + rank * kAttnRows + tid, token = row / p.group;
       const bool some = row < w.u.rows;
+      const int head = w.u.kvh * p.group + (row - token * p.group);
+      const int64_t at = static_cast<int64_t>(w.u.token) + token;
       sm.lim[tid] = some ? visible(static_cast<int64_t>(w.u.first) + token, p.ratio, w.u.n) : w.u.seen;
-      sm.q_at[tid] = some ? (static_cast<int64_t>(w.u.token) + token) * p.q_row +
-                                (w.u.kvh * p.group + (row - token * p.group)) * p.q_head
-                          : -1;
+      sm.q_at[tid] = some ? at * p.q_row + head * p.q_head : -1;
+      sm.out_at[tid] = some ? at * p.out_row + head * p.out_head : -1;
+      sm.lse_at[tid] = some ? static_cast<int32_t>(at * p.q_heads + head) : -1;
+      sm.sink[tid] = some && p.sink != nullptr ? __ldg(p.sink + head) : -INFINITY;
       sm.m[tid] = kNoMax;
+    } else if (more && tid >= kSoftThreads - 3) {
+      const int i = tid - (kSoftThreads - 3);
+      reinterpret_cast<int4*>(&sm.next)[i] = __ldg(reinterpret_cast<const int4*>(p.units + w.unit + 1) + i);
     }
     named_barrier(5, kSoftThreads);
     {
@@ -736,6 +749,18 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.probs);
+      if (j == w.t0 && more) {
+        // the next unit's rows of q on their way into L2
+        named_barrier(5, kSoftThreads);
+        const int r = tid / NC, row = sm.next.block * (CL * kAttnRows) + rank * kAttnRows + r;
+        const int col = (tid % NC) * 64;
+        if (r < kAttnRows && row < sm.next.rows && col < p.d) {
+          const int token = row / p.group;
+          const uint16_t* at = p.q + (static_cast<int64_t>(sm.next.token) + token) * p.q_row +
+                               (sm.next.kvh * p.group + (row - token * p.group)) * p.q_head + col;
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+        }
+      }
     }
 
     // the unit's (or its piece's) sums are complete
@@ -754,9 +779,6 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
     l[0] += __shfl_xor_sync(0xFFFFFFFFu, l[0], 1);
     if ((lane & 1) == 0) sm.red[quad][c0 + (lane >> 1)] = l[0];
     barrier_group();
-    const AttnUnit u = read_unit(p.units + w.unit);
-    const int row0 = u.block * (CL * kAttnRows) + rank * kAttnRows;
-    const bool whole = w.t0 == 0 && w.t1 == u.tiles;
     const int64_t piece = (2 * static_cast<int64_t>(worker) + (w.t0 == 0 ? 1 : 0)) * CL + rank;
     if (quad == 0 && lane < kSoftCols) {
       const int c = c0 + lane;
@@ -766,17 +788,12 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
         ml[c] = m;
         ml[kAttnRows + c] = z;
       } else {
-        const int row = row0 + c;
-        const int head = u.kvh * p.group + row % p.group;
-        const float sink_e = p.sink != nullptr && row < u.rows ? p.sink[head] : -INFINITY;
-        const float sink = sink_e * kLog2e;
+        const float sink_e = sm.sink[c], sink = sink_e * kLog2e;
         const float mx = fmaxf(z > 0.f || z != z ? m : -INFINITY, sink);
         const float old = mx == -INFINITY ? 0.f : fast_exp2(m - mx);
         const float den = mx == -INFINITY ? 0.f : z * old + fast_exp2(sink - mx);
         sm.fac[c] = mx == -INFINITY ? 0.f : old / den;
-        if (p.lse != nullptr && row < u.rows)
-          p.lse[(static_cast<int64_t>(u.token) + row / p.group) * p.q_heads + head] =
-              z == 0.f ? sink_e : (mx + log2f(den)) * kLn2;
+        if (p.lse != nullptr && sm.lse_at[c] >= 0) p.lse[sm.lse_at[c]] = z == 0.f ? sink_e : (mx + log2f(den)) * kLn2;
       }
     }
     barrier_group();
@@ -796,12 +813,10 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
       constexpr int kPer = NC * 8;
 #pragma unroll 1
       for (int i = (tid & 127); i < kSoftCols * kPer; i += 128) {
-        const int r = c0 + i / kPer, c = i % kPer, row = row0 + r;
-        if (row < u.rows && c * 8 < p.d) {
-          const uint4 v = lds128(base + SH::kQOff + r * (SH::kDpad * 2) + c * 16);
-          *reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(u.token) + row / p.group) * p.out_row +
-                                    (u.kvh * p.group + row % p.group) * p.out_head + c * 8) = v;
-        }
+        const int r = c0 + i / kPer, c = i % kPer;
+        const int64_t at = sm.out_at[r];
+        if (at >= 0 && c * 8 < p.d)
+          *reinterpret_cast<uint4*>(p.out + at + c * 8) = lds128(base + SH::kQOff + r * (SH::kDpad * 2) + c * 16);
       }
     } else {
       // four rows of a column in 16 bytes, a warp's 32 columns side by side
@@ -812,13 +827,21 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
         tmem_load16(lanes + SH::kTmemO + b * kAttnRows + c0, v);
 #pragma unroll
         for (int c = 0; c < kSoftCols; c += 4)
-          if (row0 + c0 + c < u.rows)
+          if (sm.out_at[c0 + c] >= 0)
             o[((b * 4 + quad) * (kAttnRows / 4) + (c0 + c) / 4) * 32 + lane] =
                 make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
       }
       tc_fence_before();
     }
     named_barrier(5, kSoftThreads);  // the small arrays and the staging are free again
+    w.left -= w.t1 - w.t0;
+    ++w.unit;
+    w.t0 = 0;
+    if (more) {
+      w.u = sm.next;
+      w.bound();
+      named_barrier(5, kSoftThreads);  // (read before the one after it is written)
+    }
   }
 }
 
