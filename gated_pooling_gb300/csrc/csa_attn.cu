@@ -437,9 +437,11 @@ extern "C" csa_status_t csa_cache_attn(
   if (launch_pdl(plan, dim3(1), dim3(kPlanThreads), plan_smem, cs, args) != cudaSuccess) return CSA_ERR_CUDA;
   if (tile) {
     const int nc = tile_chunks(d);
-    // Tensor copies straight from the pages where a power of two of at least 8 entries
+    // bf16: tensor copies straight from the pages where a power of two of at least 8 entries
     // divides the page: smaller boxes copy slower than threads (8 entries 3.2 TB/s from L2,
-    // 16 4.2, 64 and up 5.7).
+    // 16 4.2, 64 and up 5.7). Codes come by threads, which have to widen them: copied first, 48
+    // sequences of up to 8192 entries took 32.5 instead of 32.0 us at d = 128, 45.9 instead of 45.6 at 256,
+    // and 80.4 instead of 77.8 at 512.
     p.box_rows = 1;
     while (p.box_rows < kAttnEntries && page_size % (2 * p.box_rows) == 0) p.box_rows *= 2;
     CUtensorMap map{};
@@ -450,16 +452,14 @@ extern "C" csa_status_t csa_cache_attn(
                                 static_cast<uint64_t>(S) * kv_heads * static_cast<uint64_t>(p.packed_rows)};
       const uint64_t strides[1] = {static_cast<uint64_t>(nc) * 128};
       const uint32_t box[2] = {64, kAttnEntries};
-      if (!encode_boxes(&map, false, p.packed, 2, dims, strides, box)) return CSA_ERR_CUDA;
-    } else if (p.box_rows >= 8 && num_pages > 0 && num_pages <= INT_MAX / page_size) {
-      const bool codes = format != CSA_CACHE_BF16;
-      const uint64_t row = codes ? (format == CSA_CACHE_E4M3 ? d : d / 2) : d;  // elements of an entry's head
-      const uint64_t size = codes ? 1 : 2;
+      if (!encode_boxes(&map, p.packed, 2, dims, strides, box)) return CSA_ERR_CUDA;
+    } else if (format == CSA_CACHE_BF16 && p.box_rows >= 8 && num_pages > 0 && num_pages <= INT_MAX / page_size) {
+      const uint64_t row = d;
       const uint64_t dims[3] = {row, static_cast<uint64_t>(kv_heads), static_cast<uint64_t>(num_pages) * page_size};
-      const uint64_t strides[2] = {row * size, row * size * kv_heads};
-      const uint32_t box[3] = {format == CSA_CACHE_E4M3 ? 128u : 64u, 1, static_cast<uint32_t>(p.box_rows)};
-      if (!encode_boxes(&map, codes, data, 3, dims, strides, box)) return CSA_ERR_CUDA;
-      source = format == CSA_CACHE_BF16 ? kFromBoxes : format == CSA_CACHE_E4M3 ? kFromE4m3Boxes : kFromE2m1Boxes;
+      const uint64_t strides[2] = {row * 2, row * 2 * kv_heads};
+      const uint32_t box[3] = {64, 1, static_cast<uint32_t>(p.box_rows)};
+      if (!encode_boxes(&map, data, 3, dims, strides, box)) return CSA_ERR_CUDA;
+      source = kFromBoxes;
     }
     size_t smem = 0;
     int threads = 0, join_threads = 0, join_items = 0;
@@ -483,10 +483,6 @@ extern "C" csa_status_t csa_cache_attn(
         });
       } else if (source == kFromBoxes) {
         use(std::integral_constant<int, kFromBoxes>{});
-      } else if (source == kFromE4m3Boxes) {
-        use(std::integral_constant<int, kFromE4m3Boxes>{});
-      } else if (source == kFromE2m1Boxes) {
-        use(std::integral_constant<int, kFromE2m1Boxes>{});
       } else {
         by_format(format, use);
       }

@@ -13,11 +13,13 @@
 //
 // Warps: 0-15 softmax (a warp reads the 32 tensor-memory lanes of its quadrant, each group of
 // four warps 16 of the 64 rows), 16 issues the products, 17 the tensor copies where the tile comes
-// by those (18 and 19 only complete the register group); otherwise 20-27 fetch: they follow the page table, widen 8- and 4-bit codes to bf16 (exact, but
-// for bf16's own subnormals) and store the swizzled tile in pairs of 64-column chunks (32 KB).
-// Two groups of four warps take alternate pairs: a group holds its next pair in registers
-// while the ring is full, and one group's loads are under way while the other stores. Rows of
-// the next tile are prefetched into L2.
+// by those (18 and 19 only complete the register group); otherwise 20-27 fetch: they follow the
+// page table, widen 8- and 4-bit codes to bf16 (exact, but for bf16's own subnormals) and store
+// the swizzled tile in pairs of 64-column chunks (32 KB). Two groups of four warps take alternate
+// pairs: a group holds its next pair in registers while the ring is full, and one group's loads
+// are under way while the other stores. At d > 256 the ring holds one tile only, so fetching is
+// part of a chain with the products and the softmax; the softmax warps, idle meanwhile, fetch
+// half of the tile's codes (48 sequences of up to 8192 8-bit entries of 512: 84 us without, 78 with).
 //
 // Softmax without a maximum per tile: the weights are taken against a running bound m that
 // only moves when some score passes it by 2^8; then m becomes the true maximum and O^T and the
@@ -41,23 +43,18 @@ constexpr int kSoftCols = 16;  // rows of a softmax thread's group
 constexpr int kTileLoaders = kTileLoadWarps * 32;
 constexpr int kTileFirstLoader = kTileSoftWarps + 4;
 // Where a tile comes from: threads that read the pages (in each of the cache's formats); tensor
-// copies of the pages' codes into the second half of a pair's slot, which threads widen over the
-// whole of it; tensor copies of the pages' bf16 boxes; or tensor copies of a sequence's packed
-// entries that go to both CTAs of a pair.
+// copies of the pages' bf16 boxes; or tensor copies of a sequence's packed entries that go to both
+// CTAs of a pair.
 enum TileSource {
   kFromBf16 = CSA_CACHE_BF16,
   kFromE4m3 = CSA_CACHE_E4M3,
   kFromE2m1 = CSA_CACHE_E2M1,
-  kFromE4m3Boxes,
-  kFromE2m1Boxes,
   kFromBoxes,
   kFromPacked
 };
 template <int SRC>
 struct TileCta {
-  static constexpr bool kByThreads = SRC < kFromBoxes;  // threads fetch or widen
-  static constexpr bool kByCopies = SRC >= kFromE4m3Boxes;
-  static constexpr int kFormat = SRC == kFromE4m3Boxes ? kFromE4m3 : SRC == kFromE2m1Boxes ? kFromE2m1 : SRC;
+  static constexpr bool kByThreads = SRC < kFromBoxes;
   static constexpr int kCluster = SRC == kFromPacked ? 2 : 1;
   static constexpr int kThreads = (kTileFirstLoader + (kByThreads ? kTileLoadWarps : 0)) * 32;
 };
@@ -65,7 +62,7 @@ struct TileCta {
 constexpr int kSoftRegs = 64, kIssueRegs = 40, kLoadRegs = 104;
 constexpr int kChunkBytes = kAttnEntries * 128;  // 128 entries x 64 columns
 constexpr int kPairBytes = 2 * kChunkBytes;
-constexpr int kSmallBytes = 8192;
+constexpr int kSmallBytes = 10240;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNoMax = -1e30f;     // bound of a row that has seen nothing
 constexpr float kRescaleAt = 8.f;    // log2 of how far a weight may pass 1
@@ -82,6 +79,10 @@ struct TileShape {
   static constexpr int kTmemUsed = kTmemS + 2 * kAttnRows;
   static constexpr int kTmemColumns = kTmemUsed <= 256 ? 256 : 512;
   static constexpr int kDpad = NC * 64;
+  // Codes, and a ring that holds one tile only, so that nobody else has work until the next one is
+  // widened: the softmax warps take the second half of its pairs.
+  template <int SRC>
+  static constexpr bool kHelped = (SRC == kFromE4m3 || SRC == kFromE2m1) && kRing == kPairs;
   // shared memory: ring, Q (the output's staging too), P, then the small arrays
   static constexpr int kQOff = kRing * kPairBytes;
   static constexpr int kPOff = kQOff + kQBytes;
@@ -91,6 +92,7 @@ struct TileShape {
 
 struct TileSmall {
   int64_t row[2][2][kAttnEntries];  // by fetching group and turn: bytes to an entry in the pool, -1: none
+  int64_t help_row[2][kAttnEntries];   // the same for the softmax warps that widen
   int64_t q_at[kAttnRows];          // elements to a row of q, -1: none
   int64_t out_at[kAttnRows];        // and of out
   AttnUnit next;                    // the worker's next unit
@@ -100,7 +102,7 @@ struct TileSmall {
   float fac[kAttnRows];
   float red[4][kAttnRows];  // column maxima, then weight sums, by quadrant
   int lim[kAttnRows];
-  uint64_t full[5], empty[5], raw[5], scores[2], probs, summed, q_full, drain;
+  uint64_t full[5], empty[5], scores[2], probs, summed, q_full, drain;
   uint32_t tmem;
   int stop;
 };
@@ -129,6 +131,14 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
 // branch, for the scales up to 2^7 (2^1) whose factor is within bf16's range, and no NaN
 // among the codes; anything else goes through fp32, code by code. (The conversion
 // instructions, 16 lanes a cycle each, took 2.2 thousand cycles for the two pairs under way.)
+// Two bytes of (w, v), each below a byte of its top bit's copies: a code at the lower end of its
+// half with its sign already above it, so that one shift and one mask place both.
+template <int SELECT>
+__device__ __forceinline__ uint32_t signed_pair(uint32_t w, uint32_t v) {
+  uint32_t x;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(x) : "r"(w), "r"(v), "n"(SELECT));
+  return x;
+}
 template <int FORMAT>
 struct Widen {
   static constexpr uint32_t kLift = FORMAT == CSA_CACHE_E4M3 ? 120 : 126;
@@ -144,16 +154,16 @@ struct Widen {
   }
   // 8 e4m3 codes
   __device__ __forceinline__ uint4 eight(uint32_t w, uint32_t v) const {
-    auto at = [&](uint32_t x) { return two(((x >> 4) & 0x07F007F0u) | (x & 0x80008000u)); };
-    return make_uint4(at(__byte_perm(w, 0, 0x1404)), at(__byte_perm(w, 0, 0x3424)), at(__byte_perm(v, 0, 0x1404)),
-                      at(__byte_perm(v, 0, 0x3424)));
+    auto at = [&](uint32_t x) { return two((x << 4) & 0x87F087F0u); };
+    return make_uint4(at(signed_pair<0x9180>(w, 0)), at(signed_pair<0xB3A2>(w, 0)), at(signed_pair<0x9180>(v, 0)),
+                      at(signed_pair<0xB3A2>(v, 0)));
   }
   // 8 e2m1 codes
   __device__ __forceinline__ uint4 eight(uint32_t w) const {
-    const uint32_t lo = (w << 4) & 0xF0F0F0F0u, hi = w & 0xF0F0F0F0u;
-    auto at = [&](uint32_t x) { return two(((x >> 6) & 0x01C001C0u) | (x & 0x80008000u)); };
-    return make_uint4(at(__byte_perm(lo, hi, 0x4400)), at(__byte_perm(lo, hi, 0x5511)), at(__byte_perm(lo, hi, 0x6622)),
-                      at(__byte_perm(lo, hi, 0x7733)));
+    const uint32_t lo = w << 4;  // each byte's low code to its top, as w has the high one
+    auto at = [&](uint32_t x) { return two((x << 2) & 0x81C081C0u); };
+    return make_uint4(at(signed_pair<0xC480>(lo, w)), at(signed_pair<0xD591>(lo, w)), at(signed_pair<0xE6A2>(lo, w)),
+                      at(signed_pair<0xF7B3>(lo, w)));
   }
 };
 // Bits left where a word holds an e4m3 NaN.
@@ -216,26 +226,14 @@ struct Take<CSA_CACHE_E4M3> {
   static __device__ __forceinline__ int column(int t) { return (t & 3) * 32; }
   uint4 a, b;
   uint32_t k;
-  bool some;
   __device__ __forceinline__ void load(const AttnParams& p, int64_t at, int col) {
+    const bool some = at >= 0 && col < p.d;
     a = b = make_uint4(0, 0, 0, 0);
-    load_scale(p, at, col);
-    if (at >= 0 && col < p.d) {
+    k = some ? __ldg(p.scales + (at >> 5) + (col >> 5)) : kNoScale;
+    if (some) {
       const uint4* w = reinterpret_cast<const uint4*>(p.data + at + col);
       a = __ldg(w);
       b = __ldg(w + 1);
-    }
-  }
-  // the scale alone (none: -1), then the codes from a copied pair (128 bytes an entry)
-  __device__ __forceinline__ void load_scale(const AttnParams& p, int64_t at, int col) {
-    some = at >= 0 && col < p.d;
-    k = some ? __ldg(p.scales + (at >> 5) + (col >> 5)) : kNoScale;
-  }
-  __device__ __forceinline__ void load_codes(uint32_t raw, int row, int t) {
-    a = b = make_uint4(0, 0, 0, 0);
-    if (some) {
-      a = lds128(raw + row * 128 + (t & 3) * 32);
-      b = lds128(raw + row * 128 + (t & 3) * 32 + 16);
     }
   }
   // 8 codes
@@ -271,18 +269,10 @@ struct Take<CSA_CACHE_E2M1> {
   static __device__ __forceinline__ int column(int t) { return (t & 3) * 32; }
   uint4 a;
   uint32_t k;
-  bool some;
   __device__ __forceinline__ void load(const AttnParams& p, int64_t at, int col) {
-    a = make_uint4(0, 0, 0, 0);
-    load_scale(p, at, col);
-    if (at >= 0 && col < p.d) a = __ldg(reinterpret_cast<const uint4*>(p.data + at + (col >> 1)));
-  }
-  __device__ __forceinline__ void load_scale(const AttnParams& p, int64_t at, int col) {
-    some = at >= 0 && col < p.d;
+    const bool some = at >= 0 && col < p.d;
     k = some ? __ldg(p.scales + (at >> 4) + (col >> 5)) : kNoScale;
-  }
-  __device__ __forceinline__ void load_codes(uint32_t raw, int row, int t) {  // 64 bytes an entry
-    a = some ? lds128(raw + row * 64 + (t & 3) * 16) : make_uint4(0, 0, 0, 0);
+    a = some ? __ldg(reinterpret_cast<const uint4*>(p.data + at + (col >> 1))) : make_uint4(0, 0, 0, 0);
   }
   static __device__ __forceinline__ uint4 widen(uint32_t k, uint32_t x) {
     return Widen<CSA_CACHE_E2M1>::plain(k) ? Widen<CSA_CACHE_E2M1>(k).eight(x) : widen_any(x, scale_value(k));
@@ -376,8 +366,7 @@ struct SegmentWalk {
 template <int NC, int SRC>
 __device__ void tile_fetch(const AttnParams& p, TileSmall& sm, uint32_t base) {
   using SH = TileShape<NC>;
-  constexpr bool kCopied = TileCta<SRC>::kByCopies;
-  using P = Take<TileCta<SRC>::kFormat>;
+  using P = Take<SRC>;
   constexpr int kGroup = kTileLoaders / 2;
   constexpr int kStep = SH::kPairs == 1 ? 2 : 1;  // tiles from one of a group's to its next
   const int lt = threadIdx.x - kTileFirstLoader * 32;
@@ -398,6 +387,8 @@ __device__ void tile_fetch(const AttnParams& p, TileSmall& sm, uint32_t base) {
       tile = w.t0;
     }
   };
+  // from one of the group's pairs to its next
+  constexpr int kPairStep = SH::template kHelped<SRC> ? SH::kPairs : 2;
   // this thread's page of tile `ahead` of unit `unit`, read early
   int page = -1, ahead = -1, unit = -1;
   auto read_page = [&](int tl) {
@@ -430,22 +421,18 @@ __device__ void tile_fetch(const AttnParams& p, TileSmall& sm, uint32_t base) {
     P v[P::kRows];
     const int64_t* at = &sm.row[group][buf][P::first_row(gt)];
     const int col = pair * 128 + P::column(gt);
-    if constexpr (kCopied) {
+    if constexpr (SH::template kHelped<SRC>) {
+      // the softmax warps' half on its way into L2, a line by one lane
+      const int far = (pair + SH::kPairs / 2) * 128;
+      if ((gt & 3) == 0 && far < p.d)
 #pragma unroll
-      for (int i = 0; i < P::kRows; ++i) v[i].load_scale(p, at[i * P::kRowStep], col);
-      tile_wait(sm, p, &sm.raw[ring.slot], ring.lap);
-#pragma unroll
-      for (int i = 0; i < P::kRows; ++i)
-        v[i].load_codes(base + ring.slot * kPairBytes + kChunkBytes, P::first_row(gt) + i * P::kRowStep, gt);
-      // The codes are in registers, and their place is written over: an 8-bit entry's is its own row's,
-      // read by four lanes of one warp; 4-bit ones lie two to a row.
-      if (TileCta<SRC>::kFormat == CSA_CACHE_E4M3) __syncwarp();
-      else named_barrier(6 + group, kGroup);
-    } else {
-#pragma unroll
-      for (int i = 0; i < P::kRows; ++i) v[i].load(p, at[i * P::kRowStep], col);
-      tile_wait(sm, p, &sm.empty[ring.slot], ring.lap ^ 1u);
+        for (int i = 0; i < P::kRows; ++i)
+          if (at[i * P::kRowStep] >= 0)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p.data + at[i * P::kRowStep] + P::row_bytes(far)));
     }
+#pragma unroll
+    for (int i = 0; i < P::kRows; ++i) v[i].load(p, at[i * P::kRowStep], col);
+    tile_wait(sm, p, &sm.empty[ring.slot], ring.lap ^ 1u);
 #pragma unroll
     for (int i = 0; i < P::kRows; ++i)
       v[i].store(base + ring.slot * kPairBytes, P::first_row(gt) + i * P::kRowStep, gt);
@@ -453,13 +440,52 @@ __device__ void tile_fetch(const AttnParams& p, TileSmall& sm, uint32_t base) {
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(&sm.full[ring.slot]);
     next_pair();
-    if (w.valid()) next_pair();
+#pragma unroll
+    for (int i = 1; i < kPairStep; ++i)
+      if (w.valid()) next_pair();
   }
 }
 
+// The softmax warps' part of fetching (kHelped): the second half of a tile's pairs, each by 256 of
+// them.
+template <int SRC>
+__device__ __forceinline__ void help_places(const AttnParams& p, TileSmall& sm, const SegmentWalk& w, int tile,
+                                            uint32_t t) {
+  const int tid = threadIdx.x;
+  if (tid >= kAttnEntries) return;
+  const int e = tile * kAttnEntries + tid;
+  int64_t at = -1;
+  if (e < w.u.seen) {
+    const int page = __ldg(p.table + static_cast<int64_t>(w.u.s) * p.max_pages + e / p.page_size);
+    if (page >= 0 && page < p.num_pages)
+      at = ((static_cast<int64_t>(page) * p.page_size + e % p.page_size) * p.kv_heads + w.u.kvh) *
+           Take<SRC>::row_bytes(p.d);
+  }
+  sm.help_row[t & 1u][tid] = at;
+}
+template <int NC, int SRC>
+__device__ __forceinline__ void tile_help(const AttnParams& p, TileSmall& sm, uint32_t base, const SegmentWalk& w,
+                                          int tile, uint32_t t) {
+  using P = Take<SRC>;
+  constexpr int kHalf = kSoftThreads / 2, kRows = 2, kRowStep = kAttnEntries / kRows;
+  const int tid = threadIdx.x, half = tid / kHalf, ht = tid % kHalf;
+  if (tile == w.t0) help_places<SRC>(p, sm, w, tile, t);
+  named_barrier(5, kSoftThreads);
+  const int pair = TileShape<NC>::kPairs / 2 + half, row = P::first_row(ht), col = pair * 128 + P::column(ht);
+  P v[kRows];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) v[i].load(p, sm.help_row[t & 1u][row + i * kRowStep], col);
+  tile_wait(sm, p, &sm.empty[pair], (t & 1u) ^ 1u);
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) v[i].store(base + pair * kPairBytes, row + i * kRowStep, ht);
+  fence_proxy_async_smem();
+  __syncwarp();
+  if ((tid & 31) == 0) mbar_arrive(&sm.full[pair]);
+  if (tile + 1 < w.t1) help_places<SRC>(p, sm, w, tile + 1, t + 1);
+}
+
 // ------------------------------------------------------------- the warp that issues tensor copies
-// From the pages: lane i copies box i mod n of chunk i / n of each pair (codes: of the pair), n =
-// 128 / box_rows of them.
+// From the pages: lane i copies box i mod n of chunk i / n of each pair, n = 128 / box_rows of them.
 // A box behind the last entry that the unit sees is not copied, and rows behind it in a copied
 // box are whatever the pool holds there: masked in the scores, and made finite where they are
 // not before the second product. From packed entries: one box of a pair by each CTA of the
@@ -486,14 +512,11 @@ __device__ void tile_copy(const AttnParams& p, TileSmall& sm, uint32_t base, con
         }
     }
   } else {
-    // boxes of a pair: of both chunks (bf16), or of the codes of both together
-    constexpr bool kCodes = SRC != kFromBoxes;
-    constexpr int kEntryBytes = SRC == kFromE2m1Boxes ? 64 : 128;
     const int n = kAttnEntries / p.box_rows, chunk = lane / n, box = lane % n;
     for (SegmentWalk w(p, blockIdx.x); w.valid(); w.next()) {
       for (int tile = w.t0; tile < w.t1; ++tile) {
         const int e = tile * kAttnEntries + box * p.box_rows;
-        bool on = chunk < (kCodes ? 1 : 2) && e < w.u.seen;
+        bool on = chunk < 2 && e < w.u.seen;
         int slot = 0;
         if (on) {
           const int page = __ldg(p.table + static_cast<int64_t>(w.u.s) * p.max_pages + e / p.page_size);
@@ -503,23 +526,20 @@ __device__ void tile_copy(const AttnParams& p, TileSmall& sm, uint32_t base, con
         }
         // the next tile's boxes on their way into L2 meanwhile
         const int e1 = e + kAttnEntries;
-        if (chunk < (kCodes ? 1 : 2) && tile + 1 < w.t1 && e1 < w.u.seen) {
+        if (chunk < 2 && tile + 1 < w.t1 && e1 < w.u.seen) {
           const int page = __ldg(p.table + static_cast<int64_t>(w.u.s) * p.max_pages + e1 / p.page_size);
           if (page >= 0 && page < p.num_pages)
             for (int c = 0; c < SH::kPairs; ++c)
-              box_prefetch3(map, kCodes ? c * kEntryBytes : c * 128 + chunk * 64, w.u.kvh,
-                            page * p.page_size + e1 % p.page_size);
+              box_prefetch3(map, c * 128 + chunk * 64, w.u.kvh, page * p.page_size + e1 % p.page_size);
         }
-        const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, on)) * p.box_rows * kEntryBytes;
+        const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, on)) * p.box_rows * 128;
         for (int c = 0; c < SH::kPairs; ++c, ring.next(), ++issued) {
           tile_wait(sm, p, &sm.empty[ring.slot], ring.lap ^ 1u);
-          uint64_t* bar = kCodes ? &sm.raw[ring.slot] : &sm.full[ring.slot];
-          if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+          if (lane == 0) mbar_arrive_expect_tx(&sm.full[ring.slot], bytes);
           __syncwarp();
           if (on)
-            box_load3(base + ring.slot * kPairBytes + (kCodes ? 1 : chunk) * kChunkBytes +
-                          box * p.box_rows * kEntryBytes,
-                      map, kCodes ? c * kEntryBytes : c * 128 + chunk * 64, w.u.kvh, slot, bar);
+            box_load3(base + ring.slot * kPairBytes + chunk * kChunkBytes + box * p.box_rows * 128, map,
+                      c * 128 + chunk * 64, w.u.kvh, slot, &sm.full[ring.slot]);
         }
       }
     }
@@ -531,8 +551,7 @@ __device__ void tile_copy(const AttnParams& p, TileSmall& sm, uint32_t base, con
   // after a stop, the copies that nobody waited for: the last lap of the ring
   if (*reinterpret_cast<volatile int*>(&sm.stop) != 0)
     for (uint32_t k = issued > SH::kRing ? issued - SH::kRing : 0; k < issued; ++k)
-      mbar_wait_bounded(SRC < kFromBoxes ? &sm.raw[k % SH::kRing] : &sm.full[k % SH::kRing], (k / SH::kRing) & 1u,
-                        kWaitCycles);
+      mbar_wait_bounded(&sm.full[k % SH::kRing], (k / SH::kRing) & 1u, kWaitCycles);
 }
 
 // ------------------------------------------------- the products' warp (all lanes take part)
@@ -592,9 +611,10 @@ __device__ void tile_products(const AttnParams& p, TileSmall& sm, uint32_t base,
 }
 
 // ------------------------------------------------------------------------- the softmax warps
-template <int NC, int CL>
+template <int NC, int SRC>
 __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* smem, uint32_t base, uint32_t tmem) {
   using SH = TileShape<NC>;
+  constexpr int CL = TileCta<SRC>::kCluster;
   const int tid = threadIdx.x, lane = tid & 31, quad = (tid >> 5) & 3, group = tid >> 7;
   const int c0 = group * kSoftCols;     // the rows (columns of S^T) of this group of four warps
   const int e0 = quad * 32 + lane;      // the entry (row of S^T) of this thread
@@ -651,6 +671,7 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
     for (int c = 0; c < kSoftCols; ++c) l[c] = 0.f;
 
     for (int j = w.t0; j < w.t1; ++j, ++t) {
+      if constexpr (SH::template kHelped<SRC>) tile_help<NC, SRC>(p, sm, base, w, j, t);
       const int e = j * kAttnEntries + e0;
       const bool masked = (j + 1) * static_cast<int64_t>(kAttnEntries) > seen_all;
       const uint32_t s_at = lanes + SH::kTmemS + (t & 1u) * kAttnRows + c0;
@@ -907,9 +928,9 @@ __global__ void __launch_bounds__(TileCta<SRC>::kThreads, 1)
   if (warp == 0) tmem_alloc(&sm.tmem, SH::kTmemColumns);
   if (threadIdx.x == 32) {
     for (int i = 0; i < SH::kRing; ++i) {
-      mbar_init(&sm.full[i], CTA::kByThreads ? kTileLoadWarps / 2 : 1);
+      const bool helped = SH::template kHelped<SRC> && i >= SH::kPairs / 2;
+      mbar_init(&sm.full[i], helped ? kTileSoftWarps / 2 : CTA::kByThreads ? kTileLoadWarps / 2 : 1);
       mbar_init(&sm.empty[i], CL);
-      mbar_init(&sm.raw[i], 1);
     }
     mbar_init(&sm.scores[0], 1);
     mbar_init(&sm.scores[1], 1);
@@ -934,16 +955,14 @@ __global__ void __launch_bounds__(TileCta<SRC>::kThreads, 1)
     } else if (warp >= kTileSoftWarps) {
       regs_down<kIssueRegs>();
       if (run && warp == kTileSoftWarps) tile_products<NC, CL>(p, sm, base, tmem);
-      if constexpr (CTA::kByCopies)
-        if (run && warp == kTileSoftWarps + 1) tile_copy<NC, SRC>(p, sm, base, &map);
     } else {
       regs_down<kSoftRegs>();
-      if (run) tile_softmax<NC, CL>(p, sm, smem, base, tmem);
+      if (run) tile_softmax<NC, SRC>(p, sm, smem, base, tmem);
     }
   } else if (run) {
     if (warp == kTileSoftWarps) tile_products<NC, CL>(p, sm, base, tmem);
     else if (warp == kTileSoftWarps + 1) tile_copy<NC, SRC>(p, sm, base, &map);
-    else if (warp < kTileSoftWarps) tile_softmax<NC, CL>(p, sm, smem, base, tmem);
+    else if (warp < kTileSoftWarps) tile_softmax<NC, SRC>(p, sm, smem, base, tmem);
   }
   tc_fence_before();
   __syncthreads();

@@ -26,12 +26,11 @@ cudaError_t device_sms(int dev, int* sms);
 cudaError_t blocks_per_sm(int dev, const void* kernel, int threads, size_t smem, int* blocks);
 cudaError_t launch_pdl(const void* k, dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
                        void** args, int cluster = 1);
-// encode_boxes(): tensor map of an array of bf16 values or bytes (rank 2 or 3, dims and box
-// innermost first, strides in bytes from the second dimension on) whose boxes land in shared
-// memory with the 128-byte swizzle (bf16) or row by row (bytes); false when the driver has no
-// such call or refuses the shape.
-bool encode_boxes(CUtensorMap* map, bool bytes, const void* base, int rank, const uint64_t* dims,
-                  const uint64_t* strides, const uint32_t* box);
+// encode_boxes(): tensor map of an array of bf16 values (rank 2 or 3, dims and box innermost
+// first, strides in bytes from the second dimension on) whose boxes land in shared memory with
+// the 128-byte swizzle; false when the driver has no such call or refuses the shape.
+bool encode_boxes(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+                  const uint32_t* box);
 // launch_partial_reduce(): out[e] = (accumulate ? out[e] : 0) + sum of part[0..R-1][e] over n
 // entries, in a fixed order with compensated sums; a non-zero *status (may be NULL) on the
 // device leaves out untouched.
