@@ -61,8 +61,8 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnParams p) {
   extern __shared__ int s_first[];  // [S + 1] first row block of each sequence
   __shared__ int64_t s_warps[32];
   __shared__ int64_t s_work[kPlanUnits + 1];  // where the units' work begins, if there are no more
-  __shared__ int s_joins;
-  if (threadIdx.x == 0) s_joins = 0;
+  __shared__ int s_joins[2];  // of few pieces, of many
+  if (threadIdx.x < 2) s_joins[threadIdx.x] = 0;
   pdl_wait();
   const int per = (p.S + kPlanThreads - 1) / kPlanThreads;
   const int lo = min(p.S, static_cast<int>(threadIdx.x) * per), hi = min(p.S, lo + per);
@@ -153,13 +153,19 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnParams p) {
         int last = i + 1;
         while (share(last + 1) < end) ++last;
         join.pieces = last - i + 1;
-        p.joins[atomicAdd(&s_joins, 1)] = join;  // (in any order: each is joined by itself)
+        // (in any order: each is joined by itself; those of many pieces from the list's other end)
+        const bool few = join.pieces <= kFewPieces;
+        const int at = atomicAdd(&s_joins[few ? 0 : 1], 1);
+        p.joins[few ? at : p.workers - 1 - at] = join;
       }
     }
     p.starts[i] = start;
   }
   __syncthreads();
-  if (threadIdx.x == 0) p.head->joins = s_joins;
+  if (threadIdx.x == 0) {
+    p.head->few = s_joins[0];
+    p.head->many = s_joins[1];
+  }
 }
 
 // Scalar kernel, any d and alignment: a warp per new token and query head, a lane the columns
@@ -462,13 +468,11 @@ extern "C" csa_status_t csa_cache_attn(
       source = kFromBoxes;
     }
     size_t smem = 0;
-    int threads = 0, join_threads = 0, join_items = 0;
+    int threads = 0;
     const void *k = nullptr, *join = nullptr, *pack = nullptr;
     by_chunks(nc, [&](auto c) {
       constexpr int NC = decltype(c)::value;
       smem = TileShape<NC>::kSmemBytes;
-      join_threads = JoinShape<NC>::kWarps * 32;
-      join_items = JoinShape<NC>::kItems;
       auto use = [&](auto src) {
         constexpr int SRC = decltype(src)::value;
         k = reinterpret_cast<const void*>(attn_tile_kernel<NC, SRC>);
@@ -503,7 +507,7 @@ extern "C" csa_status_t csa_cache_attn(
     void* targs[] = {&p, &map};
     if (launch_pdl(k, dim3(p.workers * cluster), dim3(threads), smem, cs, targs, cluster) != cudaSuccess)
       return CSA_ERR_CUDA;
-    return launch_pdl(join, dim3(5 * sms), dim3(join_threads), 0, cs, args) == cudaSuccess
+    return launch_pdl(join, dim3(kJoinBlocks * sms), dim3(kJoinThreads), 0, cs, args) == cudaSuccess
                ? CSA_OK
                : CSA_ERR_CUDA;
   }

@@ -37,8 +37,8 @@ struct alignas(16) AttnJoin {  // a unit whose tiles several workers share, from
 };
 struct alignas(16) AttnHead {
   int32_t status;  // 0, or why the call's lengths were refused
-  int32_t joins;   // shared units
-  int32_t pad[2];
+  int32_t few, many;  // shared units, of few pieces and of many
+  int32_t pad;
 };
 static_assert(sizeof(AttnUnit) == 48 && sizeof(AttnStart) == 64 && sizeof(AttnJoin) == 64 && sizeof(AttnHead) == 16,
               "read in 16-byte pieces");
@@ -58,7 +58,7 @@ struct AttnParams {
   // workspace
   AttnHead* head;
   AttnStart* starts;    // [workers]
-  AttnJoin* joins;      // [workers]
+  AttnJoin* joins;      // [workers]: those of few pieces from its start, of many from its end
   AttnUnit* units;      // [max_units]
   int64_t* unit_first;  // [max_units + 1]: where each unit's work begins
   float* part_o;        // [2 workers][CTAs of one][64 x dpad]: sums of the pieces of shared units

@@ -971,110 +971,124 @@ __global__ void __launch_bounds__(TileCta<SRC>::kThreads, 1)
   if (warp == 0) tmem_free(tmem, SH::kTmemColumns);
 }
 
-// Joins the pieces of the units that workers share, four rows at a time: the blocks take (unit, four
-// rows) in turn. Lane k of every warp holds piece k's weights for the four rows (32 pieces at a
-// time); a warp adds up 32 columns of them, four pieces' loads under way. Small blocks, all of them
-// resident at once: the kernel is a chain of five loads, and blocks behind others would double it.
-template <int NC>
-struct JoinShape {
-  static constexpr int kWarps = NC < 4 ? NC * 2 : 8;                   // of 32 columns
-  static constexpr int kSplit = NC * 2 / kWarps;                       // blocks for all columns
-  static constexpr int kItems = kAttnRows / 4 * kSplit;                // of 64 rows
-};
+// Joins the pieces of the units that workers share. What it costs is a chain of loads (the list,
+// the pieces' maxima and weight sums, their sums) and instructions: a warp takes four rows and 64
+// columns, four pieces' loads under way at once and the first four's before their weights are
+// known; lane 8 r + k works out row r's weight of piece k. A unit of many pieces (a long sequence
+// by itself) is split over a block's warps, which take four pieces each in turn and meet in shared
+// memory. The order of the sums is fixed. (Redundant work in the warps took 33 of 720 us for 75 units of
+// 128 rows x 512 in two pieces each, 12 of 701 so.)
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kJoinBlocks = 3;  // blocks an SM
+constexpr int kFewPieces = 8;
 template <int NC, int CL>
-__global__ void __launch_bounds__(JoinShape<NC>::kWarps * 32, 5) attn_join_kernel(const __grid_constant__ AttnParams p) {
-  using SH = TileShape<NC>;
-  constexpr int kSplit = JoinShape<NC>::kSplit;
-  constexpr int kParts = CL * JoinShape<NC>::kItems;  // of a unit
-  constexpr int kPiece = kAttnRows * SH::kDpad / 4;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(kJoinThreads, kJoinBlocks) attn_join_kernel(const __grid_constant__ AttnParams p) {
+  constexpr int kQuads = kAttnRows / 4;           // fours of rows
+  constexpr int kTasks = CL * kQuads * NC;        // of a unit: four rows, 64 columns
+  constexpr int kFewItems = kTasks / kJoinWarps;  // blocks of a unit of few pieces; kTasks of one of many
+  constexpr int kPiece = kAttnRows * NC * 64 / 4, kFlight = 4;
+  __shared__ float4 s_sum[kJoinWarps][2][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 3, kk = lane & 7;
   pdl_wait();
   const int4 head = *reinterpret_cast<const int4*>(p.head);
   if (head.x != 0) return;
-  for (int item = blockIdx.x; item < head.y * kParts; item += gridDim.x) {
-    const AttnJoin& J = p.joins[item / kParts];
-    const int part = item % kParts / kSplit, rank = part / (kAttnRows / 4), quarter = part % (kAttnRows / 4);
-    const int columns = (item % kSplit) * JoinShape<NC>::kWarps + warp;  // block of 32
+  const int few_items = head.y * kFewItems, items = few_items + head.z * kTasks;  // (of at most one unit a worker)
+  for (int item = blockIdx.x; item < items; item += gridDim.x) {
+    const bool few = item < few_items;
+    const int rest = few ? item : item - few_items;
+    const int task = few ? rest % kFewItems * kJoinWarps + warp : rest % kTasks;
+    const AttnJoin& J = p.joins[few ? rest / kFewItems : p.workers - 1 - rest / kTasks];
+    const int quad = task % kQuads, chunk = task / kQuads % NC, rank = task / (kQuads * NC);
     const AttnUnit u = J.u;
-    const int i = J.worker, n = J.pieces;
-    const int r0 = quarter * 4, row0 = (u.block * CL + rank) * kAttnRows + r0;
-    if (row0 >= u.rows) continue;
-    auto slot = [&](int k) { return (2 * static_cast<int64_t>(i + k) + (k == 0 ? 1 : 0)) * CL + rank; };
-
-    float sink_e[4], mx[4], den[4], acc[4];
-    bool some[4];
+    const int first = J.worker, n = J.pieces;
+    const int row0 = (u.block * CL + rank) * kAttnRows + quad * 4, row = row0 + r;
+    if (row0 >= u.rows) continue;  // (all of a block's warps, where they share a task)
+    auto slot = [&](int k) { return (2 * static_cast<int64_t>(first + k) + (k == 0 ? 1 : 0)) * CL + rank; };
+    const float4* o = reinterpret_cast<const float4*>(p.part_o) + (chunk * 2 * kQuads + quad) * 32 + lane;
+    const float* ml = p.part_ml + quad * 4 + r;
+    const int step = few ? kFlight : kFlight * kJoinWarps;
+    int k0 = few ? 0 : warp * kFlight;
+    float4 v[kFlight][2];
+    float m0;  // piece k0 + kk's bound
+    auto fetch = [&]() {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int row = row0 + r;
-      sink_e[r] = p.sink != nullptr && row < u.rows ? p.sink[u.kvh * p.group + row % p.group] : -INFINITY;
-      mx[r] = sink_e[r] * kLog2e;
-      some[r] = false;
-      den[r] = acc[r] = 0.f;
-    }
-    auto read = [&](int k, float (&m)[4], float (&z)[4]) {
-      const float* ml = p.part_ml + slot(k) * 2 * kAttnRows + r0;
-      const float4 a = *reinterpret_cast<const float4*>(ml), b = *reinterpret_cast<const float4*>(ml + kAttnRows);
-      m[0] = a.x, m[1] = a.y, m[2] = a.z, m[3] = a.w;
-      z[0] = b.x, z[1] = b.y, z[2] = b.z, z[3] = b.w;
+      for (int k = 0; k < kFlight; ++k)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          v[k][h] = k0 + k < n ? o[slot(k0 + k) * kPiece + h * (kQuads * 32)] : make_float4(0.f, 0.f, 0.f, 0.f);
+      m0 = k0 + kk < n ? ml[slot(k0 + kk) * 2 * kAttnRows] : kNoMax;
     };
-    for (int k = lane; k < n; k += 32) {
-      float m[4], z[4];
-      read(k, m, z);
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        if (!(z[r] <= 0.f)) {
-          mx[r] = fmaxf(mx[r], m[r]);
-          some[r] = true;
-        }
-    }
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      mx[r] = warp_max_f32(mx[r]);
-      some[r] = __any_sync(0xFFFFFFFFu, some[r]);
-    }
-    const float4* o = reinterpret_cast<const float4*>(p.part_o) + (columns * (kAttnRows / 4) + quarter) * 32 + lane;
-    for (int k0 = 0; k0 < n; k0 += 32) {
-      float f[4] = {0.f, 0.f, 0.f, 0.f};
-      if (k0 + lane < n) {
-        float m[4], z[4];
-        read(k0 + lane, m, z);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          f[r] = mx[r] == -INFINITY ? 0.f : fast_exp2(m[r] - mx[r]);
-          den[r] += f[r] * z[r];
-        }
-      }
-      const int some_k = min(32, n - k0);
-#pragma unroll 1
-      for (int k1 = 0; k1 < some_k; k1 += 4) {
-        float4 v[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          v[k] = k1 + k < some_k ? o[slot(k0 + k1 + k) * kPiece] : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          acc[0] = fmaf(__shfl_sync(0xFFFFFFFFu, f[0], k1 + k), v[k].x, acc[0]);
-          acc[1] = fmaf(__shfl_sync(0xFFFFFFFFu, f[1], k1 + k), v[k].y, acc[1]);
-          acc[2] = fmaf(__shfl_sync(0xFFFFFFFFu, f[2], k1 + k), v[k].z, acc[2]);
-          acc[3] = fmaf(__shfl_sync(0xFFFFFFFFu, f[3], k1 + k), v[k].w, acc[3]);
-        }
+    fetch();
+    const int token = row / p.group, head_of = u.kvh * p.group + (row - token * p.group);
+    const int64_t at = static_cast<int64_t>(u.token) + token, out_at = at * p.out_row + head_of * p.out_head;
+    const float sink_e = p.sink != nullptr && row < u.rows ? __ldg(p.sink + head_of) : -INFINITY;
+    float mx = sink_e * kLog2e, den = 0.f;
+    bool some = false;
+    for (int k = kk; k < n; k += 8) {
+      const float* x = ml + slot(k) * 2 * kAttnRows;
+      const float m = x[0], z = x[kAttnRows];
+      if (!(z <= 0.f)) {
+        mx = fmaxf(mx, m);
+        some = true;
       }
     }
+    some = (__ballot_sync(0xFFFFFFFFu, some) >> (8 * r) & 0xFFu) != 0;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int row = row0 + r;
-#pragma unroll
-      for (int s = 16; s > 0; s >>= 1) den[r] += __shfl_xor_sync(0xFFFFFFFFu, den[r], s);
-      if (row >= u.rows) continue;
-      const int head_of = u.kvh * p.group + row % p.group;
-      const int64_t token = static_cast<int64_t>(u.token) + row / p.group;
-      const float all = mx[r] == -INFINITY ? 1.f : den[r] + fast_exp2(sink_e[r] * kLog2e - mx[r]);
-      const int col = columns * 32 + lane;
-      if (col < p.d)
-        p.out[token * p.out_row + head_of * p.out_head + col] = Element<CSA_DTYPE_BF16>::from_float(acc[r] * (1.f / all));
-      if (p.lse != nullptr && columns == 0 && lane == 0)
-        p.lse[token * p.q_heads + head_of] = some[r] ? (mx[r] + log2f(all)) * kLn2 : sink_e[r];
+    for (int s = 4; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, s));
+    for (int k = kk; k < n; k += 8) {
+      const float* x = ml + slot(k) * 2 * kAttnRows;
+      den += mx == -INFINITY ? 0.f : fast_exp2(x[0] - mx) * x[kAttnRows];
     }
+#pragma unroll
+    for (int s = 4; s > 0; s >>= 1) den += __shfl_xor_sync(0xFFFFFFFFu, den, s);
+    const float all = mx == -INFINITY ? 1.f : den + fast_exp2(sink_e * kLog2e - mx), inverse = 1.f / all;
+    float4 acc[2] = {};
+    while (true) {
+      const float f = mx == -INFINITY ? 0.f : fast_exp2(m0 - mx);
+#pragma unroll
+      for (int k = 0; k < kFlight; ++k) {
+        const float fx = __shfl_sync(0xFFFFFFFFu, f, k), fy = __shfl_sync(0xFFFFFFFFu, f, 8 + k);
+        const float fz = __shfl_sync(0xFFFFFFFFu, f, 16 + k), fw = __shfl_sync(0xFFFFFFFFu, f, 24 + k);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          acc[h].x = fmaf(fx, v[k][h].x, acc[h].x);
+          acc[h].y = fmaf(fy, v[k][h].y, acc[h].y);
+          acc[h].z = fmaf(fz, v[k][h].z, acc[h].z);
+          acc[h].w = fmaf(fw, v[k][h].w, acc[h].w);
+        }
+      }
+      k0 += step;
+      if (k0 >= n) break;
+      fetch();
+    }
+    if (!few) {
+      s_sum[warp][0][lane] = acc[0];
+      s_sum[warp][1][lane] = acc[1];
+      __syncthreads();
+      if (warp < 2) {
+        acc[0] = s_sum[0][warp][lane];
+#pragma unroll
+        for (int k = 1; k < kJoinWarps; ++k) {
+          const float4 w = s_sum[k][warp][lane];
+          acc[0].x += w.x, acc[0].y += w.y, acc[0].z += w.z, acc[0].w += w.w;
+        }
+      }
+      __syncthreads();
+      if (warp >= 2) continue;
+    }
+    const int col = chunk * 64 + (few ? 0 : warp * 32) + lane;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float f = __shfl_sync(0xFFFFFFFFu, inverse, 8 * i);
+      uint16_t* to = p.out + __shfl_sync(0xFFFFFFFFu, out_at, 8 * i) + col;
+      const float a = i == 0 ? acc[0].x : i == 1 ? acc[0].y : i == 2 ? acc[0].z : acc[0].w;
+      const float b = i == 0 ? acc[1].x : i == 1 ? acc[1].y : i == 2 ? acc[1].z : acc[1].w;
+      if (row0 + i < u.rows) {
+        if (col < p.d) to[0] = Element<CSA_DTYPE_BF16>::from_float(a * f);
+        if (few && col + 32 < p.d) to[32] = Element<CSA_DTYPE_BF16>::from_float(b * f);
+      }
+    }
+    if (p.lse != nullptr && chunk == 0 && (few || warp == 0) && kk == 0 && row < u.rows)
+      p.lse[at * p.q_heads + head_of] = some ? (mx + log2f(all)) * kLn2 : sink_e;
   }
 }
 
