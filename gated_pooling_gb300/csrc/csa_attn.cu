@@ -445,9 +445,15 @@ extern "C" csa_status_t csa_cache_attn(
     const int nc = tile_chunks(d);
     // bf16: tensor copies straight from the pages where a power of two of at least 8 entries
     // divides the page: smaller boxes copy slower than threads (8 entries 3.2 TB/s from L2,
-    // 16 4.2, 64 and up 5.7). Codes come by threads, which have to widen them: copied first, 48
-    // sequences of up to 8192 entries took 32.5 instead of 32.0 us at d = 128, 45.9 instead of 45.6 at 256,
-    // and 80.4 instead of 77.8 at 512.
+    // 16 4.2, 64 and up 5.7). 48 sequences of up to 8192 entries, 8 heads of 128: 104 us against 165
+    // by threads; 4 of 256: 91 against 134. At d > 256, where shared memory holds one tile,
+    // the next one's copies wait for room that threads need not have (they load into registers):
+    // 104 us against 79, so copies only if every share is about one tile (18.6 against 21.1 for one
+    // token over 512 entries). Codes come by threads, which have to widen them: copied first,
+    // the same sequences took 32.5 instead of 32.0 us at d = 128, 45.9 instead of 45.6 at 256, and
+    // 80.4 instead of 77.8 at 512.
+    const int64_t most_tiles = p.max_units * ((max_entries + kAttnEntries - 1) / kAttnEntries);
+    const bool copies = format == CSA_CACHE_BF16 && (nc < 8 || most_tiles <= p.workers);
     p.box_rows = 1;
     while (p.box_rows < kAttnEntries && page_size % (2 * p.box_rows) == 0) p.box_rows *= 2;
     CUtensorMap map{};
@@ -459,7 +465,7 @@ extern "C" csa_status_t csa_cache_attn(
       const uint64_t strides[1] = {static_cast<uint64_t>(nc) * 128};
       const uint32_t box[2] = {64, kAttnEntries};
       if (!encode_boxes(&map, p.packed, 2, dims, strides, box)) return CSA_ERR_CUDA;
-    } else if (format == CSA_CACHE_BF16 && p.box_rows >= 8 && num_pages > 0 && num_pages <= INT_MAX / page_size) {
+    } else if (copies && p.box_rows >= 8 && num_pages > 0 && num_pages <= INT_MAX / page_size) {
       const uint64_t row = d;
       const uint64_t dims[3] = {row, static_cast<uint64_t>(kv_heads), static_cast<uint64_t>(num_pages) * page_size};
       const uint64_t strides[2] = {row * 2, row * 2 * kv_heads};

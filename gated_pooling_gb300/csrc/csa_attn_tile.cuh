@@ -524,14 +524,6 @@ __device__ void tile_copy(const AttnParams& p, TileSmall& sm, uint32_t base, con
           if (on) slot = page * p.page_size + e % p.page_size;
           else if (p.dev_error != nullptr) *p.dev_error = CSA_DEVERR_PAGE;
         }
-        // the next tile's boxes on their way into L2 meanwhile
-        const int e1 = e + kAttnEntries;
-        if (chunk < 2 && tile + 1 < w.t1 && e1 < w.u.seen) {
-          const int page = __ldg(p.table + static_cast<int64_t>(w.u.s) * p.max_pages + e1 / p.page_size);
-          if (page >= 0 && page < p.num_pages)
-            for (int c = 0; c < SH::kPairs; ++c)
-              box_prefetch3(map, c * 128 + chunk * 64, w.u.kvh, page * p.page_size + e1 % p.page_size);
-        }
         const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, on)) * p.box_rows * 128;
         for (int c = 0; c < SH::kPairs; ++c, ring.next(), ++issued) {
           tile_wait(sm, p, &sm.empty[ring.slot], ring.lap ^ 1u);

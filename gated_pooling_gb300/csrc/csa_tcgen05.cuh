@@ -87,10 +87,6 @@ __device__ __forceinline__ void box_load3(uint32_t dst, const CUtensorMap* map, 
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
       : "memory");
 }
-__device__ __forceinline__ void box_prefetch3(const CUtensorMap* map, int x, int y, int z) {
-  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(map), "r"(x), "r"(y), "r"(z)
-               : "memory");
-}
 __device__ __forceinline__ void box_load2_all(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar,
                                               uint16_t mask) {
   asm volatile(
