@@ -330,11 +330,11 @@ cudaError_t plan_sizes(AttnParams& p, int* sms, int32_t S, int64_t tokens, int32
   return cudaSuccess;
 }
 
-// Whether a call's chunks are long enough for pairs of CTAs over packed entries: 256 rows (two
+// Whether a call's chunks may be long enough for pairs of CTAs over packed entries: kChunkRows rows (two
 // units) a sequence on average, so that packing an entry (read and written once) is small
-// beside the units that read it, and packed entries within kMaxPacked bytes. Measured: 606
-// GFLOP of three chunks of up to 1024 tokens x 64 heads of 512
-constexpr int64_t kChunkRows = 256;
+// beside the units that read it, and packed entries within kMaxPacked bytes. (The workspace has
+// room for them then; the call decides, where it knows the cache.)
+constexpr int64_t kChunkRows = 256, kChunkRowsWide = 384;
 constexpr int64_t kMaxPacked = int64_t{4} << 30;
 bool chunked(const AttnParams& p) {
   if (p.d > kTileMaxDim || p.S < 1 || p.tokens * p.group < kChunkRows * p.S) return false;
@@ -403,11 +403,36 @@ extern "C" csa_status_t csa_cache_attn(
     p.head = static_cast<AttnHead*>(workspace);
   }
   if (!tile) p.units = nullptr;
-  const bool chunks = tile && chunked(p);
+  const int nc = tile_chunks(d);
+  // bf16: tensor copies straight from the pages where a power of two of at least 8 entries
+  // divides the page: smaller boxes copy slower than threads (8 entries 3.2 TB/s from L2,
+  // 16 4.2, 64 and up 5.7). 48 sequences of up to 8192 entries, 8 heads of 128: 104 us against 165
+  // by threads; 4 of 256: 91 against 134. At d > 256, where shared memory holds one tile,
+  // the next one's copies wait for room that threads need not have (they load into registers):
+  // 104 us against 79, so copies only if every share is about one tile (18.6 against 21.1 for one
+  // token over 512 entries). Codes come by threads, which have to widen them: copied first,
+  // the same sequences took 32.5 instead of 32.0 us at d = 128, 45.9 instead of 45.6 at 256, and
+  // 80.4 instead of 77.8 at 512.
+  p.box_rows = 1;
+  while (p.box_rows < kAttnEntries && page_size % (2 * p.box_rows) == 0) p.box_rows *= 2;
+  const int64_t most_tiles = p.max_units * ((max_entries + kAttnEntries - 1) / kAttnEntries);
+  const bool copies = format == CSA_CACHE_BF16 && p.box_rows >= 8 && num_pages > 0 &&
+                      num_pages <= INT_MAX / page_size && (nc < 8 || most_tiles <= p.workers);
+  // Packing first. Up to d = 256 a tile's time is the softmax's, so packing entries that can be copied
+  // from the pages gains nothing (3 chunks of 1024 tokens x 64 heads of 256: 974 us packed, 973 not;
+  // 48 of 8 tokens: 211 and 170). Codes are widened once instead of by every unit (974 and
+  // 1784), from 256 rows a sequence on at d = 128 (417 and 560), later above (256 rows of 256: 134
+  // and 125, of 512: 251 and 227; 384 of 512: 311 and 312; 512 of 256: 212 and 238, of 512: 400 and
+  // 441). bf16 at d = 512: 256 rows 252 and 277, three chunks of 1024 tokens 700 and 1345.
+  const bool wide = format != CSA_CACHE_BF16 && d > 128;
+  const bool chunks = tile && chunked(p) && !(copies && nc < 8) &&
+                      tokens * p.group >= (wide ? kChunkRowsWide : kChunkRows) * S;
   // A unit's own cost (q in, output out, the pipeline's start) in tiles, by which shares are
-  // evened out: measured best of 1 to 12 for chunks at d = 512 (606 GFLOP in 731 us; at 1 867 us)
-  // and 128 (86 GFLOP in 138 us; at 1 161 us), and for single tokens (84 us; at 4 89 us).
-  p.unit_cost = 1;
+  // evened out, measured best of 1 to 14. Packed: d = 512 (606 GFLOP in 731 us; at 1 867 us) and
+  // 128 (86 GFLOP in 138 us; at 1 161 us). Single tokens: 48 sequences at d = 512 67.0 us (at 1
+  // 70.2), and where copies make the tiles short, with 8 heads of 128, 79 us (at 1 104; 48
+  // of 128 tokens 641, at 2 813); codes of 256 40.3 us (at 1 43.0, at 6 41.6).
+  p.unit_cost = copies && nc < 8 ? 6 : 2;
   if (chunks) {
     p.workers = sms / 2;
     p.unit_rows = 2 * kAttnRows;
@@ -442,20 +467,6 @@ extern "C" csa_status_t csa_cache_attn(
   if (blocks_per_sm(dev, plan, kPlanThreads, plan_smem, &bps) != cudaSuccess) return CSA_ERR_CUDA;
   if (launch_pdl(plan, dim3(1), dim3(kPlanThreads), plan_smem, cs, args) != cudaSuccess) return CSA_ERR_CUDA;
   if (tile) {
-    const int nc = tile_chunks(d);
-    // bf16: tensor copies straight from the pages where a power of two of at least 8 entries
-    // divides the page: smaller boxes copy slower than threads (8 entries 3.2 TB/s from L2,
-    // 16 4.2, 64 and up 5.7). 48 sequences of up to 8192 entries, 8 heads of 128: 104 us against 165
-    // by threads; 4 of 256: 91 against 134. At d > 256, where shared memory holds one tile,
-    // the next one's copies wait for room that threads need not have (they load into registers):
-    // 104 us against 79, so copies only if every share is about one tile (18.6 against 21.1 for one
-    // token over 512 entries). Codes come by threads, which have to widen them: copied first,
-    // the same sequences took 32.5 instead of 32.0 us at d = 128, 45.9 instead of 45.6 at 256, and
-    // 80.4 instead of 77.8 at 512.
-    const int64_t most_tiles = p.max_units * ((max_entries + kAttnEntries - 1) / kAttnEntries);
-    const bool copies = format == CSA_CACHE_BF16 && (nc < 8 || most_tiles <= p.workers);
-    p.box_rows = 1;
-    while (p.box_rows < kAttnEntries && page_size % (2 * p.box_rows) == 0) p.box_rows *= 2;
     CUtensorMap map{};
     int source = format;
     if (chunks) {
@@ -465,7 +476,7 @@ extern "C" csa_status_t csa_cache_attn(
       const uint64_t strides[1] = {static_cast<uint64_t>(nc) * 128};
       const uint32_t box[2] = {64, kAttnEntries};
       if (!encode_boxes(&map, p.packed, 2, dims, strides, box)) return CSA_ERR_CUDA;
-    } else if (copies && p.box_rows >= 8 && num_pages > 0 && num_pages <= INT_MAX / page_size) {
+    } else if (copies) {
       const uint64_t row = d;
       const uint64_t dims[3] = {row, static_cast<uint64_t>(kv_heads), static_cast<uint64_t>(num_pages) * page_size};
       const uint64_t strides[2] = {row * 2, row * 2 * kv_heads};
