@@ -367,3 +367,34 @@ def test_a_table_much_larger_than_its_sequences(cuda_lib):
     wide[:, :c.table.shape[1]] = c.table
     c.table, c.max_pages = wide, 4000
     c.check(cuda_lib)
+
+
+@pytest.mark.parametrize("fmt", [R.BF16, R.E4M3, R.FP4])
+@pytest.mark.parametrize("H,kv,d", [(16, 1, 128), (8, 1, 256), (64, 1, 512)])
+@pytest.mark.parametrize("entries", [[1030], [1500, 9], [3001, 0, 2500, 128, 129], [20500]])
+def test_shares_of_long_contexts(cuda_lib, fmt, H, kv, d, entries):
+    """One token over contexts that many workers share: units of two pieces to more than 32, the widest
+    heads' entries by copies (short tables) and by threads (long ones)."""
+    n = len(entries)
+    Case([1] * n, entries, H, kv, d, fmt, page=64, ratio=0, sink=True, seed=sum(entries) + d).check(cuda_lib)
+
+
+@pytest.mark.parametrize("fmt", [R.BF16, R.E4M3, R.FP4])
+@pytest.mark.parametrize("H,kv,d,lens", [(64, 1, 128, [5, 9]), (16, 2, 96, [60, 41, 3]), (32, 1, 256, [14, 0, 26]),
+                                         (32, 1, 320, [13, 25])])
+def test_packed_from_any_page(cuda_lib, fmt, H, kv, d, lens):
+    """Chunks of enough rows to be packed, from pages that no tensor copy takes."""
+    Case(lens, [430, 131, 255][:len(lens)], H, kv, d, fmt, page=9, ratio=1, first="end", sink=True,
+         seed=H + d).check(cuda_lib)
+
+
+@pytest.mark.parametrize("d", [128, 512])
+def test_joins_of_pieces_that_see_nothing(cuda_lib, d):
+    """Rows whose early positions hide most of a shared unit's entries, or all: some pieces, then every one, weigh
+    nothing."""
+    c = Case([40], [3000], 16, 1, d, page=64, ratio=1, first=[30], seed=d)
+    c.check(cuda_lib)
+    c = Case([40], [3000], 16, 1, d, page=64, ratio=1, first=[2950], seed=d)
+    c.check(cuda_lib)
+    c = Case([3, 2], [2600, 2600], 16, 1, d, page=64, ratio=64, first=[0, 70], sink=True, seed=d)
+    c.check(cuda_lib)
