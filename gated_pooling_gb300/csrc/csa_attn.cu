@@ -271,7 +271,8 @@ csa_status_t check_attn_sizes(int32_t S, int64_t tokens, int32_t q_heads, int32_
   if (S < 0 || tokens < 0 || q_heads < 1 || kv_heads < 1 || d < 1 || max_entries < 0 ||
       q_heads % kv_heads != 0)
     return CSA_ERR_INVALID_VALUE;
-  if (d > CSA_MAX_HEAD_DIM || S > CSA_MAX_SEGMENTS || tokens > INT_MAX / q_heads ||
+  // (row numbers go up to a last unit's end in 32 bits)
+  if (d > CSA_MAX_HEAD_DIM || S > CSA_MAX_SEGMENTS || tokens > (INT_MAX - 256) / q_heads ||
       max_entries > INT_MAX)
     return CSA_ERR_UNSUPPORTED;
   return CSA_OK;
@@ -330,10 +331,10 @@ cudaError_t plan_sizes(AttnParams& p, int* sms, int32_t S, int64_t tokens, int32
   return cudaSuccess;
 }
 
-// Whether a call's chunks may be long enough for pairs of CTAs over packed entries: kChunkRows rows (two
-// units) a sequence on average, so that packing an entry (read and written once) is small
-// beside the units that read it, and packed entries within kMaxPacked bytes. (The workspace has
-// room for them then; the call decides, where it knows the cache.)
+// Whether a call's chunks may be long enough for pairs of CTAs over packed entries: kChunkRows
+// rows (two units) a sequence on average, so that packing an entry (read and written once) is
+// small beside the units that read it, and packed entries within kMaxPacked bytes. (The
+// workspace has room for them then; the call decides, where it knows the cache.)
 constexpr int64_t kChunkRows = 256, kChunkRowsWide = 384;
 constexpr int64_t kMaxPacked = int64_t{4} << 30;
 bool chunked(const AttnParams& p) {

@@ -81,7 +81,7 @@ __device__ __forceinline__ int visible(int64_t pos, int ratio, int n) {
                                            : static_cast<uint64_t>(pos + 1) / static_cast<uint32_t>(ratio);
   return done < static_cast<uint64_t>(n) ? static_cast<int>(done) : n;
 }
-// Rows of a sequence and cache head (below 2^31: tokens * q_heads is).
+// Rows of a sequence and cache head (below 2^31 - 256: tokens * q_heads is).
 __device__ __forceinline__ int sequence_rows(const AttnParams& p, int s) {
   return (__ldg(p.cu + s + 1) - __ldg(p.cu + s)) * p.group;
 }

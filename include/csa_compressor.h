@@ -360,8 +360,9 @@ csa_status_t csa_cache_write(const void* x, int32_t dtype, int64_t rows, int32_t
                              int32_t* dev_error, csa_stream_t stream);
 
 /* Reads rows of the cache back: out[r] = the entry in slots[r], in `dtype`, out [rows, heads,
- * d] with strides in elements that give every element a place of its own. A negative slot leaves its row of out as it was, so does one
- * >= num_slots, which reports CSA_DEVERR_SLOT. Any slot may be read by several rows. */
+ * d] with strides in elements that give every element a place of its own. A negative slot
+ * leaves its row of out as it was, so does one >= num_slots, which reports CSA_DEVERR_SLOT. Any
+ * slot may be read by several rows. */
 csa_status_t csa_cache_read(const void* data, const uint8_t* scales, int32_t format,
                             const int64_t* slots, int64_t rows, int64_t num_slots, int32_t heads,
                             int32_t d, void* out, int32_t dtype, int64_t out_row_stride,
@@ -406,10 +407,15 @@ size_t csa_cache_attn_workspace_bytes(int32_t S, int64_t tokens, int32_t q_heads
  * multiple of kv_heads, negative sizes or strides, strides of out under which two elements share
  * a place, softmax_scale not finite. CSA_ERR_UNSUPPORTED: d >
  * CSA_MAX_HEAD_DIM, quantised formats with d not a multiple of 32, S > CSA_MAX_SEGMENTS,
- * tokens * q_heads or max_pages * page_size >= 2^31, an unknown format. A bad
+ * tokens * q_heads >= 2^31 - 256, max_pages * page_size >= 2^31, an unknown format. A bad
  * cu_seqlens or entries (CSA_DEVERR_CU_SEQLENS, CSA_DEVERR_ENTRIES) skips all outputs; after
  * CSA_DEVERR_PAGE the outputs of that sequence are unspecified. Results are bitwise
- * reproducible for the same arguments on the same device. */
+ * reproducible for the same arguments on the same device. The tensor-core kernel runs when
+ * d <= 512, d and the strides of q and out are multiples of 8, and q, out and data 16-byte
+ * aligned; anything else takes a scalar kernel, many times slower. With many new tokens a
+ * sequence the workspace has room for the sequences' entries as bf16 rows of 128, 256 or 512
+ * columns (up to 4 GiB, of max_entries each). A wait that runs out reports CSA_DEVERR_TIMEOUT
+ * and leaves the outputs unspecified. */
 csa_status_t csa_cache_attn(const void* q, int64_t q_row_stride, int64_t q_head_stride,
                             const int32_t* cu_seqlens, int32_t S, int64_t tokens, int32_t q_heads,
                             int32_t kv_heads, int32_t d, const void* data, const uint8_t* scales,

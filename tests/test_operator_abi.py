@@ -199,6 +199,13 @@ def test_attn_refusals(lib, over, code):
     assert attn(lib, **over) == code
 
 
+@pytest.mark.parametrize("tokens", [(1 << 31) - 1, (1 << 31) - 128, (1 << 31) - 256])
+def test_attn_row_numbers_stay_in_32_bits(lib, tokens):
+    """A unit's rows are numbered up to its end, 64 or 128 rows on from its first."""
+    assert attn(lib, tokens=tokens, H=1, kv=1) == UNSUPPORTED
+    assert gp.csa_cache_attn_workspace_bytes(2, tokens, 1, 1, 64, 64) == 0
+
+
 def test_attn_workspace_query_refuses(lib):
     for bad in ((-1, 1, 1, 1, 64, 16), (1, -1, 1, 1, 64, 16), (1, 1, 3, 2, 64, 16), (1, 1, 1, 1, 0, 16),
                 (1, 1, 1, 1, 1025, 16), (1, 1, 1, 1, 64, -1), (1, 1 << 30, 4, 1, 64, 16)):
