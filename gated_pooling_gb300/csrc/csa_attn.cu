@@ -411,7 +411,7 @@ extern "C" csa_status_t csa_cache_attn(
   // by threads; 4 of 256: 91 against 134. At d > 256, where shared memory holds one tile,
   // the next one's copies wait for room that threads need not have (they load into registers):
   // 104 us against 79, so copies only if every share is about one tile (18.6 against 21.1 for one
-  // token over 512 entries). Codes come by threads, which have to widen them: copied first,
+  // token over 2048 entries). Codes come by threads, which have to widen them: copied first,
   // the same sequences took 32.5 instead of 32.0 us at d = 128, 45.9 instead of 45.6 at 256, and
   // 80.4 instead of 77.8 at 512.
   p.box_rows = 1;
