@@ -429,15 +429,16 @@ extern "C" csa_status_t csa_cache_attn(
   const bool chunks = tile && chunked(p) && !(copies && nc < 8) &&
                       tokens * p.group >= (wide ? kChunkRowsWide : kChunkRows) * S;
   // A unit's own cost (q in, output out, the pipeline's start) in tiles, by which shares are
-  // evened out, measured best of 1 to 14. Packed: d = 512 (606 GFLOP in 731 us; at 1 867 us) and
-  // 128 (86 GFLOP in 138 us; at 1 161 us). Single tokens: 48 sequences at d = 512 67.0 us (at 1
+  // evened out, measured best of 1 to 14. Packed: three chunks of 1024 tokens x 64 heads of 512 952 us
+  // (at 2 975, at 6 1010), of 256 957 (at 2 1014, at 8 989); 48 of 64 tokens over 8 heads of 128 420
+  // (at 2 451, at 8 422). Single tokens: 48 sequences at d = 512 67.0 us (at 1
   // 70.2), and where copies make the tiles short, with 8 heads of 128, 79 us (at 1 104; 48
   // of 128 tokens 641, at 2 813); codes of 256 40.3 us (at 1 43.0, at 6 41.6).
   p.unit_cost = copies && nc < 8 ? 6 : 2;
   if (chunks) {
     p.workers = sms / 2;
     p.unit_rows = 2 * kAttnRows;
-    p.unit_cost = d > 256 ? 4 : 6;
+    p.unit_cost = nc == 8 ? 3 : nc == 4 ? 4 : 6;
   }
   p.q = static_cast<const uint16_t*>(q);
   p.cu = cu_seqlens;
