@@ -811,25 +811,32 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
     }
     barrier_group();
     if (whole) {
-      // O^T times the rows' factors, as bf16 rows in q's buffer, then out in 16-byte pieces
-      uint16_t* stage = reinterpret_cast<uint16_t*>(smem + SH::kQOff);
+      // O^T times the rows' factors, as bf16 rows in q's buffer (transposed by 8 x 8 matrices; 16-byte pieces
+      // change places within 128 bytes by row, as in the tiles), then out in 16-byte pieces
+      constexpr int kPer = NC * 8;
+      const int c = c0 + 2 * (lane & 3);
+      const float f0 = sm.fac[c], f1 = sm.fac[c + 1], f2 = sm.fac[c + 8], f3 = sm.fac[c + 9];
+      const int to_row = c0 + ((lane >> 4) << 3) + (lane & 7), to_piece = quad * 4 + ((lane >> 3) & 1);
+      const uint32_t to = base + SH::kQOff + to_row * (SH::kDpad * 2);
 #pragma unroll 1
       for (int b = 0; b < SH::kPairs; ++b) {
-        float v[kSoftCols];
-        tmem_load16(lanes + SH::kTmemO + b * kAttnRows + c0, v);
+        float v[2][8];
+        tmem_load_fragments(lanes + SH::kTmemO + b * kAttnRows + c0, v);
 #pragma unroll
-        for (int c = 0; c < kSoftCols; ++c)
-          stage[(c0 + c) * SH::kDpad + b * 128 + e0] = Element<CSA_DTYPE_BF16>::from_float(v[c] * sm.fac[c0 + c]);
+        for (int h = 0; h < 2; ++h)
+          store_transposed(to + (((b * 16 + to_piece + h * 2) ^ (to_row & 7)) << 4),
+                           pack_bf16x2(v[h][0] * f0, v[h][1] * f1), pack_bf16x2(v[h][2] * f0, v[h][3] * f1),
+                           pack_bf16x2(v[h][4] * f2, v[h][5] * f3), pack_bf16x2(v[h][6] * f2, v[h][7] * f3));
       }
       tc_fence_before();
       barrier_group();
-      constexpr int kPer = NC * 8;
 #pragma unroll 1
       for (int i = (tid & 127); i < kSoftCols * kPer; i += 128) {
         const int r = c0 + i / kPer, c = i % kPer;
         const int64_t at = sm.out_at[r];
         if (at >= 0 && c * 8 < p.d)
-          *reinterpret_cast<uint4*>(p.out + at + c * 8) = lds128(base + SH::kQOff + r * (SH::kDpad * 2) + c * 16);
+          *reinterpret_cast<uint4*>(p.out + at + c * 8) =
+              lds128(base + SH::kQOff + r * (SH::kDpad * 2) + ((c ^ (r & 7)) << 4));
       }
     } else {
       // four rows of a column in 16 bytes, a warp's 32 columns side by side
