@@ -420,25 +420,25 @@ extern "C" csa_status_t csa_cache_attn(
   const bool copies = format == CSA_CACHE_BF16 && p.box_rows >= 8 && num_pages > 0 &&
                       num_pages <= INT_MAX / page_size && (nc < 8 || most_tiles <= p.workers);
   // Packing first. Up to d = 256 a tile's time is the softmax's, so packing entries that can be copied
-  // from the pages gains nothing (3 chunks of 1024 tokens x 64 heads of 256: 974 us packed, 973 not;
-  // 48 of 8 tokens: 211 and 170). Codes are widened once instead of by every unit (974 and
+  // from the pages gains nothing (3 chunks of 1024 tokens x 64 heads of 256: 922 us packed, 936 not;
+  // 48 of 8 tokens: 211 and 170). Codes are widened once instead of by every unit (922 and
   // 1784), from 256 rows a sequence on at d = 128 (417 and 560), later above (256 rows of 256: 134
   // and 125, of 512: 251 and 227; 384 of 512: 311 and 312; 512 of 256: 212 and 238, of 512: 400 and
-  // 441). bf16 at d = 512: 256 rows 252 and 277, three chunks of 1024 tokens 700 and 1345.
+  // 441). bf16 at d = 512: 256 rows 252 and 277, three chunks of 1024 tokens 894 and 1345.
   const bool wide = format != CSA_CACHE_BF16 && d > 128;
   const bool chunks = tile && chunked(p) && !(copies && nc < 8) &&
                       tokens * p.group >= (wide ? kChunkRowsWide : kChunkRows) * S;
-  // A unit's own cost (q in, output out, the pipeline's start) in tiles, by which shares are
-  // evened out, measured best of 1 to 14. Packed: three chunks of 1024 tokens x 64 heads of 512 952 us
-  // (at 2 975, at 6 1010), of 256 957 (at 2 1014, at 8 989); 48 of 64 tokens over 8 heads of 128 420
-  // (at 2 451, at 8 422). Single tokens: 48 sequences at d = 512 67.0 us (at 1
-  // 70.2), and where copies make the tiles short, with 8 heads of 128, 79 us (at 1 104; 48
-  // of 128 tokens 641, at 2 813); codes of 256 40.3 us (at 1 43.0, at 6 41.6).
-  p.unit_cost = copies && nc < 8 ? 6 : 2;
+  // A unit's own cost (q in, output out, the pipeline's start) in tiles, by which shares are evened
+  // out, measured best of 1 to 6. Packed: three chunks of 1024 tokens x 64 heads of 512 894 us (at 3
+  // 936, at 6 991), of 256 922 (at 1 958, at 6 950); 48 of 64 tokens over 8 heads of 128 420 (at 1
+  // 447). Otherwise: 48 single tokens at d = 512 67.8 us (at 4 71.7), over codes of 256 40.4 (at 1
+  // 41.3, at 6 42.1); where copies make the tiles short, 8 heads of 128, 78.3 us (at 1 98.2), and of
+  // 128 tokens each 637 (at 1 815).
+  p.unit_cost = copies && nc < 8 ? 5 : 2;
   if (chunks) {
     p.workers = sms / 2;
     p.unit_rows = 2 * kAttnRows;
-    p.unit_cost = nc == 8 ? 3 : nc == 4 ? 4 : 6;
+    p.unit_cost = nc == 8 ? 1 : nc == 4 ? 3 : 5;
   }
   p.q = static_cast<const uint16_t*>(q);
   p.cu = cu_seqlens;

@@ -26,6 +26,10 @@
 // sums are rescaled. Weights up to 2^8 lose nothing (bf16 and fp32 are floating), and the sums
 // stay per lane until the end of the unit.
 //
+// Between units: the next one's q is copied in as soon as the last scores are there, so that its
+// first scores are computed while the softmax warps bring this one's output out (7.3 thousand
+// cycles from the last sums to the next softmax instead of 13).
+//
 // Shared memory's 128 bytes a cycle bound the products (6 KB for 32 cycles' worth of them at 64
 // rows), HBM the decoding of a long cache.
 #pragma once
@@ -62,7 +66,7 @@ struct TileCta {
 constexpr int kSoftRegs = 64, kIssueRegs = 40, kLoadRegs = 104;
 constexpr int kChunkBytes = kAttnEntries * 128;  // 128 entries x 64 columns
 constexpr int kPairBytes = 2 * kChunkBytes;
-constexpr int kSmallBytes = 10240;
+constexpr int kSmallBytes = 11264;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNoMax = -1e30f;     // bound of a row that has seen nothing
 constexpr float kRescaleAt = 8.f;    // log2 of how far a weight may pass 1
@@ -83,7 +87,7 @@ struct TileShape {
   // widened: the softmax warps take the second half of its pairs.
   template <int SRC>
   static constexpr bool kHelped = (SRC == kFromE4m3 || SRC == kFromE2m1) && kRing == kPairs;
-  // shared memory: ring, Q (the output's staging too), P, then the small arrays
+  // shared memory: ring, Q, P (the output's staging too), then the small arrays
   static constexpr int kQOff = kRing * kPairBytes;
   static constexpr int kPOff = kQOff + kQBytes;
   static constexpr int kSmallOff = kPOff + kPBytes;
@@ -94,14 +98,14 @@ struct TileSmall {
   int64_t row[2][2][kAttnEntries];  // by fetching group and turn: bytes to an entry in the pool, -1: none
   int64_t help_row[2][kAttnEntries];   // the same for the softmax warps that widen
   int64_t q_at[kAttnRows];          // elements to a row of q, -1: none
-  int64_t out_at[kAttnRows];        // and of out
+  int64_t out_at[2][kAttnRows];     // and of out (this unit's and the next one's, as all with [2] here)
   AttnUnit next;                    // the worker's next unit
-  float sink[kAttnRows];
-  int32_t lse_at[kAttnRows];
+  float sink[2][kAttnRows];
+  int32_t lse_at[2][kAttnRows];
   float m[kAttnRows];
   float fac[kAttnRows];
   float red[4][kAttnRows];  // column maxima, then weight sums, by quadrant
-  int lim[kAttnRows];
+  int lim[2][kAttnRows];
   uint64_t full[5], empty[5], scores[2], probs, summed, q_full, drain;
   uint32_t tmem;
   int stop;
@@ -186,6 +190,10 @@ __device__ __forceinline__ uint4 widen_any(uint32_t w, float s) {
     r[i] = pack_bf16x2(f.x * s, f.y * s);
   }
   return make_uint4(r[0], r[1], r[2], r[3]);
+}
+// 16 bytes, or zeros, into shared memory without a register.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, bool some) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(some ? 16 : 0) : "memory");
 }
 constexpr uint32_t kNoScale = 0;  // no entry here: zeros at any scale
 template <int FORMAT>
@@ -617,46 +625,53 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
   auto barrier_group = [&]() { named_barrier(1 + group, 128); };
 
   const int worker = blockIdx.x / CL, rank = CL == 1 ? 0 : static_cast<int>(cluster_rank());
+  // where each row of a unit's q, out and lse lies, what it sees, its sink (rows behind the last one
+  // are zeros, see what the last one sees, and are never stored)
+  auto set_up = [&](const AttnUnit& u, int par) {
+    const int row = u.block * (CL * kAttnRows) + rank * kAttnRows + tid, token = row / p.group;
+    const bool some = row < u.rows;
+    const int head = u.kvh * p.group + (row - token * p.group);
+    const int64_t at = static_cast<int64_t>(u.token) + token;
+    sm.lim[par][tid] = some ? visible(static_cast<int64_t>(u.first) + token, p.ratio, u.n) : u.seen;
+    sm.q_at[tid] = some ? at * p.q_row + head * p.q_head : -1;
+    sm.out_at[par][tid] = some ? at * p.out_row + head * p.out_head : -1;
+    sm.lse_at[par][tid] = some ? static_cast<int32_t>(at * p.q_heads + head) : -1;
+    sm.sink[par][tid] = some && p.sink != nullptr ? __ldg(p.sink + head) : -INFINITY;
+  };
+  auto copy_q = [&]() {
+    constexpr int kPer = NC * 8;  // 16-byte pieces of a row; NC pieces a thread
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int at = tid + i * kSoftThreads, r = at / kPer, c = at % kPer;
+      const int64_t q_at = sm.q_at[r];
+      const bool some = q_at >= 0 && c * 8 < p.d;
+      copy16(base + SH::kQOff + (c >> 3) * (kAttnRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+             p.q + (some ? q_at + c * 8 : 0), some);
+    }
+  };
+  auto q_copied = [&]() {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.q_full);
+  };
+  int par = 0;
   SegmentWalk w(p, worker);
-  while (w.valid()) {
-    const int seen_all = w.u.seen_all;
-    const bool whole = w.t0 == 0 && w.t1 == w.u.tiles, more = !w.last();
-    // where each row of q, out and lse lies, what it sees, its sink (rows behind the last one are
-    // zeros, see what the last one sees, and are never stored); and the next unit on its way
+  if (w.valid()) {
     if (tid < kAttnRows) {
-      const int row = w.u.block * (CL * kAttnRows) + rank * kAttnRows + tid, token = row / p.group;
-      const bool some = row < w.u.rows;
-      const int head = w.u.kvh * p.group + (row - token * p.group);
-      const int64_t at = static_cast<int64_t>(w.u.token) + token;
-      sm.lim[tid] = some ? visible(static_cast<int64_t>(w.u.first) + token, p.ratio, w.u.n) : w.u.seen;
-      sm.q_at[tid] = some ? at * p.q_row + head * p.q_head : -1;
-      sm.out_at[tid] = some ? at * p.out_row + head * p.out_head : -1;
-      sm.lse_at[tid] = some ? static_cast<int32_t>(at * p.q_heads + head) : -1;
-      sm.sink[tid] = some && p.sink != nullptr ? __ldg(p.sink + head) : -INFINITY;
+      set_up(w.u, 0);
       sm.m[tid] = kNoMax;
-    } else if (more && tid >= kSoftThreads - 3) {
-      const int i = tid - (kSoftThreads - 3);
-      reinterpret_cast<int4*>(&sm.next)[i] = __ldg(reinterpret_cast<const int4*>(p.units + w.unit + 1) + i);
     }
     named_barrier(5, kSoftThreads);
-    {
-      constexpr int kPer = NC * 8;  // 16-byte pieces of a row; NC pieces a thread
-      uint4 v[NC];
-#pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        const int at = tid + i * kSoftThreads, r = at / kPer, c = at % kPer;
-        const int64_t q_at = sm.q_at[r];
-        v[i] = make_uint4(0, 0, 0, 0);
-        if (q_at >= 0 && c * 8 < p.d) v[i] = __ldg(reinterpret_cast<const uint4*>(p.q + q_at + c * 8));
-      }
-#pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        const int at = tid + i * kSoftThreads, r = at / kPer, c = at % kPer;
-        sts128(base + SH::kQOff + (c >> 3) * (kAttnRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4), v[i]);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.q_full);
+    copy_q();
+    q_copied();
+  }
+  for (; w.valid(); par ^= 1) {
+    const int seen_all = w.u.seen_all;
+    const bool whole = w.t0 == 0 && w.t1 == w.u.tiles, more = !w.last();
+    if (more && tid >= kSoftThreads - 3) {  // the next unit on its way
+      const int i = tid - (kSoftThreads - 3);
+      reinterpret_cast<int4*>(&sm.next)[i] = __ldg(reinterpret_cast<const int4*>(p.units + w.unit + 1) + i);
     }
     float l[kSoftCols];
 #pragma unroll
@@ -676,7 +691,7 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
         if (masked) {
 #pragma unroll
           for (int c = 0; c < kSoftCols; ++c)
-            if (e >= sm.lim[c0 + c]) {
+            if (e >= sm.lim[par][c0 + c]) {
               odd = odd || !(fabsf(s[c]) <= 3.4028234e38f);
               s[c] = sl2 < 0.f ? INFINITY : -INFINITY;  // -inf once scaled
             }
@@ -763,8 +778,9 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.probs);
       if (j == w.t0 && more) {
-        // the next unit's rows of q on their way into L2
+        // the next unit's places, and its rows of q on their way into L2
         named_barrier(5, kSoftThreads);
+        if (tid < kAttnRows) set_up(sm.next, par ^ 1);
         const int r = tid / NC, row = sm.next.block * (CL * kAttnRows) + rank * kAttnRows + r;
         const int col = (tid % NC) * 64;
         if (r < kAttnRows && row < sm.next.rows && col < p.d) {
@@ -776,6 +792,12 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
       }
     }
 
+    if (more) {
+      // q's place is free, the last scores being there: the next unit's rows come, and its first
+      // scores follow, while this one's sums go out
+      named_barrier(5, kSoftThreads);
+      copy_q();
+    }
     // the unit's (or its piece's) sums are complete
     tile_wait(sm, p, &sm.summed, (t - 1u) & 1u);
     tc_fence_after();
@@ -801,43 +823,48 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
         ml[c] = m;
         ml[kAttnRows + c] = z;
       } else {
-        const float sink_e = sm.sink[c], sink = sink_e * kLog2e;
+        const float sink_e = sm.sink[par][c], sink = sink_e * kLog2e;
         const float mx = fmaxf(z > 0.f || z != z ? m : -INFINITY, sink);
         const float old = mx == -INFINITY ? 0.f : fast_exp2(m - mx);
         const float den = mx == -INFINITY ? 0.f : z * old + fast_exp2(sink - mx);
         sm.fac[c] = mx == -INFINITY ? 0.f : old / den;
-        if (p.lse != nullptr && sm.lse_at[c] >= 0) p.lse[sm.lse_at[c]] = z == 0.f ? sink_e : (mx + log2f(den)) * kLn2;
+        if (p.lse != nullptr && sm.lse_at[par][c] >= 0) p.lse[sm.lse_at[par][c]] = z == 0.f ? sink_e : (mx + log2f(den)) * kLn2;
       }
+      sm.m[c] = kNoMax;  // for the next unit
     }
+    if (more) q_copied();
     barrier_group();
     if (whole) {
-      // O^T times the rows' factors, as bf16 rows in q's buffer (transposed by 8 x 8 matrices; 16-byte pieces
-      // change places within 128 bytes by row, as in the tiles), then out in 16-byte pieces
-      constexpr int kPer = NC * 8;
+      // O^T times the rows' factors, as bf16 rows: a warp's 32 columns of its 16 rows at a time are
+      // transposed by 8 x 8 matrices through its 1 KB of P's place (two rows to 128 bytes, their 16-byte
+      // pieces at other places from pair to pair), and go out in 16-byte pieces
       const int c = c0 + 2 * (lane & 3);
       const float f0 = sm.fac[c], f1 = sm.fac[c + 1], f2 = sm.fac[c + 8], f3 = sm.fac[c + 9];
-      const int to_row = c0 + ((lane >> 4) << 3) + (lane & 7), to_piece = quad * 4 + ((lane >> 3) & 1);
-      const uint32_t to = base + SH::kQOff + to_row * (SH::kDpad * 2);
+      const uint32_t stage = base + SH::kPOff + (tid >> 5) * 1024;
+      auto place = [&](int r, int piece) {
+        return stage + (r >> 1) * 128 + (((r & 1) * 4 + (piece ^ ((r >> 1) & 3))) << 4);
+      };
+      const int to_row = ((lane >> 4) << 3) + (lane & 7), to_piece = (lane >> 3) & 1;
 #pragma unroll 1
       for (int b = 0; b < SH::kPairs; ++b) {
         float v[2][8];
         tmem_load_fragments(lanes + SH::kTmemO + b * kAttnRows + c0, v);
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          store_transposed(to + (((b * 16 + to_piece + h * 2) ^ (to_row & 7)) << 4),
-                           pack_bf16x2(v[h][0] * f0, v[h][1] * f1), pack_bf16x2(v[h][2] * f0, v[h][3] * f1),
-                           pack_bf16x2(v[h][4] * f2, v[h][5] * f3), pack_bf16x2(v[h][6] * f2, v[h][7] * f3));
+          store_transposed(place(to_row, to_piece + h * 2), pack_bf16x2(v[h][0] * f0, v[h][1] * f1),
+                           pack_bf16x2(v[h][2] * f0, v[h][3] * f1), pack_bf16x2(v[h][4] * f2, v[h][5] * f3),
+                           pack_bf16x2(v[h][6] * f2, v[h][7] * f3));
+        __syncwarp();
+        const int col = b * 128 + quad * 32 + (lane & 3) * 8;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = h * 8 + (lane >> 2);
+          const int64_t at = sm.out_at[par][c0 + r];
+          if (at >= 0 && col < p.d) *reinterpret_cast<uint4*>(p.out + at + col) = lds128(place(r, lane & 3));
+        }
+        __syncwarp();
       }
       tc_fence_before();
-      barrier_group();
-#pragma unroll 1
-      for (int i = (tid & 127); i < kSoftCols * kPer; i += 128) {
-        const int r = c0 + i / kPer, c = i % kPer;
-        const int64_t at = sm.out_at[r];
-        if (at >= 0 && c * 8 < p.d)
-          *reinterpret_cast<uint4*>(p.out + at + c * 8) =
-              lds128(base + SH::kQOff + r * (SH::kDpad * 2) + ((c ^ (r & 7)) << 4));
-      }
     } else {
       // four rows of a column in 16 bytes, a warp's 32 columns side by side
       float4* o = reinterpret_cast<float4*>(p.part_o + piece * kAttnRows * SH::kDpad);
@@ -847,21 +874,20 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
         tmem_load16(lanes + SH::kTmemO + b * kAttnRows + c0, v);
 #pragma unroll
         for (int c = 0; c < kSoftCols; c += 4)
-          if (sm.out_at[c0 + c] >= 0)
+          if (sm.out_at[par][c0 + c] >= 0)
             o[((b * 4 + quad) * (kAttnRows / 4) + (c0 + c) / 4) * 32 + lane] =
                 make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
       }
       tc_fence_before();
     }
-    named_barrier(5, kSoftThreads);  // the small arrays and the staging are free again
     w.left -= w.t1 - w.t0;
     ++w.unit;
     w.t0 = 0;
     if (more) {
       w.u = sm.next;
       w.bound();
-      named_barrier(5, kSoftThreads);  // (read before the one after it is written)
     }
+    named_barrier(5, kSoftThreads);  // sm.next and P's place are free again
   }
 }
 
