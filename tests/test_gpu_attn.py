@@ -398,3 +398,24 @@ def test_joins_of_pieces_that_see_nothing(cuda_lib, d):
     c.check(cuda_lib)
     c = Case([3, 2], [2600, 2600], 16, 1, d, page=64, ratio=64, first=[0, 70], sink=True, seed=d)
     c.check(cuda_lib)
+
+
+@pytest.mark.parametrize("fmt", [R.BF16, R.E4M3, R.FP4])
+@pytest.mark.parametrize("H,kv,d,page", [(64, 1, 512, 64), (64, 2, 256, 16), (128, 1, 128, 48), (64, 1, 512, 9),
+                                         (64, 1, 256, 9), (128, 1, 128, 9)])
+def test_many_units_of_chunks(cuda_lib, fmt, H, kv, d, page):
+    """More units than workers, each worker going from one to the next: the next one's rows come while one's go."""
+    Case([170, 1, 150, 0, 60], [430, 260, 129, 40, 1], H, kv, d, fmt, page=page, ratio=1, first="end", sink=True,
+         seed=d + page).check(cuda_lib)
+
+
+@pytest.mark.parametrize("fmt", [R.BF16, R.E4M3, R.FP4])
+@pytest.mark.parametrize("H,d,page", [(64, 512, 64), (20, 256, 16), (8, 128, 64), (64, 512, 3)])
+def test_many_units_of_single_tokens(cuda_lib, fmt, H, d, page):
+    """Several sequences to a worker, some of no entries, some of no token."""
+    g = torch.Generator().manual_seed(d + H)
+    S = 500
+    lens = (torch.rand(S, generator=g) < 0.9).int().tolist()
+    entries = torch.randint(0, 400, (S,), generator=g).tolist()
+    entries[3] = entries[77] = 0
+    Case(lens, entries, H, 1, d, fmt, page=page, ratio=0, sink=d == 256, seed=d).check(cuda_lib)
