@@ -150,8 +150,9 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnParams p) {
         AttnJoin join{};
         join.u = p.units[b.unit];
         join.worker = i;
-        int last = i + 1;
+        int last = max(i + 1, share.near(end - 1));  // the worker whose share the unit's last tile lies in
         while (share(last + 1) < end) ++last;
+        while (last > i + 1 && share(last) >= end) --last;
         join.pieces = last - i + 1;
         // (in any order: each is joined by itself; those of many pieces from the list's other end)
         const bool few = join.pieces <= kFewPieces;

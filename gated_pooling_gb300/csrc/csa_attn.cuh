@@ -116,6 +116,10 @@ struct AttnShares {
   __device__ __forceinline__ int64_t operator()(int i) const {
     return i >= n ? work : q * i + static_cast<int>(static_cast<uint32_t>(r) * static_cast<uint32_t>(i) / static_cast<uint32_t>(n));
   }
+  // the worker whose share x < work lies in, or one next to it
+  __device__ __forceinline__ int near(int64_t x) const {
+    return min(n - 1, static_cast<int>(static_cast<float>(x) * (static_cast<float>(n) / static_cast<float>(work))));
+  }
 };
 
 }  // namespace csa
