@@ -48,6 +48,21 @@ __device__ __forceinline__ void turn_cos_sin(int32_t pos, uint64_t per, float am
   s *= amp;
 }
 
+// 16-bit types take cos and sin from the hardware approximation (within 2^-21 of the value at
+// an angle already brought to half a turn either way: 2^-9 and 2^-12 of a result are
+// rounded away behind it); fp32 from CUDA's functions.
+template <int DTYPE>
+__device__ __forceinline__ void cos_sin(int32_t pos, uint64_t per, float amp, float& c, float& s) {
+  if constexpr (DTYPE == CSA_DTYPE_FP32) {
+    turn_cos_sin(pos, per, amp, c, s);
+  } else {
+    const uint64_t t = static_cast<uint64_t>(static_cast<int64_t>(pos)) * per;
+    const float x = static_cast<float>(static_cast<int32_t>(t >> 32)) * 1.46291807926715968105e-9f;  // pi 2^-31
+    c = __cosf(x) * amp;
+    s = __sinf(x) * amp;
+  }
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
@@ -75,7 +90,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_scalar_kernel(RopeParams p)
   pdl_wait();
   for (int64_t u = static_cast<int64_t>(blockIdx.x) * kRopeWarps + (threadIdx.x >> 5); u < p.units;
        u += static_cast<int64_t>(gridDim.x) * kRopeWarps) {
-    const int64_t row = u / p.heads, head = u - row * p.heads;
+    const int64_t row = static_cast<int>(u) / p.heads, head = u - row * p.heads;  // (units below 2^31)
     const int32_t pos = p.pos != nullptr ? p.pos[row] : 0;
     if (pos < 0) continue;
     const T* x = static_cast<const T*>(p.x) + row * p.x_row + head * p.x_head;
@@ -97,7 +112,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_scalar_kernel(RopeParams p)
       int a, b;
       pair_columns(p, i, a, b);
       float cs, sn;
-      turn_cos_sin(pos, p.turns[i], p.amp, cs, sn);
+      cos_sin<DTYPE>(pos, __ldg(p.turns + i), p.amp, cs, sn);
       const float va = normed(a), vb = normed(b);
       y[a] = E::from_float(va * cs - vb * sn);
       y[b] = E::from_float(va * sn + vb * cs);
@@ -127,7 +142,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_scalar_bwd_kernel(RopeParam
   pdl_wait();
   for (int64_t u = static_cast<int64_t>(blockIdx.x) * kRopeWarps + warp; u < p.units;
        u += static_cast<int64_t>(gridDim.x) * kRopeWarps) {
-    const int64_t row = u / p.heads, head = u - row * p.heads;
+    const int64_t row = static_cast<int>(u) / p.heads, head = u - row * p.heads;  // (units below 2^31)
     const int32_t pos = p.pos != nullptr ? p.pos[row] : 0;
     if (pos < 0) continue;
     const T* x = static_cast<const T*>(p.x) + row * p.x_row + head * p.x_head;
@@ -140,7 +155,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_scalar_bwd_kernel(RopeParam
         int a, b;
         pair_columns(p, i, a, b);
         float cs, sn;
-        turn_cos_sin(pos, p.turns[i], p.amp, cs, sn);
+        cos_sin<DTYPE>(pos, __ldg(p.turns + i), p.amp, cs, sn);
         const float ga = E::to_float(dy[a]), gb = E::to_float(dy[b]);
         f(a, ga * cs + gb * sn);
         f(b, gb * cs - ga * sn);
@@ -197,10 +212,6 @@ __global__ void __launch_bounds__(kRopeThreads) rope_scalar_bwd_kernel(RopeParam
 // pieces are loaded while one is computed. Three blocks an SM forward (two or four: 57.6 or
 // 55.3 us instead of 51.5 for 8192 rows of 64 heads of 128, 5.2 TB/s), two backward (one:
 // 67.9 us instead of 48.1 for 32 heads, 4.2 TB/s).
-//
-// 16-bit types take cos and sin from the hardware approximation (within 2^-21 of the value at
-// an angle already brought to half a turn either way: 2^-9 and 2^-12 of a result are
-// rounded away behind it); fp32 from CUDA's functions.
 // ---------------------------------------------------------------------------------
 template <int DTYPE, int PP>
 struct RopeLane {
@@ -242,16 +253,6 @@ struct RopeLane {
     }
   }
 
-  __device__ __forceinline__ void angle(const RopeParams& p, int32_t pos, uint64_t per, float& c, float& s) {
-    if constexpr (DTYPE == CSA_DTYPE_FP32) {
-      turn_cos_sin(pos, per, p.amp, c, s);
-    } else {
-      const uint64_t t = static_cast<uint64_t>(static_cast<int64_t>(pos)) * per;
-      const float x = static_cast<float>(static_cast<int32_t>(t >> 32)) * 1.46291807926715968105e-9f;  // pi 2^-31
-      c = __cosf(x) * p.amp;
-      s = __sinf(x) * p.amp;
-    }
-  }
   // the angles of a row
   __device__ __forceinline__ void turn_to(const RopeParams& p, int32_t pos) {
 #pragma unroll
@@ -264,8 +265,8 @@ struct RopeLane {
 #pragma unroll
         for (int i = 0; i < 4; i += 2) {
           const ulonglong2 per = __ldg(reinterpret_cast<const ulonglong2*>(p.turns + i0 + i));
-          angle(p, pos, per.x, cs[s][4 * h + i], sn[s][4 * h + i]);
-          angle(p, pos, per.y, cs[s][4 * h + i + 1], sn[s][4 * h + i + 1]);
+          cos_sin<DTYPE>(pos, per.x, p.amp, cs[s][4 * h + i], sn[s][4 * h + i]);
+          cos_sin<DTYPE>(pos, per.y, p.amp, cs[s][4 * h + i + 1], sn[s][4 * h + i + 1]);
         }
       }
     }
