@@ -91,8 +91,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_scalar_kernel(RopeParams p)
   for (int64_t u = static_cast<int64_t>(blockIdx.x) * kRopeWarps + (threadIdx.x >> 5); u < p.units;
        u += static_cast<int64_t>(gridDim.x) * kRopeWarps) {
     const int64_t row = static_cast<int>(u) / p.heads, head = u - row * p.heads;  // (units below 2^31)
-    const int32_t pos = p.pos != nullptr ? p.pos[row] : 0;
-    if (pos < 0) continue;
+    // (the position, the row and the first angle load side by side)
+    const int32_t pos = p.pos != nullptr ? __ldg(p.pos + row) : 0;
+    const uint64_t per0 = lane < p.rot / 2 ? __ldg(p.turns + lane) : 0;
     const T* x = static_cast<const T*>(p.x) + row * p.x_row + head * p.x_head;
     T* y = static_cast<T*>(p.y) + row * p.y_row + head * p.y_head;
     float r = 1.f;
@@ -104,6 +105,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_scalar_kernel(RopeParams p)
       }
       r = 1.f / sqrtf(warp_sum(ss) / static_cast<float>(p.d) + p.eps);
     }
+    if (pos < 0) continue;
     auto normed = [&](int c) {
       const float v = E::to_float(x[c]);
       return p.norm ? (p.weight != nullptr ? v * r * p.weight[c] : v * r) : v;
@@ -112,7 +114,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_scalar_kernel(RopeParams p)
       int a, b;
       pair_columns(p, i, a, b);
       float cs, sn;
-      cos_sin<DTYPE>(pos, __ldg(p.turns + i), p.amp, cs, sn);
+      cos_sin<DTYPE>(pos, i == lane ? per0 : __ldg(p.turns + i), p.amp, cs, sn);
       const float va = normed(a), vb = normed(b);
       y[a] = E::from_float(va * cs - vb * sn);
       y[b] = E::from_float(va * sn + vb * cs);
