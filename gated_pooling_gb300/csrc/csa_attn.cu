@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnParams p) {
   for (int s = lo; s < hi; ++s) {
     const int32_t a = __ldg(p.cu + s), b = __ldg(p.cu + s + 1), n = __ldg(p.entries + s);
     if (b < a || a < 0 || b > p.tokens) bad |= 1;
-    else mine += ((b - a) * p.group + p.unit_rows - 1) / p.unit_rows;
+    else mine += ((b - a) * p.group + kAttnRows - 1) / kAttnRows;
     if (n < 0 || n > p.max_entries) bad |= 2;
   }
   int code = 0;
@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnParams p) {
   int64_t at = plan_scan(mine, s_warps, blocks);
   for (int s = lo; s < hi; ++s) {
     s_first[s] = static_cast<int>(at);
-    at += (sequence_rows(p, s) + p.unit_rows - 1) / p.unit_rows;
+    at += (sequence_rows(p, s) + kAttnRows - 1) / kAttnRows;
   }
   if (threadIdx.x == 0) s_first[p.S] = static_cast<int>(blocks);
   __syncthreads();
@@ -325,15 +325,14 @@ cudaError_t plan_sizes(AttnParams& p, int* sms, int32_t S, int64_t tokens, int32
   p.group = q_heads / kv_heads;
   p.d = d;
   p.workers = *sms;
-  p.unit_rows = kAttnRows;
   p.max_entries = max_entries;
   p.max_units = ((tokens * p.group + kAttnRows - 1) / kAttnRows + S) * kv_heads;
   p.packed_rows = static_cast<int>((max_entries + kAttnEntries - 1) / kAttnEntries * kAttnEntries);
   return cudaSuccess;
 }
 
-// Whether a call's chunks may be long enough for pairs of CTAs over packed entries: kChunkRows
-// rows (two units) a sequence on average, so that packing an entry (read and written once) is
+// Whether a call's chunks may be long enough for packed entries: kChunkRows rows (four units) a
+// sequence on average, so that packing an entry (read and written once) is
 // small beside the units that read it, and packed entries within kMaxPacked bytes. (The
 // workspace has room for them then; the call decides, where it knows the cache.)
 constexpr int64_t kChunkRows = 256, kChunkRowsWide = 384;
@@ -421,24 +420,23 @@ extern "C" csa_status_t csa_cache_attn(
   const bool copies = format == CSA_CACHE_BF16 && p.box_rows >= 8 && num_pages > 0 &&
                       num_pages <= INT_MAX / page_size && (nc < 8 || most_tiles <= p.workers);
   // Packing first. Up to d = 256 a tile's time is the softmax's, so packing entries that can be copied
-  // from the pages gains nothing (3 chunks of 1024 tokens x 64 heads of 256: 922 us packed, 936 not;
-  // 48 of 8 tokens: 211 and 170). Codes are widened once instead of by every unit (922 and
-  // 1784), from 256 rows a sequence on at d = 128 (417 and 560), later above (256 rows of 256: 134
-  // and 125, of 512: 251 and 227; 384 of 512: 311 and 312; 512 of 256: 212 and 238, of 512: 400 and
-  // 441). bf16 at d = 512: 256 rows 252 and 277, three chunks of 1024 tokens 894 and 1345.
+  // from the pages gains little (3 chunks of 1024 tokens x 64 heads of 256: 450 us packed, 471 not)
+  // or loses (48 of 8 tokens: 205 and 165). Codes are widened once instead of by every unit (450 and
+  // 787), from 256 rows a sequence on at d = 128 (496 and 675), later above (256 rows of 256: 132
+  // and 123, of 512: 255 and 227; 384 of 256: 160 and 169, of 512: 314 and 313; 512 of 256: 206 and
+  // 232, of 512: 407 and 435). bf16 at d = 512: 256 rows 256 and 285, three chunks of 1024 tokens
+  // 909 and 1382.
   const bool wide = format != CSA_CACHE_BF16 && d > 128;
   const bool chunks = tile && chunked(p) && !(copies && nc < 8) &&
                       tokens * p.group >= (wide ? kChunkRowsWide : kChunkRows) * S;
   // A unit's own cost (q in, output out, the pipeline's start) in tiles, by which shares are evened
-  // out, measured best of 1 to 6. Packed: three chunks of 1024 tokens x 64 heads of 512 894 us (at 3
-  // 936, at 6 991), of 256 922 (at 1 958, at 6 950); 48 of 64 tokens over 8 heads of 128 420 (at 1
-  // 447). Otherwise: 48 single tokens at d = 512 67.8 us (at 4 71.7), over codes of 256 40.4 (at 1
+  // out, measured best of 1 to 5 or 6. Packed: three chunks of 1024 tokens x 64 heads of 512 910 us (at 3
+  // 945, at 5 987), of 256 450 (at 1 513, at 5 468); 48 of 64 tokens x 8 heads of 128 100 (at 1
+  // 112). Otherwise: 48 single tokens at d = 512 67.8 us (at 4 71.7), over codes of 256 40.4 (at 1
   // 41.3, at 6 42.1); where copies make the tiles short, 8 heads of 128, 78.3 us (at 1 98.2), and of
   // 128 tokens each 637 (at 1 815).
   p.unit_cost = copies && nc < 8 ? 5 : 2;
   if (chunks) {
-    p.workers = sms / 2;
-    p.unit_rows = 2 * kAttnRows;
     p.unit_cost = nc == 8 ? 1 : nc == 4 ? 3 : 5;
   }
   p.q = static_cast<const uint16_t*>(q);
@@ -497,7 +495,7 @@ extern "C" csa_status_t csa_cache_attn(
         constexpr int SRC = decltype(src)::value;
         k = reinterpret_cast<const void*>(attn_tile_kernel<NC, SRC>);
         threads = TileCta<SRC>::kThreads;
-        join = reinterpret_cast<const void*>(attn_join_kernel<NC, TileCta<SRC>::kCluster>);
+        join = reinterpret_cast<const void*>(attn_join_kernel<NC>);
         return 0;
       };
       if (source == kFromPacked) {
@@ -514,7 +512,6 @@ extern "C" csa_status_t csa_cache_attn(
     });
     if (blocks_per_sm(dev, k, threads, smem, &bps) != cudaSuccess) return CSA_ERR_CUDA;
     if (bps < 1) return CSA_ERR_UNSUPPORTED;
-    const int cluster = chunks ? 2 : 1;
     if (chunks) {
       // a few blocks an SM, which go on to their sequence's next entries: the table's capacity may
       // be far above what the sequences hold
@@ -525,7 +522,7 @@ extern "C" csa_status_t csa_cache_attn(
         return CSA_ERR_CUDA;
     }
     void* targs[] = {&p, &map};
-    if (launch_pdl(k, dim3(p.workers * cluster), dim3(threads), smem, cs, targs, cluster) != cudaSuccess)
+    if (launch_pdl(k, dim3(p.workers), dim3(threads), smem, cs, targs) != cudaSuccess)
       return CSA_ERR_CUDA;
     return launch_pdl(join, dim3(kJoinBlocks * sms), dim3(kJoinThreads), 0, cs, args) == cudaSuccess
                ? CSA_OK

@@ -13,10 +13,9 @@ namespace csa {
 constexpr int kAttnRows = 64;      // (token, head) rows of a unit
 constexpr int kAttnEntries = 128;  // entries of a tile
 
-// A unit is up to unit_rows (64, or 128 for a pair of CTAs) consecutive rows (token, head of the
-// group) of one sequence and cache head; its work is a run of tiles of 128 entries, at least
-// one. The work of all units in order is split evenly over the workers, CTAs or pairs of them
-// (AttnShares).
+// A unit is up to 64 consecutive rows (token, head of the group) of one sequence and cache head; its
+// work is a run of tiles of 128 entries, at least one. The work of all units in order is split
+// evenly over the workers, a CTA each (AttnShares).
 struct alignas(16) AttnUnit {
   int32_t s, kvh, block, tiles;
   int32_t token, rows;  // the sequence's first token, and its rows
@@ -61,13 +60,13 @@ struct AttnParams {
   AttnJoin* joins;      // [workers]: those of few pieces from its start, of many from its end
   AttnUnit* units;      // [max_units]
   int64_t* unit_first;  // [max_units + 1]: where each unit's work begins
-  float* part_o;        // [2 workers][CTAs of one][64 x dpad]: sums of the pieces of shared units
-  float* part_ml;       // likewise [2][64]: their maxima (in log2) and weight sums
+  float* part_o;        // [2 workers][64 x dpad]: sums of the pieces of shared units
+  float* part_ml;       // [2 workers][2][64]: their maxima (in log2) and weight sums
   uint16_t* packed;     // chunks: the sequences' entries as bf16 rows [S][kv_heads][packed_rows][dpad]
   int64_t q_row, q_head, out_row, out_head;
   int64_t tokens, num_pages, max_entries, max_units;
   int S, q_heads, kv_heads, group, d, max_pages, page_size, ratio;
-  int workers, unit_rows, unit_cost;
+  int workers, unit_cost;
   int packed_rows;  // rows of a sequence's cache head in `packed`, a multiple of 128
   int box_rows;     // entries of a tensor copy's box from the pages
   float scale;  // softmax_scale
@@ -95,8 +94,8 @@ __device__ __forceinline__ AttnUnit make_unit(const AttnParams& p, int s, int kv
   u.rows = sequence_rows(p, s);
   u.first = p.first != nullptr ? __ldg(p.first + s) : 0;
   u.n = __ldg(p.entries + s);
-  const int last = min(block * p.unit_rows + p.unit_rows, u.rows) - 1;
-  u.seen_all = visible(static_cast<int64_t>(u.first) + block * p.unit_rows / p.group, p.ratio, u.n);
+  const int last = min(block * kAttnRows + kAttnRows, u.rows) - 1;
+  u.seen_all = visible(static_cast<int64_t>(u.first) + block * kAttnRows / p.group, p.ratio, u.n);
   u.seen = visible(static_cast<int64_t>(u.first) + last / p.group, p.ratio, u.n);
   u.tiles = u.seen <= kAttnEntries ? 1 : (u.seen - 1) / kAttnEntries + 1;
   return u;

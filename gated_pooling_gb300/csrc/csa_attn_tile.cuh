@@ -47,8 +47,7 @@ constexpr int kSoftCols = 16;  // rows of a softmax thread's group
 constexpr int kTileLoaders = kTileLoadWarps * 32;
 constexpr int kTileFirstLoader = kTileSoftWarps + 4;
 // Where a tile comes from: threads that read the pages (in each of the cache's formats); tensor
-// copies of the pages' bf16 boxes; or tensor copies of a sequence's packed entries that go to both
-// CTAs of a pair.
+// copies of the pages' bf16 boxes; or tensor copies of a sequence's packed entries.
 enum TileSource {
   kFromBf16 = CSA_CACHE_BF16,
   kFromE4m3 = CSA_CACHE_E4M3,
@@ -59,7 +58,6 @@ enum TileSource {
 template <int SRC>
 struct TileCta {
   static constexpr bool kByThreads = SRC < kFromBoxes;
-  static constexpr int kCluster = SRC == kFromPacked ? 2 : 1;
   static constexpr int kThreads = (kTileFirstLoader + (kByThreads ? kTileLoadWarps : 0)) * 32;
 };
 // Registers a thread: 896 threads launch with 72, and 16 x 64 + 4 x 40 + 8 x 104 = 28 x 72.
@@ -496,8 +494,7 @@ __device__ __forceinline__ void tile_help(const AttnParams& p, TileSmall& sm, ui
 // From the pages: lane i copies box i mod n of chunk i / n of each pair, n = 128 / box_rows of them.
 // A box behind the last entry that the unit sees is not copied, and rows behind it in a copied
 // box are whatever the pool holds there: masked in the scores, and made finite where they are
-// not before the second product. From packed entries: one box of a pair by each CTA of the
-// pair, to both.
+// not before the second product. From packed entries: a pair's two chunks by a lane each.
 template <int NC, int SRC>
 __device__ void tile_copy(const AttnParams& p, TileSmall& sm, uint32_t base, const CUtensorMap* map) {
   using SH = TileShape<NC>;
@@ -505,18 +502,16 @@ __device__ void tile_copy(const AttnParams& p, TileSmall& sm, uint32_t base, con
   RingAt<SH::kRing> ring;
   uint32_t issued = 0;
   if constexpr (SRC == kFromPacked) {
-    const int rank = static_cast<int>(cluster_rank());
-    for (SegmentWalk w(p, blockIdx.x / 2); w.valid(); w.next()) {
+    for (SegmentWalk w(p, blockIdx.x); w.valid(); w.next()) {
       const int row = (w.u.s * p.kv_heads + w.u.kvh) * p.packed_rows;
       for (int tile = w.t0; tile < w.t1; ++tile)
         for (int c = 0; c < SH::kPairs; ++c, ring.next(), ++issued) {
           tile_wait(sm, p, &sm.empty[ring.slot], ring.lap ^ 1u);
-          if (lane == 0) {
-            mbar_arrive_expect_tx(&sm.full[ring.slot], kPairBytes);
-            box_load2_all(base + ring.slot * kPairBytes + rank * kChunkBytes, map, c * 128 + rank * 64,
-                          row + tile * kAttnEntries, &sm.full[ring.slot], 3);
-          }
+          if (lane == 0) mbar_arrive_expect_tx(&sm.full[ring.slot], kPairBytes);
           __syncwarp();
+          if (lane < 2)
+            box_load2(base + ring.slot * kPairBytes + lane * kChunkBytes, map, c * 128 + lane * 64,
+                      row + tile * kAttnEntries, &sm.full[ring.slot]);
         }
     }
   } else {
@@ -544,10 +539,6 @@ __device__ void tile_copy(const AttnParams& p, TileSmall& sm, uint32_t base, con
       }
     }
   }
-  // the other CTA's last arrivals have come in before this one's barriers go
-  if constexpr (SRC == kFromPacked)
-    for (uint32_t k = issued > SH::kRing ? issued - SH::kRing : 0; k < issued; ++k)
-      tile_wait(sm, p, &sm.empty[k % SH::kRing], (k / SH::kRing) & 1u);
   // after a stop, the copies that nobody waited for: the last lap of the ring
   if (*reinterpret_cast<volatile int*>(&sm.stop) != 0)
     for (uint32_t k = issued > SH::kRing ? issued - SH::kRing : 0; k < issued; ++k)
@@ -555,7 +546,7 @@ __device__ void tile_copy(const AttnParams& p, TileSmall& sm, uint32_t base, con
 }
 
 // ------------------------------------------------- the products' warp (all lanes take part)
-template <int NC, int CL>
+template <int NC>
 __device__ void tile_products(const AttnParams& p, TileSmall& sm, uint32_t base, uint32_t tmem) {
   using SH = TileShape<NC>;
   constexpr uint32_t kScoreDesc = mma_desc(128, kAttnRows, 0, 0);
@@ -581,7 +572,7 @@ __device__ void tile_products(const AttnParams& p, TileSmall& sm, uint32_t base,
     ++t;
   };
   uint32_t done = 0, seg = 0;  // tiles summed, segments
-  for (SegmentWalk w(p, blockIdx.x / CL); w.valid(); w.next(), ++seg) {
+  for (SegmentWalk w(p, blockIdx.x); w.valid(); w.next(), ++seg) {
     const int tiles = w.t1 - w.t0;
     tile_wait(sm, p, &sm.q_full, seg & 1u);
     tc_fence_after();
@@ -597,8 +588,7 @@ __device__ void tile_products(const AttnParams& p, TileSmall& sm, uint32_t base,
         for (int k = 0; k < 8; ++k)  // 16 entries a step
           tc_mma(tmem + SH::kTmemO + c * kAttnRows, a + k * (2048 >> 4), probs + k * (2048 >> 4), kSumDesc,
                  j > 0 || k > 0);
-        if (CL == 1) tc_commit(&sm.empty[ro.slot]);
-        else tc_commit_all(&sm.empty[ro.slot], 3);  // a pair's slot is free when both have used it
+        tc_commit(&sm.empty[ro.slot]);
       }
       tc_commit(&sm.summed);
       ++done;
@@ -614,7 +604,6 @@ __device__ void tile_products(const AttnParams& p, TileSmall& sm, uint32_t base,
 template <int NC, int SRC>
 __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* smem, uint32_t base, uint32_t tmem) {
   using SH = TileShape<NC>;
-  constexpr int CL = TileCta<SRC>::kCluster;
   const int tid = threadIdx.x, lane = tid & 31, quad = (tid >> 5) & 3, group = tid >> 7;
   const int c0 = group * kSoftCols;     // the rows (columns of S^T) of this group of four warps
   const int e0 = quad * 32 + lane;      // the entry (row of S^T) of this thread
@@ -624,11 +613,10 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
   uint32_t t = 0;  // tiles so far
   auto barrier_group = [&]() { named_barrier(1 + group, 128); };
 
-  const int worker = blockIdx.x / CL, rank = CL == 1 ? 0 : static_cast<int>(cluster_rank());
   // where each row of a unit's q, out and lse lies, what it sees, its sink (rows behind the last one
   // are zeros, see what the last one sees, and are never stored)
   auto set_up = [&](const AttnUnit& u, int par) {
-    const int row = u.block * (CL * kAttnRows) + rank * kAttnRows + tid, token = row / p.group;
+    const int row = u.block * kAttnRows + tid, token = row / p.group;
     const bool some = row < u.rows;
     const int head = u.kvh * p.group + (row - token * p.group);
     const int64_t at = static_cast<int64_t>(u.token) + token;
@@ -656,7 +644,7 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
     if (lane == 0) mbar_arrive(&sm.q_full);
   };
   int par = 0;
-  SegmentWalk w(p, worker);
+  SegmentWalk w(p, blockIdx.x);
   if (w.valid()) {
     if (tid < kAttnRows) {
       set_up(w.u, 0);
@@ -781,7 +769,7 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
         // the next unit's places, and its rows of q on their way into L2
         named_barrier(5, kSoftThreads);
         if (tid < kAttnRows) set_up(sm.next, par ^ 1);
-        const int r = tid / NC, row = sm.next.block * (CL * kAttnRows) + rank * kAttnRows + r;
+        const int r = tid / NC, row = sm.next.block * kAttnRows + r;
         const int col = (tid % NC) * 64;
         if (r < kAttnRows && row < sm.next.rows && col < p.d) {
           const int token = row / p.group;
@@ -814,7 +802,7 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
     l[0] += __shfl_xor_sync(0xFFFFFFFFu, l[0], 1);
     if ((lane & 1) == 0) sm.red[quad][c0 + (lane >> 1)] = l[0];
     barrier_group();
-    const int64_t piece = (2 * static_cast<int64_t>(worker) + (w.t0 == 0 ? 1 : 0)) * CL + rank;
+    const int64_t piece = 2 * static_cast<int64_t>(blockIdx.x) + (w.t0 == 0 ? 1 : 0);
     if (quad == 0 && lane < kSoftCols) {
       const int c = c0 + lane;
       const float z = (sm.red[0][c] + sm.red[1][c]) + (sm.red[2][c] + sm.red[3][c]), m = sm.m[c];
@@ -893,7 +881,7 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
 
 // Chunks: the entries that a sequence's last token sees, as bf16 rows in order, zeros up to the next
 // multiple of 128 rows and of 64 NC columns, so that the tile kernel's copies are whole boxes
-// whatever the format, the page size and the heads. Every unit of the sequence (one per 128
+// whatever the format, the page size and the heads. Every unit of the sequence (one per 64
 // rows) reads them again; packing reads and writes them once. Block (x, s, cache head): 32
 // entries at a time, a thread 8 columns at a time.
 constexpr int kPackThreads = 256, kPackRows = 32;
@@ -944,7 +932,6 @@ __global__ void __launch_bounds__(TileCta<SRC>::kThreads, 1)
     attn_tile_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap map) {
   using SH = TileShape<NC>;
   using CTA = TileCta<SRC>;
-  constexpr int CL = CTA::kCluster;
   extern __shared__ unsigned char raw[];
   unsigned char* smem = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
   TileSmall& sm = *reinterpret_cast<TileSmall*>(smem + SH::kSmallOff);
@@ -955,7 +942,7 @@ __global__ void __launch_bounds__(TileCta<SRC>::kThreads, 1)
     for (int i = 0; i < SH::kRing; ++i) {
       const bool helped = SH::template kHelped<SRC> && i >= SH::kPairs / 2;
       mbar_init(&sm.full[i], helped ? kTileSoftWarps / 2 : CTA::kByThreads ? kTileLoadWarps / 2 : 1);
-      mbar_init(&sm.empty[i], CL);
+      mbar_init(&sm.empty[i], 1);
     }
     mbar_init(&sm.scores[0], 1);
     mbar_init(&sm.scores[1], 1);
@@ -968,7 +955,6 @@ __global__ void __launch_bounds__(TileCta<SRC>::kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if constexpr (CL > 1) cluster_barrier();  // both CTAs' barriers are set up
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
   pdl_wait();
@@ -979,19 +965,18 @@ __global__ void __launch_bounds__(TileCta<SRC>::kThreads, 1)
       if (run) tile_fetch<NC, SRC>(p, sm, base);
     } else if (warp >= kTileSoftWarps) {
       regs_down<kIssueRegs>();
-      if (run && warp == kTileSoftWarps) tile_products<NC, CL>(p, sm, base, tmem);
+      if (run && warp == kTileSoftWarps) tile_products<NC>(p, sm, base, tmem);
     } else {
       regs_down<kSoftRegs>();
       if (run) tile_softmax<NC, SRC>(p, sm, smem, base, tmem);
     }
   } else if (run) {
-    if (warp == kTileSoftWarps) tile_products<NC, CL>(p, sm, base, tmem);
+    if (warp == kTileSoftWarps) tile_products<NC>(p, sm, base, tmem);
     else if (warp == kTileSoftWarps + 1) tile_copy<NC, SRC>(p, sm, base, &map);
     else if (warp < kTileSoftWarps) tile_softmax<NC, SRC>(p, sm, smem, base, tmem);
   }
   tc_fence_before();
   __syncthreads();
-  if constexpr (CL > 1) cluster_barrier();  // nothing of the other CTA's is on its way here
   tc_fence_after();
   if (warp == 0) tmem_free(tmem, SH::kTmemColumns);
 }
@@ -1001,14 +986,14 @@ __global__ void __launch_bounds__(TileCta<SRC>::kThreads, 1)
 // columns, four pieces' loads under way at once and the first four's before their weights are
 // known; lane 8 r + k works out row r's weight of piece k. A unit of many pieces (a long sequence
 // by itself) is split over a block's warps, which take four pieces each in turn and meet in shared
-// memory. The order of the sums is fixed. (Redundant work in the warps took 33 of 720 us for 75 units of
-// 128 rows x 512 in two pieces each, 12 of 701 so.)
+// memory. The order of the sums is fixed. (Redundant work in the warps took 33 of 720 us for 150 units of
+// 64 rows x 512 in two pieces each, 12 of 701 so.)
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kJoinBlocks = 3;  // blocks an SM
 constexpr int kFewPieces = 8;
-template <int NC, int CL>
+template <int NC>
 __global__ void __launch_bounds__(kJoinThreads, kJoinBlocks) attn_join_kernel(const __grid_constant__ AttnParams p) {
   constexpr int kQuads = kAttnRows / 4;           // fours of rows
-  constexpr int kTasks = CL * kQuads * NC;        // of a unit: four rows, 64 columns
+  constexpr int kTasks = kQuads * NC;             // of a unit: four rows, 64 columns
   constexpr int kFewItems = kTasks / kJoinWarps;  // blocks of a unit of few pieces; kTasks of one of many
   constexpr int kPiece = kAttnRows * NC * 64 / 4, kFlight = 4;
   __shared__ float4 s_sum[kJoinWarps][2][32];
@@ -1022,12 +1007,12 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinBlocks) attn_join_kernel(co
     const int rest = few ? item : item - few_items;
     const int task = few ? rest % kFewItems * kJoinWarps + warp : rest % kTasks;
     const AttnJoin& J = p.joins[few ? rest / kFewItems : p.workers - 1 - rest / kTasks];
-    const int quad = task % kQuads, chunk = task / kQuads % NC, rank = task / (kQuads * NC);
+    const int quad = task % kQuads, chunk = task / kQuads;
     const AttnUnit u = J.u;
     const int first = J.worker, n = J.pieces;
-    const int row0 = (u.block * CL + rank) * kAttnRows + quad * 4, row = row0 + r;
+    const int row0 = u.block * kAttnRows + quad * 4, row = row0 + r;
     if (row0 >= u.rows) continue;  // (all of a block's warps, where they share a task)
-    auto slot = [&](int k) { return (2 * static_cast<int64_t>(first + k) + (k == 0 ? 1 : 0)) * CL + rank; };
+    auto slot = [&](int k) { return 2 * static_cast<int64_t>(first + k) + (k == 0 ? 1 : 0); };
     const float4* o = reinterpret_cast<const float4*>(p.part_o) + (chunk * 2 * kQuads + quad) * 32 + lane;
     const float* ml = p.part_ml + quad * 4 + r;
     const int step = few ? kFlight : kFlight * kJoinWarps;

@@ -20,12 +20,12 @@ PoolKernel bwd_kernel_for(const Plan& pl);
 // device (cached). blocks_per_sm(): resident blocks of `kernel` per SM with `smem` bytes
 // of dynamic shared memory (cached; raises the kernel's dynamic shared-memory limit
 // once). launch_pdl(): launches `k` as a programmatic dependent of the stream's previous
-// kernel, in clusters of `cluster` blocks.
+// kernel.
 cudaError_t note(cudaError_t e);
 cudaError_t device_sms(int dev, int* sms);
 cudaError_t blocks_per_sm(int dev, const void* kernel, int threads, size_t smem, int* blocks);
 cudaError_t launch_pdl(const void* k, dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
-                       void** args, int cluster = 1);
+                       void** args);
 // encode_boxes(): tensor map of an array of bf16 values (rank 2 or 3, dims and box innermost
 // first, strides in bytes from the second dimension on) whose boxes land in shared memory with
 // the 128-byte swizzle; false when the driver has no such call or refuses the shape.

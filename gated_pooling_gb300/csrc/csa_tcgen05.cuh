@@ -88,18 +88,7 @@ __device__ __forceinline__ void tc_commit(uint64_t* bar) {
       : "memory");
 }
 
-// The same on the barriers at this address of every block of the cluster in `mask`.
-__device__ __forceinline__ void tc_commit_all(uint64_t* bar, uint16_t mask) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xFFFFFFFF;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
-          smem_addr(bar)),
-      "h"(mask)
-      : "memory");
-}
-
-// Tensor copies into shared memory, counted in bytes on `bar`: a box of a rank-3 map; a box of a
-// rank-2 map into the same place of every block of the cluster in `mask`, on each one's barrier.
+// Tensor copies of a box of a rank-3 or rank-2 map into shared memory, counted in bytes on `bar`.
 __device__ __forceinline__ void box_load3(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
@@ -107,22 +96,12 @@ __device__ __forceinline__ void box_load3(uint32_t dst, const CUtensorMap* map, 
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
       : "memory");
 }
-__device__ __forceinline__ void box_load2_all(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar,
-                                              uint16_t mask) {
+__device__ __forceinline__ void box_load2(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster [%0], "
-      "[%1, {%2, %3}], [%4], %5;" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar)), "h"(mask)
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          dst),
+      "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
       : "memory");
-}
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-// All threads of the cluster.
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // Registers per thread from here on, for a whole group of four warps; the groups' shares have
