@@ -30,11 +30,14 @@ std::vector<OccEntry> g_occ;
 std::vector<int> g_sms;
 std::vector<std::pair<int, const void*>> g_attr_set;
 thread_local cudaError_t t_last_error = cudaSuccess;
-// Test hook state (csa_compressor_test_hooks): the pipeline wait bound and the withheld row.
+// Test hook state (csa_compressor_test_hooks): the pipeline wait bound and the withheld row or tile.
 std::atomic<long long> g_wait_cycles{kWaitCycles};
 std::atomic<int> g_withhold_row{-1};
 
 }  // namespace
+
+long long hooked_wait_cycles() { return g_wait_cycles.load(std::memory_order_relaxed); }
+int hooked_withhold() { return g_withhold_row.load(std::memory_order_relaxed); }
 
 // Records a failing CUDA call for csa_last_error_string() and passes the code on.
 cudaError_t note(cudaError_t e) {
@@ -233,8 +236,8 @@ PoolParams base_params(const Plan& pl, const void* kv, const void* score, const 
   p.bar_off = pl.bar_off;
   p.box_rows = pl.box_rows;
   p.np = pl.np;
-  p.wait_cycles = g_wait_cycles.load(std::memory_order_relaxed);
-  p.withhold_row = g_withhold_row.load(std::memory_order_relaxed);
+  p.wait_cycles = hooked_wait_cycles();
+  p.withhold_row = hooked_withhold();
   return p;
 }
 

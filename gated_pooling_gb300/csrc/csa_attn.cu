@@ -459,6 +459,8 @@ extern "C" csa_status_t csa_cache_attn(
   p.page_size = page_size;
   p.ratio = ratio;
   p.scale = softmax_scale;
+  p.wait_cycles = hooked_wait_cycles();
+  p.withhold_tile = hooked_withhold();
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   void* args[] = {&p};
   int dev = 0, bps = 0;

@@ -70,6 +70,8 @@ struct AttnParams {
   int packed_rows;  // rows of a sequence's cache head in `packed`, a multiple of 128
   int box_rows;     // entries of a tensor copy's box from the pages
   float scale;  // softmax_scale
+  int withhold_tile;      // test hook: tile of the first CTA's first unit that never comes, -1: none
+  long long wait_cycles;  // bound of each wait on a barrier in shared memory, in SM clock cycles
 };
 
 // Entries that the token at position pos sees, of a sequence's n.

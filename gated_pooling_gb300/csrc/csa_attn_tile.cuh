@@ -302,17 +302,25 @@ struct Take<CSA_CACHE_E2M1> {
 // Waits are bounded: one that runs out sets the CTA's stop word and reports, after which every
 // wait returns at once and every role runs through the rest of its (finite) loops, so that
 // the barriers among its warps stay matched; the products already issued are drained before
-// the tensor memory is freed. Nothing else is ever in flight.
+// the tensor memory is freed. The warp that issues tensor copies issues no more of them (it could
+// not tell when a slot is free, nor count what is under way) and waits for those it has issued.
 __device__ __forceinline__ void tile_wait(TileSmall& sm, const AttnParams& p, uint64_t* bar, uint32_t parity) {
   if (mbar_try_wait(bar, parity)) return;
   const long long t0 = clock64();
   while (!mbar_try_wait(bar, parity)) {
     if (*reinterpret_cast<volatile int*>(&sm.stop) != 0) return;
-    if (clock64() - t0 > kWaitCycles) {
+    if (clock64() - t0 > p.wait_cycles) {
       stop_pipeline(&sm.stop, p.dev_error);
       return;
     }
   }
+}
+__device__ __forceinline__ bool tile_stopped(const TileSmall& sm) {
+  return *reinterpret_cast<const volatile int*>(&sm.stop) != 0;
+}
+// test hook: the first CTA never fills this tile's place in the ring
+__device__ __forceinline__ bool tile_withheld(const AttnParams& p, int unit, int tile) {
+  return tile == p.withhold_tile && unit == 0 && blockIdx.x == 0;
 }
 
 // Place in the ring of pairs: slot, and the parity of its current lap.
@@ -444,7 +452,7 @@ __device__ void tile_fetch(const AttnParams& p, TileSmall& sm, uint32_t base) {
       v[i].store(base + ring.slot * kPairBytes, P::first_row(gt) + i * P::kRowStep, gt);
     fence_proxy_async_smem();
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(&sm.full[ring.slot]);
+    if ((threadIdx.x & 31) == 0 && !tile_withheld(p, w.unit, tile)) mbar_arrive(&sm.full[ring.slot]);
     next_pair();
 #pragma unroll
     for (int i = 1; i < kPairStep; ++i)
@@ -500,24 +508,38 @@ __device__ void tile_copy(const AttnParams& p, TileSmall& sm, uint32_t base, con
   using SH = TileShape<NC>;
   const int lane = threadIdx.x & 31;
   RingAt<SH::kRing> ring;
-  uint32_t issued = 0;
+  uint32_t places = 0;                     // of the ring, one after another, that this warp has filled
+  uint32_t skipped_from = 0, skipped = 0;  // (test hook) those that it left empty: [skipped_from, skipped)
+  // the next place is free, and the CTA has not stopped (one answer for the warp)
+  auto room = [&]() {
+    tile_wait(sm, p, &sm.empty[ring.slot], ring.lap ^ 1u);
+    return !__any_sync(0xFFFFFFFFu, tile_stopped(sm));
+  };
+  bool go = true;
   if constexpr (SRC == kFromPacked) {
-    for (SegmentWalk w(p, blockIdx.x); w.valid(); w.next()) {
+    for (SegmentWalk w(p, blockIdx.x); go && w.valid(); w.next()) {
       const int row = (w.u.s * p.kv_heads + w.u.kvh) * p.packed_rows;
-      for (int tile = w.t0; tile < w.t1; ++tile)
-        for (int c = 0; c < SH::kPairs; ++c, ring.next(), ++issued) {
-          tile_wait(sm, p, &sm.empty[ring.slot], ring.lap ^ 1u);
+      for (int tile = w.t0; go && tile < w.t1; ++tile) {
+        const bool withheld = tile_withheld(p, w.unit, tile);
+        for (int c = 0; c < SH::kPairs && (go = room()); ++c, ring.next()) {
+          ++places;
+          if (withheld) {
+            if (skipped == 0) skipped_from = places - 1;
+            skipped = places;
+            continue;
+          }
           if (lane == 0) mbar_arrive_expect_tx(&sm.full[ring.slot], kPairBytes);
           __syncwarp();
           if (lane < 2)
             box_load2(base + ring.slot * kPairBytes + lane * kChunkBytes, map, c * 128 + lane * 64,
                       row + tile * kAttnEntries, &sm.full[ring.slot]);
         }
+      }
     }
   } else {
     const int n = kAttnEntries / p.box_rows, chunk = lane / n, box = lane % n;
-    for (SegmentWalk w(p, blockIdx.x); w.valid(); w.next()) {
-      for (int tile = w.t0; tile < w.t1; ++tile) {
+    for (SegmentWalk w(p, blockIdx.x); go && w.valid(); w.next()) {
+      for (int tile = w.t0; go && tile < w.t1; ++tile) {
         const int e = tile * kAttnEntries + box * p.box_rows;
         bool on = chunk < 2 && e < w.u.seen;
         int slot = 0;
@@ -528,8 +550,14 @@ __device__ void tile_copy(const AttnParams& p, TileSmall& sm, uint32_t base, con
           else if (p.dev_error != nullptr) *p.dev_error = CSA_DEVERR_PAGE;
         }
         const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, on)) * p.box_rows * 128;
-        for (int c = 0; c < SH::kPairs; ++c, ring.next(), ++issued) {
-          tile_wait(sm, p, &sm.empty[ring.slot], ring.lap ^ 1u);
+        const bool withheld = tile_withheld(p, w.unit, tile);
+        for (int c = 0; c < SH::kPairs && (go = room()); ++c, ring.next()) {
+          ++places;
+          if (withheld) {
+            if (skipped == 0) skipped_from = places - 1;
+            skipped = places;
+            continue;
+          }
           if (lane == 0) mbar_arrive_expect_tx(&sm.full[ring.slot], bytes);
           __syncwarp();
           if (on)
@@ -539,9 +567,11 @@ __device__ void tile_copy(const AttnParams& p, TileSmall& sm, uint32_t base, con
       }
     }
   }
-  // after a stop, the copies that nobody waited for: the last lap of the ring
-  if (*reinterpret_cast<volatile int*>(&sm.stop) != 0)
-    for (uint32_t k = issued > SH::kRing ? issued - SH::kRing : 0; k < issued; ++k)
+  // A stop may come at any time from now on, after which nobody else waits for a copy: this warp stays
+  // until those of the ring's last lap have landed. (Each earlier one was waited for before its place was
+  // free again.)
+  for (uint32_t k = places > SH::kRing ? places - SH::kRing : 0; k < places; ++k)
+    if (k < skipped_from || k >= skipped)
       mbar_wait_bounded(&sm.full[k % SH::kRing], (k / SH::kRing) & 1u, kWaitCycles);
 }
 

@@ -26,6 +26,9 @@ cudaError_t device_sms(int dev, int* sms);
 cudaError_t blocks_per_sm(int dev, const void* kernel, int threads, size_t smem, int* blocks);
 cudaError_t launch_pdl(const void* k, dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
                        void** args);
+// hooked_wait_cycles(), hooked_withhold(): what csa_compressor_test_hooks has set.
+long long hooked_wait_cycles();
+int hooked_withhold();
 // encode_boxes(): tensor map of an array of bf16 values (rank 2 or 3, dims and box innermost
 // first, strides in bytes from the second dimension on) whose boxes land in shared memory with
 // the 128-byte swizzle; false when the driver has no such call or refuses the shape.

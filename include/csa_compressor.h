@@ -185,14 +185,17 @@ csa_status_t csa_compressor_bwd_noalloc(const void* kv, const void* score, const
 
 /* Test hook for the bounded waits: lets a test make a pipeline wait run out without any
  * fault. The pages have no counterpart; it is this library's own.
- *   wait_cycles   bound of every later pooling launch's pipeline waits, in SM clock
- *                 cycles (CSA_TEST_MIN_WAIT_CYCLES .. about 2 s); 0 restores the default
- *                 of about 2 s
+ *   wait_cycles   bound of every later pooling or cache attention launch's pipeline waits,
+ *                 in SM clock cycles (CSA_TEST_MIN_WAIT_CYCLES .. about 2 s); 0 restores the
+ *                 default of about 2 s
  *   withhold_row  >= 0: in every later launch of a bulk-copy kernel (the block-streaming
  *                 and long-window kernels), the producer of CTA (0, 0) skips the copies
  *                 of row `withhold_row` of its row range, so the waits for that stage run
  *                 out, the kernel writes CSA_DEVERR_TIMEOUT to *dev_error, lets its own
- *                 copies land and returns; < 0: off (the default)
+ *                 copies land and returns; in every later launch of the cache attention's
+ *                 tensor-core kernel, the first CTA never fills the place of tile
+ *                 `withhold_row` (128 entries) of its first unit, with the same outcome; < 0:
+ *                 off (the default)
  * Process-wide; applies to calls made after it returns, from any host thread.
  * CSA_ERR_INVALID_VALUE for a bound outside the range above. */
 csa_status_t csa_compressor_test_hooks(int64_t wait_cycles, int32_t withhold_row);
