@@ -235,7 +235,16 @@ __global__ void __launch_bounds__(kScalarThreads) attn_scalar_kernel(AttnParams 
   }
   const float sink = p.sink != nullptr ? p.sink[h] : -INFINITY;
   const float top = fmaxf(m, sink);
-  if (top != -INFINITY) {
+  // a row that has seen an infinity or NaN has one in its sums (0 * inf where its weight was 0)
+  bool odd = false;
+#pragma unroll
+  for (int j = 0; j < NL; ++j) odd = odd || acc[j] != acc[j];
+  odd = __any_sync(0xFFFFFFFFu, odd);
+  if (odd) {
+#pragma unroll
+    for (int j = 0; j < NL; ++j) acc[j] = __uint_as_float(0x7FFFFFFFu);
+    z = acc[0];
+  } else if (top != -INFINITY) {
     const float old = m == -INFINITY ? 0.f : expf(m - top);
     z = z * old + (sink == -INFINITY ? 0.f : expf(sink - top));
     const float f = old / z;
@@ -248,7 +257,7 @@ __global__ void __launch_bounds__(kScalarThreads) attn_scalar_kernel(AttnParams 
     const int c = lane + 32 * j;
     if (c < p.d) out[c] = B::from_float(acc[j]);
   }
-  if (p.lse != nullptr && lane == 0) p.lse[u] = top == -INFINITY ? -INFINITY : top + logf(z);
+  if (p.lse != nullptr && lane == 0) p.lse[u] = top == -INFINITY && !odd ? -INFINITY : top + logf(z);
 }
 
 template <typename F>

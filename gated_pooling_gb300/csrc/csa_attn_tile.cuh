@@ -64,7 +64,7 @@ struct TileCta {
 constexpr int kSoftRegs = 64, kIssueRegs = 40, kLoadRegs = 104;
 constexpr int kChunkBytes = kAttnEntries * 128;  // 128 entries x 64 columns
 constexpr int kPairBytes = 2 * kChunkBytes;
-constexpr int kSmallBytes = 11264;
+constexpr int kSmallBytes = 11776;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNoMax = -1e30f;     // bound of a row that has seen nothing
 constexpr float kRescaleAt = 8.f;    // log2 of how far a weight may pass 1
@@ -104,6 +104,7 @@ struct TileSmall {
   float fac[kAttnRows];
   float red[4][kAttnRows];  // column maxima, then weight sums, by quadrant
   int lim[2][kAttnRows];
+  uint32_t odd[kAttnEntries];  // tile (counted from 1) in which an entry of this place was found not to be finite
   uint64_t full[5], empty[5], scores[2], probs, summed, q_full, drain;
   uint32_t tmem;
   int stop;
@@ -188,6 +189,11 @@ __device__ __forceinline__ uint4 widen_any(uint32_t w, float s) {
     r[i] = pack_bf16x2(f.x * s, f.y * s);
   }
   return make_uint4(r[0], r[1], r[2], r[3]);
+}
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
 }
 // 16 bytes, or zeros, into shared memory without a register.
 __device__ __forceinline__ void copy16(uint32_t to, const void* from, bool some) {
@@ -630,6 +636,68 @@ __device__ void tile_products(const AttnParams& p, TileSmall& sm, uint32_t base,
   mbar_wait_bounded(&sm.drain, 0, kWaitCycles);
 }
 
+// Makes the infinities and NaN of entry e0 of tile t 0; whether it had any. Four threads do this for an
+// entry, one a group: one that comes late finds the others' mark.
+template <int NC>
+__device__ __forceinline__ bool clear_odd(TileSmall& sm, unsigned char* smem, uint32_t t, int e0) {
+  volatile uint32_t* const mark = &sm.odd[e0];
+  bool found = false;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
+    for (int i = 0; i < NC * 64; ++i) {
+      const uint32_t pair = t * TileShape<NC>::kPairs + (i >> 7);
+      unsigned char* at = smem + pair % TileShape<NC>::kRing * kPairBytes + (i >> 6 & 1) * kChunkBytes + e0 * 128;
+      volatile uint16_t* v = reinterpret_cast<volatile uint16_t*>(at) + (i & 63);
+      if ((*v & 0x7F80u) == 0x7F80u) {
+        found = true;
+        if (pass == 1) *v = 0;
+      }
+    }
+    __threadfence_block();
+    if (!found) found = *mark == t + 1u;
+    if (!found) break;
+    *mark = t + 1u;
+    __threadfence_block();
+  }
+  return found;
+}
+
+// A row that has seen an infinity or NaN has one in its sums (0 * inf where its weight was 0): out and lse,
+// or its piece's weight sum, become NaN throughout. (All softmax warps, rarely.)
+template <int NC>
+__device__ __forceinline__ void spread_nans(const AttnParams& p, TileSmall& sm, uint32_t sums, int par, bool whole,
+                                            int64_t piece) {
+  const int tid = threadIdx.x, lane = tid & 31, quad = (tid >> 5) & 3, c0 = (tid >> 7) * kSoftCols;
+  tc_fence_after();
+  uint32_t odd = 0;  // rows of the group
+#pragma unroll 1
+  for (int b = 0; b < TileShape<NC>::kPairs; ++b) {
+    float v[kSoftCols];
+    tmem_load16(sums + b * kAttnRows, v);
+#pragma unroll
+    for (int c = 0; c < kSoftCols; ++c) odd |= (fabsf(v[c]) <= 3.4028234e38f ? 0u : 1u) << c;
+  }
+  tc_fence_before();
+  odd = __reduce_or_sync(0xFFFFFFFFu, odd);
+  if (lane == 0) sm.red[quad][c0] = __uint_as_float(odd);
+  named_barrier(1 + (tid >> 7), 128);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) odd |= __float_as_uint(sm.red[q][c0]);
+  const float nan = __uint_as_float(0x7FFFFFFFu);
+#pragma unroll 1
+  for (int c = 0; c < kSoftCols; ++c) {
+    const int row = c0 + c;
+    if ((odd >> c & 1u) == 0 || sm.out_at[par][row] < 0) continue;
+    if (whole) {
+      for (int col = quad * 32 + lane; col < p.d; col += 128) p.out[sm.out_at[par][row] + col] = 0x7FFF;
+      if (p.lse != nullptr && quad == 0 && lane == 0) p.lse[sm.lse_at[par][row]] = nan;
+    } else if (quad == 0 && lane == 0) {
+      p.part_ml[piece * 2 * kAttnRows + kAttnRows + row] = nan;
+    }
+  }
+}
+
 // ------------------------------------------------------------------------- the softmax warps
 template <int NC, int SRC>
 __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* smem, uint32_t base, uint32_t tmem) {
@@ -674,6 +742,7 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
     if (lane == 0) mbar_arrive(&sm.q_full);
   };
   int par = 0;
+  if (tid < kAttnEntries) sm.odd[tid] = 0;
   SegmentWalk w(p, blockIdx.x);
   if (w.valid()) {
     if (tid < kAttnRows) {
@@ -703,16 +772,15 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
       tile_wait(sm, p, &sm.scores[t & 1u], (t >> 1) & 1u);
       tc_fence_after();
       float s[kSoftCols];
-      bool odd = false;  // a masked score of this entry is not finite
+      bool odd = false;  // some row of the tile does not see all of it, and a score of this entry is not finite
       auto take = [&](bool subtract) {
         tmem_load16(s_at, s);
         if (masked) {
 #pragma unroll
-          for (int c = 0; c < kSoftCols; ++c)
-            if (e >= sm.lim[par][c0 + c]) {
-              odd = odd || !(fabsf(s[c]) <= 3.4028234e38f);
-              s[c] = sl2 < 0.f ? INFINITY : -INFINITY;  // -inf once scaled
-            }
+          for (int c = 0; c < kSoftCols; ++c) {
+            odd = odd || !(fabsf(s[c]) <= 3.4028234e38f);
+            if (e >= sm.lim[par][c0 + c]) s[c] = sl2 < 0.f ? INFINITY : -INFINITY;  // -inf once scaled
+          }
         }
 #pragma unroll
         for (int c = 0; c < kSoftCols; c += 4) {
@@ -777,19 +845,19 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
 #pragma unroll
       for (int c = 0; c < 2; ++c)
         sts128(row + (((group * 2 + c) ^ (e0 & 7)) << 4), make_uint4(w2[4 * c], w2[4 * c + 1], w2[4 * c + 2], w2[4 * c + 3]));
-      if (odd) {
-        // 0 * NaN would reach the rows that do not see this entry: its non-finite values become
-        // 0 before the second product (the rows that see it have a non-finite score)
-#pragma unroll 1
-        for (int b = 0; b < NC; ++b) {
-          const int slot = static_cast<int>((t * SH::kPairs + (b >> 1)) % SH::kRing);
-          unsigned char* at = smem + slot * kPairBytes + (b & 1) * kChunkBytes + e0 * 128;
-#pragma unroll 1
-          for (int i = 0; i < 64; ++i) {
-            uint16_t* v = reinterpret_cast<uint16_t*>(at) + i;
-            if ((*v & 0x7F80u) == 0x7F80u) *v = 0;
-          }
-        }
+      if (masked && __any_sync(0xFFFFFFFFu, odd)) {
+        // 0 * NaN would reach the rows that do not see this entry: its non-finite values become 0, and the
+        // weights of the rows that see it (whose scores are not finite either) NaN
+        tmem_load16(s_at, s);
+        if (odd && clear_odd<NC>(sm, smem, t, e0))
+#pragma unroll
+          for (int c = 0; c < kSoftCols; ++c)
+            if (e < sm.lim[par][c0 + c] && !(fabsf(s[c]) <= 3.4028234e38f)) {
+              l[c] = __uint_as_float(0x7FFFFFFFu);
+              asm volatile("st.shared.b16 [%0], %1;" ::"r"(row + (((group * 2 + (c >> 3)) ^ (e0 & 7)) << 4) + 2 * (c & 7)),
+                           "h"(static_cast<uint16_t>(0x7FFF))
+                           : "memory");
+            }
       }
       fence_proxy_async_smem();
       tc_fence_before();
@@ -852,6 +920,7 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
     }
     if (more) q_copied();
     barrier_group();
+    uint32_t probe = 0;  // two bf16, one NaN once one of this thread's sums is (or, harmlessly, at huge ones)
     if (whole) {
       // O^T times the rows' factors, as bf16 rows: a warp's 32 columns of its 16 rows at a time are
       // transposed by 8 x 8 matrices through its 1 KB of P's place (two rows to 128 bytes, their 16-byte
@@ -868,10 +937,12 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
         float v[2][8];
         tmem_load_fragments(lanes + SH::kTmemO + b * kAttnRows + c0, v);
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          store_transposed(place(to_row, to_piece + h * 2), pack_bf16x2(v[h][0] * f0, v[h][1] * f1),
-                           pack_bf16x2(v[h][2] * f0, v[h][3] * f1), pack_bf16x2(v[h][4] * f2, v[h][5] * f3),
-                           pack_bf16x2(v[h][6] * f2, v[h][7] * f3));
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t a = pack_bf16x2(v[h][0] * f0, v[h][1] * f1), b2 = pack_bf16x2(v[h][2] * f0, v[h][3] * f1);
+          const uint32_t c2 = pack_bf16x2(v[h][4] * f2, v[h][5] * f3), d = pack_bf16x2(v[h][6] * f2, v[h][7] * f3);
+          store_transposed(place(to_row, to_piece + h * 2), a, b2, c2, d);
+          probe = fma_bf16x2(c2, d, fma_bf16x2(a, b2, probe));
+        }
         __syncwarp();
         const int col = b * 128 + quad * 32 + (lane & 3) * 8;
 #pragma unroll
@@ -890,6 +961,10 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
       for (int b = 0; b < SH::kPairs; ++b) {
         float v[kSoftCols];
         tmem_load16(lanes + SH::kTmemO + b * kAttnRows + c0, v);
+        float product = 0.f;
+#pragma unroll
+        for (int c = 0; c < kSoftCols; c += 2) product = fmaf(v[c], v[c + 1], product);
+        probe |= product != product ? 0x7FFFu : 0u;
 #pragma unroll
         for (int c = 0; c < kSoftCols; c += 4)
           if (sm.out_at[par][c0 + c] >= 0)
@@ -905,7 +980,9 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
       w.u = sm.next;
       w.bound();
     }
-    named_barrier(5, kSoftThreads);  // sm.next and P's place are free again
+    // (sm.next and P's place are free again)
+    if (named_barrier_or(5, kSoftThreads, (probe & 0x7FFFu) > 0x7F80u || (probe >> 16 & 0x7FFFu) > 0x7F80u))
+      spread_nans<NC>(p, sm, lanes + SH::kTmemO + c0, par, whole, piece);
   }
 }
 

@@ -384,7 +384,9 @@ csa_status_t csa_cache_read(const void* data, const uint8_t* scales, int32_t for
  *     out = sum_e w_e k_e,  w_e = exp(softmax_scale q.k_e) / (sum over seen entries + exp(sink[h]))
  *     lse = log(that denominator)
  *   (sink NULL: no such term). A token that sees nothing gets out = 0 and lse = sink[h], or
- *   -inf without a sink. An infinity or NaN in an entry reaches only the tokens that see it.
+ *   -inf without a sink. An entry that holds an infinity or NaN makes out and lse NaN for the tokens
+ *   that see it (all columns of the heads that read it), and reaches no other token. A score of +inf
+ *   or NaN does the same to its row; one of -inf (finite values past fp32) weighs nothing.
  *   Scores, maxima and sums are fp32; the weights are rounded to bf16 before the second
  *   product on the tensor cores (off by at most 2^-8 of each, as the outputs themselves are).
  * ------------------------------------------------------------------------------------ */
