@@ -66,7 +66,7 @@ constexpr int kChunkBytes = kAttnEntries * 128;  // 128 entries x 64 columns
 constexpr int kPairBytes = 2 * kChunkBytes;
 constexpr int kSmallBytes = 11776;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kNoMax = -1e30f;     // bound of a row that has seen nothing
+constexpr float kNoMax = -3.4028234e38f;  // bound of a row that has seen nothing: no score lies below it
 constexpr float kRescaleAt = 8.f;    // log2 of how far a weight may pass 1
 
 // NC: 64-column chunks of an entry (2, 4, 8).
@@ -773,7 +773,7 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
       tc_fence_after();
       float s[kSoftCols];
       bool odd = false;  // some row of the tile does not see all of it, and a score of this entry is not finite
-      auto take = [&](bool subtract) {
+      auto take = [&]() {
         tmem_load16(s_at, s);
         if (masked) {
 #pragma unroll
@@ -782,26 +782,31 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
             if (e >= sm.lim[par][c0 + c]) s[c] = sl2 < 0.f ? INFINITY : -INFINITY;  // -inf once scaled
           }
         }
+      };
+      auto scale = [&]() {
 #pragma unroll
         for (int c = 0; c < kSoftCols; c += 4) {
-          const float4 m = subtract ? *reinterpret_cast<const float4*>(&sm.m[c0 + c]) : make_float4(0.f, 0.f, 0.f, 0.f);
+          const float4 m = *reinterpret_cast<const float4*>(&sm.m[c0 + c]);
           s[c] = fmaf(s[c], sl2, -m.x);
           s[c + 1] = fmaf(s[c + 1], sl2, -m.y);
           s[c + 2] = fmaf(s[c + 2], sl2, -m.z);
           s[c + 3] = fmaf(s[c + 3], sl2, -m.w);
         }
       };
-      take(true);
+      take();
+      scale();
       float top = fmaxf(s[0], s[1]);
 #pragma unroll
       for (int c = 2; c < kSoftCols; c += 2) top = fmax3(top, s[c], s[c + 1]);
       if (named_barrier_or(1 + group, 128, top > kRescaleAt)) {
-        // new bounds: the true maxima so far
-        take(false);
+        // new bounds: the true maxima so far, rounded down. A score less its row's maximum is then what the
+        // rounding left, never below 0; far from zero (2^27 and more) that may pass any weight, and is
+        // cut off (a difference of one step of the fp32 score that it stands for).
+        take();
         float mine = kNoMax;
 #pragma unroll
         for (int c = 0; c < kSoftCols; ++c) {
-          const float v = warp_max_f32(s[c]);
+          const float v = warp_max_f32(__fmul_rd(s[c], sl2));
           if (lane == c) mine = v;
         }
         if (lane < kSoftCols) sm.red[quad][c0 + lane] = mine;
@@ -829,7 +834,10 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
             tmem_store16(at, s);
           }
         }
-        take(true);
+        take();
+        scale();
+#pragma unroll
+        for (int c = 0; c < kSoftCols; ++c) s[c] = min_nan(s[c], kRescaleAt);
       }
       // weights; their sums before rounding
       uint32_t w2[kSoftCols / 2];

@@ -130,6 +130,12 @@ __host__ __device__ constexpr uint32_t mma_desc(int m, int n, int a_along_k, int
          (static_cast<uint32_t>(m / 16) << 24);
 }
 
+// The smaller one, NaN if either is.
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 // Maximum over the warp's lanes (NaN ignored unless every lane has one).
 __device__ __forceinline__ float warp_max_f32(float v) {
   float r;

@@ -115,3 +115,31 @@ def test_rows_that_score_everything_below_fp32(cuda_lib, way, sink):
     assert err == 0 and (out[:n] == 0).all()
     want = torch.full((n, H), -math.inf) if c.sink is None else c.sink.expand(n, H)
     assert torch.equal(lse[:n].cpu(), want)
+
+
+@pytest.mark.parametrize("way", WAYS)
+@pytest.mark.parametrize("size", [1e7, 1e9, 1e11, 1e16, 1e28, 1e30, 1e33, 1e37])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("sink", [False, True])
+def test_scores_far_from_zero(cuda_lib, way, size, sign, sink):
+    """Every score finite and far from zero, a single exact product: the highest one has all the weight (out is
+    its entry, the weight and the output rounded to 16 bits, 2^-8 each), and lse is its score or (far below
+    zero) the sink. Its scale and the scale's way through log2 and back (two constants and two products)
+    round it five times by half a step (U), the score's own product once by a whole one."""
+    H, kv, d, page, n = way
+    c = Case([n], [300], H, kv, d, page=page, ratio=0, sink=sink, seed=d + 1)
+    c.q.zero_()
+    c.q[:, :, 3] = math.sqrt(size)
+    top = 170
+    for e in range(300):
+        c.data[slot_of(c, e), :, 3] = sign * math.sqrt(size) * (1 if e == top else 1 - sign * 0.5)
+    out, lse, err = c.run(cuda_lib)
+    score = c.q[0, 0, 3].double() * c.data[slot_of(c, top), 0, 3].double() * c.scale
+    out, lse = out[:n].double().cpu(), lse[:n].double().cpu()
+    assert err == 0
+    if sink and sign < 0:
+        assert (out == 0).all() and ((lse - c.sink).abs() <= 7 * R.U * c.sink.abs()).all()
+    else:
+        want = c.data[slot_of(c, top)].double().repeat_interleave(H // kv, 0).expand(n, H, d)
+        assert ((out - want).abs() <= 2.01 * 2.0 ** -8 * want.abs()).all()
+        assert ((lse - score).abs() <= 7 * R.U * score.abs()).all()
