@@ -706,8 +706,9 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
   const int c0 = group * kSoftCols;     // the rows (columns of S^T) of this group of four warps
   const int e0 = quad * 32 + lane;      // the entry (row of S^T) of this thread
   const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-  // (a scale of 0, under which every score is equal, becomes one that no score can show)
-  const float sl2 = p.scale == 0.f ? 1.17549435e-38f : p.scale * kLog2e;
+  // (a scale of 0, under which every score is equal, becomes the least one: no finite score exceeds 2^-20
+  // under it, and masked ones stay infinite)
+  const float sl2 = p.scale == 0.f ? 1.4e-45f : p.scale * kLog2e;
   uint32_t t = 0;  // tiles so far
   auto barrier_group = [&]() { named_barrier(1 + group, 128); };
 

@@ -143,3 +143,19 @@ def test_scores_far_from_zero(cuda_lib, way, size, sign, sink):
         want = c.data[slot_of(c, top)].double().repeat_interleave(H // kv, 0).expand(n, H, d)
         assert ((out - want).abs() <= 2.01 * 2.0 ** -8 * want.abs()).all()
         assert ((lse - score).abs() <= 7 * R.U * score.abs()).all()
+
+
+@pytest.mark.parametrize("way", WAYS)
+@pytest.mark.parametrize("scale", [0.0, -0.0, -0.3, 1e-45, 1e-30])
+@pytest.mark.parametrize("place", PLACES)
+def test_scales_of_zero_and_below(cuda_lib, way, scale, place):
+    """A scale of 0 weighs every entry alike however large the products, a negative one turns their order, and
+    neither lets a masked entry through."""
+    c, _, _ = case(cuda_lib, way, place, True)
+    c.scale = scale
+    if scale >= 0:
+        c.q[:, :, 3] = 1e19
+        sign = torch.sign(c.data[:, :, 3].float())
+        c.data[:, :, 3] = (sign * 1e18).to(torch.bfloat16)
+        c.values = c.data.double()
+    agree(c, list(range(c.cu[1])), c.reference())
