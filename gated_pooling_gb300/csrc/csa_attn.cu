@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kScalarThreads) attn_scalar_kernel(AttnParams 
     z = acc[0];
   } else if (top != -INFINITY) {
     const float old = m == -INFINITY ? 0.f : expf(m - top);
-    z = z * old + (sink == -INFINITY ? 0.f : expf(sink - top));
+    z = z * old + (sink == -INFINITY ? 0.f : sink == top ? 1.f : expf(sink - top));
     const float f = old / z;
 #pragma unroll
     for (int j = 0; j < NL; ++j) acc[j] *= f;
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kScalarThreads) attn_scalar_kernel(AttnParams 
     const int c = lane + 32 * j;
     if (c < p.d) out[c] = B::from_float(acc[j]);
   }
-  if (p.lse != nullptr && lane == 0) p.lse[u] = top == -INFINITY && !odd ? -INFINITY : top + logf(z);
+  if (p.lse != nullptr && lane == 0) p.lse[u] = top == -INFINITY && !odd ? sink : top + logf(z);
 }
 
 template <typename F>

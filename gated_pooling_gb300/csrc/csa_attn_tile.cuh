@@ -195,6 +195,8 @@ __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t 
   asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
   return d;
 }
+// Weight of a sink (in log2) at the row's maximum, which it may be, an infinite one too.
+__device__ __forceinline__ float sink_weight(float sink, float mx) { return sink == mx ? 1.f : fast_exp2(sink - mx); }
 // 16 bytes, or zeros, into shared memory without a register.
 __device__ __forceinline__ void copy16(uint32_t to, const void* from, bool some) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(some ? 16 : 0) : "memory");
@@ -921,7 +923,7 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
         const float sink_e = sm.sink[par][c], sink = sink_e * kLog2e;
         const float mx = fmaxf(z > 0.f || z != z ? m : -INFINITY, sink);
         const float old = mx == -INFINITY ? 0.f : fast_exp2(m - mx);
-        const float den = mx == -INFINITY ? 0.f : z * old + fast_exp2(sink - mx);
+        const float den = mx == -INFINITY ? 0.f : z * old + sink_weight(sink, mx);
         sm.fac[c] = mx == -INFINITY ? 0.f : old / den;
         if (p.lse != nullptr && sm.lse_at[par][c] >= 0) p.lse[sm.lse_at[par][c]] = z == 0.f ? sink_e : (mx + log2f(den)) * kLn2;
       }
@@ -1147,7 +1149,7 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinBlocks) attn_join_kernel(co
     const int token = row / p.group, head_of = u.kvh * p.group + (row - token * p.group);
     const int64_t at = static_cast<int64_t>(u.token) + token, out_at = at * p.out_row + head_of * p.out_head;
     const float sink_e = p.sink != nullptr && row < u.rows ? __ldg(p.sink + head_of) : -INFINITY;
-    float mx = sink_e * kLog2e, den = 0.f;
+    float mx = fmaxf(sink_e * kLog2e, -INFINITY), den = 0.f;  // (a sink of NaN is no maximum)
     bool some = false;
     for (int k = kk; k < n; k += 8) {
       const float* x = ml + slot(k) * 2 * kAttnRows;
@@ -1166,7 +1168,7 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinBlocks) attn_join_kernel(co
     }
 #pragma unroll
     for (int s = 4; s > 0; s >>= 1) den += __shfl_xor_sync(0xFFFFFFFFu, den, s);
-    const float all = mx == -INFINITY ? 1.f : den + fast_exp2(sink_e * kLog2e - mx), inverse = 1.f / all;
+    const float all = mx == -INFINITY ? 1.f : den + sink_weight(sink_e * kLog2e, mx), inverse = 1.f / all;
     float4 acc[2] = {};
     while (true) {
       const float f = mx == -INFINITY ? 0.f : fast_exp2(m0 - mx);

@@ -383,7 +383,7 @@ csa_status_t csa_cache_read(const void* data, const uint8_t* scales, int32_t for
  *   Query head h reads the entries' head h / (q_heads / kv_heads):
  *     out = sum_e w_e k_e,  w_e = exp(softmax_scale q.k_e) / (sum over seen entries + exp(sink[h]))
  *     lse = log(that denominator)
- *   (sink NULL: no such term). A token that sees nothing gets out = 0 and lse = sink[h], or
+ *   (sink NULL: no such term, nor at a sink of -inf; one of +inf takes all the weight). A token that sees nothing gets out = 0 and lse = sink[h], or
  *   -inf without a sink. An entry that holds an infinity or NaN makes out and lse NaN for the tokens
  *   that see it (all columns of the heads that read it), and reaches no other token. A score of +inf
  *   or NaN does the same to its row; one of -inf (finite values past fp32) weighs nothing.

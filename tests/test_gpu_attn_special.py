@@ -159,3 +159,47 @@ def test_scales_of_zero_and_below(cuda_lib, way, scale, place):
         c.data[:, :, 3] = (sign * 1e18).to(torch.bfloat16)
         c.values = c.data.double()
     agree(c, list(range(c.cu[1])), c.reference())
+
+
+@pytest.mark.parametrize("way,lens,entries,first", [(w, [w[4], 3], [300, 40], [0, 60]) for w in WAYS] + [
+    ((16, 1, 128, 64, 1), [1], [3001], [6001]), ((16, 1, 512, 64, 2), [2], [20500], [40999]),
+    ((64, 1, 128, 9, 1), [1, 1], [1500, 3001], [2999, 6001])])
+def test_sinks_that_are_not_finite(cuda_lib, way, lens, entries, first):
+    """A sink of -inf is none, one of +inf takes all the weight (out 0, lse +inf), one of NaN makes NaN; a token
+    that sees nothing gets out 0 and lse the sink, whatever it is. In units by themselves and joined ones."""
+    H, kv, d, page, _ = way
+    c = Case(lens, entries, H, kv, d, page=page, ratio=2, first=first, seed=d)
+    free = c.reference()
+    c.sink = torch.tensor([math.inf, math.nan, -math.inf, 1.5])[torch.arange(H) % 4]
+    held = Case(lens, entries, H, kv, d, page=page, ratio=2, first=first, seed=d)
+    held.sink = torch.where(torch.isfinite(c.sink), c.sink, torch.zeros(()))
+    held = held.reference()
+    out, lse, err = c.run(cuda_lib)
+    out, lse, T = out.double().cpu(), lse.double().cpu(), c.cu[-1]
+    assert err == 0
+    blind = torch.isinf(free[1][:T]).any(1)  # (without a sink)
+    assert blind[0] == (first[0] == 0) and not blind.all()
+    assert (out[:T][blind] == 0).all()
+    assert torch.equal(lse[:T][blind].nan_to_num(7.0, 8.0, 9.0), c.sink.double().nan_to_num(7.0, 8.0, 9.0).expand(int(blind.sum()), H))
+    sees = ~blind
+    for h in range(H):
+        got, gl = out[:T, h][sees], lse[:T, h][sees]
+        if c.sink[h] == math.inf:
+            assert (got == 0).all() and (gl == math.inf).all()
+        elif torch.isnan(c.sink[h]):
+            assert torch.isnan(got).all() and torch.isnan(gl).all()
+        else:
+            ref, rl, tol, ltol = (t[:T, h][sees] for t in (free if c.sink[h] == -math.inf else held))
+            assert ((got - ref).abs() <= tol).all() and ((gl - rl).abs() <= ltol).all()
+
+
+@pytest.mark.parametrize("way", WAYS)
+def test_a_row_whose_scores_are_all_nan(cuda_lib, way):
+    """out and lse NaN, with a sink and without."""
+    H, kv, d, page, n = way
+    for sink in (False, True):
+        c = Case([n], [20], H, kv, d, page=page, ratio=0, sink=sink, seed=d)
+        c.q[1, 1, 0] = math.nan
+        out, lse, err = c.run(cuda_lib)
+        assert err == 0 and torch.isnan(out[1, 1]).all() and torch.isnan(lse[1, 1])
+        assert int(torch.isnan(lse).sum()) == 1 and int(torch.isnan(out).any(-1).sum()) == 1
