@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnParams p) {
   for (int i = threadIdx.x; i < p.workers; i += kPlanThreads) {
     const Place a = place(share(i)), b = place(share(i + 1));
     AttnStart start{};
-    start.left = static_cast<int32_t>(b.before - a.before);
+    start.left = b.before - a.before;
     if (start.left > 0) {
       start.u = p.units[a.unit];
       start.unit = static_cast<int32_t>(a.unit);

@@ -27,7 +27,8 @@ struct alignas(16) AttnUnit {
 };
 struct alignas(16) AttnStart {  // a worker's share: its first unit, the tile there, and how many tiles
   AttnUnit u;
-  int32_t unit, tile, left, pad;
+  int32_t unit, tile;
+  int64_t left;
 };
 struct alignas(16) AttnJoin {  // a unit whose tiles several workers share, from `worker` on
   AttnUnit u;
@@ -108,13 +109,13 @@ __device__ __forceinline__ AttnUnit make_unit(const AttnParams& p, int s, int kv
 struct AttnShares {
   int64_t work, q;
   int n, r;
-  __device__ __forceinline__ AttnShares(int64_t w, int workers) : work(w) {
+  __host__ __device__ __forceinline__ AttnShares(int64_t w, int workers) : work(w) {
     n = w < workers ? static_cast<int>(w) : workers;
     const int d = n > 0 ? n : 1;
     q = w < INT_MAX ? static_cast<int>(w) / d : w / d;
     r = static_cast<int>(w - q * d);
   }
-  __device__ __forceinline__ int64_t operator()(int i) const {
+  __host__ __device__ __forceinline__ int64_t operator()(int i) const {
     return i >= n ? work : q * i + static_cast<int>(static_cast<uint32_t>(r) * static_cast<uint32_t>(i) / static_cast<uint32_t>(n));
   }
   // the worker whose share x < work lies in, or one next to it

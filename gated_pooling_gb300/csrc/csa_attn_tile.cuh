@@ -359,18 +359,19 @@ __device__ __forceinline__ AttnUnit read_unit(const AttnUnit* at) {
 // The runs of tiles of one unit in a worker's share.
 struct SegmentWalk {
   const AttnParams& p;
-  int unit, t0, t1, left;  // (a CTA's share stays below 2^31 tiles: checked on the host)
+  int unit, t0, t1;
+  int64_t left;
   AttnUnit u;
   __device__ __forceinline__ SegmentWalk(const AttnParams& pp, int worker) : p(pp) {
     const AttnStart* at = p.starts + worker;
     u = read_unit(&at->u);
-    const int4 v = __ldg(reinterpret_cast<const int4*>(at) + 3);
-    unit = v.x;
-    t0 = v.y;
-    left = v.z;
+    const longlong2 v = __ldg(reinterpret_cast<const longlong2*>(at) + 3);
+    unit = static_cast<int>(v.x);
+    t0 = static_cast<int>(v.x >> 32);
+    left = v.y;
     bound();
   }
-  __device__ __forceinline__ void bound() { t1 = left < u.tiles - t0 ? t0 + left : u.tiles; }
+  __device__ __forceinline__ void bound() { t1 = left < u.tiles - t0 ? t0 + static_cast<int>(left) : u.tiles; }
   __device__ __forceinline__ bool valid() const { return left > 0; }
   __device__ __forceinline__ void next() {
     left -= t1 - t0;
