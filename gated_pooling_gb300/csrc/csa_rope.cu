@@ -6,7 +6,8 @@
 //
 // Angles: a pair turns by positions[r] * turns[i] in units of 2^-64 of a full turn, an
 // integer product modulo 2^64. Its upper 32 bits, taken as a signed number, are the angle
-// within half a turn either way, to 2^-32 of a turn, whatever the position; only then does
+// within half a turn either way, to 2^-32 of a turn, whatever the position (turns[i] is the nearest
+// whole number, so a position below 2^31 is off by 2^-34 of a turn from it); only then does
 // it become a float. No position loses precision, and no 64-bit floating point is needed.
 #include <cmath>
 #include <climits>
@@ -652,6 +653,65 @@ RopeParams rope_params(int64_t rows, int32_t heads, int32_t d, const float* weig
   return p;
 }
 
+// Numbers as the unevaluated sum of two doubles, |lo| at most half a step of hi, for the table on the
+// host: 64 bits of a turn are more than a double holds. Sums and products with the errors of their
+// roundings as in Dekker (1971) and Knuth; each operation is within a few 2^-104. (volatile: no sum is
+// contracted with the product before it, whatever the compiler's default.)
+struct Twofold {
+  double hi, lo;
+};
+constexpr Twofold kInvTwoPi{0x1.45f306dc9c883p-3, -0x1.6b01ec5417056p-57};
+constexpr Twofold kLnTwo{0x1.62e42fefa39efp-1, 0x1.abc9e3b39803fp-56};
+Twofold sum_of(double a, double b) {
+  const volatile double s = a + b, v = s - a, u = s - v;
+  const volatile double x = a - u, y = b - v;
+  return {s, x + y};
+}
+Twofold plus(Twofold a, Twofold b) {
+  const Twofold s = sum_of(a.hi, b.hi);
+  const volatile double low = a.lo + b.lo;
+  const Twofold t = sum_of(s.hi, s.lo + low);
+  return t;
+}
+Twofold times(Twofold a, Twofold b) {
+  const volatile double p = a.hi * b.hi, x = a.hi * b.lo, y = a.lo * b.hi;
+  const volatile double e = std::fma(a.hi, b.hi, -p), c = x + y;
+  return sum_of(p, e + c);
+}
+Twofold over(Twofold a, double b) {
+  const volatile double q = a.hi / b;
+  const Twofold back = times({q, 0.0}, {b, 0.0});
+  const Twofold rest = plus(a, {-back.hi, -back.lo});
+  return sum_of(q, rest.hi / b);
+}
+// e^x = the result times 2^*e: Taylor's series of the remainder's 256th part, squared eight times.
+Twofold exp_of(Twofold x, int* e) {
+  const double k = std::nearbyint(x.hi / kLnTwo.hi);
+  const Twofold r = plus(x, times(kLnTwo, {-k, 0.0}));
+  const Twofold y{r.hi / 256, r.lo / 256};
+  Twofold s{1.0, 0.0};
+  for (int n = 16; n > 0; --n) s = plus({1.0, 0.0}, times(over(y, n), s));
+  for (int n = 0; n < 8; ++n) s = times(s, s);
+  *e = static_cast<int>(k);
+  return s;
+}
+// ln x of a double above 0: one step of Newton's method from the double's.
+Twofold log_of(double x) {
+  int e, k;
+  const double m = std::frexp(x, &e), y = std::log(m);
+  Twofold b = exp_of({-y, 0.0}, &k);
+  b = {std::ldexp(b.hi, k), std::ldexp(b.lo, k)};
+  const Twofold rest = plus(times(b, {m, 0.0}), {-1.0, 0.0});
+  return plus(times(kLnTwo, {static_cast<double>(e), 0.0}), plus({y, 0.0}, rest));
+}
+// x 2^e, between 0 and 2^63, to the nearest whole number.
+uint64_t nearest(Twofold x, int e) {
+  const double hi = std::ldexp(x.hi, e), whole = std::nearbyint(hi);
+  const volatile double left = hi - whole;
+  return static_cast<uint64_t>(static_cast<int64_t>(whole) +
+                               static_cast<int64_t>(std::nearbyint(left + std::ldexp(x.lo, e))));
+}
+
 }  // namespace
 }  // namespace csa
 
@@ -681,14 +741,16 @@ extern "C" csa_status_t csa_rope_table(int32_t rot_dim, double base, int32_t sca
     const double hi = std::fmin(std::fmax(std::ceil(at(beta_slow)), 0.0), last);
     span = std::fmax(hi - lo, 0.001);
   }
+  const Twofold one{1.0, 0.0}, log_base = log_of(base);
   for (int32_t i = 0; i < rot_dim / 2; ++i) {
-    double f = std::pow(base, -2.0 * i / rot_dim);
-    if (scaling == CSA_ROPE_LINEAR) f /= factor;
+    int e;
+    Twofold f = exp_of(times(over(log_base, rot_dim), {-2.0 * i, 0.0}), &e);
+    if (scaling == CSA_ROPE_LINEAR) f = over(f, factor);
     if (scaling == CSA_ROPE_YARN) {
-      const double m = std::fmin(std::fmax((i - lo) / span, 0.0), 1.0);
-      f = f / factor * m + f * (1.0 - m);
+      const Twofold m = i <= lo ? Twofold{0.0, 0.0} : i - lo >= span ? one : over({i - lo, 0.0}, span);
+      f = plus(times(over(f, factor), m), times(f, plus(one, {-m.hi, -m.lo})));
     }
-    turns_host[i] = static_cast<uint64_t>(std::nearbyint(std::ldexp(f / two_pi, 64)));
+    turns_host[i] = nearest(times(f, kInvTwoPi), e + 64);
   }
   if (amplitude != nullptr)
     *amplitude = scaling == CSA_ROPE_YARN ? static_cast<float>(0.1 * std::log(factor) + 1.0) : 1.f;
