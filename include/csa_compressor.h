@@ -417,9 +417,12 @@ size_t csa_cache_attn_workspace_bytes(int32_t S, int64_t tokens, int32_t q_heads
  * CSA_DEVERR_PAGE the outputs of that sequence are unspecified. Results are bitwise
  * reproducible for the same arguments on the same device. The tensor-core kernel runs when
  * d <= 512, d and the strides of q and out are multiples of 8, and q, out and data 16-byte
- * aligned; anything else takes a scalar kernel, many times slower. With many new tokens a
- * sequence the workspace has room for the sequences' entries as bf16 rows of 128, 256 or 512
- * columns (up to 4 GiB, of max_entries each). A wait that runs out reports CSA_DEVERR_TIMEOUT
+ * aligned; anything else takes a scalar kernel, many times slower (with many rows, slower than
+ * ordinary matrix products would be). With many new tokens a sequence the workspace has room
+ * for the sequences' entries as bf16 rows of 128, 256 or 512 columns (up to 4 GiB, of max_entries
+ * each), whether the format and the pages come to use it or not. "Many" is the average of
+ * `tokens` over S: where a few long chunks come with many single tokens, or `tokens` is far above
+ * cu_seqlens[S], a call for each kind, or with the tokens there are, is faster. A wait that runs out reports CSA_DEVERR_TIMEOUT
  * and leaves the outputs unspecified. */
 csa_status_t csa_cache_attn(const void* q, int64_t q_row_stride, int64_t q_head_stride,
                             const int32_t* cu_seqlens, int32_t S, int64_t tokens, int32_t q_heads,
