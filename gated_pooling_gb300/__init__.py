@@ -23,6 +23,7 @@ _lib: Optional[ctypes.CDLL] = None
 CSA_OK, CSA_ERR_INVALID_VALUE, CSA_ERR_UNSUPPORTED, CSA_ERR_WORKSPACE, CSA_ERR_CUDA = 0, 1, 2, 3, 4
 CSA_DEVERR_CU_SEQLENS, CSA_DEVERR_OUT_ROWS, CSA_DEVERR_TIMEOUT, CSA_DEVERR_LEAD = 1, 2, 3, 4
 CSA_DEVERR_SLOT, CSA_DEVERR_ENTRIES, CSA_DEVERR_PAGE = 5, 6, 7
+CSA_DEVERR_STATE, CSA_DEVERR_PREFIX = 8, 9
 CSA_DTYPE_BF16, CSA_DTYPE_FP16, CSA_DTYPE_FP32 = 0, 1, 2
 CSA_ROPE_PLAIN, CSA_ROPE_LINEAR, CSA_ROPE_YARN = 0, 1, 2
 CSA_ROPE_HALF, CSA_ROPE_INTERLEAVED = 0, 1
@@ -35,7 +36,8 @@ EXPORTED = ("csa_status_string", "csa_last_error_string", "csa_compressor_total_
             "csa_compressor_bwd_noalloc", "csa_compressor_test_hooks",
             "csa_compressor_map_blocks", "csa_kpool_total", "csa_kpool_fwd", "csa_rope_table",
             "csa_norm_rope_fwd", "csa_norm_rope_bwd_workspace_bytes", "csa_norm_rope_bwd",
-            "csa_cache_write", "csa_cache_read", "csa_cache_attn_workspace_bytes", "csa_cache_attn")
+            "csa_cache_write", "csa_cache_read", "csa_cache_attn_workspace_bytes", "csa_cache_attn",
+            "csa_compressor_step", "csa_cache_append")
 
 
 class CsaError(RuntimeError):
@@ -102,6 +104,12 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.csa_cache_attn.restype = ctypes.c_int
     lib.csa_cache_attn.argtypes = [vp, i64, i64, vp, i32, i64, i32, i32, i32, vp, vp, i32, vp, i32,
                                    i64, i32, vp, vp, i32, f32, vp, vp, i64, i64, vp, vp, sz, vp, vp]
+    lib.csa_compressor_step.restype = ctypes.c_int
+    lib.csa_compressor_step.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, i64, vp, vp, vp, i64, vp, vp,
+                                        vp, i64, vp, vp, i32, i32, i32, vp, vp, vp, vp, vp]
+    lib.csa_cache_append.restype = ctypes.c_int
+    lib.csa_cache_append.argtypes = [vp, i32, i64, i32, i32, i64, i64, vp, i32, f32, vp, vp, i32, i32, i32,
+                                     f32, vp, i64, i32, vp, vp, vp, vp]
     if path == LIB_PATH:
         _lib = lib
     return lib
@@ -316,3 +324,31 @@ def csa_cache_attn(q, q_row_stride: int, q_head_stride: int, cu_seqlens, S: int,
                                  out_row_stride, out_head_stride, _ptr(lse), _ptr(workspace),
                                  workspace_bytes, _ptr(dev_error), _stream(stream)),
            "csa_cache_attn")
+
+
+def csa_compressor_step(kv, score, ape, cu_seqlens, S: int, ratio: int, coff: int, d: int,
+                        capacity: int, first, source, target, num_states: int, kv_state,
+                        score_state, out, out_rows: int, base=None, page_table=None,
+                        max_pages: int = 0, page_size: int = 1, position_offset: int = 0,
+                        positions=None, slots=None, entries=None, dev_error=None,
+                        stream=None) -> None:
+    """New tokens of each sequence pooled on from a state, which is updated."""
+    _check(load().csa_compressor_step(_ptr(kv), _ptr(score), _ptr(ape), _ptr(cu_seqlens), S, ratio,
+                                      coff, d, capacity, _ptr(first), _ptr(source), _ptr(target),
+                                      num_states, _ptr(kv_state), _ptr(score_state), _ptr(out),
+                                      out_rows, _ptr(base), _ptr(page_table), max_pages, page_size,
+                                      position_offset, _ptr(positions), _ptr(slots), _ptr(entries),
+                                      _ptr(dev_error), _stream(stream)), "csa_compressor_step")
+
+
+def csa_cache_append(x, dtype: int, rows: int, heads: int, d: int, x_row_stride: int,
+                     x_head_stride: int, weight, norm: int, eps: float, positions, turns,
+                     rot_dim: int, rot_start: int, layout: int, amplitude: float, slots,
+                     num_slots: int, format: int, data, scales, dev_error=None,
+                     stream=None) -> None:
+    """Rows normed, turned to their positions and put into slots of the paged cache."""
+    _check(load().csa_cache_append(_ptr(x), dtype, rows, heads, d, x_row_stride, x_head_stride,
+                                   _ptr(weight), int(norm), eps, _ptr(positions), _ptr(turns),
+                                   rot_dim, rot_start, layout, amplitude, _ptr(slots), num_slots,
+                                   format, _ptr(data), _ptr(scales), _ptr(dev_error),
+                                   _stream(stream)), "csa_cache_append")

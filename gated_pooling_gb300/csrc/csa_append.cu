@@ -1,0 +1,302 @@
+// csa_append.cu -- rows normed, turned to their positions and put into slots of the paged cache in one
+// pass (the interface is in csa_compressor.h; norm and rotation as in csa_rope.cu, formats as in
+// csa_cache.cu).
+//
+// What lies between reading x and writing the codes stays in registers, so a value is rounded once, to
+// its code, where a norm and rotation followed by a cache write round twice and pass the row through
+// memory in between. Bound by HBM bytes: x once, codes and scales once.
+//
+// Angles and roots are taken as for fp32 results whatever x's type: a code's border may be anywhere, and
+// what fp32 rounding leaves is what a code may be off by.
+#include <climits>
+#include <cstdint>
+#include <type_traits>
+
+#include "csa_compressor.h"
+#include "csa_element.cuh"
+#include "csa_internal.h"
+#include "csa_rope.cuh"
+
+namespace csa {
+namespace {
+
+struct AppendParams {
+  RopeParams r;
+  uint8_t* data;
+  uint8_t* scales;
+  const int64_t* slots;
+  int64_t num_slots;
+  int32_t* dev_error;
+};
+
+// A row's slot, -1 where the row is left out (a negative position or slot, or one past the pool, which is
+// reported).
+__device__ __forceinline__ int64_t append_slot(const AppendParams& p, int64_t row, int32_t pos) {
+  const int64_t s = __ldg(p.slots + row);
+  if (pos < 0 || s < 0) return -1;
+  if (s < p.num_slots) return s;
+  if (p.dev_error != nullptr) *p.dev_error = CSA_DEVERR_SLOT;
+  return -1;
+}
+
+// Scalar kernel, any d and alignment: a warp per row and head, which leaves the finished row in shared
+// memory and then takes it 32 columns, a scale's, at a time.
+template <int DTYPE, int FORMAT>
+__global__ void __launch_bounds__(kRopeThreads) append_scalar_kernel(AppendParams q) {
+  using E = Element<DTYPE>;
+  using T = typename E::T;
+  extern __shared__ float s_rows[];  // [warps][d]
+  const RopeParams& p = q.r;
+  const int lane = threadIdx.x & 31, groups = (p.d + 31) / 32;
+  float* n = s_rows + (threadIdx.x >> 5) * p.d;
+  pdl_wait();
+  for (int64_t u = static_cast<int64_t>(blockIdx.x) * kRopeWarps + (threadIdx.x >> 5); u < p.units;
+       u += static_cast<int64_t>(gridDim.x) * kRopeWarps) {
+    const int64_t row = static_cast<int>(u) / p.heads, head = u - row * p.heads;  // (units below 2^31)
+    const int32_t pos = p.pos != nullptr ? __ldg(p.pos + row) : 0;
+    const int64_t slot = append_slot(q, row, pos);
+    if (slot < 0) continue;
+    const T* x = static_cast<const T*>(p.x) + row * p.x_row + head * p.x_head;
+    float ss = 0.f;
+    for (int c = lane; c < p.d; c += 32) {
+      const float v = E::to_float(x[c]);
+      n[c] = v;
+      ss = fmaf(v, v, ss);
+    }
+    if (p.norm) {
+      const float r = __frsqrt_rn(warp_sum(ss) / static_cast<float>(p.d) + p.eps);
+      for (int c = lane; c < p.d; c += 32) n[c] = p.weight != nullptr ? n[c] * r * __ldg(p.weight + c) : n[c] * r;
+    }
+    __syncwarp();
+    for (int i = lane; i < p.rot / 2; i += 32) {
+      int a, b;
+      pair_columns(p, i, a, b);
+      float cs, sn;
+      turn_cos_sin(pos, __ldg(p.turns + i), p.amp, cs, sn);
+      const float va = n[a], vb = n[b];
+      n[a] = va * cs - vb * sn;
+      n[b] = va * sn + vb * cs;
+    }
+    __syncwarp();
+    const int64_t entry = slot * p.heads + head;
+    for (int g = 0; g < groups; ++g) {
+      const int col = g * 32 + lane;
+      const float v = col < p.d ? n[col] : 0.f;
+      if constexpr (FORMAT == CSA_CACHE_BF16) {
+        if (col < p.d) reinterpret_cast<uint16_t*>(q.data)[entry * p.d + col] = Element<CSA_DTYPE_BF16>::from_float(v);
+      } else {
+        const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v) & 0x7FFFFFFFu);
+        const uint32_t k = scale_byte<FORMAT>(top);
+        const float c = v * scale_inverse(k == 255u ? 127u : k);
+        if (lane == 0) q.scales[entry * groups + g] = static_cast<uint8_t>(k);
+        if constexpr (FORMAT == CSA_CACHE_E4M3) {
+          q.data[entry * p.d + col] = static_cast<uint8_t>(float2_to_e4m3x2(c, 0.f) & 0xFFu);
+        } else {
+          const float hi = __shfl_down_sync(0xFFFFFFFFu, c, 1);
+          if (lane % 2 == 0) q.data[entry * (p.d / 2) + col / 2] = static_cast<uint8_t>(float2_to_e2m1x2(c, hi));
+        }
+      }
+    }
+    __syncwarp();
+  }
+}
+
+// Vector kernel: lanes, pieces and runs as in the norm and rotation's. A scale belongs to four
+// pieces of 8 columns, which the rotation's pairing leaves with any lanes; the pieces' largest
+// magnitudes meet in shared memory, 4 bytes a piece, and each lane reads its group's four at once.
+template <int DTYPE, int PP, int FORMAT>
+__global__ void __launch_bounds__(kRopeThreads, PP == 1 && DTYPE != CSA_DTYPE_FP32 ? 3 : 2)
+    append_vec_kernel(AppendParams q) {
+  __shared__ __align__(16) float s_w[CSA_MAX_HEAD_DIM];
+  __shared__ __align__(16) uint32_t s_top[kRopeWarps][64 * PP];
+  const RopeParams& p = q.r;
+  RopeLane<DTYPE, PP> L(p);
+  uint32_t* top = s_top[threadIdx.x >> 5] + L.group * (p.d / 8);
+  pdl_wait();
+  stage_weight(p, s_w);
+  const float inv_d = 1.f / static_cast<float>(p.d);
+  RopeRun run(p, L.group, L.groups);
+  int64_t base = run.u - L.group;  // the warp's first unit: all its lanes leave the loop together
+  RopePieces<DTYPE, PP> cur, nxt;
+  int32_t pos = -1, pos_n = -1;
+  int64_t slot = -1, slot_n = -1;
+  auto fetch = [&](RopePieces<DTYPE, PP>& v, int32_t& ps, int64_t& at) {
+    ps = -1;
+    at = -1;
+    if (run.valid()) {
+      ps = p.pos != nullptr ? __ldg(p.pos + run.row) : 0;
+      at = append_slot(q, run.row, ps);
+      v.load(L, p.x, run.row * p.x_row + run.head * p.x_head);
+    }
+  };
+  fetch(cur, pos, slot);
+  int64_t turned = -1;
+  for (; base < run.end; base += L.groups) {
+    const int64_t row = run.row;
+    const int head = run.head;
+    run.next(p, L.groups);
+    fetch(nxt, pos_n, slot_n);
+    float xa[PP][8], xb[PP][8];
+    float ss = 0.f;
+#pragma unroll
+    for (int s = 0; s < PP; ++s) {
+      cur.a[s].get(xa[s]);
+      cur.b[s].get(xb[s]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (L.a[s] >= 0) ss = fmaf(xa[s][i], xa[s][i], ss);
+        if (L.b[s] >= 0) ss = fmaf(xb[s][i], xb[s][i], ss);
+      }
+    }
+    const float r = p.norm ? __frsqrt_rn(fmaf(L.sum(p, ss), inv_d, p.eps)) : 1.f;
+    if (slot >= 0) {
+      if (row != turned) {
+        L.template turn_to<CSA_DTYPE_FP32>(p, pos);
+        turned = row;
+      }
+#pragma unroll
+      for (int s = 0; s < PP; ++s) {
+        if (p.norm) {
+          float w[8];
+          if (L.a[s] >= 0) {
+            read_weight(s_w, L.a[s], w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) xa[s][i] = xa[s][i] * r * w[i];
+          }
+          if (L.b[s] >= 0) {
+            read_weight(s_w, L.b[s], w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) xb[s][i] = xb[s][i] * r * w[i];
+          }
+        }
+        L.template turn<false>(p, s, xa[s], xb[s]);
+      }
+    }
+    const int64_t entry = slot * p.heads + head;
+    if constexpr (FORMAT == CSA_CACHE_BF16) {
+      uint16_t* y = reinterpret_cast<uint16_t*>(q.data) + entry * p.d;
+#pragma unroll
+      for (int s = 0; s < PP; ++s) {
+        Eight<CSA_DTYPE_BF16> o;
+        if (slot >= 0 && L.a[s] >= 0) {
+          o.set(xa[s]);
+          o.store(y + L.a[s]);
+        }
+        if (slot >= 0 && L.b[s] >= 0) {
+          o.set(xb[s]);
+          o.store(y + L.b[s]);
+        }
+      }
+    } else {
+      auto largest = [](const float (&v)[8]) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+        return m;
+      };
+#pragma unroll
+      for (int s = 0; s < PP; ++s) {
+        if (L.a[s] >= 0) top[L.a[s] >> 3] = largest(xa[s]);
+        if (L.b[s] >= 0) top[L.b[s] >> 3] = largest(xb[s]);
+      }
+      __syncwarp();
+      auto put = [&](int col, const float (&v)[8]) {
+        const uint4 g = *reinterpret_cast<const uint4*>(top + (col >> 5) * 4);
+        const uint32_t k = scale_byte<FORMAT>(max(max(g.x, g.y), max(g.z, g.w)));
+        const float inv = scale_inverse(k == 255u ? 127u : k);
+        if constexpr (FORMAT == CSA_CACHE_E4M3) {
+          uint2 w;
+          w.x = float2_to_e4m3x2(v[0] * inv, v[1] * inv) | (static_cast<uint32_t>(float2_to_e4m3x2(v[2] * inv, v[3] * inv)) << 16);
+          w.y = float2_to_e4m3x2(v[4] * inv, v[5] * inv) | (static_cast<uint32_t>(float2_to_e4m3x2(v[6] * inv, v[7] * inv)) << 16);
+          *reinterpret_cast<uint2*>(q.data + entry * p.d + col) = w;
+        } else {
+          *reinterpret_cast<uint32_t*>(q.data + entry * (p.d / 2) + col / 2) =
+              float2_to_e2m1x2(v[0] * inv, v[1] * inv) | (float2_to_e2m1x2(v[2] * inv, v[3] * inv) << 8) |
+              (float2_to_e2m1x2(v[4] * inv, v[5] * inv) << 16) | (float2_to_e2m1x2(v[6] * inv, v[7] * inv) << 24);
+        }
+        if ((col & 31) == 0) q.scales[entry * (p.d / CSA_CACHE_GROUP) + col / CSA_CACHE_GROUP] = static_cast<uint8_t>(k);
+      };
+      if (slot >= 0) {
+#pragma unroll
+        for (int s = 0; s < PP; ++s) {
+          if (L.a[s] >= 0) put(L.a[s], xa[s]);
+          if (L.b[s] >= 0) put(L.b[s], xb[s]);
+        }
+      }
+      __syncwarp();
+    }
+    cur = nxt;
+    pos = pos_n;
+    slot = slot_n;
+  }
+}
+
+template <typename F>
+auto by_format(int format, F f) {
+  return format == CSA_CACHE_BF16   ? f(std::integral_constant<int, CSA_CACHE_BF16>{})
+         : format == CSA_CACHE_E4M3 ? f(std::integral_constant<int, CSA_CACHE_E4M3>{})
+                                    : f(std::integral_constant<int, CSA_CACHE_E2M1>{});
+}
+
+}  // namespace
+}  // namespace csa
+
+using namespace csa;
+
+extern "C" csa_status_t csa_cache_append(const void* x, int32_t dtype, int64_t rows, int32_t heads,
+                                         int32_t d, int64_t x_row_stride, int64_t x_head_stride,
+                                         const float* weight, int32_t norm, float eps,
+                                         const int32_t* positions, const uint64_t* turns,
+                                         int32_t rot_dim, int32_t rot_start, int32_t layout,
+                                         float amplitude, const int64_t* slots, int64_t num_slots,
+                                         int32_t format, void* data, uint8_t* scales,
+                                         int32_t* dev_error, csa_stream_t stream) {
+  const csa_status_t st = check_rope(dtype, rows, heads, d, weight, norm, eps, positions, turns, rot_dim,
+                                     rot_start, layout);
+  if (st != CSA_OK) return st;
+  if (x_row_stride < 0 || x_head_stride < 0 || num_slots < 0) return CSA_ERR_INVALID_VALUE;
+  if (format < CSA_CACHE_BF16 || format > CSA_CACHE_E2M1) return CSA_ERR_UNSUPPORTED;
+  if (format != CSA_CACHE_BF16 && d % CSA_CACHE_GROUP != 0) return CSA_ERR_UNSUPPORTED;
+  if (num_slots > INT64_MAX / 64 / (static_cast<int64_t>(heads) * d)) return CSA_ERR_UNSUPPORTED;
+  if (!is_aligned(x, dtype_size(dtype)) || !is_aligned(slots, 8) || !is_aligned(dev_error, 4) ||
+      (format == CSA_CACHE_BF16 && !is_aligned(data, 2)))
+    return CSA_ERR_INVALID_VALUE;
+  if (rows > 0 && (x == nullptr || slots == nullptr)) return CSA_ERR_INVALID_VALUE;
+  if (num_slots > 0 && (data == nullptr || (format != CSA_CACHE_BF16 && scales == nullptr)))
+    return CSA_ERR_INVALID_VALUE;
+  if (rows == 0) return CSA_OK;
+  AppendParams p{};
+  p.r = rope_params(rows, heads, d, weight, norm, eps, positions, turns, rot_dim, rot_start, layout, amplitude);
+  p.r.x = x;
+  p.r.x_row = x_row_stride;
+  p.r.x_head = x_head_stride;
+  p.r.lanes = vector_lanes(p.r, dtype, x, data, nullptr);
+  p.data = static_cast<uint8_t*>(data);
+  p.scales = scales;
+  p.slots = slots;
+  p.num_slots = num_slots;
+  p.dev_error = dev_error;
+  const bool wide = vector_pairs(p.r) == 2;
+  const void* k = by_dtype(dtype, [&](auto t) {
+    return by_format(format, [&](auto f) {
+      constexpr int T = decltype(t)::value, F = decltype(f)::value;
+      return p.r.lanes == 0 ? reinterpret_cast<const void*>(append_scalar_kernel<T, F>)
+             : wide         ? reinterpret_cast<const void*>(append_vec_kernel<T, 2, F>)
+                            : reinterpret_cast<const void*>(append_vec_kernel<T, 1, F>);
+    });
+  });
+  // one run of heads a resident warp
+  const size_t smem = p.r.lanes == 0 ? sizeof(float) * kRopeWarps * d : 0;
+  int dev = 0, sms = 0, bps = 0;
+  if (note(cudaGetDevice(&dev)) != cudaSuccess || device_sms(dev, &sms) != cudaSuccess ||
+      blocks_per_sm(dev, k, kRopeThreads, smem, &bps) != cudaSuccess)
+    return CSA_ERR_CUDA;
+  const int64_t per = kRopeWarps * (p.r.lanes == 0 ? 1 : 32 / p.r.lanes), most = static_cast<int64_t>(sms) * bps;
+  int64_t blocks = (p.r.units + per - 1) / per;
+  if (blocks > most) blocks = most;
+  void* args[] = {&p};
+  return launch_pdl(k, dim3(static_cast<unsigned>(blocks)), dim3(kRopeThreads), smem,
+                    reinterpret_cast<cudaStream_t>(stream), args) == cudaSuccess
+             ? CSA_OK
+             : CSA_ERR_CUDA;
+}

@@ -73,7 +73,13 @@ typedef enum {
 #define CSA_DEVERR_SLOT 5       /* cache: a slot >= num_slots (that row alone is skipped) */
 #define CSA_DEVERR_ENTRIES 6    /* cache attention: entries[s] < 0 or > max_pages * page_size */
 #define CSA_DEVERR_PAGE 7       /* cache attention: a page number a sequence needs is outside
-                                   [0, num_pages); its entries are not read */
+                                   [0, num_pages); its entries are not read. Step: an entry's page is
+                                   behind the table's end or negative; its slot is -1 */
+#define CSA_DEVERR_STATE 8      /* step: first[s] negative or past 2^31 with the new tokens, source[s] or
+                                   target[s] >= num_states, or source[s] < 0 where tokens of earlier
+                                   calls are needed */
+#define CSA_DEVERR_PREFIX 9     /* prefix attention: prefix_seqs does not run from 0 to S without decreasing, or
+                                   prefix_entries[g] < 0 or > max_prefix_pages * page_size */
 
 /* Limits checked on the host (CSA_ERR_UNSUPPORTED beyond them). */
 #define CSA_MAX_SEGMENTS 16384   /* S */
@@ -208,6 +214,62 @@ csa_status_t csa_compressor_test_hooks(int64_t wait_cycles, int32_t withhold_row
 csa_status_t csa_compressor_map_blocks(const int32_t* cu_seqlens, int32_t S, int32_t ratio,
                                        int64_t capacity, int64_t out_rows, int32_t* seg_blk_base,
                                        int32_t* dev_error, csa_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * Pooling of a stream: the windows of csa_compressor_fwd over tokens that come in several calls, one
+ * or many a sequence at a time.
+ *
+ *   Sequence s has had first[s] tokens before this call, and its new ones are [cu_seqlens[s],
+ *   cu_seqlens[s+1]): token cu_seqlens[s] + i stands at position p = first[s] + i. Its block b
+ *   covers the positions [b ratio, (b + 1) ratio), and an entry is made of every block whose last
+ *   token is among the new ones, with the window, the softmax and the rounding of
+ *   csa_compressor_fwd (a window whose scores are all -inf gives NaN). out's rows are these
+ *   entries, sequence by sequence, blocks in order:
+ *     sum over s of floor((first[s] + n_s) / ratio) - floor(first[s] / ratio), n_s new tokens.
+ *   What a later window still reads lies in a state, kv and score bf16 [ratio * coff, coff * d] each;
+ *   position p's row is p mod (ratio * coff). Sequence s goes on from state source[s] and
+ *   leaves its tokens in state target[s], often the same one. With B = floor((first[s] + n_s) / ratio)
+ *   the elements that state target[s] holds after the call are
+ *     coff=1: all columns of the positions p >= B ratio;
+ *     coff=2: the columns < d of p >= (B - 1) ratio, and the columns >= d of p >= B ratio;
+ *   all other elements stay as they were. Several sequences may go on from one state (samples of one
+ *   prompt); a state that one sequence leaves its tokens in belongs to that sequence alone: no other
+ *   sequence of the call may name it. Negative: source[s] where nothing of earlier calls is needed
+ *   (first[s] = 0; at coff=1 a multiple of ratio, at coff=2 also any first[s] < ratio that is one), target[s]
+ *   where nothing is to be kept. A sequence without new tokens has its state copied if source and target
+ *   differ.
+ * ------------------------------------------------------------------------------------ */
+
+/*   kv, score, ape, cu_seqlens, capacity, out   as for csa_compressor_fwd
+ *   first, source, target   int32 [S] (device)
+ *   kv_state, score_state   bf16 [num_states, ratio * coff, coff * d] (device)
+ *   out_rows    rows of out, positions and slots; more entries than that skip all outputs
+ *               (CSA_DEVERR_OUT_ROWS)
+ *   base        int32 [S] (device) or NULL (0): how many of a sequence's first entries lie elsewhere, as a
+ *               shared prefix does; entry b is number b - base[s] in the sequence's pages
+ *   page_table  int32 [S, max_pages] (device), read only where slots are wanted
+ *   positions   int32 [out_rows] (device) or NULL: b * ratio + position_offset of each row's block
+ *               (0 <= position_offset < ratio), -1 in the rows behind the last entry
+ *   slots       int64 [out_rows] (device) or NULL: where each row goes in a cache of pages of page_size
+ *               entries, -1 behind the last entry, where b < base[s], and where the page is
+ *               negative or behind the table's end (the latter two report CSA_DEVERR_PAGE)
+ *   entries     int32 [S] (device) or NULL: the entries that lie in the sequence's own pages after the
+ *               call, max(0, B - base[s])
+ * positions and slots are what csa_cache_append takes, entries what the attention takes, so a step needs
+ * no number on the host. Outputs overlap no input but for the states. Bad lengths or states (CSA_DEVERR_CU_SEQLENS,
+ * CSA_DEVERR_STATE) skip all outputs. CSA_ERR_INVALID_VALUE and CSA_ERR_UNSUPPORTED as for
+ * csa_compressor_fwd (any d and ratio up to CSA_MAX_WINDOW / coff; no smaller limit for unaligned
+ * tensors), and num_states above 2^31 - 1. The vector kernels run when d is a multiple of 8 and kv, score, ape,
+ * out and the states are 16-byte aligned; anything else takes a column a thread. One kernel is enqueued. */
+csa_status_t csa_compressor_step(const void* kv, const void* score, const float* ape,
+                                 const int32_t* cu_seqlens, int32_t S, int32_t ratio, int32_t coff,
+                                 int32_t d, int64_t capacity, const int32_t* first,
+                                 const int32_t* source, const int32_t* target, int64_t num_states,
+                                 void* kv_state, void* score_state, void* out, int64_t out_rows,
+                                 const int32_t* base, const int32_t* page_table, int32_t max_pages,
+                                 int32_t page_size, int32_t position_offset, int32_t* positions,
+                                 int64_t* slots, int32_t* entries, int32_t* dev_error,
+                                 csa_stream_t stream);
 
 /* ------------------------------------------------------------------------------------
  * KPool: the DSA indexer's key pooling ("Megatron-LM PR #8835", the KPool commits: the
@@ -361,6 +423,23 @@ csa_status_t csa_cache_write(const void* x, int32_t dtype, int64_t rows, int32_t
                              int64_t x_row_stride, int64_t x_head_stride, const int64_t* slots,
                              int64_t num_slots, int32_t format, void* data, uint8_t* scales,
                              int32_t* dev_error, csa_stream_t stream);
+
+/* Norms rows, turns them to their positions and writes them into the cache: csa_norm_rope_fwd and
+ * csa_cache_write in one pass, without the rounding to x's type between them (each value is worked out in
+ * fp32 and rounded once, to the format).
+ *   x           dtype [rows, heads, d] with row and head strides in elements (device); may repeat
+ *   weight, norm, eps, positions, turns, rot_dim, rot_start, layout, amplitude   as for csa_norm_rope_fwd
+ *   slots, num_slots, format, data, scales, dev_error   as for csa_cache_write
+ * A row whose position or whose slot is negative is left out. x overlaps neither data nor scales. Refusals as
+ * for the two calls. The vector kernel runs where csa_norm_rope_fwd's does with data in y's place;
+ * anything else takes a scalar kernel. */
+csa_status_t csa_cache_append(const void* x, int32_t dtype, int64_t rows, int32_t heads, int32_t d,
+                              int64_t x_row_stride, int64_t x_head_stride, const float* weight,
+                              int32_t norm, float eps, const int32_t* positions,
+                              const uint64_t* turns, int32_t rot_dim, int32_t rot_start,
+                              int32_t layout, float amplitude, const int64_t* slots,
+                              int64_t num_slots, int32_t format, void* data, uint8_t* scales,
+                              int32_t* dev_error, csa_stream_t stream);
 
 /* Reads rows of the cache back: out[r] = the entry in slots[r], in `dtype`, out [rows, heads,
  * d] with strides in elements that give every element a place of its own. A negative slot

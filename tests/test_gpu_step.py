@@ -1,0 +1,266 @@
+"""Pooling of a stream through the C ABI against the 64-bit windows: calls of one and of many tokens, blocks that
+begin in one call and end in another, every kernel, states kept in place, copied and forked, entries'
+positions and slots, values out of the ordinary, refusals on the device, graphs."""
+import math
+import random
+
+import pytest
+import torch
+
+from tests import operator_reference as R
+from tests import serving_reference as V
+
+pytestmark = pytest.mark.gpu
+I32 = dict(dtype=torch.int32, device="cuda")
+
+
+class Stream:
+    """Sequences whose tokens come call by call, the state slots that they use, and what they have had."""
+
+    def __init__(self, gp, S, ratio, coff, d, total, seed=0, shift=0, states=None, page=4):
+        g = torch.Generator().manual_seed(seed)
+        self.gp, self.S, self.ratio, self.coff, self.d, self.shift, self.page = gp, S, ratio, coff, d, shift, page
+        C, W = coff * d, coff * ratio
+        self.kv, self.score = (torch.randn(S, total, C, generator=g).to(torch.bfloat16) for _ in range(2))
+        self.ape = 0.3 * torch.randn(ratio, C, generator=g)
+        self.states = S + 2 if states is None else states
+        self.kv_state, self.score_state = (self.dev(torch.full((self.states, W, C), float("nan"), dtype=torch.bfloat16))
+                                           for _ in range(2))
+        self.first = [0] * S
+        self.slot = torch.randperm(self.states, generator=g)[:S].tolist()
+        self.max_pages = max(1, -(-(total // ratio) // page))
+        self.table = torch.randperm(S * self.max_pages, generator=g).reshape(S, -1).to(torch.int32)
+
+    def dev(self, t):
+        flat = torch.empty(t.numel() + 16, dtype=t.dtype, device="cuda")
+        v = flat[self.shift:self.shift + t.numel()].view(t.shape)
+        v.copy_(t)
+        return v
+
+    def call(self, lens, source=None, target=None, spare=3, pad=2, lead=0, base=None, offset=0):
+        """One call, checked in full; the sequences have len more tokens after it."""
+        source, target = self.slot if source is None else source, self.slot if target is None else target
+        S, ratio, coff, d, page = self.S, self.ratio, self.coff, self.d, self.page
+        cu = [lead]
+        for n in lens:
+            cu.append(cu[-1] + n)
+        rows = sum((f + n) // ratio - f // ratio for f, n in zip(self.first, lens)) + spare
+        kv, score = (torch.full((cu[-1] + pad, coff * d), float("nan"), dtype=torch.bfloat16) for _ in range(2))
+        for s, n in enumerate(lens):
+            for to, of in ((kv, self.kv), (score, self.score)):
+                to[cu[s]:cu[s] + n] = of[s, self.first[s]:self.first[s] + n]
+        before = [t.clone() for t in (self.kv_state, self.score_state)]
+        out = self.dev(torch.full((rows, d), 7.0, dtype=torch.bfloat16))
+        positions = torch.full((rows,), 77, **I32)
+        slots = torch.full((rows,), 77, dtype=torch.int64, device="cuda")
+        entries, err = torch.full((S,), 77, **I32), torch.zeros(1, **I32)
+        dbase = None if base is None else torch.tensor(base, **I32)
+        self.gp.csa_compressor_step(
+            self.dev(kv), self.dev(score), self.ape.cuda() if not self.shift else self.dev(self.ape), torch.tensor(cu, **I32), S, ratio, coff, d,
+            cu[-1] + pad, torch.tensor(self.first, **I32), torch.tensor(source, **I32), torch.tensor(target, **I32),
+            self.states, self.kv_state, self.score_state, out, rows, dbase, self.table.cuda(), self.max_pages, page, offset,
+            positions, slots, entries, err)
+        torch.cuda.synchronize()
+        assert int(err) == 0
+        out, positions, slots = out.double().cpu(), positions.tolist(), slots.tolist()
+        row, after = 0, [t.cpu().clone() for t in before]
+        for s, n in enumerate(lens):
+            f, mine = self.first[s], 0 if base is None else base[s]
+            for b in range(f // ratio, (f + n) // ratio):
+                ref, bound = V.window_entry(self.kv[s], self.score[s], self.ape, b, ratio, coff, d)
+                off = (out[row] - ref).abs()
+                assert (off <= bound).all(), (s, b, float((off / bound).max()))
+                assert positions[row] == b * ratio + offset
+                e = b - mine
+                assert slots[row] == (int(self.table[s, e // page]) * page + e % page if e >= 0 else -1)
+                row += 1
+            assert int(entries[s]) == max(0, (f + n) // ratio - mine)
+            if target[s] >= 0:
+                at = V.held(f, n, ratio, coff, d)
+                cols = torch.arange(coff * d).expand_as(at)
+                for want, of in zip(after, (self.kv, self.score)):
+                    want[target[s]] = torch.where(at >= 0, of[s][at.clamp(min=0), cols], want[target[s]])
+            self.first[s] = f + n
+        assert (out[row:] == 7.0).all() and positions[row:] == [-1] * spare and slots[row:] == [-1] * spare
+        for want, got in zip(after, (self.kv_state, self.score_state)):
+            assert torch.equal(want.view(torch.int16), got.cpu().view(torch.int16))
+
+
+SHAPES = [(4, 2, 512), (4, 2, 64), (2, 2, 128), (1, 2, 64), (1, 1, 64), (2, 1, 40), (3, 1, 64), (4, 1, 128), (8, 1, 128),
+          (8, 2, 64), (5, 2, 64), (3, 2, 552), (16, 1, 64), (128, 1, 64), (128, 2, 32), (40, 2, 24), (4, 2, 65), (1, 1, 7),
+          (128, 2, 9), (2, 1, 13), (7, 1, 33), (4, 1, 5)]
+
+
+@pytest.mark.parametrize("ratio,coff,d,shift", [(*s, 0) for s in SHAPES] + [(*s, 1) for s in SHAPES if s[2] in (64, 512)])
+def test_calls_of_any_length(cuda_lib, ratio, coff, d, shift):
+    rng = random.Random(ratio * 64 + d)
+    st = Stream(cuda_lib, 5, ratio, coff, d, 8 * ratio + 40, seed=d, shift=shift)
+    for i in range(6):
+        most = [1, ratio, 2 * ratio + 3, 1, ratio + 1, 2][i]
+        st.call([rng.randint(0, most) if i else most for _ in range(5)], spare=i % 3, lead=i, offset=i % ratio)
+
+
+@pytest.mark.parametrize("ratio,coff,d", [(4, 2, 512), (4, 1, 64), (16, 2, 64), (2, 2, 64), (3, 2, 11)])
+def test_single_tokens(cuda_lib, ratio, coff, d):
+    st = Stream(cuda_lib, 7, ratio, coff, d, 5 * ratio + 6, seed=3)
+    st.call([s for s in range(7)])  # every sequence at another place of its block
+    for _ in range(3 * ratio - 1):
+        st.call([1] * 7, spare=1)
+
+
+@pytest.mark.parametrize("ratio,coff,d", [(4, 2, 512), (4, 1, 512), (128, 1, 64), (128, 2, 128), (1, 1, 512), (2, 1, 256)])
+def test_long_chunks(cuda_lib, ratio, coff, d):
+    st = Stream(cuda_lib, 3, ratio, coff, d, 1700, seed=4)
+    st.call([5, 0, 700], spare=0)
+    st.call([901, 333, 130], pad=0)
+    st.call([1, 511, 0])
+
+
+@pytest.mark.parametrize("S", [1, 300, 2000])
+def test_many_sequences(cuda_lib, S):
+    st = Stream(cuda_lib, S, 4, 2, 16, 12, seed=5)
+    st.call([s % 5 for s in range(S)], spare=5)
+    st.call([(s * 7) % 4 for s in range(S)], spare=0)
+    st.call([1] * S, spare=0)
+
+
+@pytest.mark.parametrize("ratio,coff,d", [(4, 2, 64), (4, 1, 64), (16, 2, 32), (3, 2, 5)])
+def test_states_copied_and_forked(cuda_lib, ratio, coff, d):
+    """Two prompts; then five sequences go on from the first one's state in states of their own, one without a
+    token; a sequence that keeps nothing."""
+    S = 6
+    st = Stream(cuda_lib, S, ratio, coff, d, 6 * ratio, seed=6, states=2 * S)
+    for t in (st.kv, st.score):
+        t[1:5, :2 * ratio + 1] = t[0, :2 * ratio + 1]
+    begun = 2 * ratio + 1
+    st.call([begun, 0, 0, 0, 0, ratio], target=[0, -1, -1, -1, -1, 1], source=[-1] * S)
+    st.first[1:5] = [begun] * 4
+    st.call([1, ratio, 0, 2, ratio + 2, 1], source=[0] * 5 + [1], target=[5, 6, 7, 8, 9, 1])
+    st.call([ratio] * 5 + [2], source=[5, 6, 7, 8, 9, 1], target=[5, 6, 7, 8, 9, 11])
+    st.call([ratio - 1] * 5 + [2], source=[5, 6, 7, 8, 9, 11], target=[-1] * 6)
+
+
+def test_prefix_entries_lie_elsewhere(cuda_lib):
+    st = Stream(cuda_lib, 3, 4, 2, 64, 60, seed=7)
+    st.call([21, 8, 30], base=[3, 0, 9])
+    st.call([9, 8, 30], base=[3, 0, 9])
+
+
+def test_calls_are_repeatable(cuda_lib):
+    """The same bits from the same inputs, whatever lay in the outputs."""
+    for ratio, coff, d in ((4, 2, 512), (128, 2, 64)):
+        got = []
+        for _ in range(2):
+            st = Stream(cuda_lib, 4, ratio, coff, d, 700, seed=8)
+            st.call([300, 7, 0, 129])
+            st.call([200, 400, 1, 3])
+            got.append((st.kv_state.clone(), st.score_state.clone()))
+        assert all(torch.equal(a.view(torch.int16), b.view(torch.int16)) for a, b in zip(*got))
+
+
+def raw(gp, ratio=2, coff=1, d=8, cu=(0, 4), first=(0,), source=(0,), target=(0,), states=1, rows=4, kv=None, score=None, table=None,
+        max_pages=0, page=1, base=None, capacity=None, nulls=False):
+    """A small call whatever it holds; its outputs."""
+    S = len(cu) - 1
+    capacity = max(cu[-1], 0) if capacity is None else capacity
+    C, W = coff * d, coff * ratio
+    kv = torch.ones(capacity, C, dtype=torch.bfloat16, device="cuda") if kv is None else kv
+    score = torch.zeros(capacity, C, dtype=torch.bfloat16, device="cuda") if score is None else score
+    st = [torch.full((states, W, C), 5.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    out = torch.full((rows, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    pos, slots = torch.full((rows,), 77, **I32), torch.full((rows,), 77, dtype=torch.int64, device="cuda")
+    entries, err = torch.full((max(S, 1),), 77, **I32), torch.zeros(1, **I32)
+    t = lambda v: torch.tensor(v, **I32)  # noqa: E731
+    gp.csa_compressor_step(kv, score, torch.zeros(ratio, C, device="cuda"), t(cu), S, ratio, coff, d, capacity, t(first), t(source),
+                           t(target), states, *st, out, rows, None if base is None else t(base), None if table is None else t(table),
+                           max_pages, page, 0, None if nulls else pos, None if nulls or table is None else slots,
+                           None if nulls else entries, err)
+    torch.cuda.synchronize()
+    return int(err), out.cpu(), st, pos.tolist(), slots.tolist(), entries.tolist()
+
+
+@pytest.mark.parametrize("code,how", [
+    (1, dict(cu=(0, 5, 3), first=(0, 0), source=(0, 0), target=(0, 0), capacity=8)), (1, dict(cu=(0, 9), capacity=8)),
+    (1, dict(cu=(-1, 3), capacity=8)), (2, dict(rows=1)), (8, dict(first=(-1,))), (8, dict(first=(2 ** 31 - 2,))),
+    (8, dict(source=(1,))), (8, dict(target=(7,))), (8, dict(first=(3,), source=(-1,))),
+    (8, dict(coff=2, first=(2,), source=(-1,))), (8, dict(cu=(0, 0), first=(3,), source=(-1,), rows=0, capacity=1)),
+])
+def test_device_refusals_leave_all_as_it_was(cuda_lib, code, how):
+    err, out, st, pos, slots, entries = raw(cuda_lib, **how)
+    assert err == code and (out == 7.0).all() and all((t == 5.0).all() for t in st)
+    assert set(pos) <= {77} and set(entries) == {77}
+
+
+def test_calls_that_need_no_state(cuda_lib):
+    assert raw(cuda_lib, first=(4,), source=(-1,))[0] == 0  # coff 1 at a block's beginning
+    err, out, st, *_ = raw(cuda_lib, cu=(0, 3), source=(-1,), target=(-1,), states=0)
+    assert err == 0 and (out[0] == 1.0).all() and (out[1:] == 7.0).all()
+    assert raw(cuda_lib, cu=(0, 0), first=(3,), source=(-1,), target=(-1,), rows=2, capacity=1)[3] == [-1, -1]  # a padded sequence
+    assert raw(cuda_lib, cu=(0,), first=(), source=(), target=(), rows=2, capacity=1)[3] == [-1, -1]  # no sequence at all
+    assert raw(cuda_lib, nulls=True)[0] == 0
+
+
+def test_pages_that_are_missing(cuda_lib):
+    err, out, _, pos, slots, entries = raw(cuda_lib, cu=(0, 8), rows=5, table=((3, -1),), max_pages=2, page=1)
+    assert err == 7 and slots == [3, -1, -1, -1, -1] and pos == [0, 2, 4, 6, -1] and entries == [4] and (out[:4] == 1.0).all()
+    err, _, _, _, slots, entries = raw(cuda_lib, cu=(0, 8), rows=4, table=((3, 9),), max_pages=2, page=1, base=(2,))
+    assert err == 0 and slots == [-1, -1, 3, 9] and entries == [2]
+
+
+@pytest.mark.parametrize("ratio,coff,d", [(4, 1, 8), (4, 1, 7), (32, 1, 8), (2, 1, 8)])
+def test_values_out_of_the_ordinary(cuda_lib, ratio, coff, d):
+    """A score of -inf weighs nothing, a window of nothing else is NaN, as are those with a score of +inf or
+    NaN; a lowest score beside others weighs nothing."""
+    g = torch.Generator().manual_seed(9)
+    kv = torch.randn(5 * ratio, d, generator=g).to(torch.bfloat16)
+    score = torch.randn(5 * ratio, d, generator=g).to(torch.bfloat16)
+    score[1, :] = -math.inf
+    score[ratio:2 * ratio, :] = -math.inf
+    score[2 * ratio, :] = math.inf
+    score[3 * ratio + 1, :] = math.nan
+    score[4 * ratio:5 * ratio - 1, :] = -3.3895e38
+    err, out, *_ = raw(cuda_lib, ratio, coff, d, (0, 5 * ratio), rows=5, kv=kv.cuda(), score=score.cuda())
+    assert err == 0 and torch.isnan(out[1:4]).all()
+    for b in (0, 4):
+        x = score[b * ratio:(b + 1) * ratio].double()
+        ref = (torch.softmax(x, 0) * kv[b * ratio:(b + 1) * ratio].double()).sum(0)
+        assert ((out[b].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 1e-5).all()  # (fp32: about 50 U of values of 4 at most)
+
+
+def test_graph_of_steps(cuda_lib):
+    """A captured step that moves its own lengths on, replayed, against the calls one by one."""
+    ratio, coff, d, S = 4, 2, 64, 3
+    g = torch.Generator().manual_seed(10)
+    steps = [torch.randn(S, coff * d, generator=g).to(torch.bfloat16).cuda() for _ in range(19)]
+    ape = torch.randn(ratio, coff * d, generator=g).cuda()
+
+    def make():
+        c = dict(kv=torch.zeros(S, coff * d, dtype=torch.bfloat16, device="cuda"), first=torch.tensor([0, 1, 2], **I32),
+                 own=torch.arange(S, **I32), cu=torch.arange(S + 1, **I32), err=torch.zeros(1, **I32),
+                 out=torch.zeros(S, d, dtype=torch.bfloat16, device="cuda"), pos=torch.zeros(S, **I32))
+        c["state"] = [torch.zeros(S, coff * ratio, coff * d, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        return c
+
+    def step(c):
+        cuda_lib.csa_compressor_step(c["kv"], c["kv"], ape, c["cu"], S, ratio, coff, d, S, c["first"], c["own"], c["own"], S,
+                                     *c["state"], c["out"], S, None, None, 0, 1, 0, c["pos"], None, None, c["err"])
+        c["first"] += 1
+
+    one, two = make(), make()
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        step(make())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            step(two)
+    torch.cuda.synchronize()
+    for x in steps:
+        for c in (one, two):
+            c["kv"].copy_(x)
+        step(one)
+        graph.replay()
+        torch.cuda.synchronize()
+        for k in ("out", "pos", "first", "err"):
+            assert torch.equal(one[k], two[k])
+        assert int(one["err"]) == 0
+    assert torch.equal(one["state"][0], two["state"][0])

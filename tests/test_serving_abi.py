@@ -1,0 +1,110 @@
+"""Host side of the serving step's entry points: every refusal, and the references against plain loops. CPU
+only: each call is refused (or is an empty one) before any CUDA runtime call."""
+import math
+
+import pytest
+import torch
+
+import gated_pooling_gb300 as gp
+from tests import operator_reference as R
+from tests import serving_reference as V
+
+FAKE = 1 << 20  # a 16-byte aligned non-null address; never dereferenced
+INVALID, UNSUPPORTED, WORKSPACE, OK = (gp.CSA_ERR_INVALID_VALUE, gp.CSA_ERR_UNSUPPORTED, gp.CSA_ERR_WORKSPACE, gp.CSA_OK)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return gp.load()
+
+
+# ------------------------------------------------------------------------------------- step
+def step(lib, **over):
+    a = dict(kv=FAKE, score=FAKE, ape=FAKE, cu=FAKE, S=2, ratio=4, coff=2, d=64, capacity=16, first=FAKE, source=FAKE, target=FAKE,
+             states=4, kvs=FAKE, scs=FAKE, out=FAKE, rows=8, base=FAKE, table=FAKE, max_pages=4, page=16, offset=0, pos=FAKE, slots=FAKE,
+             entries=FAKE, err=None)
+    a.update(over)
+    return lib.csa_compressor_step(*a.values(), None)
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(S=-1), INVALID), (dict(ratio=0), INVALID), (dict(d=0), INVALID), (dict(capacity=-1), INVALID), (dict(rows=-1), INVALID),
+    (dict(states=-1), INVALID), (dict(max_pages=-1), INVALID), (dict(page=0), INVALID), (dict(offset=-1), INVALID),
+    (dict(offset=4), INVALID), (dict(coff=0), UNSUPPORTED), (dict(coff=3), UNSUPPORTED), (dict(S=20000), UNSUPPORTED),
+    (dict(ratio=1025), UNSUPPORTED), (dict(ratio=2049, coff=1), UNSUPPORTED), (dict(d=1 << 20), UNSUPPORTED),
+    (dict(capacity=1 << 25), UNSUPPORTED), (dict(rows=1 << 26), UNSUPPORTED), (dict(states=1 << 31), UNSUPPORTED),
+    (dict(states=1 << 62), UNSUPPORTED), (dict(kv=None), INVALID), (dict(score=None), INVALID), (dict(ape=None), INVALID),
+    (dict(cu=None), INVALID), (dict(first=None), INVALID), (dict(source=None), INVALID), (dict(target=None), INVALID),
+    (dict(kvs=None), INVALID), (dict(scs=None), INVALID), (dict(out=None), INVALID), (dict(table=None), INVALID),
+    (dict(kv=FAKE + 1), INVALID), (dict(score=FAKE + 1), INVALID), (dict(ape=FAKE + 2), INVALID), (dict(cu=FAKE + 2), INVALID),
+    (dict(first=FAKE + 2), INVALID), (dict(source=FAKE + 2), INVALID), (dict(target=FAKE + 2), INVALID), (dict(kvs=FAKE + 1), INVALID),
+    (dict(scs=FAKE + 1), INVALID), (dict(out=FAKE + 1), INVALID), (dict(base=FAKE + 2), INVALID), (dict(table=FAKE + 2), INVALID),
+    (dict(pos=FAKE + 2), INVALID), (dict(slots=FAKE + 4), INVALID), (dict(entries=FAKE + 2), INVALID), (dict(err=FAKE + 1), INVALID),
+    (dict(S=0, rows=0), OK), (dict(S=0, pos=None, slots=None), OK),
+])
+def test_step_refusals(lib, over, code):
+    assert step(lib, **over) == code
+
+
+# ----------------------------------------------------------------------------------- append
+def append(lib, **over):
+    a = dict(x=FAKE, dtype=0, rows=4, heads=2, d=64, xr=128, xh=64, w=FAKE, norm=1, eps=1e-6, pos=FAKE, turns=FAKE, rot=64, start=0,
+             layout=0, amp=1.0, slots=FAKE, n=16, fmt=1, data=FAKE, scales=FAKE, err=None)
+    a.update(over)
+    return lib.csa_cache_append(*a.values(), None)
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(rows=-1), INVALID), (dict(heads=0), INVALID), (dict(d=0), INVALID), (dict(norm=2), INVALID), (dict(rot=63), INVALID),
+    (dict(rot=-2), INVALID), (dict(rot=66), INVALID), (dict(start=2), INVALID), (dict(start=-1, rot=2), INVALID),
+    (dict(eps=-1.0), INVALID), (dict(eps=math.nan), INVALID), (dict(eps=math.inf), INVALID), (dict(xr=-1), INVALID),
+    (dict(xh=-1), INVALID), (dict(n=-1), INVALID), (dict(pos=None), INVALID), (dict(turns=None), INVALID), (dict(x=None), INVALID),
+    (dict(slots=None), INVALID), (dict(data=None), INVALID), (dict(scales=None), INVALID), (dict(norm=0), INVALID),
+    (dict(x=FAKE + 1), INVALID), (dict(x=FAKE + 2, dtype=2), INVALID), (dict(w=FAKE + 2), INVALID), (dict(pos=FAKE + 2), INVALID),
+    (dict(turns=FAKE + 4), INVALID), (dict(slots=FAKE + 4), INVALID), (dict(err=FAKE + 2), INVALID),
+    (dict(data=FAKE + 1, fmt=0), INVALID), (dict(d=1056), UNSUPPORTED), (dict(rows=1 << 31, heads=1), UNSUPPORTED),
+    (dict(dtype=3), UNSUPPORTED), (dict(layout=2), UNSUPPORTED), (dict(fmt=3), UNSUPPORTED), (dict(fmt=-1), UNSUPPORTED),
+    (dict(d=72), UNSUPPORTED), (dict(n=1 << 62), UNSUPPORTED),
+    (dict(rows=0), OK), (dict(rows=0, x=None, slots=None, pos=None, turns=None), OK),
+])
+def test_append_refusals(lib, over, code):
+    assert append(lib, **over) == code
+
+
+# ------------------------------------------------------------- the references check themselves
+@pytest.mark.parametrize("ratio,coff", [(1, 1), (1, 2), (3, 1), (4, 2)])
+def test_held_elements_are_those_that_later_windows_read(ratio, coff):
+    """By trying every later block: an element is held when its token is there and a window to come reads it."""
+    d = 2
+    for total in range(0, 5 * ratio):
+        want = {}
+        for b in range(total // ratio, total // ratio + 3):
+            for p in range(max(0, (b - coff + 1) * ratio), (b + 1) * ratio):
+                half = 0 if coff == 1 or p < b * ratio else 1
+                if p < total:
+                    want[p % (ratio * coff), half] = p
+        got = V.held(0, total, ratio, coff, d)
+        for r in range(ratio * coff):
+            for half in range(coff):
+                assert (got[r, half * d:half * d + d] == want.get((r, half), -1)).all()
+
+
+def test_window_entry_of_equal_scores_is_the_mean():
+    kv = torch.arange(16.0).reshape(8, 2).to(torch.bfloat16)
+    zero, ape = torch.zeros(8, 2, dtype=torch.bfloat16), torch.zeros(4, 2)
+    out, bound = V.window_entry(kv, zero, ape, 1, 4, 2, 1)
+    assert abs(float(out[0]) - (0 + 2 + 4 + 6 + 9 + 11 + 13 + 15) / 8) < 1e-12 and float(bound[0]) < 2 * 2.0 ** -8 * 7.5
+
+
+@pytest.mark.parametrize("fmt", [R.E4M3, R.FP4])
+def test_code_check_takes_the_quantiser_and_refuses_a_step_off(fmt):
+    g = torch.Generator().manual_seed(1)
+    x = torch.randn(40, 64, generator=g, dtype=torch.float64)
+    codes, k = R.quantise(x, fmt)
+    V.check_codes(codes, k, fmt, x, torch.zeros_like(x))
+    for c, s in ((codes, k + 1), (codes, k - 1), (codes.clone(), k)):
+        if s is k:
+            mag = 126 if fmt == R.E4M3 else 7
+            c[3, 5] += 2 if (int(c[3, 5]) & mag) < mag - 2 else -2
+        with pytest.raises(AssertionError):
+            V.check_codes(c, s, fmt, x, torch.zeros_like(x))
