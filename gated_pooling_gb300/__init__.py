@@ -37,7 +37,8 @@ EXPORTED = ("csa_status_string", "csa_last_error_string", "csa_compressor_total_
             "csa_compressor_map_blocks", "csa_kpool_total", "csa_kpool_fwd", "csa_rope_table",
             "csa_norm_rope_fwd", "csa_norm_rope_bwd_workspace_bytes", "csa_norm_rope_bwd",
             "csa_cache_write", "csa_cache_read", "csa_cache_attn_workspace_bytes", "csa_cache_attn",
-            "csa_compressor_step", "csa_cache_append")
+            "csa_compressor_step", "csa_cache_append", "csa_cache_attn_prefix_workspace_bytes",
+            "csa_cache_attn_prefix")
 
 
 class CsaError(RuntimeError):
@@ -110,6 +111,11 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.csa_cache_append.restype = ctypes.c_int
     lib.csa_cache_append.argtypes = [vp, i32, i64, i32, i32, i64, i64, vp, i32, f32, vp, vp, i32, i32, i32,
                                      f32, vp, i64, i32, vp, vp, vp, vp]
+    lib.csa_cache_attn_prefix_workspace_bytes.restype = sz
+    lib.csa_cache_attn_prefix_workspace_bytes.argtypes = [i32, i32, i64, i32, i32, i32, i64, i64]
+    lib.csa_cache_attn_prefix.restype = ctypes.c_int
+    lib.csa_cache_attn_prefix.argtypes = [vp, i64, i64, vp, i32, i64, i32, i32, i32, vp, vp, i32, vp, i32, vp, i32, vp,
+                                          vp, i32, i64, i32, vp, vp, i32, f32, vp, vp, i64, i64, vp, vp, sz, vp, vp]
     if path == LIB_PATH:
         _lib = lib
     return lib
@@ -352,3 +358,26 @@ def csa_cache_append(x, dtype: int, rows: int, heads: int, d: int, x_row_stride:
                                    rot_dim, rot_start, layout, amplitude, _ptr(slots), num_slots,
                                    format, _ptr(data), _ptr(scales), _ptr(dev_error),
                                    _stream(stream)), "csa_cache_append")
+
+
+def csa_cache_attn_prefix_workspace_bytes(S: int, G: int, tokens: int, q_heads: int, kv_heads: int, d: int,
+                                          max_entries: int, max_prefix_entries: int) -> int:
+    return int(load().csa_cache_attn_prefix_workspace_bytes(S, G, tokens, q_heads, kv_heads, d, max_entries,
+                                                            max_prefix_entries))
+
+
+def csa_cache_attn_prefix(q, q_row_stride: int, q_head_stride: int, cu_seqlens, S: int, tokens: int,
+                          q_heads: int, kv_heads: int, d: int, data, scales, format: int, prefix_seqs,
+                          G: int, prefix_table, max_prefix_pages: int, prefix_entries, page_table,
+                          max_pages: int, num_pages: int, page_size: int, entries, first, ratio: int,
+                          softmax_scale: float, sink, out, out_row_stride: int, out_head_stride: int,
+                          lse, workspace, workspace_bytes: int, dev_error=None, stream=None) -> None:
+    """New tokens over the entries that a group of sequences shares and each sequence's own."""
+    _check(load().csa_cache_attn_prefix(_ptr(q), q_row_stride, q_head_stride, _ptr(cu_seqlens), S, tokens,
+                                        q_heads, kv_heads, d, _ptr(data), _ptr(scales), format,
+                                        _ptr(prefix_seqs), G, _ptr(prefix_table), max_prefix_pages,
+                                        _ptr(prefix_entries), _ptr(page_table), max_pages, num_pages,
+                                        page_size, _ptr(entries), _ptr(first), ratio, softmax_scale,
+                                        _ptr(sink), _ptr(out), out_row_stride, out_head_stride, _ptr(lse),
+                                        _ptr(workspace), workspace_bytes, _ptr(dev_error),
+                                        _stream(stream)), "csa_cache_attn_prefix")

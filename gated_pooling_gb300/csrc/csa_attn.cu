@@ -54,6 +54,68 @@ __device__ __forceinline__ int64_t plan_scan(int64_t v, int64_t* warps, int64_t&
   return x - v + (warp > 0 ? warps[warp - 1] : 0);
 }
 
+// Where each worker's share of the units' work begins, and the units that several workers share. All threads
+// of the plan's block; `work`: where each unit's work begins, `all` of them together.
+__device__ __forceinline__ void plan_shares(const AttnParams& p, int64_t units, int64_t all, const int64_t* work, int* s_joins) {
+  // the unit and tile that a place in the work stands for, and how many tiles lie before it
+  struct Place {
+    int64_t unit, tile, before;
+  };
+  auto place = [&](int64_t x) {
+    if (x >= all) return Place{units, 0, all - units * p.unit_cost};
+    int64_t l = 0, h = units;  // work[l] <= x < work[h]
+    while (h - l > 1) {
+      const int64_t mid = (l + h) / 2;
+      if (work[mid] <= x) l = mid;
+      else h = mid;
+    }
+    const int64_t tile = x - work[l];
+    if (tile >= work[l + 1] - work[l] - p.unit_cost) return Place{l + 1, 0, work[l + 1] - (l + 1) * p.unit_cost};  // behind the unit's last tile
+    return Place{l, tile, x - l * p.unit_cost};
+  };
+  const AttnShares share(all, p.workers);
+  for (int i = threadIdx.x; i < p.workers; i += kPlanThreads) {
+    const Place a = place(share(i)), b = place(share(i + 1));
+    AttnStart start{};
+    start.left = b.before - a.before;
+    if (start.left > 0) {
+      start.u = p.units[a.unit];
+      start.unit = static_cast<int32_t>(a.unit);
+      start.tile = static_cast<int32_t>(a.tile);
+      if (p.groups > 0) {  // behind prefixes: the span that tile lies in
+        int l = start.u.span, h = l + start.u.spans;
+        while (h - l > 1) {
+          const int mid = (l + h) / 2;
+          if (p.spans[mid].tile <= start.tile) l = mid;
+          else h = mid;
+        }
+        start.u.span = l;
+      }
+      // a unit that begins in this share and goes on in later ones
+      if (b.tile > 0 && (b.unit > a.unit || a.tile == 0)) {
+        const int64_t end = work[b.unit + 1] - p.unit_cost;
+        AttnJoin join{};
+        join.u = p.units[b.unit];
+        join.worker = i;
+        int last = max(i + 1, share.near(end - 1));  // the worker whose share the unit's last tile lies in
+        while (share(last + 1) < end) ++last;
+        while (last > i + 1 && share(last) >= end) --last;
+        join.pieces = last - i + 1;
+        // (in any order: each is joined by itself; those of many pieces from the list's other end)
+        const bool few = join.pieces <= kFewPieces;
+        const int at = atomicAdd(&s_joins[few ? 0 : 1], 1);
+        p.joins[few ? at : p.workers - 1 - at] = join;
+      }
+    }
+    p.starts[i] = start;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    p.head->few = s_joins[0];
+    p.head->many = s_joins[1];
+  }
+}
+
 // One block: checks the call's lengths, publishes the verdict for the kernels behind it, and
 // (units wanted) lists the units, where each worker's share begins, and the units that several
 // workers share.
@@ -118,61 +180,198 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnParams p) {
     if (few) s_work[units] = all;
   }
   __syncthreads();
-  const int64_t* work = few ? s_work : p.unit_first;
-  // the unit and tile that a place in the work stands for, and how many tiles lie before it
-  struct Place {
-    int64_t unit, tile, before;
-  };
-  auto place = [&](int64_t x) {
-    if (x >= all) return Place{units, 0, all - units * p.unit_cost};
-    int64_t l = 0, h = units;  // work[l] <= x < work[h]
-    while (h - l > 1) {
-      const int64_t mid = (l + h) / 2;
-      if (work[mid] <= x) l = mid;
-      else h = mid;
-    }
-    const int64_t tile = x - work[l];
-    if (tile >= work[l + 1] - work[l] - p.unit_cost) return Place{l + 1, 0, work[l + 1] - (l + 1) * p.unit_cost};  // behind the unit's last tile
-    return Place{l, tile, x - l * p.unit_cost};
-  };
-  const AttnShares share(all, p.workers);
-  for (int i = threadIdx.x; i < p.workers; i += kPlanThreads) {
-    const Place a = place(share(i)), b = place(share(i + 1));
-    AttnStart start{};
-    start.left = b.before - a.before;
-    if (start.left > 0) {
-      start.u = p.units[a.unit];
-      start.unit = static_cast<int32_t>(a.unit);
-      start.tile = static_cast<int32_t>(a.tile);
-      // a unit that begins in this share and goes on in later ones
-      if (b.tile > 0 && (b.unit > a.unit || a.tile == 0)) {
-        const int64_t end = work[b.unit + 1] - p.unit_cost;
-        AttnJoin join{};
-        join.u = p.units[b.unit];
-        join.worker = i;
-        int last = max(i + 1, share.near(end - 1));  // the worker whose share the unit's last tile lies in
-        while (share(last + 1) < end) ++last;
-        while (last > i + 1 && share(last) >= end) --last;
-        join.pieces = last - i + 1;
-        // (in any order: each is joined by itself; those of many pieces from the list's other end)
-        const bool few = join.pieces <= kFewPieces;
-        const int at = atomicAdd(&s_joins[few ? 0 : 1], 1);
-        p.joins[few ? at : p.workers - 1 - at] = join;
+  plan_shares(p, units, all, few ? s_work : p.unit_first, s_joins);
+}
+
+// The same behind shared prefixes: units of a group's rows, whatever sequences they are of, and their spans.
+// Sequences' numbers are looked up again and again: they are held in shared memory up to kPlanCached of them.
+constexpr int kPlanCached = 4096;
+__global__ void __launch_bounds__(kPlanThreads) attn_prefix_plan_kernel(AttnParams p) {
+  extern __shared__ int s_mem[];
+  __shared__ int64_t s_warps[32];
+  __shared__ int64_t s_work[kPlanUnits + 1];
+  __shared__ int s_joins[2];
+  int* s_first = s_mem;  // [groups + 1] first row block of each group
+  const bool cached = p.S <= kPlanCached;
+  const int32_t *cu = p.cu, *own = p.entries, *first = p.first;
+  if (threadIdx.x < 2) s_joins[threadIdx.x] = 0;
+  pdl_wait();
+  int bad = 0;
+  {
+    int* s_cu = s_mem + p.groups + 1;
+    int* s_own = s_cu + p.S + 1;
+    int* s_pos = s_own + p.S;
+    for (int s = threadIdx.x; s < p.S; s += kPlanThreads) {
+      const int32_t a = __ldg(p.cu + s), b = __ldg(p.cu + s + 1), n = __ldg(p.entries + s);
+      if (b < a || a < 0 || b > p.tokens) bad |= 1;
+      if (n < 0 || n > p.max_entries) bad |= 2;
+      if (cached) {
+        s_cu[s] = a;
+        if (s == p.S - 1) s_cu[s + 1] = b;
+        s_own[s] = n;
+        s_pos[s] = p.first != nullptr ? __ldg(p.first + s) : 0;
       }
     }
-    p.starts[i] = start;
+    if (cached) {
+      cu = s_cu;
+      own = s_own;
+      first = s_pos;
+    }
+  }
+  for (int g = threadIdx.x; g < p.groups; g += kPlanThreads) {
+    const int32_t a = __ldg(p.prefix_seqs + g), b = __ldg(p.prefix_seqs + g + 1), n = __ldg(p.prefix_entries + g);
+    if (a < 0 || b < a || b > p.S || (g == 0 && a != 0) || (g == p.groups - 1 && b != p.S) || n < 0 || n > p.max_prefix) bad |= 4;
+  }
+  int code = 0;
+  if (__syncthreads_or(bad & 1)) code = CSA_DEVERR_CU_SEQLENS;
+  else if (__syncthreads_or(bad & 2)) code = CSA_DEVERR_ENTRIES;
+  else if (__syncthreads_or(bad & 4)) code = CSA_DEVERR_PREFIX;
+  if (threadIdx.x == 0) {
+    p.head->status = code;
+    if (code != 0 && p.dev_error != nullptr) *p.dev_error = code;
+  }
+  if (code != 0 || p.units == nullptr) return;
+  auto group_rows = [&](int g) { return (cu[p.prefix_seqs[g + 1]] - cu[p.prefix_seqs[g]]) * p.group; };
+  const int per = (p.groups + kPlanThreads - 1) / kPlanThreads;
+  const int lo = min(p.groups, static_cast<int>(threadIdx.x) * per), hi = min(p.groups, lo + per);
+  int64_t mine = 0, blocks = 0;
+  for (int g = lo; g < hi; ++g) mine += (group_rows(g) + kAttnRows - 1) / kAttnRows;
+  int64_t at = plan_scan(mine, s_warps, blocks);
+  for (int g = lo; g < hi; ++g) {
+    s_first[g] = static_cast<int>(at);
+    at += (group_rows(g) + kAttnRows - 1) / kAttnRows;
+  }
+  if (threadIdx.x == 0) s_first[p.groups] = static_cast<int>(blocks);
+  __syncthreads();
+  const int64_t units = blocks * p.kv_heads;
+  const bool few = units <= kPlanUnits;
+  int64_t all = 0, all_spans = 0;
+  for (int64_t u0 = 0; u0 < units; u0 += kPlanThreads) {
+    const int64_t i = u0 + threadIdx.x;
+    AttnUnit u{};
+    int seq0 = 0, seq1 = -1, prefix_seen = 0, prefix_all = INT_MAX, row0 = 0, before = 0, t0 = 0, t1 = 0;
+    // own entries of the unit's sequence s: what some row sees, and what every row of it sees
+    auto sees = [&](int s, int& some, int& every) {
+      const int a = cu[s], b = cu[s + 1];
+      const int64_t pos = first != nullptr ? first[s] : 0;
+      every = visible(pos + (max(a, t0) - a), p.ratio, before + own[s]);
+      some = visible(pos + (min(b - 1, t1) - a), p.ratio, before + own[s]);
+    };
+    if (i < units) {
+      const int b = static_cast<int>(units < INT_MAX ? static_cast<int>(i) / p.kv_heads : i / p.kv_heads);
+      int g = 0, h = p.groups;  // s_first[g] <= b < s_first[h]
+      while (h - g > 1) {
+        const int mid = (g + h) / 2;
+        if (s_first[mid] <= b) g = mid;
+        else h = mid;
+      }
+      const int from = p.prefix_seqs[g], to = p.prefix_seqs[g + 1];
+      u.s = g;
+      u.kvh = static_cast<int>(i - static_cast<int64_t>(b) * p.kv_heads);
+      u.block = b - s_first[g];
+      u.token = cu[from];
+      u.rows = group_rows(g);
+      row0 = u.block * kAttnRows;
+      t0 = u.token + row0 / p.group;
+      t1 = u.token + (min(row0 + kAttnRows, u.rows) - 1) / p.group;
+      auto sequence = [&](int t) {  // the last one that begins by t, of the group: it holds t
+        int l = from, r = to;
+        while (r - l > 1) {
+          const int mid = (l + r) / 2;
+          if (cu[mid] <= t) l = mid;
+          else r = mid;
+        }
+        return l;
+      };
+      seq0 = sequence(t0);
+      seq1 = sequence(t1);
+      before = p.prefix_entries[g];
+      for (int s = seq0; s <= seq1; ++s) {
+        if (cu[s + 1] == cu[s]) continue;
+        int some, every;
+        sees(s, some, every);
+        prefix_seen = max(prefix_seen, min(some, before));
+        prefix_all = min(prefix_all, min(every, before));
+        u.tiles += tiles_of(some - before);
+        u.spans += some > before ? 1 : 0;
+      }
+      // (a unit that sees nothing has a tile of nothing)
+      if (prefix_seen > 0 || u.tiles == 0) {
+        u.tiles += max(1, tiles_of(prefix_seen));
+        u.spans += 1;
+      }
+    }
+    int64_t sum = 0;
+    const int64_t begin = all + plan_scan(i < units ? u.tiles + p.unit_cost : 0, s_warps, sum);
+    all += sum;
+    const int64_t span = all_spans + plan_scan(u.spans, s_warps, sum);
+    all_spans += sum;
+    if (i < units) {
+      u.span = static_cast<int32_t>(span);
+      p.units[i] = u;
+      p.unit_first[i] = begin;
+      if (few) s_work[i] = begin;
+      AttnSpan* out = p.spans + span;
+      int tile = 0;
+      auto put = [&](AttnSpan v) {
+        v.unit = static_cast<int32_t>(i);
+        v.tile = tile;
+        v.tiles = max(1, tiles_of(v.seen));
+        tile += v.tiles;
+        *out++ = v;
+      };
+      int own_spans = 0;
+      for (int s = seq0; s <= seq1; ++s) {
+        if (cu[s + 1] == cu[s]) continue;
+        int some, every;
+        sees(s, some, every);
+        own_spans += some > before ? 1 : 0;
+      }
+      if (own_spans < u.spans) {
+        AttnSpan v{};
+        v.table = p.prefix_table + static_cast<int64_t>(u.s) * p.max_prefix_pages;
+        v.seen = prefix_seen;
+        v.seen_all = prefix_all;
+        v.row1 = kAttnRows;
+        v.token = seq0;
+        v.first = seq1;
+        v.n = before;
+        v.packed = (u.s * p.kv_heads + u.kvh) * p.prefix_rows;
+        put(v);
+      }
+      for (int s = seq0; s <= seq1; ++s) {
+        if (cu[s + 1] == cu[s]) continue;
+        int some, every;
+        sees(s, some, every);
+        if (some <= before) continue;
+        AttnSpan v{};
+        v.table = p.table + static_cast<int64_t>(s) * p.max_pages;
+        v.seen = some - before;
+        v.row0 = max(0, (cu[s] - u.token) * p.group - row0);
+        v.row1 = s == seq1 ? kAttnRows : min(kAttnRows, (cu[s + 1] - u.token) * p.group - row0);
+        v.seen_all = v.row0 == 0 && v.row1 == kAttnRows ? max(0, every - before) : 0;
+        v.token = cu[s];
+        v.first = first != nullptr ? first[s] : 0;
+        v.n = before + own[s];
+        v.before = before;
+        v.packed = p.groups * p.kv_heads * p.prefix_rows + (s * p.kv_heads + u.kvh) * p.packed_rows;
+        v.own = 1;
+        put(v);
+      }
+    }
+  }
+  if (threadIdx.x == 0) {
+    p.unit_first[units] = all;
+    if (few) s_work[units] = all;
   }
   __syncthreads();
-  if (threadIdx.x == 0) {
-    p.head->few = s_joins[0];
-    p.head->many = s_joins[1];
-  }
+  plan_shares(p, units, all, few ? s_work : p.unit_first, s_joins);
 }
 
 // Scalar kernel, any d and alignment: a warp per new token and query head, a lane the columns
 // lane, lane + 32, ...; one pass over the entries with the running maximum and sum.
 constexpr int kScalarThreads = 128;
-template <int FORMAT, int NL>
+template <int FORMAT, int NL, bool PREFIX>
 __global__ void __launch_bounds__(kScalarThreads) attn_scalar_kernel(AttnParams p) {
   using B = Element<CSA_DTYPE_BF16>;
   const int lane = threadIdx.x & 31;
@@ -185,7 +384,21 @@ __global__ void __launch_bounds__(kScalarThreads) attn_scalar_kernel(AttnParams 
   const int s = sequence_of(p.cu, p.S, t);
   if (s < 0) return;
   const int64_t pos = static_cast<int64_t>(p.first != nullptr ? p.first[s] : 0) + (t - p.cu[s]);
-  const int n = visible(pos, p.ratio, p.entries[s]);
+  // behind a prefix its entries come first
+  int before = 0;
+  const int32_t* table = p.table + static_cast<int64_t>(s) * p.max_pages;
+  const int32_t* prefix = nullptr;
+  if constexpr (PREFIX) {
+    int lo = 0, hi = p.groups;  // the last group that begins by s: it holds s
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (p.prefix_seqs[mid] <= s) lo = mid;
+      else hi = mid;
+    }
+    before = p.prefix_entries[lo];
+    prefix = p.prefix_table + static_cast<int64_t>(lo) * p.max_prefix_pages;
+  }
+  const int n = visible(pos, p.ratio, before + p.entries[s]);
   const uint16_t* q = p.q + t * p.q_row + h * p.q_head;
   float qv[NL], acc[NL];
 #pragma unroll
@@ -197,12 +410,14 @@ __global__ void __launch_bounds__(kScalarThreads) attn_scalar_kernel(AttnParams 
   float m = -INFINITY, z = 0.f;
   const int kvh = h / p.group;
   for (int e = 0; e < n; ++e) {
-    const int page = p.table[static_cast<int64_t>(s) * p.max_pages + e / p.page_size];
+    const bool own = !PREFIX || e >= before;
+    const int at = own ? e - before : e;
+    const int page = own ? table[at / p.page_size] : prefix[at / p.page_size];
     if (page < 0 || page >= p.num_pages) {
       if (p.dev_error != nullptr) *p.dev_error = CSA_DEVERR_PAGE;
       continue;
     }
-    const int64_t entry = (static_cast<int64_t>(page) * p.page_size + e % p.page_size) * p.kv_heads + kvh;
+    const int64_t entry = (static_cast<int64_t>(page) * p.page_size + at % p.page_size) * p.kv_heads + kvh;
     float k[NL], x = 0.f;
 #pragma unroll
     for (int j = 0; j < NL; ++j) {
@@ -266,12 +481,13 @@ auto by_format(int format, F f) {
          : format == CSA_CACHE_E4M3 ? f(std::integral_constant<int, CSA_CACHE_E4M3>{})
                                     : f(std::integral_constant<int, CSA_CACHE_E2M1>{});
 }
+template <bool PREFIX>
 const void* scalar_kernel_for(int format, int d) {
   auto pick = [&](auto f) -> const void* {
     constexpr int F = decltype(f)::value;
-    return d <= 128   ? reinterpret_cast<const void*>(attn_scalar_kernel<F, 4>)
-           : d <= 512 ? reinterpret_cast<const void*>(attn_scalar_kernel<F, 16>)
-                      : reinterpret_cast<const void*>(attn_scalar_kernel<F, 32>);
+    return d <= 128   ? reinterpret_cast<const void*>(attn_scalar_kernel<F, 4, PREFIX>)
+           : d <= 512 ? reinterpret_cast<const void*>(attn_scalar_kernel<F, 16, PREFIX>)
+                      : reinterpret_cast<const void*>(attn_scalar_kernel<F, 32, PREFIX>);
   };
   return by_format(format, pick);
 }
@@ -293,11 +509,9 @@ constexpr int kTileMaxDim = 512;
 
 int tile_chunks(int d) { return d <= 128 ? 2 : d <= 256 ? 4 : 8; }
 
-template <typename F>
-auto by_chunks(int chunks, F f) {
-  return chunks == 2   ? f(std::integral_constant<int, 2>{})
-         : chunks == 4 ? f(std::integral_constant<int, 4>{})
-                       : f(std::integral_constant<int, 8>{});
+// Rows of all packed entries.
+int64_t packed_rows(const AttnParams& p) {
+  return (static_cast<int64_t>(p.groups) * p.prefix_rows + static_cast<int64_t>(p.S) * p.packed_rows) * p.kv_heads;
 }
 
 // The workspace: the plan, the pieces, and (chunks) the packed entries. base may be null (sizes only).
@@ -313,17 +527,17 @@ size_t lay_out(AttnParams& p, int sms, bool chunks, unsigned char* base) {
   p.joins = reinterpret_cast<AttnJoin*>(take(sizeof(AttnJoin) * sms));
   p.units = reinterpret_cast<AttnUnit*>(take(sizeof(AttnUnit) * p.max_units));
   p.unit_first = reinterpret_cast<int64_t*>(take(sizeof(int64_t) * (p.max_units + 1)));
+  if (p.groups > 0) p.spans = reinterpret_cast<AttnSpan*>(take(sizeof(AttnSpan) * p.max_spans));
   const size_t pieces = 2 * static_cast<size_t>(sms), dpad = tile_chunks(p.d) * 64;
   p.part_ml = reinterpret_cast<float*>(take(pieces * 2 * kAttnRows * sizeof(float)));
   p.part_o = reinterpret_cast<float*>(take(pieces * kAttnRows * dpad * sizeof(float)));
-  if (chunks)
-    p.packed = reinterpret_cast<uint16_t*>(take(static_cast<size_t>(p.S) * p.kv_heads * p.packed_rows * dpad * 2));
+  if (chunks) p.packed = reinterpret_cast<uint16_t*>(take(static_cast<size_t>(packed_rows(p)) * dpad * 2));
   return at;
 }
 
 // Sizes that the workspace depends on; d beyond the tile kernel's needs the status alone.
 cudaError_t plan_sizes(AttnParams& p, int* sms, int32_t S, int64_t tokens, int32_t q_heads, int32_t kv_heads,
-                       int32_t d, int64_t max_entries) {
+                       int32_t d, int64_t max_entries, int32_t groups, int64_t max_prefix) {
   int dev = 0;
   cudaError_t e = note(cudaGetDevice(&dev));
   if (e != cudaSuccess || (e = device_sms(dev, sms)) != cudaSuccess) return e;
@@ -335,8 +549,14 @@ cudaError_t plan_sizes(AttnParams& p, int* sms, int32_t S, int64_t tokens, int32
   p.d = d;
   p.workers = *sms;
   p.max_entries = max_entries;
-  p.max_units = ((tokens * p.group + kAttnRows - 1) / kAttnRows + S) * kv_heads;
+  p.groups = groups;
+  p.max_prefix = max_prefix;
+  const int64_t blocks = (tokens * p.group + kAttnRows - 1) / kAttnRows + (groups > 0 ? groups : S);
+  p.max_units = blocks * kv_heads;
+  p.max_spans = groups > 0 ? (2 * blocks + S) * kv_heads : 0;  // a prefix a unit, and a unit more or less for a sequence
   p.packed_rows = static_cast<int>((max_entries + kAttnEntries - 1) / kAttnEntries * kAttnEntries);
+  p.prefix_rows = static_cast<int>((max_prefix + kAttnEntries - 1) / kAttnEntries * kAttnEntries);
+  if (groups > 0 && p.prefix_rows == 0) p.prefix_rows = kAttnEntries;  // (a tile of nothing)
   return cudaSuccess;
 }
 
@@ -347,53 +567,82 @@ cudaError_t plan_sizes(AttnParams& p, int* sms, int32_t S, int64_t tokens, int32
 constexpr int64_t kChunkRows = 256, kChunkRowsWide = 384;
 constexpr int64_t kMaxPacked = int64_t{4} << 30;
 bool chunked(const AttnParams& p) {
-  if (p.d > kTileMaxDim || p.S < 1 || p.tokens * p.group < kChunkRows * p.S) return false;
-  const int64_t rows = static_cast<int64_t>(p.S) * p.kv_heads * p.packed_rows;
-  return rows > 0 && rows < INT_MAX && rows * tile_chunks(p.d) * 128 <= kMaxPacked && p.S < 65536 && p.kv_heads < 65536;
+  if (p.d > kTileMaxDim || p.S < 1) return false;
+  if (p.groups > 0) {
+    // behind prefixes: four units a prefix, and the own entries, which fewer units read, no more than
+    // the prefixes
+    if (p.tokens * p.group < kChunkRows * p.groups || static_cast<int64_t>(p.S) * p.packed_rows > static_cast<int64_t>(p.groups) * p.prefix_rows)
+      return false;
+  } else if (p.tokens * p.group < kChunkRows * p.S) {
+    return false;
+  }
+  const int64_t rows = packed_rows(p);
+  return rows > 0 && rows < INT_MAX && rows * tile_chunks(p.d) * 128 <= kMaxPacked && p.S + p.groups < 65536 && p.kv_heads < 65536;
 }
 
-}  // namespace
-}  // namespace csa
+// A call of either entry point; groups is 0 without prefixes.
+struct AttnCall {
+  const void* q;
+  int64_t q_row_stride, q_head_stride;
+  const int32_t* cu_seqlens;
+  int32_t S;
+  int64_t tokens;
+  int32_t q_heads, kv_heads, d;
+  const void* data;
+  const uint8_t* scales;
+  int32_t format;
+  const int32_t* prefix_seqs;
+  int32_t groups;
+  const int32_t* prefix_table;
+  int32_t max_prefix_pages;
+  const int32_t* prefix_entries;
+  const int32_t* page_table;
+  int32_t max_pages;
+  int64_t num_pages;
+  int32_t page_size;
+  const int32_t *entries, *first;
+  int32_t ratio;
+  float softmax_scale;
+  const float* sink;
+  void* out;
+  int64_t out_row_stride, out_head_stride;
+  float* lse;
+  void* workspace;
+  size_t workspace_bytes;
+  int32_t* dev_error;
+};
 
-using namespace csa;
-
-extern "C" size_t csa_cache_attn_workspace_bytes(int32_t S, int64_t tokens, int32_t q_heads,
-                                                 int32_t kv_heads, int32_t d, int64_t max_entries) {
-  if (check_attn_sizes(S, tokens, q_heads, kv_heads, d, max_entries) != CSA_OK) return 0;
-  if (d > kTileMaxDim) return kStatusBytes;
-  AttnParams p{};
-  int sms = 0;
-  if (plan_sizes(p, &sms, S, tokens, q_heads, kv_heads, d, max_entries) != cudaSuccess) return 0;
-  return lay_out(p, sms, chunked(p), nullptr);
-}
-
-extern "C" csa_status_t csa_cache_attn(
-    const void* q, int64_t q_row_stride, int64_t q_head_stride, const int32_t* cu_seqlens, int32_t S,
-    int64_t tokens, int32_t q_heads, int32_t kv_heads, int32_t d, const void* data,
-    const uint8_t* scales, int32_t format, const int32_t* page_table, int32_t max_pages,
-    int64_t num_pages, int32_t page_size, const int32_t* entries, const int32_t* first,
-    int32_t ratio, float softmax_scale, const float* sink, void* out, int64_t out_row_stride,
-    int64_t out_head_stride, float* lse, void* workspace, size_t workspace_bytes,
-    int32_t* dev_error, csa_stream_t stream) {
-  if (max_pages < 0 || page_size < 1 || num_pages < 0 || ratio < 0 || q_row_stride < 0 ||
-      q_head_stride < 0 || out_row_stride < 0 || out_head_stride < 0 || !std::isfinite(softmax_scale))
+csa_status_t run_attn(const AttnCall& c, csa_stream_t stream) {
+  const int32_t S = c.S, q_heads = c.q_heads, kv_heads = c.kv_heads, d = c.d, format = c.format, groups = c.groups;
+  const int32_t max_pages = c.max_pages, page_size = c.page_size;
+  const int64_t tokens = c.tokens, num_pages = c.num_pages;
+  const int64_t q_row_stride = c.q_row_stride, q_head_stride = c.q_head_stride;
+  const int64_t out_row_stride = c.out_row_stride, out_head_stride = c.out_head_stride;
+  const void *q = c.q, *data = c.data;
+  void *out = c.out, *workspace = c.workspace;
+  const uint8_t* scales = c.scales;
+  const size_t workspace_bytes = c.workspace_bytes;
+  if (max_pages < 0 || page_size < 1 || num_pages < 0 || c.ratio < 0 || q_row_stride < 0 ||
+      q_head_stride < 0 || out_row_stride < 0 || out_head_stride < 0 || !std::isfinite(c.softmax_scale))
     return CSA_ERR_INVALID_VALUE;
   const int64_t max_entries = static_cast<int64_t>(max_pages) * page_size;
+  const int64_t max_prefix = static_cast<int64_t>(c.max_prefix_pages) * page_size;
   const csa_status_t st = check_attn_sizes(S, tokens, q_heads, kv_heads, d, max_entries);
   if (st != CSA_OK) return st;
+  if (groups > CSA_MAX_SEGMENTS || max_prefix > INT_MAX || max_entries + max_prefix > INT_MAX) return CSA_ERR_UNSUPPORTED;
   if (format < CSA_CACHE_BF16 || format > CSA_CACHE_E2M1) return CSA_ERR_UNSUPPORTED;
   if (format != CSA_CACHE_BF16 && d % CSA_CACHE_GROUP != 0) return CSA_ERR_UNSUPPORTED;
   if (num_pages > INT64_MAX / 64 / page_size / (static_cast<int64_t>(kv_heads) * d))
     return CSA_ERR_UNSUPPORTED;
-  if (cu_seqlens == nullptr || (S > 0 && entries == nullptr)) return CSA_ERR_INVALID_VALUE;
+  if (c.cu_seqlens == nullptr || (S > 0 && c.entries == nullptr)) return CSA_ERR_INVALID_VALUE;
   if (tokens > 0 && (q == nullptr || out == nullptr || !separate(tokens, q_heads, d, out_row_stride, out_head_stride)))
     return CSA_ERR_INVALID_VALUE;
-  if (S > 0 && max_pages > 0 && page_table == nullptr) return CSA_ERR_INVALID_VALUE;
+  if (S > 0 && max_pages > 0 && c.page_table == nullptr) return CSA_ERR_INVALID_VALUE;
   if (num_pages > 0 && (data == nullptr || (format != CSA_CACHE_BF16 && scales == nullptr)))
     return CSA_ERR_INVALID_VALUE;
-  if (!is_aligned(q, 2) || !is_aligned(out, 2) || !is_aligned(cu_seqlens, 4) ||
-      !is_aligned(page_table, 4) || !is_aligned(entries, 4) || !is_aligned(first, 4) ||
-      !is_aligned(sink, 4) || !is_aligned(lse, 4) || !is_aligned(dev_error, 4) ||
+  if (!is_aligned(q, 2) || !is_aligned(out, 2) || !is_aligned(c.cu_seqlens, 4) ||
+      !is_aligned(c.page_table, 4) || !is_aligned(c.entries, 4) || !is_aligned(c.first, 4) ||
+      !is_aligned(c.sink, 4) || !is_aligned(c.lse, 4) || !is_aligned(c.dev_error, 4) ||
       !is_aligned(workspace, 16) || (format == CSA_CACHE_BF16 && !is_aligned(data, 2)))
     return CSA_ERR_INVALID_VALUE;
   if (S == 0 || tokens == 0) return CSA_OK;
@@ -401,11 +650,15 @@ extern "C" csa_status_t csa_cache_attn(
 
   AttnParams p{};
   int sms = 0;
-  if (plan_sizes(p, &sms, S, tokens, q_heads, kv_heads, d, max_entries) != cudaSuccess) return CSA_ERR_CUDA;
+  if (plan_sizes(p, &sms, S, tokens, q_heads, kv_heads, d, max_entries, groups, max_prefix) != cudaSuccess) return CSA_ERR_CUDA;
   // a call's pointers and strides decide between the kernels, its workspace serves either
   const bool tile = d <= kTileMaxDim && d % 8 == 0 && q_row_stride % 8 == 0 && q_head_stride % 8 == 0 &&
                     out_row_stride % 8 == 0 && out_head_stride % 8 == 0 && is_aligned(q, 16) &&
                     is_aligned(out, 16) && is_aligned(data, 16);
+  p.prefix_seqs = c.prefix_seqs;
+  p.prefix_table = c.prefix_table;
+  p.max_prefix_pages = c.max_prefix_pages;
+  p.prefix_entries = c.prefix_entries;
   if (d <= kTileMaxDim) {
     if (workspace_bytes < lay_out(p, sms, chunked(p), nullptr)) return CSA_ERR_WORKSPACE;
     lay_out(p, sms, chunked(p), static_cast<unsigned char*>(workspace));
@@ -425,7 +678,7 @@ extern "C" csa_status_t csa_cache_attn(
   // 80.4 instead of 77.8 at 512.
   p.box_rows = 1;
   while (p.box_rows < kAttnEntries && page_size % (2 * p.box_rows) == 0) p.box_rows *= 2;
-  const int64_t most_tiles = p.max_units * ((max_entries + kAttnEntries - 1) / kAttnEntries);
+  const int64_t most_tiles = p.max_units * ((max_entries + max_prefix + kAttnEntries - 1) / kAttnEntries);
   const bool copies = format == CSA_CACHE_BF16 && p.box_rows >= 8 && num_pages > 0 &&
                       num_pages <= INT_MAX / page_size && (nc < 8 || most_tiles <= p.workers);
   // Packing first. Up to d = 256 a tile's time is the softmax's, so packing entries that can be copied
@@ -437,7 +690,7 @@ extern "C" csa_status_t csa_cache_attn(
   // 909 and 1382.
   const bool wide = format != CSA_CACHE_BF16 && d > 128;
   const bool chunks = tile && chunked(p) && !(copies && nc < 8) &&
-                      tokens * p.group >= (wide ? kChunkRowsWide : kChunkRows) * S;
+                      tokens * p.group >= (wide ? kChunkRowsWide : kChunkRows) * (groups > 0 ? groups : S);
   // A unit's own cost (q in, output out, the pipeline's start) in tiles, by which shares are evened
   // out, measured best of 1 to 5 or 6. Packed: three chunks of 1024 tokens x 64 heads of 512 910 us (at 3
   // 945, at 5 987), of 256 450 (at 1 513, at 5 468); 48 of 64 tokens x 8 heads of 128 100 (at 1
@@ -449,16 +702,16 @@ extern "C" csa_status_t csa_cache_attn(
     p.unit_cost = nc == 8 ? 1 : nc == 4 ? 3 : 5;
   }
   p.q = static_cast<const uint16_t*>(q);
-  p.cu = cu_seqlens;
+  p.cu = c.cu_seqlens;
   p.data = static_cast<const uint8_t*>(data);
   p.scales = scales;
-  p.table = page_table;
-  p.entries = entries;
-  p.first = first;
-  p.sink = sink;
+  p.table = c.page_table;
+  p.entries = c.entries;
+  p.first = c.first;
+  p.sink = c.sink;
   p.out = static_cast<uint16_t*>(out);
-  p.lse = lse;
-  p.dev_error = dev_error;
+  p.lse = c.lse;
+  p.dev_error = c.dev_error;
   p.q_row = q_row_stride;
   p.q_head = q_head_stride;
   p.out_row = out_row_stride;
@@ -466,16 +719,17 @@ extern "C" csa_status_t csa_cache_attn(
   p.num_pages = num_pages;
   p.max_pages = max_pages;
   p.page_size = page_size;
-  p.ratio = ratio;
-  p.scale = softmax_scale;
+  p.ratio = c.ratio;
+  p.scale = c.softmax_scale;
   p.wait_cycles = hooked_wait_cycles();
   p.withhold_tile = hooked_withhold();
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   void* args[] = {&p};
   int dev = 0, bps = 0;
   if (note(cudaGetDevice(&dev)) != cudaSuccess) return CSA_ERR_CUDA;
-  const size_t plan_smem = sizeof(int) * (static_cast<size_t>(S) + 1);
-  const void* plan = reinterpret_cast<const void*>(attn_plan_kernel);
+  const size_t plan_smem = sizeof(int) * (groups > 0 ? static_cast<size_t>(groups) + 1 + (S <= kPlanCached ? 3 * static_cast<size_t>(S) + 1 : 0)
+                                                     : static_cast<size_t>(S) + 1);
+  const void* plan = groups > 0 ? reinterpret_cast<const void*>(attn_prefix_plan_kernel) : reinterpret_cast<const void*>(attn_plan_kernel);
   if (blocks_per_sm(dev, plan, kPlanThreads, plan_smem, &bps) != cudaSuccess) return CSA_ERR_CUDA;
   if (launch_pdl(plan, dim3(1), dim3(kPlanThreads), plan_smem, cs, args) != cudaSuccess) return CSA_ERR_CUDA;
   if (tile) {
@@ -484,7 +738,7 @@ extern "C" csa_status_t csa_cache_attn(
     if (chunks) {
       source = kFromPacked;
       const uint64_t dims[2] = {static_cast<uint64_t>(nc) * 64,
-                                static_cast<uint64_t>(S) * kv_heads * static_cast<uint64_t>(p.packed_rows)};
+                                static_cast<uint64_t>(packed_rows(p))};
       const uint64_t strides[1] = {static_cast<uint64_t>(nc) * 128};
       const uint32_t box[2] = {64, kAttnEntries};
       if (!encode_boxes(&map, p.packed, 2, dims, strides, box)) return CSA_ERR_CUDA;
@@ -496,39 +750,19 @@ extern "C" csa_status_t csa_cache_attn(
       if (!encode_boxes(&map, data, 3, dims, strides, box)) return CSA_ERR_CUDA;
       source = kFromBoxes;
     }
-    size_t smem = 0;
-    int threads = 0;
-    const void *k = nullptr, *join = nullptr, *pack = nullptr;
-    by_chunks(nc, [&](auto c) {
-      constexpr int NC = decltype(c)::value;
-      smem = TileShape<NC>::kSmemBytes;
-      auto use = [&](auto src) {
-        constexpr int SRC = decltype(src)::value;
-        k = reinterpret_cast<const void*>(attn_tile_kernel<NC, SRC>);
-        threads = TileCta<SRC>::kThreads;
-        join = reinterpret_cast<const void*>(attn_join_kernel<NC>);
-        return 0;
-      };
-      if (source == kFromPacked) {
-        use(std::integral_constant<int, kFromPacked>{});
-        pack = by_format(format, [](auto f) {
-          return reinterpret_cast<const void*>(attn_pack_kernel<NC, decltype(f)::value>);
-        });
-      } else if (source == kFromBoxes) {
-        use(std::integral_constant<int, kFromBoxes>{});
-      } else {
-        by_format(format, use);
-      }
-      return 0;
-    });
+    const TileKernels kernels = groups > 0 ? prefix_tile_kernels(nc, source, format) : tile_kernels<false>(nc, source, format);
+    const void *k = kernels.tile, *join = kernels.join, *pack = kernels.pack;
+    const size_t smem = kernels.smem;
+    const int threads = kernels.threads;
     if (blocks_per_sm(dev, k, threads, smem, &bps) != cudaSuccess) return CSA_ERR_CUDA;
     if (bps < 1) return CSA_ERR_UNSUPPORTED;
     if (chunks) {
       // a few blocks an SM, which go on to their sequence's next entries: the table's capacity may
       // be far above what the sequences hold
-      const int64_t heads = static_cast<int64_t>(S) * kv_heads, most = p.packed_rows / kPackRows;
+      const int64_t heads = static_cast<int64_t>(S + groups) * kv_heads;
+      const int64_t most = (groups > 0 && p.prefix_rows > p.packed_rows ? p.prefix_rows : p.packed_rows) / kPackRows;
       const int64_t want = (16 * static_cast<int64_t>(sms) + heads - 1) / heads;
-      if (launch_pdl(pack, dim3(static_cast<unsigned>(want < most ? want : most), S, kv_heads), dim3(kPackThreads), 0,
+      if (launch_pdl(pack, dim3(static_cast<unsigned>(want < most ? want : most), S + groups, kv_heads), dim3(kPackThreads), 0,
                      cs, args) != cudaSuccess)
         return CSA_ERR_CUDA;
     }
@@ -541,8 +775,73 @@ extern "C" csa_status_t csa_cache_attn(
   }
   const int64_t warps = tokens * q_heads;
   const int64_t blocks = (warps + kScalarThreads / 32 - 1) / (kScalarThreads / 32);
-  return launch_pdl(scalar_kernel_for(format, d), dim3(static_cast<unsigned>(blocks)),
+  return launch_pdl(groups > 0 ? scalar_kernel_for<true>(format, d) : scalar_kernel_for<false>(format, d), dim3(static_cast<unsigned>(blocks)),
                     dim3(kScalarThreads), 0, cs, args) == cudaSuccess
              ? CSA_OK
              : CSA_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace csa
+
+using namespace csa;
+
+extern "C" size_t csa_cache_attn_workspace_bytes(int32_t S, int64_t tokens, int32_t q_heads,
+                                                 int32_t kv_heads, int32_t d, int64_t max_entries) {
+  if (check_attn_sizes(S, tokens, q_heads, kv_heads, d, max_entries) != CSA_OK) return 0;
+  if (d > kTileMaxDim) return kStatusBytes;
+  AttnParams p{};
+  int sms = 0;
+  if (plan_sizes(p, &sms, S, tokens, q_heads, kv_heads, d, max_entries, 0, 0) != cudaSuccess) return 0;
+  return lay_out(p, sms, chunked(p), nullptr);
+}
+
+extern "C" csa_status_t csa_cache_attn(
+    const void* q, int64_t q_row_stride, int64_t q_head_stride, const int32_t* cu_seqlens, int32_t S,
+    int64_t tokens, int32_t q_heads, int32_t kv_heads, int32_t d, const void* data,
+    const uint8_t* scales, int32_t format, const int32_t* page_table, int32_t max_pages,
+    int64_t num_pages, int32_t page_size, const int32_t* entries, const int32_t* first,
+    int32_t ratio, float softmax_scale, const float* sink, void* out, int64_t out_row_stride,
+    int64_t out_head_stride, float* lse, void* workspace, size_t workspace_bytes,
+    int32_t* dev_error, csa_stream_t stream) {
+  return run_attn({q, q_row_stride, q_head_stride, cu_seqlens, S, tokens, q_heads, kv_heads, d, data, scales, format,
+                   nullptr, 0, nullptr, 0, nullptr, page_table, max_pages, num_pages, page_size, entries, first,
+                   ratio, softmax_scale, sink, out, out_row_stride, out_head_stride, lse, workspace, workspace_bytes,
+                   dev_error},
+                  stream);
+}
+
+extern "C" size_t csa_cache_attn_prefix_workspace_bytes(int32_t S, int32_t G, int64_t tokens, int32_t q_heads,
+                                                        int32_t kv_heads, int32_t d, int64_t max_entries,
+                                                        int64_t max_prefix_entries) {
+  if (check_attn_sizes(S, tokens, q_heads, kv_heads, d, max_entries) != CSA_OK) return 0;
+  if (G < 0 || (G == 0 && S > 0) || G > CSA_MAX_SEGMENTS || max_prefix_entries < 0 || max_prefix_entries > INT_MAX ||
+      max_entries + max_prefix_entries > INT_MAX)
+    return 0;
+  if (d > kTileMaxDim || G == 0) return kStatusBytes;
+  AttnParams p{};
+  int sms = 0;
+  if (plan_sizes(p, &sms, S, tokens, q_heads, kv_heads, d, max_entries, G, max_prefix_entries) != cudaSuccess) return 0;
+  return lay_out(p, sms, chunked(p), nullptr);
+}
+
+extern "C" csa_status_t csa_cache_attn_prefix(
+    const void* q, int64_t q_row_stride, int64_t q_head_stride, const int32_t* cu_seqlens, int32_t S,
+    int64_t tokens, int32_t q_heads, int32_t kv_heads, int32_t d, const void* data,
+    const uint8_t* scales, int32_t format, const int32_t* prefix_seqs, int32_t G, const int32_t* prefix_table,
+    int32_t max_prefix_pages, const int32_t* prefix_entries, const int32_t* page_table, int32_t max_pages,
+    int64_t num_pages, int32_t page_size, const int32_t* entries, const int32_t* first,
+    int32_t ratio, float softmax_scale, const float* sink, void* out, int64_t out_row_stride,
+    int64_t out_head_stride, float* lse, void* workspace, size_t workspace_bytes,
+    int32_t* dev_error, csa_stream_t stream) {
+  if (G < 0 || max_prefix_pages < 0 || (G == 0 && S > 0)) return CSA_ERR_INVALID_VALUE;
+  if (G > 0 && (prefix_seqs == nullptr || prefix_entries == nullptr || (max_prefix_pages > 0 && prefix_table == nullptr)))
+    return CSA_ERR_INVALID_VALUE;
+  if (!is_aligned(prefix_seqs, 4) || !is_aligned(prefix_table, 4) || !is_aligned(prefix_entries, 4))
+    return CSA_ERR_INVALID_VALUE;
+  return run_attn({q, q_row_stride, q_head_stride, cu_seqlens, S, tokens, q_heads, kv_heads, d, data, scales, format,
+                   prefix_seqs, G, prefix_table, max_prefix_pages, prefix_entries, page_table, max_pages, num_pages,
+                   page_size, entries, first, ratio, softmax_scale, sink, out, out_row_stride, out_head_stride, lse,
+                   workspace, workspace_bytes, dev_error},
+                  stream);
 }

@@ -23,7 +23,22 @@ struct alignas(16) AttnUnit {
   int32_t n;            // the sequence's entries
   int32_t seen_all;     // entries that every row of the unit sees
   int32_t seen;         // entries that some row sees
-  int32_t pad[2];
+  int32_t span, spans;  // behind prefixes: its first span, and how many it has (a worker's start: the span it begins in)
+};
+// Behind shared prefixes a unit's rows may be of several sequences of a group, and its tiles are runs of
+// tiles ("spans"): the group's prefix, then each of its sequences' own entries.
+struct alignas(16) AttnSpan {
+  const int32_t* table;  // its pages
+  int32_t unit;
+  int32_t tile, tiles;     // its first tile in the unit, and how many
+  int32_t seen, seen_all;  // of its entries: those that some row of the unit sees, and that all see
+  int32_t row0, row1;      // rows of the unit that see any
+  int32_t token, first;    // own entries: the sequence's first token and its position; the prefix: the unit's
+                           // first sequence and its last
+  int32_t n, before;       // entries of the sequence, and those of them before the span's
+  int32_t packed;          // row of its first entry among the packed ones
+  int32_t own;
+  int32_t pad;
 };
 struct alignas(16) AttnStart {  // a worker's share: its first unit, the tile there, and how many tiles
   AttnUnit u;
@@ -40,7 +55,7 @@ struct alignas(16) AttnHead {
   int32_t few, many;  // shared units, of few pieces and of many
   int32_t pad;
 };
-static_assert(sizeof(AttnUnit) == 48 && sizeof(AttnStart) == 64 && sizeof(AttnJoin) == 64 && sizeof(AttnHead) == 16,
+static_assert(sizeof(AttnSpan) == 64 && sizeof(AttnUnit) == 48 && sizeof(AttnStart) == 64 && sizeof(AttnJoin) == 64 && sizeof(AttnHead) == 16,
               "read in 16-byte pieces");
 
 struct AttnParams {
@@ -71,6 +86,14 @@ struct AttnParams {
   int packed_rows;  // rows of a sequence's cache head in `packed`, a multiple of 128
   int box_rows;     // entries of a tensor copy's box from the pages
   float scale;  // softmax_scale
+  // groups of sequences behind a shared prefix (csa_cache_attn_prefix)
+  const int32_t* prefix_seqs;     // [groups + 1]: each group's first sequence
+  const int32_t* prefix_table;    // [groups, max_prefix_pages]
+  const int32_t* prefix_entries;  // [groups]
+  AttnSpan* spans;                // workspace: [max_spans]
+  int64_t max_prefix, max_spans;  // entries of a prefix, at most
+  int groups, max_prefix_pages;
+  int prefix_rows;    // rows of a prefix's cache head in `packed`; the sequences' own lie behind all prefixes
   int withhold_tile;      // test hook: tile of the first CTA's first unit that never comes, -1: none
   long long wait_cycles;  // bound of each wait on a barrier in shared memory, in SM clock cycles
 };
@@ -87,6 +110,10 @@ __device__ __forceinline__ int visible(int64_t pos, int ratio, int n) {
 __device__ __forceinline__ int sequence_rows(const AttnParams& p, int s) {
   return (__ldg(p.cu + s + 1) - __ldg(p.cu + s)) * p.group;
 }
+// Tiles of a run of entries.
+__device__ __forceinline__ int tiles_of(int entries) {
+  return entries <= kAttnEntries ? (entries > 0 ? 1 : 0) : (entries - 1) / kAttnEntries + 1;
+}
 // A unit of sequence s from its place.
 __device__ __forceinline__ AttnUnit make_unit(const AttnParams& p, int s, int kvh, int block) {
   AttnUnit u{};
@@ -100,7 +127,7 @@ __device__ __forceinline__ AttnUnit make_unit(const AttnParams& p, int s, int kv
   const int last = min(block * kAttnRows + kAttnRows, u.rows) - 1;
   u.seen_all = visible(static_cast<int64_t>(u.first) + block * kAttnRows / p.group, p.ratio, u.n);
   u.seen = visible(static_cast<int64_t>(u.first) + last / p.group, p.ratio, u.n);
-  u.tiles = u.seen <= kAttnEntries ? 1 : (u.seen - 1) / kAttnEntries + 1;
+  u.tiles = max(1, tiles_of(u.seen));
   return u;
 }
 

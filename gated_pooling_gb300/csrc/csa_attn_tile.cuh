@@ -35,6 +35,7 @@
 #pragma once
 
 #include <climits>
+#include <type_traits>
 
 #include "csa_attn.cuh"
 #include "csa_tcgen05.cuh"
@@ -353,7 +354,19 @@ __device__ __forceinline__ AttnUnit read_unit(const AttnUnit* at) {
     asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v[i].x), "=r"(v[i].y), "=r"(v[i].z), "=r"(v[i].w)
                  : "l"(reinterpret_cast<const int4*>(at) + i));
-  return {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w, v[2].x, v[2].y, {0, 0}};
+  return {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w, v[2].x, v[2].y, v[2].z, v[2].w};
+}
+__device__ __forceinline__ AttnSpan read_span(const AttnSpan* at) {
+  union {
+    int4 v[4];
+    AttnSpan s;
+  } r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.v[i].x), "=r"(r.v[i].y), "=r"(r.v[i].z), "=r"(r.v[i].w)
+                 : "l"(reinterpret_cast<const int4*>(at) + i));
+  return r.s;
 }
 
 // The runs of tiles of one unit in a worker's share.
@@ -385,8 +398,65 @@ struct SegmentWalk {
   __device__ __forceinline__ bool last() const { return left == t1 - t0; }
 };
 
+// The walk with what a tile's entries are: the unit's sequence, or behind prefixes the span that the
+// tile lies in, which enter() finds (tiles in order; some may be passed over).
+template <bool PREFIX>
+struct TileWalk : SegmentWalk {
+  __device__ __forceinline__ TileWalk(const AttnParams& pp, int worker) : SegmentWalk(pp, worker) {}
+  __device__ __forceinline__ bool enter(int) { return false; }
+  __device__ __forceinline__ int at(int tile) const { return tile; }  // among the list of entries that it belongs to
+  __device__ __forceinline__ int run_end() const { return t1; }
+  __device__ __forceinline__ int seen() const { return u.seen; }
+  __device__ __forceinline__ int seen_all() const { return u.seen_all; }
+  __device__ __forceinline__ const int32_t* table() const { return p.table + static_cast<int64_t>(u.s) * p.max_pages; }
+  __device__ __forceinline__ int packed() const { return (u.s * p.kv_heads + u.kvh) * p.packed_rows; }
+};
+template <>
+struct TileWalk<true> : SegmentWalk {
+  AttnSpan span;
+  const AttnSpan* next_span;
+  __device__ __forceinline__ TileWalk(const AttnParams& pp, int worker) : SegmentWalk(pp, worker) {
+    next_span = p.spans + u.span;
+    span.unit = -1;
+  }
+  // whether the tile lies in another span than the one before
+  __device__ __forceinline__ bool enter(int tile) {
+    bool moved = false;
+    while (span.unit < unit || tile >= span.tile + span.tiles) {
+      span = read_span(next_span++);
+      moved = true;
+    }
+    return moved;
+  }
+  __device__ __forceinline__ int at(int tile) const { return tile - span.tile; }
+  __device__ __forceinline__ int run_end() const { return min(t1, span.tile + span.tiles); }
+  __device__ __forceinline__ int seen() const { return span.seen; }
+  __device__ __forceinline__ int seen_all() const { return span.seen_all; }
+  __device__ __forceinline__ const int32_t* table() const { return span.table; }
+  __device__ __forceinline__ int packed() const { return span.packed; }
+};
+// What row `row` of a unit (`some`: it is one of the group's) sees of a span's entries.
+__device__ __forceinline__ int span_limit(const AttnParams& p, const AttnUnit& u, const AttnSpan& v, int r) {
+  const int row = u.block * kAttnRows + r;
+  if (row >= u.rows) return v.seen;
+  const int token = u.token + row / p.group;
+  if (v.own != 0) {
+    if (r < v.row0 || r >= v.row1) return 0;
+    return max(0, visible(static_cast<int64_t>(v.first) + (token - v.token), p.ratio, v.n) - v.before);
+  }
+  if (v.seen_all >= v.seen) return v.seen;
+  int lo = v.token, hi = v.first + 1;  // the token's sequence: cu[lo] <= token < cu[hi], the last such one
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (__ldg(p.cu + mid) <= token) lo = mid;
+    else hi = mid;
+  }
+  const int64_t pos = static_cast<int64_t>(p.first != nullptr ? __ldg(p.first + lo) : 0) + (token - __ldg(p.cu + lo));
+  return visible(pos, p.ratio, v.seen);
+}
+
 // ------------------------------------------------------------------------------ the fetchers
-template <int NC, int SRC>
+template <int NC, int SRC, bool PREFIX>
 __device__ void tile_fetch(const AttnParams& p, TileSmall& sm, uint32_t base) {
   using SH = TileShape<NC>;
   using P = Take<SRC>;
@@ -396,7 +466,7 @@ __device__ void tile_fetch(const AttnParams& p, TileSmall& sm, uint32_t base) {
   const int group = lt / kGroup, gt = lt % kGroup;
   const int row_bytes = P::row_bytes(p.d);
 
-  SegmentWalk w(p, blockIdx.x);
+  TileWalk<PREFIX> w(p, blockIdx.x);
   int tile = w.t0, pair = 0, buf = 0;
   RingAt<SH::kRing> ring;
   bool fresh = true;  // the tile's rows are still to be looked up
@@ -415,19 +485,20 @@ __device__ void tile_fetch(const AttnParams& p, TileSmall& sm, uint32_t base) {
   // this thread's page of tile `ahead` of unit `unit`, read early
   int page = -1, ahead = -1, unit = -1;
   auto read_page = [&](int tl) {
-    const int e = tl * kAttnEntries + gt;
+    const int e = w.at(tl) * kAttnEntries + gt;
     ahead = tl;
     unit = w.unit;
-    page = e < w.u.seen ? __ldg(p.table + static_cast<int64_t>(w.u.s) * p.max_pages + e / p.page_size) : -1;
+    page = e < w.seen() ? __ldg(w.table() + e / p.page_size) : -1;
   };
   auto entry_at = [&](int e) {
     return ((static_cast<int64_t>(page) * p.page_size + e % p.page_size) * p.kv_heads + w.u.kvh) * row_bytes;
   };
   auto rows = [&]() {
+    w.enter(tile);
     if (ahead != tile || unit != w.unit) read_page(tile);
-    const int e = tile * kAttnEntries + gt;
+    const int e = w.at(tile) * kAttnEntries + gt;
     int64_t at = -1;
-    if (e < w.u.seen) {
+    if (e < w.seen()) {
       if (page >= 0 && page < p.num_pages) at = entry_at(e);
       else if (p.dev_error != nullptr) *p.dev_error = CSA_DEVERR_PAGE;
     }
@@ -435,7 +506,7 @@ __device__ void tile_fetch(const AttnParams& p, TileSmall& sm, uint32_t base) {
     sm.row[group][buf][gt] = at;
     named_barrier(6 + group, kGroup);
     fresh = false;
-    if (tile + kStep < w.t1) read_page(tile + kStep);
+    if (tile + kStep < w.run_end()) read_page(tile + kStep);
   };
 
   if (group == 1 && w.valid()) next_pair();
@@ -471,28 +542,27 @@ __device__ void tile_fetch(const AttnParams& p, TileSmall& sm, uint32_t base) {
 
 // The softmax warps' part of fetching (kHelped): the second half of a tile's pairs, each by 256 of
 // them.
-template <int SRC>
-__device__ __forceinline__ void help_places(const AttnParams& p, TileSmall& sm, const SegmentWalk& w, int tile,
-                                            uint32_t t) {
+template <int SRC, typename W>
+__device__ __forceinline__ void help_places(const AttnParams& p, TileSmall& sm, const W& w, int tile, uint32_t t) {
   const int tid = threadIdx.x;
   if (tid >= kAttnEntries) return;
-  const int e = tile * kAttnEntries + tid;
+  const int e = w.at(tile) * kAttnEntries + tid;
   int64_t at = -1;
-  if (e < w.u.seen) {
-    const int page = __ldg(p.table + static_cast<int64_t>(w.u.s) * p.max_pages + e / p.page_size);
+  if (e < w.seen()) {
+    const int page = __ldg(w.table() + e / p.page_size);
     if (page >= 0 && page < p.num_pages)
       at = ((static_cast<int64_t>(page) * p.page_size + e % p.page_size) * p.kv_heads + w.u.kvh) *
            Take<SRC>::row_bytes(p.d);
   }
   sm.help_row[t & 1u][tid] = at;
 }
-template <int NC, int SRC>
-__device__ __forceinline__ void tile_help(const AttnParams& p, TileSmall& sm, uint32_t base, const SegmentWalk& w,
-                                          int tile, uint32_t t) {
+template <int NC, int SRC, typename W>
+__device__ __forceinline__ void tile_help(const AttnParams& p, TileSmall& sm, uint32_t base, const W& w, int tile,
+                                          uint32_t t, bool moved) {
   using P = Take<SRC>;
   constexpr int kHalf = kSoftThreads / 2, kRows = 2, kRowStep = kAttnEntries / kRows;
   const int tid = threadIdx.x, half = tid / kHalf, ht = tid % kHalf;
-  if (tile == w.t0) help_places<SRC>(p, sm, w, tile, t);
+  if (moved || tile == w.t0) help_places<SRC>(p, sm, w, tile, t);
   named_barrier(5, kSoftThreads);
   const int pair = TileShape<NC>::kPairs / 2 + half, row = P::first_row(ht), col = pair * 128 + P::column(ht);
   P v[kRows];
@@ -504,7 +574,7 @@ __device__ __forceinline__ void tile_help(const AttnParams& p, TileSmall& sm, ui
   fence_proxy_async_smem();
   __syncwarp();
   if ((tid & 31) == 0) mbar_arrive(&sm.full[pair]);
-  if (tile + 1 < w.t1) help_places<SRC>(p, sm, w, tile + 1, t + 1);
+  if (tile + 1 < w.run_end()) help_places<SRC>(p, sm, w, tile + 1, t + 1);
 }
 
 // ------------------------------------------------------------- the warp that issues tensor copies
@@ -512,7 +582,7 @@ __device__ __forceinline__ void tile_help(const AttnParams& p, TileSmall& sm, ui
 // A box behind the last entry that the unit sees is not copied, and rows behind it in a copied
 // box are whatever the pool holds there: masked in the scores, and made finite where they are
 // not before the second product. From packed entries: a pair's two chunks by a lane each.
-template <int NC, int SRC>
+template <int NC, int SRC, bool PREFIX>
 __device__ void tile_copy(const AttnParams& p, TileSmall& sm, uint32_t base, const CUtensorMap* map) {
   using SH = TileShape<NC>;
   const int lane = threadIdx.x & 31;
@@ -526,9 +596,10 @@ __device__ void tile_copy(const AttnParams& p, TileSmall& sm, uint32_t base, con
   };
   bool go = true;
   if constexpr (SRC == kFromPacked) {
-    for (SegmentWalk w(p, blockIdx.x); go && w.valid(); w.next()) {
-      const int row = (w.u.s * p.kv_heads + w.u.kvh) * p.packed_rows;
+    for (TileWalk<PREFIX> w(p, blockIdx.x); go && w.valid(); w.next()) {
       for (int tile = w.t0; go && tile < w.t1; ++tile) {
+        w.enter(tile);
+        const int row = w.packed() + w.at(tile) * kAttnEntries;
         const bool withheld = tile_withheld(p, w.unit, tile);
         for (int c = 0; c < SH::kPairs && (go = room()); ++c, ring.next()) {
           ++places;
@@ -540,20 +611,21 @@ __device__ void tile_copy(const AttnParams& p, TileSmall& sm, uint32_t base, con
           if (lane == 0) mbar_arrive_expect_tx(&sm.full[ring.slot], kPairBytes);
           __syncwarp();
           if (lane < 2)
-            box_load2(base + ring.slot * kPairBytes + lane * kChunkBytes, map, c * 128 + lane * 64,
-                      row + tile * kAttnEntries, &sm.full[ring.slot]);
+            box_load2(base + ring.slot * kPairBytes + lane * kChunkBytes, map, c * 128 + lane * 64, row,
+                      &sm.full[ring.slot]);
         }
       }
     }
   } else {
     const int n = kAttnEntries / p.box_rows, chunk = lane / n, box = lane % n;
-    for (SegmentWalk w(p, blockIdx.x); go && w.valid(); w.next()) {
+    for (TileWalk<PREFIX> w(p, blockIdx.x); go && w.valid(); w.next()) {
       for (int tile = w.t0; go && tile < w.t1; ++tile) {
-        const int e = tile * kAttnEntries + box * p.box_rows;
-        bool on = chunk < 2 && e < w.u.seen;
+        w.enter(tile);
+        const int e = w.at(tile) * kAttnEntries + box * p.box_rows;
+        bool on = chunk < 2 && e < w.seen();
         int slot = 0;
         if (on) {
-          const int page = __ldg(p.table + static_cast<int64_t>(w.u.s) * p.max_pages + e / p.page_size);
+          const int page = __ldg(w.table() + e / p.page_size);
           on = page >= 0 && page < p.num_pages;
           if (on) slot = page * p.page_size + e % p.page_size;
           else if (p.dev_error != nullptr) *p.dev_error = CSA_DEVERR_PAGE;
@@ -702,7 +774,7 @@ __device__ __forceinline__ void spread_nans(const AttnParams& p, TileSmall& sm, 
 }
 
 // ------------------------------------------------------------------------- the softmax warps
-template <int NC, int SRC>
+template <int NC, int SRC, bool PREFIX>
 __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* smem, uint32_t base, uint32_t tmem) {
   using SH = TileShape<NC>;
   const int tid = threadIdx.x, lane = tid & 31, quad = (tid >> 5) & 3, group = tid >> 7;
@@ -722,7 +794,7 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
     const bool some = row < u.rows;
     const int head = u.kvh * p.group + (row - token * p.group);
     const int64_t at = static_cast<int64_t>(u.token) + token;
-    sm.lim[par][tid] = some ? visible(static_cast<int64_t>(u.first) + token, p.ratio, u.n) : u.seen;
+    if constexpr (!PREFIX) sm.lim[par][tid] = some ? visible(static_cast<int64_t>(u.first) + token, p.ratio, u.n) : u.seen;
     sm.q_at[tid] = some ? at * p.q_row + head * p.q_head : -1;
     sm.out_at[par][tid] = some ? at * p.out_row + head * p.out_head : -1;
     sm.lse_at[par][tid] = some ? static_cast<int32_t>(at * p.q_heads + head) : -1;
@@ -747,7 +819,8 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
   };
   int par = 0;
   if (tid < kAttnEntries) sm.odd[tid] = 0;
-  SegmentWalk w(p, blockIdx.x);
+  TileWalk<PREFIX> w(p, blockIdx.x);
+  int lim_at = 0;  // which of the two lists of limits holds: the unit's, or behind prefixes the span's
   if (w.valid()) {
     if (tid < kAttnRows) {
       set_up(w.u, 0);
@@ -758,7 +831,7 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
     q_copied();
   }
   for (; w.valid(); par ^= 1) {
-    const int seen_all = w.u.seen_all;
+    if constexpr (!PREFIX) lim_at = par;
     const bool whole = w.t0 == 0 && w.t1 == w.u.tiles, more = !w.last();
     if (more && tid >= kSoftThreads - 3) {  // the next unit on its way
       const int i = tid - (kSoftThreads - 3);
@@ -769,9 +842,19 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
     for (int c = 0; c < kSoftCols; ++c) l[c] = 0.f;
 
     for (int j = w.t0; j < w.t1; ++j, ++t) {
-      if constexpr (SH::template kHelped<SRC>) tile_help<NC, SRC>(p, sm, base, w, j, t);
-      const int e = j * kAttnEntries + e0;
-      const bool masked = (j + 1) * static_cast<int64_t>(kAttnEntries) > seen_all;
+      const bool moved = w.enter(j);
+      if constexpr (SH::template kHelped<SRC>) tile_help<NC, SRC>(p, sm, base, w, j, t, moved);
+      if constexpr (PREFIX) {
+        // the span's limits for the group's rows, in the list that no warp of the group reads any more (all
+        // have passed a barrier since the span before the last one)
+        if (moved) {
+          lim_at ^= 1;
+          if (quad == 0 && lane < kSoftCols) sm.lim[lim_at][c0 + lane] = span_limit(p, w.u, w.span, c0 + lane);
+          barrier_group();
+        }
+      }
+      const int e = w.at(j) * kAttnEntries + e0;
+      const bool masked = (w.at(j) + 1) * static_cast<int64_t>(kAttnEntries) > w.seen_all();
       const uint32_t s_at = lanes + SH::kTmemS + (t & 1u) * kAttnRows + c0;
       tile_wait(sm, p, &sm.scores[t & 1u], (t >> 1) & 1u);
       tc_fence_after();
@@ -783,7 +866,7 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
 #pragma unroll
           for (int c = 0; c < kSoftCols; ++c) {
             odd = odd || !(fabsf(s[c]) <= 3.4028234e38f);
-            if (e >= sm.lim[par][c0 + c]) s[c] = sl2 < 0.f ? INFINITY : -INFINITY;  // -inf once scaled
+            if (e >= sm.lim[lim_at][c0 + c]) s[c] = sl2 < 0.f ? INFINITY : -INFINITY;  // -inf once scaled
           }
         }
       };
@@ -864,7 +947,7 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
         if (odd && clear_odd<NC>(sm, smem, t, e0))
 #pragma unroll
           for (int c = 0; c < kSoftCols; ++c)
-            if (e < sm.lim[par][c0 + c] && !(fabsf(s[c]) <= 3.4028234e38f)) {
+            if (e < sm.lim[lim_at][c0 + c] && !(fabsf(s[c]) <= 3.4028234e38f)) {
               l[c] = __uint_as_float(0x7FFFFFFFu);
               asm volatile("st.shared.b16 [%0], %1;" ::"r"(row + (((group * 2 + (c >> 3)) ^ (e0 & 7)) << 4) + 2 * (c & 7)),
                            "h"(static_cast<uint16_t>(0x7FFF))
@@ -1004,18 +1087,43 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
 // rows) reads them again; packing reads and writes them once. Block (x, s, cache head): 32
 // entries at a time, a thread 8 columns at a time.
 constexpr int kPackThreads = 256, kPackRows = 32;
-template <int NC, int FORMAT>
+template <int NC, int FORMAT, bool PREFIX>
 __global__ void __launch_bounds__(kPackThreads) attn_pack_kernel(const __grid_constant__ AttnParams p) {
   constexpr int kPer = NC * 8;  // pieces of 8 columns
   pdl_wait();
   if (p.head->status != 0) return;
-  const int seq = blockIdx.y, kvh = blockIdx.z;
-  const int rows = sequence_rows(p, seq);
-  if (rows == 0) return;
-  const int64_t first = p.first != nullptr ? __ldg(p.first + seq) : 0;
-  const int n = visible(first + rows / p.group - 1, p.ratio, __ldg(p.entries + seq));
+  const int kvh = blockIdx.z;
+  const int32_t* table;
+  int64_t row0;  // of the run's first entry
+  int n;
+  if (PREFIX && static_cast<int>(blockIdx.y) < p.groups) {
+    const int g = blockIdx.y;
+    if (__ldg(p.cu + __ldg(p.prefix_seqs + g + 1)) == __ldg(p.cu + __ldg(p.prefix_seqs + g))) return;
+    n = __ldg(p.prefix_entries + g);
+    table = p.prefix_table + static_cast<int64_t>(g) * p.max_prefix_pages;
+    row0 = (static_cast<int64_t>(g) * p.kv_heads + kvh) * p.prefix_rows;
+  } else {
+    const int seq = blockIdx.y - (PREFIX ? p.groups : 0);
+    const int rows = sequence_rows(p, seq);
+    if (rows == 0) return;
+    int before = 0;
+    if constexpr (PREFIX) {
+      int lo = 0, hi = p.groups;  // the sequence's group
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (__ldg(p.prefix_seqs + mid) <= seq) lo = mid;
+        else hi = mid;
+      }
+      before = __ldg(p.prefix_entries + lo);
+    }
+    const int64_t first = p.first != nullptr ? __ldg(p.first + seq) : 0;
+    n = max(0, visible(first + rows / p.group - 1, p.ratio, before + __ldg(p.entries + seq)) - before);
+    table = p.table + static_cast<int64_t>(seq) * p.max_pages;
+    row0 = (static_cast<int64_t>(seq) * p.kv_heads + kvh) * p.packed_rows + static_cast<int64_t>(PREFIX ? p.groups : 0) * p.kv_heads * p.prefix_rows;
+    if (PREFIX && n == 0) return;
+  }
   const int end = max(kAttnEntries, (n + kAttnEntries - 1) / kAttnEntries * kAttnEntries);
-  uint16_t* all = p.packed + (static_cast<int64_t>(seq) * p.kv_heads + kvh) * p.packed_rows * (NC * 64);
+  uint16_t* all = p.packed + row0 * (NC * 64);
   for (int e0 = blockIdx.x * kPackRows; e0 < end; e0 += gridDim.x * kPackRows) {
     uint16_t* to = all + static_cast<int64_t>(e0) * (NC * 64);
 #pragma unroll 4
@@ -1023,7 +1131,7 @@ __global__ void __launch_bounds__(kPackThreads) attn_pack_kernel(const __grid_co
       const int r = i / kPer, col = (i % kPer) * 8, e = e0 + r;
       uint4 v = make_uint4(0, 0, 0, 0);
       if (e < n && col < p.d) {
-        const int page = __ldg(p.table + static_cast<int64_t>(seq) * p.max_pages + e / p.page_size);
+        const int page = __ldg(table + e / p.page_size);
         if (page >= 0 && page < p.num_pages) {
           const int64_t entry = (static_cast<int64_t>(page) * p.page_size + e % p.page_size) * p.kv_heads + kvh;
           if constexpr (FORMAT == CSA_CACHE_BF16) {
@@ -1046,7 +1154,7 @@ __global__ void __launch_bounds__(kPackThreads) attn_pack_kernel(const __grid_co
   }
 }
 
-template <int NC, int SRC>
+template <int NC, int SRC, bool PREFIX>
 __global__ void __launch_bounds__(TileCta<SRC>::kThreads, 1)
     attn_tile_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap map) {
   using SH = TileShape<NC>;
@@ -1081,18 +1189,18 @@ __global__ void __launch_bounds__(TileCta<SRC>::kThreads, 1)
   if constexpr (CTA::kByThreads) {
     if (warp >= kTileFirstLoader) {
       regs_up<kLoadRegs>();
-      if (run) tile_fetch<NC, SRC>(p, sm, base);
+      if (run) tile_fetch<NC, SRC, PREFIX>(p, sm, base);
     } else if (warp >= kTileSoftWarps) {
       regs_down<kIssueRegs>();
       if (run && warp == kTileSoftWarps) tile_products<NC>(p, sm, base, tmem);
     } else {
       regs_down<kSoftRegs>();
-      if (run) tile_softmax<NC, SRC>(p, sm, smem, base, tmem);
+      if (run) tile_softmax<NC, SRC, PREFIX>(p, sm, smem, base, tmem);
     }
   } else if (run) {
     if (warp == kTileSoftWarps) tile_products<NC>(p, sm, base, tmem);
-    else if (warp == kTileSoftWarps + 1) tile_copy<NC, SRC>(p, sm, base, &map);
-    else if (warp < kTileSoftWarps) tile_softmax<NC, SRC>(p, sm, smem, base, tmem);
+    else if (warp == kTileSoftWarps + 1) tile_copy<NC, SRC, PREFIX>(p, sm, base, &map);
+    else if (warp < kTileSoftWarps) tile_softmax<NC, SRC, PREFIX>(p, sm, smem, base, tmem);
   }
   tc_fence_before();
   __syncthreads();
@@ -1220,5 +1328,45 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinBlocks) attn_join_kernel(co
       p.lse[at * p.q_heads + head_of] = some ? (mx + log2f(all)) * kLn2 : sink_e;
   }
 }
+
+// The kernels of a call: chunks of 64 columns, where a tile comes from, the cache's format.
+struct TileKernels {
+  const void *tile, *join, *pack;
+  int threads;
+  size_t smem;
+};
+template <typename F>
+auto by_chunks(int chunks, F f) {
+  return chunks == 2   ? f(std::integral_constant<int, 2>{})
+         : chunks == 4 ? f(std::integral_constant<int, 4>{})
+                       : f(std::integral_constant<int, 8>{});
+}
+template <bool PREFIX>
+TileKernels tile_kernels(int nc, int source, int format) {
+  return by_chunks(nc, [&](auto c) {
+    constexpr int NC = decltype(c)::value;
+    TileKernels r{};
+    r.smem = TileShape<NC>::kSmemBytes;
+    r.join = reinterpret_cast<const void*>(attn_join_kernel<NC>);
+    auto use = [&](auto src) {
+      constexpr int SRC = decltype(src)::value;
+      r.tile = reinterpret_cast<const void*>(attn_tile_kernel<NC, SRC, PREFIX>);
+      r.threads = TileCta<SRC>::kThreads;
+    };
+    switch (source) {
+      case kFromPacked: use(std::integral_constant<int, kFromPacked>{}); break;
+      case kFromBoxes: use(std::integral_constant<int, kFromBoxes>{}); break;
+      case kFromBf16: use(std::integral_constant<int, kFromBf16>{}); break;
+      case kFromE4m3: use(std::integral_constant<int, kFromE4m3>{}); break;
+      default: use(std::integral_constant<int, kFromE2m1>{}); break;
+    }
+    r.pack = format == CSA_CACHE_BF16   ? reinterpret_cast<const void*>(attn_pack_kernel<NC, CSA_CACHE_BF16, PREFIX>)
+             : format == CSA_CACHE_E4M3 ? reinterpret_cast<const void*>(attn_pack_kernel<NC, CSA_CACHE_E4M3, PREFIX>)
+                                        : reinterpret_cast<const void*>(attn_pack_kernel<NC, CSA_CACHE_E2M1, PREFIX>);
+    return r;
+  });
+}
+// Those behind shared prefixes (csa_attn_prefix.cu: they compile beside the others).
+TileKernels prefix_tile_kernels(int nc, int source, int format);
 
 }  // namespace csa

@@ -513,6 +513,42 @@ csa_status_t csa_cache_attn(const void* q, int64_t q_row_stride, int64_t q_head_
                             int64_t out_head_stride, float* lse, void* workspace,
                             size_t workspace_bytes, int32_t* dev_error, csa_stream_t stream);
 
+/* ------------------------------------------------------------------------------------
+ * Attention behind shared prefixes: csa_cache_attn for a batch whose sequences begin alike. Sequences lie in
+ * groups, group g those of [prefix_seqs[g], prefix_seqs[g+1]); its prefix_entries[g] entries lie in
+ * the pages prefix_table[g], once for all, and come before each sequence's own entries[s]:
+ *   entry e < prefix_entries[g] of sequence s is the prefix's, entry prefix_entries[g] + j its own number j,
+ * and out, lse, the entries that a token sees, sinks and the rules for values out of the ordinary are those of
+ * csa_cache_attn over prefix_entries[g] + entries[s] entries. The rows of a group's tokens read a prefix
+ * together, 64 (token, head) pairs at a time, where a call without prefixes reads it again for every sequence.
+ * ------------------------------------------------------------------------------------ */
+
+/* Bytes of device workspace csa_cache_attn_prefix needs on the current device; 0 on bad sizes.
+ * max_entries = max_pages * page_size, max_prefix_entries = max_prefix_pages * page_size of the call. */
+size_t csa_cache_attn_prefix_workspace_bytes(int32_t S, int32_t G, int64_t tokens, int32_t q_heads,
+                                             int32_t kv_heads, int32_t d, int64_t max_entries,
+                                             int64_t max_prefix_entries);
+
+/*   prefix_seqs     int32 [G+1] (device), non-decreasing from 0 to S; a group may be empty
+ *   prefix_table    int32 [G, max_prefix_pages] (device); only the pages that a prefix needs are read
+ *   prefix_entries  int32 [G] (device); 0 where a group shares nothing
+ *   first           int32 [S] or NULL: positions in the whole sequence, the prefix's tokens counted
+ * All else as for csa_cache_attn, with max_entries + max_prefix_entries below 2^31 and G up to CSA_MAX_SEGMENTS
+ * (CSA_ERR_UNSUPPORTED), G >= 1 unless S = 0. Bad prefixes skip all outputs (CSA_DEVERR_PREFIX); after CSA_DEVERR_PAGE the
+ * outputs of the sequences that need the page are unspecified. */
+csa_status_t csa_cache_attn_prefix(const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                                   const int32_t* cu_seqlens, int32_t S, int64_t tokens,
+                                   int32_t q_heads, int32_t kv_heads, int32_t d, const void* data,
+                                   const uint8_t* scales, int32_t format, const int32_t* prefix_seqs,
+                                   int32_t G, const int32_t* prefix_table, int32_t max_prefix_pages,
+                                   const int32_t* prefix_entries, const int32_t* page_table,
+                                   int32_t max_pages, int64_t num_pages, int32_t page_size,
+                                   const int32_t* entries, const int32_t* first, int32_t ratio,
+                                   float softmax_scale, const float* sink, void* out,
+                                   int64_t out_row_stride, int64_t out_head_stride, float* lse,
+                                   void* workspace, size_t workspace_bytes, int32_t* dev_error,
+                                   csa_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

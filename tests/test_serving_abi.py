@@ -71,6 +71,44 @@ def test_append_refusals(lib, over, code):
     assert append(lib, **over) == code
 
 
+# ------------------------------------------------------------------ attention behind prefixes
+def attn(lib, **over):
+    a = dict(q=FAKE, qr=128, qh=64, cu=FAKE, S=2, tokens=4, H=2, kv=1, d=64, data=FAKE, scales=FAKE, fmt=1, seqs=FAKE, G=1, ptable=FAKE,
+             max_prefix=4, pentries=FAKE, table=FAKE, max_pages=4, num_pages=8, page=16, entries=FAKE, first=FAKE, ratio=4, scale=0.125,
+             sink=FAKE, out=FAKE, outr=128, outh=64, lse=FAKE, ws=FAKE, nb=1 << 30, err=None)
+    a.update(over)
+    return lib.csa_cache_attn_prefix(*a.values(), None)
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(S=-1), INVALID), (dict(tokens=-1), INVALID), (dict(H=0), INVALID), (dict(kv=0), INVALID), (dict(H=3, kv=2), INVALID),
+    (dict(d=0), INVALID), (dict(G=-1), INVALID), (dict(G=0), INVALID), (dict(max_prefix=-1), INVALID), (dict(seqs=None), INVALID),
+    (dict(ptable=None), INVALID), (dict(pentries=None), INVALID), (dict(seqs=FAKE + 2), INVALID), (dict(ptable=FAKE + 2), INVALID),
+    (dict(pentries=FAKE + 2), INVALID), (dict(max_pages=-1), INVALID), (dict(num_pages=-1), INVALID), (dict(page=0), INVALID),
+    (dict(ratio=-1), INVALID), (dict(qr=-1), INVALID), (dict(qh=-1), INVALID), (dict(outr=-1), INVALID), (dict(outh=-1), INVALID),
+    (dict(scale=math.nan), INVALID), (dict(scale=math.inf), INVALID), (dict(cu=None), INVALID), (dict(entries=None), INVALID),
+    (dict(q=None), INVALID), (dict(out=None), INVALID), (dict(table=None), INVALID), (dict(data=None), INVALID),
+    (dict(scales=None), INVALID), (dict(q=FAKE + 1), INVALID), (dict(out=FAKE + 1), INVALID), (dict(cu=FAKE + 2), INVALID),
+    (dict(table=FAKE + 2), INVALID), (dict(entries=FAKE + 2), INVALID), (dict(first=FAKE + 2), INVALID),
+    (dict(sink=FAKE + 2), INVALID), (dict(lse=FAKE + 2), INVALID), (dict(err=FAKE + 2), INVALID), (dict(ws=FAKE + 8), INVALID),
+    (dict(data=FAKE + 1, fmt=0), INVALID), (dict(d=1025, fmt=0), UNSUPPORTED), (dict(d=72), UNSUPPORTED), (dict(fmt=3), UNSUPPORTED),
+    (dict(S=20000), UNSUPPORTED), (dict(G=20000), UNSUPPORTED), (dict(tokens=1 << 30), UNSUPPORTED),
+    (dict(max_pages=1 << 30), UNSUPPORTED), (dict(max_prefix=1 << 30), UNSUPPORTED),
+    (dict(max_pages=1 << 26, max_prefix=1 << 26), UNSUPPORTED), (dict(num_pages=1 << 60), UNSUPPORTED), (dict(ws=None), WORKSPACE),
+    (dict(nb=8), WORKSPACE), (dict(S=0), OK), (dict(S=0, G=0, seqs=None, ptable=None, pentries=None), OK), (dict(tokens=0), OK),
+    (dict(outh=63), INVALID), (dict(outr=127), INVALID), (dict(outr=0), INVALID), (dict(outr=64, outh=255), INVALID),
+])
+def test_attn_refusals(lib, over, code):
+    assert attn(lib, **over) == code
+
+
+def test_attn_workspace_query_refuses(lib):
+    for bad in ((-1, 1, 1, 1, 1, 64, 16, 16), (1, 0, 1, 1, 1, 64, 16, 16), (1, -1, 1, 1, 1, 64, 16, 16), (1, 20000, 1, 1, 1, 64, 16, 16),
+                (1, 1, 1, 1, 1, 64, -1, 16), (1, 1, 1, 1, 1, 64, 16, -1), (1, 1, 1, 1, 1, 64, 1 << 30, 1 << 30),
+                (1, 1, 1, 3, 2, 64, 16, 16), (1, 1, 1, 1, 1, 1025, 16, 16)):
+        assert gp.csa_cache_attn_prefix_workspace_bytes(*bad) == 0
+
+
 # ------------------------------------------------------------- the references check themselves
 @pytest.mark.parametrize("ratio,coff", [(1, 1), (1, 2), (3, 1), (4, 2)])
 def test_held_elements_are_those_that_later_windows_read(ratio, coff):
