@@ -56,7 +56,9 @@ __device__ __forceinline__ int64_t plan_scan(int64_t v, int64_t* warps, int64_t&
 
 // Where each worker's share of the units' work begins, and the units that several workers share. All threads
 // of the plan's block; `work`: where each unit's work begins, `all` of them together.
-__device__ __forceinline__ void plan_shares(const AttnParams& p, int64_t units, int64_t all, const int64_t* work, int* s_joins) {
+// span_tile: behind prefixes the spans' first tiles, where shared memory holds them.
+__device__ __forceinline__ void plan_shares(const AttnParams& p, int64_t units, int64_t all, const int64_t* work, int* s_joins,
+                                            const int* span_tile) {
   // the unit and tile that a place in the work stands for, and how many tiles lie before it
   struct Place {
     int64_t unit, tile, before;
@@ -86,7 +88,7 @@ __device__ __forceinline__ void plan_shares(const AttnParams& p, int64_t units, 
         int l = start.u.span, h = l + start.u.spans;
         while (h - l > 1) {
           const int mid = (l + h) / 2;
-          if (p.spans[mid].tile <= start.tile) l = mid;
+          if ((span_tile != nullptr ? span_tile[mid] : p.spans[mid].tile) <= start.tile) l = mid;
           else h = mid;
         }
         start.u.span = l;
@@ -180,101 +182,104 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnParams p) {
     if (few) s_work[units] = all;
   }
   __syncthreads();
-  plan_shares(p, units, all, few ? s_work : p.unit_first, s_joins);
+  plan_shares(p, units, all, few ? s_work : p.unit_first, s_joins, nullptr);
 }
 
 // The same behind shared prefixes: units of a group's rows, whatever sequences they are of, and their spans.
-// Sequences' numbers are looked up again and again: they are held in shared memory up to kPlanCached of them.
-constexpr int kPlanCached = 4096;
-__global__ void __launch_bounds__(kPlanThreads) attn_prefix_plan_kernel(AttnParams p) {
+// `lanes` neighbouring threads work on a block of 64 rows, a sequence each (as many as single tokens have in
+// one), and write its units of all cache heads. What is looked up again and again is held in shared
+// memory: sequences' numbers up to kPlanCached of them, spans' first tiles up to kPlanSpans.
+// (A thread a unit, which walked through its sequences three times, took 9 us for 64 sequences of 64 heads
+// and 23 for 120 of 8; so it takes 5 and 6.)
+constexpr int kPlanCached = 4096, kPlanSpans = 2048;
+__global__ void __launch_bounds__(kPlanThreads) attn_prefix_plan_kernel(AttnParams p, int lanes) {
   extern __shared__ int s_mem[];
   __shared__ int64_t s_warps[32];
   __shared__ int64_t s_work[kPlanUnits + 1];
+  __shared__ int64_t s_begin[kPlanThreads];  // of a round's blocks: where their units' work begins,
+  __shared__ int s_span[kPlanThreads];       // their first spans,
+  __shared__ int s_tiles[kPlanThreads], s_spans[kPlanThreads];  // and how many tiles and spans a unit has
+  __shared__ int s_span_tile[kPlanSpans];
   __shared__ int s_joins[2];
-  int* s_first = s_mem;  // [groups + 1] first row block of each group
+  const int G = p.groups;
+  int* s_first = s_mem;          // [groups + 1] first row block of each group
+  int* s_seqs = s_first + G + 1;  // [groups + 1]
+  int* s_prefix = s_seqs + G + 1;  // [groups]
+  int* s_cu = s_prefix + G;
+  int* s_own = s_cu + p.S + 1;
+  int* s_pos = s_own + p.S;
   const bool cached = p.S <= kPlanCached;
-  const int32_t *cu = p.cu, *own = p.entries, *first = p.first;
   if (threadIdx.x < 2) s_joins[threadIdx.x] = 0;
   pdl_wait();
   int bad = 0;
-  {
-    int* s_cu = s_mem + p.groups + 1;
-    int* s_own = s_cu + p.S + 1;
-    int* s_pos = s_own + p.S;
-    for (int s = threadIdx.x; s < p.S; s += kPlanThreads) {
-      const int32_t a = __ldg(p.cu + s), b = __ldg(p.cu + s + 1), n = __ldg(p.entries + s);
-      if (b < a || a < 0 || b > p.tokens) bad |= 1;
-      if (n < 0 || n > p.max_entries) bad |= 2;
-      if (cached) {
-        s_cu[s] = a;
-        if (s == p.S - 1) s_cu[s + 1] = b;
-        s_own[s] = n;
-        s_pos[s] = p.first != nullptr ? __ldg(p.first + s) : 0;
-      }
-    }
-    if (cached) {
-      cu = s_cu;
-      own = s_own;
-      first = s_pos;
-    }
-  }
-  for (int g = threadIdx.x; g < p.groups; g += kPlanThreads) {
+  for (int g = threadIdx.x; g < G; g += kPlanThreads) {
     const int32_t a = __ldg(p.prefix_seqs + g), b = __ldg(p.prefix_seqs + g + 1), n = __ldg(p.prefix_entries + g);
-    if (a < 0 || b < a || b > p.S || (g == 0 && a != 0) || (g == p.groups - 1 && b != p.S) || n < 0 || n > p.max_prefix) bad |= 4;
+    if (a < 0 || b < a || b > p.S || (g == 0 && a != 0) || (g == G - 1 && b != p.S) || n < 0 || n > p.max_prefix) bad |= 4;
+    s_seqs[g] = a;
+    s_prefix[g] = n;
+    if (g == G - 1) s_seqs[G] = b;
   }
+  for (int s = threadIdx.x; s < p.S; s += kPlanThreads) {
+    const int32_t a = __ldg(p.cu + s), b = __ldg(p.cu + s + 1), n = __ldg(p.entries + s);
+    if (b < a || a < 0 || b > p.tokens) bad |= 1;
+    if (n < 0 || n > p.max_entries) bad |= 2;
+    if (cached) {
+      s_cu[s] = a;
+      if (s == p.S - 1) s_cu[s + 1] = b;
+      s_own[s] = n;
+      s_pos[s] = p.first != nullptr ? __ldg(p.first + s) : 0;
+    }
+  }
+  const int32_t* const cu = cached ? s_cu : p.cu;
+  const int32_t* const own = cached ? s_own : p.entries;
+  const int32_t* const first = cached ? s_pos : p.first;
   int code = 0;
-  if (__syncthreads_or(bad & 1)) code = CSA_DEVERR_CU_SEQLENS;
-  else if (__syncthreads_or(bad & 2)) code = CSA_DEVERR_ENTRIES;
-  else if (__syncthreads_or(bad & 4)) code = CSA_DEVERR_PREFIX;
+  if (__syncthreads_or(bad)) {
+    code = __syncthreads_or(bad & 1) ? CSA_DEVERR_CU_SEQLENS : CSA_DEVERR_PREFIX;
+    if (__syncthreads_or(bad & 2) && code == CSA_DEVERR_PREFIX) code = CSA_DEVERR_ENTRIES;
+  }
   if (threadIdx.x == 0) {
     p.head->status = code;
     if (code != 0 && p.dev_error != nullptr) *p.dev_error = code;
   }
   if (code != 0 || p.units == nullptr) return;
-  auto group_rows = [&](int g) { return (cu[p.prefix_seqs[g + 1]] - cu[p.prefix_seqs[g]]) * p.group; };
-  const int per = (p.groups + kPlanThreads - 1) / kPlanThreads;
-  const int lo = min(p.groups, static_cast<int>(threadIdx.x) * per), hi = min(p.groups, lo + per);
-  int64_t mine = 0, blocks = 0;
-  for (int g = lo; g < hi; ++g) mine += (group_rows(g) + kAttnRows - 1) / kAttnRows;
-  int64_t at = plan_scan(mine, s_warps, blocks);
-  for (int g = lo; g < hi; ++g) {
-    s_first[g] = static_cast<int>(at);
-    at += (group_rows(g) + kAttnRows - 1) / kAttnRows;
+  auto group_rows = [&](int g) { return (cu[s_seqs[g + 1]] - cu[s_seqs[g]]) * p.group; };
+  int64_t blocks = 0;
+  {
+    const int per = (G + kPlanThreads - 1) / kPlanThreads;
+    const int lo = min(G, static_cast<int>(threadIdx.x) * per), hi = min(G, lo + per);
+    int64_t mine = 0;
+    for (int g = lo; g < hi; ++g) mine += (group_rows(g) + kAttnRows - 1) / kAttnRows;
+    int64_t at = plan_scan(mine, s_warps, blocks);
+    for (int g = lo; g < hi; ++g) {
+      s_first[g] = static_cast<int>(at);
+      at += (group_rows(g) + kAttnRows - 1) / kAttnRows;
+    }
+    if (threadIdx.x == 0) s_first[G] = static_cast<int>(blocks);
   }
-  if (threadIdx.x == 0) s_first[p.groups] = static_cast<int>(blocks);
   __syncthreads();
   const int64_t units = blocks * p.kv_heads;
   const bool few = units <= kPlanUnits;
-  int64_t all = 0, all_spans = 0;
-  for (int64_t u0 = 0; u0 < units; u0 += kPlanThreads) {
-    const int64_t i = u0 + threadIdx.x;
-    AttnUnit u{};
-    int seq0 = 0, seq1 = -1, prefix_seen = 0, prefix_all = INT_MAX, row0 = 0, before = 0, t0 = 0, t1 = 0;
-    // own entries of the unit's sequence s: what some row sees, and what every row of it sees
-    auto sees = [&](int s, int& some, int& every) {
-      const int a = cu[s], b = cu[s + 1];
-      const int64_t pos = first != nullptr ? first[s] : 0;
-      every = visible(pos + (max(a, t0) - a), p.ratio, before + own[s]);
-      some = visible(pos + (min(b - 1, t1) - a), p.ratio, before + own[s]);
-    };
-    if (i < units) {
-      const int b = static_cast<int>(units < INT_MAX ? static_cast<int>(i) / p.kv_heads : i / p.kv_heads);
-      int g = 0, h = p.groups;  // s_first[g] <= b < s_first[h]
+  int64_t all = 0;
+  int all_spans = 0;
+  const int round = kPlanThreads / lanes, mine = threadIdx.x / lanes, lane = threadIdx.x % lanes;
+  for (int64_t b0 = 0; b0 < blocks; b0 += round) {
+    const int64_t b = b0 + mine;
+    int g = 0, seq0 = 0, seq1 = -1, row0 = 0, before = 0, t0 = 0, t1 = 0, token = 0, rows = 0;
+    if (b < blocks) {
+      int h = G;  // s_first[g] <= b < s_first[h]
       while (h - g > 1) {
         const int mid = (g + h) / 2;
         if (s_first[mid] <= b) g = mid;
         else h = mid;
       }
-      const int from = p.prefix_seqs[g], to = p.prefix_seqs[g + 1];
-      u.s = g;
-      u.kvh = static_cast<int>(i - static_cast<int64_t>(b) * p.kv_heads);
-      u.block = b - s_first[g];
-      u.token = cu[from];
-      u.rows = group_rows(g);
-      row0 = u.block * kAttnRows;
-      t0 = u.token + row0 / p.group;
-      t1 = u.token + (min(row0 + kAttnRows, u.rows) - 1) / p.group;
-      auto sequence = [&](int t) {  // the last one that begins by t, of the group: it holds t
+      const int from = s_seqs[g], to = s_seqs[g + 1];
+      token = cu[from];
+      rows = group_rows(g);
+      row0 = static_cast<int>(b - s_first[g]) * kAttnRows;
+      t0 = token + row0 / p.group;
+      t1 = token + (min(row0 + kAttnRows, rows) - 1) / p.group;
+      auto sequence = [&](int t) {  // the last one of the group that begins by t: it holds t
         int l = from, r = to;
         while (r - l > 1) {
           const int mid = (l + r) / 2;
@@ -285,87 +290,127 @@ __global__ void __launch_bounds__(kPlanThreads) attn_prefix_plan_kernel(AttnPara
       };
       seq0 = sequence(t0);
       seq1 = sequence(t1);
-      before = p.prefix_entries[g];
-      for (int s = seq0; s <= seq1; ++s) {
-        if (cu[s + 1] == cu[s]) continue;
-        int some, every;
-        sees(s, some, every);
-        prefix_seen = max(prefix_seen, min(some, before));
-        prefix_all = min(prefix_all, min(every, before));
-        u.tiles += tiles_of(some - before);
-        u.spans += some > before ? 1 : 0;
-      }
-      // (a unit that sees nothing has a tile of nothing)
-      if (prefix_seen > 0 || u.tiles == 0) {
-        u.tiles += max(1, tiles_of(prefix_seen));
-        u.spans += 1;
+      before = s_prefix[g];
+    }
+    // what the block's tokens of sequence s see: all of them, and some
+    auto sees = [&](int s, int& some, int& every) {
+      const int a = cu[s], e = cu[s + 1];
+      if (s > seq1 || a == e) return false;
+      const int64_t pos = first != nullptr ? first[s] : 0;
+      every = visible(pos + (max(a, t0) - a), p.ratio, before + own[s]);
+      some = p.ratio == 0 ? every : visible(pos + (min(e - 1, t1) - a), p.ratio, before + own[s]);
+      return true;
+    };
+    int own_tiles = 0, own_spans = 0, seen = 0, seen_all = INT_MAX;
+    for (int s = seq0 + lane; s <= seq1; s += lanes) {
+      int some, every;
+      if (!sees(s, some, every)) continue;
+      seen = max(seen, min(some, before));
+      seen_all = min(seen_all, min(every, before));
+      own_tiles += tiles_of(some - before);
+      own_spans += some > before ? 1 : 0;
+    }
+    __syncwarp();
+    for (int o = lanes / 2; o > 0; o >>= 1) {
+      seen = max(seen, __shfl_xor_sync(0xFFFFFFFFu, seen, o));
+      seen_all = min(seen_all, __shfl_xor_sync(0xFFFFFFFFu, seen_all, o));
+      own_tiles += __shfl_xor_sync(0xFFFFFFFFu, own_tiles, o);
+      own_spans += __shfl_xor_sync(0xFFFFFFFFu, own_spans, o);
+    }
+    // (a unit that sees nothing has a tile of nothing)
+    const bool prefix = seen > 0 || own_tiles == 0;
+    const int prefix_tiles = prefix ? max(1, tiles_of(seen)) : 0;
+    if (lane == 0) {
+      s_tiles[mine] = b < blocks ? own_tiles + prefix_tiles : 0;
+      s_spans[mine] = b < blocks ? own_spans + (prefix ? 1 : 0) : 0;
+    }
+    __syncthreads();
+    const bool holds = static_cast<int>(threadIdx.x) < round && b0 + threadIdx.x < blocks;
+    int64_t sum = 0;
+    const int64_t begin = all + plan_scan(holds ? static_cast<int64_t>(s_tiles[threadIdx.x] + p.unit_cost) * p.kv_heads : 0, s_warps, sum);
+    all += sum;
+    const int64_t span = all_spans + plan_scan(holds ? s_spans[threadIdx.x] * p.kv_heads : 0, s_warps, sum);
+    all_spans += static_cast<int>(sum);
+    if (holds) {
+      s_begin[threadIdx.x] = begin;
+      s_span[threadIdx.x] = static_cast<int>(span);
+    }
+    __syncthreads();
+    const int unit_tiles = s_tiles[mine], unit_spans = s_spans[mine], span0 = s_span[mine];
+    auto put = [&](int at, AttnSpan v, int kvh, int packed) {  // the unit's span `at`
+      v.unit = static_cast<int32_t>(b * p.kv_heads + kvh);
+      v.tiles = max(1, tiles_of(v.seen));
+      v.packed = packed;
+      const int to = span0 + kvh * unit_spans + at;
+      p.spans[to] = v;
+      if (to < kPlanSpans) s_span_tile[to] = v.tile;
+    };
+    if (b < blocks && lane == 0) {
+      AttnUnit u{};
+      u.s = g;
+      u.block = row0 / kAttnRows;
+      u.tiles = unit_tiles;
+      u.token = token;
+      u.rows = rows;
+      u.spans = unit_spans;
+      AttnSpan v{};
+      v.table = p.prefix_table + static_cast<int64_t>(g) * p.max_prefix_pages;
+      v.seen = seen;
+      v.seen_all = seen_all;
+      v.row1 = kAttnRows;
+      v.token = seq0;
+      v.first = seq1;
+      v.n = before;
+      for (int kvh = 0; kvh < p.kv_heads; ++kvh) {
+        const int64_t i = b * p.kv_heads + kvh, at = s_begin[mine] + kvh * static_cast<int64_t>(unit_tiles + p.unit_cost);
+        u.kvh = kvh;
+        u.span = span0 + kvh * unit_spans;
+        p.units[i] = u;
+        p.unit_first[i] = at;
+        if (few) s_work[i] = at;
+        if (prefix) put(0, v, kvh, (g * p.kv_heads + kvh) * p.prefix_rows);
       }
     }
-    int64_t sum = 0;
-    const int64_t begin = all + plan_scan(i < units ? u.tiles + p.unit_cost : 0, s_warps, sum);
-    all += sum;
-    const int64_t span = all_spans + plan_scan(u.spans, s_warps, sum);
-    all_spans += sum;
-    if (i < units) {
-      u.span = static_cast<int32_t>(span);
-      p.units[i] = u;
-      p.unit_first[i] = begin;
-      if (few) s_work[i] = begin;
-      AttnSpan* out = p.spans + span;
-      int tile = 0;
-      auto put = [&](AttnSpan v) {
-        v.unit = static_cast<int32_t>(i);
-        v.tile = tile;
-        v.tiles = max(1, tiles_of(v.seen));
-        tile += v.tiles;
-        *out++ = v;
-      };
-      int own_spans = 0;
-      for (int s = seq0; s <= seq1; ++s) {
-        if (cu[s + 1] == cu[s]) continue;
-        int some, every;
-        sees(s, some, every);
-        own_spans += some > before ? 1 : 0;
+    int tile = prefix_tiles, at = prefix ? 1 : 0;  // of the next of the lanes' sequences
+    for (int s = seq0 + lane; __any_sync(0xFFFFFFFFu, s <= seq1); s += lanes) {
+      int some = 0, every = 0;
+      const bool has = s <= seq1 && sees(s, some, every) && some > before;
+      const int mine_tiles = has ? tiles_of(some - before) : 0;
+      int to_tile = mine_tiles, to_span = has ? 1 : 0;  // inclusive sums over the lanes
+      for (int o = 1; o < lanes; o <<= 1) {
+        const int x = __shfl_up_sync(0xFFFFFFFFu, to_tile, o, lanes), y = __shfl_up_sync(0xFFFFFFFFu, to_span, o, lanes);
+        if (lane >= o) {
+          to_tile += x;
+          to_span += y;
+        }
       }
-      if (own_spans < u.spans) {
-        AttnSpan v{};
-        v.table = p.prefix_table + static_cast<int64_t>(u.s) * p.max_prefix_pages;
-        v.seen = prefix_seen;
-        v.seen_all = prefix_all;
-        v.row1 = kAttnRows;
-        v.token = seq0;
-        v.first = seq1;
-        v.n = before;
-        v.packed = (u.s * p.kv_heads + u.kvh) * p.prefix_rows;
-        put(v);
-      }
-      for (int s = seq0; s <= seq1; ++s) {
-        if (cu[s + 1] == cu[s]) continue;
-        int some, every;
-        sees(s, some, every);
-        if (some <= before) continue;
+      if (has) {
         AttnSpan v{};
         v.table = p.table + static_cast<int64_t>(s) * p.max_pages;
+        v.tile = tile + to_tile - mine_tiles;
         v.seen = some - before;
-        v.row0 = max(0, (cu[s] - u.token) * p.group - row0);
-        v.row1 = s == seq1 ? kAttnRows : min(kAttnRows, (cu[s + 1] - u.token) * p.group - row0);
+        v.row0 = max(0, (cu[s] - token) * p.group - row0);
+        v.row1 = s == seq1 ? kAttnRows : min(kAttnRows, (cu[s + 1] - token) * p.group - row0);
         v.seen_all = v.row0 == 0 && v.row1 == kAttnRows ? max(0, every - before) : 0;
         v.token = cu[s];
         v.first = first != nullptr ? first[s] : 0;
         v.n = before + own[s];
         v.before = before;
-        v.packed = p.groups * p.kv_heads * p.prefix_rows + (s * p.kv_heads + u.kvh) * p.packed_rows;
         v.own = 1;
-        put(v);
+        for (int kvh = 0; kvh < p.kv_heads; ++kvh)
+          put(at + to_span - 1, v, kvh, G * p.kv_heads * p.prefix_rows + (s * p.kv_heads + kvh) * p.packed_rows);
       }
+      tile += __shfl_sync(0xFFFFFFFFu, to_tile, lanes - 1, lanes);
+      at += __shfl_sync(0xFFFFFFFFu, to_span, lanes - 1, lanes);
     }
+    __syncthreads();
   }
   if (threadIdx.x == 0) {
     p.unit_first[units] = all;
     if (few) s_work[units] = all;
   }
   __syncthreads();
-  plan_shares(p, units, all, few ? s_work : p.unit_first, s_joins);
+  plan_shares(p, units, all, few ? s_work : p.unit_first, s_joins, all_spans <= kPlanSpans ? s_span_tile : nullptr);
 }
 
 // Scalar kernel, any d and alignment: a warp per new token and query head, a lane the columns
@@ -569,10 +614,14 @@ constexpr int64_t kMaxPacked = int64_t{4} << 30;
 bool chunked(const AttnParams& p) {
   if (p.d > kTileMaxDim || p.S < 1) return false;
   if (p.groups > 0) {
-    // behind prefixes: four units a prefix, and the own entries, which fewer units read, no more than
-    // the prefixes
-    if (p.tokens * p.group < kChunkRows * p.groups || static_cast<int64_t>(p.S) * p.packed_rows > static_cast<int64_t>(p.groups) * p.prefix_rows)
-      return false;
+    // Behind prefixes: by the tiles that units read of prefixes and those that are packed, own entries too, at the
+    // tables' capacity. Measured over codes at d = 128, 256 and 512, packing saves 5, 8 and 17 ns a tile read and
+    // costs 27, 24 and 66 ns a tile packed, and a launch: 64 sequences of 64 heads of 512 behind 16384 entries
+    // take 193 us packed and 298 not, 16 57.8 and 67.6 behind 2048, but with up to 2000 own entries each 112
+    // and 89; 4 sequences 47.7 and 48.4.
+    const int64_t units = (p.tokens * p.group + kAttnRows - 1) / kAttnRows, tiles = p.prefix_rows / kAttnEntries;
+    const int64_t packed = p.groups * tiles + static_cast<int64_t>(p.S) * (p.packed_rows / kAttnEntries);
+    if (units * tiles < 4 * packed + 256) return false;
   } else if (p.tokens * p.group < kChunkRows * p.S) {
     return false;
   }
@@ -680,7 +729,7 @@ csa_status_t run_attn(const AttnCall& c, csa_stream_t stream) {
   while (p.box_rows < kAttnEntries && page_size % (2 * p.box_rows) == 0) p.box_rows *= 2;
   const int64_t most_tiles = p.max_units * ((max_entries + max_prefix + kAttnEntries - 1) / kAttnEntries);
   const bool copies = format == CSA_CACHE_BF16 && p.box_rows >= 8 && num_pages > 0 &&
-                      num_pages <= INT_MAX / page_size && (nc < 8 || most_tiles <= p.workers);
+                      num_pages <= INT_MAX / page_size && (nc < 8 || groups > 0 || most_tiles <= p.workers);
   // Packing first. Up to d = 256 a tile's time is the softmax's, so packing entries that can be copied
   // from the pages gains little (3 chunks of 1024 tokens x 64 heads of 256: 450 us packed, 471 not)
   // or loses (48 of 8 tokens: 205 and 165). Codes are widened once instead of by every unit (450 and
@@ -689,8 +738,11 @@ csa_status_t run_attn(const AttnCall& c, csa_stream_t stream) {
   // 232, of 512: 407 and 435). bf16 at d = 512: 256 rows 256 and 285, three chunks of 1024 tokens
   // 909 and 1382.
   const bool wide = format != CSA_CACHE_BF16 && d > 128;
-  const bool chunks = tile && chunked(p) && !(copies && nc < 8) &&
-                      tokens * p.group >= (wide ? kChunkRowsWide : kChunkRows) * (groups > 0 ? groups : S);
+  // Behind prefixes bf16 comes by copies at any d: the prefix's come from L2 (64 sequences of 64 heads of 512
+  // behind 16384 entries: 168 us, by threads 280, packed 246; 48 with up to 8000 own entries behind 128: 80,
+  // 111 and 150).
+  const bool chunks = tile && chunked(p) && (groups > 0 ? !copies : !(copies && nc < 8) &&
+                      tokens * p.group >= (wide ? kChunkRowsWide : kChunkRows) * S);
   // A unit's own cost (q in, output out, the pipeline's start) in tiles, by which shares are evened
   // out, measured best of 1 to 5 or 6. Packed: three chunks of 1024 tokens x 64 heads of 512 910 us (at 3
   // 945, at 5 987), of 256 450 (at 1 513, at 5 468); 48 of 64 tokens x 8 heads of 128 100 (at 1
@@ -701,6 +753,7 @@ csa_status_t run_attn(const AttnCall& c, csa_stream_t stream) {
   if (chunks) {
     p.unit_cost = nc == 8 ? 1 : nc == 4 ? 3 : 5;
   }
+  if (groups > 0) p.unit_cost = nc == 8 ? 2 : 3;
   p.q = static_cast<const uint16_t*>(q);
   p.cu = c.cu_seqlens;
   p.data = static_cast<const uint8_t*>(data);
@@ -727,11 +780,16 @@ csa_status_t run_attn(const AttnCall& c, csa_stream_t stream) {
   void* args[] = {&p};
   int dev = 0, bps = 0;
   if (note(cudaGetDevice(&dev)) != cudaSuccess) return CSA_ERR_CUDA;
-  const size_t plan_smem = sizeof(int) * (groups > 0 ? static_cast<size_t>(groups) + 1 + (S <= kPlanCached ? 3 * static_cast<size_t>(S) + 1 : 0)
+  const size_t plan_smem = sizeof(int) * (groups > 0 ? 3 * static_cast<size_t>(groups) + 2 + (S <= kPlanCached ? 3 * static_cast<size_t>(S) + 1 : 0)
                                                      : static_cast<size_t>(S) + 1);
   const void* plan = groups > 0 ? reinterpret_cast<const void*>(attn_prefix_plan_kernel) : reinterpret_cast<const void*>(attn_plan_kernel);
   if (blocks_per_sm(dev, plan, kPlanThreads, plan_smem, &bps) != cudaSuccess) return CSA_ERR_CUDA;
-  if (launch_pdl(plan, dim3(1), dim3(kPlanThreads), plan_smem, cs, args) != cudaSuccess) return CSA_ERR_CUDA;
+  // behind prefixes: a thread for each sequence that single tokens would have in 64 rows
+  const int per_block = kAttnRows % p.group == 0 ? kAttnRows / p.group : kAttnRows / p.group + 2;
+  int plan_lanes = 1;
+  while (plan_lanes < per_block && plan_lanes < 32) plan_lanes *= 2;
+  void* plan_args[] = {&p, &plan_lanes};
+  if (launch_pdl(plan, dim3(1), dim3(kPlanThreads), plan_smem, cs, plan_args) != cudaSuccess) return CSA_ERR_CUDA;
   if (tile) {
     CUtensorMap map{};
     int source = format;
@@ -758,13 +816,22 @@ csa_status_t run_attn(const AttnCall& c, csa_stream_t stream) {
     if (bps < 1) return CSA_ERR_UNSUPPORTED;
     if (chunks) {
       // a few blocks an SM, which go on to their sequence's next entries: the table's capacity may
-      // be far above what the sequences hold
-      const int64_t heads = static_cast<int64_t>(S + groups) * kv_heads;
-      const int64_t most = (groups > 0 && p.prefix_rows > p.packed_rows ? p.prefix_rows : p.packed_rows) / kPackRows;
-      const int64_t want = (16 * static_cast<int64_t>(sms) + heads - 1) / heads;
-      if (launch_pdl(pack, dim3(static_cast<unsigned>(want < most ? want : most), S + groups, kv_heads), dim3(kPackThreads), 0,
-                     cs, args) != cudaSuccess)
-        return CSA_ERR_CUDA;
+      // be far above what the sequences hold (behind prefixes a grid over all capacities, 33 thousand blocks for
+      // 64 sequences, took 46 us)
+      const int64_t heads = static_cast<int64_t>(S) * kv_heads, most = p.packed_rows / kPackRows;
+      int64_t want = (16 * static_cast<int64_t>(sms) + heads - 1) / heads;
+      want = want < most ? want : most;
+      dim3 grid(static_cast<unsigned>(want), S, kv_heads);
+      int prefix_blocks = 0;
+      if (groups > 0) {
+        const int64_t steps = static_cast<int64_t>(groups) * kv_heads * (p.prefix_rows / kPackRows);
+        prefix_blocks = static_cast<int>(steps < 8 * sms ? steps : 8 * sms);
+        want = (4 * static_cast<int64_t>(sms) + heads - 1) / heads;
+        want = want < most ? want : most;
+        grid = dim3(static_cast<unsigned>(prefix_blocks + want * heads));
+      }
+      void* pack_args[] = {&p, &prefix_blocks};
+      if (launch_pdl(pack, grid, dim3(kPackThreads), 0, cs, pack_args) != cudaSuccess) return CSA_ERR_CUDA;
     }
     void* targs[] = {&p, &map};
     if (launch_pdl(k, dim3(p.workers), dim3(threads), smem, cs, targs) != cudaSuccess)

@@ -399,7 +399,8 @@ struct SegmentWalk {
 };
 
 // The walk with what a tile's entries are: the unit's sequence, or behind prefixes the span that the
-// tile lies in, which enter() finds (tiles in order; some may be passed over).
+// tile lies in, which enter() finds (tiles in order; some may be passed over). (Spans and pages looked up a
+// span ahead took the same time.)
 template <bool PREFIX>
 struct TileWalk : SegmentWalk {
   __device__ __forceinline__ TileWalk(const AttnParams& pp, int worker) : SegmentWalk(pp, worker) {}
@@ -820,6 +821,7 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
   int par = 0;
   if (tid < kAttnEntries) sm.odd[tid] = 0;
   TileWalk<PREFIX> w(p, blockIdx.x);
+  bool idle = false;  // behind prefixes: the group's rows see nothing of the span
   int lim_at = 0;  // which of the two lists of limits holds: the unit's, or behind prefixes the span's
   if (w.valid()) {
     if (tid < kAttnRows) {
@@ -849,110 +851,121 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
         // have passed a barrier since the span before the last one)
         if (moved) {
           lim_at ^= 1;
-          if (quad == 0 && lane < kSoftCols) sm.lim[lim_at][c0 + lane] = span_limit(p, w.u, w.span, c0 + lane);
-          barrier_group();
+          // an own entry's sequence may have no row in this group: no weight then (some group has rows, and
+          // clears what is not finite)
+          idle = w.span.own != 0 && (c0 + kSoftCols <= w.span.row0 || c0 >= w.span.row1);
+          if (!idle) {
+            if (quad == 0 && lane < kSoftCols) sm.lim[lim_at][c0 + lane] = span_limit(p, w.u, w.span, c0 + lane);
+            barrier_group();
+          }
         }
       }
-      const int e = w.at(j) * kAttnEntries + e0;
-      const bool masked = (w.at(j) + 1) * static_cast<int64_t>(kAttnEntries) > w.seen_all();
-      const uint32_t s_at = lanes + SH::kTmemS + (t & 1u) * kAttnRows + c0;
-      tile_wait(sm, p, &sm.scores[t & 1u], (t >> 1) & 1u);
-      tc_fence_after();
-      float s[kSoftCols];
-      bool odd = false;  // some row of the tile does not see all of it, and a score of this entry is not finite
-      auto take = [&]() {
-        tmem_load16(s_at, s);
-        if (masked) {
+      const uint32_t row = base + SH::kPOff + e0 * 128;
+      if (PREFIX && idle) {
+        if (j > w.t0) tile_wait(sm, p, &sm.summed, (t - 1u) & 1u);  // (so the scores' barrier is not passed a lap ahead either)
 #pragma unroll
-          for (int c = 0; c < kSoftCols; ++c) {
-            odd = odd || !(fabsf(s[c]) <= 3.4028234e38f);
-            if (e >= sm.lim[lim_at][c0 + c]) s[c] = sl2 < 0.f ? INFINITY : -INFINITY;  // -inf once scaled
+        for (int c = 0; c < 2; ++c) sts128(row + (((group * 2 + c) ^ (e0 & 7)) << 4), make_uint4(0, 0, 0, 0));
+      } else {
+        const int e = w.at(j) * kAttnEntries + e0;
+        const bool masked = (w.at(j) + 1) * static_cast<int64_t>(kAttnEntries) > w.seen_all();
+        const uint32_t s_at = lanes + SH::kTmemS + (t & 1u) * kAttnRows + c0;
+        tile_wait(sm, p, &sm.scores[t & 1u], (t >> 1) & 1u);
+        tc_fence_after();
+        float s[kSoftCols];
+        bool odd = false;  // some row of the tile does not see all of it, and a score of this entry is not finite
+        auto take = [&]() {
+          tmem_load16(s_at, s);
+          if (masked) {
+#pragma unroll
+            for (int c = 0; c < kSoftCols; ++c) {
+              odd = odd || !(fabsf(s[c]) <= 3.4028234e38f);
+              if (e >= sm.lim[lim_at][c0 + c]) s[c] = sl2 < 0.f ? INFINITY : -INFINITY;  // -inf once scaled
+            }
           }
-        }
-      };
-      auto scale = [&]() {
+        };
+        auto scale = [&]() {
 #pragma unroll
-        for (int c = 0; c < kSoftCols; c += 4) {
-          const float4 m = *reinterpret_cast<const float4*>(&sm.m[c0 + c]);
-          s[c] = fmaf(s[c], sl2, -m.x);
-          s[c + 1] = fmaf(s[c + 1], sl2, -m.y);
-          s[c + 2] = fmaf(s[c + 2], sl2, -m.z);
-          s[c + 3] = fmaf(s[c + 3], sl2, -m.w);
-        }
-      };
-      take();
-      scale();
-      float top = fmaxf(s[0], s[1]);
-#pragma unroll
-      for (int c = 2; c < kSoftCols; c += 2) top = fmax3(top, s[c], s[c + 1]);
-      if (named_barrier_or(1 + group, 128, top > kRescaleAt)) {
-        // new bounds: the true maxima so far, rounded down. A score less its row's maximum is then what the
-        // rounding left, never below 0; far from zero (2^27 and more) that may pass any weight, and is
-        // cut off (a difference of one step of the fp32 score that it stands for).
-        take();
-        float mine = kNoMax;
-#pragma unroll
-        for (int c = 0; c < kSoftCols; ++c) {
-          const float v = warp_max_f32(__fmul_rd(s[c], sl2));
-          if (lane == c) mine = v;
-        }
-        if (lane < kSoftCols) sm.red[quad][c0 + lane] = mine;
-        barrier_group();
-        if (quad == 0 && lane < kSoftCols) {
-          const int c = c0 + lane;
-          const float old = sm.m[c];
-          float m = fmaxf(fmaxf(sm.red[0][c], sm.red[1][c]), fmaxf(sm.red[2][c], sm.red[3][c]));
-          m = fmaxf(old, m);
-          sm.fac[c] = fast_exp2(old - m);
-          sm.m[c] = m;
-        }
-        barrier_group();
-#pragma unroll
-        for (int c = 0; c < kSoftCols; ++c) l[c] *= sm.fac[c0 + c];
-        if (j > w.t0) {
-          tile_wait(sm, p, &sm.summed, (t - 1u) & 1u);
-          tc_fence_after();
-#pragma unroll 1
-          for (int b = 0; b < SH::kPairs; ++b) {
-            const uint32_t at = lanes + SH::kTmemO + b * kAttnRows + c0;
-            tmem_load16(at, s);
-#pragma unroll
-            for (int c = 0; c < kSoftCols; ++c) s[c] *= sm.fac[c0 + c];
-            tmem_store16(at, s);
+          for (int c = 0; c < kSoftCols; c += 4) {
+            const float4 m = *reinterpret_cast<const float4*>(&sm.m[c0 + c]);
+            s[c] = fmaf(s[c], sl2, -m.x);
+            s[c + 1] = fmaf(s[c + 1], sl2, -m.y);
+            s[c + 2] = fmaf(s[c + 2], sl2, -m.z);
+            s[c + 3] = fmaf(s[c + 3], sl2, -m.w);
           }
-        }
+        };
         take();
         scale();
+        float top = fmaxf(s[0], s[1]);
 #pragma unroll
-        for (int c = 0; c < kSoftCols; ++c) s[c] = min_nan(s[c], kRescaleAt);
-      }
-      // weights; their sums before rounding
-      uint32_t w2[kSoftCols / 2];
+        for (int c = 2; c < kSoftCols; c += 2) top = fmax3(top, s[c], s[c + 1]);
+        if (named_barrier_or(1 + group, 128, top > kRescaleAt)) {
+          // new bounds: the true maxima so far, rounded down. A score less its row's maximum is then what the
+          // rounding left, never below 0; far from zero (2^27 and more) that may pass any weight, and is
+          // cut off (a difference of one step of the fp32 score that it stands for).
+          take();
+          float mine = kNoMax;
 #pragma unroll
-      for (int c = 0; c < kSoftCols; c += 2) {
-        const float a = fast_exp2(s[c]), b = fast_exp2(s[c + 1]);
-        l[c] += a;
-        l[c + 1] += b;
-        w2[c / 2] = pack_bf16x2(a, b);
-      }
-      if (j > w.t0) tile_wait(sm, p, &sm.summed, (t - 1u) & 1u);  // P is free
-      const uint32_t row = base + SH::kPOff + e0 * 128;
+          for (int c = 0; c < kSoftCols; ++c) {
+            const float v = warp_max_f32(__fmul_rd(s[c], sl2));
+            if (lane == c) mine = v;
+          }
+          if (lane < kSoftCols) sm.red[quad][c0 + lane] = mine;
+          barrier_group();
+          if (quad == 0 && lane < kSoftCols) {
+            const int c = c0 + lane;
+            const float old = sm.m[c];
+            float m = fmaxf(fmaxf(sm.red[0][c], sm.red[1][c]), fmaxf(sm.red[2][c], sm.red[3][c]));
+            m = fmaxf(old, m);
+            sm.fac[c] = fast_exp2(old - m);
+            sm.m[c] = m;
+          }
+          barrier_group();
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
-        sts128(row + (((group * 2 + c) ^ (e0 & 7)) << 4), make_uint4(w2[4 * c], w2[4 * c + 1], w2[4 * c + 2], w2[4 * c + 3]));
-      if (masked && __any_sync(0xFFFFFFFFu, odd)) {
-        // 0 * NaN would reach the rows that do not see this entry: its non-finite values become 0, and the
-        // weights of the rows that see it (whose scores are not finite either) NaN
-        tmem_load16(s_at, s);
-        if (odd && clear_odd<NC>(sm, smem, t, e0))
+          for (int c = 0; c < kSoftCols; ++c) l[c] *= sm.fac[c0 + c];
+          if (j > w.t0) {
+            tile_wait(sm, p, &sm.summed, (t - 1u) & 1u);
+            tc_fence_after();
+#pragma unroll 1
+            for (int b = 0; b < SH::kPairs; ++b) {
+              const uint32_t at = lanes + SH::kTmemO + b * kAttnRows + c0;
+              tmem_load16(at, s);
 #pragma unroll
-          for (int c = 0; c < kSoftCols; ++c)
-            if (e < sm.lim[lim_at][c0 + c] && !(fabsf(s[c]) <= 3.4028234e38f)) {
-              l[c] = __uint_as_float(0x7FFFFFFFu);
-              asm volatile("st.shared.b16 [%0], %1;" ::"r"(row + (((group * 2 + (c >> 3)) ^ (e0 & 7)) << 4) + 2 * (c & 7)),
-                           "h"(static_cast<uint16_t>(0x7FFF))
-                           : "memory");
+              for (int c = 0; c < kSoftCols; ++c) s[c] *= sm.fac[c0 + c];
+              tmem_store16(at, s);
             }
+          }
+          take();
+          scale();
+#pragma unroll
+          for (int c = 0; c < kSoftCols; ++c) s[c] = min_nan(s[c], kRescaleAt);
+        }
+        // weights; their sums before rounding
+        uint32_t w2[kSoftCols / 2];
+#pragma unroll
+        for (int c = 0; c < kSoftCols; c += 2) {
+          const float a = fast_exp2(s[c]), b = fast_exp2(s[c + 1]);
+          l[c] += a;
+          l[c + 1] += b;
+          w2[c / 2] = pack_bf16x2(a, b);
+        }
+        if (j > w.t0) tile_wait(sm, p, &sm.summed, (t - 1u) & 1u);  // P is free
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          sts128(row + (((group * 2 + c) ^ (e0 & 7)) << 4), make_uint4(w2[4 * c], w2[4 * c + 1], w2[4 * c + 2], w2[4 * c + 3]));
+        if (masked && __any_sync(0xFFFFFFFFu, odd)) {
+          // 0 * NaN would reach the rows that do not see this entry: its non-finite values become 0, and the
+          // weights of the rows that see it (whose scores are not finite either) NaN
+          tmem_load16(s_at, s);
+          if (odd && clear_odd<NC>(sm, smem, t, e0))
+#pragma unroll
+            for (int c = 0; c < kSoftCols; ++c)
+              if (e < sm.lim[lim_at][c0 + c] && !(fabsf(s[c]) <= 3.4028234e38f)) {
+                l[c] = __uint_as_float(0x7FFFFFFFu);
+                asm volatile("st.shared.b16 [%0], %1;" ::"r"(row + (((group * 2 + (c >> 3)) ^ (e0 & 7)) << 4) + 2 * (c & 7)),
+                             "h"(static_cast<uint16_t>(0x7FFF))
+                             : "memory");
+              }
+        }
       }
       fence_proxy_async_smem();
       tc_fence_before();
@@ -1085,47 +1098,17 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
 // multiple of 128 rows and of 64 NC columns, so that the tile kernel's copies are whole boxes
 // whatever the format, the page size and the heads. Every unit of the sequence (one per 64
 // rows) reads them again; packing reads and writes them once. Block (x, s, cache head): 32
-// entries at a time, a thread 8 columns at a time.
+// entries at a time, a thread 8 columns at a time. Behind prefixes a row of blocks: prefix_blocks for all
+// prefixes, then the same number for each sequence and cache head.
 constexpr int kPackThreads = 256, kPackRows = 32;
 template <int NC, int FORMAT, bool PREFIX>
-__global__ void __launch_bounds__(kPackThreads) attn_pack_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(kPackThreads) attn_pack_kernel(const __grid_constant__ AttnParams p, int prefix_blocks) {
   constexpr int kPer = NC * 8;  // pieces of 8 columns
   pdl_wait();
   if (p.head->status != 0) return;
-  const int kvh = blockIdx.z;
-  const int32_t* table;
-  int64_t row0;  // of the run's first entry
-  int n;
-  if (PREFIX && static_cast<int>(blockIdx.y) < p.groups) {
-    const int g = blockIdx.y;
-    if (__ldg(p.cu + __ldg(p.prefix_seqs + g + 1)) == __ldg(p.cu + __ldg(p.prefix_seqs + g))) return;
-    n = __ldg(p.prefix_entries + g);
-    table = p.prefix_table + static_cast<int64_t>(g) * p.max_prefix_pages;
-    row0 = (static_cast<int64_t>(g) * p.kv_heads + kvh) * p.prefix_rows;
-  } else {
-    const int seq = blockIdx.y - (PREFIX ? p.groups : 0);
-    const int rows = sequence_rows(p, seq);
-    if (rows == 0) return;
-    int before = 0;
-    if constexpr (PREFIX) {
-      int lo = 0, hi = p.groups;  // the sequence's group
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (__ldg(p.prefix_seqs + mid) <= seq) lo = mid;
-        else hi = mid;
-      }
-      before = __ldg(p.prefix_entries + lo);
-    }
-    const int64_t first = p.first != nullptr ? __ldg(p.first + seq) : 0;
-    n = max(0, visible(first + rows / p.group - 1, p.ratio, before + __ldg(p.entries + seq)) - before);
-    table = p.table + static_cast<int64_t>(seq) * p.max_pages;
-    row0 = (static_cast<int64_t>(seq) * p.kv_heads + kvh) * p.packed_rows + static_cast<int64_t>(PREFIX ? p.groups : 0) * p.kv_heads * p.prefix_rows;
-    if (PREFIX && n == 0) return;
-  }
-  const int end = max(kAttnEntries, (n + kAttnEntries - 1) / kAttnEntries * kAttnEntries);
-  uint16_t* all = p.packed + row0 * (NC * 64);
-  for (int e0 = blockIdx.x * kPackRows; e0 < end; e0 += gridDim.x * kPackRows) {
-    uint16_t* to = all + static_cast<int64_t>(e0) * (NC * 64);
+  // 32 entries from e0 on of a run of n, whose first lies in row row0 of the packed ones
+  auto pack = [&](const int32_t* table, int64_t row0, int kvh, int n, int e0) {
+    uint16_t* to = p.packed + (row0 + e0) * (NC * 64);
 #pragma unroll 4
     for (int i = threadIdx.x; i < kPackRows * kPer; i += kPackThreads) {
       const int r = i / kPer, col = (i % kPer) * 8, e = e0 + r;
@@ -1151,7 +1134,48 @@ __global__ void __launch_bounds__(kPackThreads) attn_pack_kernel(const __grid_co
       }
       *reinterpret_cast<uint4*>(to + r * (NC * 64) + col) = v;
     }
+  };
+  auto rows_of = [](int n) { return max(kAttnEntries, (n + kAttnEntries - 1) / kAttnEntries * kAttnEntries); };
+  int seq = blockIdx.y, kvh = blockIdx.z, x = blockIdx.x, wide = gridDim.x;
+  if (PREFIX && x < prefix_blocks) {
+    // all prefixes and cache heads, in steps of 32 entries of the table's capacity, over the first blocks
+    const int steps = p.prefix_rows / kPackRows;
+    for (int64_t i = x; i < static_cast<int64_t>(p.groups) * p.kv_heads * steps; i += prefix_blocks) {
+      const int part = static_cast<int>(i / steps), e0 = static_cast<int>(i - static_cast<int64_t>(part) * steps) * kPackRows;
+      const int g = part / p.kv_heads, n = __ldg(p.prefix_entries + g);
+      if (e0 >= rows_of(n) || __ldg(p.cu + __ldg(p.prefix_seqs + g + 1)) == __ldg(p.cu + __ldg(p.prefix_seqs + g))) continue;
+      pack(p.prefix_table + static_cast<int64_t>(g) * p.max_prefix_pages, static_cast<int64_t>(part) * p.prefix_rows,
+           part - g * p.kv_heads, n, e0);
+    }
+    return;
   }
+  if constexpr (PREFIX) {  // a sequence's cache heads: as many blocks each as there are room for
+    wide = (gridDim.x - prefix_blocks) / (p.S * p.kv_heads);
+    const int part = (x - prefix_blocks) / wide;
+    x = (x - prefix_blocks) - part * wide;
+    seq = part / p.kv_heads;
+    kvh = part - seq * p.kv_heads;
+  }
+  const int rows = sequence_rows(p, seq);
+  if (rows == 0) return;
+  int before = 0;
+  if constexpr (PREFIX) {
+    int lo = 0, hi = p.groups;  // the sequence's group
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (__ldg(p.prefix_seqs + mid) <= seq) lo = mid;
+      else hi = mid;
+    }
+    before = __ldg(p.prefix_entries + lo);
+  }
+  const int64_t first = p.first != nullptr ? __ldg(p.first + seq) : 0;
+  const int n = max(0, visible(first + rows / p.group - 1, p.ratio, before + __ldg(p.entries + seq)) - before);
+  if (PREFIX && n == 0) return;
+  const int64_t row0 = (static_cast<int64_t>(seq) * p.kv_heads + kvh) * p.packed_rows +
+                       (PREFIX ? static_cast<int64_t>(p.groups) * p.kv_heads * p.prefix_rows : 0);
+  const int end = rows_of(n);
+  for (int e0 = x * kPackRows; e0 < end; e0 += wide * kPackRows)
+    pack(p.table + static_cast<int64_t>(seq) * p.max_pages, row0, kvh, n, e0);
 }
 
 template <int NC, int SRC, bool PREFIX>
@@ -1179,6 +1203,12 @@ __global__ void __launch_bounds__(TileCta<SRC>::kThreads, 1)
     mbar_init(&sm.drain, 1);
     sm.stop = 0;
     fence_mbar_init();
+  }
+  if constexpr (SRC == kFromBoxes) {
+    // rows that no box covers count as seen by nobody, but what shared memory holds of other kernels may look
+    // like infinities and NaN, which the softmax warps would have to clear one by one (7 us a tile)
+    for (uint32_t at = threadIdx.x * 16; at < SH::kRing * kPairBytes; at += CTA::kThreads * 16) sts128(base + at, make_uint4(0, 0, 0, 0));
+    fence_proxy_async_smem();
   }
   tc_fence_before();
   __syncthreads();
