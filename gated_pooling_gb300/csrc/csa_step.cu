@@ -21,7 +21,7 @@ namespace csa {
 namespace {
 
 constexpr int kStepThreads = 256;
-constexpr int kStepFlight = 8;  // (kv, score) pieces of a thread under way
+constexpr int kStepFlight = 8;  // (kv, score) pieces that a thread loads at a time
 
 struct StepParams {
   const uint16_t* kv;
@@ -43,34 +43,33 @@ struct StepParams {
   int64_t capacity, out_rows, num_states;
   int S, ratio, coff, d, C, W;
   int max_pages, page_size, offset;
-  int R;      // CTAs of a column slice
-  int CL;     // pieces of a slice
-  int PG;     // threads that share a window's positions
-  int RS;     // windows that a CTA works on at once
-  int chunks; // pieces of a row
+  int R;       // CTAs of a column slice
+  int CL;      // pieces of a slice
+  int PG;      // threads that share a window's positions
+  int RS;      // windows that a CTA works on at once
+  int chunks;  // pieces of a row
 };
 
-// VEC consecutive bf16 values (8: 16 bytes, aligned).
+// VEC consecutive bf16 values (4: 8 bytes, aligned), read once.
 template <int VEC>
 struct Piece;
 template <>
-struct Piece<8> {
-  uint4 w;
-  // evict-first where nothing reads them again
-  __device__ __forceinline__ void load_once(const uint16_t* p) {
-    asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "l"(p));
+struct Piece<4> {
+  uint2 w;
+  __device__ __forceinline__ void load(const uint16_t* p) {
+    asm volatile("ld.global.cs.v2.u32 {%0, %1}, [%2];" : "=r"(w.x), "=r"(w.y) : "l"(p));
   }
-  __device__ __forceinline__ void store(uint16_t* p) const { *reinterpret_cast<uint4*>(p) = w; }
-  __device__ __forceinline__ void clear() { w = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void store(uint16_t* p) const { *reinterpret_cast<uint2*>(p) = w; }
+  __device__ __forceinline__ void clear() { w = make_uint2(0, 0); }
   __device__ __forceinline__ float get(int i) const {
-    const uint32_t x = i < 2 ? w.x : i < 4 ? w.y : i < 6 ? w.z : w.w;
+    const uint32_t x = i < 2 ? w.x : w.y;
     return i % 2 == 0 ? bf16_lo(x) : bf16_hi(x);
   }
 };
 template <>
 struct Piece<1> {
   uint16_t w;
-  __device__ __forceinline__ void load_once(const uint16_t* p) {
+  __device__ __forceinline__ void load(const uint16_t* p) {
     asm volatile("ld.global.cs.u16 %0, [%1];" : "=h"(w) : "l"(p));
   }
   __device__ __forceinline__ void store(uint16_t* p) const { *p = w; }
@@ -79,8 +78,10 @@ struct Piece<1> {
 };
 template <int VEC>
 __device__ __forceinline__ void load_embedding(float (&a)[VEC], const float* p) {
-  if constexpr (VEC > 1) {
-    load_ape<VEC>(a, p);
+  if constexpr (VEC == 2) {
+    const float2 t = __ldg(reinterpret_cast<const float2*>(p));
+    a[0] = t.x;
+    a[1] = t.y;
   } else {
     a[0] = __ldg(p);
   }
@@ -91,7 +92,7 @@ struct StepSeq {
   int n, first, source, target;
   int64_t token0;  // where position 0 would lie among the call's tokens
   int lo, hi;      // blocks complete before the call, and after it
-  int boundary;    // completed ones whose window reaches into the state
+  int boundary;    // of those that it completes, the ones whose window reaches into the state
   __device__ __forceinline__ StepSeq(const StepParams& p, int s) {
     const int a = __ldg(p.cu + s);
     n = __ldg(p.cu + s + 1) - a;
@@ -101,245 +102,230 @@ struct StepSeq {
     token0 = static_cast<int64_t>(a) - first;
     lo = first / p.ratio;
     hi = (first + n) / p.ratio;
-    const bool part = first % p.ratio != 0;
-    boundary = min(hi - lo, p.coff == 1 ? (part ? 1 : 0) : part ? 2 : lo > 0 ? 1 : 0);
+    boundary = boundary_of(p, first, lo, hi - lo);
+  }
+  static __device__ __forceinline__ int boundary_of(const StepParams& p, int first, int lo, int made) {
+    const bool part = first != lo * p.ratio;
+    return min(made, p.coff == 1 ? (part ? 1 : 0) : part ? 2 : lo > 0 ? 1 : 0);
   }
 };
 
-// Rows before each sequence in shared memory, sB[S] = all, as build_block_prefix does for whole segments; -1
-// with the reason reported where the call's numbers are refused. Every thread of the block calls it.
-__device__ int build_step_prefix(const StepParams& p, int* sB, int* warp_sums) {
+// Rows before each sequence (x), and those of them whose windows reach into no state (y), in shared memory, [S]
+// holding all of them; false with the reason reported where the call's numbers are refused. Every thread of the
+// block calls it.
+__device__ bool build_step_prefix(const StepParams& p, int2* sB, int* warp_sums) {
   pdl_wait();
-  int carry = 0, bad = 0;
-  if (threadIdx.x == 0 && (__ldg(p.cu) < 0 || __ldg(p.cu + p.S) > p.capacity)) bad = 1;
-  for (int base = 0; base < p.S; base += blockDim.x) {
+  int2 carry = make_int2(0, 0);
+  int bad = 0;
+  for (int base = 0; base < p.S || base == 0; base += blockDim.x) {
     const int s = base + threadIdx.x;
-    int made = 0;
+    int made = 0, inner = 0;
     if (s < p.S) {
-      const int n = __ldg(p.cu + s + 1) - __ldg(p.cu + s), f = __ldg(p.first + s);
-      const int from = __ldg(p.source + s), to = __ldg(p.target + s);
-      const bool live = f % p.ratio != 0 || (p.coff == 2 && f >= p.ratio);  // the state holds something
-      if (n < 0) {
+      const int a = __ldg(p.cu + s), b = __ldg(p.cu + s + 1), f = __ldg(p.first + s);
+      const int from = __ldg(p.source + s), to = __ldg(p.target + s), n = b - a, lo = f / p.ratio;
+      const bool live = f != lo * p.ratio || (p.coff == 2 && lo > 0);  // the state holds something
+      if (b < a || a < 0 || b > p.capacity) {
         bad |= 1;
       } else if (f < 0 || f > INT_MAX - n || from >= p.num_states || to >= p.num_states ||
                  (from < 0 && live && (n > 0 || to >= 0))) {
         bad |= 2;
       } else {
-        made = (f + n) / p.ratio - f / p.ratio;
+        made = (f + n) / p.ratio - lo;
+        inner = made - StepSeq::boundary_of(p, f, lo, made);
       }
     }
-    int total;
-    const int before = block_exclusive_scan(made, warp_sums, total);
-    if (s < p.S) sB[s] = carry + before;
-    carry += total;
+    int all, all_inner = 0;
+    const int before = block_exclusive_scan(made, warp_sums, all);
+    // (a call of single tokens has no such row)
+    const int inner_before = __syncthreads_or(inner) ? block_exclusive_scan(inner, warp_sums, all_inner) : 0;
+    if (s < p.S) sB[s] = make_int2(carry.x + before, carry.y + inner_before);
+    carry.x += all;
+    carry.y += all_inner;
   }
   if (threadIdx.x == 0) sB[p.S] = carry;
   int code = 0;
-  if (__syncthreads_or(bad & 1)) code = CSA_DEVERR_CU_SEQLENS;
-  else if (__syncthreads_or(bad & 2)) code = CSA_DEVERR_STATE;
-  else if (carry > p.out_rows) code = CSA_DEVERR_OUT_ROWS;
+  if (__syncthreads_or(bad)) code = __syncthreads_or(bad & 1) ? CSA_DEVERR_CU_SEQLENS : CSA_DEVERR_STATE;
+  else if (carry.x > p.out_rows) code = CSA_DEVERR_OUT_ROWS;
   if (code != 0) {
     if (threadIdx.x == 0 && p.dev_error != nullptr) *reinterpret_cast<volatile int32_t*>(p.dev_error) = code;
-    return -1;
+    return false;
   }
-  return carry;
+  return true;
 }
 
-// A block of a sequence whose window a thread works on.
-struct StepRow {
-  int64_t token0;  // as in StepSeq
-  int64_t state;   // first element of the state that it goes on from
-  int first, block, row;
-  bool on;
-};
+// Where row o's entry goes.
+__device__ __forceinline__ void describe_row(const StepParams& p, const int2* sB, int o) {
+  int s = 0, h = p.S;  // sB[s].x <= o < sB[h].x, the last such s
+  while (h - s > 1) {
+    const int mid = (s + h) / 2;
+    if (sB[mid].x <= o) s = mid;
+    else h = mid;
+  }
+  const int block = __ldg(p.first + s) / p.ratio + (o - sB[s].x);
+  if (p.positions != nullptr) p.positions[o] = block * p.ratio + p.offset;
+  if (p.slots != nullptr) {
+    const int e = block - (p.base != nullptr ? __ldg(p.base + s) : 0);
+    int64_t slot = -1;
+    if (e >= 0) {
+      const int at = e / p.page_size;
+      const int page = at < p.max_pages ? __ldg(p.table + static_cast<int64_t>(s) * p.max_pages + at) : -1;
+      if (page >= 0) slot = static_cast<int64_t>(page) * p.page_size + (e - at * p.page_size);
+      else if (p.dev_error != nullptr) *p.dev_error = CSA_DEVERR_PAGE;
+    }
+    p.slots[o] = slot;
+  }
+}
 
-// UW: positions of a window that a thread has under way at once; windows of up to 4 positions go
-// through a thread several at a time instead, so that as many bytes are under way. SPLIT: windows of more
-// than 8 positions, which PG threads share.
+// UW: positions of a window that a thread takes; windows of up to 4 positions go through a thread several at a
+// time instead (K rows), so that as many bytes are under way. SPLIT: windows of more than 8 positions, which
+// PG threads share. The next rows' pieces are loaded while one is worked out.
 template <int VEC, int UW, bool SPLIT>
 __global__ void __launch_bounds__(kStepThreads, 2) step_kernel(const __grid_constant__ StepParams p) {
-  constexpr int K = kStepFlight / UW, PART = VEC == 8 ? 4 : 1;
-  extern __shared__ __align__(16) int s_prefix[];  // [S + 1]
+  constexpr int K = kStepFlight / UW, PART = VEC == 4 ? 2 : 1;
+  extern __shared__ __align__(16) int2 s_prefix[];  // [S + 1]
   __shared__ int warp_sums[32];
-  __shared__ __align__(16) float s_part[SPLIT ? 3 * kStepThreads * VEC : 4];
-  const int total = build_step_prefix(p, s_prefix, warp_sums);
-  if (total < 0) return;
+  __shared__ __align__(16) float s_part[SPLIT ? 2 : 1][SPLIT ? 3 * kStepThreads * VEC : 4];
+  if (!build_step_prefix(p, s_prefix, warp_sums)) return;
   const int g = blockIdx.x, tid = threadIdx.x, per = p.CL * p.PG;
   const int rs = tid / per, pg = tid % per / p.CL, cl = tid % p.CL;
-  const int chunk = blockIdx.y * p.CL + cl;
-  const bool mine = rs < p.RS && chunk < p.chunks;  // this thread has columns
-  const int c0 = chunk * VEC;
-  const bool scribe = rs < p.RS && pg == 0 && chunk == 0;  // it writes a row's position and slot
+  const int chunk = blockIdx.y * p.CL + cl, c0 = chunk * VEC;
+  const bool slot = rs < p.RS, mine = slot && chunk < p.chunks;  // this thread has a window, and columns
+  const int total = s_prefix[p.S].x, inner = s_prefix[p.S].y;
 
-  if (blockIdx.y == 0)  // rows behind the last one
-    for (int64_t o = total + static_cast<int64_t>(g) * kStepThreads + tid; o < p.out_rows;
-         o += static_cast<int64_t>(p.R) * kStepThreads) {
-      if (p.positions != nullptr) p.positions[o] = -1;
-      if (p.slots != nullptr) p.slots[o] = -1;
-    }
+  // This thread's positions: elements from the block's first one (own columns), the embedding's the same way
+  const bool two = p.coff == 2;
+  int off[UW];
+  uint32_t there = 0, own = 0;  // bits: the window has this position, the block itself has
+#pragma unroll
+  for (int u = 0; u < UW; ++u) {
+    const int w = pg + u * p.PG;
+    const bool prev = two && w < p.ratio;
+    off[u] = prev ? (w - p.ratio) * p.C - p.d : (two ? w - p.ratio : w) * p.C;
+    if (mine && w < p.W) there |= 1u << u;
+    if (!prev) own |= 1u << u;
+  }
+  const float* const ape_own = p.ape + (two ? p.d : 0) + c0;
+  const float* const ape_prev = ape_own + static_cast<int64_t>(p.ratio) * p.C;
 
-  auto describe = [&](int s, const StepRow& r) {
-    if (!scribe || !r.on) return;
-    if (p.positions != nullptr) p.positions[r.row] = r.block * p.ratio + p.offset;
-    if (p.slots != nullptr) {
-      const int e = r.block - (p.base != nullptr ? __ldg(p.base + s) : 0);
-      int64_t slot = -1;
-      if (e >= 0) {
-        const int at = e / p.page_size;
-        const int page = at < p.max_pages ? __ldg(p.table + static_cast<int64_t>(s) * p.max_pages + at) : -1;
-        if (page >= 0) slot = static_cast<int64_t>(page) * p.page_size + e % p.page_size;
-        else if (p.dev_error != nullptr) *p.dev_error = CSA_DEVERR_PAGE;
-      }
-      p.slots[r.row] = slot;
-    }
+  struct Pieces {
+    Piece<VEC> kv[UW], score[UW];
+    uint32_t on;  // positions that are there
+    int row;      // -1: none
   };
-
-  // one window's (kv, score) pieces under way, for the positions w0, w0 + PG, ...: those at once of N rows
-  auto pool = [&](auto count, const StepRow* rows) {
-    constexpr int N = decltype(count)::value;
-    float m[SPLIT ? VEC : 1], z[SPLIT ? VEC : 1], a[SPLIT ? VEC : 1];
-    if constexpr (SPLIT) {
+  // maximum, weight sum and weighted sum of this thread's positions, to the row or to the threads that share it
+  auto finish = [&](const Pieces& v, int turn) {
+    if (!SPLIT && v.row < 0) return;
+    if (mine) {
+      float top[VEC], z[VEC], a[VEC];
+      // (two columns at a time, for the registers)
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        m[i] = -INFINITY;
-        z[i] = a[i] = 0.f;
-      }
-    }
-    for (int w0 = pg; w0 < p.W; w0 += UW * p.PG) {
-      Piece<VEC> kv[N][UW], sc[N][UW];
-      uint32_t on[N];  // positions that are there, a bit each
+      for (int part = 0; part < VEC / PART; ++part) {
+        float x[UW][PART];
 #pragma unroll
-      for (int k = 0; k < N; ++k) {
-        on[k] = 0;
+        for (int i = 0; i < PART; ++i) top[part * PART + i] = -INFINITY;
 #pragma unroll
         for (int u = 0; u < UW; ++u) {
-          const int w = w0 + u * p.PG;
-          const bool prev = p.coff == 2 && w < p.ratio;
-          const int at = prev || p.coff == 1 ? w : w - p.ratio;
-          const int pos = (rows[k].block - (prev ? 1 : 0)) * p.ratio + at;
-          kv[k][u].clear();
-          sc[k][u].clear();
-          if (mine && rows[k].on && w < p.W && pos >= 0) {
-            on[k] |= 1u << u;
-            const bool old = pos < rows[k].first;
-            const int64_t off = (old ? rows[k].state + static_cast<int64_t>(pos % p.W) * p.C : (rows[k].token0 + pos) * p.C) +
-                                (prev || p.coff == 1 ? 0 : p.d) + c0;
-            kv[k][u].load_once((old ? p.kv_state : p.kv) + off);
-            sc[k][u].load_once((old ? p.score_state : p.score) + off);
+          float e[PART];
+#pragma unroll
+          for (int i = 0; i < PART; ++i) e[i] = 0.f;
+          if (there >> u & 1u) load_embedding<PART>(e, (own >> u & 1u ? ape_own : ape_prev) + off[u] + part * PART);
+#pragma unroll
+          for (int i = 0; i < PART; ++i) {
+            x[u][i] = v.on >> u & 1u ? fmaf(v.score[u].get(part * PART + i), kLog2e, e[i] * kLog2e) : -INFINITY;
+            top[part * PART + i] = fmaxf(top[part * PART + i], x[u][i]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < PART; ++i) {
+          const int c = part * PART + i;
+          const float to = top[c] == -INFINITY ? 0.f : top[c];  // (scores of -inf alone weigh nothing)
+          z[c] = a[c] = 0.f;
+#pragma unroll
+          for (int u = 0; u < UW; ++u) {
+            const float f = fast_exp2(x[u][i] - to);
+            z[c] += f;
+            a[c] = fmaf(f, v.kv[u].get(c), a[c]);
           }
         }
       }
-      if (!mine) continue;
-      // PART columns of a row at a time
+      if constexpr (SPLIT) {
+        const int wide = p.CL * VEC, step = p.PG * wide;
+        float* to = s_part[turn & 1] + rs * 3 * step + (pg * p.CL + cl) * VEC;
 #pragma unroll
-      for (int k = 0; k < N; ++k) {
-        if (on[k] == 0 && (SPLIT || !rows[k].on)) continue;
-        uint32_t y[VEC / 2 > 0 ? VEC / 2 : 1];
-#pragma unroll
-        for (int part = 0; part < VEC / PART; ++part) {
-          float x[UW][PART];
-          float top[PART], zz[PART], aa[PART];
-#pragma unroll
-          for (int i = 0; i < PART; ++i) top[i] = -INFINITY;
-#pragma unroll
-          for (int u = 0; u < UW; ++u) {
-            const int w = w0 + u * p.PG;
-            const bool own = p.coff == 2 && w >= p.ratio;
-            float e[PART];
-#pragma unroll
-            for (int i = 0; i < PART; ++i) e[i] = 0.f;
-            if (w < p.W) load_embedding<PART>(e, p.ape + static_cast<int64_t>(own ? w - p.ratio : w) * p.C + (own ? p.d : 0) + c0 + part * PART);
-#pragma unroll
-            for (int i = 0; i < PART; ++i) {
-              x[u][i] = on[k] >> u & 1u ? fmaf(sc[k][u].get(part * PART + i), kLog2e, e[i] * kLog2e) : -INFINITY;
-              top[i] = fmaxf(top[i], x[u][i]);
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < PART; ++i) {
-            // (while all scores are -inf their weights are 0)
-            const float to = top[i] == -INFINITY ? 0.f : top[i];
-            zz[i] = aa[i] = 0.f;
-#pragma unroll
-            for (int u = 0; u < UW; ++u) {
-              const float f = fast_exp2(x[u][i] - to);
-              zz[i] += f;
-              aa[i] = fmaf(f, kv[k][u].get(part * PART + i), aa[i]);
-            }
-          }
-          if constexpr (SPLIT) {
-#pragma unroll
-            for (int i = 0; i < PART; ++i) {
-              const int c = part * PART + i;
-              if (w0 == pg) {
-                m[c] = top[i];
-                z[c] = zz[i];
-                a[c] = aa[i];
-              } else {
-                const float both = fmaxf(m[c], top[i]), to = both == -INFINITY ? 0.f : both;
-                const float f = fast_exp2(m[c] - to), g2 = fast_exp2(top[i] - to);
-                m[c] = both;
-                z[c] = z[c] * f + zz[i] * g2;
-                a[c] = a[c] * f + aa[i] * g2;
-              }
-            }
-          } else if constexpr (VEC == 1) {
-            p.out[static_cast<int64_t>(rows[k].row) * p.d + c0] = Element<CSA_DTYPE_BF16>::from_float(aa[0] / zz[0]);
-          } else {
-#pragma unroll
-            for (int i = 0; i < PART; i += 2) y[(part * PART + i) / 2] = pack_bf16x2(aa[i] * rcp_nr(zz[i]), aa[i + 1] * rcp_nr(zz[i + 1]));
-          }
+        for (int i = 0; i < VEC; ++i) {
+          to[i] = top[i];
+          to[step + i] = z[i];
+          to[2 * step + i] = a[i];
         }
-        if constexpr (!SPLIT && VEC == 8)
-          *reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(rows[k].row) * p.d + c0) = make_uint4(y[0], y[1], y[2], y[3]);
+      } else {
+        uint16_t* to = p.out + static_cast<int64_t>(v.row) * p.d + c0;
+        if constexpr (VEC == 4) {
+          *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(a[0] * rcp_nr(z[0]), a[1] * rcp_nr(z[1])),
+                                                     pack_bf16x2(a[2] * rcp_nr(z[2]), a[3] * rcp_nr(z[3])));
+        } else {
+          *to = Element<CSA_DTYPE_BF16>::from_float(a[0] * rcp_nr(z[0]));
+        }
       }
     }
     if constexpr (SPLIT) {
-      // (N is 1) the position groups' parts meet in shared memory, a column to a thread, in their order
-      const int wide = p.CL * VEC;
-      float* part = s_part + static_cast<size_t>(rs) * 3 * p.PG * wide;
-      if (rs < p.RS) {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          float* to = part + (pg * p.CL + cl) * VEC + i;
-          to[0] = m[i];
-          to[p.PG * wide] = z[i];
-          to[2 * p.PG * wide] = a[i];
-        }
-      }
+      // the parts meet in shared memory, a column to a thread, in the positions' order (two turns' parts, so
+      // that one barrier a row is enough)
       __syncthreads();
-      if (rs < p.RS && rows[0].on) {
+      if (slot && v.row >= 0) {
+        const int wide = p.CL * VEC, step = p.PG * wide;
+        const float* part = s_part[turn & 1] + rs * 3 * step;
         for (int c = tid % per; c < wide; c += per) {
           const int col = blockIdx.y * wide + c;
           if (col >= p.d) break;
-          float top = -INFINITY, zz = 0.f, aa = 0.f;
-          for (int q = 0; q < p.PG; ++q) top = fmaxf(top, part[q * wide + c]);
-          const float to = top == -INFINITY ? 0.f : top;
+          float m = -INFINITY, zz = 0.f, aa = 0.f;
+#pragma unroll 8
+          for (int q = 0; q < p.PG; ++q) m = fmaxf(m, part[q * wide + c]);
+          const float to = m == -INFINITY ? 0.f : m;
+#pragma unroll 8
           for (int q = 0; q < p.PG; ++q) {
             const float f = fast_exp2(part[q * wide + c] - to);
-            zz = fmaf(part[(p.PG + q) * wide + c], f, zz);
-            aa = fmaf(part[(2 * p.PG + q) * wide + c], f, aa);
+            zz = fmaf(part[step + q * wide + c], f, zz);
+            aa = fmaf(part[2 * step + q * wide + c], f, aa);
           }
-          p.out[static_cast<int64_t>(rows[0].row) * p.d + col] = Element<CSA_DTYPE_BF16>::from_float(aa / zz);
+          p.out[static_cast<int64_t>(v.row) * p.d + col] = Element<CSA_DTYPE_BF16>::from_float(aa * rcp_nr(zz));
         }
       }
-      __syncthreads();
     }
   };
 
   // sequences: the blocks that reach into the state, then the state
   const int64_t state = static_cast<int64_t>(p.W) * p.C;
+  int turn = 0;
   for (int s0 = g * p.RS; s0 < p.S; s0 += p.R * p.RS) {
     const int s = s0 + rs;
-    const bool some = rs < p.RS && s < p.S;
+    const bool some = slot && s < p.S;
     const StepSeq q(p, some ? s : s0);
+#pragma unroll 1
     for (int i = 0; i < p.coff; ++i) {
-      const StepRow r{q.token0, q.source * state, q.first, q.lo + i, s_prefix[some ? s : s0] + i, some && i < q.boundary};
-      pool(std::integral_constant<int, 1>{}, &r);
-      describe(s, r);
+      const bool now = some && i < q.boundary;
+      if (SPLIT ? !__syncthreads_or(now) : !now) continue;
+      Pieces v;
+      v.on = 0;
+      v.row = now ? s_prefix[s].x + i : -1;
+#pragma unroll
+      for (int u = 0; u < UW; ++u) {
+        v.kv[u].clear();
+        v.score[u].clear();
+        const int w = pg + u * p.PG;
+        const int pos = (q.lo + i - (two ? 1 : 0)) * p.ratio + w;
+        if (now && (there >> u & 1u) && pos >= 0) {
+          v.on |= 1u << u;
+          const bool old = pos < q.first;
+          const int64_t at = (old ? q.source * state + static_cast<int64_t>(pos % p.W) * p.C : (q.token0 + pos) * p.C) +
+                             (two && (own >> u & 1u) ? p.d : 0) + c0;
+          v.kv[u].load((old ? p.kv_state : p.kv) + at);
+          v.score[u].load((old ? p.score_state : p.score) + at);
+        }
+      }
+      finish(v, turn++);
     }
     if (!some) continue;
-    if (scribe && p.entries != nullptr) p.entries[s] = max(0, q.hi - (p.base != nullptr ? __ldg(p.base + s) : 0));
+    if (chunk == 0 && pg == 0 && p.entries != nullptr) p.entries[s] = max(0, q.hi - (p.base != nullptr ? __ldg(p.base + s) : 0));
     if (!mine || q.target < 0) continue;
     asm volatile("" ::: "memory");  // the state is read above, by loads that the compiler does not see as such
     for (int half = 0; half < p.coff; ++half) {
@@ -350,41 +336,80 @@ __global__ void __launch_bounds__(kStepThreads, 2) step_kernel(const __grid_cons
         const int64_t at = static_cast<int64_t>(pos % p.W) * p.C + half * p.d + c0;
         const int64_t from = old ? q.source * state + at : (q.token0 + pos) * p.C + half * p.d + c0;
         Piece<VEC> k, x;
-        k.load_once((old ? p.kv_state : p.kv) + from);
-        x.load_once((old ? p.score_state : p.score) + from);
+        k.load((old ? p.kv_state : p.kv) + from);
+        x.load((old ? p.score_state : p.score) + from);
         k.store(p.kv_state + q.target * state + at);
         x.store(p.score_state + q.target * state + at);
       }
     }
   }
 
-  // all other blocks: contiguous runs of rows
-  const int o0 = static_cast<int>(static_cast<int64_t>(g) * total / p.R);
-  const int o1 = static_cast<int>(static_cast<int64_t>(g + 1) * total / p.R);
-  if (o0 >= o1) return;
-  int seg = find_segment(s_prefix, p.S, o0);
-  for (int o = o0; o < o1; o += p.RS * K) {
-    StepRow rows[K];
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int at = o + k * p.RS + rs;
-      rows[k].on = false;
-      rows[k].row = at;
-      rows[k].block = 0;
-      rows[k].first = 0;
-      rows[k].state = rows[k].token0 = 0;
-      if (rs < p.RS && at < o1) {
-        seg = advance_segment(s_prefix, seg, at);
-        const StepSeq q(p, seg);
-        const int i = at - s_prefix[seg];
-        rows[k].on = i >= q.boundary;
-        rows[k].block = q.lo + i;
-        rows[k].first = q.first;
-        rows[k].token0 = q.token0;
-        describe(seg, rows[k]);
+  if (blockIdx.y == 0 && (p.positions != nullptr || p.slots != nullptr))
+    for (int64_t o = static_cast<int64_t>(g) * kStepThreads + tid; o < p.out_rows; o += static_cast<int64_t>(p.R) * kStepThreads) {
+      if (o < total) {
+        describe_row(p, s_prefix, static_cast<int>(o));
+      } else {  // behind the last entry
+        if (p.positions != nullptr) p.positions[o] = -1;
+        if (p.slots != nullptr) p.slots[o] = -1;
       }
     }
-    pool(std::integral_constant<int, K>{}, rows);
+
+  // all other blocks: contiguous runs of rows
+  const int i0 = static_cast<int>(static_cast<int64_t>(g) * inner / p.R);
+  const int i1 = static_cast<int>(static_cast<int64_t>(g + 1) * inner / p.R);
+  if (i0 >= i1) return;
+  int seg = 0, seg_end = i0;  // the sequence of the last row asked for, where its rows end,
+  int64_t seg_at = 0;         // and the element that row 0 would have for its own block's first one
+  int seg_row = 0, seg_first = -1;  // its output rows less its rows here, and the row that is its block 0, if any
+  auto fetch = [&](int i, Pieces& v) {
+    v.on = 0;
+    v.row = -1;
+    if (!slot || i >= i1) return;
+    if (i >= seg_end) {
+      int lo = seg, hi = p.S;  // sB[lo].y <= i < sB[hi].y, the last such lo
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (s_prefix[mid].y <= i) lo = mid;
+        else hi = mid;
+      }
+      seg = lo;
+      seg_end = s_prefix[lo + 1].y;
+      const StepSeq q(p, lo);
+      const int2 at = s_prefix[lo];
+      const int block = q.lo + q.boundary - at.y;  // of row 0
+      seg_at = (q.token0 + static_cast<int64_t>(block) * p.ratio) * p.C + (two ? p.d : 0) + c0;
+      seg_row = at.x + q.boundary - at.y;
+      seg_first = -block;
+    }
+    v.row = i + seg_row;
+    const int64_t at = seg_at + static_cast<int64_t>(i) * p.ratio * p.C;
+    v.on = i == seg_first ? there & own : there;
+#pragma unroll
+    for (int u = 0; u < UW; ++u) {
+      if (v.on >> u & 1u) {
+        v.kv[u].load(p.kv + at + off[u]);
+        v.score[u].load(p.score + at + off[u]);
+      } else {
+        v.kv[u].clear();
+        v.score[u].clear();
+      }
+    }
+  };
+  Pieces v[2][K];
+  const int step = p.RS * K;
+#pragma unroll
+  for (int k = 0; k < K; ++k) fetch(i0 + k * p.RS + rs, v[0][k]);
+  for (int i = i0; i < i1;) {
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      if (i < i1) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) fetch(i + step + k * p.RS + rs, v[b ^ 1][k]);
+#pragma unroll
+        for (int k = 0; k < K; ++k) finish(v[b][k], turn++);
+        i += step;
+      }
+    }
   }
 }
 
@@ -452,12 +477,11 @@ extern "C" csa_status_t csa_compressor_step(
   p.max_pages = max_pages;
   p.page_size = page_size;
   p.offset = position_offset;
-  const bool vec = d % 8 == 0 && is_aligned(kv, 16) && is_aligned(score, 16) && is_aligned(ape, 16) &&
-                   is_aligned(kv_state, 16) && is_aligned(score_state, 16) && is_aligned(out, 16);
-  p.chunks = vec ? d / 8 : d;
-  // eight positions a thread, more than that only in windows that 32 threads cannot take so
-  p.PG = 1;
-  while (p.PG < 32 && p.PG * kStepFlight < p.W) p.PG *= 2;
+  const bool vec = d % 4 == 0 && is_aligned(kv, 8) && is_aligned(score, 8) && is_aligned(ape, 16) &&
+                   is_aligned(kv_state, 8) && is_aligned(score_state, 8) && is_aligned(out, 8);
+  p.chunks = vec ? d / 4 : d;
+  p.PG = 1;  // (at most 256: CSA_MAX_WINDOW is 2048)
+  while (p.PG * kStepFlight < p.W) p.PG *= 2;
   const int most = kStepThreads / p.PG, slices = (p.chunks + most - 1) / most;
   p.CL = (p.chunks + slices - 1) / slices;
   p.RS = kStepThreads / (p.CL * p.PG);
@@ -470,8 +494,8 @@ extern "C" csa_status_t csa_compressor_step(
            : uw == 2 ? reinterpret_cast<const void*>(step_kernel<V, 2, false>)
                      : reinterpret_cast<const void*>(step_kernel<V, 1, false>);
   };
-  const void* k = vec ? pick(std::integral_constant<int, 8>{}) : pick(std::integral_constant<int, 1>{});
-  const size_t smem = sizeof(int) * (static_cast<size_t>(S) + 1);
+  const void* k = vec ? pick(std::integral_constant<int, 4>{}) : pick(std::integral_constant<int, 1>{});
+  const size_t smem = sizeof(int2) * (static_cast<size_t>(S) + 1);
   int dev = 0, sms = 0, bps = 0;
   if (note(cudaGetDevice(&dev)) != cudaSuccess || device_sms(dev, &sms) != cudaSuccess ||
       blocks_per_sm(dev, k, kStepThreads, smem, &bps) != cudaSuccess)

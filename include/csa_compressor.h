@@ -259,8 +259,8 @@ csa_status_t csa_compressor_map_blocks(const int32_t* cu_seqlens, int32_t S, int
  * no number on the host. Outputs overlap no input but for the states. Bad lengths or states (CSA_DEVERR_CU_SEQLENS,
  * CSA_DEVERR_STATE) skip all outputs. CSA_ERR_INVALID_VALUE and CSA_ERR_UNSUPPORTED as for
  * csa_compressor_fwd (any d and ratio up to CSA_MAX_WINDOW / coff; no smaller limit for unaligned
- * tensors), and num_states above 2^31 - 1. The vector kernels run when d is a multiple of 8 and kv, score, ape,
- * out and the states are 16-byte aligned; anything else takes a column a thread. One kernel is enqueued. */
+ * tensors), and num_states above 2^31 - 1. The vector kernels run when d is a multiple of 4, ape 16-byte and kv,
+ * score, out and the states 8-byte aligned; anything else takes a column a thread. One kernel is enqueued. */
 csa_status_t csa_compressor_step(const void* kv, const void* score, const float* ape,
                                  const int32_t* cu_seqlens, int32_t S, int32_t ratio, int32_t coff,
                                  int32_t d, int64_t capacity, const int32_t* first,
