@@ -22,6 +22,7 @@ namespace {
 
 constexpr int kStepThreads = 256;
 constexpr int kStepFlight = 8;  // (kv, score) pieces that a thread loads at a time
+constexpr int kStepJoin = 4;    // threads that join a column's parts, of at least as many
 
 struct StepParams {
   const uint16_t* kv;
@@ -60,11 +61,8 @@ struct Piece<4> {
     asm volatile("ld.global.cs.v2.u32 {%0, %1}, [%2];" : "=r"(w.x), "=r"(w.y) : "l"(p));
   }
   __device__ __forceinline__ void store(uint16_t* p) const { *reinterpret_cast<uint2*>(p) = w; }
-  __device__ __forceinline__ void clear() { w = make_uint2(0, 0); }
-  __device__ __forceinline__ float get(int i) const {
-    const uint32_t x = i < 2 ? w.x : w.y;
-    return i % 2 == 0 ? bf16_lo(x) : bf16_hi(x);
-  }
+  __device__ __forceinline__ void fill(uint16_t v) { w.x = w.y = v * 0x10001u; }
+  __device__ __forceinline__ uint64_t pair(int i) const { return bf2_to_f2(i == 0 ? w.x : w.y); }
 };
 template <>
 struct Piece<1> {
@@ -73,20 +71,12 @@ struct Piece<1> {
     asm volatile("ld.global.cs.u16 %0, [%1];" : "=h"(w) : "l"(p));
   }
   __device__ __forceinline__ void store(uint16_t* p) const { *p = w; }
-  __device__ __forceinline__ void clear() { w = 0; }
-  __device__ __forceinline__ float get(int) const { return __uint_as_float(static_cast<uint32_t>(w) << 16); }
+  __device__ __forceinline__ void fill(uint16_t v) { w = v; }
+  // (its second column is nobody's)
+  __device__ __forceinline__ uint64_t pair(int) const { return f2_pack(__uint_as_float(static_cast<uint32_t>(w) << 16), 0.f); }
 };
-template <int VEC>
-__device__ __forceinline__ void load_embedding(float (&a)[VEC], const float* p) {
-  if constexpr (VEC == 2) {
-    const float2 t = __ldg(reinterpret_cast<const float2*>(p));
-    a[0] = t.x;
-    a[1] = t.y;
-  } else {
-    a[0] = __ldg(p);
-  }
-}
-
+// What an absent position's pieces hold: a score of -inf, whose weight is 0, and a value of 0.
+constexpr uint16_t kAbsentScore = 0xFF80, kAbsentValue = 0;
 // What a sequence's call is.
 struct StepSeq {
   int n, first, source, target;
@@ -176,15 +166,21 @@ __device__ __forceinline__ void describe_row(const StepParams& p, const int2* sB
   }
 }
 
+__host__ __device__ constexpr int step_ape_floats(int vec, int uw) { return uw * kStepThreads * vec; }
+__host__ __device__ constexpr int step_part_floats(int vec, bool split) { return split ? 2 * 3 * kStepThreads * vec : 0; }
+
 // UW: positions of a window that a thread takes; windows of up to 4 positions go through a thread several at a
 // time instead (K rows), so that as many bytes are under way. SPLIT: windows of more than 8 positions, which
 // PG threads share. The next rows' pieces are loaded while one is worked out.
 template <int VEC, int UW, bool SPLIT>
 __global__ void __launch_bounds__(kStepThreads, 2) step_kernel(const __grid_constant__ StepParams p) {
-  constexpr int K = kStepFlight / UW, PART = VEC == 4 ? 2 : 1;
-  extern __shared__ __align__(16) int2 s_prefix[];  // [S + 1]
+  constexpr int K = SPLIT ? 1 : kStepFlight / UW, PAIRS = VEC == 4 ? 2 : 1, J = kStepJoin;
+  constexpr uint32_t kAll = (1u << UW) - 1u;
+  extern __shared__ __align__(16) unsigned char s_raw[];
   __shared__ int warp_sums[32];
-  __shared__ __align__(16) float s_part[SPLIT ? 2 : 1][SPLIT ? 3 * kStepThreads * VEC : 4];
+  float* const s_ape = reinterpret_cast<float*>(s_raw);  // [UW * PG][CL * VEC], times log2 e
+  float* const s_part = s_ape + step_ape_floats(VEC, UW);  // two turns' [RS][3][PG][CL * VEC]
+  int2* const s_prefix = reinterpret_cast<int2*>(s_part + step_part_floats(VEC, SPLIT));  // [S + 1]
   if (!build_step_prefix(p, s_prefix, warp_sums)) return;
   const int g = blockIdx.x, tid = threadIdx.x, per = p.CL * p.PG;
   const int rs = tid / per, pg = tid % per / p.CL, cl = tid % p.CL;
@@ -204,90 +200,136 @@ __global__ void __launch_bounds__(kStepThreads, 2) step_kernel(const __grid_cons
     if (mine && w < p.W) there |= 1u << u;
     if (!prev) own |= 1u << u;
   }
-  const float* const ape_own = p.ape + (two ? p.d : 0) + c0;
-  const float* const ape_prev = ape_own + static_cast<int64_t>(p.ratio) * p.C;
-
+  // the embedding of the slice's columns, once for all rows; 0 behind the window
+  bool staged = false;
+  auto stage = [&]() {
+    if (staged) return;
+    staged = true;
+    if (rs == 0) {
+      const float* const ape_own = p.ape + (two ? p.d : 0) + c0;
+      const float* const ape_prev = ape_own + static_cast<int64_t>(p.ratio) * p.C;
+#pragma unroll
+      for (int u = 0; u < UW; ++u) {
+        float e[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) e[i] = 0.f;
+        const float* from = (own >> u & 1u ? ape_own : ape_prev) + off[u];
+        if (there >> u & 1u) {
+          if constexpr (VEC == 4) load_ape<4>(e, from);
+          else e[0] = __ldg(from);
+        }
+        float* to = s_ape + ((pg + u * p.PG) * p.CL + cl) * VEC;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) to[i] = e[i] * kLog2e;
+      }
+    }
+    __syncthreads();
+  };
   struct Pieces {
     Piece<VEC> kv[UW], score[UW];
-    uint32_t on;  // positions that are there
-    int row;      // -1: none
+    int row;  // -1: none
   };
+  const int wide = p.CL * VEC, quarter = p.PG / J;
+  // (SPLIT: parts of a quarter of the positions lie eight columns on from those before, for the banks of the
+  // threads that read a column together)
+  const int turned = SPLIT ? 8 * (pg / quarter) % wide : 0, read_turned = SPLIT ? 8 * (tid % J) % wide : 0;
   // maximum, weight sum and weighted sum of this thread's positions, to the row or to the threads that share it
   auto finish = [&](const Pieces& v, int turn) {
     if (!SPLIT && v.row < 0) return;
     if (mine) {
-      float top[VEC], z[VEC], a[VEC];
-      // (two columns at a time, for the registers)
+      uint64_t z[PAIRS], a[PAIRS];
+      float top[2 * PAIRS];
+      const uint64_t log2e = f2_pack(kLog2e, kLog2e);
+      // (a pair of columns at a time, for the registers)
 #pragma unroll
-      for (int part = 0; part < VEC / PART; ++part) {
-        float x[UW][PART];
+      for (int i = 0; i < PAIRS; ++i) {
+        uint64_t x[UW];
+        float& lo = top[2 * i];
+        float& hi = top[2 * i + 1];
+        const float* e = s_ape + (pg * p.CL + cl) * VEC + 2 * i;
 #pragma unroll
-        for (int i = 0; i < PART; ++i) top[part * PART + i] = -INFINITY;
+        for (int u = 0; u < UW; ++u, e += p.PG * wide) {
+          uint64_t embedding;
+          if constexpr (VEC == 4) embedding = *reinterpret_cast<const uint64_t*>(e);
+          else embedding = f2_pack(*e, 0.f);
+          x[u] = f2_fma(v.score[u].pair(i), log2e, embedding);
+        }
+        lo = f2_lo(x[0]);
+        hi = f2_hi(x[0]);
+#pragma unroll
+        for (int u = 1; u + 1 < UW; u += 2) {
+          lo = fmax3(lo, f2_lo(x[u]), f2_lo(x[u + 1]));
+          hi = fmax3(hi, f2_hi(x[u]), f2_hi(x[u + 1]));
+        }
+        if constexpr (UW % 2 == 0) {
+          lo = fmaxf(lo, f2_lo(x[UW - 1]));
+          hi = fmaxf(hi, f2_hi(x[UW - 1]));
+        }
+        // (scores of -inf alone weigh nothing)
+        const uint64_t to = f2_pack(lo == -INFINITY ? 0.f : -lo, hi == -INFINITY ? 0.f : -hi);
+        z[i] = a[i] = 0;
 #pragma unroll
         for (int u = 0; u < UW; ++u) {
-          float e[PART];
-#pragma unroll
-          for (int i = 0; i < PART; ++i) e[i] = 0.f;
-          if (there >> u & 1u) load_embedding<PART>(e, (own >> u & 1u ? ape_own : ape_prev) + off[u] + part * PART);
-#pragma unroll
-          for (int i = 0; i < PART; ++i) {
-            x[u][i] = v.on >> u & 1u ? fmaf(v.score[u].get(part * PART + i), kLog2e, e[i] * kLog2e) : -INFINITY;
-            top[part * PART + i] = fmaxf(top[part * PART + i], x[u][i]);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < PART; ++i) {
-          const int c = part * PART + i;
-          const float to = top[c] == -INFINITY ? 0.f : top[c];  // (scores of -inf alone weigh nothing)
-          z[c] = a[c] = 0.f;
-#pragma unroll
-          for (int u = 0; u < UW; ++u) {
-            const float f = fast_exp2(x[u][i] - to);
-            z[c] += f;
-            a[c] = fmaf(f, v.kv[u].get(c), a[c]);
-          }
+          const uint64_t t = f2_add(x[u], to), f = f2_pack(fast_exp2(f2_lo(t)), fast_exp2(f2_hi(t)));
+          z[i] = f2_add(z[i], f);
+          a[i] = f2_fma(f, v.kv[u].pair(i), a[i]);
         }
       }
       if constexpr (SPLIT) {
-        const int wide = p.CL * VEC, step = p.PG * wide;
-        float* to = s_part[turn & 1] + rs * 3 * step + (pg * p.CL + cl) * VEC;
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          to[i] = top[i];
-          to[step + i] = z[i];
-          to[2 * step + i] = a[i];
+        const int step = p.PG * wide;
+        float* to = s_part + (turn & 1) * 3 * kStepThreads * VEC + rs * 3 * step + pg * wide;
+        int c = cl * VEC + turned;
+        if (c >= wide) c -= wide;
+        if constexpr (VEC == 4) {
+          *reinterpret_cast<float4*>(to + c) = make_float4(top[0], top[1], top[2], top[3]);
+          *reinterpret_cast<ulonglong2*>(to + step + c) = make_ulonglong2(z[0], z[1]);
+          *reinterpret_cast<ulonglong2*>(to + 2 * step + c) = make_ulonglong2(a[0], a[1]);
+        } else {
+          to[c] = top[0];
+          to[step + c] = f2_lo(z[0]);
+          to[2 * step + c] = f2_lo(a[0]);
         }
       } else {
         uint16_t* to = p.out + static_cast<int64_t>(v.row) * p.d + c0;
-        if constexpr (VEC == 4) {
-          *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(a[0] * rcp_nr(z[0]), a[1] * rcp_nr(z[1])),
-                                                     pack_bf16x2(a[2] * rcp_nr(z[2]), a[3] * rcp_nr(z[3])));
-        } else {
-          *to = Element<CSA_DTYPE_BF16>::from_float(a[0] * rcp_nr(z[0]));
-        }
+        auto two_columns = [&](int i) {
+          return f2_to_bf2(f2_mul(a[i], f2_pack(rcp_nr(f2_lo(z[i])), rcp_nr(f2_hi(z[i])))));
+        };
+        if constexpr (VEC == 4) *reinterpret_cast<uint2*>(to) = make_uint2(two_columns(0), two_columns(1));
+        else *to = Element<CSA_DTYPE_BF16>::from_float(f2_lo(a[0]) * rcp_nr(f2_lo(z[0])));
       }
     }
     if constexpr (SPLIT) {
-      // the parts meet in shared memory, a column to a thread, in the positions' order (two turns' parts, so
-      // that one barrier a row is enough)
+      // the parts meet in shared memory in a fixed order, a column to J neighbouring threads (two turns'
+      // parts, so that one barrier a row is enough)
       __syncthreads();
       if (slot && v.row >= 0) {
-        const int wide = p.CL * VEC, step = p.PG * wide;
-        const float* part = s_part[turn & 1] + rs * 3 * step;
-        for (int c = tid % per; c < wide; c += per) {
+        const int step = p.PG * wide, j = tid % J;
+        const float* part = s_part + (turn & 1) * 3 * kStepThreads * VEC + rs * 3 * step + j * quarter * wide;
+        const uint32_t mask = ((1u << J) - 1u) << (tid & 31 & ~(J - 1));
+        for (int c = tid % per / J; c < wide; c += per / J) {
           const int col = blockIdx.y * wide + c;
           if (col >= p.d) break;
+          int from = c + read_turned;
+          if (from >= wide) from -= wide;
+          const float* at = part + from;
           float m = -INFINITY, zz = 0.f, aa = 0.f;
-#pragma unroll 8
-          for (int q = 0; q < p.PG; ++q) m = fmaxf(m, part[q * wide + c]);
+#pragma unroll 4
+          for (int q = 0; q < quarter; ++q) m = fmaxf(m, at[q * wide]);
+#pragma unroll
+          for (int o = 1; o < J; o <<= 1) m = fmaxf(m, __shfl_xor_sync(mask, m, o));
           const float to = m == -INFINITY ? 0.f : m;
-#pragma unroll 8
-          for (int q = 0; q < p.PG; ++q) {
-            const float f = fast_exp2(part[q * wide + c] - to);
-            zz = fmaf(part[step + q * wide + c], f, zz);
-            aa = fmaf(part[2 * step + q * wide + c], f, aa);
+#pragma unroll 4
+          for (int q = 0; q < quarter; ++q) {
+            const float f = fast_exp2(at[q * wide] - to);
+            zz = fmaf(at[step + q * wide], f, zz);
+            aa = fmaf(at[2 * step + q * wide], f, aa);
           }
-          p.out[static_cast<int64_t>(v.row) * p.d + col] = Element<CSA_DTYPE_BF16>::from_float(aa * rcp_nr(zz));
+#pragma unroll
+          for (int o = 1; o < J; o <<= 1) {
+            zz += __shfl_xor_sync(mask, zz, o);
+            aa += __shfl_xor_sync(mask, aa, o);
+          }
+          if (j == 0) p.out[static_cast<int64_t>(v.row) * p.d + col] = Element<CSA_DTYPE_BF16>::from_float(aa * rcp_nr(zz));
         }
       }
     }
@@ -303,18 +345,16 @@ __global__ void __launch_bounds__(kStepThreads, 2) step_kernel(const __grid_cons
 #pragma unroll 1
     for (int i = 0; i < p.coff; ++i) {
       const bool now = some && i < q.boundary;
-      if (SPLIT ? !__syncthreads_or(now) : !now) continue;
+      if (!__syncthreads_or(now)) break;  // (the second one comes after a first)
       Pieces v;
-      v.on = 0;
       v.row = now ? s_prefix[s].x + i : -1;
 #pragma unroll
       for (int u = 0; u < UW; ++u) {
-        v.kv[u].clear();
-        v.score[u].clear();
+        v.kv[u].fill(kAbsentValue);
+        v.score[u].fill(kAbsentScore);
         const int w = pg + u * p.PG;
         const int pos = (q.lo + i - (two ? 1 : 0)) * p.ratio + w;
         if (now && (there >> u & 1u) && pos >= 0) {
-          v.on |= 1u << u;
           const bool old = pos < q.first;
           const int64_t at = (old ? q.source * state + static_cast<int64_t>(pos % p.W) * p.C : (q.token0 + pos) * p.C) +
                              (two && (own >> u & 1u) ? p.d : 0) + c0;
@@ -322,6 +362,7 @@ __global__ void __launch_bounds__(kStepThreads, 2) step_kernel(const __grid_cons
           v.score[u].load((old ? p.score_state : p.score) + at);
         }
       }
+      stage();
       finish(v, turn++);
     }
     if (!some) continue;
@@ -362,7 +403,6 @@ __global__ void __launch_bounds__(kStepThreads, 2) step_kernel(const __grid_cons
   int64_t seg_at = 0;         // and the element that row 0 would have for its own block's first one
   int seg_row = 0, seg_first = -1;  // its output rows less its rows here, and the row that is its block 0, if any
   auto fetch = [&](int i, Pieces& v) {
-    v.on = 0;
     v.row = -1;
     if (!slot || i >= i1) return;
     if (i >= seg_end) {
@@ -383,15 +423,23 @@ __global__ void __launch_bounds__(kStepThreads, 2) step_kernel(const __grid_cons
     }
     v.row = i + seg_row;
     const int64_t at = seg_at + static_cast<int64_t>(i) * p.ratio * p.C;
-    v.on = i == seg_first ? there & own : there;
+    const uint16_t *kv = p.kv + at, *score = p.score + at;
+    const uint32_t on = i == seg_first ? there & own : there;
+    if (on == kAll) {
+#pragma unroll
+      for (int u = 0; u < UW; ++u) {
+        v.kv[u].load(kv + off[u]);
+        v.score[u].load(score + off[u]);
+      }
+      return;
+    }
 #pragma unroll
     for (int u = 0; u < UW; ++u) {
-      if (v.on >> u & 1u) {
-        v.kv[u].load(p.kv + at + off[u]);
-        v.score[u].load(p.score + at + off[u]);
-      } else {
-        v.kv[u].clear();
-        v.score[u].clear();
+      v.kv[u].fill(kAbsentValue);
+      v.score[u].fill(kAbsentScore);
+      if (on >> u & 1u) {
+        v.kv[u].load(kv + off[u]);
+        v.score[u].load(score + off[u]);
       }
     }
   };
@@ -399,6 +447,7 @@ __global__ void __launch_bounds__(kStepThreads, 2) step_kernel(const __grid_cons
   const int step = p.RS * K;
 #pragma unroll
   for (int k = 0; k < K; ++k) fetch(i0 + k * p.RS + rs, v[0][k]);
+  stage();
   for (int i = i0; i < i1;) {
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
@@ -480,29 +529,32 @@ extern "C" csa_status_t csa_compressor_step(
   const bool vec = d % 4 == 0 && is_aligned(kv, 8) && is_aligned(score, 8) && is_aligned(ape, 16) &&
                    is_aligned(kv_state, 8) && is_aligned(score_state, 8) && is_aligned(out, 8);
   p.chunks = vec ? d / 4 : d;
-  p.PG = 1;  // (at most 256: CSA_MAX_WINDOW is 2048)
+  // up to 8 positions a thread; longer windows between 4 threads and more (256 at most: CSA_MAX_WINDOW is 2048)
+  p.PG = p.W > kStepFlight ? kStepJoin : 1;
   while (p.PG * kStepFlight < p.W) p.PG *= 2;
   const int most = kStepThreads / p.PG, slices = (p.chunks + most - 1) / most;
   p.CL = (p.chunks + slices - 1) / slices;
   p.RS = kStepThreads / (p.CL * p.PG);
-  const int uw = p.W > 4 ? 8 : p.W > 2 ? 4 : p.W > 1 ? 2 : 1;
+  const bool split = p.PG > 1;
+  const int uw = p.W > (split ? 16 : 4) ? 8 : p.W > 2 ? 4 : p.W > 1 ? 2 : 1;
   auto pick = [&](auto v) -> const void* {
     constexpr int V = decltype(v)::value;
-    return p.PG > 1  ? reinterpret_cast<const void*>(step_kernel<V, 8, true>)
+    return split     ? (uw == 8 ? reinterpret_cast<const void*>(step_kernel<V, 8, true>) : reinterpret_cast<const void*>(step_kernel<V, 4, true>))
            : uw == 8 ? reinterpret_cast<const void*>(step_kernel<V, 8, false>)
            : uw == 4 ? reinterpret_cast<const void*>(step_kernel<V, 4, false>)
            : uw == 2 ? reinterpret_cast<const void*>(step_kernel<V, 2, false>)
                      : reinterpret_cast<const void*>(step_kernel<V, 1, false>);
   };
   const void* k = vec ? pick(std::integral_constant<int, 4>{}) : pick(std::integral_constant<int, 1>{});
-  const size_t smem = sizeof(int2) * (static_cast<size_t>(S) + 1);
+  const size_t smem = sizeof(int2) * (static_cast<size_t>(S) + 1) +
+                      sizeof(float) * (step_ape_floats(vec ? 4 : 1, uw) + step_part_floats(vec ? 4 : 1, split));
   int dev = 0, sms = 0, bps = 0;
   if (note(cudaGetDevice(&dev)) != cudaSuccess || device_sms(dev, &sms) != cudaSuccess ||
       blocks_per_sm(dev, k, kStepThreads, smem, &bps) != cudaSuccess)
     return CSA_ERR_CUDA;
   if (bps < 1) return CSA_ERR_UNSUPPORTED;
   if (slices > 65535) return CSA_ERR_UNSUPPORTED;
-  const int64_t by_rows = (out_rows + p.RS * (kStepFlight / uw) - 1) / (p.RS * (kStepFlight / uw));
+  const int64_t rows_at_once = p.RS * (split ? 1 : kStepFlight / uw), by_rows = (out_rows + rows_at_once - 1) / rows_at_once;
   const int64_t by_seqs = (S + p.RS - 1) / p.RS;
   const int64_t want = by_rows > by_seqs ? by_rows : by_seqs, room = static_cast<int64_t>(sms) * bps / slices;
   p.R = static_cast<int>(want < room ? (want > 0 ? want : 1) : (room > 0 ? room : 1));
