@@ -20,7 +20,7 @@
 namespace csa {
 namespace {
 
-constexpr int kStepThreads = 256;
+constexpr int kStepThreads = 512;
 constexpr int kStepFlight = 8;  // (kv, score) pieces that a thread loads at a time
 constexpr int kStepJoin = 4;    // threads that join a column's parts, of at least as many
 
@@ -49,16 +49,19 @@ struct StepParams {
   int PG;      // threads that share a window's positions
   int RS;      // windows that a CTA works on at once
   int chunks;  // pieces of a row
+  int stages;  // turns under way
+  // the first CTAs of a slice see to the sequences; those behind first_row_cta to the other blocks' rows
+  int seq_ctas, first_row_cta;
 };
 
-// VEC consecutive bf16 values (4: 8 bytes, aligned), read once.
+// VEC consecutive bf16 values (4: 8 bytes, aligned; 1: any).
 template <int VEC>
 struct Piece;
 template <>
 struct Piece<4> {
   uint2 w;
   __device__ __forceinline__ void load(const uint16_t* p) {
-    asm volatile("ld.global.cs.v2.u32 {%0, %1}, [%2];" : "=r"(w.x), "=r"(w.y) : "l"(p));
+    asm volatile("ld.global.cs.v2.u32 {%0, %1}, [%2];" : "=r"(w.x), "=r"(w.y) : "l"(p) : "memory");
   }
   __device__ __forceinline__ void store(uint16_t* p) const { *reinterpret_cast<uint2*>(p) = w; }
   __device__ __forceinline__ void fill(uint16_t v) { w.x = w.y = v * 0x10001u; }
@@ -68,7 +71,7 @@ template <>
 struct Piece<1> {
   uint16_t w;
   __device__ __forceinline__ void load(const uint16_t* p) {
-    asm volatile("ld.global.cs.u16 %0, [%1];" : "=h"(w) : "l"(p));
+    asm volatile("ld.global.cs.u16 %0, [%1];" : "=h"(w) : "l"(p) : "memory");
   }
   __device__ __forceinline__ void store(uint16_t* p) const { *p = w; }
   __device__ __forceinline__ void fill(uint16_t v) { w = v; }
@@ -77,6 +80,24 @@ struct Piece<1> {
 };
 // What an absent position's pieces hold: a score of -inf, whose weight is 0, and a value of 0.
 constexpr uint16_t kAbsentScore = 0xFF80, kAbsentValue = 0;
+
+// A piece from memory into the thread's own place in shared memory, asynchronously where it has 8 bytes.
+template <int VEC>
+__device__ __forceinline__ void stage_piece(Piece<VEC>* to, const uint16_t* from) {
+  if constexpr (VEC == 4) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_addr(to)), "l"(from) : "memory");
+  } else {
+    to->load(from);
+  }
+}
+__device__ __forceinline__ void stage_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until all but the newest n stages are there.
+__device__ __forceinline__ void stage_wait(int n) {
+  if (n >= 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else if (n == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
 // What a sequence's call is.
 struct StepSeq {
   int n, first, source, target;
@@ -100,10 +121,40 @@ struct StepSeq {
   }
 };
 
+// Exclusive sums of both over the block, and the block's totals. All threads call it; warp_sums: [32].
+__device__ __forceinline__ int2 step_scan(int2 v, int2* warp_sums, int2& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int2 x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int a = __shfl_up_sync(0xFFFFFFFFu, x.x, o), b = __shfl_up_sync(0xFFFFFFFFu, x.y, o);
+    if (lane >= o) {
+      x.x += a;
+      x.y += b;
+    }
+  }
+  if (lane == 31) warp_sums[warp] = x;
+  __syncthreads();
+  int2 before = make_int2(x.x - v.x, x.y - v.y);
+  total = make_int2(0, 0);
+#pragma unroll
+  for (int w = 0; w < kStepThreads / 32; ++w) {
+    const int2 t = warp_sums[w];
+    if (w < warp) {
+      before.x += t.x;
+      before.y += t.y;
+    }
+    total.x += t.x;
+    total.y += t.y;
+  }
+  __syncthreads();
+  return before;
+}
+
 // Rows before each sequence (x), and those of them whose windows reach into no state (y), in shared memory, [S]
 // holding all of them; false with the reason reported where the call's numbers are refused. Every thread of the
 // block calls it.
-__device__ bool build_step_prefix(const StepParams& p, int2* sB, int* warp_sums) {
+__device__ bool build_step_prefix(const StepParams& p, int2* sB, int2* warp_sums) {
   pdl_wait();
   int2 carry = make_int2(0, 0);
   int bad = 0;
@@ -124,13 +175,11 @@ __device__ bool build_step_prefix(const StepParams& p, int2* sB, int* warp_sums)
         inner = made - StepSeq::boundary_of(p, f, lo, made);
       }
     }
-    int all, all_inner = 0;
-    const int before = block_exclusive_scan(made, warp_sums, all);
-    // (a call of single tokens has no such row)
-    const int inner_before = __syncthreads_or(inner) ? block_exclusive_scan(inner, warp_sums, all_inner) : 0;
-    if (s < p.S) sB[s] = make_int2(carry.x + before, carry.y + inner_before);
-    carry.x += all;
-    carry.y += all_inner;
+    int2 all;
+    const int2 before = step_scan(make_int2(made, inner), warp_sums, all);
+    if (s < p.S) sB[s] = make_int2(carry.x + before.x, carry.y + before.y);
+    carry.x += all.x;
+    carry.y += all.y;
   }
   if (threadIdx.x == 0) sB[p.S] = carry;
   int code = 0;
@@ -166,29 +215,39 @@ __device__ __forceinline__ void describe_row(const StepParams& p, const int2* sB
   }
 }
 
-__host__ __device__ constexpr int step_ape_floats(int vec, int uw) { return uw * kStepThreads * vec; }
-__host__ __device__ constexpr int step_part_floats(int vec, bool split) { return split ? 2 * 3 * kStepThreads * vec : 0; }
+// Bytes of shared memory: a stage holds the (kv, score) pieces of a thread's positions at once; SPLIT, two turns'
+// parts; then the prefix.
+__host__ __device__ constexpr int step_stage_bytes(int vec) { return 2 * kStepFlight * kStepThreads * vec * 2; }
+__host__ __device__ constexpr int step_part_bytes(int vec, bool split) { return split ? 2 * 3 * kStepThreads * vec * 4 : 0; }
 
 // UW: positions of a window that a thread takes; windows of up to 4 positions go through a thread several at a
 // time instead (K rows), so that as many bytes are under way. SPLIT: windows of more than 8 positions, which
-// PG threads share. The next rows' pieces are loaded while one is worked out.
+// PG threads share.
+//
+// A thread's pieces come into places of its own in shared memory (no barrier), p.stages turns ahead: 64 KB a turn
+// and SM. Registers held one turn ahead and less than latency asks for: 22.7 and 43.8 us for three chunks of up to
+// 8192 tokens of 512 in blocks of 4 and four of 16384 in blocks of 128.
 template <int VEC, int UW, bool SPLIT>
-__global__ void __launch_bounds__(kStepThreads, 2) step_kernel(const __grid_constant__ StepParams p) {
+__global__ void __launch_bounds__(kStepThreads, 1) step_kernel(const __grid_constant__ StepParams p) {
   constexpr int K = SPLIT ? 1 : kStepFlight / UW, PAIRS = VEC == 4 ? 2 : 1, J = kStepJoin;
   constexpr uint32_t kAll = (1u << UW) - 1u;
+  using P = Piece<VEC>;
   extern __shared__ __align__(16) unsigned char s_raw[];
-  __shared__ int warp_sums[32];
-  float* const s_ape = reinterpret_cast<float*>(s_raw);  // [UW * PG][CL * VEC], times log2 e
-  float* const s_part = s_ape + step_ape_floats(VEC, UW);  // two turns' [RS][3][PG][CL * VEC]
-  int2* const s_prefix = reinterpret_cast<int2*>(s_part + step_part_floats(VEC, SPLIT));  // [S + 1]
+  __shared__ int2 warp_sums[32];
+  float* const s_part = reinterpret_cast<float*>(s_raw + p.stages * step_stage_bytes(VEC));  // [2][RS][3][PG][CL * VEC]
+  int2* const s_prefix = reinterpret_cast<int2*>(s_raw + p.stages * step_stage_bytes(VEC) + step_part_bytes(VEC, SPLIT));  // [S + 1]
   if (!build_step_prefix(p, s_prefix, warp_sums)) return;
   const int g = blockIdx.x, tid = threadIdx.x, per = p.CL * p.PG;
   const int rs = tid / per, pg = tid % per / p.CL, cl = tid % p.CL;
   const int chunk = blockIdx.y * p.CL + cl, c0 = chunk * VEC;
   const bool slot = rs < p.RS, mine = slot && chunk < p.chunks;  // this thread has a window, and columns
   const int total = s_prefix[p.S].x, inner = s_prefix[p.S].y;
+  // kv and score pieces of stage b: [k][u], a thread's 8 or 2 bytes beside the next one's
+  auto place = [&](int b, int k, int u, int which) {
+    return reinterpret_cast<P*>(s_raw + b * step_stage_bytes(VEC)) + ((k * UW + u) * 2 + which) * kStepThreads + tid;
+  };
 
-  // This thread's positions: elements from the block's first one (own columns), the embedding's the same way
+  // This thread's positions: elements from the block's first one (own columns)
   const bool two = p.coff == 2;
   int off[UW];
   uint32_t there = 0, own = 0;  // bits: the window has this position, the block itself has
@@ -200,80 +259,79 @@ __global__ void __launch_bounds__(kStepThreads, 2) step_kernel(const __grid_cons
     if (mine && w < p.W) there |= 1u << u;
     if (!prev) own |= 1u << u;
   }
-  // the embedding of the slice's columns, once for all rows; 0 behind the window
-  bool staged = false;
-  auto stage = [&]() {
-    if (staged) return;
-    staged = true;
-    if (rs == 0) {
-      const float* const ape_own = p.ape + (two ? p.d : 0) + c0;
-      const float* const ape_prev = ape_own + static_cast<int64_t>(p.ratio) * p.C;
+  // the embedding at these positions, times log2 e, once for all rows; 0 behind the window
+  uint64_t embedding[UW][PAIRS];
+  bool embedded = false;
+  auto embed = [&]() {
+    if (embedded) return;
+    embedded = true;
+    const float* const ape_own = p.ape + (two ? p.d : 0) + c0;
+    const float* const ape_prev = ape_own + static_cast<int64_t>(p.ratio) * p.C;
 #pragma unroll
-      for (int u = 0; u < UW; ++u) {
-        float e[VEC];
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) e[i] = 0.f;
-        const float* from = (own >> u & 1u ? ape_own : ape_prev) + off[u];
-        if (there >> u & 1u) {
-          if constexpr (VEC == 4) load_ape<4>(e, from);
-          else e[0] = __ldg(from);
-        }
-        float* to = s_ape + ((pg + u * p.PG) * p.CL + cl) * VEC;
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) to[i] = e[i] * kLog2e;
+    for (int u = 0; u < UW; ++u) {
+      float e[4] = {};
+      const float* from = (own >> u & 1u ? ape_own : ape_prev) + off[u];
+      if (there >> u & 1u) {
+        if constexpr (VEC == 4) load_ape<4>(e, from);
+        else e[0] = __ldg(from);
       }
+#pragma unroll
+      for (int i = 0; i < PAIRS; ++i) embedding[u][i] = f2_pack(e[2 * i] * kLog2e, e[2 * i + 1] * kLog2e);
     }
-    __syncthreads();
   };
-  struct Pieces {
-    Piece<VEC> kv[UW], score[UW];
-    int row;  // -1: none
-  };
-  const int wide = p.CL * VEC, quarter = p.PG / J;
+
   // (SPLIT: parts of a quarter of the positions lie eight columns on from those before, for the banks of the
   // threads that read a column together)
+  const int wide = p.CL * VEC, quarter = p.PG / J;
   const int turned = SPLIT ? 8 * (pg / quarter) % wide : 0, read_turned = SPLIT ? 8 * (tid % J) % wide : 0;
-  // maximum, weight sum and weighted sum of this thread's positions, to the row or to the threads that share it
-  auto finish = [&](const Pieces& v, int turn) {
-    if (!SPLIT && v.row < 0) return;
+  // maximum, weight sum and weighted sum of this thread's positions in a stage, to the row (-1: none) or to the
+  // threads that share it
+  auto finish = [&](int b, int k, int row, int turn) {
+    if (!SPLIT && row < 0) return;
     if (mine) {
       uint64_t z[PAIRS], a[PAIRS];
       float top[2 * PAIRS];
       const uint64_t log2e = f2_pack(kLog2e, kLog2e);
-      // (a pair of columns at a time, for the registers)
+      P kv[UW], score[UW];
+#pragma unroll
+      for (int u = 0; u < UW; ++u) {
+        kv[u] = *place(b, k, u, 0);
+        score[u] = *place(b, k, u, 1);
+      }
 #pragma unroll
       for (int i = 0; i < PAIRS; ++i) {
-        uint64_t x[UW];
-        float& lo = top[2 * i];
-        float& hi = top[2 * i + 1];
-        const float* e = s_ape + (pg * p.CL + cl) * VEC + 2 * i;
-#pragma unroll
-        for (int u = 0; u < UW; ++u, e += p.PG * wide) {
-          uint64_t embedding;
-          if constexpr (VEC == 4) embedding = *reinterpret_cast<const uint64_t*>(e);
-          else embedding = f2_pack(*e, 0.f);
-          x[u] = f2_fma(v.score[u].pair(i), log2e, embedding);
-        }
-        lo = f2_lo(x[0]);
-        hi = f2_hi(x[0]);
-#pragma unroll
-        for (int u = 1; u + 1 < UW; u += 2) {
-          lo = fmax3(lo, f2_lo(x[u]), f2_lo(x[u + 1]));
-          hi = fmax3(hi, f2_hi(x[u]), f2_hi(x[u + 1]));
-        }
-        if constexpr (UW % 2 == 0) {
-          lo = fmaxf(lo, f2_lo(x[UW - 1]));
-          hi = fmaxf(hi, f2_hi(x[UW - 1]));
-        }
-        // (scores of -inf alone weigh nothing)
-        const uint64_t to = f2_pack(lo == -INFINITY ? 0.f : -lo, hi == -INFINITY ? 0.f : -hi);
-        z[i] = a[i] = 0;
+        float xl[UW], xh[UW];
 #pragma unroll
         for (int u = 0; u < UW; ++u) {
-          const uint64_t t = f2_add(x[u], to), f = f2_pack(fast_exp2(f2_lo(t)), fast_exp2(f2_hi(t)));
-          z[i] = f2_add(z[i], f);
-          a[i] = f2_fma(f, v.kv[u].pair(i), a[i]);
+          const uint64_t v = score[u].pair(i);
+          xl[u] = fmaf(f2_lo(v), kLog2e, f2_lo(embedding[u][i]));
+          xh[u] = fmaf(f2_hi(v), kLog2e, f2_hi(embedding[u][i]));
         }
+        float lo = xl[0], hi = xh[0];
+#pragma unroll
+        for (int u = 1; u + 1 < UW; u += 2) {
+          lo = fmax3(lo, xl[u], xl[u + 1]);
+          hi = fmax3(hi, xh[u], xh[u + 1]);
+        }
+        if constexpr (UW % 2 == 0) {
+          lo = fmaxf(lo, xl[UW - 1]);
+          hi = fmaxf(hi, xh[UW - 1]);
+        }
+        top[2 * i] = lo;
+        top[2 * i + 1] = hi;
+        const float tl = lo == -INFINITY ? 0.f : lo, th = hi == -INFINITY ? 0.f : hi;
+        float zl = 0.f, zh = 0.f, al = 0.f, ah = 0.f;
+#pragma unroll
+        for (int u = 0; u < UW; ++u) {
+          const float fl = fast_exp2(xl[u] - tl), fh = fast_exp2(xh[u] - th);
+          const uint64_t v = kv[u].pair(i);
+          zl += fl;
+          zh += fh;
+          al = fmaf(fl, f2_lo(v), al);
+          ah = fmaf(fh, f2_hi(v), ah);
+        }
+        z[i] = f2_pack(zl, zh);
+        a[i] = f2_pack(al, ah);
       }
       if constexpr (SPLIT) {
         const int step = p.PG * wide;
@@ -290,7 +348,7 @@ __global__ void __launch_bounds__(kStepThreads, 2) step_kernel(const __grid_cons
           to[2 * step + c] = f2_lo(a[0]);
         }
       } else {
-        uint16_t* to = p.out + static_cast<int64_t>(v.row) * p.d + c0;
+        uint16_t* to = p.out + static_cast<int64_t>(row) * p.d + c0;
         auto two_columns = [&](int i) {
           return f2_to_bf2(f2_mul(a[i], f2_pack(rcp_nr(f2_lo(z[i])), rcp_nr(f2_hi(z[i])))));
         };
@@ -302,7 +360,7 @@ __global__ void __launch_bounds__(kStepThreads, 2) step_kernel(const __grid_cons
       // the parts meet in shared memory in a fixed order, a column to J neighbouring threads (two turns'
       // parts, so that one barrier a row is enough)
       __syncthreads();
-      if (slot && v.row >= 0) {
+      if (slot && row >= 0) {
         const int step = p.PG * wide, j = tid % J;
         const float* part = s_part + (turn & 1) * 3 * kStepThreads * VEC + rs * 3 * step + j * quarter * wide;
         const uint32_t mask = ((1u << J) - 1u) << (tid & 31 & ~(J - 1));
@@ -329,7 +387,7 @@ __global__ void __launch_bounds__(kStepThreads, 2) step_kernel(const __grid_cons
             zz += __shfl_xor_sync(mask, zz, o);
             aa += __shfl_xor_sync(mask, aa, o);
           }
-          if (j == 0) p.out[static_cast<int64_t>(v.row) * p.d + col] = Element<CSA_DTYPE_BF16>::from_float(aa * rcp_nr(zz));
+          if (j == 0) p.out[static_cast<int64_t>(row) * p.d + col] = Element<CSA_DTYPE_BF16>::from_float(aa * rcp_nr(zz));
         }
       }
     }
@@ -338,7 +396,7 @@ __global__ void __launch_bounds__(kStepThreads, 2) step_kernel(const __grid_cons
   // sequences: the blocks that reach into the state, then the state
   const int64_t state = static_cast<int64_t>(p.W) * p.C;
   int turn = 0;
-  for (int s0 = g * p.RS; s0 < p.S; s0 += p.R * p.RS) {
+  for (int s0 = g * p.RS; s0 < p.S && g < p.seq_ctas; s0 += p.seq_ctas * p.RS) {
     const int s = s0 + rs;
     const bool some = slot && s < p.S;
     const StepSeq q(p, some ? s : s0);
@@ -346,29 +404,29 @@ __global__ void __launch_bounds__(kStepThreads, 2) step_kernel(const __grid_cons
     for (int i = 0; i < p.coff; ++i) {
       const bool now = some && i < q.boundary;
       if (!__syncthreads_or(now)) break;  // (the second one comes after a first)
-      Pieces v;
-      v.row = now ? s_prefix[s].x + i : -1;
 #pragma unroll
       for (int u = 0; u < UW; ++u) {
-        v.kv[u].fill(kAbsentValue);
-        v.score[u].fill(kAbsentScore);
         const int w = pg + u * p.PG;
         const int pos = (q.lo + i - (two ? 1 : 0)) * p.ratio + w;
         if (now && (there >> u & 1u) && pos >= 0) {
           const bool old = pos < q.first;
           const int64_t at = (old ? q.source * state + static_cast<int64_t>(pos % p.W) * p.C : (q.token0 + pos) * p.C) +
                              (two && (own >> u & 1u) ? p.d : 0) + c0;
-          v.kv[u].load((old ? p.kv_state : p.kv) + at);
-          v.score[u].load((old ? p.score_state : p.score) + at);
+          stage_piece(place(0, 0, u, 0), (old ? p.kv_state : p.kv) + at);
+          stage_piece(place(0, 0, u, 1), (old ? p.score_state : p.score) + at);
+        } else {
+          place(0, 0, u, 0)->fill(kAbsentValue);
+          place(0, 0, u, 1)->fill(kAbsentScore);
         }
       }
-      stage();
-      finish(v, turn++);
+      stage_commit();
+      embed();
+      stage_wait(0);
+      finish(0, 0, now ? s_prefix[s].x + i : -1, turn++);
     }
     if (!some) continue;
     if (chunk == 0 && pg == 0 && p.entries != nullptr) p.entries[s] = max(0, q.hi - (p.base != nullptr ? __ldg(p.base + s) : 0));
     if (!mine || q.target < 0) continue;
-    asm volatile("" ::: "memory");  // the state is read above, by loads that the compiler does not see as such
     for (int half = 0; half < p.coff; ++half) {
       const int keep = max(0, q.hi - (p.coff - 1 - half)) * p.ratio;  // the first position that a later window reads
       const int end = q.first + q.n;
@@ -376,7 +434,7 @@ __global__ void __launch_bounds__(kStepThreads, 2) step_kernel(const __grid_cons
         const bool old = pos < q.first;
         const int64_t at = static_cast<int64_t>(pos % p.W) * p.C + half * p.d + c0;
         const int64_t from = old ? q.source * state + at : (q.token0 + pos) * p.C + half * p.d + c0;
-        Piece<VEC> k, x;
+        P k, x;
         k.load((old ? p.kv_state : p.kv) + from);
         x.load((old ? p.score_state : p.score) + from);
         k.store(p.kv_state + q.target * state + at);
@@ -385,80 +443,100 @@ __global__ void __launch_bounds__(kStepThreads, 2) step_kernel(const __grid_cons
     }
   }
 
-  if (blockIdx.y == 0 && (p.positions != nullptr || p.slots != nullptr))
-    for (int64_t o = static_cast<int64_t>(g) * kStepThreads + tid; o < p.out_rows; o += static_cast<int64_t>(p.R) * kStepThreads) {
-      if (o < total) {
-        describe_row(p, s_prefix, static_cast<int>(o));
-      } else {  // behind the last entry
-        if (p.positions != nullptr) p.positions[o] = -1;
-        if (p.slots != nullptr) p.slots[o] = -1;
+  auto describe = [&]() {
+    if (blockIdx.y == 0 && (p.positions != nullptr || p.slots != nullptr))
+      for (int64_t o = static_cast<int64_t>(tid) * p.R + g; o < p.out_rows; o += static_cast<int64_t>(p.R) * kStepThreads) {
+        if (o < total) {
+          describe_row(p, s_prefix, static_cast<int>(o));
+        } else {  // behind the last entry
+          if (p.positions != nullptr) p.positions[o] = -1;
+          if (p.slots != nullptr) p.slots[o] = -1;
+        }
       }
-    }
+  };
 
   // all other blocks: contiguous runs of rows
-  const int i0 = static_cast<int>(static_cast<int64_t>(g) * inner / p.R);
-  const int i1 = static_cast<int>(static_cast<int64_t>(g + 1) * inner / p.R);
-  if (i0 >= i1) return;
-  int seg = 0, seg_end = i0;  // the sequence of the last row asked for, where its rows end,
-  int64_t seg_at = 0;         // and the element that row 0 would have for its own block's first one
-  int seg_row = 0, seg_first = -1;  // its output rows less its rows here, and the row that is its block 0, if any
-  auto fetch = [&](int i, Pieces& v) {
-    v.row = -1;
-    if (!slot || i >= i1) return;
-    if (i >= seg_end) {
-      int lo = seg, hi = p.S;  // sB[lo].y <= i < sB[hi].y, the last such lo
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (s_prefix[mid].y <= i) lo = mid;
-        else hi = mid;
-      }
-      seg = lo;
-      seg_end = s_prefix[lo + 1].y;
-      const StepSeq q(p, lo);
-      const int2 at = s_prefix[lo];
-      const int block = q.lo + q.boundary - at.y;  // of row 0
-      seg_at = (q.token0 + static_cast<int64_t>(block) * p.ratio) * p.C + (two ? p.d : 0) + c0;
-      seg_row = at.x + q.boundary - at.y;
-      seg_first = -block;
+  const int worker = g - p.first_row_cta, workers = p.R - p.first_row_cta;
+  const int i0 = worker < 0 ? 0 : static_cast<int>(static_cast<int64_t>(worker) * inner / workers);
+  const int i1 = worker < 0 ? 0 : static_cast<int>(static_cast<int64_t>(worker + 1) * inner / workers);
+  if (i0 >= i1) {
+    describe();
+    return;
+  }
+  // a walk over them: the sequence of the row asked for last, where its rows end,
+  struct Walk {
+    int seg = 0, end;
+    int64_t at = 0;          // the element that row 0 would have for its own block's first one,
+    int row = 0, first = -1;  // its output rows less its rows here, and the row that is its block 0, if any
+  };
+  auto find = [&](Walk& w, int i) {
+    if (i < w.end) return;
+    int lo = w.seg, hi = p.S;  // sB[lo].y <= i < sB[hi].y, the last such lo
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (s_prefix[mid].y <= i) lo = mid;
+      else hi = mid;
     }
-    v.row = i + seg_row;
-    const int64_t at = seg_at + static_cast<int64_t>(i) * p.ratio * p.C;
+    w.seg = lo;
+    w.end = s_prefix[lo + 1].y;
+    const StepSeq q(p, lo);
+    const int2 before = s_prefix[lo];
+    const int block = q.lo + q.boundary - before.y;  // of row 0
+    w.at = (q.token0 + static_cast<int64_t>(block) * p.ratio) * p.C + (two ? p.d : 0) + c0;
+    w.row = before.x + q.boundary - before.y;
+    w.first = -block;
+  };
+  Walk ahead, here;
+  ahead.end = here.end = i0;
+  auto fetch = [&](int i, int b, int k) {
+    if (!mine || i >= i1) return;
+    find(ahead, i);
+    const int64_t at = ahead.at + static_cast<int64_t>(i) * p.ratio * p.C;
     const uint16_t *kv = p.kv + at, *score = p.score + at;
-    const uint32_t on = i == seg_first ? there & own : there;
+    const uint32_t on = i == ahead.first ? there & own : there;
     if (on == kAll) {
 #pragma unroll
       for (int u = 0; u < UW; ++u) {
-        v.kv[u].load(kv + off[u]);
-        v.score[u].load(score + off[u]);
+        stage_piece(place(b, k, u, 0), kv + off[u]);
+        stage_piece(place(b, k, u, 1), score + off[u]);
       }
       return;
     }
 #pragma unroll
     for (int u = 0; u < UW; ++u) {
-      v.kv[u].fill(kAbsentValue);
-      v.score[u].fill(kAbsentScore);
       if (on >> u & 1u) {
-        v.kv[u].load(kv + off[u]);
-        v.score[u].load(score + off[u]);
+        stage_piece(place(b, k, u, 0), kv + off[u]);
+        stage_piece(place(b, k, u, 1), score + off[u]);
+      } else {
+        place(b, k, u, 0)->fill(kAbsentValue);
+        place(b, k, u, 1)->fill(kAbsentScore);
       }
     }
   };
-  Pieces v[2][K];
   const int step = p.RS * K;
+  for (int b = 0; b < p.stages; ++b) {
 #pragma unroll
-  for (int k = 0; k < K; ++k) fetch(i0 + k * p.RS + rs, v[0][k]);
-  stage();
-  for (int i = i0; i < i1;) {
+    for (int k = 0; k < K; ++k) fetch(i0 + b * step + k * p.RS + rs, b, k);
+    stage_commit();
+  }
+  embed();
+  describe();  // (while the first rows are on their way)
+  for (int i = i0, b = 0; i < i1; i += step) {
+    stage_wait(p.stages - 1);
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      if (i < i1) {
-#pragma unroll
-        for (int k = 0; k < K; ++k) fetch(i + step + k * p.RS + rs, v[b ^ 1][k]);
-#pragma unroll
-        for (int k = 0; k < K; ++k) finish(v[b][k], turn++);
-        i += step;
+    for (int k = 0; k < K; ++k) {
+      const int mine_i = i + k * p.RS + rs;
+      int row = -1;
+      if (slot && mine_i < i1) {
+        find(here, mine_i);
+        row = mine_i + here.row;
       }
+      finish(b, k, row, turn++);
     }
+#pragma unroll
+    for (int k = 0; k < K; ++k) fetch(i + p.stages * step + k * p.RS + rs, b, k);
+    stage_commit();
+    if (++b == p.stages) b = 0;
   }
 }
 
@@ -546,8 +624,13 @@ extern "C" csa_status_t csa_compressor_step(
                      : reinterpret_cast<const void*>(step_kernel<V, 1, false>);
   };
   const void* k = vec ? pick(std::integral_constant<int, 4>{}) : pick(std::integral_constant<int, 1>{});
-  const size_t smem = sizeof(int2) * (static_cast<size_t>(S) + 1) +
-                      sizeof(float) * (step_ape_floats(vec ? 4 : 1, uw) + step_part_floats(vec ? 4 : 1, split));
+  // three turns under way, fewer where many sequences' numbers need the room
+  constexpr size_t kRoom = 224 * 1024;
+  const int width = vec ? 4 : 1;
+  const size_t fixed = sizeof(int2) * (static_cast<size_t>(S) + 1) + step_part_bytes(width, split);
+  p.stages = 3;
+  while (p.stages > 1 && fixed + static_cast<size_t>(p.stages) * step_stage_bytes(width) > kRoom) --p.stages;
+  const size_t smem = fixed + static_cast<size_t>(p.stages) * step_stage_bytes(width);
   int dev = 0, sms = 0, bps = 0;
   if (note(cudaGetDevice(&dev)) != cudaSuccess || device_sms(dev, &sms) != cudaSuccess ||
       blocks_per_sm(dev, k, kStepThreads, smem, &bps) != cudaSuccess)
@@ -558,6 +641,10 @@ extern "C" csa_status_t csa_compressor_step(
   const int64_t by_seqs = (S + p.RS - 1) / p.RS;
   const int64_t want = by_rows > by_seqs ? by_rows : by_seqs, room = static_cast<int64_t>(sms) * bps / slices;
   p.R = static_cast<int>(want < room ? (want > 0 ? want : 1) : (room > 0 ? room : 1));
+  // Few sequences (a chunk's) have CTAs of their own, so that nobody comes late to the rows; many (single
+  // tokens') are spread over all.
+  p.seq_ctas = static_cast<int>(by_seqs < p.R ? (by_seqs > 0 ? by_seqs : 1) : p.R);
+  p.first_row_cta = 4 * p.seq_ctas <= p.R ? p.seq_ctas : 0;
   void* args[] = {&p};
   return launch_pdl(k, dim3(p.R, slices), dim3(kStepThreads), smem, reinterpret_cast<cudaStream_t>(stream), args) ==
                  cudaSuccess
