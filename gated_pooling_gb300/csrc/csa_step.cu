@@ -151,6 +151,14 @@ __device__ __forceinline__ int2 step_scan(int2 v, int2* warp_sums, int2& total) 
   return before;
 }
 
+// What is wrong with a sequence's numbers: 0, 1 (offsets) or 2 (lengths and states).
+__device__ __forceinline__ int step_wrong(const StepParams& p, int a, int b, int f, int from, int to) {
+  if (b < a || a < 0 || b > p.capacity) return 1;
+  const int n = b - a;
+  const bool live = f % p.ratio != 0 || (p.coff == 2 && f >= p.ratio);  // the state holds something
+  return f < 0 || f > INT_MAX - n || from >= p.num_states || to >= p.num_states || (from < 0 && live && (n > 0 || to >= 0)) ? 2 : 0;
+}
+
 // Rows before each sequence (x), and those of them whose windows reach into no state (y), in shared memory, [S]
 // holding all of them; false with the reason reported where the call's numbers are refused. Every thread of the
 // block calls it.
@@ -163,15 +171,11 @@ __device__ bool build_step_prefix(const StepParams& p, int2* sB, int2* warp_sums
     int made = 0, inner = 0;
     if (s < p.S) {
       const int a = __ldg(p.cu + s), b = __ldg(p.cu + s + 1), f = __ldg(p.first + s);
-      const int from = __ldg(p.source + s), to = __ldg(p.target + s), n = b - a, lo = f / p.ratio;
-      const bool live = f != lo * p.ratio || (p.coff == 2 && lo > 0);  // the state holds something
-      if (b < a || a < 0 || b > p.capacity) {
-        bad |= 1;
-      } else if (f < 0 || f > INT_MAX - n || from >= p.num_states || to >= p.num_states ||
-                 (from < 0 && live && (n > 0 || to >= 0))) {
-        bad |= 2;
-      } else {
-        made = (f + n) / p.ratio - lo;
+      const int why = step_wrong(p, a, b, f, __ldg(p.source + s), __ldg(p.target + s));
+      bad |= why;
+      if (why == 0) {
+        const int lo = f / p.ratio;
+        made = (f + (b - a)) / p.ratio - lo;
         inner = made - StepSeq::boundary_of(p, f, lo, made);
       }
     }
@@ -192,15 +196,8 @@ __device__ bool build_step_prefix(const StepParams& p, int2* sB, int2* warp_sums
   return true;
 }
 
-// Where row o's entry goes.
-__device__ __forceinline__ void describe_row(const StepParams& p, const int2* sB, int o) {
-  int s = 0, h = p.S;  // sB[s].x <= o < sB[h].x, the last such s
-  while (h - s > 1) {
-    const int mid = (s + h) / 2;
-    if (sB[mid].x <= o) s = mid;
-    else h = mid;
-  }
-  const int block = __ldg(p.first + s) / p.ratio + (o - sB[s].x);
+// Where the entry of a sequence's block goes, which is row o.
+__device__ __forceinline__ void describe_row(const StepParams& p, int s, int block, int64_t o) {
   if (p.positions != nullptr) p.positions[o] = block * p.ratio + p.offset;
   if (p.slots != nullptr) {
     const int e = block - (p.base != nullptr ? __ldg(p.base + s) : 0);
@@ -213,6 +210,92 @@ __device__ __forceinline__ void describe_row(const StepParams& p, const int2* sB
     }
     p.slots[o] = slot;
   }
+}
+__device__ __forceinline__ void no_row(const StepParams& p, int64_t o) {  // behind the last entry
+  if (p.positions != nullptr) p.positions[o] = -1;
+  if (p.slots != nullptr) p.slots[o] = -1;
+}
+
+// The maximum of a thread's positions (times log2 e), the sum of their weights against it, and their weighted sum,
+// of each of its columns.
+template <int VEC>
+struct Weighed {
+  static constexpr int kPairs = VEC == 4 ? 2 : 1;
+  uint64_t z[kPairs], a[kPairs];
+  float top[2 * kPairs];
+  template <int UW>
+  __device__ __forceinline__ void of(const Piece<VEC> (&kv)[UW], const Piece<VEC> (&score)[UW], const uint64_t (&embedding)[UW][kPairs]) {
+    const uint64_t log2e = f2_pack(kLog2e, kLog2e);
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+      uint64_t x[UW];
+#pragma unroll
+      for (int u = 0; u < UW; ++u) x[u] = f2_fma(score[u].pair(i), log2e, embedding[u][i]);
+      float lo = f2_lo(x[0]), hi = f2_hi(x[0]);
+#pragma unroll
+      for (int u = 1; u + 1 < UW; u += 2) {
+        lo = fmax3(lo, f2_lo(x[u]), f2_lo(x[u + 1]));
+        hi = fmax3(hi, f2_hi(x[u]), f2_hi(x[u + 1]));
+      }
+      if constexpr (UW % 2 == 0) {
+        lo = fmaxf(lo, f2_lo(x[UW - 1]));
+        hi = fmaxf(hi, f2_hi(x[UW - 1]));
+      }
+      top[2 * i] = lo;
+      top[2 * i + 1] = hi;
+      // (scores of -inf alone weigh nothing)
+      const uint64_t to = f2_pack(lo == -INFINITY ? 0.f : -lo, hi == -INFINITY ? 0.f : -hi);
+      z[i] = a[i] = 0;
+#pragma unroll
+      for (int u = 0; u < UW; ++u) {
+        const uint64_t t = f2_add(x[u], to), f = f2_pack(fast_exp2(f2_lo(t)), fast_exp2(f2_hi(t)));
+        z[i] = f2_add(z[i], f);
+        a[i] = f2_fma(f, kv[u].pair(i), a[i]);
+      }
+    }
+  }
+  __device__ __forceinline__ uint32_t two_columns(int i) const {
+    return f2_to_bf2(f2_mul(a[i], f2_pack(rcp_nr(f2_lo(z[i])), rcp_nr(f2_hi(z[i])))));
+  }
+  __device__ __forceinline__ void store(uint16_t* to) const {  // the entry, of whole windows
+    if constexpr (VEC == 4) *reinterpret_cast<uint2*>(to) = make_uint2(two_columns(0), two_columns(1));
+    else *to = static_cast<uint16_t>(two_columns(0));
+  }
+  __device__ __forceinline__ void leave(float* to, int step) const {  // as a part: three rows of a column each
+    if constexpr (VEC == 4) {
+      *reinterpret_cast<float4*>(to) = make_float4(top[0], top[1], top[2], top[3]);
+      *reinterpret_cast<ulonglong2*>(to + step) = make_ulonglong2(z[0], z[1]);
+      *reinterpret_cast<ulonglong2*>(to + 2 * step) = make_ulonglong2(a[0], a[1]);
+    } else {
+      to[0] = top[0];
+      to[step] = f2_lo(z[0]);
+      to[2 * step] = f2_lo(a[0]);
+    }
+  }
+};
+// Joins a column's parts, `many` to each of kStepJoin neighbouring threads (from `at` on, `wide` apart), and stores it.
+__device__ __forceinline__ void join_parts(const float* at, int step, int wide, int many, uint16_t* to) {
+  constexpr int J = kStepJoin;
+  const int lane = threadIdx.x & 31;
+  const uint32_t mask = ((1u << J) - 1u) << (lane & ~(J - 1));
+  float m = -INFINITY, z = 0.f, a = 0.f;
+#pragma unroll 4
+  for (int q = 0; q < many; ++q) m = fmaxf(m, at[q * wide]);
+#pragma unroll
+  for (int o = 1; o < J; o <<= 1) m = fmaxf(m, __shfl_xor_sync(mask, m, o));
+  const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll 4
+  for (int q = 0; q < many; ++q) {
+    const float f = fast_exp2(at[q * wide] - base);
+    z = fmaf(at[step + q * wide], f, z);
+    a = fmaf(at[2 * step + q * wide], f, a);
+  }
+#pragma unroll
+  for (int o = 1; o < J; o <<= 1) {
+    z += __shfl_xor_sync(mask, z, o);
+    a += __shfl_xor_sync(mask, a, o);
+  }
+  if (lane % J == 0) *to = Element<CSA_DTYPE_BF16>::from_float(a * rcp_nr(z));
 }
 
 // Bytes of shared memory: a stage holds the (kv, score) pieces of a thread's positions at once; SPLIT, two turns'
@@ -289,71 +372,22 @@ __global__ void __launch_bounds__(kStepThreads, 1) step_kernel(const __grid_cons
   auto finish = [&](int b, int k, int row, int turn) {
     if (!SPLIT && row < 0) return;
     if (mine) {
-      uint64_t z[PAIRS], a[PAIRS];
-      float top[2 * PAIRS];
-      const uint64_t log2e = f2_pack(kLog2e, kLog2e);
       P kv[UW], score[UW];
 #pragma unroll
       for (int u = 0; u < UW; ++u) {
         kv[u] = *place(b, k, u, 0);
         score[u] = *place(b, k, u, 1);
       }
-#pragma unroll
-      for (int i = 0; i < PAIRS; ++i) {
-        float xl[UW], xh[UW];
-#pragma unroll
-        for (int u = 0; u < UW; ++u) {
-          const uint64_t v = score[u].pair(i);
-          xl[u] = fmaf(f2_lo(v), kLog2e, f2_lo(embedding[u][i]));
-          xh[u] = fmaf(f2_hi(v), kLog2e, f2_hi(embedding[u][i]));
-        }
-        float lo = xl[0], hi = xh[0];
-#pragma unroll
-        for (int u = 1; u + 1 < UW; u += 2) {
-          lo = fmax3(lo, xl[u], xl[u + 1]);
-          hi = fmax3(hi, xh[u], xh[u + 1]);
-        }
-        if constexpr (UW % 2 == 0) {
-          lo = fmaxf(lo, xl[UW - 1]);
-          hi = fmaxf(hi, xh[UW - 1]);
-        }
-        top[2 * i] = lo;
-        top[2 * i + 1] = hi;
-        const float tl = lo == -INFINITY ? 0.f : lo, th = hi == -INFINITY ? 0.f : hi;
-        float zl = 0.f, zh = 0.f, al = 0.f, ah = 0.f;
-#pragma unroll
-        for (int u = 0; u < UW; ++u) {
-          const float fl = fast_exp2(xl[u] - tl), fh = fast_exp2(xh[u] - th);
-          const uint64_t v = kv[u].pair(i);
-          zl += fl;
-          zh += fh;
-          al = fmaf(fl, f2_lo(v), al);
-          ah = fmaf(fh, f2_hi(v), ah);
-        }
-        z[i] = f2_pack(zl, zh);
-        a[i] = f2_pack(al, ah);
-      }
+      Weighed<VEC> r;
+      r.template of<UW>(kv, score, embedding);
       if constexpr (SPLIT) {
         const int step = p.PG * wide;
         float* to = s_part + (turn & 1) * 3 * kStepThreads * VEC + rs * 3 * step + pg * wide;
         int c = cl * VEC + turned;
         if (c >= wide) c -= wide;
-        if constexpr (VEC == 4) {
-          *reinterpret_cast<float4*>(to + c) = make_float4(top[0], top[1], top[2], top[3]);
-          *reinterpret_cast<ulonglong2*>(to + step + c) = make_ulonglong2(z[0], z[1]);
-          *reinterpret_cast<ulonglong2*>(to + 2 * step + c) = make_ulonglong2(a[0], a[1]);
-        } else {
-          to[c] = top[0];
-          to[step + c] = f2_lo(z[0]);
-          to[2 * step + c] = f2_lo(a[0]);
-        }
+        r.leave(to + c, step);
       } else {
-        uint16_t* to = p.out + static_cast<int64_t>(row) * p.d + c0;
-        auto two_columns = [&](int i) {
-          return f2_to_bf2(f2_mul(a[i], f2_pack(rcp_nr(f2_lo(z[i])), rcp_nr(f2_hi(z[i])))));
-        };
-        if constexpr (VEC == 4) *reinterpret_cast<uint2*>(to) = make_uint2(two_columns(0), two_columns(1));
-        else *to = Element<CSA_DTYPE_BF16>::from_float(f2_lo(a[0]) * rcp_nr(f2_lo(z[0])));
+        r.store(p.out + static_cast<int64_t>(row) * p.d + c0);
       }
     }
     if constexpr (SPLIT) {
@@ -363,31 +397,12 @@ __global__ void __launch_bounds__(kStepThreads, 1) step_kernel(const __grid_cons
       if (slot && row >= 0) {
         const int step = p.PG * wide, j = tid % J;
         const float* part = s_part + (turn & 1) * 3 * kStepThreads * VEC + rs * 3 * step + j * quarter * wide;
-        const uint32_t mask = ((1u << J) - 1u) << (tid & 31 & ~(J - 1));
         for (int c = tid % per / J; c < wide; c += per / J) {
           const int col = blockIdx.y * wide + c;
           if (col >= p.d) break;
           int from = c + read_turned;
           if (from >= wide) from -= wide;
-          const float* at = part + from;
-          float m = -INFINITY, zz = 0.f, aa = 0.f;
-#pragma unroll 4
-          for (int q = 0; q < quarter; ++q) m = fmaxf(m, at[q * wide]);
-#pragma unroll
-          for (int o = 1; o < J; o <<= 1) m = fmaxf(m, __shfl_xor_sync(mask, m, o));
-          const float to = m == -INFINITY ? 0.f : m;
-#pragma unroll 4
-          for (int q = 0; q < quarter; ++q) {
-            const float f = fast_exp2(at[q * wide] - to);
-            zz = fmaf(at[step + q * wide], f, zz);
-            aa = fmaf(at[2 * step + q * wide], f, aa);
-          }
-#pragma unroll
-          for (int o = 1; o < J; o <<= 1) {
-            zz += __shfl_xor_sync(mask, zz, o);
-            aa += __shfl_xor_sync(mask, aa, o);
-          }
-          if (j == 0) p.out[static_cast<int64_t>(row) * p.d + col] = Element<CSA_DTYPE_BF16>::from_float(aa * rcp_nr(zz));
+          join_parts(part + from, step, wide, quarter, p.out + static_cast<int64_t>(row) * p.d + col);
         }
       }
     }
@@ -446,12 +461,17 @@ __global__ void __launch_bounds__(kStepThreads, 1) step_kernel(const __grid_cons
   auto describe = [&]() {
     if (blockIdx.y == 0 && (p.positions != nullptr || p.slots != nullptr))
       for (int64_t o = static_cast<int64_t>(tid) * p.R + g; o < p.out_rows; o += static_cast<int64_t>(p.R) * kStepThreads) {
-        if (o < total) {
-          describe_row(p, s_prefix, static_cast<int>(o));
-        } else {  // behind the last entry
-          if (p.positions != nullptr) p.positions[o] = -1;
-          if (p.slots != nullptr) p.slots[o] = -1;
+        if (o >= total) {
+          no_row(p, o);
+          continue;
         }
+        int s = 0, h = p.S;  // rows before s <= o < rows before h, the last such s
+        while (h - s > 1) {
+          const int mid = (s + h) / 2;
+          if (s_prefix[mid].x <= o) s = mid;
+          else h = mid;
+        }
+        describe_row(p, s, __ldg(p.first + s) / p.ratio + static_cast<int>(o - s_prefix[s].x), o);
       }
   };
 
@@ -540,6 +560,150 @@ __global__ void __launch_bounds__(kStepThreads, 1) step_kernel(const __grid_cons
   }
 }
 
+// Calls of few tokens a sequence: a CTA per sequence and column slice, whose blocks it works out one after another.
+// What counts is the way from the lengths to the entry, so there is little code, the window and the embedding come
+// while the rows before it are counted, and what goes into the state with them.
+constexpr int kFewThreads = 256;
+template <int VEC, int UW, bool SPLIT>
+__global__ void __launch_bounds__(kFewThreads) step_few_kernel(const __grid_constant__ StepParams p) {
+  constexpr int J = kStepJoin;
+  using P = Piece<VEC>;
+  __shared__ __align__(16) float s_part[SPLIT ? 3 * kFewThreads * VEC : 4];
+  __shared__ int s_sums[2][kFewThreads / 32];
+  const int tid = threadIdx.x, per = p.CL * p.PG, s = blockIdx.x;
+  const int pg = tid / p.CL, cl = tid - pg * p.CL;
+  const int chunk = blockIdx.y * p.CL + cl, c0 = chunk * VEC;
+  const bool two = p.coff == 2, mine = tid < per && chunk < p.chunks;
+  pdl_wait();
+  // the whole call's lengths: what is wrong with them, the rows before this sequence and of all
+  int bad = 0, before = 0, all = 0;
+  for (int i = tid; i < p.S; i += blockDim.x) {
+    const int a = __ldg(p.cu + i), b = __ldg(p.cu + i + 1), f = __ldg(p.first + i);
+    const int from = __ldg(p.source + i), to = __ldg(p.target + i), why = step_wrong(p, a, b, f, from, to);
+    bad |= why;
+    if (why == 0) {
+      const int made = (f + (b - a)) / p.ratio - f / p.ratio;
+      all += made;
+      before += i < s ? made : 0;
+    }
+  }
+  const StepSeq q(p, s);
+  const bool fine = step_wrong(p, __ldg(p.cu + s), __ldg(p.cu + s + 1), q.first, q.source, q.target) == 0;
+  const int64_t state = static_cast<int64_t>(p.W) * p.C;
+  P kv[UW], score[UW];
+  uint64_t embedding[UW][Weighed<VEC>::kPairs];
+  auto fetch = [&](int block, bool first) {
+#pragma unroll
+    for (int u = 0; u < UW; ++u) {
+      const int w = pg + u * p.PG;
+      const bool prev = two && w < p.ratio;
+      const int at = prev || !two ? w : w - p.ratio, half = prev || !two ? 0 : p.d;
+      const int pos = (block - (prev ? 1 : 0)) * p.ratio + at;
+      const bool there = mine && w < p.W;
+      kv[u].fill(kAbsentValue);
+      score[u].fill(kAbsentScore);
+      if (there && pos >= 0) {
+        const bool old = pos < q.first;
+        const int64_t from = (old ? q.source * state + static_cast<int64_t>(pos % p.W) * p.C : (q.token0 + pos) * p.C) + half + c0;
+        kv[u].load((old ? p.kv_state : p.kv) + from);
+        score[u].load((old ? p.score_state : p.score) + from);
+      }
+      if (first) {
+        float e[4] = {};
+        if (there) {
+          const float* from = p.ape + static_cast<int64_t>(at) * p.C + half + c0;
+          if constexpr (VEC == 4) load_ape<4>(e, from);
+          else e[0] = __ldg(from);
+        }
+#pragma unroll
+        for (int i = 0; i < Weighed<VEC>::kPairs; ++i) embedding[u][i] = f2_pack(e[2 * i] * kLog2e, e[2 * i + 1] * kLog2e);
+      }
+    }
+  };
+  const int made = fine ? q.hi - q.lo : 0;
+  if (made > 0) fetch(q.lo, true);
+  // this thread's first pieces that go into the state
+  const int end = q.first + q.n;
+  auto keep_from = [&](int half) {
+    const int keep = max(0, q.hi - (p.coff - 1 - half)) * p.ratio;
+    return (q.source == q.target ? max(keep, q.first) : keep) + pg;
+  };
+  auto keep_place = [&](int half, int pos) { return static_cast<int64_t>(pos % p.W) * p.C + half * p.d + c0; };
+  auto keep_load = [&](int half, int pos, P& k, P& x) {
+    const bool old = pos < q.first;
+    const int64_t from = old ? q.source * state + keep_place(half, pos) : (q.token0 + pos) * p.C + half * p.d + c0;
+    k.load((old ? p.kv_state : p.kv) + from);
+    x.load((old ? p.score_state : p.score) + from);
+  };
+  auto keep_store = [&](int half, int pos, const P& k, const P& x) {
+    const int64_t to = q.target * state + keep_place(half, pos);
+    k.store(p.kv_state + to);
+    x.store(p.score_state + to);
+  };
+  const bool keeps = fine && mine && q.target >= 0;
+  const int from0 = keeps ? keep_from(0) : end, from1 = keeps && two ? keep_from(1) : end;
+  P k0, x0, k1, x1;
+  if (from0 < end) keep_load(0, from0, k0, x0);
+  if (from1 < end) keep_load(1, from1, k1, x1);
+
+  before = __reduce_add_sync(0xFFFFFFFFu, before);
+  all = __reduce_add_sync(0xFFFFFFFFu, all);
+  if ((tid & 31) == 0) {
+    s_sums[0][tid >> 5] = before;
+    s_sums[1][tid >> 5] = all;
+  }
+  const bool wrong = __syncthreads_or(bad) != 0;
+  before = all = 0;
+  for (int w = 0; w < static_cast<int>(blockDim.x) / 32; ++w) {
+    before += s_sums[0][w];
+    all += s_sums[1][w];
+  }
+  if (wrong || all > p.out_rows) {
+    const int which = __syncthreads_or(bad & 1) ? CSA_DEVERR_CU_SEQLENS : wrong ? CSA_DEVERR_STATE : CSA_DEVERR_OUT_ROWS;
+    if (tid == 0 && p.dev_error != nullptr) *reinterpret_cast<volatile int32_t*>(p.dev_error) = which;
+    return;
+  }
+  const int wide = p.CL * VEC, quarter = p.PG / J, step = p.PG * wide;
+  for (int i = 0; i < made; ++i) {
+    if (i > 0) fetch(q.lo + i, false);
+    uint16_t* out = p.out + static_cast<int64_t>(before + i) * p.d;
+    if (mine) {
+      Weighed<VEC> r;
+      r.template of<UW>(kv, score, embedding);
+      if constexpr (SPLIT) {
+        int c = cl * VEC + 8 * (pg / quarter) % wide;
+        if (c >= wide) c -= wide;
+        r.leave(s_part + pg * wide + c, step);
+      } else {
+        r.store(out + c0);
+      }
+    }
+    if constexpr (SPLIT) {
+      __syncthreads();
+      if (tid < per)
+        for (int c = tid / J, j = tid % J; c < wide && blockIdx.y * wide + c < p.d; c += per / J) {
+          int from = c + 8 * j % wide;
+          if (from >= wide) from -= wide;
+          join_parts(s_part + j * quarter * wide + from, step, wide, quarter, out + blockIdx.y * wide + c);
+        }
+      __syncthreads();
+    }
+  }
+  // (the state was read by this thread, or before the last barrier)
+  if (from0 < end) keep_store(0, from0, k0, x0);
+  if (from1 < end) keep_store(1, from1, k1, x1);
+  for (int half = 0; half < p.coff && keeps; ++half)
+    for (int pos = (half == 0 ? from0 : from1) + p.PG; pos < end; pos += p.PG) {
+      keep_load(half, pos, k0, x0);
+      keep_store(half, pos, k0, x0);
+    }
+  // where the rows go; those behind the last entry
+  if (blockIdx.y != 0) return;
+  for (int i = static_cast<int>(blockDim.x) - 1 - tid; i < made; i += blockDim.x) describe_row(p, s, q.lo + i, before + i);
+  if (tid == static_cast<int>(blockDim.x) - 1 && p.entries != nullptr) p.entries[s] = max(0, q.hi - (p.base != nullptr ? __ldg(p.base + s) : 0));
+  for (int64_t o = all + static_cast<int64_t>(s) * blockDim.x + tid; o < p.out_rows; o += static_cast<int64_t>(p.S) * blockDim.x) no_row(p, o);
+}
+
 }  // namespace
 }  // namespace csa
 
@@ -610,13 +774,22 @@ extern "C" csa_status_t csa_compressor_step(
   // up to 8 positions a thread; longer windows between 4 threads and more (256 at most: CSA_MAX_WINDOW is 2048)
   p.PG = p.W > kStepFlight ? kStepJoin : 1;
   while (p.PG * kStepFlight < p.W) p.PG *= 2;
-  const int most = kStepThreads / p.PG, slices = (p.chunks + most - 1) / most;
+  // Few tokens a sequence: the kernel without a pipeline, a CTA a sequence (64 single tokens of 512 in blocks of 4
+  // in 5 instead of 7.7 us; 200 of 128 in blocks of 128 in 7 instead of 11.5), up to where one sequence may
+  // have most of them.
+  const bool few = S > 0 && S <= 512 && capacity <= 8 * static_cast<int64_t>(S);
+  const int threads = few ? kFewThreads : kStepThreads;
+  const int most = threads / p.PG, slices = (p.chunks + most - 1) / most;
   p.CL = (p.chunks + slices - 1) / slices;
-  p.RS = kStepThreads / (p.CL * p.PG);
+  p.RS = threads / (p.CL * p.PG);
   const bool split = p.PG > 1;
   const int uw = p.W > (split ? 16 : 4) ? 8 : p.W > 2 ? 4 : p.W > 1 ? 2 : 1;
   auto pick = [&](auto v) -> const void* {
     constexpr int V = decltype(v)::value;
+    if (few)
+      return split      ? reinterpret_cast<const void*>(step_few_kernel<V, 8, true>)
+             : p.W <= 4 ? reinterpret_cast<const void*>(step_few_kernel<V, 4, false>)
+                        : reinterpret_cast<const void*>(step_few_kernel<V, 8, false>);
     return split     ? (uw == 8 ? reinterpret_cast<const void*>(step_kernel<V, 8, true>) : reinterpret_cast<const void*>(step_kernel<V, 4, true>))
            : uw == 8 ? reinterpret_cast<const void*>(step_kernel<V, 8, false>)
            : uw == 4 ? reinterpret_cast<const void*>(step_kernel<V, 4, false>)
@@ -624,6 +797,13 @@ extern "C" csa_status_t csa_compressor_step(
                      : reinterpret_cast<const void*>(step_kernel<V, 1, false>);
   };
   const void* k = vec ? pick(std::integral_constant<int, 4>{}) : pick(std::integral_constant<int, 1>{});
+  if (slices > 65535) return CSA_ERR_UNSUPPORTED;
+  void* args[] = {&p};
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  if (few) {
+    const int block = (p.CL * p.PG + 31) / 32 * 32;
+    return launch_pdl(k, dim3(S, slices), dim3(block < 64 ? 64 : block), 0, cs, args) == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
+  }
   // three turns under way, fewer where many sequences' numbers need the room
   constexpr size_t kRoom = 224 * 1024;
   const int width = vec ? 4 : 1;
@@ -636,7 +816,6 @@ extern "C" csa_status_t csa_compressor_step(
       blocks_per_sm(dev, k, kStepThreads, smem, &bps) != cudaSuccess)
     return CSA_ERR_CUDA;
   if (bps < 1) return CSA_ERR_UNSUPPORTED;
-  if (slices > 65535) return CSA_ERR_UNSUPPORTED;
   const int64_t rows_at_once = p.RS * (split ? 1 : kStepFlight / uw), by_rows = (out_rows + rows_at_once - 1) / rows_at_once;
   const int64_t by_seqs = (S + p.RS - 1) / p.RS;
   const int64_t want = by_rows > by_seqs ? by_rows : by_seqs, room = static_cast<int64_t>(sms) * bps / slices;
@@ -645,9 +824,5 @@ extern "C" csa_status_t csa_compressor_step(
   // tokens') are spread over all.
   p.seq_ctas = static_cast<int>(by_seqs < p.R ? (by_seqs > 0 ? by_seqs : 1) : p.R);
   p.first_row_cta = 4 * p.seq_ctas <= p.R ? p.seq_ctas : 0;
-  void* args[] = {&p};
-  return launch_pdl(k, dim3(p.R, slices), dim3(kStepThreads), smem, reinterpret_cast<cudaStream_t>(stream), args) ==
-                 cudaSuccess
-             ? CSA_OK
-             : CSA_ERR_CUDA;
+  return launch_pdl(k, dim3(p.R, slices), dim3(kStepThreads), smem, cs, args) == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
 }
