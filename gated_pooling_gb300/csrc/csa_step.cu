@@ -560,9 +560,10 @@ __global__ void __launch_bounds__(kStepThreads, 1) step_kernel(const __grid_cons
   }
 }
 
-// Calls of few tokens a sequence: a CTA per sequence and column slice, whose blocks it works out one after another.
-// What counts is the way from the lengths to the entry, so there is little code, the window and the embedding come
-// while the rows before it are counted, and what goes into the state with them.
+// Calls of few tokens a sequence: a CTA per p.RS sequences and column slice, whose blocks it works out one after
+// another. What counts is the way from the lengths to the entry, so there is little code; the first window and the
+// embedding come while the rows before it are counted, and so does what goes into the states, which the lines of CL
+// threads share out among them.
 constexpr int kFewThreads = 256;
 template <int VEC, int UW, bool SPLIT>
 __global__ void __launch_bounds__(kFewThreads) step_few_kernel(const __grid_constant__ StepParams p) {
@@ -570,12 +571,12 @@ __global__ void __launch_bounds__(kFewThreads) step_few_kernel(const __grid_cons
   using P = Piece<VEC>;
   __shared__ __align__(16) float s_part[SPLIT ? 3 * kFewThreads * VEC : 4];
   __shared__ int s_sums[2][kFewThreads / 32];
-  const int tid = threadIdx.x, per = p.CL * p.PG, s = blockIdx.x;
+  const int tid = threadIdx.x, per = p.CL * p.PG, s0 = blockIdx.x * p.RS, s1 = min(p.S, s0 + p.RS);
   const int pg = tid / p.CL, cl = tid - pg * p.CL;
   const int chunk = blockIdx.y * p.CL + cl, c0 = chunk * VEC;
   const bool two = p.coff == 2, mine = tid < per && chunk < p.chunks;
   pdl_wait();
-  // the whole call's lengths: what is wrong with them, the rows before this sequence and of all
+  // the whole call's lengths: what is wrong with them, the rows before these sequences and of all
   int bad = 0, before = 0, all = 0;
   for (int i = tid; i < p.S; i += blockDim.x) {
     const int a = __ldg(p.cu + i), b = __ldg(p.cu + i + 1), f = __ldg(p.first + i);
@@ -584,63 +585,78 @@ __global__ void __launch_bounds__(kFewThreads) step_few_kernel(const __grid_cons
     if (why == 0) {
       const int made = (f + (b - a)) / p.ratio - f / p.ratio;
       all += made;
-      before += i < s ? made : 0;
+      before += i < s0 ? made : 0;
     }
   }
-  const StepSeq q(p, s);
-  const bool fine = step_wrong(p, __ldg(p.cu + s), __ldg(p.cu + s + 1), q.first, q.source, q.target) == 0;
+  // (numbers of one sequence, of which nothing is read until they are known to be right)
+  auto fine = [&](const StepSeq& q, int s) {
+    return step_wrong(p, __ldg(p.cu + s), __ldg(p.cu + s + 1), q.first, q.source, q.target) == 0;
+  };
   const int64_t state = static_cast<int64_t>(p.W) * p.C;
   P kv[UW], score[UW];
   uint64_t embedding[UW][Weighed<VEC>::kPairs];
-  auto fetch = [&](int block, bool first) {
+  auto fetch = [&](const StepSeq& q, int block) {
 #pragma unroll
     for (int u = 0; u < UW; ++u) {
       const int w = pg + u * p.PG;
       const bool prev = two && w < p.ratio;
-      const int at = prev || !two ? w : w - p.ratio, half = prev || !two ? 0 : p.d;
-      const int pos = (block - (prev ? 1 : 0)) * p.ratio + at;
-      const bool there = mine && w < p.W;
+      const int pos = (block - (two ? 1 : 0)) * p.ratio + w;
       kv[u].fill(kAbsentValue);
       score[u].fill(kAbsentScore);
-      if (there && pos >= 0) {
+      if (mine && w < p.W && pos >= 0) {
         const bool old = pos < q.first;
-        const int64_t from = (old ? q.source * state + static_cast<int64_t>(pos % p.W) * p.C : (q.token0 + pos) * p.C) + half + c0;
+        const int64_t from = (old ? q.source * state + static_cast<int64_t>(pos % p.W) * p.C : (q.token0 + pos) * p.C) +
+                             (two && !prev ? p.d : 0) + c0;
         kv[u].load((old ? p.kv_state : p.kv) + from);
         score[u].load((old ? p.score_state : p.score) + from);
       }
-      if (first) {
-        float e[4] = {};
-        if (there) {
-          const float* from = p.ape + static_cast<int64_t>(at) * p.C + half + c0;
-          if constexpr (VEC == 4) load_ape<4>(e, from);
-          else e[0] = __ldg(from);
-        }
-#pragma unroll
-        for (int i = 0; i < Weighed<VEC>::kPairs; ++i) embedding[u][i] = f2_pack(e[2 * i] * kLog2e, e[2 * i + 1] * kLog2e);
-      }
     }
   };
-  const int made = fine ? q.hi - q.lo : 0;
-  if (made > 0) fetch(q.lo, true);
-  // this thread's first pieces that go into the state
-  const int end = q.first + q.n;
+  int next = s0;  // the first of the sequences that completes a block
+  while (next < s1) {
+    const StepSeq q(p, next);
+    if (q.hi > q.lo && fine(q, next)) {
+      fetch(q, q.lo);
+      break;
+    }
+    ++next;
+  }
+  if (next < s1) {
+#pragma unroll
+    for (int u = 0; u < UW; ++u) {
+      const int w = pg + u * p.PG;
+      const bool prev = two && w < p.ratio;
+      float e[4] = {};
+      if (mine && w < p.W) {
+        const float* from = p.ape + static_cast<int64_t>(prev || !two ? w : w - p.ratio) * p.C + (two && !prev ? p.d : 0) + c0;
+        if constexpr (VEC == 4) load_ape<4>(e, from);
+        else e[0] = __ldg(from);
+      }
+#pragma unroll
+      for (int i = 0; i < Weighed<VEC>::kPairs; ++i) embedding[u][i] = f2_pack(e[2 * i] * kLog2e, e[2 * i + 1] * kLog2e);
+    }
+  }
+  // what goes into the states: lines / RS of them to a sequence, each the positions of its turn
+  const int lines = p.PG / p.RS, ks = s0 + pg / lines;
+  const StepSeq kq(p, min(ks, p.S - 1));
+  const bool keeps = mine && ks < s1 && kq.target >= 0 && fine(kq, ks);
+  const int end = kq.first + kq.n;
   auto keep_from = [&](int half) {
-    const int keep = max(0, q.hi - (p.coff - 1 - half)) * p.ratio;
-    return (q.source == q.target ? max(keep, q.first) : keep) + pg;
+    const int keep = max(0, kq.hi - (p.coff - 1 - half)) * p.ratio;
+    return (kq.source == kq.target ? max(keep, kq.first) : keep) + pg % lines;
   };
   auto keep_place = [&](int half, int pos) { return static_cast<int64_t>(pos % p.W) * p.C + half * p.d + c0; };
   auto keep_load = [&](int half, int pos, P& k, P& x) {
-    const bool old = pos < q.first;
-    const int64_t from = old ? q.source * state + keep_place(half, pos) : (q.token0 + pos) * p.C + half * p.d + c0;
+    const bool old = pos < kq.first;
+    const int64_t from = old ? kq.source * state + keep_place(half, pos) : (kq.token0 + pos) * p.C + half * p.d + c0;
     k.load((old ? p.kv_state : p.kv) + from);
     x.load((old ? p.score_state : p.score) + from);
   };
   auto keep_store = [&](int half, int pos, const P& k, const P& x) {
-    const int64_t to = q.target * state + keep_place(half, pos);
+    const int64_t to = kq.target * state + keep_place(half, pos);
     k.store(p.kv_state + to);
     x.store(p.score_state + to);
   };
-  const bool keeps = fine && mine && q.target >= 0;
   const int from0 = keeps ? keep_from(0) : end, from1 = keeps && two ? keep_from(1) : end;
   P k0, x0, k1, x1;
   if (from0 < end) keep_load(0, from0, k0, x0);
@@ -664,44 +680,55 @@ __global__ void __launch_bounds__(kFewThreads) step_few_kernel(const __grid_cons
     return;
   }
   const int wide = p.CL * VEC, quarter = p.PG / J, step = p.PG * wide;
-  for (int i = 0; i < made; ++i) {
-    if (i > 0) fetch(q.lo + i, false);
-    uint16_t* out = p.out + static_cast<int64_t>(before + i) * p.d;
-    if (mine) {
-      Weighed<VEC> r;
-      r.template of<UW>(kv, score, embedding);
+  bool here = true;  // the window is there already
+  for (int s = next, row = before; s < s1; ++s) {
+    const StepSeq q(p, s);
+    for (int block = q.lo; block < q.hi; ++block, ++row) {
+      if (!here) fetch(q, block);
+      here = false;
+      uint16_t* out = p.out + static_cast<int64_t>(row) * p.d;
+      if (mine) {
+        Weighed<VEC> r;
+        r.template of<UW>(kv, score, embedding);
+        if constexpr (SPLIT) {
+          int c = cl * VEC + 8 * (pg / quarter) % wide;
+          if (c >= wide) c -= wide;
+          r.leave(s_part + pg * wide + c, step);
+        } else {
+          r.store(out + c0);
+        }
+      }
       if constexpr (SPLIT) {
-        int c = cl * VEC + 8 * (pg / quarter) % wide;
-        if (c >= wide) c -= wide;
-        r.leave(s_part + pg * wide + c, step);
-      } else {
-        r.store(out + c0);
+        __syncthreads();
+        if (tid < per)
+          for (int c = tid / J, j = tid % J; c < wide && blockIdx.y * wide + c < p.d; c += per / J) {
+            int from = c + 8 * j % wide;
+            if (from >= wide) from -= wide;
+            join_parts(s_part + j * quarter * wide + from, step, wide, quarter, out + blockIdx.y * wide + c);
+          }
+        __syncthreads();
       }
     }
-    if constexpr (SPLIT) {
-      __syncthreads();
-      if (tid < per)
-        for (int c = tid / J, j = tid % J; c < wide && blockIdx.y * wide + c < p.d; c += per / J) {
-          int from = c + 8 * j % wide;
-          if (from >= wide) from -= wide;
-          join_parts(s_part + j * quarter * wide + from, step, wide, quarter, out + blockIdx.y * wide + c);
-        }
-      __syncthreads();
-    }
   }
-  // (the state was read by this thread, or before the last barrier)
+  // (the states were read by this thread, or before the last barrier)
   if (from0 < end) keep_store(0, from0, k0, x0);
   if (from1 < end) keep_store(1, from1, k1, x1);
   for (int half = 0; half < p.coff && keeps; ++half)
-    for (int pos = (half == 0 ? from0 : from1) + p.PG; pos < end; pos += p.PG) {
+    for (int pos = (half == 0 ? from0 : from1) + lines; pos < end; pos += lines) {
       keep_load(half, pos, k0, x0);
       keep_store(half, pos, k0, x0);
     }
-  // where the rows go; those behind the last entry
+  // where the rows go, by the last threads; those behind the last entry
   if (blockIdx.y != 0) return;
-  for (int i = static_cast<int>(blockDim.x) - 1 - tid; i < made; i += blockDim.x) describe_row(p, s, q.lo + i, before + i);
-  if (tid == static_cast<int>(blockDim.x) - 1 && p.entries != nullptr) p.entries[s] = max(0, q.hi - (p.base != nullptr ? __ldg(p.base + s) : 0));
-  for (int64_t o = all + static_cast<int64_t>(s) * blockDim.x + tid; o < p.out_rows; o += static_cast<int64_t>(p.S) * blockDim.x) no_row(p, o);
+  const int back = static_cast<int>(blockDim.x) - 1 - tid;
+  for (int s = s0, row = before; s < s1; ++s) {
+    const int lo = __ldg(p.first + s) / p.ratio, hi = (__ldg(p.first + s) + __ldg(p.cu + s + 1) - __ldg(p.cu + s)) / p.ratio;
+    for (int i = back; i < hi - lo; i += blockDim.x) describe_row(p, s, lo + i, row + i);
+    if (back == 0 && p.entries != nullptr) p.entries[s] = max(0, hi - (p.base != nullptr ? __ldg(p.base + s) : 0));
+    row += hi - lo;
+  }
+  for (int64_t o = all + static_cast<int64_t>(blockIdx.x) * blockDim.x + tid; o < p.out_rows; o += static_cast<int64_t>(gridDim.x) * blockDim.x)
+    no_row(p, o);
 }
 
 }  // namespace
@@ -800,9 +827,14 @@ extern "C" csa_status_t csa_compressor_step(
   if (slices > 65535) return CSA_ERR_UNSUPPORTED;
   void* args[] = {&p};
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  int dev = 0, sms = 0, bps = 0;
+  if (note(cudaGetDevice(&dev)) != cudaSuccess || device_sms(dev, &sms) != cudaSuccess) return CSA_ERR_CUDA;
   if (few) {
+    // as many sequences a CTA as leave about two CTAs an SM, no more than have lines of threads of their own
+    p.RS = 1;
+    while (2 * p.RS <= p.PG && static_cast<int64_t>(S) * slices > 2 * static_cast<int64_t>(sms) * p.RS) p.RS *= 2;
     const int block = (p.CL * p.PG + 31) / 32 * 32;
-    return launch_pdl(k, dim3(S, slices), dim3(block < 64 ? 64 : block), 0, cs, args) == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
+    return launch_pdl(k, dim3((S + p.RS - 1) / p.RS, slices), dim3(block < 64 ? 64 : block), 0, cs, args) == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
   }
   // three turns under way, fewer where many sequences' numbers need the room
   constexpr size_t kRoom = 224 * 1024;
@@ -811,10 +843,7 @@ extern "C" csa_status_t csa_compressor_step(
   p.stages = 3;
   while (p.stages > 1 && fixed + static_cast<size_t>(p.stages) * step_stage_bytes(width) > kRoom) --p.stages;
   const size_t smem = fixed + static_cast<size_t>(p.stages) * step_stage_bytes(width);
-  int dev = 0, sms = 0, bps = 0;
-  if (note(cudaGetDevice(&dev)) != cudaSuccess || device_sms(dev, &sms) != cudaSuccess ||
-      blocks_per_sm(dev, k, kStepThreads, smem, &bps) != cudaSuccess)
-    return CSA_ERR_CUDA;
+  if (blocks_per_sm(dev, k, kStepThreads, smem, &bps) != cudaSuccess) return CSA_ERR_CUDA;
   if (bps < 1) return CSA_ERR_UNSUPPORTED;
   const int64_t rows_at_once = p.RS * (split ? 1 : kStepFlight / uw), by_rows = (out_rows + rows_at_once - 1) / rows_at_once;
   const int64_t by_seqs = (S + p.RS - 1) / p.RS;
