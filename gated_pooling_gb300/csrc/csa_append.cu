@@ -39,6 +39,13 @@ __device__ __forceinline__ int64_t append_slot(const AppendParams& p, int64_t ro
   return -1;
 }
 
+// The largest magnitude of three, NaN if one is.
+__device__ __forceinline__ float max_magnitude(float a, float b, float c) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // Scalar kernel, any d and alignment: a warp per row and head, which leaves the finished row in shared
 // memory and then takes it 32 columns, a scale's, at a time.
 template <int DTYPE, int FORMAT>
@@ -104,20 +111,24 @@ __global__ void __launch_bounds__(kRopeThreads) append_scalar_kernel(AppendParam
 // Vector kernel: lanes, pieces and runs as in the norm and rotation's. A scale belongs to four
 // pieces of 8 columns, which the rotation's pairing leaves with any lanes; the pieces' largest
 // magnitudes meet in shared memory, 4 bytes a piece, and each lane reads its group's four at once.
-template <int DTYPE, int PP, int FORMAT>
+// Bound by instructions (24571 entries of 512 into e4m3), so what a lane has is told apart as little as can be: FULL,
+// every lane has all its pieces.
+template <int DTYPE, int PP, int FORMAT, bool FULL>
 __global__ void __launch_bounds__(kRopeThreads, PP == 1 && DTYPE != CSA_DTYPE_FP32 ? 3 : 2)
-    append_vec_kernel(AppendParams q) {
+    append_vec_kernel(const __grid_constant__ AppendParams q) {
+  using T = typename Element<DTYPE>::T;
   __shared__ __align__(16) float s_w[CSA_MAX_HEAD_DIM];
   __shared__ __align__(16) uint32_t s_top[kRopeWarps][64 * PP];
+  __shared__ __align__(16) float2 s_turn[kRopeWarps][256 * PP];  // cos and sin of each group's row, pair by pair
   const RopeParams& p = q.r;
   RopeLane<DTYPE, PP> L(p);
-  uint32_t* top = s_top[threadIdx.x >> 5] + L.group * (p.d / 8);
+  uint32_t* const top = s_top[threadIdx.x >> 5] + L.group * (p.d / 8);
   pdl_wait();
   stage_weight(p, s_w);
   const float inv_d = 1.f / static_cast<float>(p.d);
   RopeRun run(p, L.group, L.groups);
   int64_t base = run.u - L.group;  // the warp's first unit: all its lanes leave the loop together
-  RopePieces<DTYPE, PP> cur, nxt;
+  RopePieces<DTYPE, PP> cur{}, nxt{};  // (pieces that a lane does not have stay 0)
   int32_t pos = -1, pos_n = -1;
   int64_t slot = -1, slot_n = -1;
   auto fetch = [&](RopePieces<DTYPE, PP>& v, int32_t& ps, int64_t& at) {
@@ -125,17 +136,23 @@ __global__ void __launch_bounds__(kRopeThreads, PP == 1 && DTYPE != CSA_DTYPE_FP
     at = -1;
     if (run.valid()) {
       ps = p.pos != nullptr ? __ldg(p.pos + run.row) : 0;
-      at = append_slot(q, run.row, ps);
-      v.load(L, p.x, run.row * p.x_row + run.head * p.x_head);
+      at = __ldg(q.slots + run.row);
+      const T* x = static_cast<const T*>(p.x) + run.row * p.x_row + run.head * p.x_head;
+#pragma unroll
+      for (int s = 0; s < PP; ++s) {
+        if (FULL || L.a[s] >= 0) v.a[s].load(x + L.a[s]);
+        if (FULL || L.b[s] >= 0) v.b[s].load(x + L.b[s]);
+      }
     }
   };
   fetch(cur, pos, slot);
-  int64_t turned = -1;
+  int turned = -1;
   for (; base < run.end; base += L.groups) {
-    const int64_t row = run.row;
-    const int head = run.head;
+    const int row = static_cast<int>(run.row), head = run.head;
     run.next(p, L.groups);
     fetch(nxt, pos_n, slot_n);
+    const bool live = pos >= 0 && static_cast<uint64_t>(slot) < static_cast<uint64_t>(q.num_slots);
+    if (pos >= 0 && slot >= q.num_slots && q.dev_error != nullptr) *q.dev_error = CSA_DEVERR_SLOT;
     float xa[PP][8], xb[PP][8];
     float ss = 0.f;
 #pragma unroll
@@ -144,33 +161,59 @@ __global__ void __launch_bounds__(kRopeThreads, PP == 1 && DTYPE != CSA_DTYPE_FP
       cur.b[s].get(xb[s]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        if (L.a[s] >= 0) ss = fmaf(xa[s][i], xa[s][i], ss);
-        if (L.b[s] >= 0) ss = fmaf(xb[s][i], xb[s][i], ss);
+        ss = fmaf(xa[s][i], xa[s][i], ss);
+        ss = fmaf(xb[s][i], xb[s][i], ss);
       }
     }
-    const float r = p.norm ? __frsqrt_rn(fmaf(L.sum(p, ss), inv_d, p.eps)) : 1.f;
-    if (slot >= 0) {
-      if (row != turned) {
-        L.template turn_to<CSA_DTYPE_FP32>(p, pos);
-        turned = row;
+    // A row's angles are worked out by all lanes of its heads, or of the warp where it has one row, whichever
+    // turn columns by them (with 64 of 512 columns turned, four at a time in eight lanes took as long as the
+    // rest).
+    if (p.rot > 0 && __any_sync(0xFFFFFFFFu, live && row != turned)) {
+      const bool one = __all_sync(0xFFFFFFFFu, row == __shfl_sync(0xFFFFFFFFu, row, 0));
+      const int32_t at = one ? __shfl_sync(0xFFFFFFFFu, pos, 0) : pos;
+      float2* turn = s_turn[threadIdx.x >> 5] + (one ? 0 : L.group * (p.rot / 2));
+      for (int i = one ? L.lane : L.sub; i < p.rot / 2; i += one ? 32 : p.lanes) {
+        float c, n;
+        turn_cos_sin(at, __ldg(p.turns + i), p.amp, c, n);
+        turn[i] = make_float2(c, n);
       }
+      __syncwarp();
+      L.read_turns(p, turn);
+      turned = row;
+      __syncwarp();
+    }
+    if (p.norm) {
+      const float r = __frsqrt_rn(fmaf(L.sum(p, ss), inv_d, p.eps));
 #pragma unroll
       for (int s = 0; s < PP; ++s) {
-        if (p.norm) {
-          float w[8];
-          if (L.a[s] >= 0) {
-            read_weight(s_w, L.a[s], w);
+        float w[8];
+        read_weight(s_w, FULL ? L.a[s] : max(L.a[s], 0), w);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) xa[s][i] = xa[s][i] * r * w[i];
-          }
-          if (L.b[s] >= 0) {
-            read_weight(s_w, L.b[s], w);
+        for (int i = 0; i < 8; ++i) xa[s][i] = xa[s][i] * r * w[i];
+        read_weight(s_w, FULL ? L.b[s] : max(L.b[s], 0), w);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) xb[s][i] = xb[s][i] * r * w[i];
-          }
-        }
-        L.template turn<false>(p, s, xa[s], xb[s]);
+        for (int i = 0; i < 8; ++i) xb[s][i] = xb[s][i] * r * w[i];
       }
+    }
+#pragma unroll
+    for (int s = 0; s < PP; ++s) {
+      auto turn_pair = [](float& u, float& v, float c, float n) {
+        const float w = u * c - v * n;
+        v = u * n + v * c;
+        u = w;
+      };
+      if (!p.interleaved) {
+        if (L.ia[s] >= 0)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) turn_pair(xa[s][i], xb[s][i], L.cs[s][i], L.sn[s][i]);
+        continue;
+      }
+      if (L.ia[s] >= 0)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) turn_pair(xa[s][2 * i], xa[s][2 * i + 1], L.cs[s][i], L.sn[s][i]);
+      if (L.ib[s] >= 0)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) turn_pair(xb[s][2 * i], xb[s][2 * i + 1], L.cs[s][4 + i], L.sn[s][4 + i]);
     }
     const int64_t entry = slot * p.heads + head;
     if constexpr (FORMAT == CSA_CACHE_BF16) {
@@ -178,29 +221,26 @@ __global__ void __launch_bounds__(kRopeThreads, PP == 1 && DTYPE != CSA_DTYPE_FP
 #pragma unroll
       for (int s = 0; s < PP; ++s) {
         Eight<CSA_DTYPE_BF16> o;
-        if (slot >= 0 && L.a[s] >= 0) {
-          o.set(xa[s]);
-          o.store(y + L.a[s]);
-        }
-        if (slot >= 0 && L.b[s] >= 0) {
-          o.set(xb[s]);
-          o.store(y + L.b[s]);
-        }
+        o.set(xa[s]);
+        if (live && (FULL || L.a[s] >= 0)) o.store(y + L.a[s]);
+        o.set(xb[s]);
+        if (live && (FULL || L.b[s] >= 0)) o.store(y + L.b[s]);
       }
     } else {
-      auto largest = [](const float (&v)[8]) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-        return m;
+      auto largest = [](const float (&v)[8]) {  // (NaN if one is)
+        const float a = max_magnitude(v[0], v[1], v[2]), b = max_magnitude(v[3], v[4], v[5]);
+        return __float_as_uint(max_magnitude(max_magnitude(a, b, v[6]), v[7], v[7])) & 0x7FFFFFFFu;
       };
 #pragma unroll
       for (int s = 0; s < PP; ++s) {
-        if (L.a[s] >= 0) top[L.a[s] >> 3] = largest(xa[s]);
-        if (L.b[s] >= 0) top[L.b[s] >> 3] = largest(xb[s]);
+        if (FULL || L.a[s] >= 0) top[L.a[s] >> 3] = largest(xa[s]);
+        if (FULL || L.b[s] >= 0) top[L.b[s] >> 3] = largest(xb[s]);
       }
       __syncwarp();
+      uint8_t* const data = q.data + entry * (FORMAT == CSA_CACHE_E4M3 ? p.d : p.d / 2);
+      uint8_t* const scales = q.scales + entry * (p.d / CSA_CACHE_GROUP);
       auto put = [&](int col, const float (&v)[8]) {
+        if (!FULL && col < 0) return;
         const uint4 g = *reinterpret_cast<const uint4*>(top + (col >> 5) * 4);
         const uint32_t k = scale_byte<FORMAT>(max(max(g.x, g.y), max(g.z, g.w)));
         const float inv = scale_inverse(k == 255u ? 127u : k);
@@ -208,20 +248,18 @@ __global__ void __launch_bounds__(kRopeThreads, PP == 1 && DTYPE != CSA_DTYPE_FP
           uint2 w;
           w.x = float2_to_e4m3x2(v[0] * inv, v[1] * inv) | (static_cast<uint32_t>(float2_to_e4m3x2(v[2] * inv, v[3] * inv)) << 16);
           w.y = float2_to_e4m3x2(v[4] * inv, v[5] * inv) | (static_cast<uint32_t>(float2_to_e4m3x2(v[6] * inv, v[7] * inv)) << 16);
-          *reinterpret_cast<uint2*>(q.data + entry * p.d + col) = w;
+          if (live) *reinterpret_cast<uint2*>(data + col) = w;
         } else {
-          *reinterpret_cast<uint32_t*>(q.data + entry * (p.d / 2) + col / 2) =
-              float2_to_e2m1x2(v[0] * inv, v[1] * inv) | (float2_to_e2m1x2(v[2] * inv, v[3] * inv) << 8) |
-              (float2_to_e2m1x2(v[4] * inv, v[5] * inv) << 16) | (float2_to_e2m1x2(v[6] * inv, v[7] * inv) << 24);
+          const uint32_t w = float2_to_e2m1x2(v[0] * inv, v[1] * inv) | (float2_to_e2m1x2(v[2] * inv, v[3] * inv) << 8) |
+                             (float2_to_e2m1x2(v[4] * inv, v[5] * inv) << 16) | (float2_to_e2m1x2(v[6] * inv, v[7] * inv) << 24);
+          if (live) *reinterpret_cast<uint32_t*>(data + col / 2) = w;
         }
-        if ((col & 31) == 0) q.scales[entry * (p.d / CSA_CACHE_GROUP) + col / CSA_CACHE_GROUP] = static_cast<uint8_t>(k);
+        if (live && (col & 31) == 0) scales[col >> 5] = static_cast<uint8_t>(k);
       };
-      if (slot >= 0) {
 #pragma unroll
-        for (int s = 0; s < PP; ++s) {
-          if (L.a[s] >= 0) put(L.a[s], xa[s]);
-          if (L.b[s] >= 0) put(L.b[s], xb[s]);
-        }
+      for (int s = 0; s < PP; ++s) {
+        put(L.a[s], xa[s]);
+        put(L.b[s], xb[s]);
       }
       __syncwarp();
     }
@@ -276,13 +314,14 @@ extern "C" csa_status_t csa_cache_append(const void* x, int32_t dtype, int64_t r
   p.slots = slots;
   p.num_slots = num_slots;
   p.dev_error = dev_error;
-  const bool wide = vector_pairs(p.r) == 2;
+  const bool wide = vector_pairs(p.r) == 2, full = d / 8 == 2 * p.r.lanes;
   const void* k = by_dtype(dtype, [&](auto t) {
     return by_format(format, [&](auto f) {
       constexpr int T = decltype(t)::value, F = decltype(f)::value;
       return p.r.lanes == 0 ? reinterpret_cast<const void*>(append_scalar_kernel<T, F>)
-             : wide         ? reinterpret_cast<const void*>(append_vec_kernel<T, 2, F>)
-                            : reinterpret_cast<const void*>(append_vec_kernel<T, 1, F>);
+             : wide         ? reinterpret_cast<const void*>(append_vec_kernel<T, 2, F, false>)
+             : full         ? reinterpret_cast<const void*>(append_vec_kernel<T, 1, F, true>)
+                            : reinterpret_cast<const void*>(append_vec_kernel<T, 1, F, false>);
     });
   });
   // one run of heads a resident warp

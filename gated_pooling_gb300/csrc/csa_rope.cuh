@@ -129,8 +129,7 @@ struct RopeLane {
     }
   }
 
-  // the angles of a row, as for results of type ANGLES
-  template <int ANGLES = DTYPE>
+  // the angles of a row
   __device__ __forceinline__ void turn_to(const RopeParams& p, int32_t pos) {
 #pragma unroll
     for (int s = 0; s < PP; ++s) {
@@ -142,8 +141,28 @@ struct RopeLane {
 #pragma unroll
         for (int i = 0; i < 4; i += 2) {
           const ulonglong2 per = __ldg(reinterpret_cast<const ulonglong2*>(p.turns + i0 + i));
-          cos_sin<ANGLES>(pos, per.x, p.amp, cs[s][4 * h + i], sn[s][4 * h + i]);
-          cos_sin<ANGLES>(pos, per.y, p.amp, cs[s][4 * h + i + 1], sn[s][4 * h + i + 1]);
+          cos_sin<DTYPE>(pos, per.x, p.amp, cs[s][4 * h + i], sn[s][4 * h + i]);
+          cos_sin<DTYPE>(pos, per.y, p.amp, cs[s][4 * h + i + 1], sn[s][4 * h + i + 1]);
+        }
+      }
+    }
+  }
+  // the same from a list of each pair's cos and sin
+  __device__ __forceinline__ void read_turns(const RopeParams& p, const float2* list) {
+#pragma unroll
+    for (int s = 0; s < PP; ++s) {
+      if (ia[s] < 0 && ib[s] < 0) continue;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int i0 = h == 0 ? ia[s] : (p.interleaved ? ib[s] : ia[s] + 4);
+        if (i0 < 0) continue;
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+          const float4 v = *reinterpret_cast<const float4*>(list + i0 + i);
+          cs[s][4 * h + i] = v.x;
+          sn[s][4 * h + i] = v.y;
+          cs[s][4 * h + i + 1] = v.z;
+          sn[s][4 * h + i + 1] = v.w;
         }
       }
     }
