@@ -27,6 +27,7 @@ struct AppendParams {
   const int64_t* slots;
   int64_t num_slots;
   int32_t* dev_error;
+  int each, more;  // vector kernel: heads of a warp, and the first warps that have one more
 };
 
 // A row's slot, -1 where the row is left out (a negative position or slot, or one past the pool, which is
@@ -37,6 +38,27 @@ __device__ __forceinline__ int64_t append_slot(const AppendParams& p, int64_t ro
   if (s < p.num_slots) return s;
   if (p.dev_error != nullptr) *p.dev_error = CSA_DEVERR_SLOT;
   return -1;
+}
+
+// cos and sin of a turn, times amp, without a branch: the nearest quarter of a turn is taken off the 32-bit fraction
+// exactly, what is left, at most pi / 4 either way, goes through Taylor's series (the next terms are below 2e-9 and
+// 3e-8), and the quarter swaps them and sets their signs.
+__device__ __forceinline__ void quarter_cos_sin(int32_t pos, uint64_t per, float amp, float& c, float& s) {
+  const uint64_t t = static_cast<uint64_t>(static_cast<int64_t>(pos)) * per;
+  const uint32_t whole = static_cast<uint32_t>(t >> 32), q = (whole + 0x20000000u) >> 30;
+  const float x = static_cast<float>(static_cast<int32_t>(whole - (q << 30))) * 1.46291807926715968105e-9f;  // pi 2^-31
+  const float y = x * x;
+  float a = fmaf(y, 1.f / 362880.f, -1.f / 5040.f);
+  a = fmaf(y, a, 1.f / 120.f);
+  a = fmaf(y, a, -1.f / 6.f);
+  a = fmaf(x * y, a, x);
+  float b = fmaf(y, 1.f / 40320.f, -1.f / 720.f);
+  b = fmaf(y, b, 1.f / 24.f);
+  b = fmaf(y, b, -0.5f);
+  b = fmaf(y, b, 1.f);
+  const bool odd = (q & 1u) != 0;
+  c = (odd ? a : b) * __uint_as_float(__float_as_uint(amp) ^ (((q + 1u) & 2u) << 30));
+  s = (odd ? b : a) * __uint_as_float(__float_as_uint(amp) ^ ((q & 2u) << 30));
 }
 
 // The largest magnitude of three, NaN if one is.
@@ -79,7 +101,7 @@ __global__ void __launch_bounds__(kRopeThreads) append_scalar_kernel(AppendParam
       int a, b;
       pair_columns(p, i, a, b);
       float cs, sn;
-      turn_cos_sin(pos, __ldg(p.turns + i), p.amp, cs, sn);
+      quarter_cos_sin(pos, __ldg(p.turns + i), p.amp, cs, sn);
       const float va = n[a], vb = n[b];
       n[a] = va * cs - vb * sn;
       n[b] = va * sn + vb * cs;
@@ -108,6 +130,41 @@ __global__ void __launch_bounds__(kRopeThreads) append_scalar_kernel(AppendParam
   }
 }
 
+// A warp's run of heads (of less than 2^31, as RopeRun): this lane's row and head, and where its x begins, moving on
+// by the warp's groups with additions alone.
+template <typename T>
+struct AppendRun {
+  int u, end, row, head;  // unit of this lane's group, end of the warp's run
+  const T* x;
+  int groups, step_rows, step_heads;
+  int64_t step, wrap;
+  __device__ __forceinline__ AppendRun(const AppendParams& q, int group, int n) : groups(n) {
+    const RopeParams& p = q.r;
+    const int w = blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
+    u = w * q.each + min(w, q.more);
+    end = u + q.each + (w < q.more ? 1 : 0);
+    u += group;
+    row = p.heads == 1 ? u : u / p.heads;
+    head = u - row * p.heads;
+    step_rows = p.heads == 1 ? groups : groups / p.heads;
+    step_heads = groups - step_rows * p.heads;
+    x = static_cast<const T*>(p.x) + row * p.x_row + head * p.x_head;
+    step = step_rows * p.x_row + step_heads * p.x_head;
+    wrap = p.x_row - p.heads * p.x_head;
+  }
+  __device__ __forceinline__ void next(const RopeParams& p) {
+    u += groups;
+    row += step_rows;
+    head += step_heads;
+    x += step;
+    if (head >= p.heads) {
+      head -= p.heads;
+      ++row;
+      x += wrap;
+    }
+  }
+};
+
 // Vector kernel: lanes, pieces and runs as in the norm and rotation's. A scale belongs to four
 // pieces of 8 columns, which the rotation's pairing leaves with any lanes; the pieces' largest
 // magnitudes meet in shared memory, 4 bytes a piece, and each lane reads its group's four at once.
@@ -126,30 +183,29 @@ __global__ void __launch_bounds__(kRopeThreads, PP == 1 && DTYPE != CSA_DTYPE_FP
   pdl_wait();
   stage_weight(p, s_w);
   const float inv_d = 1.f / static_cast<float>(p.d);
-  RopeRun run(p, L.group, L.groups);
-  int64_t base = run.u - L.group;  // the warp's first unit: all its lanes leave the loop together
+  AppendRun<T> run(q, L.group, L.groups);
+  int base = run.u - L.group;  // the warp's first unit: all its lanes leave the loop together
   RopePieces<DTYPE, PP> cur{}, nxt{};  // (pieces that a lane does not have stay 0)
   int32_t pos = -1, pos_n = -1;
   int64_t slot = -1, slot_n = -1;
   auto fetch = [&](RopePieces<DTYPE, PP>& v, int32_t& ps, int64_t& at) {
     ps = -1;
     at = -1;
-    if (run.valid()) {
+    if (run.u < run.end) {
       ps = p.pos != nullptr ? __ldg(p.pos + run.row) : 0;
       at = __ldg(q.slots + run.row);
-      const T* x = static_cast<const T*>(p.x) + run.row * p.x_row + run.head * p.x_head;
 #pragma unroll
       for (int s = 0; s < PP; ++s) {
-        if (FULL || L.a[s] >= 0) v.a[s].load(x + L.a[s]);
-        if (FULL || L.b[s] >= 0) v.b[s].load(x + L.b[s]);
+        if (FULL || L.a[s] >= 0) v.a[s].load(run.x + L.a[s]);
+        if (FULL || L.b[s] >= 0) v.b[s].load(run.x + L.b[s]);
       }
     }
   };
   fetch(cur, pos, slot);
   int turned = -1;
   for (; base < run.end; base += L.groups) {
-    const int row = static_cast<int>(run.row), head = run.head;
-    run.next(p, L.groups);
+    const int row = run.row, head = run.head;
+    run.next(p);
     fetch(nxt, pos_n, slot_n);
     const bool live = pos >= 0 && static_cast<uint64_t>(slot) < static_cast<uint64_t>(q.num_slots);
     if (pos >= 0 && slot >= q.num_slots && q.dev_error != nullptr) *q.dev_error = CSA_DEVERR_SLOT;
@@ -174,7 +230,7 @@ __global__ void __launch_bounds__(kRopeThreads, PP == 1 && DTYPE != CSA_DTYPE_FP
       float2* turn = s_turn[threadIdx.x >> 5] + (one ? 0 : L.group * (p.rot / 2));
       for (int i = one ? L.lane : L.sub; i < p.rot / 2; i += one ? 32 : p.lanes) {
         float c, n;
-        turn_cos_sin(at, __ldg(p.turns + i), p.amp, c, n);
+        quarter_cos_sin(at, __ldg(p.turns + i), p.amp, c, n);
         turn[i] = make_float2(c, n);
       }
       __syncwarp();
@@ -183,7 +239,7 @@ __global__ void __launch_bounds__(kRopeThreads, PP == 1 && DTYPE != CSA_DTYPE_FP
       __syncwarp();
     }
     if (p.norm) {
-      const float r = __frsqrt_rn(fmaf(L.sum(p, ss), inv_d, p.eps));
+      const float r = rsqrtf(fmaf(L.sum(p, ss), inv_d, p.eps));
 #pragma unroll
       for (int s = 0; s < PP; ++s) {
         float w[8];
@@ -333,6 +389,8 @@ extern "C" csa_status_t csa_cache_append(const void* x, int32_t dtype, int64_t r
   const int64_t per = kRopeWarps * (p.r.lanes == 0 ? 1 : 32 / p.r.lanes), most = static_cast<int64_t>(sms) * bps;
   int64_t blocks = (p.r.units + per - 1) / per;
   if (blocks > most) blocks = most;
+  p.each = static_cast<int>(p.r.units / (blocks * kRopeWarps));
+  p.more = static_cast<int>(p.r.units - p.each * blocks * kRopeWarps);
   void* args[] = {&p};
   return launch_pdl(k, dim3(static_cast<unsigned>(blocks)), dim3(kRopeThreads), smem,
                     reinterpret_cast<cudaStream_t>(stream), args) == cudaSuccess
