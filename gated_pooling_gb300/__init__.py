@@ -1,8 +1,9 @@
 """GB300 (sm_103a) CSA/HCA KV-compressor gated-softmax pooling over THD packs.
 
-A thin ctypes binding of the C ABI in ``include/csa_compressor.h``: the functions
+A thin binding of the C ABI in ``include/csa_compressor.h``: the functions
 below have the C names and arguments, and only marshal them (tensor -> device
-pointer, stream -> cudaStream_t). Every step of the pooling runs in the library's
+pointer, stream -> cudaStream_t), those that enqueue work through a small module of
+their own, the others through ctypes. Every step of the pooling runs in the library's
 CUDA kernels. There is no fallback: if the library is missing, loading raises.
 
 Tensors are torch CUDA tensors (bf16 for kv/score/dout/out/dkv/dscore and the KPool
@@ -12,6 +13,7 @@ only provides device memory and streams.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 from typing import Optional
 
@@ -127,6 +129,21 @@ def _ptr(x) -> Optional[int]:
     return x.data_ptr()
 
 
+_calls = None
+
+
+def _load_calls():
+    """The module that the functions below call the library through (csrc/csa_call.cpp); it and ctypes
+    share one library."""
+    global _calls
+    load()
+    spec = importlib.util.spec_from_file_location("_csa_call", _build.CALL)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    _calls = module
+    return module
+
+
 _raw_stream = None
 
 
@@ -180,9 +197,8 @@ def csa_compressor_total_comp(cu_seqlens_host, S: int, ratio: int) -> int:
 
 def csa_compressor_fwd(kv, score, ape, cu_seqlens, S: int, ratio: int, coff: int, d: int,
                        capacity: int, out, out_rows: int, dev_error=None, stream=None) -> None:
-    _check(load().csa_compressor_fwd(_ptr(kv), _ptr(score), _ptr(ape), _ptr(cu_seqlens), S,
-                                     ratio, coff, d, capacity, _ptr(out), out_rows,
-                                     _ptr(dev_error), _stream(stream)), "csa_compressor_fwd")
+    _check((_calls or _load_calls()).csa_compressor_fwd(kv, score, ape, cu_seqlens, S, ratio, coff, d,
+        capacity, out, out_rows, dev_error, _stream(stream)), "csa_compressor_fwd")
 
 
 def csa_compressor_bwd_workspace_bytes(S: int, ratio: int, coff: int, d: int, capacity: int,
@@ -193,11 +209,9 @@ def csa_compressor_bwd_workspace_bytes(S: int, ratio: int, coff: int, d: int, ca
 def csa_compressor_bwd(kv, score, ape, cu_seqlens, dout, S: int, ratio: int, coff: int, d: int,
                        capacity: int, out_rows: int, dkv, dscore, dape, accumulate_dape: int,
                        workspace, workspace_bytes: int, dev_error=None, stream=None) -> None:
-    _check(load().csa_compressor_bwd(_ptr(kv), _ptr(score), _ptr(ape), _ptr(cu_seqlens),
-                                     _ptr(dout), S, ratio, coff, d, capacity, out_rows, _ptr(dkv),
-                                     _ptr(dscore), _ptr(dape), int(accumulate_dape),
-                                     _ptr(workspace), workspace_bytes, _ptr(dev_error),
-                                     _stream(stream)), "csa_compressor_bwd")
+    _check((_calls or _load_calls()).csa_compressor_bwd(kv, score, ape, cu_seqlens, dout, S, ratio, coff, d,
+        capacity, out_rows, dkv, dscore, dape, int(accumulate_dape), workspace, workspace_bytes, dev_error,
+        _stream(stream)), "csa_compressor_bwd")
 
 
 def csa_compressor_bwd_noalloc(kv, score, ape, cu_seqlens, dout, S: int, ratio: int, coff: int,
@@ -205,11 +219,9 @@ def csa_compressor_bwd_noalloc(kv, score, ape, cu_seqlens, dout, S: int, ratio: 
                                accumulate_dape: int, dev_error=None, stream=None) -> None:
     """Backward without a caller workspace, for callers that cannot allocate device
     memory; see include/csa_compressor.h for the shared scratch array's rules."""
-    _check(load().csa_compressor_bwd_noalloc(_ptr(kv), _ptr(score), _ptr(ape), _ptr(cu_seqlens),
-                                             _ptr(dout), S, ratio, coff, d, capacity, out_rows,
-                                             _ptr(dkv), _ptr(dscore), _ptr(dape),
-                                             int(accumulate_dape), _ptr(dev_error),
-                                             _stream(stream)), "csa_compressor_bwd_noalloc")
+    _check((_calls or _load_calls()).csa_compressor_bwd_noalloc(kv, score, ape, cu_seqlens, dout, S, ratio,
+        coff, d, capacity, out_rows, dkv, dscore, dape, int(accumulate_dape), dev_error, _stream(stream)),
+        "csa_compressor_bwd_noalloc")
 
 
 def csa_compressor_test_hooks(wait_cycles: int, withhold_row: int) -> None:
@@ -221,9 +233,8 @@ def csa_compressor_test_hooks(wait_cycles: int, withhold_row: int) -> None:
 
 def csa_compressor_map_blocks(cu_seqlens, S: int, ratio: int, capacity: int, out_rows: int,
                               seg_blk_base, dev_error=None, stream=None) -> None:
-    _check(load().csa_compressor_map_blocks(_ptr(cu_seqlens), S, ratio, capacity, out_rows,
-                                            _ptr(seg_blk_base), _ptr(dev_error),
-                                            _stream(stream)), "csa_compressor_map_blocks")
+    _check((_calls or _load_calls()).csa_compressor_map_blocks(cu_seqlens, S, ratio, capacity, out_rows,
+        seg_blk_base, dev_error, _stream(stream)), "csa_compressor_map_blocks")
 
 
 def csa_kpool_total(cu_seqlens_host, lead_host, S: int, pool: int) -> int:
@@ -244,9 +255,8 @@ def csa_kpool_total(cu_seqlens_host, lead_host, S: int, pool: int) -> int:
 def csa_kpool_fwd(key, gate, cu_seqlens, lead, S: int, pool: int, d: int, capacity: int, out,
                   out_rows: int, compress: int = 0, dev_error=None, stream=None) -> None:
     """KPool forward (the DSA indexer's key pooling); ``lead`` may be None."""
-    _check(load().csa_kpool_fwd(_ptr(key), _ptr(gate), _ptr(cu_seqlens), _ptr(lead), S, pool, d,
-                                capacity, _ptr(out), out_rows, int(compress), _ptr(dev_error),
-                                _stream(stream)), "csa_kpool_fwd")
+    _check((_calls or _load_calls()).csa_kpool_fwd(key, gate, cu_seqlens, lead, S, pool, d, capacity, out,
+        out_rows, int(compress), dev_error, _stream(stream)), "csa_kpool_fwd")
 
 
 
@@ -269,10 +279,9 @@ def csa_norm_rope_fwd(x, dtype: int, rows: int, heads: int, d: int, x_row_stride
                       rot_dim: int, rot_start: int, layout: int, amplitude: float, y,
                       y_row_stride: int, y_head_stride: int, stream=None) -> None:
     """Norm of every head and rotation to the row's position; strides in elements."""
-    _check(load().csa_norm_rope_fwd(_ptr(x), dtype, rows, heads, d, x_row_stride, x_head_stride,
-                                    _ptr(weight), int(norm), eps, _ptr(positions), _ptr(turns),
-                                    rot_dim, rot_start, layout, amplitude, _ptr(y), y_row_stride,
-                                    y_head_stride, _stream(stream)), "csa_norm_rope_fwd")
+    _check((_calls or _load_calls()).csa_norm_rope_fwd(x, dtype, rows, heads, d, x_row_stride,
+        x_head_stride, weight, int(norm), eps, positions, turns, rot_dim, rot_start, layout, amplitude, y,
+        y_row_stride, y_head_stride, _stream(stream)), "csa_norm_rope_fwd")
 
 
 def csa_norm_rope_bwd_workspace_bytes(rows: int, heads: int, d: int) -> int:
@@ -285,31 +294,26 @@ def csa_norm_rope_bwd(x, dy, dtype: int, rows: int, heads: int, d: int, x_row_st
                       layout: int, amplitude: float, dx, dx_row_stride: int, dx_head_stride: int,
                       dweight, accumulate_dweight: int, workspace, workspace_bytes: int,
                       stream=None) -> None:
-    _check(load().csa_norm_rope_bwd(_ptr(x), _ptr(dy), dtype, rows, heads, d, x_row_stride,
-                                    x_head_stride, dy_row_stride, dy_head_stride, _ptr(weight),
-                                    int(norm), eps, _ptr(positions), _ptr(turns), rot_dim,
-                                    rot_start, layout, amplitude, _ptr(dx), dx_row_stride,
-                                    dx_head_stride, _ptr(dweight), int(accumulate_dweight),
-                                    _ptr(workspace), workspace_bytes, _stream(stream)),
-           "csa_norm_rope_bwd")
+    _check((_calls or _load_calls()).csa_norm_rope_bwd(x, dy, dtype, rows, heads, d, x_row_stride,
+        x_head_stride, dy_row_stride, dy_head_stride, weight, int(norm), eps, positions, turns, rot_dim,
+        rot_start, layout, amplitude, dx, dx_row_stride, dx_head_stride, dweight, int(accumulate_dweight),
+        workspace, workspace_bytes, _stream(stream)), "csa_norm_rope_bwd")
 
 
 def csa_cache_write(x, dtype: int, rows: int, heads: int, d: int, x_row_stride: int,
                     x_head_stride: int, slots, num_slots: int, format: int, data, scales,
                     dev_error=None, stream=None) -> None:
     """Rows into slots of the paged cache, quantised as ``format`` says."""
-    _check(load().csa_cache_write(_ptr(x), dtype, rows, heads, d, x_row_stride, x_head_stride,
-                                  _ptr(slots), num_slots, format, _ptr(data), _ptr(scales),
-                                  _ptr(dev_error), _stream(stream)), "csa_cache_write")
+    _check((_calls or _load_calls()).csa_cache_write(x, dtype, rows, heads, d, x_row_stride, x_head_stride,
+        slots, num_slots, format, data, scales, dev_error, _stream(stream)), "csa_cache_write")
 
 
 def csa_cache_read(data, scales, format: int, slots, rows: int, num_slots: int, heads: int, d: int,
                    out, dtype: int, out_row_stride: int, out_head_stride: int, dev_error=None,
                    stream=None) -> None:
     """Slots of the paged cache back into rows of ``dtype``."""
-    _check(load().csa_cache_read(_ptr(data), _ptr(scales), format, _ptr(slots), rows, num_slots,
-                                 heads, d, _ptr(out), dtype, out_row_stride, out_head_stride,
-                                 _ptr(dev_error), _stream(stream)), "csa_cache_read")
+    _check((_calls or _load_calls()).csa_cache_read(data, scales, format, slots, rows, num_slots, heads, d,
+        out, dtype, out_row_stride, out_head_stride, dev_error, _stream(stream)), "csa_cache_read")
 
 
 def csa_cache_attn_workspace_bytes(S: int, tokens: int, q_heads: int, kv_heads: int, d: int,
@@ -323,13 +327,10 @@ def csa_cache_attn(q, q_row_stride: int, q_head_stride: int, cu_seqlens, S: int,
                    softmax_scale: float, sink, out, out_row_stride: int, out_head_stride: int,
                    lse, workspace, workspace_bytes: int, dev_error=None, stream=None) -> None:
     """New tokens over the paged cache, an entry being key and value at once."""
-    _check(load().csa_cache_attn(_ptr(q), q_row_stride, q_head_stride, _ptr(cu_seqlens), S, tokens,
-                                 q_heads, kv_heads, d, _ptr(data), _ptr(scales), format,
-                                 _ptr(page_table), max_pages, num_pages, page_size, _ptr(entries),
-                                 _ptr(first), ratio, softmax_scale, _ptr(sink), _ptr(out),
-                                 out_row_stride, out_head_stride, _ptr(lse), _ptr(workspace),
-                                 workspace_bytes, _ptr(dev_error), _stream(stream)),
-           "csa_cache_attn")
+    _check((_calls or _load_calls()).csa_cache_attn(q, q_row_stride, q_head_stride, cu_seqlens, S, tokens,
+        q_heads, kv_heads, d, data, scales, format, page_table, max_pages, num_pages, page_size, entries,
+        first, ratio, softmax_scale, sink, out, out_row_stride, out_head_stride, lse, workspace,
+        workspace_bytes, dev_error, _stream(stream)), "csa_cache_attn")
 
 
 def csa_compressor_step(kv, score, ape, cu_seqlens, S: int, ratio: int, coff: int, d: int,
@@ -339,12 +340,10 @@ def csa_compressor_step(kv, score, ape, cu_seqlens, S: int, ratio: int, coff: in
                         positions=None, slots=None, entries=None, dev_error=None,
                         stream=None) -> None:
     """New tokens of each sequence pooled on from a state, which is updated."""
-    _check(load().csa_compressor_step(_ptr(kv), _ptr(score), _ptr(ape), _ptr(cu_seqlens), S, ratio,
-                                      coff, d, capacity, _ptr(first), _ptr(source), _ptr(target),
-                                      num_states, _ptr(kv_state), _ptr(score_state), _ptr(out),
-                                      out_rows, _ptr(base), _ptr(page_table), max_pages, page_size,
-                                      position_offset, _ptr(positions), _ptr(slots), _ptr(entries),
-                                      _ptr(dev_error), _stream(stream)), "csa_compressor_step")
+    _check((_calls or _load_calls()).csa_compressor_step(kv, score, ape, cu_seqlens, S, ratio, coff, d,
+        capacity, first, source, target, num_states, kv_state, score_state, out, out_rows, base, page_table,
+        max_pages, page_size, position_offset, positions, slots, entries, dev_error, _stream(stream)),
+        "csa_compressor_step")
 
 
 def csa_cache_append(x, dtype: int, rows: int, heads: int, d: int, x_row_stride: int,
@@ -353,11 +352,9 @@ def csa_cache_append(x, dtype: int, rows: int, heads: int, d: int, x_row_stride:
                      num_slots: int, format: int, data, scales, dev_error=None,
                      stream=None) -> None:
     """Rows normed, turned to their positions and put into slots of the paged cache."""
-    _check(load().csa_cache_append(_ptr(x), dtype, rows, heads, d, x_row_stride, x_head_stride,
-                                   _ptr(weight), int(norm), eps, _ptr(positions), _ptr(turns),
-                                   rot_dim, rot_start, layout, amplitude, _ptr(slots), num_slots,
-                                   format, _ptr(data), _ptr(scales), _ptr(dev_error),
-                                   _stream(stream)), "csa_cache_append")
+    _check((_calls or _load_calls()).csa_cache_append(x, dtype, rows, heads, d, x_row_stride, x_head_stride,
+        weight, int(norm), eps, positions, turns, rot_dim, rot_start, layout, amplitude, slots, num_slots,
+        format, data, scales, dev_error, _stream(stream)), "csa_cache_append")
 
 
 def csa_cache_attn_prefix_workspace_bytes(S: int, G: int, tokens: int, q_heads: int, kv_heads: int, d: int,
@@ -373,11 +370,8 @@ def csa_cache_attn_prefix(q, q_row_stride: int, q_head_stride: int, cu_seqlens, 
                           softmax_scale: float, sink, out, out_row_stride: int, out_head_stride: int,
                           lse, workspace, workspace_bytes: int, dev_error=None, stream=None) -> None:
     """New tokens over the entries that a group of sequences shares and each sequence's own."""
-    _check(load().csa_cache_attn_prefix(_ptr(q), q_row_stride, q_head_stride, _ptr(cu_seqlens), S, tokens,
-                                        q_heads, kv_heads, d, _ptr(data), _ptr(scales), format,
-                                        _ptr(prefix_seqs), G, _ptr(prefix_table), max_prefix_pages,
-                                        _ptr(prefix_entries), _ptr(page_table), max_pages, num_pages,
-                                        page_size, _ptr(entries), _ptr(first), ratio, softmax_scale,
-                                        _ptr(sink), _ptr(out), out_row_stride, out_head_stride, _ptr(lse),
-                                        _ptr(workspace), workspace_bytes, _ptr(dev_error),
-                                        _stream(stream)), "csa_cache_attn_prefix")
+    _check((_calls or _load_calls()).csa_cache_attn_prefix(q, q_row_stride, q_head_stride, cu_seqlens, S,
+        tokens, q_heads, kv_heads, d, data, scales, format, prefix_seqs, G, prefix_table, max_prefix_pages,
+        prefix_entries, page_table, max_pages, num_pages, page_size, entries, first, ratio, softmax_scale,
+        sink, out, out_row_stride, out_head_stride, lse, workspace, workspace_bytes, dev_error,
+        _stream(stream)), "csa_cache_attn_prefix")

@@ -211,6 +211,9 @@ __global__ void __launch_bounds__(kPlanThreads) attn_prefix_plan_kernel(AttnPara
   const bool cached = p.S <= kPlanCached;
   if (threadIdx.x < 2) s_joins[threadIdx.x] = 0;
   pdl_wait();
+  // (one block, which leaves room for the next kernel's: they set themselves up meanwhile, and wait for this one's
+  // end before they read anything; 36.0 -> 34.8 us for 120 sequences of grouped heads)
+  asm volatile("griddepcontrol.launch_dependents;");
   int bad = 0;
   for (int g = threadIdx.x; g < G; g += kPlanThreads) {
     const int32_t a = __ldg(p.prefix_seqs + g), b = __ldg(p.prefix_seqs + g + 1), n = __ldg(p.prefix_entries + g);
@@ -615,13 +618,12 @@ bool chunked(const AttnParams& p) {
   if (p.d > kTileMaxDim || p.S < 1) return false;
   if (p.groups > 0) {
     // Behind prefixes: by the tiles that units read of prefixes and those that are packed, own entries too, at the
-    // tables' capacity. Measured over codes at d = 128, 256 and 512, packing saves 5, 8 and 17 ns a tile read and
-    // costs 27, 24 and 66 ns a tile packed, and a launch: 64 sequences of 64 heads of 512 behind 16384 entries
-    // take 193 us packed and 298 not, 16 57.8 and 67.6 behind 2048, but with up to 2000 own entries each 112
-    // and 89; 4 sequences 47.7 and 48.4.
+    // tables' capacity. Over codes, 64 sequences of 64 heads of 512 behind 16384 entries take 186 us packed and 297
+    // not, 64 54.5 and 68.3 behind 2048, but with up to 2000 own entries each 112 and 90; 4 sequences 45.8 and
+    // 48.6, one 43.1 and 38.4; of 128 columns 77 and 115, 31.5 and 34.4, 46.1 and 40.2; 26.7 and 25.4, 31.0 and 27.6.
     const int64_t units = (p.tokens * p.group + kAttnRows - 1) / kAttnRows, tiles = p.prefix_rows / kAttnEntries;
     const int64_t packed = p.groups * tiles + static_cast<int64_t>(p.S) * (p.packed_rows / kAttnEntries);
-    if (units * tiles < 4 * packed + 256) return false;
+    if (units * tiles < 2 * packed + 200) return false;
   } else if (p.tokens * p.group < kChunkRows * p.S) {
     return false;
   }
@@ -818,13 +820,14 @@ csa_status_t run_attn(const AttnCall& c, csa_stream_t stream) {
       // a few blocks an SM, which go on to their sequence's next entries: the table's capacity may
       // be far above what the sequences hold (behind prefixes a grid over all capacities, 33 thousand blocks for
       // 64 sequences, took 46 us)
-      const int64_t heads = static_cast<int64_t>(S) * kv_heads, most = p.packed_rows / kPackRows;
+      const int rows = pack_rows(nc, groups > 0);
+      const int64_t heads = static_cast<int64_t>(S) * kv_heads, most = p.packed_rows / rows;
       int64_t want = (16 * static_cast<int64_t>(sms) + heads - 1) / heads;
       want = want < most ? want : most;
       dim3 grid(static_cast<unsigned>(want), S, kv_heads);
       int prefix_blocks = 0;
       if (groups > 0) {
-        const int64_t steps = static_cast<int64_t>(groups) * kv_heads * (p.prefix_rows / kPackRows);
+        const int64_t steps = static_cast<int64_t>(groups) * kv_heads * (p.prefix_rows / rows);
         prefix_blocks = static_cast<int>(steps < 8 * sms ? steps : 8 * sms);
         want = (4 * static_cast<int64_t>(sms) + heads - 1) / heads;
         want = want < most ? want : most;

@@ -1100,48 +1100,71 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
 // rows) reads them again; packing reads and writes them once. Block (x, s, cache head): 32
 // entries at a time, a thread 8 columns at a time. Behind prefixes a row of blocks: prefix_blocks for all
 // prefixes, then the same number for each sequence and cache head.
-constexpr int kPackThreads = 256, kPackRows = 32;
+constexpr int kPackThreads = 256;
+// Entries at a time: 32, behind prefixes 32 to 128 of 64 KB in all, so that a thread has eight pieces under way
+// (32 of 128 columns each, two pieces a thread, took 21.5 us for 31 thousand entries of 4 heads).
+__host__ __device__ constexpr int pack_rows(int nc, bool prefix) { return prefix ? 256 / nc : 32; }
 template <int NC, int FORMAT, bool PREFIX>
 __global__ void __launch_bounds__(kPackThreads) attn_pack_kernel(const __grid_constant__ AttnParams p, int prefix_blocks) {
   constexpr int kPer = NC * 8;  // pieces of 8 columns
   pdl_wait();
   if (p.head->status != 0) return;
-  // 32 entries from e0 on of a run of n, whose first lies in row row0 of the packed ones
+  // kRows entries from e0 on of a run of n, whose first lies in row row0 of the packed ones
+  constexpr int kRows = pack_rows(NC, PREFIX), kAtOnce = PREFIX ? 8 : 4;
   auto pack = [&](const int32_t* table, int64_t row0, int kvh, int n, int e0) {
     uint16_t* to = p.packed + (row0 + e0) * (NC * 64);
-#pragma unroll 4
-    for (int i = threadIdx.x; i < kPackRows * kPer; i += kPackThreads) {
-      const int r = i / kPer, col = (i % kPer) * 8, e = e0 + r;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (e < n && col < p.d) {
-        const int page = __ldg(table + e / p.page_size);
-        if (page >= 0 && page < p.num_pages) {
-          const int64_t entry = (static_cast<int64_t>(page) * p.page_size + e % p.page_size) * p.kv_heads + kvh;
-          if constexpr (FORMAT == CSA_CACHE_BF16) {
-            v = __ldg(reinterpret_cast<const uint4*>(p.data + (entry * p.d + col) * 2));
-          } else {
-            const uint32_t k = __ldg(p.scales + entry * (p.d / CSA_CACHE_GROUP) + col / CSA_CACHE_GROUP);
-            if constexpr (FORMAT == CSA_CACHE_E4M3) {
-              const uint2 w = __ldg(reinterpret_cast<const uint2*>(p.data + entry * p.d + col));
-              v = Take<FORMAT>::widen(k, w.x, w.y);
-            } else {
-              v = Take<FORMAT>::widen(k, __ldg(reinterpret_cast<const uint32_t*>(p.data + entry * (p.d / 2) + col / 2)));
-            }
-          }
-        } else if (p.dev_error != nullptr) {
-          *p.dev_error = CSA_DEVERR_PAGE;
+#pragma unroll 1
+    for (int i0 = threadIdx.x; i0 < kRows * kPer; i0 += kAtOnce * kPackThreads) {
+      // pages, then codes, then rows: each step's loads side by side
+      int page[kAtOnce];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const int i = i0 + k * kPackThreads, e = e0 + i / kPer;
+        page[k] = e < n && (i % kPer) * 8 < p.d ? __ldg(table + e / p.page_size) : -1;
+        if (e < n && (page[k] < 0 || page[k] >= p.num_pages) && (i % kPer) * 8 < p.d) {
+          page[k] = -1;
+          if (p.dev_error != nullptr) *p.dev_error = CSA_DEVERR_PAGE;
         }
       }
-      *reinterpret_cast<uint4*>(to + r * (NC * 64) + col) = v;
+      uint4 v[kAtOnce];
+      uint32_t scale[kAtOnce];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const int i = i0 + k * kPackThreads, col = (i % kPer) * 8, e = e0 + i / kPer;
+        v[k] = make_uint4(0, 0, 0, 0);
+        scale[k] = kNoScale;
+        if (page[k] >= 0) {
+          const int64_t entry = (static_cast<int64_t>(page[k]) * p.page_size + e % p.page_size) * p.kv_heads + kvh;
+          if constexpr (FORMAT == CSA_CACHE_BF16) {
+            v[k] = __ldg(reinterpret_cast<const uint4*>(p.data + (entry * p.d + col) * 2));
+          } else {
+            scale[k] = __ldg(p.scales + entry * (p.d / CSA_CACHE_GROUP) + col / CSA_CACHE_GROUP);
+            if constexpr (FORMAT == CSA_CACHE_E4M3) {
+              const uint2 w = __ldg(reinterpret_cast<const uint2*>(p.data + entry * p.d + col));
+              v[k].x = w.x;
+              v[k].y = w.y;
+            } else {
+              v[k].x = __ldg(reinterpret_cast<const uint32_t*>(p.data + entry * (p.d / 2) + col / 2));
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const int i = i0 + k * kPackThreads;
+        if constexpr (FORMAT == CSA_CACHE_E4M3) v[k] = Take<FORMAT>::widen(scale[k], v[k].x, v[k].y);
+        if constexpr (FORMAT == CSA_CACHE_E2M1) v[k] = Take<FORMAT>::widen(scale[k], v[k].x);
+        *reinterpret_cast<uint4*>(to + (i / kPer) * (NC * 64) + (i % kPer) * 8) = v[k];
+      }
     }
   };
   auto rows_of = [](int n) { return max(kAttnEntries, (n + kAttnEntries - 1) / kAttnEntries * kAttnEntries); };
   int seq = blockIdx.y, kvh = blockIdx.z, x = blockIdx.x, wide = gridDim.x;
   if (PREFIX && x < prefix_blocks) {
-    // all prefixes and cache heads, in steps of 32 entries of the table's capacity, over the first blocks
-    const int steps = p.prefix_rows / kPackRows;
+    // all prefixes and cache heads, in steps of the table's capacity, over the first blocks
+    const int steps = p.prefix_rows / kRows;
     for (int64_t i = x; i < static_cast<int64_t>(p.groups) * p.kv_heads * steps; i += prefix_blocks) {
-      const int part = static_cast<int>(i / steps), e0 = static_cast<int>(i - static_cast<int64_t>(part) * steps) * kPackRows;
+      const int part = static_cast<int>(i / steps), e0 = static_cast<int>(i - static_cast<int64_t>(part) * steps) * kRows;
       const int g = part / p.kv_heads, n = __ldg(p.prefix_entries + g);
       if (e0 >= rows_of(n) || __ldg(p.cu + __ldg(p.prefix_seqs + g + 1)) == __ldg(p.cu + __ldg(p.prefix_seqs + g))) continue;
       pack(p.prefix_table + static_cast<int64_t>(g) * p.max_prefix_pages, static_cast<int64_t>(part) * p.prefix_rows,
@@ -1174,7 +1197,7 @@ __global__ void __launch_bounds__(kPackThreads) attn_pack_kernel(const __grid_co
   const int64_t row0 = (static_cast<int64_t>(seq) * p.kv_heads + kvh) * p.packed_rows +
                        (PREFIX ? static_cast<int64_t>(p.groups) * p.kv_heads * p.prefix_rows : 0);
   const int end = rows_of(n);
-  for (int e0 = x * kPackRows; e0 < end; e0 += wide * kPackRows)
+  for (int e0 = x * kRows; e0 < end; e0 += wide * kRows)
     pack(p.table + static_cast<int64_t>(seq) * p.max_pages, row0, kvh, n, e0);
 }
 

@@ -146,3 +146,33 @@ def test_code_check_takes_the_quantiser_and_refuses_a_step_off(fmt):
             c[3, 5] += 2 if (int(c[3, 5]) & mag) < mag - 2 else -2
         with pytest.raises(AssertionError):
             V.check_codes(c, s, fmt, x, torch.zeros_like(x))
+
+
+# ------------------------------------------------------------------------ calls from Python
+def python_append(**over):
+    a = dict(x=FAKE, dtype=0, rows=0, heads=2, d=64, x_row_stride=128, x_head_stride=64, weight=None, norm=1, eps=1e-6, positions=FAKE,
+             turns=FAKE, rot_dim=64, rot_start=0, layout=0, amplitude=1.0, slots=FAKE, num_slots=16, format=1, data=FAKE, scales=FAKE,
+             dev_error=None, stream=0)
+    a.update(over)
+    gp.csa_cache_append(**a)
+
+
+def test_python_calls_marshal_and_raise(lib):
+    t = torch.zeros(64)
+    python_append()                        # addresses and None
+    python_append(x=t, weight=t, slots=t)  # tensors
+    python_append(norm=True, eps=0, amplitude=1)
+    for over, code in ((dict(x=FAKE + 1), INVALID), (dict(d=72), UNSUPPORTED), (dict(weight=FAKE + 2), INVALID)):
+        with pytest.raises(gp.CsaError) as e:
+            python_append(**over)
+        assert e.value.status == code and "csa_cache_append" in str(e.value)
+    for over, kind in ((dict(heads=1 << 31), OverflowError), (dict(rows=1 << 63), OverflowError), (dict(x=-1), OverflowError),
+                       (dict(x="x"), AttributeError), (dict(d=1.5), TypeError), (dict(eps="1"), TypeError)):
+        with pytest.raises(kind):
+            python_append(**over)
+
+
+def test_python_calls_and_ctypes_share_one_library(lib):
+    python_append()
+    paths = {line.split()[-1] for line in open("/proc/self/maps") if "libcsa_compressor" in line}
+    assert len(paths) == 1
