@@ -56,32 +56,34 @@ __device__ __forceinline__ int64_t plan_scan(int64_t v, int64_t* warps, int64_t&
 
 // Where each worker's share of the units' work begins, and the units that several workers share. All threads
 // of the plan's block; `work`: where each unit's work begins, `all` of them together.
-// span_tile: behind prefixes the spans' first tiles, where shared memory holds them.
-__device__ __forceinline__ void plan_shares(const AttnParams& p, int64_t units, int64_t all, const int64_t* work, int* s_joins,
-                                            const int* span_tile) {
+// span_tile and held: behind prefixes the spans' first tiles and the units, where shared memory holds them. W: int
+// where all of the work fits it.
+template <typename W>
+__device__ __forceinline__ void plan_shares(const AttnParams& p, W units, W all, const W* work, int* s_joins,
+                                            const int* span_tile, const AttnUnit* held) {
   // the unit and tile that a place in the work stands for, and how many tiles lie before it
   struct Place {
-    int64_t unit, tile, before;
+    W unit, tile, before;
   };
-  auto place = [&](int64_t x) {
+  auto place = [&](W x) {
     if (x >= all) return Place{units, 0, all - units * p.unit_cost};
-    int64_t l = 0, h = units;  // work[l] <= x < work[h]
+    W l = 0, h = units;  // work[l] <= x < work[h]
     while (h - l > 1) {
-      const int64_t mid = (l + h) / 2;
+      const W mid = (l + h) / 2;
       if (work[mid] <= x) l = mid;
       else h = mid;
     }
-    const int64_t tile = x - work[l];
+    const W tile = x - work[l];
     if (tile >= work[l + 1] - work[l] - p.unit_cost) return Place{l + 1, 0, work[l + 1] - (l + 1) * p.unit_cost};  // behind the unit's last tile
     return Place{l, tile, x - l * p.unit_cost};
   };
   const AttnShares share(all, p.workers);
   for (int i = threadIdx.x; i < p.workers; i += kPlanThreads) {
-    const Place a = place(share(i)), b = place(share(i + 1));
+    const Place a = place(static_cast<W>(share(i))), b = place(static_cast<W>(share(i + 1)));
     AttnStart start{};
     start.left = b.before - a.before;
     if (start.left > 0) {
-      start.u = p.units[a.unit];
+      start.u = held != nullptr ? held[a.unit] : p.units[a.unit];
       start.unit = static_cast<int32_t>(a.unit);
       start.tile = static_cast<int32_t>(a.tile);
       if (p.groups > 0) {  // behind prefixes: the span that tile lies in
@@ -95,9 +97,9 @@ __device__ __forceinline__ void plan_shares(const AttnParams& p, int64_t units, 
       }
       // a unit that begins in this share and goes on in later ones
       if (b.tile > 0 && (b.unit > a.unit || a.tile == 0)) {
-        const int64_t end = work[b.unit + 1] - p.unit_cost;
+        const W end = work[b.unit + 1] - p.unit_cost;
         AttnJoin join{};
-        join.u = p.units[b.unit];
+        join.u = held != nullptr ? held[b.unit] : p.units[b.unit];
         join.worker = i;
         int last = max(i + 1, share.near(end - 1));  // the worker whose share the unit's last tile lies in
         while (share(last + 1) < end) ++last;
@@ -116,6 +118,29 @@ __device__ __forceinline__ void plan_shares(const AttnParams& p, int64_t units, 
     p.head->few = s_joins[0];
     p.head->many = s_joins[1];
   }
+}
+
+// Exclusive sums of two ints over the block, and the block's totals; all threads call it, sums: [kPlanThreads / 32].
+__device__ __forceinline__ int2 plan_scan(int2 v, int2* sums, int2& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int2 x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int a = __shfl_up_sync(0xFFFFFFFFu, x.x, o), b = __shfl_up_sync(0xFFFFFFFFu, x.y, o);
+    if (lane >= o) x.x += a, x.y += b;
+  }
+  if (lane == 31) sums[warp] = x;
+  __syncthreads();
+  int2 before = make_int2(x.x - v.x, x.y - v.y);
+  total = make_int2(0, 0);
+#pragma unroll
+  for (int w = 0; w < kPlanThreads / 32; ++w) {
+    const int2 t = sums[w];
+    if (w < warp) before.x += t.x, before.y += t.y;
+    total.x += t.x, total.y += t.y;
+  }
+  __syncthreads();
+  return before;
 }
 
 // One block: checks the call's lengths, publishes the verdict for the kernels behind it, and
@@ -182,7 +207,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnParams p) {
     if (few) s_work[units] = all;
   }
   __syncthreads();
-  plan_shares(p, units, all, few ? s_work : p.unit_first, s_joins, nullptr);
+  plan_shares<int64_t>(p, units, all, few ? s_work : p.unit_first, s_joins, nullptr, nullptr);
 }
 
 // The same behind shared prefixes: units of a group's rows, whatever sequences they are of, and their spans.
@@ -190,16 +215,22 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnParams p) {
 // one), and write its units of all cache heads. What is looked up again and again is held in shared
 // memory: sequences' numbers up to kPlanCached of them, spans' first tiles up to kPlanSpans.
 // (A thread a unit, which walked through its sequences three times, took 9 us for 64 sequences of 64 heads
-// and 23 for 120 of 8; so it takes 5 and 6.)
-constexpr int kPlanCached = 4096, kPlanSpans = 2048;
+// and 23 for 120 of 8.)
+// SMALL: at most kSmallSeqs sequences and 32 groups, whose blocks go through in one round, and up to kSmallUnits
+// units with all their work in 32 bits. There the plan's time is a chain of loads and code that runs once, so the
+// loads come side by side, and nothing is 64 bits wide or read back from memory.
+constexpr int kPlanCached = 4096, kPlanSpans = 2048, kSmallSeqs = kPlanThreads, kSmallUnits = 256;
+template <bool SMALL>
 __global__ void __launch_bounds__(kPlanThreads) attn_prefix_plan_kernel(AttnParams p, int lanes) {
+  using W = std::conditional_t<SMALL, int, int64_t>;
   extern __shared__ int s_mem[];
   __shared__ int64_t s_warps[32];
-  __shared__ int64_t s_work[kPlanUnits + 1];
-  __shared__ int64_t s_begin[kPlanThreads];  // of a round's blocks: where their units' work begins,
+  __shared__ W s_work[(SMALL ? kSmallUnits : kPlanUnits) + 1];
+  __shared__ W s_begin[kPlanThreads];  // of a round's blocks: where their units' work begins,
   __shared__ int s_span[kPlanThreads];       // their first spans,
   __shared__ int s_tiles[kPlanThreads], s_spans[kPlanThreads];  // and how many tiles and spans a unit has
   __shared__ int s_span_tile[kPlanSpans];
+  __shared__ __align__(16) AttnUnit s_units[SMALL ? kSmallUnits : 1];
   __shared__ int s_joins[2];
   const int G = p.groups;
   int* s_first = s_mem;          // [groups + 1] first row block of each group
@@ -208,30 +239,40 @@ __global__ void __launch_bounds__(kPlanThreads) attn_prefix_plan_kernel(AttnPara
   int* s_cu = s_prefix + G;
   int* s_own = s_cu + p.S + 1;
   int* s_pos = s_own + p.S;
-  const bool cached = p.S <= kPlanCached;
+  const bool cached = SMALL || p.S <= kPlanCached;
   if (threadIdx.x < 2) s_joins[threadIdx.x] = 0;
   pdl_wait();
   // (one block, which leaves room for the next kernel's: they set themselves up meanwhile, and wait for this one's
   // end before they read anything; 36.0 -> 34.8 us for 120 sequences of grouped heads)
   asm volatile("griddepcontrol.launch_dependents;");
   int bad = 0;
-  for (int g = threadIdx.x; g < G; g += kPlanThreads) {
-    const int32_t a = __ldg(p.prefix_seqs + g), b = __ldg(p.prefix_seqs + g + 1), n = __ldg(p.prefix_entries + g);
+  auto group = [&](int g, int a, int b, int n) {
     if (a < 0 || b < a || b > p.S || (g == 0 && a != 0) || (g == G - 1 && b != p.S) || n < 0 || n > p.max_prefix) bad |= 4;
     s_seqs[g] = a;
     s_prefix[g] = n;
     if (g == G - 1) s_seqs[G] = b;
-  }
-  for (int s = threadIdx.x; s < p.S; s += kPlanThreads) {
-    const int32_t a = __ldg(p.cu + s), b = __ldg(p.cu + s + 1), n = __ldg(p.entries + s);
+  };
+  auto sequence_numbers = [&](int s, int a, int b, int n, int pos) {
     if (b < a || a < 0 || b > p.tokens) bad |= 1;
     if (n < 0 || n > p.max_entries) bad |= 2;
     if (cached) {
       s_cu[s] = a;
       if (s == p.S - 1) s_cu[s + 1] = b;
       s_own[s] = n;
-      s_pos[s] = p.first != nullptr ? __ldg(p.first + s) : 0;
+      s_pos[s] = pos;
     }
+  };
+  if constexpr (SMALL) {
+    const int t = threadIdx.x, s = min(t, p.S - 1), g = min(t, G - 1);
+    const int a = __ldg(p.cu + s), b = __ldg(p.cu + s + 1), n = __ldg(p.entries + s), pos = p.first != nullptr ? __ldg(p.first + s) : 0;
+    const int ga = __ldg(p.prefix_seqs + g), gb = __ldg(p.prefix_seqs + g + 1), gn = __ldg(p.prefix_entries + g);
+    if (t < p.S) sequence_numbers(t, a, b, n, pos);
+    if (t < G) group(t, ga, gb, gn);
+  } else {
+    for (int g = threadIdx.x; g < G; g += kPlanThreads)
+      group(g, __ldg(p.prefix_seqs + g), __ldg(p.prefix_seqs + g + 1), __ldg(p.prefix_entries + g));
+    for (int s = threadIdx.x; s < p.S; s += kPlanThreads)
+      sequence_numbers(s, __ldg(p.cu + s), __ldg(p.cu + s + 1), __ldg(p.entries + s), p.first != nullptr ? __ldg(p.first + s) : 0);
   }
   const int32_t* const cu = cached ? s_cu : p.cu;
   const int32_t* const own = cached ? s_own : p.entries;
@@ -247,8 +288,22 @@ __global__ void __launch_bounds__(kPlanThreads) attn_prefix_plan_kernel(AttnPara
   }
   if (code != 0 || p.units == nullptr) return;
   auto group_rows = [&](int g) { return (cu[s_seqs[g + 1]] - cu[s_seqs[g]]) * p.group; };
-  int64_t blocks = 0;
-  {
+  W blocks = 0;
+  if constexpr (SMALL) {
+    if (threadIdx.x < 32) {
+      const int g = threadIdx.x, mine = g < G ? (group_rows(g) + kAttnRows - 1) / kAttnRows : 0;
+      int x = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+        if (g >= o) x += y;
+      }
+      if (g < G) s_first[g] = x - mine;
+      if (g == G - 1) s_first[G] = x;
+    }
+    __syncthreads();
+    blocks = s_first[G];
+  } else {
     const int per = (G + kPlanThreads - 1) / kPlanThreads;
     const int lo = min(G, static_cast<int>(threadIdx.x) * per), hi = min(G, lo + per);
     int64_t mine = 0;
@@ -259,15 +314,15 @@ __global__ void __launch_bounds__(kPlanThreads) attn_prefix_plan_kernel(AttnPara
       at += (group_rows(g) + kAttnRows - 1) / kAttnRows;
     }
     if (threadIdx.x == 0) s_first[G] = static_cast<int>(blocks);
+    __syncthreads();
   }
-  __syncthreads();
-  const int64_t units = blocks * p.kv_heads;
-  const bool few = units <= kPlanUnits;
-  int64_t all = 0;
+  const W units = blocks * p.kv_heads;
+  const bool few = SMALL || units <= kPlanUnits;
+  W all = 0;
   int all_spans = 0;
-  const int round = kPlanThreads / lanes, mine = threadIdx.x / lanes, lane = threadIdx.x % lanes;
-  for (int64_t b0 = 0; b0 < blocks; b0 += round) {
-    const int64_t b = b0 + mine;
+  const int shift = __ffs(lanes) - 1, round = kPlanThreads >> shift, mine = threadIdx.x >> shift, lane = threadIdx.x & (lanes - 1);
+  for (W b0 = 0; b0 < blocks; b0 += round) {
+    const W b = b0 + mine;
     int g = 0, seq0 = 0, seq1 = -1, row0 = 0, before = 0, t0 = 0, t1 = 0, token = 0, rows = 0;
     if (b < blocks) {
       int h = G;  // s_first[g] <= b < s_first[h]
@@ -329,14 +384,26 @@ __global__ void __launch_bounds__(kPlanThreads) attn_prefix_plan_kernel(AttnPara
     }
     __syncthreads();
     const bool holds = static_cast<int>(threadIdx.x) < round && b0 + threadIdx.x < blocks;
-    int64_t sum = 0;
-    const int64_t begin = all + plan_scan(holds ? static_cast<int64_t>(s_tiles[threadIdx.x] + p.unit_cost) * p.kv_heads : 0, s_warps, sum);
-    all += sum;
-    const int64_t span = all_spans + plan_scan(holds ? s_spans[threadIdx.x] * p.kv_heads : 0, s_warps, sum);
-    all_spans += static_cast<int>(sum);
-    if (holds) {
-      s_begin[threadIdx.x] = begin;
-      s_span[threadIdx.x] = static_cast<int>(span);
+    if constexpr (SMALL) {
+      int2 sum;
+      const int2 at = plan_scan(holds ? make_int2((s_tiles[threadIdx.x] + p.unit_cost) * p.kv_heads, s_spans[threadIdx.x] * p.kv_heads)
+                                      : make_int2(0, 0), reinterpret_cast<int2*>(s_warps), sum);
+      all = sum.x;
+      all_spans = sum.y;
+      if (holds) {
+        s_begin[threadIdx.x] = at.x;
+        s_span[threadIdx.x] = at.y;
+      }
+    } else {
+      int64_t sum = 0;
+      const int64_t begin = all + plan_scan(holds ? static_cast<int64_t>(s_tiles[threadIdx.x] + p.unit_cost) * p.kv_heads : 0, s_warps, sum);
+      all += sum;
+      const int64_t span = all_spans + plan_scan(holds ? s_spans[threadIdx.x] * p.kv_heads : 0, s_warps, sum);
+      all_spans += static_cast<int>(sum);
+      if (holds) {
+        s_begin[threadIdx.x] = begin;
+        s_span[threadIdx.x] = static_cast<int>(span);
+      }
     }
     __syncthreads();
     const int unit_tiles = s_tiles[mine], unit_spans = s_spans[mine], span0 = s_span[mine];
@@ -365,10 +432,11 @@ __global__ void __launch_bounds__(kPlanThreads) attn_prefix_plan_kernel(AttnPara
       v.first = seq1;
       v.n = before;
       for (int kvh = 0; kvh < p.kv_heads; ++kvh) {
-        const int64_t i = b * p.kv_heads + kvh, at = s_begin[mine] + kvh * static_cast<int64_t>(unit_tiles + p.unit_cost);
+        const W i = b * p.kv_heads + kvh, at = s_begin[mine] + kvh * static_cast<W>(unit_tiles + p.unit_cost);
         u.kvh = kvh;
         u.span = span0 + kvh * unit_spans;
         p.units[i] = u;
+        if constexpr (SMALL) s_units[i] = u;
         p.unit_first[i] = at;
         if (few) s_work[i] = at;
         if (prefix) put(0, v, kvh, (g * p.kv_heads + kvh) * p.prefix_rows);
@@ -413,7 +481,9 @@ __global__ void __launch_bounds__(kPlanThreads) attn_prefix_plan_kernel(AttnPara
     if (few) s_work[units] = all;
   }
   __syncthreads();
-  plan_shares(p, units, all, few ? s_work : p.unit_first, s_joins, all_spans <= kPlanSpans ? s_span_tile : nullptr);
+  const int* const span_tile = all_spans <= kPlanSpans ? s_span_tile : nullptr;
+  if constexpr (SMALL) plan_shares<int>(p, units, all, s_work, s_joins, span_tile, s_units);
+  else plan_shares<int64_t>(p, units, all, few ? s_work : p.unit_first, s_joins, span_tile, nullptr);
 }
 
 // Scalar kernel, any d and alignment: a warp per new token and query head, a lane the columns
@@ -784,12 +854,18 @@ csa_status_t run_attn(const AttnCall& c, csa_stream_t stream) {
   if (note(cudaGetDevice(&dev)) != cudaSuccess) return CSA_ERR_CUDA;
   const size_t plan_smem = sizeof(int) * (groups > 0 ? 3 * static_cast<size_t>(groups) + 2 + (S <= kPlanCached ? 3 * static_cast<size_t>(S) + 1 : 0)
                                                      : static_cast<size_t>(S) + 1);
-  const void* plan = groups > 0 ? reinterpret_cast<const void*>(attn_prefix_plan_kernel) : reinterpret_cast<const void*>(attn_plan_kernel);
-  if (blocks_per_sm(dev, plan, kPlanThreads, plan_smem, &bps) != cudaSuccess) return CSA_ERR_CUDA;
   // behind prefixes: a thread for each sequence that single tokens would have in 64 rows
   const int per_block = kAttnRows % p.group == 0 ? kAttnRows / p.group : kAttnRows / p.group + 2;
   int plan_lanes = 1;
   while (plan_lanes < per_block && plan_lanes < 32) plan_lanes *= 2;
+  const int64_t most_blocks = p.max_units / kv_heads, unit_most = (max_prefix + kAttnEntries - 1) / kAttnEntries + p.unit_cost +
+                                                                kAttnRows * ((max_entries + kAttnEntries - 1) / kAttnEntries);
+  const bool small = S <= kSmallSeqs && groups <= 32 && most_blocks * plan_lanes <= kPlanThreads && p.max_units <= kSmallUnits &&
+                     p.max_units * unit_most < INT_MAX;
+  const void* plan = groups == 0 ? reinterpret_cast<const void*>(attn_plan_kernel)
+                     : small     ? reinterpret_cast<const void*>(attn_prefix_plan_kernel<true>)
+                                 : reinterpret_cast<const void*>(attn_prefix_plan_kernel<false>);
+  if (blocks_per_sm(dev, plan, kPlanThreads, plan_smem, &bps) != cudaSuccess) return CSA_ERR_CUDA;
   void* plan_args[] = {&p, &plan_lanes};
   if (launch_pdl(plan, dim3(1), dim3(kPlanThreads), plan_smem, cs, plan_args) != cudaSuccess) return CSA_ERR_CUDA;
   if (tile) {
