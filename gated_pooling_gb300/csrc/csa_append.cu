@@ -68,10 +68,11 @@ __device__ __forceinline__ float max_magnitude(float a, float b, float c) {
   return d;
 }
 
-// Scalar kernel, any d and alignment: a warp per row and head, which leaves the finished row in shared
-// memory and then takes it 32 columns, a scale's, at a time.
+// Scalar kernel, any d, rotation and alignment: a warp per row and head, which leaves the finished row in shared
+// memory and then takes it 32 columns, a scale's, at a time. Four of everything side by side: few rows take as
+// long as one, a chain of loads, angles and sums over lanes.
 template <int DTYPE, int FORMAT>
-__global__ void __launch_bounds__(kRopeThreads) append_scalar_kernel(AppendParams q) {
+__global__ void __launch_bounds__(kRopeThreads) append_scalar_kernel(const __grid_constant__ AppendParams q) {
   using E = Element<DTYPE>;
   using T = typename E::T;
   extern __shared__ float s_rows[];  // [warps][d]
@@ -84,45 +85,82 @@ __global__ void __launch_bounds__(kRopeThreads) append_scalar_kernel(AppendParam
     const int64_t row = static_cast<int>(u) / p.heads, head = u - row * p.heads;  // (units below 2^31)
     const int32_t pos = p.pos != nullptr ? __ldg(p.pos + row) : 0;
     const int64_t slot = append_slot(q, row, pos);
-    if (slot < 0) continue;
     const T* x = static_cast<const T*>(p.x) + row * p.x_row + head * p.x_head;
     float ss = 0.f;
-    for (int c = lane; c < p.d; c += 32) {
-      const float v = E::to_float(x[c]);
-      n[c] = v;
-      ss = fmaf(v, v, ss);
+    for (int c0 = lane; c0 < p.d; c0 += 256) {
+      T v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c0 + 32 * i < p.d) v[i] = x[c0 + 32 * i];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c0 + 32 * i < p.d) {
+          const float f = E::to_float(v[i]);
+          n[c0 + 32 * i] = f;
+          ss = fmaf(f, f, ss);
+        }
+    }
+    if (slot < 0) {
+      __syncwarp();
+      continue;
     }
     if (p.norm) {
-      const float r = __frsqrt_rn(warp_sum(ss) / static_cast<float>(p.d) + p.eps);
-      for (int c = lane; c < p.d; c += 32) n[c] = p.weight != nullptr ? n[c] * r * __ldg(p.weight + c) : n[c] * r;
+      const float r = rsqrtf(warp_sum(ss) / static_cast<float>(p.d) + p.eps);
+      for (int c0 = lane; c0 < p.d; c0 += 256) {
+        float w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = p.weight != nullptr && c0 + 32 * i < p.d ? __ldg(p.weight + c0 + 32 * i) : 1.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (c0 + 32 * i < p.d) n[c0 + 32 * i] = n[c0 + 32 * i] * r * w[i];
+      }
     }
     __syncwarp();
-    for (int i = lane; i < p.rot / 2; i += 32) {
-      int a, b;
-      pair_columns(p, i, a, b);
-      float cs, sn;
-      quarter_cos_sin(pos, __ldg(p.turns + i), p.amp, cs, sn);
-      const float va = n[a], vb = n[b];
-      n[a] = va * cs - vb * sn;
-      n[b] = va * sn + vb * cs;
+    for (int i0 = lane; i0 < p.rot / 2; i0 += 128) {
+      uint64_t per[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) per[k] = i0 + 32 * k < p.rot / 2 ? __ldg(p.turns + i0 + 32 * k) : 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float cs, sn;
+        quarter_cos_sin(pos, per[k], p.amp, cs, sn);
+        if (i0 + 32 * k < p.rot / 2) {
+          int a, b;
+          pair_columns(p, i0 + 32 * k, a, b);
+          const float va = n[a], vb = n[b];
+          n[a] = va * cs - vb * sn;
+          n[b] = va * sn + vb * cs;
+        }
+      }
     }
     __syncwarp();
     const int64_t entry = slot * p.heads + head;
-    for (int g = 0; g < groups; ++g) {
-      const int col = g * 32 + lane;
-      const float v = col < p.d ? n[col] : 0.f;
+    for (int g0 = 0; g0 < groups; g0 += 4) {
+      float v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = (g0 + k) * 32 + lane < p.d ? n[(g0 + k) * 32 + lane] : 0.f;
       if constexpr (FORMAT == CSA_CACHE_BF16) {
-        if (col < p.d) reinterpret_cast<uint16_t*>(q.data)[entry * p.d + col] = Element<CSA_DTYPE_BF16>::from_float(v);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int col = (g0 + k) * 32 + lane;
+          if (col < p.d) reinterpret_cast<uint16_t*>(q.data)[entry * p.d + col] = Element<CSA_DTYPE_BF16>::from_float(v[k]);
+        }
       } else {
-        const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v) & 0x7FFFFFFFu);
-        const uint32_t k = scale_byte<FORMAT>(top);
-        const float c = v * scale_inverse(k == 255u ? 127u : k);
-        if (lane == 0) q.scales[entry * groups + g] = static_cast<uint8_t>(k);
-        if constexpr (FORMAT == CSA_CACHE_E4M3) {
-          q.data[entry * p.d + col] = static_cast<uint8_t>(float2_to_e4m3x2(c, 0.f) & 0xFFu);
-        } else {
-          const float hi = __shfl_down_sync(0xFFFFFFFFu, c, 1);
-          if (lane % 2 == 0) q.data[entry * (p.d / 2) + col / 2] = static_cast<uint8_t>(float2_to_e2m1x2(c, hi));
+        uint32_t top[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) top[k] = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v[k]) & 0x7FFFFFFFu);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int g = g0 + k, col = g * 32 + lane;
+          const uint32_t s = scale_byte<FORMAT>(top[k]);
+          const float c = v[k] * scale_inverse(s == 255u ? 127u : s), hi = __shfl_down_sync(0xFFFFFFFFu, c, 1);
+          if (g >= groups) continue;
+          if (lane == 0) q.scales[entry * groups + g] = static_cast<uint8_t>(s);
+          if constexpr (FORMAT == CSA_CACHE_E4M3) {
+            q.data[entry * p.d + col] = static_cast<uint8_t>(float2_to_e4m3x2(c, 0.f) & 0xFFu);
+          } else {
+            if (lane % 2 == 0) q.data[entry * (p.d / 2) + col / 2] = static_cast<uint8_t>(float2_to_e2m1x2(c, hi));
+          }
         }
       }
     }

@@ -408,17 +408,18 @@ __global__ void __launch_bounds__(kStepThreads, 1) step_kernel(const __grid_cons
     }
   };
 
-  // sequences: the blocks that reach into the state, then the state
+  // Sequences: the blocks that reach into the state (two at most), then the state. All that is loaded for a sequence
+  // is under way together, by way of this thread's places for three turns, where there are three.
   const int64_t state = static_cast<int64_t>(p.W) * p.C;
   int turn = 0;
+  const bool room = p.stages == 3;
   for (int s0 = g * p.RS; s0 < p.S && g < p.seq_ctas; s0 += p.seq_ctas * p.RS) {
     const int s = s0 + rs;
     const bool some = slot && s < p.S;
     const StepSeq q(p, some ? s : s0);
-#pragma unroll 1
-    for (int i = 0; i < p.coff; ++i) {
-      const bool now = some && i < q.boundary;
-      if (!__syncthreads_or(now)) break;  // (the second one comes after a first)
+    const bool now0 = some && q.boundary > 0, now1 = some && q.boundary > 1;
+    const bool any0 = __syncthreads_or(now0), any1 = any0 && __syncthreads_or(now1);
+    auto window = [&](int b, int i, bool now) {
 #pragma unroll
       for (int u = 0; u < UW; ++u) {
         const int w = pg + u * p.PG;
@@ -427,40 +428,87 @@ __global__ void __launch_bounds__(kStepThreads, 1) step_kernel(const __grid_cons
           const bool old = pos < q.first;
           const int64_t at = (old ? q.source * state + static_cast<int64_t>(pos % p.W) * p.C : (q.token0 + pos) * p.C) +
                              (two && (own >> u & 1u) ? p.d : 0) + c0;
-          stage_piece(place(0, 0, u, 0), (old ? p.kv_state : p.kv) + at);
-          stage_piece(place(0, 0, u, 1), (old ? p.score_state : p.score) + at);
+          stage_piece(place(b, 0, u, 0), (old ? p.kv_state : p.kv) + at);
+          stage_piece(place(b, 0, u, 1), (old ? p.score_state : p.score) + at);
         } else {
-          place(0, 0, u, 0)->fill(kAbsentValue);
-          place(0, 0, u, 1)->fill(kAbsentScore);
+          place(b, 0, u, 0)->fill(kAbsentValue);
+          place(b, 0, u, 1)->fill(kAbsentScore);
         }
       }
-      stage_commit();
-      embed();
-      stage_wait(0);
-      finish(0, 0, now ? s_prefix[s].x + i : -1, turn++);
-    }
-    if (!some) continue;
-    if (chunk == 0 && pg == 0 && p.entries != nullptr) p.entries[s] = max(0, q.hi - (p.base != nullptr ? __ldg(p.base + s) : 0));
-    if (!mine || q.target < 0) continue;
-    for (int half = 0; half < p.coff; ++half) {
+    };
+    // what goes into the state of a half's columns: the thread's positions from `from` on, kStepFlight at a time
+    const int end = some && mine && q.target >= 0 ? q.first + q.n : 0;
+    auto keep_from = [&](int half) {
       const int keep = max(0, q.hi - (p.coff - 1 - half)) * p.ratio;  // the first position that a later window reads
-      const int end = q.first + q.n;
-      for (int pos = (q.source == q.target ? max(keep, q.first) : keep) + pg; pos < end; pos += p.PG) {
+      return (q.source == q.target ? max(keep, q.first) : keep) + pg;
+    };
+    auto keep_place = [&](int half, int pos) { return static_cast<int64_t>(pos % p.W) * p.C + half * p.d + c0; };
+    auto keep_load = [&](int b, int half, int from) {
+#pragma unroll
+      for (int i = 0; i < kStepFlight; ++i) {
+        const int pos = from + i * p.PG;
+        if (pos >= end) continue;
         const bool old = pos < q.first;
-        const int64_t at = static_cast<int64_t>(pos % p.W) * p.C + half * p.d + c0;
-        const int64_t from = old ? q.source * state + at : (q.token0 + pos) * p.C + half * p.d + c0;
-        P k, x;
-        k.load((old ? p.kv_state : p.kv) + from);
-        x.load((old ? p.score_state : p.score) + from);
-        k.store(p.kv_state + q.target * state + at);
-        x.store(p.score_state + q.target * state + at);
+        const int64_t at = old ? q.source * state + keep_place(half, pos) : (q.token0 + pos) * p.C + half * p.d + c0;
+        stage_piece(place(b, 0, i, 0), (old ? p.kv_state : p.kv) + at);
+        stage_piece(place(b, 0, i, 1), (old ? p.score_state : p.score) + at);
       }
+    };
+    auto keep_store = [&](int b, int half, int from) {
+#pragma unroll
+      for (int i = 0; i < kStepFlight; ++i) {
+        const int pos = from + i * p.PG;
+        if (pos >= end) continue;
+        place(b, 0, i, 0)->store(p.kv_state + q.target * state + keep_place(half, pos));
+        place(b, 0, i, 1)->store(p.score_state + q.target * state + keep_place(half, pos));
+      }
+    };
+    const int from0 = keep_from(0), from1 = two ? keep_from(1) : 0;
+    if (any0) window(0, 0, now0);
+    stage_commit();
+    if (room) {
+      if (any1) window(1, 1, now1);
+      stage_commit();
+      keep_load(2, 0, from0);
+      stage_commit();
     }
+    if (any0) {
+      embed();
+      stage_wait(room ? 2 : 0);
+      finish(0, 0, now0 ? s_prefix[s].x : -1, turn++);
+    }
+    if (any1 && !room) {
+      window(0, 1, now1);
+      stage_commit();
+    }
+    if (room && two) {
+      keep_load(0, 1, from1);
+      stage_commit();
+    }
+    if (any1) {
+      stage_wait(room ? 2 : 0);
+      finish(room ? 1 : 0, 0, now1 ? s_prefix[s].x + 1 : -1, turn++);
+    }
+    if (some && chunk == 0 && pg == 0 && p.entries != nullptr)
+      p.entries[s] = max(0, q.hi - (p.base != nullptr ? __ldg(p.base + s) : 0));
+    stage_wait(0);
+    if (room) {
+      keep_store(2, 0, from0);
+      if (two) keep_store(0, 1, from1);
+    }
+    for (int half = 0; half < p.coff; ++half)
+      for (int from = (half == 0 ? from0 : from1) + (room ? kStepFlight * p.PG : 0); from < end; from += kStepFlight * p.PG) {
+        keep_load(0, half, from);
+        stage_commit();
+        stage_wait(0);
+        keep_store(0, half, from);
+      }
   }
 
+  const int worker = g - p.first_row_cta, workers = p.R - p.first_row_cta;
   auto describe = [&]() {
-    if (blockIdx.y == 0 && (p.positions != nullptr || p.slots != nullptr))
-      for (int64_t o = static_cast<int64_t>(tid) * p.R + g; o < p.out_rows; o += static_cast<int64_t>(p.R) * kStepThreads) {
+    if (blockIdx.y == 0 && g >= p.first_row_cta && (p.positions != nullptr || p.slots != nullptr))
+      for (int64_t o = static_cast<int64_t>(tid) * workers + worker; o < p.out_rows; o += static_cast<int64_t>(workers) * kStepThreads) {
         if (o >= total) {
           no_row(p, o);
           continue;
@@ -476,7 +524,6 @@ __global__ void __launch_bounds__(kStepThreads, 1) step_kernel(const __grid_cons
   };
 
   // all other blocks: contiguous runs of rows
-  const int worker = g - p.first_row_cta, workers = p.R - p.first_row_cta;
   const int i0 = worker < 0 ? 0 : static_cast<int>(static_cast<int64_t>(worker) * inner / workers);
   const int i1 = worker < 0 ? 0 : static_cast<int>(static_cast<int64_t>(worker + 1) * inner / workers);
   if (i0 >= i1) {
@@ -714,9 +761,14 @@ __global__ void __launch_bounds__(kFewThreads) step_few_kernel(const __grid_cons
   if (from0 < end) keep_store(0, from0, k0, x0);
   if (from1 < end) keep_store(1, from1, k1, x1);
   for (int half = 0; half < p.coff && keeps; ++half)
-    for (int pos = (half == 0 ? from0 : from1) + lines; pos < end; pos += lines) {
-      keep_load(half, pos, k0, x0);
-      keep_store(half, pos, k0, x0);
+    for (int pos0 = (half == 0 ? from0 : from1) + lines; pos0 < end; pos0 += 4 * lines) {
+      P k[4], x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (pos0 + i * lines < end) keep_load(half, pos0 + i * lines, k[i], x[i]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (pos0 + i * lines < end) keep_store(half, pos0 + i * lines, k[i], x[i]);
     }
   // where the rows go, by the last threads; those behind the last entry
   if (blockIdx.y != 0) return;
