@@ -12,6 +12,7 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "csa_compressor.h"
 #include "csa_element.cuh"
@@ -273,30 +274,45 @@ struct Weighed {
     }
   }
 };
-// Joins a column's parts, `many` to each of kStepJoin neighbouring threads (from `at` on, `wide` apart), and stores it.
-__device__ __forceinline__ void join_parts(const float* at, int step, int wide, int many, uint16_t* to) {
-  constexpr int J = kStepJoin;
-  const int lane = threadIdx.x & 31;
-  const uint32_t mask = ((1u << J) - 1u) << (lane & ~(J - 1));
-  float m = -INFINITY, z = 0.f, a = 0.f;
-#pragma unroll 4
-  for (int q = 0; q < many; ++q) m = fmaxf(m, at[q * wide]);
-#pragma unroll
-  for (int o = 1; o < J; o <<= 1) m = fmaxf(m, __shfl_xor_sync(mask, m, o));
-  const float base = m == -INFINITY ? 0.f : m;
-#pragma unroll 4
-  for (int q = 0; q < many; ++q) {
-    const float f = fast_exp2(at[q * wide] - base);
-    z = fmaf(at[step + q * wide], f, z);
-    a = fmaf(at[2 * step + q * wide], f, a);
+
+// Parts of a window's columns, of PG threads, [3][PG][wide], and the threads that join them: kStepJoin neighbouring ones
+// to a column. The parts of each of those lie 8 columns on from the one's before, for the banks of the threads that
+// read them together.
+struct Join {
+  static constexpr int kJ = kStepJoin, kTurn = 32 / kJ;
+  int wide, many, step, from, turned;
+  __device__ __forceinline__ Join(int PG, int wide_)
+      : wide(wide_), many(PG / kJ), step(PG * wide), from(threadIdx.x % kJ * many * wide), turned(threadIdx.x % kJ * kTurn % wide) {}
+  // where column c of part pg lies
+  __device__ __forceinline__ int place(int pg, int c) const {
+    c += pg / many * kTurn % wide;
+    return pg * wide + (c >= wide ? c - wide : c);
   }
+  // Column c of `parts`, for this thread's share of them, to `to` where that is given. All lanes of a warp call it
+  // together (shuffles of a few lanes each by their own mask run one after another).
+  __device__ __forceinline__ void column(const float* parts, int c, uint16_t* to) const {
+    c += turned;
+    const float* at = parts + from + (c >= wide ? c - wide : c);
+    float m = -INFINITY, z = 0.f, a = 0.f;
+#pragma unroll 4
+    for (int q = 0; q < many; ++q) m = fmaxf(m, at[q * wide]);
 #pragma unroll
-  for (int o = 1; o < J; o <<= 1) {
-    z += __shfl_xor_sync(mask, z, o);
-    a += __shfl_xor_sync(mask, a, o);
+    for (int o = 1; o < kJ; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll 4
+    for (int q = 0; q < many; ++q) {
+      const float f = fast_exp2(at[q * wide] - base);
+      z = fmaf(at[step + q * wide], f, z);
+      a = fmaf(at[2 * step + q * wide], f, a);
+    }
+#pragma unroll
+    for (int o = 1; o < kJ; o <<= 1) {
+      z += __shfl_xor_sync(0xFFFFFFFFu, z, o);
+      a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+    }
+    if (to != nullptr && threadIdx.x % kJ == 0) *to = Element<CSA_DTYPE_BF16>::from_float(a * rcp_nr(z));
   }
-  if (lane % J == 0) *to = Element<CSA_DTYPE_BF16>::from_float(a * rcp_nr(z));
-}
+};
 
 // Bytes of shared memory: a stage holds the (kv, score) pieces of a thread's positions at once; SPLIT, two turns'
 // parts; then the prefix.
@@ -308,11 +324,11 @@ __host__ __device__ constexpr int step_part_bytes(int vec, bool split) { return 
 // PG threads share.
 //
 // A thread's pieces come into places of its own in shared memory (no barrier), p.stages turns ahead: 64 KB a turn
-// and SM. Registers held one turn ahead and less than latency asks for: 22.7 and 43.8 us for three chunks of up to
-// 8192 tokens of 512 in blocks of 4 and four of 16384 in blocks of 128.
+// and SM. Three chunks of up to 8192 tokens of 512 in blocks of 4 take 17.7 us (56 % of the copy rate), four of up to
+// 16384 in blocks of 128 36.6 us (55 %); registers held one turn ahead, less than latency asks for: 22.7 and 43.8 us.
 template <int VEC, int UW, bool SPLIT>
 __global__ void __launch_bounds__(kStepThreads, 1) step_kernel(const __grid_constant__ StepParams p) {
-  constexpr int K = SPLIT ? 1 : kStepFlight / UW, PAIRS = VEC == 4 ? 2 : 1, J = kStepJoin;
+  constexpr int K = SPLIT ? 1 : kStepFlight / UW, PAIRS = VEC == 4 ? 2 : 1;
   constexpr uint32_t kAll = (1u << UW) - 1u;
   using P = Piece<VEC>;
   extern __shared__ __align__(16) unsigned char s_raw[];
@@ -363,10 +379,9 @@ __global__ void __launch_bounds__(kStepThreads, 1) step_kernel(const __grid_cons
     }
   };
 
-  // (SPLIT: parts of a quarter of the positions lie eight columns on from those before, for the banks of the
-  // threads that read a column together)
-  const int wide = p.CL * VEC, quarter = p.PG / J;
-  const int turned = SPLIT ? 8 * (pg / quarter) % wide : 0, read_turned = SPLIT ? 8 * (tid % J) % wide : 0;
+  const int wide = p.CL * VEC;
+  const Join join(SPLIT ? p.PG : kStepJoin, wide);
+  const int part_at = SPLIT ? join.place(pg, cl * VEC) : 0;
   // maximum, weight sum and weighted sum of this thread's positions in a stage, to the row (-1: none) or to the
   // threads that share it
   auto finish = [&](int b, int k, int row, int turn) {
@@ -381,11 +396,7 @@ __global__ void __launch_bounds__(kStepThreads, 1) step_kernel(const __grid_cons
       Weighed<VEC> r;
       r.template of<UW>(kv, score, embedding);
       if constexpr (SPLIT) {
-        const int step = p.PG * wide;
-        float* to = s_part + (turn & 1) * 3 * kStepThreads * VEC + rs * 3 * step + pg * wide;
-        int c = cl * VEC + turned;
-        if (c >= wide) c -= wide;
-        r.leave(to + c, step);
+        r.leave(s_part + (turn & 1) * 3 * kStepThreads * VEC + rs * 3 * join.step + part_at, join.step);
       } else {
         r.store(p.out + static_cast<int64_t>(row) * p.d + c0);
       }
@@ -394,16 +405,11 @@ __global__ void __launch_bounds__(kStepThreads, 1) step_kernel(const __grid_cons
       // the parts meet in shared memory in a fixed order, a column to J neighbouring threads (two turns'
       // parts, so that one barrier a row is enough)
       __syncthreads();
-      if (slot && row >= 0) {
-        const int step = p.PG * wide, j = tid % J;
-        const float* part = s_part + (turn & 1) * 3 * kStepThreads * VEC + rs * 3 * step + j * quarter * wide;
-        for (int c = tid % per / J; c < wide; c += per / J) {
-          const int col = blockIdx.y * wide + c;
-          if (col >= p.d) break;
-          int from = c + read_turned;
-          if (from >= wide) from -= wide;
-          join_parts(part + from, step, wide, quarter, p.out + static_cast<int64_t>(row) * p.d + col);
-        }
+      const float* part = s_part + (turn & 1) * 3 * kStepThreads * VEC + min(rs, p.RS - 1) * 3 * join.step;
+      for (int c0 = 0; c0 < wide; c0 += per / Join::kJ) {  // (as often for every lane)
+        const int c = c0 + tid % per / Join::kJ, col = blockIdx.y * wide + c;
+        join.column(part, min(c, wide - 1),
+                    slot && row >= 0 && c < wide && col < p.d ? p.out + static_cast<int64_t>(row) * p.d + col : nullptr);
       }
     }
   };
@@ -419,22 +425,33 @@ __global__ void __launch_bounds__(kStepThreads, 1) step_kernel(const __grid_cons
     const StepSeq q(p, some ? s : s0);
     const bool now0 = some && q.boundary > 0, now1 = some && q.boundary > 1;
     const bool any0 = __syncthreads_or(now0), any1 = any0 && __syncthreads_or(now1);
-    auto window = [&](int b, int i, bool now) {
+    const int64_t old_at = q.source * state + c0, new_at = q.token0 * p.C + c0, keep_at = q.target * state + c0;
+    // f(i, position, its row in a state) for kStepFlight (or n) positions from `from` on, p.PG apart
+    auto each = [&](auto n, int from, auto f) {
+      int r = max(from, 0) % p.W;  // (a position below 0 is not asked for)
+      if (from < 0) r = from + p.W;
 #pragma unroll
-      for (int u = 0; u < UW; ++u) {
-        const int w = pg + u * p.PG;
-        const int pos = (q.lo + i - (two ? 1 : 0)) * p.ratio + w;
+      for (int i = 0; i < decltype(n)::value; ++i) {
+        f(i, from + i * p.PG, r);
+        r += p.PG;
+        if (r >= p.W) r -= p.W;
+      }
+    };
+    auto load = [&](int b, int i, int pos, int r, int half) {
+      const bool old = pos < q.first;
+      const int64_t at = (old ? old_at + static_cast<int64_t>(r) * p.C : new_at + static_cast<int64_t>(pos) * p.C) + half;
+      stage_piece(place(b, 0, i, 0), (old ? p.kv_state : p.kv) + at);
+      stage_piece(place(b, 0, i, 1), (old ? p.score_state : p.score) + at);
+    };
+    auto window = [&](int b, int block, bool now) {
+      each(std::integral_constant<int, UW>{}, (block - (two ? 1 : 0)) * p.ratio + pg, [&](int u, int pos, int r) {
         if (now && (there >> u & 1u) && pos >= 0) {
-          const bool old = pos < q.first;
-          const int64_t at = (old ? q.source * state + static_cast<int64_t>(pos % p.W) * p.C : (q.token0 + pos) * p.C) +
-                             (two && (own >> u & 1u) ? p.d : 0) + c0;
-          stage_piece(place(b, 0, u, 0), (old ? p.kv_state : p.kv) + at);
-          stage_piece(place(b, 0, u, 1), (old ? p.score_state : p.score) + at);
+          load(b, u, pos, r, two && (own >> u & 1u) ? p.d : 0);
         } else {
           place(b, 0, u, 0)->fill(kAbsentValue);
           place(b, 0, u, 1)->fill(kAbsentScore);
         }
-      }
+      });
     };
     // what goes into the state of a half's columns: the thread's positions from `from` on, kStepFlight at a time
     const int end = some && mine && q.target >= 0 ? q.first + q.n : 0;
@@ -442,32 +459,26 @@ __global__ void __launch_bounds__(kStepThreads, 1) step_kernel(const __grid_cons
       const int keep = max(0, q.hi - (p.coff - 1 - half)) * p.ratio;  // the first position that a later window reads
       return (q.source == q.target ? max(keep, q.first) : keep) + pg;
     };
-    auto keep_place = [&](int half, int pos) { return static_cast<int64_t>(pos % p.W) * p.C + half * p.d + c0; };
     auto keep_load = [&](int b, int half, int from) {
-#pragma unroll
-      for (int i = 0; i < kStepFlight; ++i) {
-        const int pos = from + i * p.PG;
-        if (pos >= end) continue;
-        const bool old = pos < q.first;
-        const int64_t at = old ? q.source * state + keep_place(half, pos) : (q.token0 + pos) * p.C + half * p.d + c0;
-        stage_piece(place(b, 0, i, 0), (old ? p.kv_state : p.kv) + at);
-        stage_piece(place(b, 0, i, 1), (old ? p.score_state : p.score) + at);
-      }
+      if (from >= end) return;
+      each(std::integral_constant<int, kStepFlight>{}, from, [&](int i, int pos, int r) {
+        if (pos < end) load(b, i, pos, r, half * p.d);
+      });
     };
     auto keep_store = [&](int b, int half, int from) {
-#pragma unroll
-      for (int i = 0; i < kStepFlight; ++i) {
-        const int pos = from + i * p.PG;
-        if (pos >= end) continue;
-        place(b, 0, i, 0)->store(p.kv_state + q.target * state + keep_place(half, pos));
-        place(b, 0, i, 1)->store(p.score_state + q.target * state + keep_place(half, pos));
-      }
+      if (from >= end) return;
+      each(std::integral_constant<int, kStepFlight>{}, from, [&](int i, int pos, int r) {
+        if (pos >= end) return;
+        const int64_t to = keep_at + static_cast<int64_t>(r) * p.C + half * p.d;
+        place(b, 0, i, 0)->store(p.kv_state + to);
+        place(b, 0, i, 1)->store(p.score_state + to);
+      });
     };
     const int from0 = keep_from(0), from1 = two ? keep_from(1) : 0;
-    if (any0) window(0, 0, now0);
+    if (any0) window(0, q.lo, now0);
     stage_commit();
     if (room) {
-      if (any1) window(1, 1, now1);
+      if (any1) window(1, q.lo + 1, now1);
       stage_commit();
       keep_load(2, 0, from0);
       stage_commit();
@@ -478,7 +489,7 @@ __global__ void __launch_bounds__(kStepThreads, 1) step_kernel(const __grid_cons
       finish(0, 0, now0 ? s_prefix[s].x : -1, turn++);
     }
     if (any1 && !room) {
-      window(0, 1, now1);
+      window(0, q.lo + 1, now1);
       stage_commit();
     }
     if (room && two) {
@@ -613,8 +624,7 @@ __global__ void __launch_bounds__(kStepThreads, 1) step_kernel(const __grid_cons
 // threads share out among them.
 constexpr int kFewThreads = 256;
 template <int VEC, int UW, bool SPLIT>
-__global__ void __launch_bounds__(kFewThreads) step_few_kernel(const __grid_constant__ StepParams p) {
-  constexpr int J = kStepJoin;
+__global__ void __launch_bounds__(kFewThreads, SPLIT ? 2 : 1) step_few_kernel(const __grid_constant__ StepParams p) {
   using P = Piece<VEC>;
   __shared__ __align__(16) float s_part[SPLIT ? 3 * kFewThreads * VEC : 4];
   __shared__ int s_sums[2][kFewThreads / 32];
@@ -643,19 +653,23 @@ __global__ void __launch_bounds__(kFewThreads) step_few_kernel(const __grid_cons
   P kv[UW], score[UW];
   uint64_t embedding[UW][Weighed<VEC>::kPairs];
   auto fetch = [&](const StepSeq& q, int block) {
+    const int from = (block - (two ? 1 : 0)) * p.ratio + pg;
+    int ring = from < 0 ? from + p.W : from % p.W;  // a position's row in a state
 #pragma unroll
     for (int u = 0; u < UW; ++u) {
-      const int w = pg + u * p.PG;
+      const int w = pg + u * p.PG, r = ring;
       const bool prev = two && w < p.ratio;
-      const int pos = (block - (two ? 1 : 0)) * p.ratio + w;
+      const int pos = from + u * p.PG;
+      ring += p.PG;
+      if (ring >= p.W) ring -= p.W;
       kv[u].fill(kAbsentValue);
       score[u].fill(kAbsentScore);
       if (mine && w < p.W && pos >= 0) {
         const bool old = pos < q.first;
-        const int64_t from = (old ? q.source * state + static_cast<int64_t>(pos % p.W) * p.C : (q.token0 + pos) * p.C) +
-                             (two && !prev ? p.d : 0) + c0;
-        kv[u].load((old ? p.kv_state : p.kv) + from);
-        score[u].load((old ? p.score_state : p.score) + from);
+        const int64_t at = (old ? q.source * state + static_cast<int64_t>(r) * p.C : (q.token0 + pos) * p.C) +
+                           (two && !prev ? p.d : 0) + c0;
+        kv[u].load((old ? p.kv_state : p.kv) + at);
+        score[u].load((old ? p.score_state : p.score) + at);
       }
     }
   };
@@ -726,7 +740,8 @@ __global__ void __launch_bounds__(kFewThreads) step_few_kernel(const __grid_cons
     if (tid == 0 && p.dev_error != nullptr) *reinterpret_cast<volatile int32_t*>(p.dev_error) = which;
     return;
   }
-  const int wide = p.CL * VEC, quarter = p.PG / J, step = p.PG * wide;
+  const int wide = p.CL * VEC;
+  const Join join(SPLIT ? p.PG : kStepJoin, wide);
   bool here = true;  // the window is there already
   for (int s = next, row = before; s < s1; ++s) {
     const StepSeq q(p, s);
@@ -738,21 +753,17 @@ __global__ void __launch_bounds__(kFewThreads) step_few_kernel(const __grid_cons
         Weighed<VEC> r;
         r.template of<UW>(kv, score, embedding);
         if constexpr (SPLIT) {
-          int c = cl * VEC + 8 * (pg / quarter) % wide;
-          if (c >= wide) c -= wide;
-          r.leave(s_part + pg * wide + c, step);
+          r.leave(s_part + join.place(pg, cl * VEC), join.step);
         } else {
           r.store(out + c0);
         }
       }
       if constexpr (SPLIT) {
         __syncthreads();
-        if (tid < per)
-          for (int c = tid / J, j = tid % J; c < wide && blockIdx.y * wide + c < p.d; c += per / J) {
-            int from = c + 8 * j % wide;
-            if (from >= wide) from -= wide;
-            join_parts(s_part + j * quarter * wide + from, step, wide, quarter, out + blockIdx.y * wide + c);
-          }
+        for (int c0 = 0; c0 < wide; c0 += per / Join::kJ) {  // (as often for every lane)
+          const int c = c0 + tid / Join::kJ, col = blockIdx.y * wide + c;
+          join.column(s_part, min(c, wide - 1), tid < per && c < wide && col < p.d ? out + col : nullptr);
+        }
         __syncthreads();
       }
     }
@@ -854,7 +865,7 @@ extern "C" csa_status_t csa_compressor_step(
   p.PG = p.W > kStepFlight ? kStepJoin : 1;
   while (p.PG * kStepFlight < p.W) p.PG *= 2;
   // Few tokens a sequence: the kernel without a pipeline, a CTA a sequence (64 single tokens of 512 in blocks of 4
-  // in 5 instead of 7.7 us; 200 of 128 in blocks of 128 in 7 instead of 11.5), up to where one sequence may
+  // in 5.2 instead of 7.7 us; 200 of 128 in blocks of 128 in 8.2 instead of 11.5), up to where one sequence may
   // have most of them.
   const bool few = S > 0 && S <= 512 && capacity <= 8 * static_cast<int64_t>(S);
   const int threads = few ? kFewThreads : kStepThreads;
