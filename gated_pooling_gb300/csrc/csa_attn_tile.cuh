@@ -1110,7 +1110,9 @@ __global__ void __launch_bounds__(kPackThreads) attn_pack_kernel(const __grid_co
   pdl_wait();
   if (p.head->status != 0) return;
   // kRows entries from e0 on of a run of n, whose first lies in row row0 of the packed ones
-  constexpr int kRows = pack_rows(NC, PREFIX), kAtOnce = PREFIX ? 8 : 4;
+  constexpr int kRows = pack_rows(NC, PREFIX), kPieces = kRows * kPer / kPackThreads;  // a thread's
+  constexpr int kAtOnce = kPieces < (PREFIX ? 8 : 4) ? kPieces : PREFIX ? 8 : 4;
+  static_assert(kPieces % kAtOnce == 0 && kPieces * kPackThreads == kRows * kPer && kAttnEntries % kRows == 0);
   auto pack = [&](const int32_t* table, int64_t row0, int kvh, int n, int e0) {
     uint16_t* to = p.packed + (row0 + e0) * (NC * 64);
 #pragma unroll 1
@@ -1227,7 +1229,7 @@ __global__ void __launch_bounds__(TileCta<SRC>::kThreads, 1)
     sm.stop = 0;
     fence_mbar_init();
   }
-  if constexpr (SRC == kFromBoxes) {
+  if constexpr (PREFIX && SRC == kFromBoxes) {
     // rows that no box covers count as seen by nobody, but what shared memory holds of other kernels may look
     // like infinities and NaN, which the softmax warps would have to clear one by one (7 us a tile)
     for (uint32_t at = threadIdx.x * 16; at < SH::kRing * kPairBytes; at += CTA::kThreads * 16) sts128(base + at, make_uint4(0, 0, 0, 0));

@@ -264,6 +264,33 @@ def test_as_without_prefixes(cuda_lib, fmt, H, kv, d):
     assert ((out - c.out).abs().double().cpu()[:n] <= 2 * tol[:n]).all() and ((lse - c.lse).abs().double().cpu()[:n] <= 2 * ltol[:n]).all()
 
 
+@pytest.mark.parametrize("fmt", [R.BF16, R.E4M3, R.FP4])
+@pytest.mark.parametrize("H,kv,d,page", [(16, 2, 128, 16), (8, 1, 64, 4), (8, 1, 256, 16), (64, 1, 512, 4)])
+def test_full_tables_and_exact_workspaces(cuda_lib, fmt, H, kv, d, page):
+    """Chunks whose entries fill every table (and every place that the call may pack them in): right, by both entry
+    points, and nothing behind a workspace of exactly the size that is asked for is touched."""
+    def spare(n):
+        ws = torch.full((n + 65536,), 0x5A, dtype=torch.uint8, device="cuda")
+        return ws, ws[:n]
+    c = Case([(512, [(200, 256), (330, 256), (3, 256)]), (512, [(410, 256)])], H, kv, d, fmt, page=page, ratio=1, seed=21, lead=3)
+    c.tables = [t[:, :-1].contiguous() for t in c.tables]  # (the tables are as wide as what they hold)
+    n = cuda_lib.csa_cache_attn_prefix_workspace_bytes(c.S, c.G, c.tokens, H, kv, d, 256, 512)
+    ws, view = spare(n)
+    c.check(cuda_lib, ws=view)
+    assert (ws[n:] == 0x5A).all()
+    c = Case([(0, [(200, 384), (330, 384), (384, 384)])], H, kv, d, fmt, page=page, ratio=1, seed=22)
+    c.tables = [c.tables[0], c.tables[1][:, :-1].contiguous()]
+    a = list(c.args(cuda_lib))
+    n = cuda_lib.csa_cache_attn_workspace_bytes(c.S, c.tokens, H, kv, d, 384)
+    ws, view = spare(n)
+    cuda_lib.csa_cache_attn(*a[:12], *a[17:30], view, n, a[32])
+    torch.cuda.synchronize()
+    assert (ws[n:] == 0x5A).all() and int(c.err) == 0
+    ref, rl, tol, ltol = c.reference()
+    end = c.cu[-1]
+    assert ((c.out.double().cpu() - ref).abs() <= tol)[:end].all() and ((c.lse.double().cpu() - rl).abs() <= ltol)[:end].all()
+
+
 def test_repeats_and_graph(cuda_lib):
     """The same bits from the same inputs; a captured call replayed on other lengths than it was captured with."""
     def make():
