@@ -24,6 +24,9 @@ namespace {
 constexpr int kStepThreads = 512;
 constexpr int kStepFlight = 8;  // (kv, score) pieces that a thread loads at a time
 constexpr int kStepJoin = 4;    // threads that join a column's parts, of at least as many
+// A sequence's positions end below this, so that one that is counted on by a round (kStepFlight times the threads that
+// share a window, CSA_MAX_WINDOW), or by two, is an int still.
+constexpr int kStepEnd = INT_MAX - 2 * CSA_MAX_WINDOW;
 
 struct StepParams {
   const uint16_t* kv;
@@ -157,7 +160,7 @@ __device__ __forceinline__ int step_wrong(const StepParams& p, int a, int b, int
   if (b < a || a < 0 || b > p.capacity) return 1;
   const int n = b - a;
   const bool live = f % p.ratio != 0 || (p.coff == 2 && f >= p.ratio);  // the state holds something
-  return f < 0 || f > INT_MAX - n || from >= p.num_states || to >= p.num_states || (from < 0 && live && (n > 0 || to >= 0)) ? 2 : 0;
+  return f < 0 || f > kStepEnd - n || from >= p.num_states || to >= p.num_states || (from < 0 && live && (n > 0 || to >= 0)) ? 2 : 0;
 }
 
 // Rows before each sequence (x), and those of them whose windows reach into no state (y), in shared memory, [S]
@@ -566,12 +569,12 @@ __global__ void __launch_bounds__(kStepThreads, 1) step_kernel(const __grid_cons
   };
   Walk ahead, here;
   ahead.end = here.end = i0;
-  auto fetch = [&](int i, int b, int k) {
-    if (!mine || i >= i1) return;
-    find(ahead, i);
+  auto fetch = [&](unsigned i, int b, int k) {  // (may have passed 2^31 - 1)
+    if (!mine || i >= static_cast<unsigned>(i1)) return;
+    find(ahead, static_cast<int>(i));
     const int64_t at = ahead.at + static_cast<int64_t>(i) * p.ratio * p.C;
     const uint16_t *kv = p.kv + at, *score = p.score + at;
-    const uint32_t on = i == ahead.first ? there & own : there;
+    const uint32_t on = static_cast<int>(i) == ahead.first ? there & own : there;
     if (on == kAll) {
 #pragma unroll
       for (int u = 0; u < UW; ++u) {
@@ -599,22 +602,22 @@ __global__ void __launch_bounds__(kStepThreads, 1) step_kernel(const __grid_cons
   }
   embed();
   describe();  // (while the first rows are on their way)
-  for (int i = i0, b = 0; i < i1; i += step) {
+  for (unsigned i = i0, b = 0; i < static_cast<unsigned>(i1); i += step) {
     stage_wait(p.stages - 1);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int mine_i = i + k * p.RS + rs;
+      const unsigned mine_i = i + k * p.RS + rs;
       int row = -1;
-      if (slot && mine_i < i1) {
-        find(here, mine_i);
-        row = mine_i + here.row;
+      if (slot && mine_i < static_cast<unsigned>(i1)) {
+        find(here, static_cast<int>(mine_i));
+        row = static_cast<int>(mine_i) + here.row;
       }
       finish(b, k, row, turn++);
     }
 #pragma unroll
     for (int k = 0; k < K; ++k) fetch(i + p.stages * step + k * p.RS + rs, b, k);
     stage_commit();
-    if (++b == p.stages) b = 0;
+    if (++b == static_cast<unsigned>(p.stages)) b = 0;
   }
 }
 
@@ -858,11 +861,16 @@ extern "C" csa_status_t csa_compressor_step(
   p.max_pages = max_pages;
   p.page_size = page_size;
   p.offset = position_offset;
+  // (four columns a thread, and the numbers of very many sequences, want more shared memory than there is)
+  constexpr size_t kRoom = 224 * 1024;
+  const bool split = W > kStepFlight;
+  const size_t numbers = sizeof(int2) * (static_cast<size_t>(S) + 1);
   const bool vec = d % 4 == 0 && is_aligned(kv, 8) && is_aligned(score, 8) && is_aligned(ape, 16) &&
-                   is_aligned(kv_state, 8) && is_aligned(score_state, 8) && is_aligned(out, 8);
+                   is_aligned(kv_state, 8) && is_aligned(score_state, 8) && is_aligned(out, 8) &&
+                   numbers + step_part_bytes(4, split) + step_stage_bytes(4) <= kRoom;
   p.chunks = vec ? d / 4 : d;
   // up to 8 positions a thread; longer windows between 4 threads and more (256 at most: CSA_MAX_WINDOW is 2048)
-  p.PG = p.W > kStepFlight ? kStepJoin : 1;
+  p.PG = split ? kStepJoin : 1;
   while (p.PG * kStepFlight < p.W) p.PG *= 2;
   // Few tokens a sequence: the kernel without a pipeline, a CTA a sequence (64 single tokens of 512 in blocks of 4
   // in 5.2 instead of 7.7 us; 200 of 128 in blocks of 128 in 8.2 instead of 11.5), up to where one sequence may
@@ -872,7 +880,6 @@ extern "C" csa_status_t csa_compressor_step(
   const int most = threads / p.PG, slices = (p.chunks + most - 1) / most;
   p.CL = (p.chunks + slices - 1) / slices;
   p.RS = threads / (p.CL * p.PG);
-  const bool split = p.PG > 1;
   const int uw = p.W > (split ? 16 : 4) ? 8 : p.W > 2 ? 4 : p.W > 1 ? 2 : 1;
   auto pick = [&](auto v) -> const void* {
     constexpr int V = decltype(v)::value;
@@ -900,9 +907,8 @@ extern "C" csa_status_t csa_compressor_step(
     return launch_pdl(k, dim3((S + p.RS - 1) / p.RS, slices), dim3(block < 64 ? 64 : block), 0, cs, args) == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
   }
   // three turns under way, fewer where many sequences' numbers need the room
-  constexpr size_t kRoom = 224 * 1024;
   const int width = vec ? 4 : 1;
-  const size_t fixed = sizeof(int2) * (static_cast<size_t>(S) + 1) + step_part_bytes(width, split);
+  const size_t fixed = numbers + step_part_bytes(width, split);
   p.stages = 3;
   while (p.stages > 1 && fixed + static_cast<size_t>(p.stages) * step_stage_bytes(width) > kRoom) --p.stages;
   const size_t smem = fixed + static_cast<size_t>(p.stages) * step_stage_bytes(width);

@@ -228,7 +228,8 @@ csa_status_t csa_compressor_map_blocks(const int32_t* cu_seqlens, int32_t S, int
  *     sum over s of floor((first[s] + n_s) / ratio) - floor(first[s] / ratio), n_s new tokens.
  *   What a later window still reads lies in a state, kv and score bf16 [ratio * coff, coff * d] each;
  *   position p's row is p mod (ratio * coff). Sequence s goes on from state source[s] and
- *   leaves its tokens in state target[s], often the same one. With B = floor((first[s] + n_s) / ratio)
+ *   leaves its tokens in state target[s], often the same one. first[s] + n_s is below 2^31 - 4096.
+ *   With B = floor((first[s] + n_s) / ratio)
  *   the elements that state target[s] holds after the call are
  *     coff=1: all columns of the positions p >= B ratio;
  *     coff=2: the columns < d of p >= (B - 1) ratio, and the columns >= d of p >= B ratio;

@@ -200,6 +200,73 @@ def test_calls_that_need_no_state(cuda_lib):
     assert raw(cuda_lib, nulls=True)[0] == 0
 
 
+@pytest.mark.parametrize("ratio,coff,tokens", [(2, 1, 5), (2, 2, 5), (4, 1, 90), (16, 1, 5), (16, 2, 90), (2048, 1, 90), (1024, 2, 5)])
+def test_last_positions(cuda_lib, ratio, coff, tokens):
+    """The last tokens that positions reach: their blocks and what the state holds of them; and one more is refused."""
+    end, d = 2 ** 31 - 4097, 8
+    g = torch.Generator().manual_seed(11)
+    kv, score = (torch.randn(tokens, coff * d, generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    first = end - tokens
+    made = end // ratio - first // ratio
+    err, out, st, pos, _, entries = raw(cuda_lib, ratio, coff, d, (0, tokens), (first,), rows=made + 1, kv=kv, score=score)
+    assert err == 0 and entries == [end // ratio]
+    assert pos == [(first // ratio + i) * ratio for i in range(made)] + [-1]
+    full = torch.full((ratio * coff + tokens, coff * d), 5.0, dtype=torch.bfloat16)  # the state's positions, then the new ones
+    full[-tokens:] = kv.cpu()
+    sc = torch.full_like(full, 5.0)
+    sc[-tokens:] = score.cpu()
+    for i in range(made):
+        x, k = [], []
+        for p in range((first // ratio + i - coff + 1) * ratio, (first // ratio + i + 1) * ratio):
+            half = 0 if coff == 1 or p < (first // ratio + i) * ratio else 1
+            row = p - first + ratio * coff
+            k.append(full[row, half * d:half * d + d].double())
+            x.append(sc[row, half * d:half * d + d].double())
+        x, k = torch.stack(x), torch.stack(k)
+        ref = (torch.softmax(x, 0) * k).sum(0)
+        assert ((out[i].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 1e-4).all()  # (values and scores of 5: 150 U of them)
+    W = ratio * coff
+    for half in range(coff):
+        keep = max(0, end // ratio - (coff - 1 - half)) * ratio
+        for p in range(max(keep, first), end):
+            for t, of in zip(st, (kv, score)):
+                assert torch.equal(t[0, p % W, half * d:half * d + d], of[p - first, half * d:half * d + d])
+    err, out, st, *_ = raw(cuda_lib, ratio, coff, d, (0, tokens), (first + 1,), rows=made + 1, kv=kv, score=score)
+    assert err == 8 and all((t == 5.0).all() for t in st)
+
+
+@pytest.mark.parametrize("ratio,coff,d", [(4, 2, 8), (16, 1, 4), (16, 2, 3)])
+def test_most_sequences(cuda_lib, ratio, coff, d):
+    """As many sequences as a call may have, whose numbers leave less room for tokens under way: the same bits as a
+    quarter of them at a time."""
+    S = 16384
+    g = torch.Generator().manual_seed(12)
+    lens = torch.randint(0, 2 * ratio, (S,), generator=g)
+    first = torch.randint(0, 3 * ratio, (S,), generator=g).to(torch.int32)
+    W, C = coff * ratio, coff * d
+    kv, score = (torch.randn(int(lens.sum()), C, generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    ape = torch.randn(ratio, C, generator=g).cuda()
+    states = [torch.randn(S, W, C, generator=g).to(torch.bfloat16).cuda() for _ in range(2)]
+    cu = torch.cat([torch.zeros(1, dtype=torch.int64), lens.cumsum(0)])
+    made = (first + lens) // ratio - first // ratio
+    slot = torch.arange(S, **I32)
+
+    def call(a, b, st):
+        rows, t0, t1 = int(made[a:b].sum()), int(cu[a]), int(cu[b])
+        out, pos, err = torch.zeros(rows, d, dtype=torch.bfloat16, device="cuda"), torch.zeros(rows, **I32), torch.zeros(1, **I32)
+        cuda_lib.csa_compressor_step(kv[t0:t1].clone(), score[t0:t1].clone(), ape, (cu[a:b + 1] - t0).to(torch.int32).cuda(), b - a, ratio, coff, d,
+                                     t1 - t0, first[a:b].cuda(), slot[a:b].clone(), slot[a:b].clone(), S, *st, out, rows, None, None, 0, 1, 0,
+                                     pos, None, None, err)
+        torch.cuda.synchronize()
+        assert int(err) == 0
+        return out, pos
+    one, two = [t.clone() for t in states], [t.clone() for t in states]
+    whole = call(0, S, one)
+    parts = [call(a, a + S // 4, two) for a in range(0, S, S // 4)]
+    assert torch.equal(whole[0], torch.cat([x[0] for x in parts])) and torch.equal(whole[1], torch.cat([x[1] for x in parts]))
+    assert all(torch.equal(x, y) for x, y in zip(one, two))
+
+
 def test_pages_that_are_missing(cuda_lib):
     err, out, _, pos, slots, entries = raw(cuda_lib, cu=(0, 8), rows=5, table=((3, -1),), max_pages=2, page=1)
     assert err == 7 and slots == [3, -1, -1, -1, -1] and pos == [0, 2, 4, 6, -1] and entries == [4] and (out[:4] == 1.0).all()
