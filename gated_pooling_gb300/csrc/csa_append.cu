@@ -168,18 +168,18 @@ __global__ void __launch_bounds__(kRopeThreads) append_scalar_kernel(const __gri
   }
 }
 
-// A warp's run of heads (of less than 2^31, as RopeRun): this lane's row and head, and where its x begins, moving on
-// by the warp's groups with additions alone.
+// A warp's run of heads (of less than 2^31, as RopeRun; counted without a sign, since the last step may pass that): this
+// lane's row and head, and where its x begins, moving on by the warp's groups with additions alone.
 template <typename T>
 struct AppendRun {
-  int u, end, row, head;  // unit of this lane's group, end of the warp's run
+  unsigned u, end, row, head;  // unit of this lane's group, end of the warp's run
   const T* x;
   int groups, step_rows, step_heads;
   int64_t step, wrap;
   __device__ __forceinline__ AppendRun(const AppendParams& q, int group, int n) : groups(n) {
     const RopeParams& p = q.r;
     const int w = blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
-    u = w * q.each + min(w, q.more);
+    u = static_cast<unsigned>(w * q.each + min(w, q.more));
     end = u + q.each + (w < q.more ? 1 : 0);
     u += group;
     row = p.heads == 1 ? u : u / p.heads;
@@ -195,7 +195,7 @@ struct AppendRun {
     row += step_rows;
     head += step_heads;
     x += step;
-    if (head >= p.heads) {
+    if (head >= static_cast<unsigned>(p.heads)) {
       head -= p.heads;
       ++row;
       x += wrap;
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(kRopeThreads, PP == 1 && DTYPE != CSA_DTYPE_FP
   stage_weight(p, s_w);
   const float inv_d = 1.f / static_cast<float>(p.d);
   AppendRun<T> run(q, L.group, L.groups);
-  int base = run.u - L.group;  // the warp's first unit: all its lanes leave the loop together
+  unsigned base = run.u - L.group;  // the warp's first unit: all its lanes leave the loop together
   RopePieces<DTYPE, PP> cur{}, nxt{};  // (pieces that a lane does not have stay 0)
   int32_t pos = -1, pos_n = -1;
   int64_t slot = -1, slot_n = -1;
@@ -240,9 +240,9 @@ __global__ void __launch_bounds__(kRopeThreads, PP == 1 && DTYPE != CSA_DTYPE_FP
     }
   };
   fetch(cur, pos, slot);
-  int turned = -1;
+  unsigned turned = ~0u;
   for (; base < run.end; base += L.groups) {
-    const int row = run.row, head = run.head;
+    const unsigned row = run.row, head = run.head;
     run.next(p);
     fetch(nxt, pos_n, slot_n);
     const bool live = pos >= 0 && static_cast<uint64_t>(slot) < static_cast<uint64_t>(q.num_slots);

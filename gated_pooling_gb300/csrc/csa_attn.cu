@@ -213,13 +213,15 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnParams p) {
 // The same behind shared prefixes: units of a group's rows, whatever sequences they are of, and their spans.
 // `lanes` neighbouring threads work on a block of 64 rows, a sequence each (as many as single tokens have in
 // one), and write its units of all cache heads. What is looked up again and again is held in shared
-// memory: sequences' numbers up to kPlanCached of them, spans' first tiles up to kPlanSpans.
+// memory: sequences' numbers where they fit beside the groups' (plan_cached), spans' first tiles up to kPlanSpans.
 // (A thread a unit, which walked through its sequences three times, took 9 us for 64 sequences of 64 heads
 // and 23 for 120 of 8.)
 // SMALL: at most kSmallSeqs sequences and 32 groups, whose blocks go through in one round, and up to kSmallUnits
 // units with all their work in 32 bits. There the plan's time is a chain of loads and code that runs once, so the
 // loads come side by side, and nothing is 64 bits wide or read back from memory.
-constexpr int kPlanCached = 4096, kPlanSpans = 2048, kSmallSeqs = kPlanThreads, kSmallUnits = 256;
+constexpr int kPlanSpans = 2048, kSmallSeqs = kPlanThreads, kSmallUnits = 256;
+// (4096 sequences, fewer beside more than 12500 groups, whose numbers are held in any case)
+__host__ __device__ constexpr bool plan_cached(int S, int G) { return S <= 4096 && S + G <= 16600; }
 template <bool SMALL>
 __global__ void __launch_bounds__(kPlanThreads) attn_prefix_plan_kernel(AttnParams p, int lanes) {
   using W = std::conditional_t<SMALL, int, int64_t>;
@@ -239,7 +241,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_prefix_plan_kernel(AttnPara
   int* s_cu = s_prefix + G;
   int* s_own = s_cu + p.S + 1;
   int* s_pos = s_own + p.S;
-  const bool cached = SMALL || p.S <= kPlanCached;
+  const bool cached = SMALL || plan_cached(p.S, G);
   if (threadIdx.x < 2) s_joins[threadIdx.x] = 0;
   pdl_wait();
   // (one block, which leaves room for the next kernel's: they set themselves up meanwhile, and wait for this one's
@@ -852,7 +854,7 @@ csa_status_t run_attn(const AttnCall& c, csa_stream_t stream) {
   void* args[] = {&p};
   int dev = 0, bps = 0;
   if (note(cudaGetDevice(&dev)) != cudaSuccess) return CSA_ERR_CUDA;
-  const size_t plan_smem = sizeof(int) * (groups > 0 ? 3 * static_cast<size_t>(groups) + 2 + (S <= kPlanCached ? 3 * static_cast<size_t>(S) + 1 : 0)
+  const size_t plan_smem = sizeof(int) * (groups > 0 ? 3 * static_cast<size_t>(groups) + 2 + (plan_cached(S, groups) ? 3 * static_cast<size_t>(S) + 1 : 0)
                                                      : static_cast<size_t>(S) + 1);
   // behind prefixes: a thread for each sequence that single tokens would have in 64 rows
   const int per_block = kAttnRows % p.group == 0 ? kAttnRows / p.group : kAttnRows / p.group + 2;

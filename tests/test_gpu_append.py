@@ -186,3 +186,17 @@ def test_graph_and_repeats(cuda_lib):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(one[0], two[0]) and torch.equal(one[1], two[1])
+
+
+def test_heads_up_to_the_last_number(cuda_lib):
+    """2^31 - 1 rows' heads that repeat one row of x: the count goes on past 2^31 in no warp."""
+    heads, d = 2 ** 31 - 1, 8
+    x = torch.randn(1, 1, d).to(torch.bfloat16).cuda()
+    data = torch.zeros(heads, d, dtype=torch.bfloat16, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    cuda_lib.csa_cache_append(x, 0, 1, heads, d, 0, 0, None, 0, 0.0, None, None, 0, 0, 0, 1.0, torch.zeros(1, dtype=torch.int64, device="cuda"),
+                              1, R.BF16, data, None, err)
+    torch.cuda.synchronize()
+    assert int(err) == 0
+    for at in range(0, heads, 1 << 28):
+        assert (data[at:at + (1 << 28)].view(torch.int64) == x.view(torch.int64).view(1, 2)).all()

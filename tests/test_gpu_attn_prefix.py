@@ -320,6 +320,17 @@ def test_repeats_and_graph(cuda_lib):
     assert ((one.out.double().cpu() - ref).abs() <= tol)[:4].all()
 
 
+@pytest.mark.parametrize("groups,seqs", [(16384, 1), (12300, 1300), (16384, 300), (16000, 700), (1, 4200), (1300, 16384)])
+def test_most_groups_and_sequences(cuda_lib, groups, seqs):
+    """Group and sequence lists of any size, most of the one empty or all of the other alone."""
+    rng = random.Random(groups + seqs)
+    some = sorted(rng.randrange(groups) for _ in range(seqs))
+    lists = [[] for _ in range(groups)]
+    for g in some:
+        lists[g].append((1 if rng.random() < 0.9 else 0, rng.randrange(0, 20)))
+    Case([(rng.randrange(0, 9) if x else 0, x) for x in lists], 2, 1, 64, page=8, seed=31).check(cuda_lib)
+
+
 @pytest.mark.parametrize("fmt,lens", [(R.BF16, 1), (R.E4M3, 1), (R.E4M3, 40)])
 def test_a_wait_that_runs_out(cuda_lib, fmt, lens):
     """A tile that never comes in: the call returns, reports it, leaves other rows alone, and the next one is right."""
