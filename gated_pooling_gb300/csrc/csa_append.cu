@@ -259,14 +259,14 @@ __global__ void __launch_bounds__(kRopeThreads, PP == 1 && DTYPE != CSA_DTYPE_FP
         ss = fmaf(xb[s][i], xb[s][i], ss);
       }
     }
-    // A row's angles are worked out by all lanes of its heads, or of the warp where it has one row, whichever
-    // turn columns by them (with 64 of 512 columns turned, four at a time in eight lanes took as long as the
-    // rest).
+    // A row's angles are worked out by all lanes of its heads in the warp, whichever turn columns by them (with 64 of
+    // 512 columns turned, four at a time in eight lanes took as long as the rest; 22706 rows of 2 heads of 128,
+    // put in and read back: 12.8 us, 14.1 where each head's lanes worked out all of them).
     if (p.rot > 0 && __any_sync(0xFFFFFFFFu, live && row != turned)) {
-      const bool one = __all_sync(0xFFFFFFFFu, row == __shfl_sync(0xFFFFFFFFu, row, 0));
-      const int32_t at = one ? __shfl_sync(0xFFFFFFFFu, pos, 0) : pos;
-      float2* turn = s_turn[threadIdx.x >> 5] + (one ? 0 : L.group * (p.rot / 2));
-      for (int i = one ? L.lane : L.sub; i < p.rot / 2; i += one ? 32 : p.lanes) {
+      const int h = static_cast<int>(head), g0 = max(0, L.group - h), g1 = L.group + min(L.groups - L.group, p.heads - h);
+      const int32_t at = __shfl_sync(0xFFFFFFFFu, pos, g0 * p.lanes);  // (the first of them is there if any is)
+      float2* turn = s_turn[threadIdx.x >> 5] + g0 * (p.rot / 2);
+      for (int i = L.lane - g0 * p.lanes; i < p.rot / 2; i += (g1 - g0) * p.lanes) {
         float c, n;
         quarter_cos_sin(at, __ldg(p.turns + i), p.amp, c, n);
         turn[i] = make_float2(c, n);
