@@ -163,16 +163,31 @@ __device__ __forceinline__ int step_wrong(const StepParams& p, int a, int b, int
   return f < 0 || f > kStepEnd - n || from >= p.num_states || to >= p.num_states || (from < 0 && live && (n > 0 || to >= 0)) ? 2 : 0;
 }
 
+// Asks L2 for the tokens of about the first `rows` rows of this CTA, by its place among those that see to rows: which
+// they are is not known before the rows are counted, but the rows lie about as the tokens do.
+__device__ __forceinline__ void ask_ahead(const StepParams& p, int tokens, int rows) {
+  const int worker = static_cast<int>(blockIdx.x) - p.first_row_cta, workers = p.R - p.first_row_cta;
+  if (worker < 0 || blockIdx.y != 0 || tokens <= 0 || tokens > p.capacity) return;
+  const int64_t t0 = static_cast<int64_t>(tokens) * worker / workers, share = static_cast<int64_t>(tokens) * (worker + 1) / workers;
+  const int64_t t1 = min(share, t0 + static_cast<int64_t>(rows) * p.ratio);
+  const char *kv = reinterpret_cast<const char*>(p.kv), *score = reinterpret_cast<const char*>(p.score);
+  for (int64_t at = t0 * p.C * 2 + threadIdx.x * 128; at < t1 * p.C * 2; at += kStepThreads * 128) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(kv + at));
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(score + at));
+  }
+}
+
 // Rows before each sequence (x), and those of them whose windows reach into no state (y), in shared memory, [S]
 // holding all of them; false with the reason reported where the call's numbers are refused. Every thread of the
 // block calls it.
-__device__ bool build_step_prefix(const StepParams& p, int2* sB, int2* warp_sums) {
+__device__ bool build_step_prefix(const StepParams& p, int2* sB, int2* warp_sums, int rows) {
   pdl_wait();
   int2 carry = make_int2(0, 0);
   int bad = 0;
   for (int base = 0; base < p.S || base == 0; base += blockDim.x) {
     const int s = base + threadIdx.x;
     int made = 0, inner = 0;
+    const int tokens = base == 0 ? __ldg(p.cu + p.S) : 0;
     if (s < p.S) {
       const int a = __ldg(p.cu + s), b = __ldg(p.cu + s + 1), f = __ldg(p.first + s);
       const int why = step_wrong(p, a, b, f, __ldg(p.source + s), __ldg(p.target + s));
@@ -183,6 +198,7 @@ __device__ bool build_step_prefix(const StepParams& p, int2* sB, int2* warp_sums
         inner = made - StepSeq::boundary_of(p, f, lo, made);
       }
     }
+    if (base == 0) ask_ahead(p, tokens, rows);
     int2 all;
     const int2 before = step_scan(make_int2(made, inner), warp_sums, all);
     if (s < p.S) sB[s] = make_int2(carry.x + before.x, carry.y + before.y);
@@ -338,7 +354,7 @@ __global__ void __launch_bounds__(kStepThreads, 1) step_kernel(const __grid_cons
   __shared__ int2 warp_sums[32];
   float* const s_part = reinterpret_cast<float*>(s_raw + p.stages * step_stage_bytes(VEC));  // [2][RS][3][PG][CL * VEC]
   int2* const s_prefix = reinterpret_cast<int2*>(s_raw + p.stages * step_stage_bytes(VEC) + step_part_bytes(VEC, SPLIT));  // [S + 1]
-  if (!build_step_prefix(p, s_prefix, warp_sums)) return;
+  if (!build_step_prefix(p, s_prefix, warp_sums, p.stages * p.RS * K)) return;
   const int g = blockIdx.x, tid = threadIdx.x, per = p.CL * p.PG;
   const int rs = tid / per, pg = tid % per / p.CL, cl = tid % p.CL;
   const int chunk = blockIdx.y * p.CL + cl, c0 = chunk * VEC;
