@@ -21,9 +21,10 @@
 namespace csa {
 namespace {
 
-constexpr int kStepThreads = 512;
+constexpr int kStepThreads = 256;
 constexpr int kStepFlight = 8;  // (kv, score) pieces that a thread loads at a time
 constexpr int kStepJoin = 4;    // threads that join a column's parts, of at least as many
+constexpr int kStepRound = 4;   // sequences whose numbers a thread looks up at a time, where there are many
 // A sequence's positions end below this, so that one that is counted on by a round (kStepFlight times the threads that
 // share a window, CSA_MAX_WINDOW), or by two, is an int still.
 constexpr int kStepEnd = INT_MAX - 2 * CSA_MAX_WINDOW;
@@ -184,24 +185,41 @@ __device__ bool build_step_prefix(const StepParams& p, int2* sB, int2* warp_sums
   pdl_wait();
   int2 carry = make_int2(0, 0);
   int bad = 0;
-  for (int base = 0; base < p.S || base == 0; base += blockDim.x) {
-    const int s = base + threadIdx.x;
-    int made = 0, inner = 0;
+  // a sequence a thread; of more than there are threads four neighbouring ones, so that there are fewer rounds
+  const int per = p.S > kStepThreads ? kStepRound : 1;
+  for (int base = 0; base < p.S || base == 0; base += kStepThreads * per) {
+    const int s0 = base + static_cast<int>(threadIdx.x) * per;
     const int tokens = base == 0 ? __ldg(p.cu + p.S) : 0;
-    if (s < p.S) {
-      const int a = __ldg(p.cu + s), b = __ldg(p.cu + s + 1), f = __ldg(p.first + s);
-      const int why = step_wrong(p, a, b, f, __ldg(p.source + s), __ldg(p.target + s));
-      bad |= why;
-      if (why == 0) {
-        const int lo = f / p.ratio;
-        made = (f + (b - a)) / p.ratio - lo;
-        inner = made - StepSeq::boundary_of(p, f, lo, made);
+    int a[kStepRound + 1], f[kStepRound], from[kStepRound], to[kStepRound];
+    int2 rows_of[kStepRound], mine = make_int2(0, 0);
+    if (s0 < p.S) a[0] = __ldg(p.cu + s0);
+#pragma unroll
+    for (int j = 0; j < kStepRound; ++j)
+      if (j < per && s0 + j < p.S) {
+        a[j + 1] = __ldg(p.cu + s0 + j + 1);
+        f[j] = __ldg(p.first + s0 + j);
+        from[j] = __ldg(p.source + s0 + j);
+        to[j] = __ldg(p.target + s0 + j);
+      }
+    if (base == 0) ask_ahead(p, tokens, rows);
+#pragma unroll
+    for (int j = 0; j < kStepRound; ++j) {
+      rows_of[j] = mine;
+      if (j < per && s0 + j < p.S) {
+        const int why = step_wrong(p, a[j], a[j + 1], f[j], from[j], to[j]);
+        bad |= why;
+        if (why == 0) {
+          const int lo = f[j] / p.ratio, made = (f[j] + (a[j + 1] - a[j])) / p.ratio - lo;
+          mine.x += made;
+          mine.y += made - StepSeq::boundary_of(p, f[j], lo, made);
+        }
       }
     }
-    if (base == 0) ask_ahead(p, tokens, rows);
     int2 all;
-    const int2 before = step_scan(make_int2(made, inner), warp_sums, all);
-    if (s < p.S) sB[s] = make_int2(carry.x + before.x, carry.y + before.y);
+    const int2 before = step_scan(mine, warp_sums, all);
+#pragma unroll
+    for (int j = 0; j < kStepRound; ++j)
+      if (j < per && s0 + j < p.S) sB[s0 + j] = make_int2(carry.x + before.x + rows_of[j].x, carry.y + before.y + rows_of[j].y);
     carry.x += all.x;
     carry.y += all.y;
   }
@@ -342,11 +360,13 @@ __host__ __device__ constexpr int step_part_bytes(int vec, bool split) { return 
 // time instead (K rows), so that as many bytes are under way. SPLIT: windows of more than 8 positions, which
 // PG threads share.
 //
-// A thread's pieces come into places of its own in shared memory (no barrier), p.stages turns ahead: 64 KB a turn
-// and SM. Three chunks of up to 8192 tokens of 512 in blocks of 4 take 17.7 us (56 % of the copy rate), four of up to
-// 16384 in blocks of 128 36.6 us (55 %); registers held one turn ahead, less than latency asks for: 22.7 and 43.8 us.
+// A thread's pieces come into places of its own in shared memory (no barrier), p.stages turns ahead: 32 KB a turn
+// and CTA. Two CTAs an SM, so that one has something to do while the other counts rows, waits or joins parts (one
+// of 512 threads: 16.7, 35.7 and 14.1 us below). Three chunks of up to 8192 tokens of 512 in blocks of 4 take 15.9 us
+// (62 % of the copy rate), four of up to 16384 in blocks of 128 33.6 us (60 %), five of up to 1805 tokens of 128 in
+// blocks of 16 11.8; registers held one turn ahead, less than latency asks for: 22.7 and 43.8 for the first two.
 template <int VEC, int UW, bool SPLIT>
-__global__ void __launch_bounds__(kStepThreads, 1) step_kernel(const __grid_constant__ StepParams p) {
+__global__ void __launch_bounds__(kStepThreads, 2) step_kernel(const __grid_constant__ StepParams p) {
   constexpr int K = SPLIT ? 1 : kStepFlight / UW, PAIRS = VEC == 4 ? 2 : 1;
   constexpr uint32_t kAll = (1u << UW) - 1u;
   using P = Piece<VEC>;
@@ -877,13 +897,9 @@ extern "C" csa_status_t csa_compressor_step(
   p.max_pages = max_pages;
   p.page_size = page_size;
   p.offset = position_offset;
-  // (four columns a thread, and the numbers of very many sequences, want more shared memory than there is)
-  constexpr size_t kRoom = 224 * 1024;
   const bool split = W > kStepFlight;
-  const size_t numbers = sizeof(int2) * (static_cast<size_t>(S) + 1);
   const bool vec = d % 4 == 0 && is_aligned(kv, 8) && is_aligned(score, 8) && is_aligned(ape, 16) &&
-                   is_aligned(kv_state, 8) && is_aligned(score_state, 8) && is_aligned(out, 8) &&
-                   numbers + step_part_bytes(4, split) + step_stage_bytes(4) <= kRoom;
+                   is_aligned(kv_state, 8) && is_aligned(score_state, 8) && is_aligned(out, 8);
   p.chunks = vec ? d / 4 : d;
   // up to 8 positions a thread; longer windows between 4 threads and more (256 at most: CSA_MAX_WINDOW is 2048)
   p.PG = split ? kStepJoin : 1;
@@ -922,12 +938,14 @@ extern "C" csa_status_t csa_compressor_step(
     const int block = (p.CL * p.PG + 31) / 32 * 32;
     return launch_pdl(k, dim3((S + p.RS - 1) / p.RS, slices), dim3(block < 64 ? 64 : block), 0, cs, args) == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
   }
-  // three turns under way, fewer where many sequences' numbers need the room
+  // Three turns under way, or as many as leave room for two CTAs an SM beside the sequences' numbers; a CTA an SM where
+  // not one does (at most 155 KB of numbers and parts: one turn fits always).
   const int width = vec ? 4 : 1;
-  const size_t fixed = numbers + step_part_bytes(width, split);
+  const size_t fixed = sizeof(int2) * (static_cast<size_t>(S) + 1) + step_part_bytes(width, split), turn = step_stage_bytes(width);
+  const size_t room_for = fixed + turn <= 112 * 1024 ? 112 * 1024 : 224 * 1024;
   p.stages = 3;
-  while (p.stages > 1 && fixed + static_cast<size_t>(p.stages) * step_stage_bytes(width) > kRoom) --p.stages;
-  const size_t smem = fixed + static_cast<size_t>(p.stages) * step_stage_bytes(width);
+  while (p.stages > 1 && fixed + p.stages * turn > room_for) --p.stages;
+  const size_t smem = fixed + p.stages * turn;
   if (blocks_per_sm(dev, k, kStepThreads, smem, &bps) != cudaSuccess) return CSA_ERR_CUDA;
   if (bps < 1) return CSA_ERR_UNSUPPORTED;
   const int64_t rows_at_once = p.RS * (split ? 1 : kStepFlight / uw), by_rows = (out_rows + rows_at_once - 1) / rows_at_once;
