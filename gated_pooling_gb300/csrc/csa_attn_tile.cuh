@@ -1109,34 +1109,39 @@ __global__ void __launch_bounds__(kPackThreads) attn_pack_kernel(const __grid_co
   constexpr int kPer = NC * 8;  // pieces of 8 columns
   pdl_wait();
   if (p.head->status != 0) return;
-  // kRows entries from e0 on of a run of n, whose first lies in row row0 of the packed ones
+  // kRows entries from e0 on of a run of n, whose first lies in row row0 of the packed ones: each row's place in the
+  // pool once, by a thread each, then the pieces
   constexpr int kRows = pack_rows(NC, PREFIX), kPieces = kRows * kPer / kPackThreads;  // a thread's
   constexpr int kAtOnce = kPieces < (PREFIX ? 8 : 4) ? kPieces : PREFIX ? 8 : 4;
-  static_assert(kPieces % kAtOnce == 0 && kPieces * kPackThreads == kRows * kPer && kAttnEntries % kRows == 0);
+  static_assert(kPieces % kAtOnce == 0 && kPieces * kPackThreads == kRows * kPer && kAttnEntries % kRows == 0 &&
+                kRows <= kPackThreads);
+  __shared__ int64_t s_entry[kRows];
   auto pack = [&](const int32_t* table, int64_t row0, int kvh, int n, int e0) {
     uint16_t* to = p.packed + (row0 + e0) * (NC * 64);
+    __syncthreads();
+    if (threadIdx.x < kRows) {
+      const int e = e0 + threadIdx.x;
+      int64_t entry = -1;
+      if (e < n) {
+        const int page = __ldg(table + e / p.page_size);
+        if (page >= 0 && page < p.num_pages) entry = (static_cast<int64_t>(page) * p.page_size + e % p.page_size) * p.kv_heads + kvh;
+        else if (p.dev_error != nullptr) *p.dev_error = CSA_DEVERR_PAGE;
+      }
+      s_entry[threadIdx.x] = entry;
+    }
+    __syncthreads();
 #pragma unroll 1
     for (int i0 = threadIdx.x; i0 < kRows * kPer; i0 += kAtOnce * kPackThreads) {
-      // pages, then codes, then rows: each step's loads side by side
-      int page[kAtOnce];
-#pragma unroll
-      for (int k = 0; k < kAtOnce; ++k) {
-        const int i = i0 + k * kPackThreads, e = e0 + i / kPer;
-        page[k] = e < n && (i % kPer) * 8 < p.d ? __ldg(table + e / p.page_size) : -1;
-        if (e < n && (page[k] < 0 || page[k] >= p.num_pages) && (i % kPer) * 8 < p.d) {
-          page[k] = -1;
-          if (p.dev_error != nullptr) *p.dev_error = CSA_DEVERR_PAGE;
-        }
-      }
+      // codes, then rows: each step's loads side by side
       uint4 v[kAtOnce];
       uint32_t scale[kAtOnce];
 #pragma unroll
       for (int k = 0; k < kAtOnce; ++k) {
-        const int i = i0 + k * kPackThreads, col = (i % kPer) * 8, e = e0 + i / kPer;
+        const int i = i0 + k * kPackThreads, col = (i % kPer) * 8;
+        const int64_t entry = s_entry[i / kPer];
         v[k] = make_uint4(0, 0, 0, 0);
         scale[k] = kNoScale;
-        if (page[k] >= 0) {
-          const int64_t entry = (static_cast<int64_t>(page[k]) * p.page_size + e % p.page_size) * p.kv_heads + kvh;
+        if (entry >= 0 && col < p.d) {
           if constexpr (FORMAT == CSA_CACHE_BF16) {
             v[k] = __ldg(reinterpret_cast<const uint4*>(p.data + (entry * p.d + col) * 2));
           } else {
