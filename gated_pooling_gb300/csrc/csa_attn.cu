@@ -690,9 +690,10 @@ bool chunked(const AttnParams& p) {
   if (p.d > kTileMaxDim || p.S < 1) return false;
   if (p.groups > 0) {
     // Behind prefixes: by the tiles that units read of prefixes and those that are packed, own entries too, at the
-    // tables' capacity. Over codes, 64 sequences of 64 heads of 512 behind 16384 entries take 186 us packed and 297
-    // not, 64 54.5 and 68.3 behind 2048, but with up to 2000 own entries each 112 and 90; 4 sequences 45.8 and
-    // 48.6, one 43.1 and 38.4; of 128 columns 77 and 115, 31.5 and 34.4, 46.1 and 40.2; 26.7 and 25.4, 31.0 and 27.6.
+    // tables' capacity. Over codes, 64 sequences of 64 heads of 512 with up to 500 own entries behind 16384 take
+    // 176 us packed and 294 not; with 20 behind 2048 47 and 64; 4 sequences behind 16384 39.9 and 44.0, one 36.9 and
+    // 33.8; with 2000 own ones behind 2048, of which the table knows the most there may be, 83 and 87. Of 128 columns 69 and
+    // 112, 27.2 and 32.3, 22.9 and 23.6, 27.2 and 26.1, 35.2 and 37.9.
     const int64_t units = (p.tokens * p.group + kAttnRows - 1) / kAttnRows, tiles = p.prefix_rows / kAttnEntries;
     const int64_t packed = p.groups * tiles + static_cast<int64_t>(p.S) * (p.packed_rows / kAttnEntries);
     if (units * tiles < 2 * packed + 200) return false;
@@ -813,8 +814,8 @@ csa_status_t run_attn(const AttnCall& c, csa_stream_t stream) {
   // 909 and 1382.
   const bool wide = format != CSA_CACHE_BF16 && d > 128;
   // Behind prefixes bf16 comes by copies at any d: the prefix's come from L2 (64 sequences of 64 heads of 512
-  // behind 16384 entries: 168 us, by threads 280, packed 246; 48 with up to 8000 own entries behind 128: 80,
-  // 111 and 150).
+  // behind 16384 entries: 164 us, by threads 280, packed 179; 48 with up to 8000 own entries behind 128: 46, packed
+  // 103).
   const bool chunks = tile && chunked(p) && (groups > 0 ? !copies : !(copies && nc < 8) &&
                       tokens * p.group >= (wide ? kChunkRowsWide : kChunkRows) * S);
   // A unit's own cost (q in, output out, the pipeline's start) in tiles, by which shares are evened
