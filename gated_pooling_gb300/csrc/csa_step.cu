@@ -660,28 +660,33 @@ __global__ void __launch_bounds__(kStepThreads, 2) step_kernel(const __grid_cons
 // Calls of few tokens a sequence: a CTA per p.RS sequences and column slice, whose blocks it works out one after
 // another. What counts is the way from the lengths to the entry, so there is little code; the first window and the
 // embedding come while the rows before it are counted, and so does what goes into the states, which the lines of CL
-// threads share out among them.
-constexpr int kFewThreads = 256;
+// threads share out among them. Where one sequence has more tokens than the others (a chunk of a prompt in a batch of
+// single ones), its blocks from the kFewBlocks-th on, which read no state, are shared out among all CTAs (440 tokens
+// beside 63 single ones, blocks of 4, d 512: 17.6 us, 130 in one CTA; 3500 beside 511 26 and 1012).
+constexpr int kFewThreads = 256, kFewSeqs = 512, kFewBlocks = 8;
 template <int VEC, int UW, bool SPLIT>
 __global__ void __launch_bounds__(kFewThreads, SPLIT ? 2 : 1) step_few_kernel(const __grid_constant__ StepParams p) {
   using P = Piece<VEC>;
   __shared__ __align__(16) float s_part[SPLIT ? 3 * kFewThreads * VEC : 4];
-  __shared__ int s_sums[2][kFewThreads / 32];
+  __shared__ int2 s_sums[kFewThreads / 32];
+  __shared__ int2 s_rows[kFewSeqs];  // where blocks are shared out: rows before each sequence, and of those shared out
   const int tid = threadIdx.x, per = p.CL * p.PG, s0 = blockIdx.x * p.RS, s1 = min(p.S, s0 + p.RS);
   const int pg = tid / p.CL, cl = tid - pg * p.CL;
   const int chunk = blockIdx.y * p.CL + cl, c0 = chunk * VEC;
   const bool two = p.coff == 2, mine = tid < per && chunk < p.chunks;
   pdl_wait();
-  // the whole call's lengths: what is wrong with them, the rows before these sequences and of all
-  int bad = 0, before = 0, all = 0;
+  // the whole call's lengths: what is wrong with them, the rows before these sequences and (from bit 13 on: at most 8
+  // tokens a sequence come here) of all, and the shared-out ones
+  static_assert(8 * kFewSeqs < 1 << 13);
+  int bad = 0, rows = 0, shared = 0;
   for (int i = tid; i < p.S; i += blockDim.x) {
     const int a = __ldg(p.cu + i), b = __ldg(p.cu + i + 1), f = __ldg(p.first + i);
     const int from = __ldg(p.source + i), to = __ldg(p.target + i), why = step_wrong(p, a, b, f, from, to);
     bad |= why;
     if (why == 0) {
       const int made = (f + (b - a)) / p.ratio - f / p.ratio;
-      all += made;
-      before += i < s0 ? made : 0;
+      rows += (made << 13) + (i < s0 ? made : 0);
+      shared += max(0, made - kFewBlocks);
     }
   }
   // (numbers of one sequence, of which nothing is read until they are known to be right)
@@ -721,7 +726,7 @@ __global__ void __launch_bounds__(kFewThreads, SPLIT ? 2 : 1) step_few_kernel(co
     }
     ++next;
   }
-  if (next < s1) {
+  auto embed = [&]() {
 #pragma unroll
     for (int u = 0; u < UW; ++u) {
       const int w = pg + u * p.PG;
@@ -735,7 +740,8 @@ __global__ void __launch_bounds__(kFewThreads, SPLIT ? 2 : 1) step_few_kernel(co
 #pragma unroll
       for (int i = 0; i < Weighed<VEC>::kPairs; ++i) embedding[u][i] = f2_pack(e[2 * i] * kLog2e, e[2 * i + 1] * kLog2e);
     }
-  }
+  };
+  if (next < s1) embed();
   // what goes into the states: lines / RS of them to a sequence, each the positions of its turn
   const int lines = p.PG / p.RS, ks = s0 + pg / lines;
   const StepSeq kq(p, min(ks, p.S - 1));
@@ -762,18 +768,16 @@ __global__ void __launch_bounds__(kFewThreads, SPLIT ? 2 : 1) step_few_kernel(co
   if (from0 < end) keep_load(0, from0, k0, x0);
   if (from1 < end) keep_load(1, from1, k1, x1);
 
-  before = __reduce_add_sync(0xFFFFFFFFu, before);
-  all = __reduce_add_sync(0xFFFFFFFFu, all);
-  if ((tid & 31) == 0) {
-    s_sums[0][tid >> 5] = before;
-    s_sums[1][tid >> 5] = all;
-  }
+  rows = __reduce_add_sync(0xFFFFFFFFu, rows);
+  shared = __reduce_add_sync(0xFFFFFFFFu, shared);
+  if ((tid & 31) == 0) s_sums[tid >> 5] = make_int2(rows, shared);
   const bool wrong = __syncthreads_or(bad) != 0;
-  before = all = 0;
+  rows = shared = 0;
   for (int w = 0; w < static_cast<int>(blockDim.x) / 32; ++w) {
-    before += s_sums[0][w];
-    all += s_sums[1][w];
+    rows += s_sums[w].x;
+    shared += s_sums[w].y;
   }
+  const int before = rows & 0x1FFF, all = rows >> 13;
   if (wrong || all > p.out_rows) {
     const int which = __syncthreads_or(bad & 1) ? CSA_DEVERR_CU_SEQLENS : wrong ? CSA_DEVERR_STATE : CSA_DEVERR_OUT_ROWS;
     if (tid == 0 && p.dev_error != nullptr) *reinterpret_cast<volatile int32_t*>(p.dev_error) = which;
@@ -782,30 +786,32 @@ __global__ void __launch_bounds__(kFewThreads, SPLIT ? 2 : 1) step_few_kernel(co
   const int wide = p.CL * VEC;
   const Join join(SPLIT ? p.PG : kStepJoin, wide);
   bool here = true;  // the window is there already
-  for (int s = next, row = before; s < s1; ++s) {
-    const StepSeq q(p, s);
-    for (int block = q.lo; block < q.hi; ++block, ++row) {
-      if (!here) fetch(q, block);
-      here = false;
-      uint16_t* out = p.out + static_cast<int64_t>(row) * p.d;
-      if (mine) {
-        Weighed<VEC> r;
-        r.template of<UW>(kv, score, embedding);
-        if constexpr (SPLIT) {
-          r.leave(s_part + join.place(pg, cl * VEC), join.step);
-        } else {
-          r.store(out + c0);
-        }
-      }
+  auto entry = [&](const StepSeq& q, int block, int row) {
+    if (!here) fetch(q, block);
+    here = false;
+    uint16_t* out = p.out + static_cast<int64_t>(row) * p.d;
+    if (mine) {
+      Weighed<VEC> r;
+      r.template of<UW>(kv, score, embedding);
       if constexpr (SPLIT) {
-        __syncthreads();
-        for (int c0 = 0; c0 < wide; c0 += per / Join::kJ) {  // (as often for every lane)
-          const int c = c0 + tid / Join::kJ, col = blockIdx.y * wide + c;
-          join.column(s_part, min(c, wide - 1), tid < per && c < wide && col < p.d ? out + col : nullptr);
-        }
-        __syncthreads();
+        r.leave(s_part + join.place(pg, cl * VEC), join.step);
+      } else {
+        r.store(out + c0);
       }
     }
+    if constexpr (SPLIT) {
+      __syncthreads();
+      for (int c0 = 0; c0 < wide; c0 += per / Join::kJ) {  // (as often for every lane)
+        const int c = c0 + tid / Join::kJ, col = blockIdx.y * wide + c;
+        join.column(s_part, min(c, wide - 1), tid < per && c < wide && col < p.d ? out + col : nullptr);
+      }
+      __syncthreads();
+    }
+  };
+  for (int s = next, row = before; s < s1; ++s) {
+    const StepSeq q(p, s);
+    for (int block = q.lo; block < min(q.hi, q.lo + kFewBlocks); ++block) entry(q, block, row + block - q.lo);
+    row += q.hi - q.lo;
   }
   // (the states were read by this thread, or before the last barrier)
   if (from0 < end) keep_store(0, from0, k0, x0);
@@ -820,6 +826,43 @@ __global__ void __launch_bounds__(kFewThreads, SPLIT ? 2 : 1) step_few_kernel(co
       for (int i = 0; i < 4; ++i)
         if (pos0 + i * lines < end) keep_store(half, pos0 + i * lines, k[i], x[i]);
     }
+  if (shared > 0) {
+    if (next >= s1) embed();  // (no sequence of this CTA's own has wanted it)
+    here = false;
+    if (tid < 32) {
+      int2 sum = make_int2(0, 0);
+      for (int i0 = 0; i0 < p.S; i0 += 32) {
+        const int i = i0 + tid;
+        int made = 0;
+        if (i < p.S) {
+          const int f = __ldg(p.first + i);
+          made = (f + __ldg(p.cu + i + 1) - __ldg(p.cu + i)) / p.ratio - f / p.ratio;
+        }
+        int2 x = make_int2(made, max(0, made - kFewBlocks));
+        const int2 own = x;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int a = __shfl_up_sync(0xFFFFFFFFu, x.x, o), b = __shfl_up_sync(0xFFFFFFFFu, x.y, o);
+          if (tid >= o) x.x += a, x.y += b;
+        }
+        if (i < p.S) s_rows[i] = make_int2(sum.x + x.x - own.x, sum.y + x.y - own.y);
+        sum.x += __shfl_sync(0xFFFFFFFFu, x.x, 31);
+        sum.y += __shfl_sync(0xFFFFFFFFu, x.y, 31);
+      }
+    }
+    __syncthreads();
+    for (int i = blockIdx.x; i < shared; i += gridDim.x) {
+      int s = 0, h = p.S;  // shared-out rows before s <= i < those before h, the last such s
+      while (h - s > 1) {
+        const int mid = (s + h) / 2;
+        if (s_rows[mid].y <= i) s = mid;
+        else h = mid;
+      }
+      const StepSeq q(p, s);
+      const int nth = kFewBlocks + i - s_rows[s].y;  // of the sequence's blocks
+      entry(q, q.lo + nth, s_rows[s].x + nth);
+    }
+  }
   // where the rows go, by the last threads; those behind the last entry
   if (blockIdx.y != 0) return;
   const int back = static_cast<int>(blockDim.x) - 1 - tid;
@@ -905,9 +948,8 @@ extern "C" csa_status_t csa_compressor_step(
   p.PG = split ? kStepJoin : 1;
   while (p.PG * kStepFlight < p.W) p.PG *= 2;
   // Few tokens a sequence: the kernel without a pipeline, a CTA a sequence (64 single tokens of 512 in blocks of 4
-  // in 5.2 instead of 7.7 us; 200 of 128 in blocks of 128 in 8.2 instead of 11.5), up to where one sequence may
-  // have most of them.
-  const bool few = S > 0 && S <= 512 && capacity <= 8 * static_cast<int64_t>(S);
+  // in 5.4 instead of 7.7 us; 200 of 128 in blocks of 128 in 8.0 instead of 11.5).
+  const bool few = S > 0 && S <= kFewSeqs && capacity <= 8 * static_cast<int64_t>(S);
   const int threads = few ? kFewThreads : kStepThreads;
   const int most = threads / p.PG, slices = (p.chunks + most - 1) / most;
   p.CL = (p.chunks + slices - 1) / slices;

@@ -100,6 +100,21 @@ def test_calls_of_any_length(cuda_lib, ratio, coff, d, shift):
         st.call([rng.randint(0, most) if i else most for _ in range(5)], spare=i % 3, lead=i, offset=i % ratio)
 
 
+@pytest.mark.parametrize("ratio,coff,d,S", [(4, 2, 512, 40), (1, 1, 64, 40), (2, 2, 64, 130), (16, 2, 64, 40), (3, 1, 11, 33), (1, 2, 7, 9),
+                                            (4, 1, 128, 512)])
+def test_a_chunk_among_single_tokens(cuda_lib, ratio, coff, d, S):
+    """Batches with room for 8 tokens a sequence, most of which one or two sequences have: their blocks are shared out."""
+    most = 8 * S
+    st = Stream(cuda_lib, S, ratio, coff, d, most + 4 * ratio, seed=S)
+    lens = [1] * S
+    lens[S // 3] = most - S - 10
+    st.call(lens, pad=0, spare=2)
+    lens = [0] * S
+    lens[1], lens[S - 1], lens[S // 3] = most // 2 - 3, most // 2 - 20, 5
+    st.call(lens, pad=0, lead=4)
+    st.call([1] * S)
+
+
 @pytest.mark.parametrize("ratio,coff,d", [(4, 2, 512), (4, 1, 64), (16, 2, 64), (2, 2, 64), (3, 2, 11)])
 def test_single_tokens(cuda_lib, ratio, coff, d):
     st = Stream(cuda_lib, 7, ratio, coff, d, 5 * ratio + 6, seed=3)
