@@ -857,12 +857,15 @@ csa_status_t run_attn(const AttnCall& c, csa_stream_t stream) {
   if (note(cudaGetDevice(&dev)) != cudaSuccess) return CSA_ERR_CUDA;
   const size_t plan_smem = sizeof(int) * (groups > 0 ? 3 * static_cast<size_t>(groups) + 2 + (plan_cached(S, groups) ? 3 * static_cast<size_t>(S) + 1 : 0)
                                                      : static_cast<size_t>(S) + 1);
-  // behind prefixes: a thread for each sequence that single tokens would have in 64 rows
+  // behind prefixes: a thread for each sequence that single tokens would have in 64 rows, or twice as many as have
+  // tokens there on average (4 sequences of 16384 tokens of one head of 64: 99 us, 398 with 32 threads a block; 64 of 64
+  // tokens of 4 heads of 128 48 and 83)
   const int per_block = kAttnRows % p.group == 0 ? kAttnRows / p.group : kAttnRows / p.group + 2;
   int plan_lanes = 1;
-  while (plan_lanes < per_block && plan_lanes < 32) plan_lanes *= 2;
-  const int64_t most_blocks = p.max_units / kv_heads, unit_most = (max_prefix + kAttnEntries - 1) / kAttnEntries + p.unit_cost +
-                                                                kAttnRows * ((max_entries + kAttnEntries - 1) / kAttnEntries);
+  const int64_t most_blocks = p.max_units / kv_heads;
+  while (plan_lanes < per_block && plan_lanes < 32 && plan_lanes * most_blocks < 2 * (most_blocks + S)) plan_lanes *= 2;
+  const int64_t unit_most = (max_prefix + kAttnEntries - 1) / kAttnEntries + p.unit_cost +
+                            kAttnRows * ((max_entries + kAttnEntries - 1) / kAttnEntries);
   const bool small = S <= kSmallSeqs && groups <= 32 && most_blocks * plan_lanes <= kPlanThreads && p.max_units <= kSmallUnits &&
                      p.max_units * unit_most < INT_MAX;
   const void* plan = groups == 0 ? reinterpret_cast<const void*>(attn_plan_kernel)

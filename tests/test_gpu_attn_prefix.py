@@ -320,6 +320,13 @@ def test_repeats_and_graph(cuda_lib):
     assert ((one.out.double().cpu() - ref).abs() <= tol)[:4].all()
 
 
+@pytest.mark.parametrize("H,kv", [(1, 1), (4, 2), (3, 1)])
+def test_chunks_beside_single_tokens(cuda_lib, H, kv):
+    """Few sequences in most blocks of 64 rows and many in some."""
+    Case([(70, [(700, 30)] + [(1, i % 9) for i in range(60)]), (0, [(1, 3)] * 5), (200, [(0, 4)] * 70 + [(2, 140), (900, 9)])], H, kv, 64,
+         page=8, ratio=1, seed=33, lead=1).check(cuda_lib)
+
+
 @pytest.mark.parametrize("groups,seqs", [(16384, 1), (12300, 1300), (16384, 300), (16000, 700), (1, 4200), (1300, 16384)])
 def test_most_groups_and_sequences(cuda_lib, groups, seqs):
     """Group and sequence lists of any size, most of the one empty or all of the other alone."""
