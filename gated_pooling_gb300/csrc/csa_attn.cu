@@ -689,14 +689,16 @@ constexpr int64_t kMaxPacked = int64_t{4} << 30;
 bool chunked(const AttnParams& p) {
   if (p.d > kTileMaxDim || p.S < 1) return false;
   if (p.groups > 0) {
-    // Behind prefixes: by the tiles that units read of prefixes and those that are packed, own entries too, at the
-    // tables' capacity. Over codes, 64 sequences of 64 heads of 512 with up to 500 own entries behind 16384 take
-    // 176 us packed and 294 not; with 20 behind 2048 47 and 64; 4 sequences behind 16384 39.9 and 44.0, one 36.9 and
-    // 33.8; with 2000 own ones behind 2048, of which the table knows the most there may be, 83 and 87. Of 128 columns 69 and
-    // 112, 27.2 and 32.3, 22.9 and 23.6, 27.2 and 26.1, 35.2 and 37.9.
-    const int64_t units = (p.tokens * p.group + kAttnRows - 1) / kAttnRows, tiles = p.prefix_rows / kAttnEntries;
-    const int64_t packed = p.groups * tiles + static_cast<int64_t>(p.S) * (p.packed_rows / kAttnEntries);
-    if (units * tiles < 2 * packed + 200) return false;
+    // Behind prefixes: by the tiles that units read (a prefix's by each, own ones by each unit of a long sequence, or by
+    // the one that several short ones share) and those that are packed, at the tables' capacity. Over codes, 64 sequences of 64
+    // heads of 512 with up to 500 own entries behind 16384 take 176 us packed and 294 not; with 1000 behind 2048 46
+    // and 51, with 2000 53 and 51; 4 sequences behind 16384 39.9 and 44.0, one 36.9 and 33.8; two chunks of up to 1500
+    // tokens of 8 heads of 128 with up to 6000 own entries 203 and 357. Of 128 columns the first take 69 and 112, 100 of
+    // 8 heads behind 4000 with 800 own ones 34.2 and 34.9.
+    const int64_t units = (p.tokens * p.group + kAttnRows - 1) / kAttnRows;
+    const int64_t tiles = p.prefix_rows / kAttnEntries, own = p.packed_rows / kAttnEntries;
+    const int64_t reads = units * tiles + (units > p.S ? units : p.S) * own, packed = p.groups * tiles + p.S * own;
+    if (reads < 2 * packed + 200) return false;
   } else if (p.tokens * p.group < kChunkRows * p.S) {
     return false;
   }
