@@ -414,27 +414,41 @@ struct TileWalk : SegmentWalk {
 };
 template <>
 struct TileWalk<true> : SegmentWalk {
-  AttnSpan span;
   const AttnSpan* next_span;
-  __device__ __forceinline__ TileWalk(const AttnParams& pp, int worker) : SegmentWalk(pp, worker) {
+  const int32_t* span_table;
+  int first, end, span_seen, span_all, span_packed;  // the span's tiles, and what is asked for at each of them
+  __device__ __forceinline__ TileWalk(const AttnParams& pp, int worker) : SegmentWalk(pp, worker) { start(); }
+  // before a unit's first tile
+  __device__ __forceinline__ void start() {
     next_span = p.spans + u.span;
-    span.unit = -1;
+    end = 0;
   }
+  __device__ __forceinline__ void next() {
+    SegmentWalk::next();
+    start();
+  }
+  __device__ __forceinline__ AttnSpan span() const { return read_span(next_span - 1); }
   // whether the tile lies in another span than the one before
   __device__ __forceinline__ bool enter(int tile) {
     bool moved = false;
-    while (span.unit < unit || tile >= span.tile + span.tiles) {
-      span = read_span(next_span++);
+    while (tile >= end) {
+      const AttnSpan v = read_span(next_span++);
+      first = v.tile;
+      end = v.tile + v.tiles;
+      span_seen = v.seen;
+      span_all = v.seen_all;
+      span_table = v.table;
+      span_packed = v.packed;
       moved = true;
     }
     return moved;
   }
-  __device__ __forceinline__ int at(int tile) const { return tile - span.tile; }
-  __device__ __forceinline__ int run_end() const { return min(t1, span.tile + span.tiles); }
-  __device__ __forceinline__ int seen() const { return span.seen; }
-  __device__ __forceinline__ int seen_all() const { return span.seen_all; }
-  __device__ __forceinline__ const int32_t* table() const { return span.table; }
-  __device__ __forceinline__ int packed() const { return span.packed; }
+  __device__ __forceinline__ int at(int tile) const { return tile - first; }
+  __device__ __forceinline__ int run_end() const { return min(t1, end); }
+  __device__ __forceinline__ int seen() const { return span_seen; }
+  __device__ __forceinline__ int seen_all() const { return span_all; }
+  __device__ __forceinline__ const int32_t* table() const { return span_table; }
+  __device__ __forceinline__ int packed() const { return span_packed; }
 };
 // What row `row` of a unit (`some`: it is one of the group's) sees of a span's entries.
 __device__ __forceinline__ int span_limit(const AttnParams& p, const AttnUnit& u, const AttnSpan& v, int r) {
@@ -853,9 +867,10 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
           lim_at ^= 1;
           // an own entry's sequence may have no row in this group: no weight then (some group has rows, and
           // clears what is not finite)
-          idle = w.span.own != 0 && (c0 + kSoftCols <= w.span.row0 || c0 >= w.span.row1);
+          const AttnSpan v = w.span();
+          idle = v.own != 0 && (c0 + kSoftCols <= v.row0 || c0 >= v.row1);
           if (!idle) {
-            if (quad == 0 && lane < kSoftCols) sm.lim[lim_at][c0 + lane] = span_limit(p, w.u, w.span, c0 + lane);
+            if (quad == 0 && lane < kSoftCols) sm.lim[lim_at][c0 + lane] = span_limit(p, w.u, v, c0 + lane);
             barrier_group();
           }
         }
@@ -1087,6 +1102,7 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
     if (more) {
       w.u = sm.next;
       w.bound();
+      if constexpr (PREFIX) w.start();
     }
     // (sm.next and P's place are free again)
     if (named_barrier_or(5, kSoftThreads, (probe & 0x7FFFu) > 0x7F80u || (probe >> 16 & 0x7FFFu) > 0x7F80u))
