@@ -431,7 +431,8 @@ csa_status_t csa_cache_write(const void* x, int32_t dtype, int64_t rows, int32_t
  *   x           dtype [rows, heads, d] with row and head strides in elements (device); may repeat
  *   weight, norm, eps, positions, turns, rot_dim, rot_start, layout, amplitude   as for csa_norm_rope_fwd
  *   slots, num_slots, format, data, scales, dev_error   as for csa_cache_write
- * A row whose position or whose slot is negative is left out. x overlaps neither data nor scales. Refusals as
+ * A row whose position or whose slot is negative is left out; rows of a call have slots of their own (of two in
+ * one, the slot holds parts of either). x overlaps neither data nor scales. Refusals as
  * for the two calls. The vector kernel runs where csa_norm_rope_fwd's does with data in y's place;
  * anything else takes a scalar kernel. */
 csa_status_t csa_cache_append(const void* x, int32_t dtype, int64_t rows, int32_t heads, int32_t d,

@@ -222,3 +222,77 @@ def test_stream_as_the_whole_pack(cuda_lib, ratio, coff, d):
             assert ((x.double() - whole[row].double()).abs() <= 2 * bound).all()
             row += 1
     assert row == rows
+
+
+def test_two_batches_at_once(cuda_lib):
+    """Two captured batches, each with states, pages and a workspace of its own, replayed on two streams at the same
+    time: the same bits as one after the other."""
+    def make(seed):
+        b = Batch(cuda_lib, [300, 64], [0] * 20 + [1] * 4, 80, 4, 2, 128, 16, R.E4M3, seed=seed)
+        b.begin()
+        base = b.prefix_entries[b.dgroups].contiguous()
+        own = [b.G + s for s in range(b.S)]
+        bufs = b.buffers(b.S, b.S * 3, [b.group_of[s] for s in range(b.S)], own)
+        b.fill(bufs, range(b.S), list(b.done), [3] * b.S)
+        bufs["q"].copy_(torch.randn(bufs["q"].shape, generator=b.gen))
+
+        def run():
+            b.pooled(bufs, b.S, base, b.dtables[1], b.pages[1])
+            b.asked(bufs)
+            bufs["first"] += 3
+            bufs["source"].copy_(bufs["target"])
+        return b, bufs, run
+
+    kept = []
+    for at_once in (False, True):
+        pairs = [make(seed) for seed in (50, 51)]
+        streams = [torch.cuda.Stream() for _ in pairs]
+        graphs = []
+        torch.cuda.synchronize()
+        for (_, _, run), stream in zip(pairs, streams):
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.stream(stream), torch.cuda.graph(graph, stream=stream):
+                run()
+            graphs.append(graph)
+        torch.cuda.synchronize()
+        for _ in range(20):
+            for graph, stream in zip(graphs, streams):
+                with torch.cuda.stream(stream):
+                    graph.replay()
+                if not at_once:
+                    torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        kept.append([t.clone() for b, bufs, _ in pairs for t in (b.data, b.kv_state, bufs["o"], bufs["lse"], bufs["out"], bufs["err"])])
+    assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(*kept))
+    assert int(kept[0][5]) == 0 and int(kept[0][11]) == 0
+
+
+@pytest.mark.parametrize("fmt", [R.E4M3, R.FP4])
+def test_packed_call_replayed_on_other_lists(cuda_lib, fmt):
+    """A captured call that packs its entries first, replayed on lists of other lengths than it was captured with."""
+    from tests.test_gpu_attn_prefix import Case
+
+    def make():
+        return Case([(2000, [(5, 300)] * 60), (900, [(7, 90)] * 30)], 16, 1, 128, fmt, ratio=1, seed=60)
+    one, two = make(), make()
+    x, y = one.args(cuda_lib), two.args(cuda_lib)
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            cuda_lib.csa_cache_attn_prefix(*y)
+    torch.cuda.synchronize()
+    new = dict(prefixes=[1290, 0], entries=[i * 3 for i in range(90)], first=[1500 + i for i in range(90)])
+    for args in (x, y):
+        args[16].copy_(torch.tensor(new["prefixes"]))
+        args[21].copy_(torch.tensor(new["entries"][:60] + [e // 3 for e in new["entries"][60:]]))
+        args[22].copy_(torch.tensor(new["first"]))
+    cuda_lib.csa_cache_attn_prefix(*x)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert int(one.err) == 0 and torch.equal(one.out, two.out) and torch.equal(one.lse, two.lse)
+    one.prefixes, one.first = new["prefixes"], new["first"]
+    one.entries = new["entries"][:60] + [e // 3 for e in new["entries"][60:]]
+    ref, _, tol, _ = one.reference()
+    assert ((one.out.double().cpu() - ref).abs() <= tol)[:one.cu[-1]].all()
