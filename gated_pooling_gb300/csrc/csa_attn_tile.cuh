@@ -101,7 +101,7 @@ struct TileSmall {
   AttnUnit next;                    // the worker's next unit
   float sink[2][kAttnRows];
   int32_t lse_at[2][kAttnRows];
-  float less[kAttnRows];  // the rows' bounds, negated
+  float m[kAttnRows];  // the rows' bounds (by copies: negated, as the sums two at a time want them)
   float fac[kAttnRows];
   float red[4][kAttnRows];  // column maxima, then weight sums, by quadrant
   int lim[2][kAttnRows];
@@ -843,7 +843,7 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
   if (w.valid()) {
     if (tid < kAttnRows) {
       set_up(w.u, 0);
-      sm.less[tid] = -kNoMax;
+      sm.m[tid] = kTwos ? -kNoMax : kNoMax;
     }
     named_barrier(5, kSoftThreads);
     copy_q();
@@ -905,7 +905,7 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
 #pragma unroll
           for (int c = 0; c < kSoftCols; c += 4) {
             if constexpr (kTwos) {
-              const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(&sm.less[c0 + c]);
+              const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(&sm.m[c0 + c]);
               const uint64_t a = f2_fma(f2_pack(s[c], s[c + 1]), f2_pack(sl2, sl2), m.x);
               const uint64_t b = f2_fma(f2_pack(s[c + 2], s[c + 3]), f2_pack(sl2, sl2), m.y);
               s[c] = f2_lo(a);
@@ -913,11 +913,11 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
               s[c + 2] = f2_lo(b);
               s[c + 3] = f2_hi(b);
             } else {
-              const float4 m = *reinterpret_cast<const float4*>(&sm.less[c0 + c]);
-              s[c] = fmaf(s[c], sl2, m.x);
-              s[c + 1] = fmaf(s[c + 1], sl2, m.y);
-              s[c + 2] = fmaf(s[c + 2], sl2, m.z);
-              s[c + 3] = fmaf(s[c + 3], sl2, m.w);
+              const float4 m = *reinterpret_cast<const float4*>(&sm.m[c0 + c]);
+              s[c] = fmaf(s[c], sl2, -m.x);
+              s[c + 1] = fmaf(s[c + 1], sl2, -m.y);
+              s[c + 2] = fmaf(s[c + 2], sl2, -m.z);
+              s[c + 3] = fmaf(s[c + 3], sl2, -m.w);
             }
           }
         };
@@ -941,11 +941,11 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
           barrier_group();
           if (quad == 0 && lane < kSoftCols) {
             const int c = c0 + lane;
-            const float old = -sm.less[c];
+            const float old = kTwos ? -sm.m[c] : sm.m[c];
             float m = fmaxf(fmaxf(sm.red[0][c], sm.red[1][c]), fmaxf(sm.red[2][c], sm.red[3][c]));
             m = fmaxf(old, m);
             sm.fac[c] = fast_exp2(old - m);
-            sm.less[c] = -m;
+            sm.m[c] = kTwos ? -m : m;
           }
           barrier_group();
 #pragma unroll
@@ -1045,7 +1045,7 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
     const int64_t piece = 2 * static_cast<int64_t>(blockIdx.x) + (w.t0 == 0 ? 1 : 0);
     if (quad == 0 && lane < kSoftCols) {
       const int c = c0 + lane;
-      const float z = (sm.red[0][c] + sm.red[1][c]) + (sm.red[2][c] + sm.red[3][c]), m = -sm.less[c];
+      const float z = (sm.red[0][c] + sm.red[1][c]) + (sm.red[2][c] + sm.red[3][c]), m = kTwos ? -sm.m[c] : sm.m[c];
       if (!whole) {
         float* ml = p.part_ml + piece * 2 * kAttnRows;
         ml[c] = m;
@@ -1058,7 +1058,7 @@ __device__ void tile_softmax(const AttnParams& p, TileSmall& sm, unsigned char* 
         sm.fac[c] = mx == -INFINITY ? 0.f : old / den;
         if (p.lse != nullptr && sm.lse_at[par][c] >= 0) p.lse[sm.lse_at[par][c]] = z == 0.f ? sink_e : (mx + log2f(den)) * kLn2;
       }
-      sm.less[c] = -kNoMax;  // for the next unit
+      sm.m[c] = kTwos ? -kNoMax : kNoMax;  // for the next unit
     }
     if (more) q_copied();
     barrier_group();
