@@ -254,8 +254,9 @@ __device__ __forceinline__ void no_row(const StepParams& p, int64_t o) {  // beh
   if (p.slots != nullptr) p.slots[o] = -1;
 }
 
-// The maximum of a thread's positions (times log2 e), the sum of their weights against it, and their weighted sum,
-// of each of its columns.
+// The maximum of a thread's positions, the sum of their weights against it, and their weighted sum, of each of its
+// columns. A score less the maximum is what log2 e multiplies: multiplied before, one beyond 2.3e38 (a type's lowest
+// value as a mask, wherever a window has no other) would be infinite.
 template <int VEC>
 struct Weighed {
   static constexpr int kPairs = VEC == 4 ? 2 : 1;
@@ -268,7 +269,7 @@ struct Weighed {
     for (int i = 0; i < kPairs; ++i) {
       uint64_t x[UW];
 #pragma unroll
-      for (int u = 0; u < UW; ++u) x[u] = f2_fma(score[u].pair(i), log2e, embedding[u][i]);
+      for (int u = 0; u < UW; ++u) x[u] = f2_add(score[u].pair(i), embedding[u][i]);
       float lo = f2_lo(x[0]), hi = f2_hi(x[0]);
 #pragma unroll
       for (int u = 1; u + 1 < UW; u += 2) {
@@ -286,7 +287,7 @@ struct Weighed {
       z[i] = a[i] = 0;
 #pragma unroll
       for (int u = 0; u < UW; ++u) {
-        const uint64_t t = f2_add(x[u], to), f = f2_pack(fast_exp2(f2_lo(t)), fast_exp2(f2_hi(t)));
+        const uint64_t t = f2_mul(f2_add(x[u], to), log2e), f = f2_pack(fast_exp2(f2_lo(t)), fast_exp2(f2_hi(t)));
         z[i] = f2_add(z[i], f);
         a[i] = f2_fma(f, kv[u].pair(i), a[i]);
       }
@@ -338,7 +339,7 @@ struct Join {
     const float base = m == -INFINITY ? 0.f : m;
 #pragma unroll 4
     for (int q = 0; q < many; ++q) {
-      const float f = fast_exp2(at[q * wide] - base);
+      const float f = fast_exp2((at[q * wide] - base) * kLog2e);
       z = fmaf(at[step + q * wide], f, z);
       a = fmaf(at[2 * step + q * wide], f, a);
     }
@@ -397,7 +398,7 @@ __global__ void __launch_bounds__(kStepThreads, 2) step_kernel(const __grid_cons
     if (mine && w < p.W) there |= 1u << u;
     if (!prev) own |= 1u << u;
   }
-  // the embedding at these positions, times log2 e, once for all rows; 0 behind the window
+  // the embedding at these positions, once for all rows; 0 behind the window
   uint64_t embedding[UW][PAIRS];
   bool embedded = false;
   auto embed = [&]() {
@@ -414,7 +415,7 @@ __global__ void __launch_bounds__(kStepThreads, 2) step_kernel(const __grid_cons
         else e[0] = __ldg(from);
       }
 #pragma unroll
-      for (int i = 0; i < PAIRS; ++i) embedding[u][i] = f2_pack(e[2 * i] * kLog2e, e[2 * i + 1] * kLog2e);
+      for (int i = 0; i < PAIRS; ++i) embedding[u][i] = f2_pack(e[2 * i], e[2 * i + 1]);
     }
   };
 
@@ -738,7 +739,7 @@ __global__ void __launch_bounds__(kFewThreads, SPLIT ? 2 : 1) step_few_kernel(co
         else e[0] = __ldg(from);
       }
 #pragma unroll
-      for (int i = 0; i < Weighed<VEC>::kPairs; ++i) embedding[u][i] = f2_pack(e[2 * i] * kLog2e, e[2 * i + 1] * kLog2e);
+      for (int i = 0; i < Weighed<VEC>::kPairs; ++i) embedding[u][i] = f2_pack(e[2 * i], e[2 * i + 1]);
     }
   };
   if (next < s1) embed();

@@ -223,7 +223,8 @@ csa_status_t csa_compressor_map_blocks(const int32_t* cu_seqlens, int32_t S, int
  *   cu_seqlens[s+1]): token cu_seqlens[s] + i stands at position p = first[s] + i. Its block b
  *   covers the positions [b ratio, (b + 1) ratio), and an entry is made of every block whose last
  *   token is among the new ones, with the window, the softmax and the rounding of
- *   csa_compressor_fwd (a window whose scores are all -inf gives NaN). out's rows are these
+ *   csa_compressor_fwd (a window whose scores are all -inf gives NaN; finite ones count as they are up to
+ *   their type's limits, where csa_compressor_fwd takes those beyond 2.3e38 for infinite). out's rows are these
  *   entries, sequence by sequence, blocks in order:
  *     sum over s of floor((first[s] + n_s) / ratio) - floor(first[s] / ratio), n_s new tokens.
  *   What a later window still reads lies in a state, kv and score bf16 [ratio * coff, coff * d] each;

@@ -309,6 +309,50 @@ def test_values_out_of_the_ordinary(cuda_lib, ratio, coff, d):
         assert ((out[b].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 1e-5).all()  # (fp32: about 50 U of values of 4 at most)
 
 
+@pytest.mark.parametrize("ratio,coff,d", [(4, 1, 8), (4, 1, 7), (32, 1, 8), (2, 2, 8), (16, 2, 4), (4, 2, 64)])
+@pytest.mark.parametrize("S", [1, 40])
+def test_scores_at_their_types_limits(cuda_lib, ratio, coff, d, S):
+    """Windows whose scores are all the lowest value weigh their positions alike, the largest value takes the weight
+    from all others, and beside the lowest one -inf still weighs nothing: by many tokens and by few a sequence."""
+    g = torch.Generator().manual_seed(13)
+    most = float(torch.finfo(torch.bfloat16).max)
+    n = 5 * ratio
+    kv, score = (torch.randn(S * n, coff * d, generator=g).to(torch.bfloat16).view(S, n, coff * d) for _ in range(2))
+    score[:, :2 * ratio] = -most
+    score[:, ratio] = -math.inf
+    score[:, 3 * ratio - 1] = most
+    score[:, 4 * ratio:] = most
+    if S == 1:
+        calls = [list(range(n))]
+    else:  # two tokens a call
+        calls = [list(range(a, min(a + 2, n))) for a in range(0, n, 2)]
+    W, C = coff * ratio, coff * d
+    states = [torch.zeros(S, W, C, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    own = torch.arange(S, **I32)
+    got = [[] for _ in range(S)]
+    for at in calls:
+        rows = (at[-1] + 1) // ratio - at[0] // ratio
+        out, err = torch.zeros(S * rows, d, dtype=torch.bfloat16, device="cuda"), torch.zeros(1, **I32)
+        cu = torch.arange(S + 1, **I32) * len(at)
+        cuda_lib.csa_compressor_step(kv[:, at].contiguous().cuda(), score[:, at].contiguous().cuda(), torch.zeros(ratio, C, device="cuda"), cu, S,
+                                     ratio, coff, d, S * len(at), torch.full((S,), at[0], **I32), own, own, S, *states, out, S * rows, dev_error=err)
+        torch.cuda.synchronize()
+        assert int(err) == 0
+        for s in range(S):
+            got[s] += list(out.view(S, rows, d)[s].double().cpu())
+    for s in range(S):
+        assert len(got[s]) == 5
+        for b in range(5):
+            half = [(p, 0 if coff == 1 or p < b * ratio else d) for p in range(max(0, b - coff + 1) * ratio, (b + 1) * ratio)]
+            x, k = (torch.stack([t[s, p, c:c + d].double() for p, c in half]) for t in (score, kv))
+            w = torch.softmax(x, 0)
+            ref = (w * k).sum(0)
+            # (as window_entry's, but that the embedding is 0: a difference from the maximum is rounded, not its terms)
+            away = torch.where(w > 0, x.amax(0) - x, 0.0)
+            mass = R.U * ((2 * (10 + min(32, len(x))) + 16) * (w * k.abs()).sum(0) + 8 * (w * (k - ref).abs() * (away + 1)).sum(0))
+            assert ((got[s][b] - ref).abs() <= 2.0 ** -8 * ref.abs() + 2 * mass).all(), (s, b)
+
+
 def test_graph_of_steps(cuda_lib):
     """A captured step that moves its own lengths on, replayed, against the calls one by one."""
     ratio, coff, d, S = 4, 2, 64, 3
