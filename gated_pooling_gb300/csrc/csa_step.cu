@@ -57,6 +57,7 @@ struct StepParams {
   int stages;  // turns under way
   // the first CTAs of a slice see to the sequences; those behind first_row_cta to the other blocks' rows
   int seq_ctas, first_row_cta;
+  unsigned checker;  // the CTA of a slice (the first one's works) that looks for states that sequences meet in
 };
 
 // VEC consecutive bf16 values (4: 8 bytes, aligned; 1: any).
@@ -162,6 +163,49 @@ __device__ __forceinline__ int step_wrong(const StepParams& p, int a, int b, int
   const int n = b - a;
   const bool live = f % p.ratio != 0 || (p.coff == 2 && f >= p.ratio);  // the state holds something
   return f < 0 || f > kStepEnd - n || from >= p.num_states || to >= p.num_states || (from < 0 && live && (n > 0 || to >= 0)) ? 2 : 0;
+}
+
+// The states that a sequence writes (x) and reads (y), -1: none. What it goes on from in place it only writes.
+__device__ __forceinline__ int2 states_of(const StepParams& p, int n, int f, int from, int to) {
+  const bool live = f % p.ratio != 0 || (p.coff == 2 && f >= p.ratio), moved = to != from && live;
+  return make_int2(to >= 0 && (n > 0 || moved) ? to : -1, from >= 0 && moved && (n > 0 || to >= 0) ? from : -1);
+}
+
+// Reports a state that one sequence writes and another one writes or reads: CTAs that do not wait for one another would
+// do so in any order. One CTA looks at all sequences, in a set of the written states (table: [slots] in shared
+// memory, twice as many as sequences at least), beside the others' work: marks made by all CTAs while they count rows
+// took 0.6 us of a single step's 4.9. All its threads; nothing is reported where the call's numbers are refused.
+__device__ __noinline__ void check_states(const StepParams& p, int* table, int slots) {
+  for (int i = threadIdx.x; i < slots; i += blockDim.x) table[i] = -1;
+  __syncthreads();
+  auto place = [&](int state) { return static_cast<int>(__umulhi(static_cast<unsigned>(state) * 0x9E3779B1u, static_cast<unsigned>(slots))); };
+  bool wrong = false, meet = false;
+  for (int s = threadIdx.x; s < p.S; s += blockDim.x) {
+    const int a = __ldg(p.cu + s), b = __ldg(p.cu + s + 1), f = __ldg(p.first + s), from = __ldg(p.source + s), to = __ldg(p.target + s);
+    if (step_wrong(p, a, b, f, from, to) != 0) {
+      wrong = true;
+      continue;
+    }
+    const int w = states_of(p, b - a, f, from, to).x;
+    for (int at = w < 0 ? -1 : place(w); at >= 0; at = at + 1 < slots ? at + 1 : 0) {
+      const int old = atomicCAS(table + at, -1, w);
+      if (old == -1) break;
+      if (old == w) {
+        meet = true;
+        break;
+      }
+    }
+  }
+  if (__syncthreads_or(wrong)) return;
+  for (int s = threadIdx.x; s < p.S; s += blockDim.x) {
+    const int r = states_of(p, __ldg(p.cu + s + 1) - __ldg(p.cu + s), __ldg(p.first + s), __ldg(p.source + s), __ldg(p.target + s)).y;
+    for (int at = r < 0 ? -1 : place(r); at >= 0 && table[at] != -1; at = at + 1 < slots ? at + 1 : 0)
+      if (table[at] == r) {
+        meet = true;
+        break;
+      }
+  }
+  if (meet && p.dev_error != nullptr) *reinterpret_cast<volatile int32_t*>(p.dev_error) = CSA_DEVERR_STATE;
 }
 
 // Asks L2 for the tokens of about the first `rows` rows of this CTA, by its place among those that see to rows: which
@@ -375,6 +419,11 @@ __global__ void __launch_bounds__(kStepThreads, 2) step_kernel(const __grid_cons
   __shared__ int2 warp_sums[32];
   float* const s_part = reinterpret_cast<float*>(s_raw + p.stages * step_stage_bytes(VEC));  // [2][RS][3][PG][CL * VEC]
   int2* const s_prefix = reinterpret_cast<int2*>(s_raw + p.stages * step_stage_bytes(VEC) + step_part_bytes(VEC, SPLIT));  // [S + 1]
+  if (blockIdx.x == static_cast<unsigned>(p.R)) {  // a CTA of its own
+    pdl_wait();
+    if (blockIdx.y == 0) check_states(p, reinterpret_cast<int*>(s_prefix), 2 * p.S);
+    return;
+  }
   if (!build_step_prefix(p, s_prefix, warp_sums, p.stages * p.RS * K)) return;
   const int g = blockIdx.x, tid = threadIdx.x, per = p.CL * p.PG;
   const int rs = tid / per, pg = tid % per / p.CL, cl = tid % p.CL;
@@ -557,6 +606,11 @@ __global__ void __launch_bounds__(kStepThreads, 2) step_kernel(const __grid_cons
   }
 
   const int worker = g - p.first_row_cta, workers = p.R - p.first_row_cta;
+  auto check_at_end = [&]() {
+    if (blockIdx.x != p.checker || blockIdx.y != 0) return;
+    __syncthreads();
+    check_states(p, reinterpret_cast<int*>(s_prefix), 2 * p.S);
+  };
   auto describe = [&]() {
     if (blockIdx.y == 0 && g >= p.first_row_cta && (p.positions != nullptr || p.slots != nullptr))
       for (int64_t o = static_cast<int64_t>(tid) * workers + worker; o < p.out_rows; o += static_cast<int64_t>(workers) * kStepThreads) {
@@ -579,6 +633,7 @@ __global__ void __launch_bounds__(kStepThreads, 2) step_kernel(const __grid_cons
   const int i1 = worker < 0 ? 0 : static_cast<int>(static_cast<int64_t>(worker + 1) * inner / workers);
   if (i0 >= i1) {
     describe();
+    check_at_end();
     return;
   }
   // a walk over them: the sequence of the row asked for last, where its rows end,
@@ -656,6 +711,7 @@ __global__ void __launch_bounds__(kStepThreads, 2) step_kernel(const __grid_cons
     stage_commit();
     if (++b == static_cast<unsigned>(p.stages)) b = 0;
   }
+  check_at_end();
 }
 
 // Calls of few tokens a sequence: a CTA per p.RS sequences and column slice, whose blocks it works out one after
@@ -676,6 +732,10 @@ __global__ void __launch_bounds__(kFewThreads, SPLIT ? 2 : 1) step_few_kernel(co
   const int chunk = blockIdx.y * p.CL + cl, c0 = chunk * VEC;
   const bool two = p.coff == 2, mine = tid < per && chunk < p.chunks;
   pdl_wait();
+  if (blockIdx.x == p.checker) {
+    if (blockIdx.y == 0) check_states(p, reinterpret_cast<int*>(s_rows), 2 * kFewSeqs);
+    return;
+  }
   // the whole call's lengths: what is wrong with them, the rows before these sequences and (from bit 13 on: at most 8
   // tokens a sequence come here) of all, and the shared-out ones
   static_assert(8 * kFewSeqs < 1 << 13);
@@ -852,7 +912,7 @@ __global__ void __launch_bounds__(kFewThreads, SPLIT ? 2 : 1) step_few_kernel(co
       }
     }
     __syncthreads();
-    for (int i = blockIdx.x; i < shared; i += gridDim.x) {
+    for (int i = blockIdx.x; i < shared; i += p.R) {
       int s = 0, h = p.S;  // shared-out rows before s <= i < those before h, the last such s
       while (h - s > 1) {
         const int mid = (s + h) / 2;
@@ -873,7 +933,7 @@ __global__ void __launch_bounds__(kFewThreads, SPLIT ? 2 : 1) step_few_kernel(co
     if (back == 0 && p.entries != nullptr) p.entries[s] = max(0, hi - (p.base != nullptr ? __ldg(p.base + s) : 0));
     row += hi - lo;
   }
-  for (int64_t o = all + static_cast<int64_t>(blockIdx.x) * blockDim.x + tid; o < p.out_rows; o += static_cast<int64_t>(gridDim.x) * blockDim.x)
+  for (int64_t o = all + static_cast<int64_t>(blockIdx.x) * blockDim.x + tid; o < p.out_rows; o += static_cast<int64_t>(p.R) * blockDim.x)
     no_row(p, o);
 }
 
@@ -979,7 +1039,9 @@ extern "C" csa_status_t csa_compressor_step(
     p.RS = 1;
     while (2 * p.RS <= p.PG && static_cast<int64_t>(S) * slices > 2 * static_cast<int64_t>(sms) * p.RS) p.RS *= 2;
     const int block = (p.CL * p.PG + 31) / 32 * 32;
-    return launch_pdl(k, dim3((S + p.RS - 1) / p.RS, slices), dim3(block < 64 ? 64 : block), 0, cs, args) == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
+    p.R = (S + p.RS - 1) / p.RS;
+    p.checker = S > 1 ? p.R : UINT_MAX;
+    return launch_pdl(k, dim3(p.R + (S > 1), slices), dim3(block < 64 ? 64 : block), 0, cs, args) == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
   }
   // Three turns under way, or as many as leave room for two CTAs an SM beside the sequences' numbers; a CTA an SM where
   // not one does (at most 155 KB of numbers and parts: one turn fits always).
@@ -999,5 +1061,13 @@ extern "C" csa_status_t csa_compressor_step(
   // tokens') are spread over all.
   p.seq_ctas = static_cast<int>(by_seqs < p.R ? (by_seqs > 0 ? by_seqs : 1) : p.R);
   p.first_row_cta = 4 * p.seq_ctas <= p.R ? p.seq_ctas : 0;
-  return launch_pdl(k, dim3(p.R, slices), dim3(kStepThreads), smem, cs, args) == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
+  // Sequences' own CTAs are done before those of rows, so the first one looks for states that sequences meet in; otherwise
+  // an additional CTA does, which has the place of one of 64 and more (or else the first one at its end).
+  const bool added = S > 1 && p.first_row_cta == 0 && (p.R < room || p.R >= 64);
+  if (added && p.R == room) {
+    --p.R;
+    p.seq_ctas = p.seq_ctas < p.R ? p.seq_ctas : p.R;
+  }
+  p.checker = S < 2 ? UINT_MAX : added ? p.R : 0;
+  return launch_pdl(k, dim3(p.R + added, slices), dim3(kStepThreads), smem, cs, args) == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
 }

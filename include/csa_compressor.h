@@ -75,9 +75,10 @@ typedef enum {
 #define CSA_DEVERR_PAGE 7       /* cache attention: a page number a sequence needs is outside
                                    [0, num_pages); its entries are not read. Step: an entry's page is
                                    behind the table's end or negative; its slot is -1 */
-#define CSA_DEVERR_STATE 8      /* step: first[s] negative or past 2^31 with the new tokens, source[s] or
-                                   target[s] >= num_states, or source[s] < 0 where tokens of earlier
-                                   calls are needed */
+#define CSA_DEVERR_STATE 8      /* step: first[s] negative or past 2^31 - 4097 with the new tokens, source[s] or
+                                   target[s] >= num_states, source[s] < 0 where tokens of earlier
+                                   calls are needed, or a state that one sequence writes and another one
+                                   writes or reads */
 #define CSA_DEVERR_PREFIX 9     /* prefix attention: prefix_seqs does not run from 0 to S without decreasing, or
                                    prefix_entries[g] < 0 or > max_prefix_pages * page_size */
 
@@ -236,7 +237,8 @@ csa_status_t csa_compressor_map_blocks(const int32_t* cu_seqlens, int32_t S, int
  *     coff=2: the columns < d of p >= (B - 1) ratio, and the columns >= d of p >= B ratio;
  *   all other elements stay as they were. Several sequences may go on from one state (samples of one
  *   prompt); a state that one sequence leaves its tokens in belongs to that sequence alone: no other
- *   sequence of the call may name it. Negative: source[s] where nothing of earlier calls is needed
+ *   sequence of the call may go on from it or leave tokens in it (a sequence that itself goes on while others fork
+ *   from it takes a target of its own). Negative: source[s] where nothing of earlier calls is needed
  *   (first[s] = 0; at coff=1 a multiple of ratio, at coff=2 also any first[s] < ratio that is one), target[s]
  *   where nothing is to be kept. A sequence without new tokens has its state copied if source and target
  *   differ.
@@ -259,7 +261,8 @@ csa_status_t csa_compressor_map_blocks(const int32_t* cu_seqlens, int32_t S, int
  *               call, max(0, B - base[s])
  * positions and slots are what csa_cache_append takes, entries what the attention takes, so a step needs
  * no number on the host. Outputs overlap no input but for the states. Bad lengths or states (CSA_DEVERR_CU_SEQLENS,
- * CSA_DEVERR_STATE) skip all outputs. CSA_ERR_INVALID_VALUE and CSA_ERR_UNSUPPORTED as for
+ * CSA_DEVERR_STATE) skip all outputs, but for sequences that meet in a state, which is reported while the others' outputs
+ * are written; what such sequences write is unspecified. CSA_ERR_INVALID_VALUE and CSA_ERR_UNSUPPORTED as for
  * csa_compressor_fwd (any d and ratio up to CSA_MAX_WINDOW / coff; no smaller limit for unaligned
  * tensors), and num_states above 2^31 - 1. The vector kernels run when d is a multiple of 4, ape 16-byte and kv,
  * score, out and the states 8-byte aligned; anything else takes a column a thread. One kernel is enqueued. */

@@ -353,6 +353,66 @@ def test_scores_at_their_types_limits(cuda_lib, ratio, coff, d, S):
             assert ((got[s][b] - ref).abs() <= 2.0 ** -8 * ref.abs() + 2 * mass).all(), (s, b)
 
 
+@pytest.mark.parametrize("S", [4, 700])
+@pytest.mark.parametrize("ratio,coff", [(2, 1), (2, 2)])
+def test_states_that_sequences_meet_in(cuda_lib, S, ratio, coff):
+    """A state that one sequence writes and another one writes or reads is reported, and all other sequences are as ever;
+    what is only read, or named by a sequence that neither reads nor writes, may be named by any."""
+    W = coff * ratio
+
+    def call(change, first=W + 1, n=1):
+        source, target, firsts, lens = [2 * s for s in range(S)], [2 * s + 1 for s in range(S)], [first] * S, [n] * S
+        for s, how in change.items():
+            source[s], target[s], firsts[s], lens[s] = (x if y is None else y for x, y in zip((source[s], target[s], firsts[s], lens[s]), how))
+        cu = [0]
+        for x in lens:
+            cu.append(cu[-1] + x)
+        err, out, st, pos, *_ = raw(cuda_lib, ratio, coff, 8, cu, firsts, source, target, 2 * S, rows=S * (1 + n), capacity=cu[-1] + 1)
+        return err, out, pos
+    a, b = 1, S - 1
+    fine, out, pos = call({})
+    assert fine == 0
+    for change in ({a: (2 * a, 2 * a, None, None), b: (2 * a, None, None, None)},         # goes on in place, and another forks from it
+                   {a: (2 * a, 2 * b + 1, None, None)},                                   # two targets
+                   {a: (2 * b + 1, None, None, None)},                                    # one's target is another's source
+                   {a: (2 * b + 1, -1, None, None)},                                      # read alone
+                   {a: (2 * b + 1, None, None, 0)},                                       # copied, without a token
+                   {a: (2 * a, 5, None, None), b: (2 * b, 5, 0, 1), 2: (None, -1, None, None)}):  # one that begins, in another's
+        err, got, at = call(change)
+        assert err == 8, change
+        if S > 4 and len(change) < 3 and all(x[3] is None for x in change.values()):
+            rest = torch.tensor([s not in change and s != b for s in range(S)])
+            assert torch.equal(got[:S][rest], out[:S][rest]) and at[:S] == pos[:S]
+    for change in ({a: (0, None, None, None), b: (0, None, None, None), 2: (0, -1, None, None)},  # forks
+                   {a: (7, 7, None, 0), b: (7, 7, None, 0), 2: (1, 1, None, 0)},                  # idle, whatever they name
+                   {a: (2 * b + 1, None, 0, None)},                                               # nothing is read at a beginning
+                   {a: (2 * b + 1, -1, None, 0)},                                                 # nor without a token or a target
+                   {a: (-1, -1, 0, None), b: (-1, -1, 0, None)}):
+        assert call(change)[0] == 0, change
+
+
+@pytest.mark.parametrize("S", [2, 5, 16384])
+def test_far_apart_states_are_not_taken_for_one(cuda_lib, S):
+    """As many states as share a place in the lists that are looked at for states that meet; and a pair that does meet
+    among them."""
+    step = 2048 * S if S < 100 else 1024
+    states, d = (S + 1) * step, 1
+    kv, score = (torch.ones(S, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    st = [torch.zeros(states, 1, d, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    err, out = torch.zeros(1, **I32), torch.zeros(S, d, dtype=torch.bfloat16, device="cuda")
+    own = torch.arange(S, **I32) * step
+
+    def call(target):
+        cuda_lib.csa_compressor_step(kv, score, torch.zeros(1, d, device="cuda"), torch.arange(S + 1, **I32), S, 1, 1, d, S,
+                                     torch.arange(S, **I32), own, target, states, *st, out, S, dev_error=err)
+        torch.cuda.synchronize()
+        return int(err)
+    assert call(own) == 0 and (out == 1).all()
+    other = own.clone()
+    other[S - 1] = own[S // 3]
+    assert call(other) == 8
+
+
 def test_graph_of_steps(cuda_lib):
     """A captured step that moves its own lengths on, replayed, against the calls one by one."""
     ratio, coff, d, S = 4, 2, 64, 3
