@@ -725,7 +725,7 @@ template <int VEC, int UW, bool SPLIT>
 __global__ void __launch_bounds__(kFewThreads, SPLIT ? 2 : 1) step_few_kernel(const __grid_constant__ StepParams p) {
   using P = Piece<VEC>;
   __shared__ __align__(16) float s_part[SPLIT ? 3 * kFewThreads * VEC : 4];
-  __shared__ int2 s_sums[kFewThreads / 32];
+  __shared__ uint2 s_sums[kFewThreads / 32];
   __shared__ int2 s_rows[kFewSeqs];  // where blocks are shared out: rows before each sequence, and of those shared out
   const int tid = threadIdx.x, per = p.CL * p.PG, s0 = blockIdx.x * p.RS, s1 = min(p.S, s0 + p.RS);
   const int pg = tid / p.CL, cl = tid - pg * p.CL;
@@ -736,18 +736,20 @@ __global__ void __launch_bounds__(kFewThreads, SPLIT ? 2 : 1) step_few_kernel(co
     if (blockIdx.y == 0) check_states(p, reinterpret_cast<int*>(s_rows), 2 * kFewSeqs);
     return;
   }
-  // the whole call's lengths: what is wrong with them, the rows before these sequences and (from bit 13 on: at most 8
-  // tokens a sequence come here) of all, and the shared-out ones
+  // the whole call's lengths: what is wrong with them, the rows before these sequences and (from bit 13 on) of all, and
+  // the shared-out ones. (All entries are at most `capacity`, of which calls with up to 8 a sequence come here, whichever
+  // sequences have them; offsets that are refused may add up to anything, without a sign so that they may.)
   static_assert(8 * kFewSeqs < 1 << 13);
-  int bad = 0, rows = 0, shared = 0;
+  int bad = 0;
+  unsigned rows = 0, shared = 0;
   for (int i = tid; i < p.S; i += blockDim.x) {
     const int a = __ldg(p.cu + i), b = __ldg(p.cu + i + 1), f = __ldg(p.first + i);
     const int from = __ldg(p.source + i), to = __ldg(p.target + i), why = step_wrong(p, a, b, f, from, to);
     bad |= why;
     if (why == 0) {
-      const int made = (f + (b - a)) / p.ratio - f / p.ratio;
-      rows += (made << 13) + (i < s0 ? made : 0);
-      shared += max(0, made - kFewBlocks);
+      const unsigned made = (f + (b - a)) / p.ratio - f / p.ratio;
+      rows += (made << 13) + (i < s0 ? made : 0u);
+      shared += made > kFewBlocks ? made - kFewBlocks : 0u;
     }
   }
   // (numbers of one sequence, of which nothing is read until they are known to be right)
@@ -831,7 +833,7 @@ __global__ void __launch_bounds__(kFewThreads, SPLIT ? 2 : 1) step_few_kernel(co
 
   rows = __reduce_add_sync(0xFFFFFFFFu, rows);
   shared = __reduce_add_sync(0xFFFFFFFFu, shared);
-  if ((tid & 31) == 0) s_sums[tid >> 5] = make_int2(rows, shared);
+  if ((tid & 31) == 0) s_sums[tid >> 5] = make_uint2(rows, shared);
   const bool wrong = __syncthreads_or(bad) != 0;
   rows = shared = 0;
   for (int w = 0; w < static_cast<int>(blockDim.x) / 32; ++w) {
@@ -912,7 +914,7 @@ __global__ void __launch_bounds__(kFewThreads, SPLIT ? 2 : 1) step_few_kernel(co
       }
     }
     __syncthreads();
-    for (int i = blockIdx.x; i < shared; i += p.R) {
+    for (int i = blockIdx.x; i < static_cast<int>(shared); i += p.R) {
       int s = 0, h = p.S;  // shared-out rows before s <= i < those before h, the last such s
       while (h - s > 1) {
         const int mid = (s + h) / 2;

@@ -206,6 +206,14 @@ def test_device_refusals_leave_all_as_it_was(cuda_lib, code, how):
     assert set(pos) <= {77} and set(entries) == {77}
 
 
+@pytest.mark.parametrize("S", [2, 511, 512, 600])
+def test_offsets_that_overlap_again_and_again(cuda_lib, S):
+    """Each second sequence has all tokens of the call: refused, however many entries that makes."""
+    cu = [8 * S * (s % 2) for s in range(S + 1)]
+    err, out, st, pos, slots, entries = raw(cuda_lib, 1, 1, 4, cu, [0] * S, [-1] * S, [-1] * S, rows=8 * S, capacity=8 * S)
+    assert err == 1 and (out == 7.0).all() and all((t == 5.0).all() for t in st) and set(pos) <= {77} and set(entries) == {77}
+
+
 def test_calls_that_need_no_state(cuda_lib):
     assert raw(cuda_lib, first=(4,), source=(-1,))[0] == 0  # coff 1 at a block's beginning
     err, out, st, *_ = raw(cuda_lib, cu=(0, 3), source=(-1,), target=(-1,), states=0)
