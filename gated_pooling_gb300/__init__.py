@@ -3,7 +3,7 @@
 A thin binding of the C ABI in ``include/csa_compressor.h``: the functions
 below have the C names and arguments, and only marshal them (tensor -> device
 pointer, stream -> cudaStream_t), those that enqueue work through a small module of
-their own, the others through ctypes. Every step of the pooling runs in the library's
+their own where it is built for this Python, else through ctypes as the others. Every step of the pooling runs in the library's
 CUDA kernels. There is no fallback: if the library is missing, loading raises.
 
 Tensors are torch CUDA tensors (bf16 for kv/score/dout/out/dkv/dscore and the KPool
@@ -14,6 +14,8 @@ from __future__ import annotations
 
 import ctypes
 import importlib.util
+import math
+import operator
 import os
 from typing import Optional
 
@@ -123,25 +125,57 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     return lib
 
 
-def _ptr(x) -> Optional[int]:
-    if x is None or isinstance(x, int):
-        return x
-    return x.data_ptr()
+def _int(x, size: int, signed: bool) -> int:
+    v = operator.index(x)
+    bits = 8 * size - (1 if signed else 0)
+    if not (-(1 << bits) if signed else 0) <= v < 1 << bits:
+        raise OverflowError(f"{v} is out of an argument's range")
+    return v
+
+
+# How an argument of a ctypes type is taken, as the module does it: pointers are None, addresses or what has a
+# data_ptr(), numbers have to fit.
+_TAKE = {
+    ctypes.c_void_p: lambda x: None if x is None else _int(x if isinstance(x, int) else x.data_ptr(), 8, False),
+    ctypes.c_int32: lambda x: _int(x, 4, True),
+    ctypes.c_int64: lambda x: _int(x, 8, True),
+    ctypes.c_size_t: lambda x: _int(x, 8, False),
+    ctypes.c_float: lambda x: math.ldexp(x, 0),
+}
+
+
+class _CtypesCalls:
+    """The functions of the module (csrc/csa_call.cpp) through ctypes: the same arguments, errors and results, a few
+    microseconds later."""
+
+    def __getattr__(self, name):
+        f = getattr(load(), name)
+        take = [_TAKE[t] for t in f.argtypes]
+
+        def call(*args):
+            if len(args) != len(take):
+                raise TypeError(f"{len(args)} arguments instead of {len(take)}")
+            return f(*[g(x) for g, x in zip(take, args)])
+        setattr(self, name, call)
+        return call
 
 
 _calls = None
 
 
 def _load_calls():
-    """The module that the functions below call the library through (csrc/csa_call.cpp); it and ctypes
-    share one library."""
+    """What the functions below call the library through: the module where there is one for this Python (it and ctypes
+    share one library), else ctypes."""
     global _calls
     load()
-    spec = importlib.util.spec_from_file_location("_csa_call", _build.CALL)
-    module = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(module)
-    _calls = module
-    return module
+    if os.path.exists(_build.CALL):
+        spec = importlib.util.spec_from_file_location("_csa_call", _build.CALL)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _calls = module
+    else:
+        _calls = _CtypesCalls()
+    return _calls
 
 
 _raw_stream = None

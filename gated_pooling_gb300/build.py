@@ -1,5 +1,6 @@
-"""Builds the CUDA library ``lib/libcsa_compressor.so`` in-tree with nvcc for sm_103a, and the Python
-module ``lib/_csa_call`` through which the package calls it.
+"""Builds the CUDA library ``lib/libcsa_compressor.so`` in-tree with nvcc for sm_103a, and, where there is
+g++ and this Python has its headers, the module ``lib/_csa_call`` through which the package calls it sooner than
+through ctypes. The library needs nvcc alone and serves any Python; the module is this Python's.
 
 Each translation unit compiles in its own nvcc process, in parallel, then one link.
 ptxas resource usage (registers, spills, shared memory) is kept in ``lib/ptxas.log``.
@@ -36,64 +37,67 @@ def nvcc() -> str:
     return path
 
 
-def cxx() -> str:
-    path = shutil.which("g++")
-    if path is None:
-        raise RuntimeError("g++ not found: it is required to build the package's calls")
-    return path
+def can_build_call() -> bool:
+    """Whether the module can be built for this Python."""
+    return shutil.which("g++") is not None and os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h"))
 
 
-def _inputs() -> List[str]:
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    return files + [os.path.join(INCLUDE, "csa_compressor.h"), os.path.abspath(__file__)]
+def _newer(out: str, inputs: List[str]) -> bool:
+    return os.path.exists(out) and all(os.path.getmtime(f) <= os.path.getmtime(out) for f in inputs)
+
+
+def library_up_to_date() -> bool:
+    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f != CALL_SOURCE]
+    return _newer(LIB, files + [os.path.join(INCLUDE, "csa_compressor.h"), os.path.abspath(__file__)])
+
+
+def call_up_to_date() -> bool:
+    return _newer(CALL, [os.path.join(CSRC, CALL_SOURCE), os.path.join(INCLUDE, "csa_compressor.h"), os.path.abspath(__file__)])
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(CALL):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(CALL))
-    return all(os.path.getmtime(f) <= t for f in _inputs())
+    return library_up_to_date() and (call_up_to_date() or not can_build_call())
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and up_to_date():
-        return LIB
-    os.makedirs(LIBDIR, exist_ok=True)
+def _run(cmd: List[str], what: str) -> str:
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"{what}:\n{res.stdout}{res.stderr}")
+    return res.stdout + res.stderr
+
+
+def _build_library(verbose: bool) -> None:
     cc = nvcc()
 
     def compile_one(src: str):
         obj = os.path.join(LIBDIR, os.path.splitext(src)[0] + ".o")
-        if src == CALL_SOURCE:
-            cmd = [cxx(), "-O2", "-std=c++17", "-fPIC", "-I", sysconfig.get_paths()["include"], "-I", INCLUDE]
-        else:
-            cmd = [cc, *ARCH, *FLAGS]
-        cmd += ["-c", os.path.join(CSRC, src), "-o", obj]
-        res = subprocess.run(cmd, capture_output=True, text=True)
-        return src, obj, res
+        return obj, f"=== {src}\n" + _run([cc, *ARCH, *FLAGS, "-c", os.path.join(CSRC, src), "-o", obj], f"nvcc failed on {src}")
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        results = list(ex.map(compile_one, [*SOURCES, CALL_SOURCE]))
-    log = []
-    for src, _, res in results:
-        log.append(f"=== {src}\n{res.stdout}{res.stderr}")
-        if res.returncode != 0:
-            raise RuntimeError(f"the compiler failed on {src}:\n{res.stdout}{res.stderr}")
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+        results = list(ex.map(compile_one, SOURCES))
+    log = "\n".join(text for _, text in results)
     with open(os.path.join(LIBDIR, "ptxas.log"), "w") as fh:
-        fh.write("\n".join(log))
-    tmp = LIB + ".tmp"
-    cmd = [cc, *ARCH, "-shared", "-o", tmp, *[o for src, o, _ in results if src != CALL_SOURCE]]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError(f"link failed:\n{res.stdout}{res.stderr}")
-    os.replace(tmp, LIB)
-    tmp = CALL + ".tmp"
-    cmd = [cxx(), "-shared", "-o", tmp, results[-1][1], "-L", LIBDIR, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError(f"link failed:\n{res.stdout}{res.stderr}")
-    os.replace(tmp, CALL)
+        fh.write(log)
+    _run([cc, *ARCH, "-shared", "-o", LIB + ".tmp", *[obj for obj, _ in results]], "link failed")
+    os.replace(LIB + ".tmp", LIB)
     if verbose:
-        print("\n".join(log))
+        print(log)
+
+
+def _build_call() -> None:
+    _run([shutil.which("g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-I", sysconfig.get_paths()["include"], "-I", INCLUDE,
+          os.path.join(CSRC, CALL_SOURCE), "-o", CALL + ".tmp", "-L", LIBDIR, "-l:" + os.path.basename(LIB),
+          "-Wl,-rpath,$ORIGIN"], f"g++ failed on {CALL_SOURCE}")
+    os.replace(CALL + ".tmp", CALL)
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """Builds what is missing or stale; the module is left out where it cannot be built."""
+    os.makedirs(LIBDIR, exist_ok=True)
+    if force or not library_up_to_date():
+        _build_library(verbose)
+    if can_build_call() and (force or not call_up_to_date()):
+        _build_call()
     return LIB
 
 

@@ -3,7 +3,8 @@
 // itself or for an address, None for NULL; what comes back is the status.
 //
 // ctypes takes 0.1 us an argument and its Python side as much again for a pointer: 6 us for the 27 arguments of a
-// step, more than the GPU works on a small one. So it takes 1.
+// step, more than the GPU works on a small one. So it takes 1. Where this module is not built for a Python, the package
+// goes through ctypes.
 #include <Python.h>
 
 #include <cstdint>
