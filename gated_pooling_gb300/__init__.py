@@ -125,37 +125,36 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     return lib
 
 
-def _int(x, size: int, signed: bool) -> int:
-    v = operator.index(x)
-    bits = 8 * size - (1 if signed else 0)
-    if not (-(1 << bits) if signed else 0) <= v < 1 << bits:
-        raise OverflowError(f"{v} is out of an argument's range")
-    return v
-
-
-# How an argument of a ctypes type is taken, as the module does it: pointers are None, addresses or what has a
-# data_ptr(), numbers have to fit.
-_TAKE = {
-    ctypes.c_void_p: lambda x: None if x is None else _int(x if isinstance(x, int) else x.data_ptr(), 8, False),
-    ctypes.c_int32: lambda x: _int(x, 4, True),
-    ctypes.c_int64: lambda x: _int(x, 8, True),
-    ctypes.c_size_t: lambda x: _int(x, 8, False),
-    ctypes.c_float: lambda x: math.ldexp(x, 0),
-}
-
-
 class _CtypesCalls:
-    """The functions of the module (csrc/csa_call.cpp) through ctypes: the same arguments, errors and results, a few
-    microseconds later."""
+    """The functions of the module (csrc/csa_call.cpp) through ctypes: the same arguments, errors and results, some
+    microseconds later. Pointers are None, addresses or what has a data_ptr(); whole numbers have to fit."""
 
     def __getattr__(self, name):
         f = getattr(load(), name)
-        take = [_TAKE[t] for t in f.argtypes]
+        kinds = list(enumerate(f.argtypes))
+        pointers = [i for i, t in kinds if t is ctypes.c_void_p]
+        whole = [(i, -1 << (8 * ctypes.sizeof(t) - 1), (1 << (8 * ctypes.sizeof(t) - 1)) - 1) if t in (ctypes.c_int32, ctypes.c_int64)
+                 else (i, 0, (1 << 64) - 1) for i, t in kinds if t in (ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p)]
+        real = [i for i, t in kinds if t is ctypes.c_float]
 
         def call(*args):
-            if len(args) != len(take):
-                raise TypeError(f"{len(args)} arguments instead of {len(take)}")
-            return f(*[g(x) for g, x in zip(take, args)])
+            if len(args) != len(kinds):
+                raise TypeError(f"{len(args)} arguments instead of {len(kinds)}")
+            v = list(args)
+            for i in pointers:
+                if v[i] is not None and not isinstance(v[i], int):
+                    v[i] = v[i].data_ptr()
+            for i, low, high in whole:
+                x = v[i]
+                if type(x) is not int:
+                    if x is None and i in pointers:
+                        continue
+                    x = v[i] = operator.index(x)
+                if x < low or x > high:
+                    raise OverflowError(f"{x} is out of an argument's range")
+            for i in real:
+                v[i] = math.ldexp(v[i], 0)
+            return f(*v)
         setattr(self, name, call)
         return call
 
