@@ -785,13 +785,6 @@ csa_status_t run_attn(const AttnCall& c, csa_stream_t stream) {
   p.prefix_table = c.prefix_table;
   p.max_prefix_pages = c.max_prefix_pages;
   p.prefix_entries = c.prefix_entries;
-  if (d <= kTileMaxDim) {
-    if (workspace_bytes < lay_out(p, sms, chunked(p), nullptr)) return CSA_ERR_WORKSPACE;
-    lay_out(p, sms, chunked(p), static_cast<unsigned char*>(workspace));
-  } else {
-    p.head = static_cast<AttnHead*>(workspace);
-  }
-  if (!tile) p.units = nullptr;
   const int nc = tile_chunks(d);
   // bf16: tensor copies straight from the pages where a power of two of at least 8 entries
   // divides the page: smaller boxes copy slower than threads (8 entries 3.2 TB/s from L2,
@@ -820,6 +813,15 @@ csa_status_t run_attn(const AttnCall& c, csa_stream_t stream) {
   // 103).
   const bool chunks = tile && chunked(p) && (groups > 0 ? !copies : !(copies && nc < 8) &&
                       tokens * p.group >= (wide ? kChunkRowsWide : kChunkRows) * S);
+  // The places of packed entries come last: behind prefixes a call that does not pack works without them.
+  if (d <= kTileMaxDim) {
+    const bool packs = groups > 0 ? chunks : chunked(p);
+    if (workspace_bytes < lay_out(p, sms, packs, nullptr)) return CSA_ERR_WORKSPACE;
+    lay_out(p, sms, packs, static_cast<unsigned char*>(workspace));
+  } else {
+    p.head = static_cast<AttnHead*>(workspace);
+  }
+  if (!tile) p.units = nullptr;
   // A unit's own cost (q in, output out, the pipeline's start) in tiles, by which shares are evened
   // out, measured best of 1 to 5 or 6. Packed: three chunks of 1024 tokens x 64 heads of 512 910 us (at 3
   // 945, at 5 987), of 256 450 (at 1 513, at 5 468); 48 of 64 tokens x 8 heads of 128 100 (at 1

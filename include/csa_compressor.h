@@ -530,7 +530,9 @@ csa_status_t csa_cache_attn(const void* q, int64_t q_row_stride, int64_t q_head_
  * ------------------------------------------------------------------------------------ */
 
 /* Bytes of device workspace csa_cache_attn_prefix needs on the current device; 0 on bad sizes.
- * max_entries = max_pages * page_size, max_prefix_entries = max_prefix_pages * page_size of the call. */
+ * max_entries = max_pages * page_size, max_prefix_entries = max_prefix_pages * page_size of the call. They matter for
+ * the room that entries are packed in (up to 4 GiB), which CSA_CACHE_BF16 in pages of a multiple of 8 entries never
+ * takes (given at least one page, and fewer than 2^31 slots): such a call needs what the query gives for 0 and 0. */
 size_t csa_cache_attn_prefix_workspace_bytes(int32_t S, int32_t G, int64_t tokens, int32_t q_heads,
                                              int32_t kv_heads, int32_t d, int64_t max_entries,
                                              int64_t max_prefix_entries);

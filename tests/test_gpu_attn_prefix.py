@@ -291,6 +291,30 @@ def test_full_tables_and_exact_workspaces(cuda_lib, fmt, H, kv, d, page):
     assert ((c.out.double().cpu() - ref).abs() <= tol)[:end].all() and ((c.lse.double().cpu() - rl).abs() <= ltol)[:end].all()
 
 
+@pytest.mark.parametrize("d", [128, 512])
+def test_workspace_without_room_to_pack(cuda_lib, d):
+    """bf16 in pages of a multiple of 8 needs what the query gives for no entries, and touches nothing behind it; codes and
+    other pages are refused with that, and bf16 with less."""
+    def case(fmt, page):
+        return Case([(2048, [(1, 700)] * 40)], 64, 1, d, fmt, page=page, ratio=1, seed=41)
+    c = case(R.BF16, 64)
+    own, pre = c.tables[1].shape[1] * 64, c.tables[0].shape[1] * 64
+    full = cuda_lib.csa_cache_attn_prefix_workspace_bytes(c.S, c.G, c.tokens, 64, 1, d, own, pre)
+    n = cuda_lib.csa_cache_attn_prefix_workspace_bytes(c.S, c.G, c.tokens, 64, 1, d, 0, 0)
+    assert n + (c.S * own + pre) * d * 2 <= full + (1 << 20)  # (the packed entries are what it lacks)
+    ws = torch.full((n + 65536,), 0x5A, dtype=torch.uint8, device="cuda")
+    c.check(cuda_lib, ws=ws[:n])
+    assert (ws[n:] == 0x5A).all()
+    for fmt, page in ((R.E4M3, 64), (R.BF16, 7)):
+        c = case(fmt, page)
+        with pytest.raises(cuda_lib.CsaError) as e:
+            c.run(cuda_lib, ws=ws[:n])
+        assert e.value.status == cuda_lib.CSA_ERR_WORKSPACE and (c.out == 7.0).all()
+    with pytest.raises(cuda_lib.CsaError) as e:
+        case(R.BF16, 64).run(cuda_lib, ws=ws[:n // 2])
+    assert e.value.status == cuda_lib.CSA_ERR_WORKSPACE
+
+
 def test_repeats_and_graph(cuda_lib):
     """The same bits from the same inputs; a captured call replayed on other lengths than it was captured with."""
     def make():
