@@ -410,7 +410,6 @@ __global__ void __launch_bounds__(kPlanThreads) attn_prefix_plan_kernel(AttnPara
     __syncthreads();
     const int unit_tiles = s_tiles[mine], unit_spans = s_spans[mine], span0 = s_span[mine];
     auto put = [&](int at, AttnSpan v, int kvh, int packed) {  // the unit's span `at`
-      v.unit = static_cast<int32_t>(b * p.kv_heads + kvh);
       v.tiles = max(1, tiles_of(v.seen));
       v.packed = packed;
       const int to = span0 + kvh * unit_spans + at;

@@ -29,7 +29,6 @@ struct alignas(16) AttnUnit {
 // tiles ("spans"): the group's prefix, then each of its sequences' own entries.
 struct alignas(16) AttnSpan {
   const int32_t* table;  // its pages
-  int32_t unit;
   int32_t tile, tiles;     // its first tile in the unit, and how many
   int32_t seen, seen_all;  // of its entries: those that some row of the unit sees, and that all see
   int32_t row0, row1;      // rows of the unit that see any
@@ -38,7 +37,7 @@ struct alignas(16) AttnSpan {
   int32_t n, before;       // entries of the sequence, and those of them before the span's
   int32_t packed;          // row of its first entry among the packed ones
   int32_t own;
-  int32_t pad;
+  int32_t pad[2];
 };
 struct alignas(16) AttnStart {  // a worker's share: its first unit, the tile there, and how many tiles
   AttnUnit u;
