@@ -224,6 +224,39 @@ def test_values_out_of_the_ordinary(cuda_lib, H, kv, d, page):
     assert torch.isnan(out[1]).all() and torch.equal(out[[0, 2, 3]], clean[[0, 2, 3]])
 
 
+@pytest.mark.parametrize("fmt", [R.BF16, R.E4M3])
+@pytest.mark.parametrize("H,kv,d", [(64, 1, 512), (16, 1, 128), (6, 1, 72), (3, 1, 128), (4, 2, 256), (1, 1, 64), (2, 1, 65)])
+@pytest.mark.parametrize("page,more", [(16, 0), (3, 0), (16, 60)])
+def test_own_entries_that_later_tokens_alone_see(cuda_lib, fmt, H, kv, d, page, more):
+    """A NaN or an infinity in an own entry that only a sequence's later tokens see, by the tile kernels' ways in
+    (`more`: tokens of other sequences, for which entries are packed): those tokens are NaN in the heads that read it, and
+    all others as they were, the same sequence's earlier ones in the same rows of a tile too."""
+    if fmt != R.BF16 and d % 32:
+        pytest.skip("codes need groups of 32")
+    groups = [(200, [(1, 40), (5, 140), (3, 7)] + [(more, 300)] * (more > 0)), (0, [(4, 130)])]
+
+    def case():
+        return Case(groups, H, kv, d, fmt, page=page, seed=51, ratio=1, sink=True)
+    clean, clean_lse, err = case().run(cuda_lib)
+    assert err == 0
+    clean, clean_lse = clean.cpu(), clean_lse.cpu()
+    for s, back in ((1, 0), (1, 2), (1, 3), (2, 1), (len(groups[0][1]), 0), (len(groups[0][1]), 2)):
+        c = case()
+        index = c.entries[s] - 1 - back  # seen from the sequence's token lens[s] - 1 - back on
+        slot, head = int(c.tables[1][s, index // page]) * page + index % page, kv - 1
+        if fmt == R.BF16:
+            c.data[slot, head, d // 3] = math.nan if back % 2 else -math.inf
+        else:
+            c.data[slot, head, d // 3] = 0x7F
+        out, lse, err = c.run(cuda_lib)
+        assert err == 0
+        hit = torch.zeros(c.tokens, H, dtype=torch.bool)
+        hit[c.cu[s] + c.lens[s] - 1 - back:c.cu[s + 1], head * (H // kv):] = True
+        out, lse = out.cpu(), lse.cpu()
+        assert torch.isnan(out[hit]).all() and torch.isnan(lse[hit]).all(), (s, back)
+        assert torch.equal(out[~hit], clean[~hit]) and torch.equal(lse[~hit], clean_lse[~hit]), (s, back)
+
+
 @pytest.mark.parametrize("d", [64, 65])
 def test_device_refusals(cuda_lib, d):
     def case():
