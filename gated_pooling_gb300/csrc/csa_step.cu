@@ -57,6 +57,7 @@ struct StepParams {
   int stages;  // turns under way
   // the first CTAs of a slice see to the sequences; those behind first_row_cta to the other blocks' rows
   int seq_ctas, first_row_cta;
+  unsigned own_blocks;  // few tokens a sequence: the blocks of one that its own CTA works out
   unsigned checker;  // the CTA of a slice (the first one's works) that looks for states that sequences meet in
 };
 
@@ -718,9 +719,10 @@ __global__ void __launch_bounds__(kStepThreads, 2) step_kernel(const __grid_cons
 // another. What counts is the way from the lengths to the entry, so there is little code; the first window and the
 // embedding come while the rows before it are counted, and so does what goes into the states, which the lines of CL
 // threads share out among them. Where one sequence has more tokens than the others (a chunk of a prompt in a batch of
-// single ones), its blocks from the kFewBlocks-th on, which read no state, are shared out among all CTAs (440 tokens
-// beside 63 single ones, blocks of 4, d 512: 17.6 us, 130 in one CTA; 3500 beside 511 26 and 1012).
-constexpr int kFewThreads = 256, kFewSeqs = 512, kFewBlocks = 8;
+// single ones), its blocks behind those of kFewTokens tokens (and behind the two that may read its state) are shared out
+// among all CTAs: a CTA works out one after another in about 1 us each (449 tokens beside 63 single ones, blocks of 4,
+// d 512: 11.0 us, 17.9 with eight blocks by its own CTA).
+constexpr int kFewThreads = 256, kFewSeqs = 512, kFewTokens = 8;
 template <int VEC, int UW, bool SPLIT>
 __global__ void __launch_bounds__(kFewThreads, SPLIT ? 2 : 1) step_few_kernel(const __grid_constant__ StepParams p) {
   using P = Piece<VEC>;
@@ -737,9 +739,9 @@ __global__ void __launch_bounds__(kFewThreads, SPLIT ? 2 : 1) step_few_kernel(co
     return;
   }
   // the whole call's lengths: what is wrong with them, the rows before these sequences and (from bit 13 on) of all, and
-  // the shared-out ones. (All entries are at most `capacity`, of which calls with up to 8 a sequence come here, whichever
+  // the shared-out ones. (All entries are at most `capacity`, of which calls with up to kFewTokens a sequence come here, whichever
   // sequences have them; offsets that are refused may add up to anything, without a sign so that they may.)
-  static_assert(8 * kFewSeqs < 1 << 13);
+  static_assert(kFewTokens * kFewSeqs < 1 << 13);
   int bad = 0;
   unsigned rows = 0, shared = 0;
   for (int i = tid; i < p.S; i += blockDim.x) {
@@ -749,7 +751,7 @@ __global__ void __launch_bounds__(kFewThreads, SPLIT ? 2 : 1) step_few_kernel(co
     if (why == 0) {
       const unsigned made = (f + (b - a)) / p.ratio - f / p.ratio;
       rows += (made << 13) + (i < s0 ? made : 0u);
-      shared += made > kFewBlocks ? made - kFewBlocks : 0u;
+      shared += made > p.own_blocks ? made - p.own_blocks : 0u;
     }
   }
   // (numbers of one sequence, of which nothing is read until they are known to be right)
@@ -873,7 +875,7 @@ __global__ void __launch_bounds__(kFewThreads, SPLIT ? 2 : 1) step_few_kernel(co
   };
   for (int s = next, row = before; s < s1; ++s) {
     const StepSeq q(p, s);
-    for (int block = q.lo; block < min(q.hi, q.lo + kFewBlocks); ++block) entry(q, block, row + block - q.lo);
+    for (int block = q.lo; block < min(q.hi, q.lo + static_cast<int>(p.own_blocks)); ++block) entry(q, block, row + block - q.lo);
     row += q.hi - q.lo;
   }
   // (the states were read by this thread, or before the last barrier)
@@ -901,7 +903,7 @@ __global__ void __launch_bounds__(kFewThreads, SPLIT ? 2 : 1) step_few_kernel(co
           const int f = __ldg(p.first + i);
           made = (f + __ldg(p.cu + i + 1) - __ldg(p.cu + i)) / p.ratio - f / p.ratio;
         }
-        int2 x = make_int2(made, max(0, made - kFewBlocks));
+        int2 x = make_int2(made, max(0, made - static_cast<int>(p.own_blocks)));
         const int2 own = x;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -922,7 +924,7 @@ __global__ void __launch_bounds__(kFewThreads, SPLIT ? 2 : 1) step_few_kernel(co
         else h = mid;
       }
       const StepSeq q(p, s);
-      const int nth = kFewBlocks + i - s_rows[s].y;  // of the sequence's blocks
+      const int nth = static_cast<int>(p.own_blocks) + i - s_rows[s].y;  // of the sequence's blocks
       entry(q, q.lo + nth, s_rows[s].x + nth);
     }
   }
@@ -1010,20 +1012,51 @@ extern "C" csa_status_t csa_compressor_step(
   // up to 8 positions a thread; longer windows between 4 threads and more (256 at most: CSA_MAX_WINDOW is 2048)
   p.PG = split ? kStepJoin : 1;
   while (p.PG * kStepFlight < p.W) p.PG *= 2;
-  // Few tokens a sequence: the kernel without a pipeline, a CTA a sequence (64 single tokens of 512 in blocks of 4
-  // in 5.4 instead of 7.7 us; 200 of 128 in blocks of 128 in 8.0 instead of 11.5).
-  const bool few = S > 0 && S <= kFewSeqs && capacity <= 8 * static_cast<int64_t>(S);
-  const int threads = few ? kFewThreads : kStepThreads;
-  const int most = threads / p.PG, slices = (p.chunks + most - 1) / most;
+  static_assert(kFewThreads == kStepThreads, "columns and lines of either kernel");
+  const int most = kStepThreads / p.PG, slices = (p.chunks + most - 1) / most;
   p.CL = (p.chunks + slices - 1) / slices;
-  p.RS = threads / (p.CL * p.PG);
-  const int uw = p.W > (split ? 16 : 4) ? 8 : p.W > 2 ? 4 : p.W > 1 ? 2 : 1;
-  auto pick = [&](auto v) -> const void* {
-    constexpr int V = decltype(v)::value;
-    if (few)
+  if (slices > 65535) return CSA_ERR_UNSUPPORTED;
+  void* args[] = {&p};
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  int dev = 0, sms = 0, bps = 0;
+  if (note(cudaGetDevice(&dev)) != cudaSuccess || device_sms(dev, &sms) != cudaSuccess) return CSA_ERR_CUDA;
+  // Few tokens a sequence: the kernel without a pipeline, a CTA a sequence, as long as all CTAs run at once (384 sequences by
+  // one token, blocks of 4, coff 2, d 512 do not: 9.4 us, 8.7 by the other). By it and by the other one, in us, with 1
+  // and 8 tokens in each of 64 sequences, and with single ones but for one of 65 and of 449 (the host knows their sum alone):
+  //   blocks of 4, coff 2, d 512     5.1 and 6.9, 8.2 and 10.5,   8.0 and 8.7, 11.0 and 9.5
+  //   blocks of 16, d 128            6.0 and 6.7, 6.4 and 7.2,    9.2 and 8.0, 9.2 and 9.3
+  //   blocks of 128, coff 2, d 128   5.1 and 6.4, 6.9 and 8.7,    6.2 and 7.2, 10.8 and 10.5
+  // of 256 sequences (and 257 and 1793 tokens)
+  //                                  5.9 and 7.2, 10.3 and 11.8,  10.3 and 9.2, 14.4 and 10.6
+  //                                  6.7 and 6.7, 7.2 and 7.4,    11.5 and 9.5, 11.5 and 10.0
+  //                                  6.4 and 12.6, 10.4 and 15.7, 14.9 and 16.6, 18.0 and 16.4
+  // More sequences only where windows are of up to 4 or more than 32 positions: 384 by 1 and 8 tokens, blocks of 1 and 64, d
+  // 128: 6.7 and 8.7, 10.3 and 16.7; 7.7 and 9.2, 10.5 and 12.3. Blocks of 16, coff 1 and 2: 9.0 and 8.5, 11.0 and 9.3; 9.5
+  // and 10.1, 13.1 and 11.8; of 4, coff 2: 7.4 and 7.9, 10.8 and 12.3, but of 512 8.7 and 8.2.
+  if (S > 0 && S <= (W > 4 && W <= 32 ? kFewSeqs / 2 : kFewSeqs) && capacity <= kFewTokens * static_cast<int64_t>(S)) {
+    auto pick = [&](auto v) -> const void* {
+      constexpr int V = decltype(v)::value;
       return split      ? reinterpret_cast<const void*>(step_few_kernel<V, 8, true>)
              : p.W <= 4 ? reinterpret_cast<const void*>(step_few_kernel<V, 4, false>)
                         : reinterpret_cast<const void*>(step_few_kernel<V, 8, false>);
+    };
+    const void* k = vec ? pick(std::integral_constant<int, 4>{}) : pick(std::integral_constant<int, 1>{});
+    // as many sequences a CTA as leave about two CTAs an SM, no more than have lines of threads of their own
+    p.RS = 1;
+    while (2 * p.RS <= p.PG && static_cast<int64_t>(S) * slices > 2 * static_cast<int64_t>(sms) * p.RS) p.RS *= 2;
+    p.R = (S + p.RS - 1) / p.RS;
+    const int block = p.CL * p.PG <= 64 ? 64 : (p.CL * p.PG + 31) / 32 * 32;
+    if (blocks_per_sm(dev, k, block, 0, &bps) != cudaSuccess) return CSA_ERR_CUDA;
+    if (static_cast<int64_t>(p.R + 1) * slices <= static_cast<int64_t>(sms) * bps) {
+      p.own_blocks = (kFewTokens + ratio - 1) / ratio > 2 ? (kFewTokens + ratio - 1) / ratio : 2;
+      p.checker = S > 1 ? p.R : UINT_MAX;
+      return launch_pdl(k, dim3(p.R + (S > 1), slices), dim3(block), 0, cs, args) == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
+    }
+  }
+  p.RS = kStepThreads / (p.CL * p.PG);
+  const int uw = p.W > (split ? 16 : 4) ? 8 : p.W > 2 ? 4 : p.W > 1 ? 2 : 1;
+  auto pick = [&](auto v) -> const void* {
+    constexpr int V = decltype(v)::value;
     return split     ? (uw == 8 ? reinterpret_cast<const void*>(step_kernel<V, 8, true>) : reinterpret_cast<const void*>(step_kernel<V, 4, true>))
            : uw == 8 ? reinterpret_cast<const void*>(step_kernel<V, 8, false>)
            : uw == 4 ? reinterpret_cast<const void*>(step_kernel<V, 4, false>)
@@ -1031,20 +1064,6 @@ extern "C" csa_status_t csa_compressor_step(
                      : reinterpret_cast<const void*>(step_kernel<V, 1, false>);
   };
   const void* k = vec ? pick(std::integral_constant<int, 4>{}) : pick(std::integral_constant<int, 1>{});
-  if (slices > 65535) return CSA_ERR_UNSUPPORTED;
-  void* args[] = {&p};
-  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  int dev = 0, sms = 0, bps = 0;
-  if (note(cudaGetDevice(&dev)) != cudaSuccess || device_sms(dev, &sms) != cudaSuccess) return CSA_ERR_CUDA;
-  if (few) {
-    // as many sequences a CTA as leave about two CTAs an SM, no more than have lines of threads of their own
-    p.RS = 1;
-    while (2 * p.RS <= p.PG && static_cast<int64_t>(S) * slices > 2 * static_cast<int64_t>(sms) * p.RS) p.RS *= 2;
-    const int block = (p.CL * p.PG + 31) / 32 * 32;
-    p.R = (S + p.RS - 1) / p.RS;
-    p.checker = S > 1 ? p.R : UINT_MAX;
-    return launch_pdl(k, dim3(p.R + (S > 1), slices), dim3(block < 64 ? 64 : block), 0, cs, args) == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
-  }
   // Three turns under way, or as many as leave room for two CTAs an SM beside the sequences' numbers; a CTA an SM where
   // not one does (at most 155 KB of numbers and parts: one turn fits always).
   const int width = vec ? 4 : 1;

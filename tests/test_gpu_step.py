@@ -116,6 +116,20 @@ def test_a_chunk_among_single_tokens(cuda_lib, ratio, coff, d, S):
     st.call([1] * S)
 
 
+@pytest.mark.parametrize("ratio,coff,d,S", [(48, 1, 8, 512), (20, 2, 9, 300), (33, 1, 8, 513), (4, 2, 64, 256), (4, 2, 64, 257),
+                                            (3, 2, 8, 250), (8, 1, 8, 60)])
+def test_a_chunk_among_as_many_sequences_as_one_kernel_takes(cuda_lib, ratio, coff, d, S):
+    """Both sides of the border between the kernels, for short windows and for long ones."""
+    st = Stream(cuda_lib, S, ratio, coff, d, 8 * S + 2 * ratio, seed=S + 1)
+    lens = [1] * S
+    lens[S - 2] = 7 * S
+    st.call(lens, pad=0, spare=1)
+    lens = [0] * S
+    lens[0], lens[S - 1], lens[S // 2] = 6 * S, 2 * ratio - 1, ratio + 1
+    st.call(lens, pad=0, lead=1)
+    st.call([s % 9 for s in range(S)], pad=0)
+
+
 @pytest.mark.parametrize("ratio,coff,d", [(4, 2, 512), (4, 1, 64), (16, 2, 64), (2, 2, 64), (3, 2, 11)])
 def test_single_tokens(cuda_lib, ratio, coff, d):
     st = Stream(cuda_lib, 7, ratio, coff, d, 5 * ratio + 6, seed=3)
