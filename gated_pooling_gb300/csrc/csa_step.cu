@@ -420,10 +420,11 @@ __global__ void __launch_bounds__(kStepThreads, 2) step_kernel(const __grid_cons
   __shared__ int2 warp_sums[32];
   float* const s_part = reinterpret_cast<float*>(s_raw + p.stages * step_stage_bytes(VEC));  // [2][RS][3][PG][CL * VEC]
   int2* const s_prefix = reinterpret_cast<int2*>(s_raw + p.stages * step_stage_bytes(VEC) + step_part_bytes(VEC, SPLIT));  // [S + 1]
-  if (blockIdx.x == static_cast<unsigned>(p.R)) {  // a CTA of its own
+  if (blockIdx.x == p.checker) {
     pdl_wait();
     if (blockIdx.y == 0) check_states(p, reinterpret_cast<int*>(s_prefix), 2 * p.S);
-    return;
+    if (blockIdx.x == static_cast<unsigned>(p.R)) return;  // a CTA of its own
+    __syncthreads();
   }
   if (!build_step_prefix(p, s_prefix, warp_sums, p.stages * p.RS * K)) return;
   const int g = blockIdx.x, tid = threadIdx.x, per = p.CL * p.PG;
@@ -607,11 +608,6 @@ __global__ void __launch_bounds__(kStepThreads, 2) step_kernel(const __grid_cons
   }
 
   const int worker = g - p.first_row_cta, workers = p.R - p.first_row_cta;
-  auto check_at_end = [&]() {
-    if (blockIdx.x != p.checker || blockIdx.y != 0) return;
-    __syncthreads();
-    check_states(p, reinterpret_cast<int*>(s_prefix), 2 * p.S);
-  };
   auto describe = [&]() {
     if (blockIdx.y == 0 && g >= p.first_row_cta && (p.positions != nullptr || p.slots != nullptr))
       for (int64_t o = static_cast<int64_t>(tid) * workers + worker; o < p.out_rows; o += static_cast<int64_t>(workers) * kStepThreads) {
@@ -634,7 +630,6 @@ __global__ void __launch_bounds__(kStepThreads, 2) step_kernel(const __grid_cons
   const int i1 = worker < 0 ? 0 : static_cast<int>(static_cast<int64_t>(worker + 1) * inner / workers);
   if (i0 >= i1) {
     describe();
-    check_at_end();
     return;
   }
   // a walk over them: the sequence of the row asked for last, where its rows end,
@@ -712,7 +707,6 @@ __global__ void __launch_bounds__(kStepThreads, 2) step_kernel(const __grid_cons
     stage_commit();
     if (++b == static_cast<unsigned>(p.stages)) b = 0;
   }
-  check_at_end();
 }
 
 // Calls of few tokens a sequence: a CTA per p.RS sequences and column slice, whose blocks it works out one after
@@ -1083,7 +1077,7 @@ extern "C" csa_status_t csa_compressor_step(
   p.seq_ctas = static_cast<int>(by_seqs < p.R ? (by_seqs > 0 ? by_seqs : 1) : p.R);
   p.first_row_cta = 4 * p.seq_ctas <= p.R ? p.seq_ctas : 0;
   // Sequences' own CTAs are done before those of rows, so the first one looks for states that sequences meet in; otherwise
-  // an additional CTA does, which has the place of one of 64 and more (or else the first one at its end).
+  // an additional CTA does, which has the place of one of 64 and more (or else the first one before its own work).
   const bool added = S > 1 && p.first_row_cta == 0 && (p.R < room || p.R >= 64);
   if (added && p.R == room) {
     --p.R;
