@@ -180,32 +180,50 @@ __device__ __noinline__ void check_states(const StepParams& p, int* table, int s
   for (int i = threadIdx.x; i < slots; i += blockDim.x) table[i] = -1;
   __syncthreads();
   auto place = [&](int state) { return static_cast<int>(__umulhi(static_cast<unsigned>(state) * 0x9E3779B1u, static_cast<unsigned>(slots))); };
-  bool wrong = false, meet = false;
-  for (int s = threadIdx.x; s < p.S; s += blockDim.x) {
-    const int a = __ldg(p.cu + s), b = __ldg(p.cu + s + 1), f = __ldg(p.first + s), from = __ldg(p.source + s), to = __ldg(p.target + s);
-    if (step_wrong(p, a, b, f, from, to) != 0) {
-      wrong = true;
-      continue;
+  // f(the states that it writes and reads) of every sequence of this thread whose numbers are right, kAt at a time: they come
+  // side by side (one after another, 16384 sequences took 82 us)
+  constexpr int kAt = 8;
+  bool wrong = false, meet = false, reads = false;
+  auto each = [&](auto f) {
+    for (int s0 = threadIdx.x; s0 < p.S; s0 += kAt * blockDim.x) {
+      int a[kAt], b[kAt], first[kAt], from[kAt], to[kAt];
+#pragma unroll
+      for (int i = 0; i < kAt; ++i) {
+        const int s = min(s0 + i * static_cast<int>(blockDim.x), p.S - 1);
+        a[i] = __ldg(p.cu + s);
+        b[i] = __ldg(p.cu + s + 1);
+        first[i] = __ldg(p.first + s);
+        from[i] = __ldg(p.source + s);
+        to[i] = __ldg(p.target + s);
+      }
+#pragma unroll
+      for (int i = 0; i < kAt; ++i) {
+        if (s0 + i * static_cast<int>(blockDim.x) >= p.S) break;
+        if (step_wrong(p, a[i], b[i], first[i], from[i], to[i]) != 0) wrong = true;
+        else f(states_of(p, b[i] - a[i], first[i], from[i], to[i]));
+      }
     }
-    const int w = states_of(p, b - a, f, from, to).x;
-    for (int at = w < 0 ? -1 : place(w); at >= 0; at = at + 1 < slots ? at + 1 : 0) {
-      const int old = atomicCAS(table + at, -1, w);
+  };
+  each([&](int2 m) {
+    reads = reads || m.y >= 0;
+    for (int at = m.x < 0 ? -1 : place(m.x); at >= 0; at = at + 1 < slots ? at + 1 : 0) {
+      const int old = atomicCAS(table + at, -1, m.x);
       if (old == -1) break;
-      if (old == w) {
+      if (old == m.x) {
         meet = true;
         break;
       }
     }
-  }
+  });
   if (__syncthreads_or(wrong)) return;
-  for (int s = threadIdx.x; s < p.S; s += blockDim.x) {
-    const int r = states_of(p, __ldg(p.cu + s + 1) - __ldg(p.cu + s), __ldg(p.first + s), __ldg(p.source + s), __ldg(p.target + s)).y;
-    for (int at = r < 0 ? -1 : place(r); at >= 0 && table[at] != -1; at = at + 1 < slots ? at + 1 : 0)
-      if (table[at] == r) {
-        meet = true;
-        break;
-      }
-  }
+  if (__syncthreads_or(reads))
+    each([&](int2 m) {
+      for (int at = m.y < 0 ? -1 : place(m.y); at >= 0 && table[at] != -1; at = at + 1 < slots ? at + 1 : 0)
+        if (table[at] == m.y) {
+          meet = true;
+          break;
+        }
+    });
   if (meet && p.dev_error != nullptr) *reinterpret_cast<volatile int32_t*>(p.dev_error) = CSA_DEVERR_STATE;
 }
 
@@ -1077,8 +1095,9 @@ extern "C" csa_status_t csa_compressor_step(
   p.seq_ctas = static_cast<int>(by_seqs < p.R ? (by_seqs > 0 ? by_seqs : 1) : p.R);
   p.first_row_cta = 4 * p.seq_ctas <= p.R ? p.seq_ctas : 0;
   // Sequences' own CTAs are done before those of rows, so the first one looks for states that sequences meet in; otherwise
-  // an additional CTA does, which has the place of one of 64 and more (or else the first one before its own work).
-  const bool added = S > 1 && p.first_row_cta == 0 && (p.R < room || p.R >= 64);
+  // an additional CTA does, which has the place of one of 32 and more (or else the first one before its own work; 12000
+  // single tokens in blocks of 128, coff 2, d 128, with 38 CTAs a slice: 727 us, 759 in the first one's place).
+  const bool added = S > 1 && p.first_row_cta == 0 && (p.R < room || p.R >= 32);
   if (added && p.R == room) {
     --p.R;
     p.seq_ctas = p.seq_ctas < p.R ? p.seq_ctas : p.R;
