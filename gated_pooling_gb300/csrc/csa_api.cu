@@ -457,7 +457,7 @@ const char* csa_status_string(int status) {
     case CSA_OK: return "CSA_OK";
     case CSA_ERR_INVALID_VALUE: return "CSA_ERR_INVALID_VALUE: null, negative or misaligned argument";
     case CSA_ERR_UNSUPPORTED: return "CSA_ERR_UNSUPPORTED: coff not in {1,2}, or a size limit exceeded";
-    case CSA_ERR_WORKSPACE: return "CSA_ERR_WORKSPACE: workspace missing or smaller than csa_compressor_bwd_workspace_bytes";
+    case CSA_ERR_WORKSPACE: return "CSA_ERR_WORKSPACE: workspace missing or smaller than the call's _workspace_bytes query gives";
     case CSA_ERR_CUDA: return "CSA_ERR_CUDA: a CUDA runtime call or kernel launch failed";
     default: return "unknown csa status";
   }

@@ -59,7 +59,7 @@ typedef enum {
   CSA_OK = 0,
   CSA_ERR_INVALID_VALUE = 1, /* NULL pointer, negative size, misaligned pointer */
   CSA_ERR_UNSUPPORTED = 2,   /* coff not in {1,2}, size limits below */
-  CSA_ERR_WORKSPACE = 3,     /* backward workspace NULL or smaller than the query's size */
+  CSA_ERR_WORKSPACE = 3,     /* workspace NULL or smaller than the size that its query gives */
   CSA_ERR_CUDA = 4           /* a CUDA runtime call or kernel launch failed */
 } csa_status_t;
 

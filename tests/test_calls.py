@@ -75,6 +75,13 @@ def test_every_function_goes_either_way(way, name, args):
     assert e.value.status == gp.CSA_ERR_INVALID_VALUE and name in str(e.value)
 
 
+def test_a_workspace_error_names_no_other_call(way):
+    with pytest.raises(gp.CsaError) as e:
+        gp.csa_cache_attn(FAKE, 64, 64, FAKE, 1, 1, 1, 1, 64, FAKE, None, 0, FAKE, 1, 1, 16, FAKE, None, 0, 1.0, None, FAKE, 64, 64, None,
+                          None, 0, None, 0)
+    assert e.value.status == gp.CSA_ERR_WORKSPACE and "csa_cache_attn: " in str(e.value) and "compressor_bwd" not in str(e.value)
+
+
 def test_the_library_needs_no_python(monkeypatch, tmp_path):
     """Without g++, or without Python's headers, the library is what there is to build; a Python that the module was not
     built for takes the library as it is."""
