@@ -426,8 +426,8 @@ __host__ __device__ constexpr int step_part_bytes(int vec, bool split) { return 
 //
 // A thread's pieces come into places of its own in shared memory (no barrier), p.stages turns ahead: 32 KB a turn
 // and CTA. Two CTAs an SM, so that one has something to do while the other counts rows, waits or joins parts (one
-// of 512 threads: 16.7, 35.7 and 14.1 us below). Three chunks of up to 8192 tokens of 512 in blocks of 4 take 15.9 us
-// (62 % of the copy rate), four of up to 16384 in blocks of 128 33.6 us (60 %), five of up to 1805 tokens of 128 in
+// of 512 threads: 16.7, 35.7 and 14.1 us below). Three chunks of up to 8192 tokens of 512 in blocks of 4 take 15.6 us
+// (64 % of the copy rate), four of up to 16384 in blocks of 128 33.6 us (60 %), five of up to 1805 tokens of 128 in
 // blocks of 16 11.8; registers held one turn ahead, less than latency asks for: 22.7 and 43.8 for the first two.
 template <int VEC, int UW, bool SPLIT>
 __global__ void __launch_bounds__(kStepThreads, 2) step_kernel(const __grid_constant__ StepParams p) {
