@@ -163,11 +163,11 @@ _calls = None
 
 
 def _load_calls():
-    """What the functions below call the library through: the module where there is one for this Python (it and ctypes
-    share one library), else ctypes."""
+    """What the functions below call the library through: the module where there is one for this Python and the present
+    header (it and ctypes share one library), else ctypes."""
     global _calls
     load()
-    if os.path.exists(_build.CALL):
+    if _build.call_up_to_date():
         spec = importlib.util.spec_from_file_location("_csa_call", _build.CALL)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)

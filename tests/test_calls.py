@@ -106,6 +106,19 @@ def test_the_library_needs_no_python(monkeypatch, tmp_path):
     assert os.path.exists(gb.CALL) and gb.up_to_date()
 
 
+def test_a_module_of_an_older_header_is_not_called(monkeypatch, tmp_path):
+    """One that cannot be built again, here for want of g++, may take other arguments than the library does by now."""
+    gp.load()
+    old = tmp_path / "_csa_call.so"
+    old.write_bytes(b"")
+    os.utime(old, (0, 0))
+    monkeypatch.setattr(gb, "CALL", str(old))
+    monkeypatch.setattr(gb, "can_build_call", lambda: False)
+    monkeypatch.setattr(gp, "_calls", None)
+    append()
+    assert isinstance(gp._calls, gp._CtypesCalls)
+
+
 def test_import_without_the_module():
     """A process of its own whose Python has no module: the package loads, calls and reports through ctypes."""
     code = ("import gated_pooling_gb300 as gp; from gated_pooling_gb300 import build as gb\n"
