@@ -19,7 +19,8 @@ PoolKernel bwd_kernel_for(const Plan& pl);
 // csa_last_error_string() and passes the code on. device_sms(): multiprocessor count of a
 // device (cached). blocks_per_sm(): resident blocks of `kernel` per SM with `smem` bytes
 // of dynamic shared memory (cached; raises the kernel's dynamic shared-memory limit
-// once). allow_shared(): that alone, for kernels whose grid does not depend on it. launch_pdl(): launches `k` as a programmatic dependent of the stream's previous
+// once). allow_shared(): the limit alone, for kernels whose grid does not depend on the
+// occupancy. launch_pdl(): launches `k` as a programmatic dependent of the stream's previous
 // kernel.
 cudaError_t note(cudaError_t e);
 cudaError_t device_sms(int dev, int* sms);

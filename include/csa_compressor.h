@@ -40,7 +40,7 @@
  *     more blocks than out_rows) make the kernels write a code to *dev_error (when
  *     dev_error is not NULL), skip all output writes, and finish normally; outputs are
  *     then unspecified. The library never clears *dev_error.
- *   - Results are bitwise reproducible run to run (no atomics anywhere).
+ *   - Results are bitwise reproducible run to run (nothing is summed by atomics).
  */
 #ifndef CSA_COMPRESSOR_H_
 #define CSA_COMPRESSOR_H_
@@ -527,7 +527,7 @@ csa_status_t csa_cache_attn(const void* q, int64_t q_row_stride, int64_t q_head_
  * and out, lse, the entries that a token sees, sinks and the rules for values out of the ordinary are those of
  * csa_cache_attn over prefix_entries[g] + entries[s] entries. The rows of a group's tokens read a prefix
  * together, 64 (token, head) pairs at a time, where a call without prefixes reads it again for every sequence. That gains
- * with few tokens a sequence (twice to six times as fast); chunks of hundreds of them fill their units alone, and up to
+ * with few tokens a sequence (one and a half to six times as fast); chunks of hundreds of them fill their units alone, and up to
  * d = 256 csa_cache_attn over tables that hold the prefix's pages too is up to a fifth faster.
  * ------------------------------------------------------------------------------------ */
 
