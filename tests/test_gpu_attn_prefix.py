@@ -224,6 +224,47 @@ def test_values_out_of_the_ordinary(cuda_lib, H, kv, d, page):
     assert torch.isnan(out[1]).all() and torch.equal(out[[0, 2, 3]], clean[[0, 2, 3]])
 
 
+WAYS = [(R.BF16, 16, 16, 2, 128, 0), (R.BF16, 3, 8, 1, 64, 0), (R.BF16, 16, 64, 1, 512, 0), (R.E4M3, 16, 16, 1, 128, 0), (R.E4M3, 16, 64, 1, 512, 0),
+        (R.E4M3, 16, 64, 1, 128, 70), (R.FP4, 8, 4, 1, 256, 0), (R.BF16, 16, 4, 1, 65, 0)]
+SOME = [(200, [(1, 40), (3, 140), (2, 0), (0, 3)]), (0, [(1, 0), (4, 130)]), (129, [(1, 1)] * 5)]
+
+
+@pytest.mark.parametrize("fmt,page,H,kv,d,more", WAYS)
+@pytest.mark.parametrize("scale", [0.0, -0.0, -0.3, 1e-30])
+def test_scales_of_zero_and_below(cuda_lib, fmt, page, H, kv, d, more, scale):
+    """A scale of 0 weighs all entries alike that a token sees, a negative one turns their order, a tiny one is no mask."""
+    for sink in (False, True):
+        c = Case(SOME + [(300, [(more, 90)])], H, kv, d, fmt, page=page, ratio=1, sink=sink, seed=61)
+        c.scale = scale
+        c.check(cuda_lib)
+
+
+@pytest.mark.parametrize("fmt,page,H,kv,d,more", WAYS)
+@pytest.mark.parametrize("long", [False, True])
+def test_sinks_that_are_not_finite(cuda_lib, fmt, page, H, kv, d, more, long):
+    """A sink of -inf is none, one of +inf takes all the weight (out 0, lse +inf), one of NaN makes NaN; in units by
+    themselves and in ones that workers share."""
+    groups = [(9000 if long else 200, SOME[0][1])] + SOME[1:] + [(300, [(more, 90)])]
+    c, free, held = (Case(groups, H, kv, d, fmt, page=page, ratio=1, sink=True, seed=62) for _ in range(3))
+    kind = torch.arange(H) % 4
+    held.sink = torch.full((H,), 1.5)
+    c.sink = torch.tensor([math.inf, math.nan, -math.inf, 1.5])[kind]
+    free.sink = None
+    out, lse, err = c.run(cuda_lib)
+    assert err == 0
+    n = c.cu[-1]
+    out, lse = out.double().cpu()[:n], lse.double().cpu()[:n]
+    sees = torch.isfinite(free.reference()[1][:n])  # (a token that sees nothing: out 0 and lse the sink)
+    assert (out[:, kind == 0] == 0).all() and (lse[:, kind == 0] == math.inf).all()
+    nan = kind == 1
+    assert torch.isnan(lse[:, nan]).all() and torch.isnan(out[:, nan][sees[:, nan]]).all() and (out[:, nan][~sees[:, nan]] == 0).all()
+    for k, like in ((2, free), (3, held)):
+        ref, rl, tol, ltol = (x[:n][:, kind == k] for x in like.reference())
+        assert ((out[:, kind == k] - ref).abs() <= tol).all()
+        fine = torch.isfinite(rl)
+        assert torch.equal(lse[:, kind == k][~fine], rl[~fine]) and ((lse[:, kind == k] - rl).abs()[fine] <= ltol[fine]).all()
+
+
 @pytest.mark.parametrize("fmt", [R.BF16, R.E4M3])
 @pytest.mark.parametrize("H,kv,d", [(64, 1, 512), (16, 1, 128), (6, 1, 72), (3, 1, 128), (4, 2, 256), (1, 1, 64), (2, 1, 65)])
 @pytest.mark.parametrize("page,more", [(16, 0), (3, 0), (16, 60)])
